@@ -13,6 +13,7 @@
 #include <utility>
 #include <vector>
 
+#include "context.h"
 #include "escha.h"
 #include "kernels.h"
 
@@ -1255,6 +1256,138 @@ int escha_moe_block_noalloc(const escha_moe_layer* L, const uint16_t* x, int T, 
     // Nothing in the scratch has to start at zero: the status word is reset
     // by the router kernel and every other region is written before it is read.
     return moe_block_impl(L, x, T, out, ids_out, w_out, ws, (size_t)ESCHA_NOALLOC_SCRATCH_BYTES, stream, nullptr);
+}
+
+}  // extern "C"
+
+// ---- token mixers and token log probabilities -------------------------------
+namespace {
+
+int check_paged_shape(int B, int Hq, int Hkv, int d, int max_len, const char* name) {
+    if (B < 1 || Hq < 1 || Hkv < 1 || max_len < 1)
+        return fail(ESCHA_E_ARG, "%s: B=%d Hq=%d Hkv=%d max_len=%d must be >= 1", name, B, Hq, Hkv, max_len);
+    if (B > 65535) return fail(ESCHA_E_SHAPE, "%s: B=%d above 65535", name, B);
+    if (Hq % Hkv || Hq / Hkv > 64 || Hkv > 1024)
+        return fail(ESCHA_E_SHAPE, "%s: Hq=%d must be 1..64 times Hkv=%d, Hkv <= 1024", name, Hq, Hkv);
+    if (d != 64 && d != 128 && d != 256) return fail(ESCHA_E_SHAPE, "%s: d=%d must be 64, 128 or 256", name, d);
+    return ESCHA_OK;
+}
+
+int check_delta_shape(int n, int T, int Hk, int Hv, int dk, int dv, int max_len, const char* name) {
+    if (n < 1 || T < 1 || Hk < 1 || Hv < 1 || max_len < 1)
+        return fail(ESCHA_E_ARG, "%s: n=%d T=%d Hk=%d Hv=%d max_len=%d must be >= 1", name, n, T, Hk, Hv, max_len);
+    if (n > 65535 || Hv > 65535 || Hv % Hk)
+        return fail(ESCHA_E_SHAPE, "%s: n=%d above 65535, or Hv=%d not a multiple of Hk=%d, 65535 at most", name, n, Hv,
+                    Hk);
+    if ((dk != 64 && dk != 128) || dv < 32 || dv > 256 || dv % 32)
+        return fail(ESCHA_E_SHAPE, "%s: dk=%d must be 64 or 128, dv=%d a multiple of 32 in 32..256", name, dk, dv);
+    return ESCHA_OK;
+}
+
+int check_logprob_shape(int M, int V, const char* name) {
+    if (M < 1 || V < 1) return fail(ESCHA_E_ARG, "%s: M=%d V=%d must be >= 1", name, M, V);
+    if (V > (1 << 30)) return fail(ESCHA_E_SHAPE, "%s: V=%d above 2^30", name, V);
+    return ESCHA_OK;
+}
+
+int check_ws(const void* ws, size_t ws_bytes, size_t need, const char* name) {
+    if (!need) return ESCHA_OK;
+    if (!ws) return fail(ESCHA_E_ARG, "%s: ws is null", name);
+    if (!aligned16(ws)) return fail(ESCHA_E_ALIGN, "%s: ws not 16-byte aligned", name);
+    if (ws_bytes < need) return fail(ESCHA_E_WORKSPACE, "%s: workspace %zu < %zu bytes", name, ws_bytes, need);
+    return ESCHA_OK;
+}
+
+}  // namespace
+
+extern "C" {
+
+size_t escha_paged_attention_workspace(int B, int Hq, int Hkv, int d, int max_len) {
+    if (check_paged_shape(B, Hq, Hkv, d, max_len, "paged_attention_workspace")) return 0;
+    return escha::paged_attention_ws_bytes(B, Hq, Hkv, d, max_len);
+}
+
+int escha_paged_attention(const void* q, void* k_pool, void* v_pool, int dtype, const int32_t* table,
+                          const int32_t* lens, int B, int Hq, int Hkv, int d, int page, int n_pages, int max_pages,
+                          int max_len, float scale, const void* k_new, const void* v_new, void* out, float* lse,
+                          void* ws, size_t ws_bytes, void* stream) {
+    const char* name = "paged_attention";
+    int r = check_paged_shape(B, Hq, Hkv, d, max_len, name);
+    if (r) return r;
+    if (!q || !k_pool || !v_pool || !table || !lens || !out) return fail(ESCHA_E_ARG, "%s: null pointer", name);
+    if (!k_new != !v_new) return fail(ESCHA_E_ARG, "%s: k_new and v_new go together", name);
+    if (dtype != ESCHA_F16 && dtype != ESCHA_BF16) return fail(ESCHA_E_ARG, "%s: dtype=%d", name, dtype);
+    if (page < 1 || n_pages < 1 || max_pages < 1)
+        return fail(ESCHA_E_ARG, "%s: page=%d n_pages=%d max_pages=%d must be >= 1", name, page, n_pages, max_pages);
+    if (!(scale == scale) || scale - scale != 0.f) return fail(ESCHA_E_ARG, "%s: scale is not finite", name);
+    if (k_pool == v_pool) return fail(ESCHA_E_ARG, "%s: k_pool and v_pool are the same buffer", name);
+    const void* ps[] = {q, k_pool, v_pool, table, lens, k_new, v_new, out, lse};
+    for (const void* p : ps)
+        if (!aligned16(p)) return fail(ESCHA_E_ALIGN, "%s: pointer not 16-byte aligned", name);
+    if ((r = check_ws(ws, ws_bytes, escha::paged_attention_ws_bytes(B, Hq, Hkv, d, max_len), name))) return r;
+    int sms;
+    if ((r = device_check(&sms))) return r;
+    const escha::PagedAttnArgs a{q,  k_pool, v_pool, table, lens, k_new,   v_new,     out,     lse,
+                                 B,  Hq,     Hkv,    d,     page, n_pages, max_pages, max_len, scale};
+    return cuda_status(escha::launch_paged_attention(a, dtype, ws, static_cast<cudaStream_t>(stream)),
+                       "paged_attention launch");
+}
+
+size_t escha_delta_rule_workspace(int n, int T, int Hk, int Hv, int dk, int dv, int max_len) {
+    if (check_delta_shape(n, T, Hk, Hv, dk, dv, max_len, "delta_rule_workspace")) return 0;
+    return escha::delta_rule_ws_bytes(n, T, Hk, Hv, dk, dv, max_len);
+}
+
+int escha_delta_rule(const void* q, const void* k, const void* v, int dtype, const float* g, const float* beta,
+                     float* state, const int32_t* at, int n, int T, int Hk, int Hv, int dk, int dv, int max_len,
+                     float scale, float norm_eps, void* out, void* ws, size_t ws_bytes, void* stream) {
+    const char* name = "delta_rule";
+    int r = check_delta_shape(n, T, Hk, Hv, dk, dv, max_len, name);
+    if (r) return r;
+    if (!q || !k || !v || !g || !beta || !state || !at || !out) return fail(ESCHA_E_ARG, "%s: null pointer", name);
+    if (dtype != ESCHA_F16 && dtype != ESCHA_BF16) return fail(ESCHA_E_ARG, "%s: dtype=%d", name, dtype);
+    if (scale - scale != 0.f || norm_eps - norm_eps != 0.f)
+        return fail(ESCHA_E_ARG, "%s: scale or norm_eps is not finite", name);
+    const void* ps[] = {q, k, v, g, beta, state, at, out};
+    for (const void* p : ps)
+        if (!aligned16(p)) return fail(ESCHA_E_ALIGN, "%s: pointer not 16-byte aligned", name);
+    if ((r = check_ws(ws, ws_bytes, escha::delta_rule_ws_bytes(n, T, Hk, Hv, dk, dv, max_len), name))) return r;
+    int sms;
+    if ((r = device_check(&sms))) return r;
+    const escha::DeltaArgs a{q, k, v, g, beta, state, at, out, n, T, Hk, Hv, dk, dv, max_len, scale, norm_eps};
+    return cuda_status(escha::launch_delta_rule(a, dtype, ws, static_cast<cudaStream_t>(stream)), "delta_rule launch");
+}
+
+size_t escha_token_logprobs_workspace(int M, int V) {
+    if (check_logprob_shape(M, V, "token_logprobs_workspace")) return 0;
+    return escha::token_logprobs_ws_bytes(M, V);
+}
+
+int escha_token_logprobs(const void* logits, int dtype, int M, int V, long long ld, const int32_t* ids, int n_ids,
+                         int top, float* logprobs, float* entropy, float* lse, int32_t* top_ids, float* top_logprobs,
+                         void* ws, size_t ws_bytes, void* stream) {
+    const char* name = "token_logprobs";
+    int r = check_logprob_shape(M, V, name);
+    if (r) return r;
+    if (!logits) return fail(ESCHA_E_ARG, "%s: logits is null", name);
+    if (dtype != ESCHA_F16 && dtype != ESCHA_BF16 && dtype != ESCHA_F32)
+        return fail(ESCHA_E_ARG, "%s: dtype=%d", name, dtype);
+    if (ld < V) return fail(ESCHA_E_SHAPE, "%s: ld=%lld below V=%d", name, ld, V);
+    if (n_ids < 0 || n_ids > 1024) return fail(ESCHA_E_ARG, "%s: n_ids=%d must be in 0..1024", name, n_ids);
+    if (top < 0 || top > escha::kLogprobMaxTop || top > V)
+        return fail(ESCHA_E_ARG, "%s: top=%d must be in 0..min(%d, V)", name, top, escha::kLogprobMaxTop);
+    if (n_ids && (!ids || !logprobs)) return fail(ESCHA_E_ARG, "%s: ids or logprobs is null", name);
+    if (top && (!top_ids || !top_logprobs)) return fail(ESCHA_E_ARG, "%s: top_ids or top_logprobs is null", name);
+    if (!n_ids && !top && !entropy && !lse) return fail(ESCHA_E_ARG, "%s: no output is asked for", name);
+    const void* ps[] = {logits, ids, logprobs, entropy, lse, top_ids, top_logprobs};
+    for (const void* p : ps)
+        if (!aligned16(p)) return fail(ESCHA_E_ALIGN, "%s: pointer not 16-byte aligned", name);
+    if ((r = check_ws(ws, ws_bytes, escha::token_logprobs_ws_bytes(M, V), name))) return r;
+    int sms;
+    if ((r = device_check(&sms))) return r;
+    const escha::LogprobArgs a{logits, ids, logprobs, entropy, lse, top_ids, top_logprobs, ld, M, V, n_ids, top};
+    return cuda_status(escha::launch_token_logprobs(a, dtype, ws, static_cast<cudaStream_t>(stream)),
+                       "token_logprobs launch");
 }
 
 }  // extern "C"

@@ -70,6 +70,12 @@ EXPORTS = [
     "escha_moe_route_workspace",
     "escha_moe_route",
     "escha_residual_rmsnorm",
+    "escha_paged_attention_workspace",
+    "escha_paged_attention",
+    "escha_delta_rule_workspace",
+    "escha_delta_rule",
+    "escha_token_logprobs_workspace",
+    "escha_token_logprobs",
     "int8_w8a16_workspace",
     "int8_w8a16_matvec",
     "int8_w8a16_dequant",
@@ -212,6 +218,21 @@ def lib() -> ctypes.CDLL:
         L.escha_moe_route.restype = _i
         L.escha_residual_rmsnorm.argtypes = [_vp, _vp, _i, _i, ctypes.c_float, _vp, _vp]
         L.escha_residual_rmsnorm.restype = _i
+        _f, _ll = ctypes.c_float, ctypes.c_longlong
+        L.escha_paged_attention_workspace.argtypes = [_i] * 5
+        L.escha_paged_attention_workspace.restype = _sz
+        L.escha_paged_attention.argtypes = [_vp, _vp, _vp, _i, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _i, _f, _vp, _vp,
+                                            _vp, _vp, _vp, _sz, _vp]
+        L.escha_paged_attention.restype = _i
+        L.escha_delta_rule_workspace.argtypes = [_i] * 7
+        L.escha_delta_rule_workspace.restype = _sz
+        L.escha_delta_rule.argtypes = [_vp, _vp, _vp, _i, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _f, _f, _vp,
+                                       _vp, _sz, _vp]
+        L.escha_delta_rule.restype = _i
+        L.escha_token_logprobs_workspace.argtypes = [_i, _i]
+        L.escha_token_logprobs_workspace.restype = _sz
+        L.escha_token_logprobs.argtypes = [_vp, _i, _i, _i, _ll, _vp, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]
+        L.escha_token_logprobs.restype = _i
         L.int8_w8a16_workspace.argtypes = [_i, _i, _i]
         L.int8_w8a16_workspace.restype = _sz
         L.int8_w8a16_matvec.argtypes = [_vp, _vp, _i, _i, _vp, _i, _i, _vp, _vp, _sz, _vp]
@@ -487,6 +508,148 @@ def residual_add(h, add, stream=None) -> None:
     _need_cuda(h, add)
     T, H = h.shape
     check(lib().escha_residual_rmsnorm(ptr(h), ptr(add), T, H, 0.0, None, stream_handle(stream)))
+
+
+class _On:
+    """The device of ``t`` current and, where one is given, ``stream`` too, so
+    that outputs and workspaces made inside belong to the stream that uses
+    them."""
+
+    def __init__(self, t: torch.Tensor, stream=None):
+        self.device = torch.cuda.device(t.device)
+        self.stream = torch.cuda.stream(stream) if stream is not None else None
+
+    def __enter__(self):
+        self.device.__enter__()
+        if self.stream is not None:
+            self.stream.__enter__()
+        return torch.cuda.current_stream().cuda_stream
+
+    def __exit__(self, *e):
+        if self.stream is not None:
+            self.stream.__exit__(*e)
+        self.device.__exit__(*e)
+
+
+def _need(name: str, t, shape, dtype, device):
+    """``t``, a contiguous CUDA tensor of this shape, type and device."""
+    if t.device != device or not t.is_cuda or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor on {device}")
+    if t.dtype != dtype:
+        raise TypeError(f"{name} is {t.dtype}, not {dtype}")
+    if tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
+    return t
+
+
+def _scratch(ws, nbytes: int, device):
+    if ws is None:
+        return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
+    if ws.device != device or not ws.is_contiguous():
+        raise ValueError(f"ws must be a contiguous CUDA tensor on {device}")
+    return ws
+
+
+def paged_attention(q, k_pool, v_pool, table, lens, k_new=None, v_new=None, scale=None, max_len=None, out=None,
+                    lse=None, ws=None, stream=None):
+    """Attention of one new token a sequence over a paged key-value cache
+    (escha_paged_attention). q [B][Hq][d] fp16 or bf16; k_pool, v_pool
+    [n_pages][Hkv][page][d]; table int32 [B][max_pages]; lens int32 [B], the
+    new token counted. k_new, v_new [B][Hkv][d] are stored at position lens - 1
+    and attended. ``scale`` is 1 / sqrt(d) by default; ``max_len`` a host-side
+    bound of lens (by default the table's). Returns (out, lse f32 [B][Hq])."""
+    if q.dim() != 3 or k_pool.dim() != 4 or table.dim() != 2:
+        raise ValueError("q is [B][Hq][d], the pools [n_pages][Hkv][page][d], table [B][max_pages]")
+    B, Hq, d = q.shape
+    n_pages, Hkv, page, _ = k_pool.shape
+    dev, dt = q.device, _dtype_tag(q)
+    _need("q", q, q.shape, q.dtype, dev)
+    _need("k_pool", k_pool, (n_pages, Hkv, page, d), q.dtype, dev)
+    _need("v_pool", v_pool, k_pool.shape, q.dtype, dev)
+    _need("table", table, (B, table.shape[1]), torch.int32, dev)
+    _need("lens", lens, (B,), torch.int32, dev)
+    if (k_new is None) != (v_new is None):
+        raise ValueError("k_new and v_new go together")
+    if k_new is not None:
+        _need("k_new", k_new, (B, Hkv, d), q.dtype, dev)
+        _need("v_new", v_new, (B, Hkv, d), q.dtype, dev)
+    if scale is None:
+        scale = d ** -0.5
+    cap = min(table.shape[1] * page, 2 ** 31 - 1)
+    max_len = cap if max_len is None else min(int(max_len), cap)
+    with _On(q, stream) as s:
+        out = torch.empty_like(q) if out is None else _need("out", out, q.shape, q.dtype, dev)
+        lse = (torch.empty((B, Hq), dtype=torch.float32, device=dev) if lse is None
+               else _need("lse", lse, (B, Hq), torch.float32, dev))
+        ws = _scratch(ws, lib().escha_paged_attention_workspace(B, Hq, Hkv, d, max_len), dev)
+        check(lib().escha_paged_attention(ptr(q), ptr(k_pool), ptr(v_pool), dt, ptr(table), ptr(lens), B, Hq, Hkv, d,
+                                          page, n_pages, table.shape[1], max_len, float(scale), ptr(k_new), ptr(v_new),
+                                          ptr(out), ptr(lse), ptr(ws), ws.numel(), s))
+    return out, lse
+
+
+def delta_rule(q, k, v, g, beta, state, at, scale=None, norm_eps=1e-6, max_len=None, out=None, ws=None, stream=None):
+    """Gated delta rule over ragged sequences (escha_delta_rule). q, k
+    [T][Hk][dk], v [T][Hv][dv] fp16 or bf16; g (log decay), beta f32 [T][Hv];
+    state f32 [n][Hv][dk][dv], updated in place; at int32 [n + 1], the first
+    token of each sequence. q and k are divided by sqrt(sum x^2 + norm_eps)
+    unless norm_eps is None. ``scale`` is 1 / sqrt(dk) by default; ``max_len``
+    an estimate of the longest sequence (by default T over n, rounded up).
+    Returns out [T][Hv][dv]; rows of no sequence in a given ``out`` are left as
+    they are."""
+    if q.dim() != 3 or v.dim() != 3 or state.dim() != 4:
+        raise ValueError("q and k are [T][Hk][dk], v is [T][Hv][dv], state [n][Hv][dk][dv]")
+    T, Hk, dk = q.shape
+    Hv, dv = v.shape[1:]
+    n, dev, dt = state.shape[0], q.device, _dtype_tag(q)
+    _need("q", q, q.shape, q.dtype, dev)
+    _need("k", k, q.shape, q.dtype, dev)
+    _need("v", v, (T, Hv, dv), q.dtype, dev)
+    _need("g", g, (T, Hv), torch.float32, dev)
+    _need("beta", beta, (T, Hv), torch.float32, dev)
+    _need("state", state, (n, Hv, dk, dv), torch.float32, dev)
+    _need("at", at, (n + 1,), torch.int32, dev)
+    if scale is None:
+        scale = dk ** -0.5
+    if norm_eps is None:
+        norm_eps = -1.0
+    elif not norm_eps >= 0:
+        raise ValueError("norm_eps must be >= 0, or None")
+    max_len = -(-T // max(n, 1)) if max_len is None else int(max_len)
+    with _On(q, stream) as s:
+        out = torch.empty_like(v) if out is None else _need("out", out, v.shape, v.dtype, dev)
+        ws = _scratch(ws, lib().escha_delta_rule_workspace(n, T, Hk, Hv, dk, dv, max_len), dev)
+        check(lib().escha_delta_rule(ptr(q), ptr(k), ptr(v), dt, ptr(g), ptr(beta), ptr(state), ptr(at), n, T, Hk, Hv,
+                                     dk, dv, max_len, float(scale), float(norm_eps), ptr(out), ptr(ws), ws.numel(), s))
+    return out
+
+
+def token_logprobs(logits, ids=None, top: int = 0, ws=None, stream=None) -> dict:
+    """Log probabilities of given tokens (escha_token_logprobs). logits [M][V]
+    fp16, bf16 or f32, rows contiguous (a row stride above V is fine); ids
+    int32 [M] or [M][n] or None; top in 0..32. Returns a dict: logprobs (of
+    ids' shape, or None), entropy [M], lse [M], top_ids int32 and top_logprobs
+    [M][top]."""
+    if logits.dim() != 2 or not logits.is_cuda:
+        raise ValueError("logits must be a CUDA tensor [M][V]")
+    M, V = logits.shape
+    ld = logits.stride(0) if M > 1 else V
+    if (V > 1 and logits.stride(1) != 1) or ld < V:
+        raise ValueError("the rows of logits must be contiguous and apart")
+    dev, dt = logits.device, _dtype_tag(logits)
+    if ids is not None:
+        _need("ids", ids, (M,) if ids.dim() == 1 else (M, ids.shape[-1]), torch.int32, dev)
+    n_ids = 0 if ids is None else (1 if ids.dim() == 1 else ids.shape[1])
+    with _On(logits, stream) as s:
+        f32 = dict(dtype=torch.float32, device=dev)
+        r = {"logprobs": None if ids is None else torch.empty(ids.shape, **f32), "entropy": torch.empty(M, **f32),
+             "lse": torch.empty(M, **f32), "top_ids": torch.empty((M, max(int(top), 0)), dtype=torch.int32, device=dev),
+             "top_logprobs": torch.empty((M, max(int(top), 0)), **f32)}
+        ws = _scratch(ws, lib().escha_token_logprobs_workspace(M, V), dev)
+        check(lib().escha_token_logprobs(ptr(logits), dt, M, V, ld, ptr(ids), n_ids, int(top), ptr(r["logprobs"]),
+                                         ptr(r["entropy"]), ptr(r["lse"]), ptr(r["top_ids"]), ptr(r["top_logprobs"]),
+                                         ptr(ws), ws.numel(), s))
+    return r
 
 
 def int8_w8a16_dequant(W, scales, stream=None) -> torch.Tensor:

@@ -4,7 +4,9 @@
  * The library computes the MoE expert path of an Escha-W2 ("eschamoe")
  * 2/3-bit Qwen3.6-35B-A3B-style layer with the packed trellis codes decoded
  * inside the GEMV, never materialised as dense weights, plus the int8 w8a16
- * matvec/GEMM of the dense layers.
+ * matvec/GEMM of the dense layers, and what stands before and behind them in
+ * a decode step: the token mixers (attention of one new token over a paged
+ * cache, gated delta rule) and the log probabilities of the head's logits.
  *
  * Sources (by page):
  *   [PR694]  hipfire PR #694 "Escha-W2 port: 2-bit trellis decoded in the GEMV"
@@ -497,6 +499,100 @@ size_t escha_moe_route_workspace(const escha_moe_layer* L, int T);
 int escha_moe_route(const escha_moe_layer* L, const uint16_t* x, int T, uint16_t* logits_out, int32_t* ids_out,
                     float* w_out, int32_t* counts_out, int32_t* offsets_out, int32_t* perm_out, void* ws,
                     size_t ws_bytes, void* stream);
+
+/* ---- attention of one new token over a paged key-value cache -----------
+ * The full-attention token mixer of a decode step. For sequence b < B and
+ * query head h, over the keys j < lens[b] of key head h / (Hq / Hkv):
+ *   x_j = scale * (q[b][h] . K_j),  m = max_j x_j,
+ *   out[b][h] = sum_j e^(x_j - m) V_j / sum_j e^(x_j - m),
+ *   lse[b][h] = m + ln sum_j e^(x_j - m).
+ * Key j of sequence b is slot j % page of the page table[b][j / page]. Scores,
+ * sums and weighted values are held in f32 and out is rounded once.
+ *   q        [B][Hq][d];  dtype ESCHA_F16 or ESCHA_BF16, of q, both pools,
+ *            k_new, v_new and out
+ *   k_pool, v_pool  [n_pages][Hkv][page][d], two buffers; any page >= 1
+ *   table    int32 [B][max_pages]; an entry outside [0, n_pages) is a page of
+ *            no keys: its positions are left out (a dropped page, say)
+ *   lens     int32 [B], the new token counted; below 0 counts as 0, above
+ *            min(max_len, max_pages * page) as that. A sequence without keys
+ *            gives out = 0 and lse = -infinity, and nothing is written for it.
+ *   k_new, v_new  [B][Hkv][d] or both NULL: the new token's key and value,
+ *            stored at position lens[b] - 1 by the call and attended with the
+ *            rest. Sequences may share pages, but not the page that holds
+ *            another's position lens - 1 (copy it first). When the page entry
+ *            of that position is outside [0, n_pages), the new token is
+ *            neither stored nor attended.
+ *   out      [B][Hq][d];  lse f32 [B][Hq] or NULL
+ *   d        64, 128 or 256;  Hq = 1..64 times Hkv, Hkv <= 1024, B <= 65535
+ *   max_len  host-side bound of lens, >= 1 (max_pages * page always serves)
+ *   ws       escha_paged_attention_workspace(B, Hq, Hkv, d, max_len) bytes;
+ *            nothing in it has to start at zero
+ * Positions at or behind lens[b] are never read: they may hold anything.
+ * Results do not depend on what else runs; a call is repeatable bit for bit.
+ * Errors: ESCHA_E_ARG, ESCHA_E_SHAPE, ESCHA_E_ALIGN, ESCHA_E_WORKSPACE,
+ * ESCHA_E_CUDA, ESCHA_E_DEVICE. */
+size_t escha_paged_attention_workspace(int B, int Hq, int Hkv, int d, int max_len);
+int escha_paged_attention(const void* q, void* k_pool, void* v_pool, int dtype, const int32_t* table,
+                          const int32_t* lens, int B, int Hq, int Hkv, int d, int page, int n_pages, int max_pages,
+                          int max_len, float scale, const void* k_new, const void* v_new, void* out, float* lse,
+                          void* ws, size_t ws_bytes, void* stream);
+
+/* ---- gated delta rule ----------------------------------------------------
+ * The linear token mixer. Sequence s < n owns the tokens at[s] <= t <
+ * at[s + 1] and a state S [dk][dv] per value head; value head h uses key head
+ * h / (Hv / Hk). In token order:
+ *   S <- e^g S,  u = beta (v - S^T k),  S <- S + k u^T,  out = scale S^T q
+ * with q and k first divided by sqrt(sum x^2 + norm_eps) where norm_eps >= 0
+ * (norm_eps < 0: taken as they are). States and sums are f32.
+ *   q, k     [T][Hk][dk];  v, out [T][Hv][dv];  dtype ESCHA_F16 or ESCHA_BF16
+ *   g        f32 [T][Hv], log decay (<= 0 in use; -infinity clears the state)
+ *   beta     f32 [T][Hv]
+ *   state    f32 [n][Hv][dk][dv], updated in place; a new sequence starts from
+ *            a state the caller has set (zeros)
+ *   at       int32 [n + 1], never descending; values outside [0, T] are
+ *            clamped. A sequence of no tokens leaves its state as it is. Rows
+ *            of out that belong to no sequence are left as they are. (Values
+ *            that descend are not allowed: no access leaves the buffers, but
+ *            a token of two sequences gets the output of one of them.)
+ *   dk       64 or 128;  dv a multiple of 32 in 32..256;  Hv a multiple of Hk;
+ *            n, Hv <= 65535
+ *   max_len  host-side estimate of the longest sequence, >= 1: it chooses
+ *            between the kernels that walk the tokens one by one and those
+ *            that take them in chunks; any value gives right results
+ *   ws       escha_delta_rule_workspace(n, T, Hk, Hv, dk, dv, max_len) bytes;
+ *            nothing in it has to start at zero
+ * q, k, v, g and beta must not overlap state or out. Errors as
+ * escha_paged_attention. */
+size_t escha_delta_rule_workspace(int n, int T, int Hk, int Hv, int dk, int dv, int max_len);
+int escha_delta_rule(const void* q, const void* k, const void* v, int dtype, const float* g, const float* beta,
+                     float* state, const int32_t* at, int n, int T, int Hk, int Hv, int dk, int dv, int max_len,
+                     float scale, float norm_eps, void* out, void* ws, size_t ws_bytes, void* stream);
+
+/* ---- log probabilities of given tokens ---------------------------------------
+ * What the head's logits (int8_w8a16_matvec's f32 output, or 16-bit ones) say
+ * about given tokens, in one read. Per row x of V logits:
+ *   lse = ln sum_i e^x_i,  logprobs[j] = x[ids[j]] - lse,
+ *   entropy = -sum_i p_i ln p_i with p_i = e^(x_i - lse), and the top largest
+ *   logits: top_ids by (value descending, id ascending), top_logprobs.
+ * -infinity logits (banned tokens) have probability 0 and add nothing. A row
+ * of nothing else gives lse and every log probability -infinity, entropy 0. A
+ * row with a NaN or +infinity gives NaN for lse, entropy and the log
+ * probabilities; in the top list NaN ranks above +infinity.
+ *   logits   [M] rows of V values, ld >= V values apart; dtype ESCHA_F16,
+ *            ESCHA_BF16 or ESCHA_F32
+ *   ids      int32 [M][n_ids], n_ids in 0..1024: id -1 gives 0 (a padded
+ *            place), another id outside [0, V) gives NaN
+ *   top      0..min(32, V)
+ *   logprobs f32 [M][n_ids];  entropy, lse f32 [M] or NULL;
+ *   top_ids  int32 [M][top];  top_logprobs f32 [M][top]
+ *   ws       escha_token_logprobs_workspace(M, V) bytes (may be 0);
+ *            nothing in it has to start at zero
+ * Pointers of outputs that are not asked for may be NULL. Errors as
+ * escha_paged_attention. */
+size_t escha_token_logprobs_workspace(int M, int V);
+int escha_token_logprobs(const void* logits, int dtype, int M, int V, long long ld, const int32_t* ids, int n_ids,
+                         int top, float* logprobs, float* entropy, float* lse, int32_t* top_ids, float* top_logprobs,
+                         void* ws, size_t ws_bytes, void* stream);
 
 /* ---- int8 w8a16 ----------------------------------------------------------
  * y[m][o] = sum_i (scale[o] * W[o][i]) * x[m][i], f32 output, with the int8

@@ -513,40 +513,45 @@ def residual_add(h, add, stream=None) -> None:
 class _On:
     """The device of ``t`` current and, where one is given, ``stream`` too, so
     that outputs and workspaces made inside belong to the stream that uses
-    them."""
+    them. Entering gives the stream's handle."""
+
+    __slots__ = ("index", "device", "stream")
 
     def __init__(self, t: torch.Tensor, stream=None):
-        self.device = torch.cuda.device(t.device)
+        self.index = t.get_device()
+        self.device = None if self.index == torch.cuda.current_device() else torch.cuda.device(self.index)
         self.stream = torch.cuda.stream(stream) if stream is not None else None
 
     def __enter__(self):
-        self.device.__enter__()
+        if self.device is not None:
+            self.device.__enter__()
         if self.stream is not None:
             self.stream.__enter__()
-        return torch.cuda.current_stream().cuda_stream
+        return torch._C._cuda_getCurrentRawStream(self.index)
 
     def __exit__(self, *e):
         if self.stream is not None:
             self.stream.__exit__(*e)
-        self.device.__exit__(*e)
+        if self.device is not None:
+            self.device.__exit__(*e)
 
 
-def _need(name: str, t, shape, dtype, device):
-    """``t``, a contiguous CUDA tensor of this shape, type and device."""
-    if t.device != device or not t.is_cuda or not t.is_contiguous():
-        raise ValueError(f"{name} must be a contiguous CUDA tensor on {device}")
-    if t.dtype != dtype:
+def _need(name: str, t, shape, dtype, index: int):
+    """``t``, a contiguous tensor of this shape and type on CUDA device ``index``."""
+    if t.dtype is dtype and t.shape == shape and t.is_contiguous() and index >= 0 and t.get_device() == index:
+        return t
+    if index < 0 or t.get_device() != index or not t.is_contiguous():
+        raise ValueError(f"{name} must be a contiguous CUDA tensor, all on one device")
+    if t.dtype is not dtype:
         raise TypeError(f"{name} is {t.dtype}, not {dtype}")
-    if tuple(t.shape) != tuple(shape):
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
-    return t
+    raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
 
 
 def _scratch(ws, nbytes: int, device):
     if ws is None:
         return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
-    if ws.device != device or not ws.is_contiguous():
-        raise ValueError(f"ws must be a contiguous CUDA tensor on {device}")
+    if ws.device != device or not ws.is_contiguous() or ws.dtype is not torch.uint8:
+        raise ValueError(f"ws must be a contiguous uint8 tensor on {device}")
     return ws
 
 
@@ -562,25 +567,25 @@ def paged_attention(q, k_pool, v_pool, table, lens, k_new=None, v_new=None, scal
         raise ValueError("q is [B][Hq][d], the pools [n_pages][Hkv][page][d], table [B][max_pages]")
     B, Hq, d = q.shape
     n_pages, Hkv, page, _ = k_pool.shape
-    dev, dt = q.device, _dtype_tag(q)
-    _need("q", q, q.shape, q.dtype, dev)
-    _need("k_pool", k_pool, (n_pages, Hkv, page, d), q.dtype, dev)
-    _need("v_pool", v_pool, k_pool.shape, q.dtype, dev)
-    _need("table", table, (B, table.shape[1]), torch.int32, dev)
-    _need("lens", lens, (B,), torch.int32, dev)
+    dev, at, dt = q.device, q.get_device(), _dtype_tag(q)
+    _need("q", q, q.shape, q.dtype, at)
+    _need("k_pool", k_pool, (n_pages, Hkv, page, d), q.dtype, at)
+    _need("v_pool", v_pool, k_pool.shape, q.dtype, at)
+    _need("table", table, (B, table.shape[1]), torch.int32, at)
+    _need("lens", lens, (B,), torch.int32, at)
     if (k_new is None) != (v_new is None):
         raise ValueError("k_new and v_new go together")
     if k_new is not None:
-        _need("k_new", k_new, (B, Hkv, d), q.dtype, dev)
-        _need("v_new", v_new, (B, Hkv, d), q.dtype, dev)
+        _need("k_new", k_new, (B, Hkv, d), q.dtype, at)
+        _need("v_new", v_new, (B, Hkv, d), q.dtype, at)
     if scale is None:
         scale = d ** -0.5
     cap = min(table.shape[1] * page, 2 ** 31 - 1)
     max_len = cap if max_len is None else min(int(max_len), cap)
     with _On(q, stream) as s:
-        out = torch.empty_like(q) if out is None else _need("out", out, q.shape, q.dtype, dev)
+        out = torch.empty_like(q) if out is None else _need("out", out, q.shape, q.dtype, at)
         lse = (torch.empty((B, Hq), dtype=torch.float32, device=dev) if lse is None
-               else _need("lse", lse, (B, Hq), torch.float32, dev))
+               else _need("lse", lse, (B, Hq), torch.float32, at))
         ws = _scratch(ws, lib().escha_paged_attention_workspace(B, Hq, Hkv, d, max_len), dev)
         check(lib().escha_paged_attention(ptr(q), ptr(k_pool), ptr(v_pool), dt, ptr(table), ptr(lens), B, Hq, Hkv, d,
                                           page, n_pages, table.shape[1], max_len, float(scale), ptr(k_new), ptr(v_new),
@@ -601,14 +606,14 @@ def delta_rule(q, k, v, g, beta, state, at, scale=None, norm_eps=1e-6, max_len=N
         raise ValueError("q and k are [T][Hk][dk], v is [T][Hv][dv], state [n][Hv][dk][dv]")
     T, Hk, dk = q.shape
     Hv, dv = v.shape[1:]
-    n, dev, dt = state.shape[0], q.device, _dtype_tag(q)
-    _need("q", q, q.shape, q.dtype, dev)
-    _need("k", k, q.shape, q.dtype, dev)
-    _need("v", v, (T, Hv, dv), q.dtype, dev)
-    _need("g", g, (T, Hv), torch.float32, dev)
-    _need("beta", beta, (T, Hv), torch.float32, dev)
-    _need("state", state, (n, Hv, dk, dv), torch.float32, dev)
-    _need("at", at, (n + 1,), torch.int32, dev)
+    n, dev, on, dt = state.shape[0], q.device, q.get_device(), _dtype_tag(q)
+    _need("q", q, q.shape, q.dtype, on)
+    _need("k", k, q.shape, q.dtype, on)
+    _need("v", v, (T, Hv, dv), q.dtype, on)
+    _need("g", g, (T, Hv), torch.float32, on)
+    _need("beta", beta, (T, Hv), torch.float32, on)
+    _need("state", state, (n, Hv, dk, dv), torch.float32, on)
+    _need("at", at, (n + 1,), torch.int32, on)
     if scale is None:
         scale = dk ** -0.5
     if norm_eps is None:
@@ -617,7 +622,7 @@ def delta_rule(q, k, v, g, beta, state, at, scale=None, norm_eps=1e-6, max_len=N
         raise ValueError("norm_eps must be >= 0, or None")
     max_len = -(-T // max(n, 1)) if max_len is None else int(max_len)
     with _On(q, stream) as s:
-        out = torch.empty_like(v) if out is None else _need("out", out, v.shape, v.dtype, dev)
+        out = torch.empty_like(v) if out is None else _need("out", out, v.shape, v.dtype, on)
         ws = _scratch(ws, lib().escha_delta_rule_workspace(n, T, Hk, Hv, dk, dv, max_len), dev)
         check(lib().escha_delta_rule(ptr(q), ptr(k), ptr(v), dt, ptr(g), ptr(beta), ptr(state), ptr(at), n, T, Hk, Hv,
                                      dk, dv, max_len, float(scale), float(norm_eps), ptr(out), ptr(ws), ws.numel(), s))
@@ -638,7 +643,7 @@ def token_logprobs(logits, ids=None, top: int = 0, ws=None, stream=None) -> dict
         raise ValueError("the rows of logits must be contiguous and apart")
     dev, dt = logits.device, _dtype_tag(logits)
     if ids is not None:
-        _need("ids", ids, (M,) if ids.dim() == 1 else (M, ids.shape[-1]), torch.int32, dev)
+        _need("ids", ids, (M,) if ids.dim() == 1 else (M, ids.shape[-1]), torch.int32, logits.get_device())
     n_ids = 0 if ids is None else (1 if ids.dim() == 1 else ids.shape[1])
     with _On(logits, stream) as s:
         f32 = dict(dtype=torch.float32, device=dev)

@@ -1319,7 +1319,9 @@ int escha_paged_attention(const void* q, void* k_pool, void* v_pool, int dtype, 
     if (dtype != ESCHA_F16 && dtype != ESCHA_BF16) return fail(ESCHA_E_ARG, "%s: dtype=%d", name, dtype);
     if (page < 1 || n_pages < 1 || max_pages < 1)
         return fail(ESCHA_E_ARG, "%s: page=%d n_pages=%d max_pages=%d must be >= 1", name, page, n_pages, max_pages);
-    if (!(scale == scale) || scale - scale != 0.f) return fail(ESCHA_E_ARG, "%s: scale is not finite", name);
+    if ((long long)n_pages * page > 0x7fffffffll / Hkv)
+        return fail(ESCHA_E_SHAPE, "%s: n_pages * Hkv * page = %d * %d * %d is above 2^31 - 1 rows", name, n_pages, Hkv, page);
+    if (scale - scale != 0.f) return fail(ESCHA_E_ARG, "%s: scale is not finite", name);
     if (k_pool == v_pool) return fail(ESCHA_E_ARG, "%s: k_pool and v_pool are the same buffer", name);
     const void* ps[] = {q, k_pool, v_pool, table, lens, k_new, v_new, out, lse};
     for (const void* p : ps)

@@ -30,24 +30,28 @@ namespace escha {
 
 namespace {
 
-constexpr int kPaWarps = 4;
-constexpr int kPaThreads = kPaWarps * 32;
-constexpr int kPaRound = 16 * kPaWarps;  // keys of a round
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 
-template <int D>
-struct PaCfg {
-    static constexpr int kStages = D == 64 ? 4 : 3;
-    static constexpr int kCtas = D == 256 ? 1 : D == 128 ? 2 : 3;  // a multiprocessor
-    static constexpr int kRow = D * 2;                              // bytes of a row
-    static constexpr int kTile = 16 * kRow;                         // one stage's keys (and values) of a warp
-    static constexpr int kRing = kPaWarps * kStages * 2 * kTile;
-};
+// A warp's ring holds kHalves halves of stages (16 keys, or their 16 values).
 template <int D, int NT>
-constexpr int pa_smem() {
-    return PaCfg<D>::kRing + 2 * 8 * NT * D * 4;
-}
+struct PaCfg {
+    static constexpr int kWarps = D == 256 ? 8 : 4;
+    static constexpr int kThreads = kWarps * 32;
+    static constexpr int kRound = 16 * kWarps;  // keys of a round
+    static constexpr int kHalves = D == 256 ? 3 : D == 128 ? 4 : 6;
+    static constexpr int kCtas = D == 256 ? 1 : D == 128 ? (NT == 1 ? 3 : 2) : (NT == 1 ? 4 : 3);  // a multiprocessor
+    static constexpr int kRow = D * 2;          // bytes of a row
+    static constexpr int kTile = 16 * kRow;     // of a half
+    static constexpr int kRing = kWarps * kHalves * kTile;
+    static constexpr int kSmem = kRing + 2 * 8 * NT * D * 4;
+};
+
+// n / d of n < 2^31 by one multiplication: mul = ceil(2^(31 + l) / d), l = ceil(log2 d).
+struct PaDiv {
+    uint32_t mul;
+    int shift;
+};
 
 template <int DT>
 __device__ __forceinline__ uint32_t pa_pack(float x, float y) {
@@ -116,48 +120,54 @@ __device__ __forceinline__ int pa_len(const PagedAttnArgs& a, int b) {
 
 // One part of a unit: 8 NT heads' weighted values, then their maxima and sums.
 struct PaParts {
-    float* acc;   // [2 G][heads][D]
-    float* ml;    // [2 G][2][heads]
-    int2* units;  // [B][units a sequence]: first CTA and number of parts (0: finished by its CTA)
+    float* acc;  // [2 G][heads][D]
+    float* ml;   // [2 G][2][heads]
+    int4* open;  // [G] the unit that begins in this CTA's range and ends in another's: sequence, key head,
+                 // tile of heads and number of parts (0: there is none)
 };
 
-// A place in the list of rounds: round r of unit u of sequence b.
+// A place in the list of rounds: round r of one (sequence, key head, tile of heads).
 struct PaPlace {
-    int b, u, r, rounds, len;
-    __device__ __forceinline__ void next(const PagedAttnArgs& a, int units) {
+    int b, kvh, tile, r, rounds, len;
+    template <int kRound>
+    __device__ __forceinline__ void next(const PagedAttnArgs& a, int tiles) {
         if (++r < rounds) return;
         r = 0;
-        if (++u < units) return;
-        u = 0;
+        if (++tile < tiles) return;
+        tile = 0;
+        if (++kvh < a.Hkv) return;
+        kvh = 0;
         do {
             if (++b >= a.B) {
                 rounds = 0;
                 return;
             }
             len = pa_len(a, b);
-            rounds = (len + kPaRound - 1) / kPaRound;
+            rounds = (len + kRound - 1) / kRound;
         } while (rounds == 0);
     }
 };
 
 template <int DT, int D, int NT>
-__global__ void __launch_bounds__(kPaThreads) paged_attention_kernel(PagedAttnArgs a, int tiles, PaParts parts) {
-    using C = PaCfg<D>;
-    constexpr int kHeads = 8 * NT, kStages = C::kStages, kTile = C::kTile, kKs = D / 16;
+__global__ void __launch_bounds__(PaCfg<D, NT>::kThreads, PaCfg<D, NT>::kCtas)
+    paged_attention_kernel(PagedAttnArgs a, int tiles, PaDiv div, PaParts parts) {
+    using C = PaCfg<D, NT>;
+    constexpr int kHeads = 8 * NT, kHalves = C::kHalves, kTile = C::kTile, kKs = D / 16, kRound = C::kRound;
+    constexpr int kWarps = C::kWarps, kThreads = C::kThreads;
     extern __shared__ __align__(1024) unsigned char smem[];
-    __shared__ long long scan[kPaWarps];
+    __shared__ long long scan[kWarps];
     __shared__ int first_s[4];
-    __shared__ float sm_m[kPaWarps][kHeads], sm_l[kPaWarps][kHeads];
+    __shared__ float sm_m[kWarps][kHeads], sm_l[kWarps][kHeads];
     pdl_wait();
     pdl_trigger();
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5, g = lane >> 2, q4 = lane & 3;
     const int units = a.Hkv * tiles, group = a.Hq / a.Hkv;
 
     // ---- this CTA's range of the rounds
-    const int per = (a.B + kPaThreads - 1) / kPaThreads;
+    const int per = (a.B + kThreads - 1) / kThreads;
     const int b0 = t * per, b1 = min(a.B, b0 + per);
     long long mine = 0;
-    for (int b = b0; b < b1; ++b) mine += (long long)((pa_len(a, b) + kPaRound - 1) / kPaRound) * units;
+    for (int b = b0; b < b1; ++b) mine += (long long)((pa_len(a, b) + kRound - 1) / kRound) * units;
     long long incl = mine;
 #pragma unroll
     for (int m = 1; m < 32; m <<= 1) {
@@ -168,22 +178,31 @@ __global__ void __launch_bounds__(kPaThreads) paged_attention_kernel(PagedAttnAr
     __syncthreads();
     long long before = 0, total = 0;
 #pragma unroll
-    for (int w = 0; w < kPaWarps; ++w) {
+    for (int w = 0; w < kWarps; ++w) {
         if (w < warp) before += scan[w];
         total += scan[w];
     }
     // every CTA that takes part has a round at least (the join counts on it)
     const long long ctas = min(static_cast<long long>(gridDim.x), total);
+    if (t == 0) parts.open[blockIdx.x] = make_int4(0, 0, 0, 0);
+    // the sequences without keys
+    for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+        if (pa_len(a, b) > 0) continue;
+        for (int i = t; i < a.Hq * D / 2; i += kThreads) static_cast<uint32_t*>(a.out)[(long long)b * a.Hq * D / 2 + i] = 0u;
+        if (a.lse)
+            for (int i = t; i < a.Hq; i += kThreads) a.lse[(long long)b * a.Hq + i] = -INFINITY;
+    }
     if (blockIdx.x >= ctas) return;
-    const long long lo = blockIdx.x * total / ctas, hi = (blockIdx.x + 1) * total / ctas;
+    const long long lo = blockIdx.x * total / ctas;
+    const long long left = (blockIdx.x + 1) * total / ctas - lo;
     long long x0 = before + incl - mine;
     if (lo >= x0 && lo < x0 + mine) {
         for (int b = b0; b < b1; ++b) {
-            const int len = pa_len(a, b), rounds = (len + kPaRound - 1) / kPaRound;
+            const int len = pa_len(a, b), rounds = (len + kRound - 1) / kRound;
             const long long n = (long long)rounds * units;
             if (lo < x0 + n) {
-                const int at = static_cast<int>(lo - x0);
-                first_s[0] = b, first_s[1] = at / rounds, first_s[2] = at % rounds, first_s[3] = len;
+                first_s[0] = b, first_s[1] = static_cast<int>((lo - x0) / rounds);
+                first_s[2] = static_cast<int>((lo - x0) % rounds), first_s[3] = len;
                 break;
             }
             x0 += n;
@@ -191,83 +210,88 @@ __global__ void __launch_bounds__(kPaThreads) paged_attention_kernel(PagedAttnAr
     }
     __syncthreads();
     PaPlace cur;
-    cur.b = first_s[0], cur.u = first_s[1], cur.r = first_s[2], cur.len = first_s[3];
-    cur.rounds = (cur.len + kPaRound - 1) / kPaRound;
+    cur.b = first_s[0], cur.kvh = first_s[1] / tiles, cur.tile = first_s[1] % tiles, cur.r = first_s[2], cur.len = first_s[3];
+    cur.rounds = (cur.len + kRound - 1) / kRound;
 
     // ---- the warp's ring
-    unsigned char* ring = smem + warp * kStages * 2 * kTile;
-    const uint32_t ring_s = static_cast<uint32_t>(__cvta_generic_to_shared(ring));
+    const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * kHalves * kTile;
     const char* kp = static_cast<const char*>(a.k_pool);
     const char* vp = static_cast<const char*>(a.v_pool);
-    PaPlace ld = cur;       // the next round to load
-    long long left = hi - lo;
-    // lane r < 16 holds row r of the round to load: its offset in values (-1: not there)
-    auto find_row = [&](const PaPlace& p) -> long long {
-        const int j = p.r * kPaRound + warp * 16 + (lane & 15);
-        if (j >= p.len) return -1;
-        const int pg = a.table[(long long)p.b * a.max_pages + j / a.page];
-        if (pg < 0 || pg >= a.n_pages) return -1;
-        return (((long long)pg * a.Hkv + p.u / tiles) * a.page + j % a.page) * D;
+    constexpr int kChunks = D / 8, kAtOnce = 32 / kChunks;
+    const int c8 = lane % kChunks, rr = lane / kChunks;
+    PaPlace ld = cur;  // the next round to load
+    // lane r < 16 (and r + 16) holds row r of that round: its number in the pool (-1: not there)
+    auto find_row = [&]() -> int {
+        const int j = ld.r * kRound + warp * 16 + (lane & 15);
+        if (j >= ld.len) return -1;
+        const int p = static_cast<int>((static_cast<unsigned long long>(j) * div.mul) >> div.shift);
+        const int pg = a.table[(long long)ld.b * a.max_pages + p];
+        if (static_cast<unsigned>(pg) >= static_cast<unsigned>(a.n_pages)) return -1;
+        return (pg * a.Hkv + ld.kvh) * a.page + (j - p * a.page);
     };
-    long long row = find_row(ld);
-    auto load = [&](int stage) {
-        constexpr int kChunks = D / 8, kAtOnce = 32 / kChunks > 0 ? 32 / kChunks : 1;
-        const uint32_t ks = ring_s + stage * 2 * kTile, vs = ks + kTile;
-        const int newest = a.k_new ? ld.len - 1 - (ld.r * kPaRound + warp * 16) : -1;  // the new token's row
-        const long long fresh = ((long long)ld.b * a.Hkv + ld.u / tiles) * D;
+    int row = find_row();
+    // one half of the round: its keys (pool kp, new rows kn) or values
+    auto load = [&](uint32_t to, const char* pool, const void* fresh) {
+        const char* base = pool + c8 * 16;
+        const int newest = a.k_new ? ld.len - 1 - (ld.r * kRound + warp * 16) : -1;  // the new token's row
+        if (static_cast<unsigned>(newest) < 16u) {
+            const char* nw = static_cast<const char*>(fresh) + ((long long)ld.b * a.Hkv + ld.kvh) * C::kRow + c8 * 16;
+#pragma unroll 1
+            for (int i = 0; i < 16; i += kAtOnce) {
+                const int r = i + rr, n = __shfl_sync(0xffffffffu, row, r);
+                const char* src = n >= 0 ? base + (long long)n * C::kRow : base;
+                if (r == newest && n >= 0) {
+                    if (ld.tile == 0) *reinterpret_cast<uint4*>(const_cast<char*>(src)) = *reinterpret_cast<const uint4*>(nw);
+                    src = nw;
+                }
+                cp16(to + r * C::kRow + ((c8 ^ (r & 7)) << 4), src, n >= 0);
+            }
+        } else {
 #pragma unroll
-        for (int i = 0; i < 16; i += kAtOnce) {
-            const int r = i + lane / kChunks, c = lane % kChunks;
-            const long long off = __shfl_sync(0xffffffffu, row, r);
-            const bool ok = off >= 0;
-            const char* ksrc = kp;
-            const char* vsrc = vp;
-            if (ok) {
-                ksrc = kp + (off + c * 8) * 2, vsrc = vp + (off + c * 8) * 2;
-                if (r == newest) {
-                    const char* kn = static_cast<const char*>(a.k_new) + (fresh + c * 8) * 2;
-                    const char* vn = static_cast<const char*>(a.v_new) + (fresh + c * 8) * 2;
-                    if (ld.u % tiles == 0) {
-                        *reinterpret_cast<uint4*>(const_cast<char*>(ksrc)) = *reinterpret_cast<const uint4*>(kn);
-                        *reinterpret_cast<uint4*>(const_cast<char*>(vsrc)) = *reinterpret_cast<const uint4*>(vn);
-                    }
-                    ksrc = kn, vsrc = vn;
+            for (int i = 0; i < 16; i += kAtOnce) {
+                const int r = i + rr, n = __shfl_sync(0xffffffffu, row, r);
+                cp16(to + r * C::kRow + ((c8 ^ (r & 7)) << 4), base + (long long)max(n, 0) * C::kRow, n >= 0);
+            }
+        }
+    };
+    // which rows of the rounds in flight hold keys, 16 bits a round, the oldest lowest
+    unsigned long long masks = 0;
+    long long issued = 0;
+    int in_masks = 0;  // rounds in `masks`
+    uint32_t to = ring;
+    auto issue = [&](bool values) {
+        if (issued < 2 * left) {
+            if (!values) {
+                masks |= static_cast<unsigned long long>(__ballot_sync(0xffffffffu, row >= 0) & 0xFFFFu) << (16 * in_masks);
+                ++in_masks;
+                load(to, kp, a.k_new);
+            } else {
+                load(to, vp, a.v_new);
+                if (issued + 1 < 2 * left) {
+                    ld.template next<kRound>(a, tiles);
+                    row = find_row();
                 }
             }
-            const uint32_t at = r * C::kRow + ((c ^ (r & 7)) << 4);
-            cp16(ks + at, ksrc, ok);
-            cp16(vs + at, vsrc, ok);
-        }
-    };
-    uint32_t there = 0;  // bit r of a byte pair per stage: which rows hold keys
-    uint32_t masks[kStages];
-#pragma unroll
-    for (int i = 0; i < kStages - 1; ++i) {
-        masks[i] = 0;
-        if (i < left) {
-            masks[i] = __ballot_sync(0xffffffffu, row >= 0) & 0xFFFFu;
-            load(i);
-            if (i + 1 < left) {
-                ld.next(a, units);
-                row = find_row(ld);
-            }
+            ++issued;
+            to = to + kTile == ring + kHalves * kTile ? ring : to + kTile;
         }
         cp_commit();
-    }
-    masks[kStages - 1] = 0;
+    };
+#pragma unroll
+    for (int i = 0; i < kHalves - 1; ++i) issue(i & 1);
 
     uint32_t qf[NT][kKs][2];
     float acc[NT][kKs][4], m[NT][2], l[NT][2];
     bool begin = true;
-    int piece_r0 = 0;
+    int piece_r0 = 0, h0 = 0, nh = 0;
     const float sc = a.scale * kLog2e;
-    int stage = 0;
+    uint32_t from = ring;
     for (long long i = 0; i < left; ++i) {
-        const int kvh = cur.u / tiles, h0 = kvh * group + (cur.u % tiles) * kHeads;
-        const int nh = min(kHeads, group - (cur.u % tiles) * kHeads);
         if (begin) {
             begin = false;
             piece_r0 = cur.r;
+            h0 = cur.kvh * group + cur.tile * kHeads;
+            nh = min(kHeads, group - cur.tile * kHeads);
 #pragma unroll
             for (int n = 0; n < NT; ++n) {
                 const int h = n * 8 + g;
@@ -282,51 +306,43 @@ __global__ void __launch_bounds__(kPaThreads) paged_attention_kernel(PagedAttnAr
                 m[n][0] = m[n][1] = -INFINITY, l[n][0] = l[n][1] = 0.f;
             }
         }
-        cp_wait<kStages - 2>();
-        __syncwarp();
-        {
-            // the stage freed in the last iteration takes the round kStages - 1 ahead
-            const int to = stage == 0 ? kStages - 1 : stage - 1;
-            if (i + kStages - 1 < left) {
-                const uint32_t mk = __ballot_sync(0xffffffffu, row >= 0) & 0xFFFFu;
-#pragma unroll
-                for (int s = 0; s < kStages; ++s)
-                    if (s == to) masks[s] = mk;
-                load(to);
-                if (i + kStages < left) {
-                    ld.next(a, units);
-                    row = find_row(ld);
-                }
-            }
-            cp_commit();
-        }
-#pragma unroll
-        for (int s = 0; s < kStages; ++s)
-            if (s == stage) there = masks[s];
-        const uint32_t ks = ring_s + stage * 2 * kTile, vs = ks + kTile;
         // ---- scores of 16 keys x 8 NT heads
-        float x[NT][2][4];
+        cp_wait<kHalves - 2>();
+        __syncwarp();
+        issue((kHalves - 1) & 1);  // into the half that the last values left
+        const uint32_t there = static_cast<uint32_t>(masks) & 0xFFFFu;
+        masks >>= 16;
+        --in_masks;
+        constexpr int kWays = NT == 1 ? 4 : 2;
+        float x[NT][kWays][4];
 #pragma unroll
         for (int n = 0; n < NT; ++n)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) x[n][0][e] = x[n][1][e] = 0.f;
+            for (int w = 0; w < kWays; ++w)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[n][w][e] = 0.f;
         {
             const int r = lane & 15, ch = lane >> 4;
 #pragma unroll
             for (int k = 0; k < kKs; ++k) {
                 uint32_t f[4];
-                ldsm4(f, ks + r * C::kRow + (((2 * k + ch) ^ (r & 7)) << 4));
+                ldsm4(f, from + r * C::kRow + (((2 * k + ch) ^ (r & 7)) << 4));
 #pragma unroll
-                for (int n = 0; n < NT; ++n) pa_mma<DT>(x[n][k & 1], f, qf[n][k][0], qf[n][k][1]);
+                for (int n = 0; n < NT; ++n) pa_mma<DT>(x[n][k % kWays], f, qf[n][k][0], qf[n][k][1]);
             }
         }
+        from = from + kTile == ring + kHalves * kTile ? ring : from + kTile;
         uint32_t ph[NT][2], pl[NT][2];
         const bool k0 = (there >> g) & 1, k1 = (there >> (g + 8)) & 1;
 #pragma unroll
         for (int n = 0; n < NT; ++n) {
             float y[4];
 #pragma unroll
-            for (int e = 0; e < 4; ++e) y[e] = (e < 2 ? k0 : k1) ? (x[n][0][e] + x[n][1][e]) * sc : -INFINITY;
+            for (int e = 0; e < 4; ++e) {
+                float v = x[n][0][e] + x[n][1][e];
+                if (kWays == 4) v += x[n][kWays - 2][e] + x[n][kWays - 1][e];
+                y[e] = (e < 2 ? k0 : k1) ? v * sc : -INFINITY;
+            }
             float p[4], corr[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
@@ -357,25 +373,33 @@ __global__ void __launch_bounds__(kPaThreads) paged_attention_kernel(PagedAttnAr
             }
         }
         // ---- weighted values
+        cp_wait<kHalves - 2>();
+        __syncwarp();
+        issue(kHalves & 1);  // into the half that these keys left
         {
             const int r = (lane & 7) + ((lane >> 4) << 3), ch = (lane >> 3) & 1;
 #pragma unroll
-            for (int k = 0; k < kKs; ++k) {
-                uint32_t f[4];
-                ldsm4t(f, vs + r * C::kRow + (((2 * k + ch) ^ (r & 7)) << 4));
+            for (int k = 0; k < kKs; k += 2) {
+                uint32_t f[2][4];
+                ldsm4t(f[0], from + r * C::kRow + (((2 * k + ch) ^ (r & 7)) << 4));
+                ldsm4t(f[1], from + r * C::kRow + (((2 * k + 2 + ch) ^ (r & 7)) << 4));
 #pragma unroll
                 for (int n = 0; n < NT; ++n) {
-                    pa_mma<DT>(acc[n][k], f, ph[n][0], ph[n][1]);
-                    pa_mma<DT>(acc[n][k], f, pl[n][0], pl[n][1]);
+                    pa_mma<DT>(acc[n][k], f[0], ph[n][0], ph[n][1]);
+                    pa_mma<DT>(acc[n][k + 1], f[1], ph[n][0], ph[n][1]);
+                }
+#pragma unroll
+                for (int n = 0; n < NT; ++n) {
+                    pa_mma<DT>(acc[n][k], f[0], pl[n][0], pl[n][1]);
+                    pa_mma<DT>(acc[n][k + 1], f[1], pl[n][0], pl[n][1]);
                 }
             }
         }
-        stage = stage + 1 == kStages ? 0 : stage + 1;
+        from = from + kTile == ring + kHalves * kTile ? ring : from + kTile;
 
         // ---- the end of a unit, or of this CTA's part of it
         const bool last = cur.r + 1 == cur.rounds;
         if (last || i + 1 == left) {
-            float* buf = reinterpret_cast<float*>(smem + C::kRing);  // [2][kHeads][D]
 #pragma unroll
             for (int n = 0; n < NT; ++n)
 #pragma unroll
@@ -393,36 +417,46 @@ __global__ void __launch_bounds__(kPaThreads) paged_attention_kernel(PagedAttnAr
                 for (int e = 0; e < 2; ++e) {
                     float top = -INFINITY;
 #pragma unroll
-                    for (int w = 0; w < kPaWarps; ++w) top = fmaxf(top, sm_m[w][n * 8 + q4 * 2 + e]);
+                    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm_m[w][n * 8 + q4 * 2 + e]);
                     f[n][e] = ex2(m[n][e] - (top == -INFINITY ? 0.f : top));
                 }
-            // element (head 8 n + 2 q4 + e, value 16 k + g + 8 r): warps 2 and 3, then 1, then 0
-            auto each = [&](auto&& fn) {
+            // element (head 8 n + 2 q4 + e, value 16 k + g + 8 r). At the end of the range every warp has a buffer,
+            // its ring; before, the ring is being filled, and the warps of each parity take turns at one.
+            const bool end = i + 1 == left;
+            float* bufs = reinterpret_cast<float*>(end ? smem : smem + C::kRing);
+            const int n_bufs = end ? kWarps : 2, apart = end ? kHalves * kTile / 4 : kHeads * D;
+            float* mybuf = bufs + (end ? warp : warp & 1) * apart;
+#pragma unroll 1
+            for (int turn = 0; turn < (end ? 1 : kWarps / 2); ++turn) {
+                if (end || warp / 2 == turn) {
 #pragma unroll
-                for (int n = 0; n < NT; ++n)
+                    for (int n = 0; n < NT; ++n)
 #pragma unroll
-                    for (int k = 0; k < kKs; ++k)
+                        for (int k = 0; k < kKs; ++k)
 #pragma unroll
-                        for (int e = 0; e < 4; ++e)
-                            fn(acc[n][k][e] * f[n][e & 1], (n * 8 + q4 * 2 + (e & 1)) * D + k * 16 + g + (e >> 1) * 8);
-            };
-            if (warp >= 2) each([&](float v, int at) { buf[(warp - 2) * kHeads * D + at] = v; });
-            __syncthreads();
-            if (warp == 1) each([&](float v, int at) { buf[kHeads * D + at] += v; });
-            if (warp == 0) each([&](float v, int at) { buf[at] += v; });
-            __syncthreads();
+                            for (int e = 0; e < 4; ++e) {
+                                const int at = (n * 8 + q4 * 2 + (e & 1)) * D + k * 16 + g + (e >> 1) * 8;
+                                const float v = acc[n][k][e] * f[n][e & 1];
+                                mybuf[at] = turn == 0 ? v : mybuf[at] + v;
+                            }
+                }
+                __syncthreads();
+            }
             const bool whole = last && piece_r0 == 0;
             const long long slot = 2ll * blockIdx.x + (piece_r0 == 0 ? 1 : 0);
-            for (int at = t * 2; at < nh * D; at += kPaThreads * 2) {
+            for (int at = t * 2; at < nh * D; at += kThreads * 2) {
                 const int h = at / D;
-                const float v0 = buf[at] + buf[kHeads * D + at], v1 = buf[at + 1] + buf[kHeads * D + at + 1];
+                float v0 = 0.f, v1 = 0.f;
+                for (int w = 0; w < n_bufs; ++w) {
+                    const float2 o = *reinterpret_cast<const float2*>(bufs + w * apart + at);
+                    v0 += o.x, v1 += o.y;
+                }
                 if (whole) {
                     float top = -INFINITY, sum = 0.f;
 #pragma unroll
-                    for (int w = 0; w < kPaWarps; ++w) top = fmaxf(top, sm_m[w][h]);
+                    for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm_m[w][h]);
 #pragma unroll
-                    for (int w = 0; w < kPaWarps; ++w)
-                        sum += sm_l[w][h] * ex2(sm_m[w][h] - (top == -INFINITY ? 0.f : top));
+                    for (int w = 0; w < kWarps; ++w) sum += sm_l[w][h] * ex2(sm_m[w][h] - (top == -INFINITY ? 0.f : top));
                     const float inv = sum == 0.f ? 0.f : 1.f / sum;
                     *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + ((long long)cur.b * a.Hq + h0) * D + at) =
                         pa_pack<DT>(v0 * inv, v1 * inv);
@@ -433,9 +467,9 @@ __global__ void __launch_bounds__(kPaThreads) paged_attention_kernel(PagedAttnAr
             if (t < nh) {
                 float top = -INFINITY, sum = 0.f;
 #pragma unroll
-                for (int w = 0; w < kPaWarps; ++w) top = fmaxf(top, sm_m[w][t]);
+                for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm_m[w][t]);
 #pragma unroll
-                for (int w = 0; w < kPaWarps; ++w) sum += sm_l[w][t] * ex2(sm_m[w][t] - (top == -INFINITY ? 0.f : top));
+                for (int w = 0; w < kWarps; ++w) sum += sm_l[w][t] * ex2(sm_m[w][t] - (top == -INFINITY ? 0.f : top));
                 if (whole) {
                     if (a.lse) a.lse[(long long)cur.b * a.Hq + h0 + t] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
                 } else {
@@ -443,99 +477,116 @@ __global__ void __launch_bounds__(kPaThreads) paged_attention_kernel(PagedAttnAr
                     parts.ml[(slot * 2 + 1) * kHeads + t] = sum;
                 }
             }
-            if (t == 0 && piece_r0 == 0) {
+            if (t == 0 && piece_r0 == 0 && !last) {
                 // the CTA that holds the unit's last round: the largest c with floor(c total / ctas) <= it
-                int2 info = make_int2(0, 0);
-                if (!last) {
-                    const long long end = lo + i + (cur.rounds - 1 - cur.r);
-                    info = make_int2(blockIdx.x, static_cast<int>(((end + 1) * ctas - 1) / total) - static_cast<int>(blockIdx.x) + 1);
-                }
-                parts.units[(long long)cur.b * units + cur.u] = info;
+                const long long end = lo + i + (cur.rounds - 1 - cur.r);
+                const int n = static_cast<int>(((end + 1) * ctas - 1) / total) - static_cast<int>(blockIdx.x) + 1;
+                parts.open[blockIdx.x] = make_int4(cur.b, cur.kvh, cur.tile, n);
             }
             __syncthreads();
             begin = true;
         }
-        cur.next(a, units);
+        cur.template next<kRound>(a, tiles);
     }
 }
 
-// Joins the parts of one (sequence, query head): 64 threads of four values for
-// each of four interleaved sets of parts.
+// Joins the parts of one query head of a unit that lies in several CTAs'
+// ranges: CTA (head of the unit, first CTA of the unit), kSets interleaved sets
+// of parts with D / 4 threads of four values each.
+constexpr int kPaSets = 8;
 template <int DT, int D>
-__global__ void __launch_bounds__(D) paged_attention_join_kernel(PagedAttnArgs a, int tiles, int heads, PaParts parts) {
-    constexpr int kCols = D / 4, kSets = 4;
-    __shared__ float4 sums[kSets][kCols];
+__global__ void __launch_bounds__(kPaSets* D / 4) paged_attention_join_kernel(PagedAttnArgs a, int heads, PaParts parts) {
+    constexpr int kCols = D / 4, kThreads = kPaSets * kCols, kW = kThreads / 32;
+    __shared__ float4 sums[kPaSets][kCols];
+    __shared__ float red[2][kW];
     pdl_wait();
     pdl_trigger();
-    const int h = blockIdx.x, b = blockIdx.y, t = threadIdx.x, col = t % kCols, set = t / kCols;
-    const int group = a.Hq / a.Hkv, kvh = h / group, tile = h % group / heads, hh = h % group % heads;
-    uint16_t* out = static_cast<uint16_t*>(a.out) + ((long long)b * a.Hq + h) * D;
-    if (pa_len(a, b) == 0) {
-        if (set == 0) *reinterpret_cast<uint2*>(out + col * 4) = make_uint2(0u, 0u);
-        if (t == 0 && a.lse) a.lse[(long long)b * a.Hq + h] = -INFINITY;
-        return;
-    }
-    const int2 info = parts.units[((long long)b * a.Hkv + kvh) * tiles + tile];
-    const int n = info.y;
-    if (n == 0) return;
+    const int4 u = parts.open[blockIdx.y];
+    const int n = u.w, hh = blockIdx.x, group = a.Hq / a.Hkv;
+    if (n == 0 || u.z * heads + hh >= group) return;
+    const int t = threadIdx.x, col = t % kCols, set = t / kCols, lane = t & 31, warp = t >> 5;
+    const long long h = (long long)u.x * a.Hq + u.y * group + u.z * heads + hh;
     // the first CTA's part is its second one
-    auto slot = [&](int i) { return 2ll * (info.x + i) + (i == 0 ? 1 : 0); };
+    auto slot = [&](int i) { return 2ll * (blockIdx.y + i) + (i == 0 ? 1 : 0); };
     float top = -INFINITY;
-    for (int i = 0; i < n; ++i) top = fmaxf(top, parts.ml[slot(i) * 2 * heads + hh]);
+    for (int i = t; i < n; i += kThreads) top = fmaxf(top, parts.ml[slot(i) * 2 * heads + hh]);
+#pragma unroll
+    for (int m = 16; m >= 1; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
+    if (lane == 0) red[0][warp] = top;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kW; ++w) top = fmaxf(top, red[0][w]);
     const float base = top == -INFINITY ? 0.f : top;
     float sum = 0.f;
-    for (int i = 0; i < n; ++i)
+    for (int i = t; i < n; i += kThreads)
         sum += parts.ml[(slot(i) * 2 + 1) * heads + hh] * ex2(parts.ml[slot(i) * 2 * heads + hh] - base);
+#pragma unroll
+    for (int m = 16; m >= 1; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
+    if (lane == 0) red[1][warp] = sum;
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
-    for (int i = set; i < n; i += kSets) {
+    for (int i = set; i < n; i += kPaSets) {
         const float f = ex2(parts.ml[slot(i) * 2 * heads + hh] - base);
         const float4 p = *reinterpret_cast<const float4*>(parts.acc + (slot(i) * heads + hh) * D + col * 4);
         v.x += f * p.x, v.y += f * p.y, v.z += f * p.z, v.w += f * p.w;
     }
     sums[set][col] = v;
     __syncthreads();
-    if (set == 0) {
-        for (int s = 1; s < kSets; ++s) {
-            const float4 o = sums[s][col];
-            v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
-        }
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        *reinterpret_cast<uint2*>(out + col * 4) = make_uint2(pa_pack<DT>(v.x * inv, v.y * inv), pa_pack<DT>(v.z * inv, v.w * inv));
+    if (set != 0) return;
+    sum = 0.f;
+#pragma unroll
+    for (int w = 0; w < kW; ++w) sum += red[1][w];
+#pragma unroll
+    for (int s = 1; s < kPaSets; ++s) {
+        const float4 o = sums[s][col];
+        v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
     }
-    if (t == 0 && a.lse) a.lse[(long long)b * a.Hq + h] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+    const float inv = sum == 0.f ? 0.f : 1.f / sum;
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + h * D + col * 4) =
+        make_uint2(pa_pack<DT>(v.x * inv, v.y * inv), pa_pack<DT>(v.z * inv, v.w * inv));
+    if (t == 0 && a.lse) a.lse[h] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
 }
 
 struct PaPlan {
     int nt, heads, tiles, ctas;
-    size_t acc, ml, units, total;
+    size_t acc, ml, open, total;
 };
-PaPlan pa_plan(int B, int Hq, int Hkv, int d) {
+template <int D>
+int pa_ctas(int nt) {
+    return kSms * (nt == 1 ? PaCfg<D, 1>::kCtas : PaCfg<D, 2>::kCtas);
+}
+PaPlan pa_plan(int Hq, int Hkv, int d) {
     PaPlan p{};
     const int group = Hq / Hkv;
     p.nt = group <= 8 ? 1 : 2;
     p.heads = 8 * p.nt;
     p.tiles = (group + p.heads - 1) / p.heads;
-    p.ctas = kSms * (d == 256 ? PaCfg<256>::kCtas : d == 128 ? PaCfg<128>::kCtas : PaCfg<64>::kCtas);
+    p.ctas = d == 256 ? pa_ctas<256>(p.nt) : d == 128 ? pa_ctas<128>(p.nt) : pa_ctas<64>(p.nt);
     p.acc = 0;
     p.ml = p.acc + static_cast<size_t>(2) * p.ctas * p.heads * d * 4;
-    p.units = p.ml + static_cast<size_t>(2) * p.ctas * 2 * p.heads * 4;
-    p.total = p.units + static_cast<size_t>(B) * Hkv * p.tiles * sizeof(int2);
+    p.open = p.ml + static_cast<size_t>(2) * p.ctas * 2 * p.heads * 4;
+    p.total = p.open + static_cast<size_t>(p.ctas) * sizeof(int4);
     return p;
+}
+PaDiv pa_div(int d) {
+    int l = 0;
+    while ((1ll << l) < d) ++l;
+    return PaDiv{static_cast<uint32_t>(((1ull << (31 + l)) + d - 1) / d), 31 + l};
 }
 
 template <int DT, int D, int NT>
 cudaError_t launch_nt(const PagedAttnArgs& a, const PaPlan& p, const PaParts& parts, cudaStream_t s) {
+    using C = PaCfg<D, NT>;
     const void* f = reinterpret_cast<const void*>(paged_attention_kernel<DT, D, NT>);
-    constexpr int smem = pa_smem<D, NT>();
-    cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     int tiles = p.tiles, heads = p.heads;
-    void* args[] = {const_cast<PagedAttnArgs*>(&a), &tiles, const_cast<PaParts*>(&parts)};
-    e = launch_kernel(f, dim3(p.ctas), dim3(kPaThreads), smem, true, s, args);
+    PaDiv div = pa_div(a.page);
+    void* args[] = {const_cast<PagedAttnArgs*>(&a), &tiles, &div, const_cast<PaParts*>(&parts)};
+    e = launch_kernel(f, dim3(p.ctas), dim3(C::kThreads), C::kSmem, true, s, args);
     if (e != cudaSuccess) return e;
-    void* jargs[] = {const_cast<PagedAttnArgs*>(&a), &tiles, &heads, const_cast<PaParts*>(&parts)};
-    return launch_kernel(reinterpret_cast<const void*>(paged_attention_join_kernel<DT, D>), dim3(a.Hq, a.B), dim3(D), 0, true, s,
+    void* jargs[] = {const_cast<PagedAttnArgs*>(&a), &heads, const_cast<PaParts*>(&parts)};
+    return launch_kernel(reinterpret_cast<const void*>(paged_attention_join_kernel<DT, D>), dim3(p.heads, p.ctas), dim3(kPaSets * D / 4), 0, true, s,
                          jargs);
 }
 
@@ -549,15 +600,15 @@ cudaError_t launch_dt(const PagedAttnArgs& a, const PaPlan& p, const PaParts& pa
 }  // namespace
 
 size_t paged_attention_ws_bytes(int B, int Hq, int Hkv, int d, int max_len) {
-    (void)max_len;
-    return pa_plan(B, Hq, Hkv, d).total;
+    (void)B, (void)max_len;
+    return pa_plan(Hq, Hkv, d).total;
 }
 
 cudaError_t launch_paged_attention(const PagedAttnArgs& a, int dtype, void* ws, cudaStream_t s) {
-    const PaPlan p = pa_plan(a.B, a.Hq, a.Hkv, a.d);
+    const PaPlan p = pa_plan(a.Hq, a.Hkv, a.d);
     char* w = static_cast<char*>(ws);
     const PaParts parts{reinterpret_cast<float*>(w + p.acc), reinterpret_cast<float*>(w + p.ml),
-                        reinterpret_cast<int2*>(w + p.units)};
+                        reinterpret_cast<int4*>(w + p.open)};
     return dtype == 1 ? launch_dt<1>(a, p, parts, s) : launch_dt<2>(a, p, parts, s);
 }
 

@@ -510,7 +510,8 @@ int escha_moe_route(const escha_moe_layer* L, const uint16_t* x, int T, uint16_t
  * sums and weighted values are held in f32 and out is rounded once.
  *   q        [B][Hq][d];  dtype ESCHA_F16 or ESCHA_BF16, of q, both pools,
  *            k_new, v_new and out
- *   k_pool, v_pool  [n_pages][Hkv][page][d], two buffers; any page >= 1
+ *   k_pool, v_pool  [n_pages][Hkv][page][d], two buffers; any page >= 1,
+ *            n_pages * Hkv * page below 2^31
  *   table    int32 [B][max_pages]; an entry outside [0, n_pages) is a page of
  *            no keys: its positions are left out (a dropped page, say)
  *   lens     int32 [B], the new token counted; below 0 counts as 0, above

@@ -37,6 +37,7 @@ def test_paged_attention_validation():
                      (E.ESCHA_E_ARG, dict(scale=float("inf"))), (E.ESCHA_E_ARG, dict(scale=float("nan"))),
                      (E.ESCHA_E_SHAPE, dict(d=96)), (E.ESCHA_E_SHAPE, dict(Hq=15)), (E.ESCHA_E_SHAPE, dict(Hq=130)),
                      (E.ESCHA_E_SHAPE, dict(B=65536)), (E.ESCHA_E_SHAPE, dict(Hq=2048, Hkv=2048)),
+                     (E.ESCHA_E_SHAPE, dict(n=1 << 24, page=64)),
                      (E.ESCHA_E_ALIGN, dict(q=G + 8)), (E.ESCHA_E_ALIGN, dict(lens=G + 4)),
                      (E.ESCHA_E_ALIGN, dict(lse=G + 4)), (E.ESCHA_E_ALIGN, dict(kn=G, vn=G + 2))):
         assert call(**kw) == code, kw

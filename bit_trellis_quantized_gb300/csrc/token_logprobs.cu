@@ -1,20 +1,35 @@
 // Log probabilities of given tokens, the entropy and the top alternatives of
 // rows of logits, in one pass over them.
 //
-// Per row, with m a running maximum, s = sum e^(x - m), t = sum (x - m) e^(x - m):
-//   lse = m + ln s,  logprob(id) = (x_id - m) - ln s,  entropy = ln s - t / s.
-// Two parts (m1, s1, t1), (m2, s2, t2) join over M = max(m1, m2) with f = e^(m1 - M):
-//   s = f s1 + ..., t = f (t1 + (m1 - M) s1) + ...
+// Per row, in units of ln 2: with c = log2 e, m a running maximum, M = c m, and
+// z_i = c x_i - M:  s = sum 2^z_i,  t = sum z_i 2^z_i,
+//   lse = ln2 (M + log2 s),  logprob(id) = ln2 (z_id - log2 s),
+//   entropy = ln2 (log2 s - t / s).
+// z is one fma with M rounded; as everything goes by that M, its rounding
+// cancels. Where |m| is 1e37 or more (c x may overflow), z = (x - m) c.
+// Two parts join over the larger maximum, f = 2^(M1 - M):
+//   s = f s1 + ...,  t = f (t1 + (M1 - M) s1) + ...
 // All in f32; m starts at the lowest finite value, so -inf logits (banned
 // tokens) add nothing and a row of them alone ends with s = 0.
 //
 // The top alternatives go by one 64-bit key per logit, (value, lower index
-// first): each warp keeps the best 32 of what it has seen, one per lane in
-// order, and looks closer only at a batch whose largest value reaches the
-// top-th best so far.
+// first). A bound from below for the top-th value comes from the first chunk of
+// each warp, out of the lanes' maxima: with q of the 8 warps having p lanes at
+// or above a value, p q >= top values are. What reaches it, a few hundred
+// values of a row in no order, is collected in shared memory. At the end the
+// same bound over what was collected leaves a few more keys than asked for, and
+// each of them counts those above it. Where the buffer is full (a row that
+// ascends, a row of one value) a warp keeps the best 32 of the rest in order,
+// one a lane. Keeping such lists throughout cost more than all else: 250 us
+// where this takes 193 (2048 rows of 152064, top 8; 187 without any).
 //
-// Bound: one read of the logits. A row is split over CTAs until the grid fills
-// the GPU; a second kernel then joins the parts of a row.
+// Bound: one read of the logits. Each lane loads a chunk ahead, and the
+// arithmetic is 5 instructions a value (pairs of f32 where there is an
+// instruction for them), so that it stays behind the loads. All rows, one after
+// another, are cut into equal ranges, one a CTA; a second kernel joins the
+// parts of rows that lie in several.
+#include <algorithm>
+
 #include "common.cuh"
 #include "context.h"
 #include "kernels.h"
@@ -28,13 +43,21 @@ constexpr int kLpThreads = 256;
 constexpr int kLpWarps = kLpThreads / 32;
 constexpr float kLowest = -3.402823466e38f;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+constexpr int kLpValues = 32;  // of a lane's chunk
 
 struct LpPart {
     float m, s, t;
 };
-struct LpRecord {  // one split of a row
+struct LpRecord {  // a part of a row
     float m, s, t, pad;
     unsigned long long key[kLogprobMaxTop];
+};
+// Where parts go: two records a CTA (a row that began before its range; one
+// that goes on behind it) and that last row with the number of its parts.
+struct LpParts {
+    LpRecord* rec;  // [G][2]
+    int2* open;     // [G]
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -43,11 +66,24 @@ __device__ __forceinline__ float ex2(float x) {
     return r;
 }
 
+constexpr float kFar = 1e37f;
+
+// M: always this rounded product (never contracted into a sum), see above.
+__device__ __forceinline__ float lp_scaled(float m) { return __fmul_rn(m, kLog2e); }
+// c x - M in units of ln 2
+__device__ __forceinline__ float lp_z(float x, float m) {
+    return fabsf(m) < kFar ? fmaf(x, kLog2e, -lp_scaled(m)) : (x - m) * kLog2e;
+}
+// the same between two maxima
+__device__ __forceinline__ float lp_shift(float a, float m) {
+    return fabsf(a) < kFar && fabsf(m) < kFar ? lp_scaled(a) - lp_scaled(m) : (a - m) * kLog2e;
+}
+
 __device__ __forceinline__ LpPart lp_join(const LpPart& a, const LpPart& b) {
     LpPart r;
     r.m = fmaxf(a.m, b.m);
-    const float da = a.m - r.m, db = b.m - r.m;
-    const float fa = ex2(da * kLog2e), fb = ex2(db * kLog2e);
+    const float da = lp_shift(a.m, r.m), db = lp_shift(b.m, r.m);
+    const float fa = ex2(da), fb = ex2(db);
     r.s = a.s * fa + b.s * fb;
     // a factor of 0 leaves nothing of t (its difference may be infinite)
     r.t = (fa == 0.f ? 0.f : fa * (a.t + da * a.s)) + (fb == 0.f ? 0.f : fb * (b.t + db * b.s));
@@ -63,10 +99,14 @@ __device__ __forceinline__ unsigned lp_order(float x) {
 __device__ __forceinline__ unsigned long long lp_key(float x, int i) {
     return (static_cast<unsigned long long>(lp_order(x)) << 32) | static_cast<unsigned>(~i);
 }
+__device__ __forceinline__ float lp_from_order(unsigned o) {
+    return __uint_as_float((o & 0x80000000u) ? (o & 0x7FFFFFFFu) : ~o);
+}
+
 __device__ __forceinline__ float lp_value(unsigned long long key) {
     const unsigned o = static_cast<unsigned>(key >> 32);
     if (key == 0) return -INFINITY;
-    return o == 0xFFFFFFFFu ? __uint_as_float(0x7FC00000u) : __uint_as_float((o & 0x80000000u) ? (o & 0x7FFFFFFFu) : ~o);
+    return o == 0xFFFFFFFFu ? __uint_as_float(0x7FC00000u) : lp_from_order(o);
 }
 
 // The warp's best 32 keys, best first by lane; `c` is the same in all lanes.
@@ -82,6 +122,8 @@ struct LpVec;
 template <>
 struct LpVec<3> {
     static constexpr int N = 4;
+    static constexpr unsigned kNone = 0xFF800000u;  // -inf
+    __device__ static uint4 two(float a, float b) { return make_uint4(__float_as_uint(a), __float_as_uint(b), kNone, kNone); }
     __device__ static void get(const uint4& r, float* x) {
         x[0] = __uint_as_float(r.x), x[1] = __uint_as_float(r.y), x[2] = __uint_as_float(r.z), x[3] = __uint_as_float(r.w);
     }
@@ -90,6 +132,11 @@ struct LpVec<3> {
 template <>
 struct LpVec<1> {
     static constexpr int N = 8;
+    static constexpr unsigned kNone = 0xFC00FC00u;
+    __device__ static uint4 two(float a, float b) {
+        const __half2 h = __floats2half2_rn(a, b);  // exact: both come from this type
+        return make_uint4(*reinterpret_cast<const unsigned*>(&h), kNone, kNone, kNone);
+    }
     __device__ static void get(const uint4& r, float* x) {
         const unsigned w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
@@ -103,6 +150,10 @@ struct LpVec<1> {
 template <>
 struct LpVec<2> {
     static constexpr int N = 8;
+    static constexpr unsigned kNone = 0xFF80FF80u;
+    __device__ static uint4 two(float a, float b) {
+        return make_uint4((__float_as_uint(a) >> 16) | (__float_as_uint(b) & 0xFFFF0000u), kNone, kNone, kNone);
+    }
     __device__ static void get(const uint4& r, float* x) {
         const unsigned w[4] = {r.x, r.y, r.z, r.w};
 #pragma unroll
@@ -115,103 +166,278 @@ struct LpVec<2> {
 // A warp's state over the values it has seen.
 struct LpWarp {
     LpPart p;
-    unsigned long long mine;
-    float thr;  // a batch below this holds no top value
+    unsigned long long mine;  // by lane: the best of what the buffer had no place for
+    float thr;                // values below this are not among the top ones
 };
 
-// N values of consecutive indexes i0.. per lane (those below `ok` count).
-template <int N>
-__device__ __forceinline__ void lp_batch(LpWarp& w, const float (&x)[N], int i0, int ok, int top, int lane) {
-    float b = kLowest;
+// The lanes' values in descending order.
+__device__ __forceinline__ unsigned lp_sort(unsigned v, int lane) {
 #pragma unroll
-    for (int j = 0; j < N; ++j) b = j < ok ? fmaxf(b, x[j]) : b;
-    if (b > w.p.m) {
-        const float d = w.p.m - b, f = ex2(d * kLog2e);
-        w.p.t = f == 0.f ? 0.f : f * (w.p.t + d * w.p.s);
-        w.p.s *= f;
-        w.p.m = b;
+    for (int k = 2; k <= 32; k <<= 1)
+#pragma unroll
+        for (int j = k >> 1; j > 0; j >>= 1) {
+            const unsigned o = __shfl_xor_sync(0xffffffffu, v, j);
+            // descending within blocks of k whose bit k is 0
+            v = ((lane & j) == 0) == ((lane & k) == 0) ? max(v, o) : min(v, o);
+        }
+    return v;
+}
+
+// A value that `top` of the threads' values v (in lp_order) reach: the q-th largest of the warps' p-th largest,
+// p q >= top. All threads of the CTA call it; `slots` may be written again after the next __syncthreads.
+__device__ __forceinline__ unsigned lp_bound(unsigned v, int top, unsigned* slots, int lane, int warp) {
+    const int p = (top + 3) / 4, q = (top + p - 1) / p;  // top <= 32: p <= 8, q <= 4
+    v = __shfl_sync(0xffffffffu, lp_sort(v, lane), p - 1);
+    if (lane == 0) slots[warp] = v;
+    __syncthreads();
+    v = lane < kLpWarps ? slots[lane] : 0u;
+    int above = 0;
+#pragma unroll
+    for (int j = 0; j < kLpWarps; ++j) {
+        const unsigned o = __shfl_sync(0xffffffffu, v, j);
+        above += o > v || (o == v && j < lane);
     }
+    return __shfl_sync(0xffffffffu, v, __ffs(__ballot_sync(0xffffffffu, lane < kLpWarps && above == q - 1)) - 1);
+}
+
+__device__ __forceinline__ unsigned long long pack2(float a, float b) {
+    unsigned long long r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(a), "f"(b));
+    return r;
+}
+__device__ __forceinline__ void unpack2(unsigned long long v, float& a, float& b) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(a), "=f"(b) : "l"(v));
+}
+__device__ __forceinline__ unsigned long long fma2(unsigned long long a, unsigned long long b, unsigned long long c) {
+    unsigned long long r;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(r) : "l"(a), "l"(b), "l"(c));
+    return r;
+}
+__device__ __forceinline__ unsigned long long add2(unsigned long long a, unsigned long long b) {
+    unsigned long long r;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(a), "l"(b));
+    return r;
+}
+// max that keeps a NaN of a
+__device__ __forceinline__ float max_nan(float a, float b) {
+    float r;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
+    return r;
+}
+
+// Adds a chunk, kLpValues values of each lane (places past the end hold -inf), to the lane's sums; vmax: its
+// vectors' maxima. `buf`: the warp's 32 kLpValues / N vectors of shared memory.
+template <int DT>
+__device__ __forceinline__ float lp_sums(LpPart& p, const uint4 (&r)[kLpValues / LpVec<DT>::N],
+                                         float (&vmax)[kLpValues / LpVec<DT>::N], uint4* buf, int lane) {
+    using V = LpVec<DT>;
+    constexpr int N = V::N, kLpLoads = kLpValues / N;
+    float b = -INFINITY;
 #pragma unroll
-    for (int j = 0; j < N; ++j) {
-        if (j < ok) {
-            const float y = x[j] - w.p.m, e = ex2(y * kLog2e);
-            w.p.s += e;
-            w.p.t += fmaxf(y, kLowest) * e;
+    for (int i = 0; i < kLpLoads; ++i) {
+        float x[N];
+        V::get(r[i], x);
+        vmax[i] = fmaxf(x[0], x[1]);
+#pragma unroll
+        for (int j = 2; j < N; j += 2) vmax[i] = fmaxf(vmax[i], fmaxf(x[j], x[j + 1]));
+        b = fmaxf(b, vmax[i]);
+    }
+    if (b > p.m) {
+        const float d = lp_shift(p.m, b), f = ex2(d);
+        p.t = f == 0.f ? 0.f : f * (p.t + d * p.s);
+        p.s *= f;
+        p.m = b;
+    }
+    const bool empty = b == -INFINITY && p.m == kLowest;  // this lane has seen nothing but -inf (or NaN)
+    if (!__any_sync(0xffffffffu, !empty && !(fabsf(p.m) < kFar))) {
+        const float M = empty ? 0.f : lp_scaled(p.m);
+        const unsigned long long c2 = pack2(kLog2e, kLog2e), m2 = pack2(-M, -M);
+        unsigned long long s2 = 0ull, t2 = 0ull;
+#pragma unroll
+        for (int i = 0; i < kLpLoads; ++i) {
+            float x[N];
+            V::get(r[i], x);
+#pragma unroll
+            for (int j = 0; j < N; j += 2) {
+                float z0, z1;
+                unpack2(fma2(pack2(x[j], x[j + 1]), c2, m2), z0, z1);
+                z0 = max_nan(z0, -160.f), z1 = max_nan(z1, -160.f);  // 2^-160 is 0: -inf times it would not be
+                const unsigned long long e = pack2(ex2(z0), ex2(z1));
+                s2 = add2(s2, e);
+                t2 = fma2(pack2(z0, z1), e, t2);
+            }
+        }
+        float s0, s1, t0, t1;
+        unpack2(s2, s0, s1);
+        unpack2(t2, t0, t1);
+        p.s += s0 + s1;
+        p.t += t0 + t1;
+    } else {
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < kLpLoads; ++i) buf[i * 32 + lane] = r[i];
+        __syncwarp();
+#pragma unroll 1
+        for (int i = 0; i < kLpLoads; ++i) {
+            float x[N];
+            V::get(buf[i * 32 + lane], x);
+#pragma unroll
+            for (int j = 0; j < N; ++j) {
+                const float z = max_nan(lp_z(x[j], p.m), -160.f), e = ex2(z);
+                p.s += e;
+                p.t += z * e;
+            }
         }
     }
-    if (top == 0) return;
-    // a NaN in s: the maximum may have passed over a NaN
-    if (__any_sync(0xffffffffu, ok > 0 && (b >= w.thr || w.p.s != w.p.s))) {
+    return b;
+}
+
+// What was collected of a row's part, in no order.
+constexpr int kLpKept = 1024;
+struct LpKept {
+    unsigned long long key[kLpKept + kLpThreads];  // at the end the warps' lists behind it
+    int count;  // of all that came, beyond kLpKept too
+};
+
+// Collects a chunk's values that reach w.thr, in `kept` (kPlaces of them) or the warp's list. `index(i, j)` is the
+// index of value j of the lane's vector i, or -1 for a place past the end.
+template <int DT, int kPlaces, typename F>
+__device__ __forceinline__ void lp_collect(LpWarp& w, const uint4 (&r)[kLpValues / LpVec<DT>::N],
+                                           const float (&vmax)[kLpValues / LpVec<DT>::N], uint4* buf, LpKept* kept, int top,
+                                           int lane, F&& index) {
+    using V = LpVec<DT>;
+    constexpr int N = V::N, kLpLoads = kLpValues / N;
+    // a NaN in the sums: a maximum may have passed over one
+    const float thr = w.p.s != w.p.s ? -INFINITY : w.thr;
+    unsigned over = 0;  // values that found no place
+#pragma unroll
+    for (int i = 0; i < kLpLoads; ++i) {
+        if (!__any_sync(0xffffffffu, !(vmax[i] < thr))) continue;
+        float x[N];
+        V::get(r[i], x);
 #pragma unroll
         for (int j = 0; j < N; ++j) {
-            const unsigned long long key = j < ok ? lp_key(x[j], i0 + j) : 0ull;
-            unsigned long long last = __shfl_sync(0xffffffffu, w.mine, top - 1);
-            unsigned todo = __ballot_sync(0xffffffffu, key > last);
-            while (todo) {
-                const int src = __ffs(todo) - 1;
-                todo &= todo - 1;
-                const unsigned long long c = __shfl_sync(0xffffffffu, key, src);
-                if (c > last) {
-                    lp_insert(w.mine, c, lane);
-                    last = __shfl_sync(0xffffffffu, w.mine, top - 1);
+            if (!(x[j] < thr)) {
+                const int id = index(i, j);
+                if (id >= 0) {
+                    const int at = kPlaces > 0 ? atomicAdd(&kept->count, 1) : 0;
+                    if (at < kPlaces)
+                        kept->key[at] = lp_key(x[j], id);
+                    else
+                        over |= 1u << (i * N + j);
                 }
             }
         }
-        w.thr = lp_value(__shfl_sync(0xffffffffu, w.mine, top - 1));
     }
-}
-
-// Joins the warps' states of a CTA; warp 0 holds the result.
-__device__ __forceinline__ void lp_join_cta(LpWarp& w, int top, int lane, int warp) {
-    __shared__ LpPart parts[kLpWarps];
-    __shared__ unsigned long long keys[kLpWarps][kLogprobMaxTop];
+    if (!__any_sync(0xffffffffu, over != 0)) return;
+    __syncwarp();
 #pragma unroll
-    for (int m = 16; m >= 1; m >>= 1) {
-        LpPart o;
-        o.m = __shfl_xor_sync(0xffffffffu, w.p.m, m);
-        o.s = __shfl_xor_sync(0xffffffffu, w.p.s, m);
-        o.t = __shfl_xor_sync(0xffffffffu, w.p.t, m);
-        // the same order of the operands in both lanes
-        w.p = (lane & m) ? lp_join(o, w.p) : lp_join(w.p, o);
-    }
-    if (lane == 0) parts[warp] = w.p;
-    keys[warp][lane] = w.mine;
-    __syncthreads();
-    if (warp != 0) return;
-    for (int i = 1; i < kLpWarps; ++i) w.p = lp_join(w.p, parts[i]);
-    if (top > 0) {
-        for (int i = 1; i < kLpWarps; ++i) {
-            const unsigned long long theirs = keys[i][lane];
-            for (int j = 0; j < top; ++j) {
-                const unsigned long long c = __shfl_sync(0xffffffffu, theirs, j);
-                if (c <= __shfl_sync(0xffffffffu, w.mine, top - 1)) break;
+    for (int i = 0; i < kLpLoads; ++i) buf[i * 32 + lane] = r[i];
+    __syncwarp();
+    unsigned long long last = __shfl_sync(0xffffffffu, w.mine, top - 1);
+#pragma unroll 1
+    for (int k = 0; k < kLpValues; ++k) {
+        const bool mine = (over >> k) & 1u;
+        if (!__any_sync(0xffffffffu, mine)) continue;
+        const float x = V::one(buf + (k / N) * 32 + lane, k % N);
+        const unsigned long long key = mine ? lp_key(x, index(k / N, k % N)) : 0ull;
+        unsigned todo = __ballot_sync(0xffffffffu, key > last);
+        while (todo) {
+            const int src = __ffs(todo) - 1;
+            todo &= todo - 1;
+            const unsigned long long c = __shfl_sync(0xffffffffu, key, src);
+            if (c > last) {
                 lp_insert(w.mine, c, lane);
+                last = __shfl_sync(0xffffffffu, w.mine, top - 1);
             }
         }
+    }
+    w.thr = fmaxf(w.thr, lp_value(last));
+}
+
+// lp_bound over n keys in shared memory, spread over the warps.
+__device__ __forceinline__ unsigned lp_keys_bound(const unsigned long long* keys, int n, int top, unsigned* slots, int lane,
+                                                  int warp) {
+    unsigned most = 0u;
+    for (int i = lane * kLpWarps + warp; i < n; i += kLpThreads) most = max(most, static_cast<unsigned>(keys[i] >> 32));
+    return lp_bound(most, top, slots, lane, warp);
+}
+
+// The best `top` of n distinct keys (0: none) in shared memory, in order, to `best`; `work` holds n keys. All
+// threads of the CTA call it; `best` can be read after it.
+__device__ __forceinline__ void lp_select(const unsigned long long* keys, int n, int top, unsigned long long* work,
+                                          unsigned long long* best, int lane, int warp) {
+    __shared__ unsigned slots[kLpWarps];
+    __shared__ int count;
+    const int t = threadIdx.x;
+    if (t == 0) count = 0;
+    if (t < kLogprobMaxTop) best[t] = 0ull;
+    const unsigned bound = lp_keys_bound(keys, n, top, slots, lane, warp);
+    for (int i = t; i < n; i += kLpThreads)
+        if (keys[i] != 0ull && static_cast<unsigned>(keys[i] >> 32) >= bound) work[atomicAdd(&count, 1)] = keys[i];
+    __syncthreads();
+    const int left = count;
+    for (int i = t; i < left; i += kLpThreads) {
+        const unsigned long long mine = work[i];
+        int above = 0;
+        for (int j = 0; j < left; ++j) above += work[j] > mine;
+        if (above < top) best[above] = mine;
+    }
+    __syncthreads();
+}
+
+// Joins the warp's sums: the maximum, then everybody's parts over it.
+__device__ __forceinline__ void lp_join_warp(LpPart& p) {
+    float m = p.m;
+#pragma unroll
+    for (int k = 16; k >= 1; k >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
+    const float d = lp_shift(p.m, m), f = ex2(d);
+    p.t = f == 0.f ? 0.f : f * (p.t + d * p.s);
+    p.s *= f;
+    p.m = m;
+#pragma unroll
+    for (int k = 16; k >= 1; k >>= 1) {
+        p.s += __shfl_xor_sync(0xffffffffu, p.s, k);
+        p.t += __shfl_xor_sync(0xffffffffu, p.t, k);
+    }
+}
+// Joins the sums of the CTA's threads; warp 0 holds the result.
+__device__ __forceinline__ void lp_join_sums(LpPart& p, int lane, int warp) {
+    __shared__ LpPart parts[kLpWarps];
+    lp_join_warp(p);
+    if (lane == 0) parts[warp] = p;
+    __syncthreads();
+    if (warp == 0) {
+        p = lane < kLpWarps ? parts[lane] : LpPart{kLowest, 0.f, 0.f};
+        lp_join_warp(p);
     }
 }
 
 template <int DT>
-__device__ __forceinline__ void lp_finish(const LogprobArgs& a, int row, const LpWarp& w, int lane) {
-    const float ls = logf(w.p.s);
-    const bool none = w.p.s == 0.f;  // every logit is -inf
+__device__ __forceinline__ void lp_finish(const LogprobArgs& a, int row, const LpPart& p, unsigned long long mine, int lane) {
+    const float ls = log2f(p.s);
+    const bool none = p.s == 0.f;  // every logit is -inf
+    auto logprob = [&](float v) {
+        if (none) return -INFINITY;
+        return fabsf(v) < kFar && fabsf(p.m) < kFar ? kLn2 * (lp_z(v, p.m) - ls) : (v - p.m) - kLn2 * ls;
+    };
     if (lane == 0) {
-        if (a.lse) a.lse[row] = none ? -INFINITY : w.p.m + ls;
-        if (a.entropy) a.entropy[row] = none ? 0.f : ls - w.p.t / w.p.s;
+        if (a.lse) a.lse[row] = none ? -INFINITY : fabsf(p.m) < kFar ? kLn2 * (lp_scaled(p.m) + ls) : p.m + kLn2 * ls;
+        if (a.entropy) a.entropy[row] = none ? 0.f : kLn2 * (ls - p.t / p.s);
     }
     const char* x = static_cast<const char*>(a.logits) + (long long)row * a.ld * (DT == 3 ? 4 : 2);
     for (int i = lane; i < a.n_ids; i += 32) {
         const int id = a.ids[(long long)row * a.n_ids + i];
         float r = 0.f;
         if (id >= 0 && id < a.V)
-            r = none ? -INFINITY : (LpVec<DT>::one(x, id) - w.p.m) - ls;
+            r = logprob(LpVec<DT>::one(x, id));
         else if (id != -1)
             r = __uint_as_float(0x7FC00000u);
         a.logprobs[(long long)row * a.n_ids + i] = r;
     }
     if (lane < a.top) {
-        a.top_ids[(long long)row * a.top + lane] = static_cast<int32_t>(~static_cast<unsigned>(w.mine));
-        a.top_logprobs[(long long)row * a.top + lane] = none ? -INFINITY : (lp_value(w.mine) - w.p.m) - ls;
+        a.top_ids[(long long)row * a.top + lane] = static_cast<int32_t>(~static_cast<unsigned>(mine));
+        a.top_logprobs[(long long)row * a.top + lane] = logprob(lp_value(mine));
     }
 }
 
@@ -223,122 +449,265 @@ __device__ __forceinline__ LpWarp lp_start() {
     return w;
 }
 
+constexpr int kLpCtas = 2;  // a multiprocessor, each lane with two chunks of loads in flight
+
+// The rows are taken in units of 32 vectors; all rows' units, in order, are cut
+// into ranges, one a CTA: `per` units, one more for the first `rest` CTAs.
+// Values before a row's first 16-byte boundary and behind its last vector go
+// with the row's first unit.
 template <int DT>
-__global__ void __launch_bounds__(kLpThreads) token_logprobs_kernel(LogprobArgs a, int splits, LpRecord* rec) {
+__global__ void __launch_bounds__(kLpThreads, kLpCtas)
+    token_logprobs_kernel(LogprobArgs a, int units, long long per, int rest, LpParts out) {
     using V = LpVec<DT>;
-    constexpr int N = V::N;
+    constexpr int N = V::N, kLpLoads = kLpValues / N;
     constexpr int size = DT == 3 ? 4 : 2;
+    __shared__ LpKept kept;
+    __shared__ unsigned long long best[kLogprobMaxTop];
+    __shared__ uint4 buf[kLpWarps][kLpLoads * 32];  // by warp; for keys once a part's values are collected
+    __shared__ unsigned slots[kLpWarps];
+    static_assert(sizeof(buf) >= sizeof(kept.key), "the keys of a part");
+    pdl_wait();
+    pdl_trigger();
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, cta = blockIdx.x;
+    long long at = cta * per + min(cta, rest);
+    const long long end = at + per + (cta < rest ? 1 : 0);
+    int row, u0;
+    if (at >> 32) {
+        row = static_cast<int>(at / units), u0 = static_cast<int>(at % units);
+    } else {
+        row = static_cast<int>(static_cast<unsigned>(at) / units), u0 = static_cast<int>(static_cast<unsigned>(at) % units);
+    }
+    if (threadIdx.x == 0) out.open[cta] = make_int2(0, 0);
+    for (; at < end; ++row, u0 = 0) {
+        const int u1 = static_cast<int>(min(static_cast<long long>(units), u0 + (end - at)));
+        const char* x = static_cast<const char*>(a.logits) + (long long)row * a.ld * size;
+        const int head = min(a.V, static_cast<int>(((16 - (reinterpret_cast<uintptr_t>(x) & 15)) & 15) / size));
+        const int nv = (a.V - head) / N, tail = head + nv * N;
+        const char* base = x + (long long)head * size;
+        LpWarp w = lp_start();
+        // each warp a run of whole units
+        const int mine = (u1 - u0 + kLpWarps - 1) / kLpWarps;
+        const int last = min(nv, min(u1, u0 + (warp + 1) * mine) * 32);
+        auto load = [&](uint4(&r)[kLpLoads], int v) {
+            const char* from = base + (long long)(v + lane) * 16;
+            if (v + 32 * kLpLoads <= last) {
+#pragma unroll
+                for (int i = 0; i < kLpLoads; ++i) r[i] = ldg_stream_v4(from + i * 512);
+            } else {
+#pragma unroll
+                for (int i = 0; i < kLpLoads; ++i) {
+                    r[i] = make_uint4(V::kNone, V::kNone, V::kNone, V::kNone);
+                    if (v + i * 32 + lane < last) r[i] = ldg_stream_v4(from + i * 512);
+                }
+            }
+        };
+        int v = (u0 + warp * mine) * 32;
+        uint4 r[kLpLoads];
+        float vmax[kLpLoads];
+        load(r, v);
+        if (threadIdx.x == 0) kept.count = 0;
+        __syncthreads();
+        if (a.top > 0) {
+            // the bound from every warp's first chunk (-inf where it has none)
+            float b = -INFINITY;
+#pragma unroll
+            for (int i = 0; i < kLpLoads; ++i) {
+                float h[N];
+                V::get(r[i], h);
+#pragma unroll
+                for (int j = 0; j < N; ++j) b = fmaxf(b, h[j]);
+            }
+            w.thr = lp_from_order(lp_bound(lp_order(b), a.top, slots, lane, warp));
+        }
+        const int chunks = (mine + kLpLoads - 1) / kLpLoads;  // the same for all warps
+        int again = 2;
+        for (int c = 0; c < chunks; ++c, v += 32 * kLpLoads) {
+            if (a.top > 0 && c == again) {
+                // 2, 8, 32, ... chunks seen: the bound from what they left
+                again *= 4;
+                __syncthreads();
+                const unsigned o = lp_keys_bound(kept.key, min(kept.count, kLpKept), a.top, slots, lane, warp);
+                if (o != 0u && o != 0xFFFFFFFFu) w.thr = fmaxf(w.thr, lp_from_order(o));
+            }
+            if (v >= last) continue;
+            uint4 ahead[kLpLoads];
+            load(ahead, v + 32 * kLpLoads);
+            lp_sums<DT>(w.p, r, vmax, buf[warp], lane);
+            if (a.top > 0)
+                lp_collect<DT, kLpKept>(w, r, vmax, buf[warp], &kept, a.top, lane, [&](int i, int j) {
+                    const int k = v + i * 32 + lane;
+                    return k < last ? head + k * N + j : -1;
+                });
+#pragma unroll
+            for (int i = 0; i < kLpLoads; ++i) r[i] = ahead[i];
+        }
+        if (u0 == 0 && warp == 0 && (head > 0 || tail < a.V)) {
+            // fewer than N values at each end: as two values of one vector
+#pragma unroll
+            for (int i = 0; i < kLpLoads; ++i) r[i] = make_uint4(V::kNone, V::kNone, V::kNone, V::kNone);
+            r[0] = V::two(lane < head ? V::one(x, lane) : -INFINITY, tail + lane < a.V ? V::one(x, tail + lane) : -INFINITY);
+            lp_sums<DT>(w.p, r, vmax, buf[0], lane);
+            if (a.top > 0)
+                lp_collect<DT, kLpKept>(w, r, vmax, buf[0], &kept, a.top, lane, [&](int i, int j) {
+                    return i > 0 ? -1 : j == 0 && lane < head ? lane : j == 1 && tail + lane < a.V ? tail + lane : -1;
+                });
+        }
+        lp_join_sums(w.p, lane, warp);  // (a barrier: all is collected)
+        if (a.top > 0) {
+            const int n = min(kept.count, kLpKept);
+            const bool lists = kept.count > kLpKept;
+            if (lists) {
+                kept.key[kLpKept + threadIdx.x] = w.mine;
+                __syncthreads();
+            }
+            lp_select(kept.key, lists ? kLpKept + kLpThreads : n, a.top, reinterpret_cast<unsigned long long*>(buf), best, lane, warp);
+        }
+        if (warp == 0) {
+            const unsigned long long key = a.top > 0 ? best[lane] : 0ull;
+            if (u0 == 0 && u1 == units) {
+                lp_finish<DT>(a, row, w.p, key, lane);
+            } else {
+                LpRecord* to = out.rec + 2ll * cta + (u0 == 0 ? 1 : 0);
+                if (lane == 0) to->m = w.p.m, to->s = w.p.s, to->t = w.p.t;
+                to->key[lane] = key;
+                if (lane == 0 && u0 == 0) {
+                    // the CTA that holds the row's last unit
+                    const long long z = at + units - 1, longer = rest * (per + 1);
+                    const long long c = z < longer ? z / (per + 1) : rest + (z - longer) / per;
+                    out.open[cta] = make_int2(row, static_cast<int>(c) - cta + 1);
+                }
+            }
+        }
+        at += u1 - u0;
+    }
+}
+
+// Short rows: a warp each, with no barrier among the warps. (3000 rows of 29 values, top 8: 67 us by the kernel
+// above, whose CTAs meet several times a row.)
+constexpr int kLpShort = 4096;
+template <int DT>
+__global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_rows_kernel(LogprobArgs a) {
+    using V = LpVec<DT>;
+    constexpr int N = V::N, kLpLoads = kLpValues / N;
+    constexpr int size = DT == 3 ? 4 : 2;
+    __shared__ uint4 buf[kLpWarps][kLpLoads * 32];
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-    const int row = blockIdx.y, split = blockIdx.x;
-    const char* x = static_cast<const char*>(a.logits) + (long long)row * a.ld * size;
-    // 16-byte vectors of the row, and the values before and behind them
-    const int head = min(a.V, static_cast<int>(((16 - (reinterpret_cast<uintptr_t>(x) & 15)) & 15) / size));
-    const int nv = (a.V - head) / N, tail = head + nv * N;
-    LpWarp w = lp_start();
-    if (split == 0 && warp == 0) {
-        // fewer than N values at each end
-        float e[2] = {0.f, 0.f};
-        const int i0 = lane, i1 = tail + lane;
-        if (i0 < head) e[0] = V::one(x, i0);
-        if (i1 < a.V) e[1] = V::one(x, i1);
-        const float h0[1] = {e[0]}, h1[1] = {e[1]};
-        lp_batch(w, h0, i0, i0 < head, a.top, lane);
-        lp_batch(w, h1, i1, i1 < a.V, a.top, lane);
-    }
-    const int per = (nv + splits - 1) / splits;
-    const int v0 = min(nv, split * per), v1 = min(nv, v0 + per);
-    const char* base = x + (long long)head * size;
-    for (int v = v0 + warp * 32; v < v1; v += kLpThreads) {
-        const bool ok = v + lane < v1;
-        uint4 r = make_uint4(0, 0, 0, 0);
-        if (ok) r = ldg_stream_v4(base + (long long)(v + lane) * 16);
-        float f[N];
-        V::get(r, f);
-        lp_batch(w, f, head + (v + lane) * N, ok ? N : 0, a.top, lane);
-    }
-    lp_join_cta(w, a.top, lane, warp);
-    if (warp != 0) return;
-    if (splits == 1) {
-        lp_finish<DT>(a, row, w, lane);
-    } else {
-        LpRecord* r = rec + (long long)row * splits + split;
-        if (lane == 0) r->m = w.p.m, r->s = w.p.s, r->t = w.p.t;
-        r->key[lane] = w.mine;
-    }
-}
-
-template <int DT>
-__global__ void __launch_bounds__(kLpThreads) token_logprobs_join_kernel(LogprobArgs a, int splits, const LpRecord* rec) {
-    pdl_wait();
-    pdl_trigger();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, row = blockIdx.x;
-    const LpRecord* r = rec + (long long)row * splits;
-    LpWarp w = lp_start();
-    // thread i joins the sums of splits i, i + 256, ...
-    for (int i = threadIdx.x; i < splits; i += kLpThreads) w.p = lp_join(w.p, LpPart{r[i].m, r[i].s, r[i].t});
-    if (a.top > 0) {
-        for (int i = warp; i < splits; i += kLpWarps) {
-            const unsigned long long theirs = r[i].key[lane];
-            for (int j = 0; j < a.top; ++j) {
-                const unsigned long long c = __shfl_sync(0xffffffffu, theirs, j);
-                if (c <= __shfl_sync(0xffffffffu, w.mine, a.top - 1)) break;
-                lp_insert(w.mine, c, lane);
+    for (long long at = (long long)blockIdx.x * kLpWarps + warp; at < a.M; at += (long long)gridDim.x * kLpWarps) {
+        const int row = static_cast<int>(at);
+        const char* x = static_cast<const char*>(a.logits) + row * a.ld * size;
+        const int head = min(a.V, static_cast<int>(((16 - (reinterpret_cast<uintptr_t>(x) & 15)) & 15) / size));
+        const int nv = (a.V - head) / N, tail = head + nv * N;
+        LpWarp w = lp_start();
+        uint4 r[kLpLoads];
+        float vmax[kLpLoads];
+        // the values at the ends, as two of one vector, after the rest
+        for (int v = 0; v < nv; v += 32 * kLpLoads) {
+#pragma unroll
+            for (int i = 0; i < kLpLoads; ++i) {
+                r[i] = make_uint4(V::kNone, V::kNone, V::kNone, V::kNone);
+                if (v + i * 32 + lane < nv)
+                    r[i] = ldg_stream_v4(x + (long long)head * size + (long long)(v + i * 32 + lane) * 16);
+            }
+            const float b = lp_sums<DT>(w.p, r, vmax, buf[warp], lane);
+            if (a.top > 0) {
+                const unsigned kth = __shfl_sync(0xffffffffu, lp_sort(lp_order(b), lane), a.top - 1);
+                w.thr = fmaxf(w.thr, lp_from_order(kth));
+                lp_collect<DT, 0>(w, r, vmax, buf[warp], nullptr, a.top, lane, [&](int i, int j) {
+                    const int k = v + i * 32 + lane;
+                    return k < nv ? head + k * N + j : -1;
+                });
             }
         }
+        if (head > 0 || tail < a.V) {
+#pragma unroll
+            for (int i = 0; i < kLpLoads; ++i) r[i] = make_uint4(V::kNone, V::kNone, V::kNone, V::kNone);
+            r[0] = V::two(lane < head ? V::one(x, lane) : -INFINITY, tail + lane < a.V ? V::one(x, tail + lane) : -INFINITY);
+            lp_sums<DT>(w.p, r, vmax, buf[warp], lane);
+            if (a.top > 0)
+                lp_collect<DT, 0>(w, r, vmax, buf[warp], nullptr, a.top, lane, [&](int i, int j) {
+                    return i > 0 ? -1 : j == 0 && lane < head ? lane : j == 1 && tail + lane < a.V ? tail + lane : -1;
+                });
+        }
+        lp_join_warp(w.p);
+        lp_finish<DT>(a, row, w.p, w.mine, lane);
     }
-    lp_join_cta(w, a.top, lane, warp);
-    if (warp == 0) lp_finish<DT>(a, row, w, lane);
 }
 
-// CTAs a row is split over: enough for four a multiprocessor, each with 1024 16-byte vectors at least.
-int lp_splits(int M, int V) {
-    const long long want = (4ll * kSms + M - 1) / M;
-    const long long most = (V + 4095) / 4096;
-    return static_cast<int>(want < most ? want : most);
+// Joins the parts of the row that begins in CTA c's range and goes on behind it.
+template <int DT>
+__global__ void __launch_bounds__(kLpThreads) token_logprobs_join_kernel(LogprobArgs a, LpParts in) {
+    extern __shared__ unsigned long long lp_smem[];  // two lists of 32 keys a part
+    __shared__ unsigned long long best[kLogprobMaxTop];
+    pdl_wait();
+    pdl_trigger();
+    const int2 o = in.open[blockIdx.x];
+    const int row = o.x, n = o.y;
+    if (n == 0) return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    // the first CTA's part is its second record
+    auto rec = [&](int i) { return in.rec + 2ll * (blockIdx.x + i) + (i == 0 ? 1 : 0); };
+    LpWarp w = lp_start();
+    for (int i = threadIdx.x; i < n; i += kLpThreads) w.p = lp_join(w.p, LpPart{rec(i)->m, rec(i)->s, rec(i)->t});
+    if (a.top > 0)
+#pragma unroll 4
+        for (int i = threadIdx.x; i < n * 32; i += kLpThreads) lp_smem[i] = rec(i >> 5)->key[i & 31];
+    lp_join_sums(w.p, lane, warp);
+    if (a.top > 0) lp_select(lp_smem, n * 32, a.top, lp_smem + n * 32, best, lane, warp);
+    if (warp == 0) lp_finish<DT>(a, row, w.p, a.top > 0 ? best[lane] : 0ull, lane);
+}
+
+struct LpPlan {
+    int units, ctas, rest, most_parts;
+    long long per;
+    bool join;
+};
+// kLpCtas CTAs a multiprocessor, while each has a row or 2048 values at least; at
+// most 74 a row, so that the lists of a row's parts fit the join's shared memory.
+LpPlan lp_plan(int M, int V, int dtype) {
+    LpPlan p;
+    const int per = 32 * 16 / (dtype == 3 ? 4 : 2);
+    p.units = (V + per - 1) / per;
+    const long long want = std::max<long long>(M, (long long)M * V / 2048), total = (long long)M * p.units;
+    p.ctas = static_cast<int>(std::min<long long>(std::min<long long>(kLpCtas * kSms, want), 74ll * M));
+    p.per = total / p.ctas;
+    p.rest = static_cast<int>(total % p.ctas);
+    p.join = p.rest != 0 || p.per % p.units != 0;
+    p.most_parts = p.ctas / M + 2;
+    return p;
 }
 
 template <int DT>
-cudaError_t launch_dt(const LogprobArgs& a, LpRecord* rec, cudaStream_t s) {
-    int splits = lp_splits(a.M, a.V);
-    LogprobArgs b = a;
-    void* args[] = {&b, &splits, &rec};
-    // rows past 65535 (the grid's y limit) go in further launches
-    for (int m0 = 0; m0 < a.M; m0 += 65535) {
-        const int m = a.M - m0 < 65535 ? a.M - m0 : 65535;
-        b.M = m;
-        b.logits = static_cast<const char*>(a.logits) + (long long)m0 * a.ld * (DT == 3 ? 4 : 2);
-        b.ids = a.ids ? a.ids + (long long)m0 * a.n_ids : nullptr;
-        b.logprobs = a.logprobs ? a.logprobs + (long long)m0 * a.n_ids : nullptr;
-        b.entropy = a.entropy ? a.entropy + m0 : nullptr;
-        b.lse = a.lse ? a.lse + m0 : nullptr;
-        b.top_ids = a.top_ids ? a.top_ids + (long long)m0 * a.top : nullptr;
-        b.top_logprobs = a.top_logprobs ? a.top_logprobs + (long long)m0 * a.top : nullptr;
-        cudaError_t e = launch_kernel(reinterpret_cast<const void*>(token_logprobs_kernel<DT>), dim3(splits, m),
-                                      dim3(kLpThreads), 0, true, s, args);
-        if (e != cudaSuccess) return e;
-        if (splits > 1) {
-            e = launch_kernel(reinterpret_cast<const void*>(token_logprobs_join_kernel<DT>), dim3(m), dim3(kLpThreads),
-                              0, true, s, args);
-            if (e != cudaSuccess) return e;
-        }
+cudaError_t launch_dt(const LogprobArgs& a, void* ws, cudaStream_t s) {
+    if (a.V <= kLpShort) {
+        const int ctas = std::min(kLpCtas * kSms, (a.M + kLpWarps - 1) / kLpWarps);
+        void* args[] = {const_cast<LogprobArgs*>(&a)};
+        return launch_kernel(reinterpret_cast<const void*>(token_logprobs_rows_kernel<DT>), dim3(ctas), dim3(kLpThreads), 0, true,
+                             s, args);
     }
-    return cudaSuccess;
+    LpPlan p = lp_plan(a.M, a.V, DT);
+    LpParts parts{static_cast<LpRecord*>(ws), reinterpret_cast<int2*>(static_cast<LpRecord*>(ws) + 2 * p.ctas)};
+    void* args[] = {const_cast<LogprobArgs*>(&a), &p.units, &p.per, &p.rest, &parts};
+    cudaError_t e = launch_kernel(reinterpret_cast<const void*>(token_logprobs_kernel<DT>), dim3(p.ctas), dim3(kLpThreads), 0,
+                                  true, s, args);
+    if (e != cudaSuccess || !p.join) return e;
+    void* jargs[] = {const_cast<LogprobArgs*>(&a), &parts};
+    return launch_kernel(reinterpret_cast<const void*>(token_logprobs_join_kernel<DT>), dim3(p.ctas), dim3(kLpThreads),
+                         a.top > 0 ? p.most_parts * 32 * 2 * 8 : 0, true, s, jargs);
 }
 
 }  // namespace
 
 size_t token_logprobs_ws_bytes(int M, int V) {
-    const int splits = lp_splits(M, V);
-    return splits > 1 ? static_cast<size_t>(M) * splits * sizeof(LpRecord) : 0;
+    if (V <= kLpShort) return 0;
+    return static_cast<size_t>(lp_plan(M, V, 3).ctas) * (2 * sizeof(LpRecord) + sizeof(int2));
 }
 
 cudaError_t launch_token_logprobs(const LogprobArgs& a, int dtype, void* ws, cudaStream_t s) {
-    LpRecord* rec = static_cast<LpRecord*>(ws);
-    if (dtype == 1) return launch_dt<1>(a, rec, s);
-    if (dtype == 2) return launch_dt<2>(a, rec, s);
-    return launch_dt<3>(a, rec, s);
+    if (dtype == 1) return launch_dt<1>(a, ws, s);
+    if (dtype == 2) return launch_dt<2>(a, ws, s);
+    return launch_dt<3>(a, ws, s);
 }
 
 }  // namespace escha

@@ -582,9 +582,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas)
     }
 }
 
-// Short rows: a warp each, with no barrier among the warps. (3000 rows of 29 values, top 8: 67 us by the kernel
-// above, whose CTAs meet several times a row.)
-constexpr int kLpShort = 4096;
+// Short rows: a warp each, with no barrier among the warps.
 template <int DT>
 __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_rows_kernel(LogprobArgs a) {
     using V = LpVec<DT>;
@@ -658,6 +656,12 @@ __global__ void __launch_bounds__(kLpThreads) token_logprobs_join_kernel(Logprob
     if (warp == 0) lp_finish<DT>(a, row, w.p, a.top > 0 ? best[lane] : 0ull, lane);
 }
 
+// Whether rows go to warps (no workspace) or are cut over CTAs; the launch and the workspace's size both go by it.
+// A warp is slower at a row than a CTA from about 1000 values on (one row of 3000, top 8: 12 us against 6), but
+// many rows keep all warps busy without the CTAs' meetings (3000 rows of 29: 19 against 67 us; 4096 rows of 3000:
+// 32 against 83; 600 rows of 3000: 15 against 22, and 32 against 25 at top 32).
+bool lp_by_rows(int M, int V) { return V <= 1024 || (V <= 4096 && M >= 2 * kLpCtas * kSms); }
+
 struct LpPlan {
     int units, ctas, rest, most_parts;
     long long per;
@@ -680,7 +684,7 @@ LpPlan lp_plan(int M, int V, int dtype) {
 
 template <int DT>
 cudaError_t launch_dt(const LogprobArgs& a, void* ws, cudaStream_t s) {
-    if (a.V <= kLpShort) {
+    if (lp_by_rows(a.M, a.V)) {
         const int ctas = std::min(kLpCtas * kSms, (a.M + kLpWarps - 1) / kLpWarps);
         void* args[] = {const_cast<LogprobArgs*>(&a)};
         return launch_kernel(reinterpret_cast<const void*>(token_logprobs_rows_kernel<DT>), dim3(ctas), dim3(kLpThreads), 0, true,
@@ -700,7 +704,7 @@ cudaError_t launch_dt(const LogprobArgs& a, void* ws, cudaStream_t s) {
 }  // namespace
 
 size_t token_logprobs_ws_bytes(int M, int V) {
-    if (V <= kLpShort) return 0;
+    if (lp_by_rows(M, V)) return 0;
     return static_cast<size_t>(lp_plan(M, V, 3).ctas) * (2 * sizeof(LpRecord) + sizeof(int2));
 }
 

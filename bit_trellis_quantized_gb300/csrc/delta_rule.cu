@@ -129,6 +129,498 @@ __global__ void __launch_bounds__(kDrThreads) delta_step_kernel(DeltaArgs a) {
     for (int i = 0; i < kPer; ++i) *reinterpret_cast<float4*>(sp + (long long)i * kRows * a.dv) = S[i];
 }
 
+// ---- chunks of 32 tokens ------------------------------------------------------
+// With G_i = g_1 + ... + g_i inside a chunk and S0 the state before it,
+//   (1 + L) U = diag(beta) (V - diag(e^G) K S0),  L_ij = beta_i e^(G_i - G_j) k_i . k_j (j < i)
+//   O = diag(e^G) Q S0 + P U,  P_ij = e^(G_i - G_j) q_i . k_j (j <= i)
+//   S = e^(G_32) S0 + sum_j e^(G_32 - G_j) k_j u_j^T
+// A first kernel makes what does not hang on the state, for all chunks at once:
+// T = (1 + L)^-1 diag(beta), P and the factors. The second walks each
+// sequence's chunks; its products run on the tensor cores.
+//
+// Precision: states stay as good as f32 makes them. Keys and queries are fp16
+// values (bf16 ones times a power of two a row), exact. Everything else enters
+// a product as two fp16 parts of its value times a power of two a row (the
+// largest of the row at 2^13): 22 bits and more of the row's largest. Sums are
+// f32.
+constexpr int kC = 32;  // tokens of a chunk
+
+// What the first kernel leaves for one (chunk, value head).
+struct DrChunk {
+    uint16_t t_hi[kC][kC], t_lo[kC][kC];  // fp16, row i times 1 / t_inv[i]
+    uint16_t p_hi[kC][kC], p_lo[kC][kC];  // fp16, row i times 1 / p_inv[i]; scale and norms in it
+    float fall[kC];                       // e^G_j / |k_j|
+    float rest[kC];                       // e^(G_32 - G_j) / |k_j|
+    float t_inv[kC], p_inv[kC];
+    float q_out[kC];  // scale e^G_i / |q_i|
+    float decay[kC];  // e^G_32 (all the same)
+};
+static_assert(sizeof(DrChunk) % 128 == 0, "rows of 16 bytes");
+
+__device__ __forceinline__ void dr_mma(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+    asm volatile("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+                 : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+                 : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ void dr_ldsm4(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ void dr_ldsm4t(uint32_t (&r)[4], uint32_t addr) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0,%1,%2,%3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr)
+                 : "memory");
+}
+__device__ __forceinline__ uint32_t dr_movm(uint32_t x) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+__device__ __forceinline__ void dr_cp16(uint32_t dst, const void* src, bool ok) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
+
+// 2^k that takes values of at most `most` below 2^14 (the largest to 2^13 and more, where k stays in -114..60).
+__device__ __forceinline__ float dr_scale(float most) {
+    const int k = min(60, max(-114, 140 - static_cast<int>(__float_as_uint(most) >> 23)));
+    return __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
+}
+// x and y as two fp16 parts each
+__device__ __forceinline__ void dr_split(float x, float y, uint32_t& hi, uint32_t& lo) {
+    const __half2 h = __floats2half2_rn(x, y);
+    const float2 b = __half22float2(h);
+    const __half2 l = __floats2half2_rn(x - b.x, y - b.y);
+    hi = *reinterpret_cast<const uint32_t*>(&h);
+    lo = *reinterpret_cast<const uint32_t*>(&l);
+}
+__device__ __forceinline__ uint32_t dr_first(float x, float y) {
+    const __half2 h = __floats2half2_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+// Place of 16-byte chunk c of row r: rows of 128 bytes and more, or of 64.
+template <int kRowBytes>
+__device__ __forceinline__ uint32_t dr_at(int r, int c) {
+    return r * kRowBytes + ((kRowBytes >= 128 ? c ^ (r & 7) : c ^ ((r >> 1) & 3)) << 4);
+}
+
+// The chunk data of sequence s begin at slot t0 / kC + s: no two sequences share one.
+__host__ __device__ inline long long dr_slots(int T, int n) { return T / kC + static_cast<long long>(n); }
+
+template <int DT, int DK>
+__global__ void __launch_bounds__(128) delta_prepare_kernel(DeltaArgs a, uint16_t* kf, uint16_t* qf, DrChunk* out) {
+    constexpr int kRow = DK * 2, kPer = DK / 4;
+    __shared__ __align__(128) unsigned char ks[kC * kRow], qs[kC * kRow];
+    __shared__ float dots[2][kC][kC + 1];  // k_i . k_j and q_i . k_j
+    __shared__ float inv[2][kC];           // 1 / |k|, 1 / |q| (with the rows' powers of two)
+    __shared__ __align__(16) float Ls[4][kC][kC];
+    pdl_wait();
+    pdl_trigger();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, hk = blockIdx.y;
+    // the sequence of this slot: the last whose first slot is not behind it
+    int s = 0;
+    for (int lo = 0, hi = a.n - 1; lo <= hi;) {
+        const int mid = (lo + hi) >> 1;
+        if (max(0, min(a.at[mid], a.T)) / kC + static_cast<long long>(mid) <= blockIdx.x)
+            s = mid, lo = mid + 1;
+        else
+            hi = mid - 1;
+    }
+    int t0, t1;
+    dr_tokens(a, s, t0, t1);
+    const long long ahead = blockIdx.x - (t0 / kC + static_cast<long long>(s));
+    if (ahead < 0 || ahead * kC >= t1 - t0) return;  // a slot that no sequence uses
+    t0 += static_cast<int>(ahead) * kC;
+    const int n = min(kC, t1 - t0);
+    {
+        // four threads a row: norms, and for bf16 the power of two that brings the row's largest value to 1..2
+        const int r = tid >> 2, part = tid & 3;
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+            const uint16_t* src = static_cast<const uint16_t*>(which ? a.q : a.k) + ((long long)(t0 + r) * a.Hk + hk) * DK + part * kPer;
+            uint4 w[kPer / 8];
+            float sum = 0.f, most = 0.f;
+#pragma unroll
+            for (int i = 0; i < kPer / 8; ++i) {
+                w[i] = r < n ? *reinterpret_cast<const uint4*>(src + i * 8) : make_uint4(0, 0, 0, 0);
+                const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float x = DT == 1 ? h2f_bits(v[j] & 0xFFFF) : __uint_as_float(v[j] << 16);
+                    const float y = DT == 1 ? h2f_bits(v[j] >> 16) : __uint_as_float(v[j] & 0xFFFF0000u);
+                    sum += x * x;
+                    sum += y * y;
+                    most = fmaxf(most, fmaxf(fabsf(x), fabsf(y)));
+                }
+            }
+            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+            float up = 1.f;
+            if (DT == 2) {
+                up = dr_scale(most) * 0x1p-13f;
+#pragma unroll
+                for (int i = 0; i < kPer / 8; ++i) {
+                    uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        v[j] = dr_first(__uint_as_float(v[j] << 16) * up, __uint_as_float(v[j] & 0xFFFF0000u) * up);
+                    w[i] = make_uint4(v[0], v[1], v[2], v[3]);
+                    if (r < n)
+                        *reinterpret_cast<uint4*>((which ? qf : kf) + ((long long)(t0 + r) * a.Hk + hk) * DK + part * kPer + i * 8) = w[i];
+                }
+            }
+            if (part == 0) inv[which][r] = r >= n ? 0.f : (a.eps >= 0.f ? 1.f / sqrtf(sum + a.eps) : 1.f) / up;
+#pragma unroll
+            for (int i = 0; i < kPer / 8; ++i)
+                *reinterpret_cast<uint4*>((which ? qs : ks) + dr_at<kRow>(r, part * (kPer / 8) + i)) = w[i];
+        }
+    }
+    __syncthreads();
+    {
+        // warps 0 and 1: k . k, 2 and 3: q . k, 16 rows each
+        const int m0 = (warp & 1) * 16;
+        const uint32_t A = static_cast<uint32_t>(__cvta_generic_to_shared(warp < 2 ? ks : qs));
+        const uint32_t B = static_cast<uint32_t>(__cvta_generic_to_shared(ks));
+        float c[4][4] = {};
+#pragma unroll
+        for (int k = 0; k < DK / 16; k += 2) {
+            uint32_t f[2][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h) dr_ldsm4(f[h], A + dr_at<kRow>(m0 + (lane & 15), 2 * (k + h) + (lane >> 4)));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t b[4];
+                dr_ldsm4(b, B + dr_at<kRow>(8 * i + (lane & 7), 2 * k + (lane >> 3)));
+                dr_mma(c[i], f[0], b[0], b[1]);
+                dr_mma(c[i], f[1], b[2], b[3]);
+            }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) dots[warp >> 1][m0 + (lane >> 2) + (e >> 1) * 8][8 * i + (lane & 3) * 2 + (e & 1)] = c[i][e];
+    }
+    __syncthreads();
+    // a warp a value head; lane j: column j
+    const int rep = a.Hv / a.Hk;
+    for (int r = warp; r < rep; r += 4) {
+        const int hv = hk * rep + r;
+        DrChunk* o = out + (long long)blockIdx.x * a.Hv + hv;
+        const long long at = (long long)(t0 + lane) * a.Hv + hv;
+        float gl = lane < n ? a.g[at] : 0.f;
+        const float beta = lane < n ? a.beta[at] : 0.f;
+        gl = gl < -1e6f ? -1e6f : gl;  // -infinity has no differences; e^-1e6 is 0 as well
+        double G = gl;                 // sums of decays in 64 bits: their differences count
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+            const double p = __shfl_up_sync(0xffffffffu, G, m);
+            if (lane >= m) G += p;
+        }
+        const double G_all = __shfl_sync(0xffffffffu, G, 31);
+        const float rk = inv[0][lane];
+        float p_inv = 0.f, t_inv = 0.f;
+        float(&L)[kC][kC] = Ls[warp];
+        __syncwarp();
+#pragma unroll 4
+        for (int i = 0; i < kC; ++i) {
+            const double Gi = __shfl_sync(0xffffffffu, G, i);
+            const float bi = __shfl_sync(0xffffffffu, beta, i);
+            const float e = lane <= i ? expf(static_cast<float>(Gi - G)) * rk : 0.f;
+            L[i][lane] = lane < i ? bi * inv[0][i] * e * dots[0][i][lane] : 0.f;
+            const float p = lane <= i ? a.scale * inv[1][i] * e * dots[1][i][lane] : 0.f;
+            const float up = dr_scale(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(p)))));
+            uint32_t hi, lo;
+            dr_split(p * up, 0.f, hi, lo);
+            o->p_hi[i][lane] = static_cast<uint16_t>(hi);
+            o->p_lo[i][lane] = static_cast<uint16_t>(lo);
+            if (lane == i) p_inv = 1.f / up;
+        }
+        __syncwarp();
+        // column `lane` of (1 + L)^-1, row by row
+        float x[kC];
+#pragma unroll
+        for (int i = 0; i < kC; ++i) {
+            float acc[4] = {lane == i ? 1.f : 0.f, 0.f, 0.f, 0.f};
+#pragma unroll
+            for (int j = 0; j < i; j += 4) {
+                const float4 l = *reinterpret_cast<const float4*>(&L[i][j]);
+                acc[0] -= l.x * x[j];
+                if (j + 1 < i) acc[1] -= l.y * x[j + 1];
+                if (j + 2 < i) acc[2] -= l.z * x[j + 2];
+                if (j + 3 < i) acc[3] -= l.w * x[j + 3];
+            }
+            x[i] = (acc[0] + acc[1]) + (acc[2] + acc[3]);
+        }
+#pragma unroll
+        for (int i = 0; i < kC; ++i) {
+            const float t = x[i] * beta;
+            const float up = dr_scale(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(t)))));
+            uint32_t hi, lo;
+            dr_split(t * up, 0.f, hi, lo);
+            o->t_hi[i][lane] = static_cast<uint16_t>(hi);
+            o->t_lo[i][lane] = static_cast<uint16_t>(lo);
+            if (lane == i) t_inv = 1.f / up;
+        }
+        const float eg = expf(static_cast<float>(G));
+        o->fall[lane] = eg * rk;
+        o->rest[lane] = expf(static_cast<float>(G_all - G)) * rk;
+        o->t_inv[lane] = t_inv;
+        o->p_inv[lane] = p_inv;
+        o->q_out[lane] = a.scale * inv[1][lane] * eg;
+        o->decay[lane] = expf(static_cast<float>(G_all));
+    }
+}
+
+// Walks the chunks of one (sequence, value head, 16 W columns of the state):
+// each warp owns 16 columns, held transposed ([16 columns][dk]) in the tensor
+// cores' accumulator layout for the whole walk. In that form each product's
+// result is the next one's left operand, register for register: S^T K^T, then
+// (V - ...)^T T^T, then U^T K, and S^T Q^T, U^T P^T for the outputs. Nothing of
+// the chain passes through shared memory; the warps meet once a chunk, where
+// the next chunks' K, Q, T, P and V arrive (cp.async).
+template <int DK, int W>
+struct DrWalk {
+    static constexpr int kRow = DK * 2, kVRow = W * 32;
+    static constexpr int kQ = kC * kRow, kV = 2 * kC * kRow, kD = kV + kC * kVRow;
+    static constexpr int kStage = kD + static_cast<int>(sizeof(DrChunk));
+    static constexpr int kStages = 3;
+    static constexpr int kSmem = kStages * kStage;
+};
+template <int DT, int DK, int W>
+__global__ void __launch_bounds__(W * 32) delta_walk_kernel(DeltaArgs a, const uint16_t* kf, const uint16_t* qf, const DrChunk* data) {
+    using C = DrWalk<DK, W>;
+    constexpr int kRow = C::kRow, kVRow = C::kVRow, kNt = DK / 8, kThreads = W * 32, kStages = C::kStages;
+    extern __shared__ __align__(1024) unsigned char smem[];
+    pdl_wait();
+    pdl_trigger();
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q4 = lane & 3;
+    const int hv = blockIdx.y, seq = blockIdx.z, hk = hv / (a.Hv / a.Hk), c0 = blockIdx.x * (16 * W);
+    int t0, t1;
+    dr_tokens(a, seq, t0, t1);
+    const int chunks = (t1 - t0 + kC - 1) / kC;
+    if (chunks == 0) return;
+    data += (t0 / kC + static_cast<long long>(seq)) * a.Hv + hv;
+    const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
+
+    auto load = [&](int c) {
+        const uint32_t to = base + (c % kStages) * C::kStage;
+        const int tc = t0 + c * kC, n = min(kC, t1 - tc);
+        constexpr int kKc = DK / 8, kVc = W * 2;
+        for (int i = tid; i < kC * kKc; i += kThreads) {
+            const int r = i / kKc, ch = i % kKc;
+            const long long off = ((long long)(tc + (r < n ? r : 0)) * a.Hk + hk) * DK + ch * 8;
+            dr_cp16(to + dr_at<kRow>(r, ch), kf + off, r < n);
+            dr_cp16(to + C::kQ + dr_at<kRow>(r, ch), qf + off, r < n);
+        }
+        for (int i = tid; i < kC * kVc; i += kThreads) {
+            const int r = i / kVc, ch = i % kVc;
+            dr_cp16(to + C::kV + dr_at<kVRow>(r, ch),
+                    static_cast<const uint16_t*>(a.v) + ((long long)(tc + (r < n ? r : 0)) * a.Hv + hv) * a.dv + c0 + ch * 8, r < n);
+        }
+        const char* d = reinterpret_cast<const char*>(data + (long long)c * a.Hv);
+        for (int i = tid; i < 4 * kC * 4; i += kThreads)  // four matrices of 32 rows of 64 bytes
+            dr_cp16(to + C::kD + (i >> 7) * (kC * 64) + dr_at<64>((i >> 2) & 31, i & 3), d + i * 16, true);
+        for (int i = tid + 4 * kC * 4; i < static_cast<int>(sizeof(DrChunk) / 16); i += kThreads) dr_cp16(to + C::kD + i * 16, d + i * 16, true);
+    };
+
+    // element e of tile k: column c0 + 16 warp + g + 8 (e / 2), key dimension 8 k + 2 q4 + e % 2
+    float S[kNt][4];
+    float* sp = a.state + ((long long)seq * a.Hv + hv) * DK * a.dv + c0 + warp * 16 + g;
+#pragma unroll
+    for (int k = 0; k < kNt; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) S[k][e] = sp[(long long)(8 * k + 2 * q4 + (e & 1)) * a.dv + (e >> 1) * 8];
+    float unit[2] = {1.f, 1.f};  // the state's columns are S unit
+
+#pragma unroll
+    for (int c = 0; c < kStages - 1; ++c) {
+        if (c < chunks) load(c);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    }
+    for (int c = 0; c < chunks; ++c) {
+        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
+        __syncthreads();
+        if (c + kStages - 1 < chunks) load(c + kStages - 1);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        const uint32_t st = base + (c % kStages) * C::kStage;
+        const unsigned char* sd = smem + (c % kStages) * C::kStage + C::kD;
+        const DrChunk* cd = reinterpret_cast<const DrChunk*>(sd);  // its factors; the matrices are swizzled
+
+        // the state's two parts
+        float most[2] = {0.f, 0.f};
+#pragma unroll
+        for (int k = 0; k < kNt; ++k) {
+            most[0] = fmaxf(most[0], fmaxf(fabsf(S[k][0]), fabsf(S[k][1])));
+            most[1] = fmaxf(most[1], fmaxf(fabsf(S[k][2]), fabsf(S[k][3])));
+        }
+        auto quad_max = [](float x) {
+            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+            return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+        };
+        float s_up[2], s_inv[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            s_up[h] = dr_scale(quad_max(most[h]));
+            s_inv[h] = unit[h] / s_up[h];
+        }
+        float x[4][4] = {}, o[4][4] = {};
+#pragma unroll
+        for (int k = 0; k < DK / 16; k += 2) {
+            uint32_t hi[2][4], lo[2][4];
+#pragma unroll
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float* v = S[2 * (k + h) + (e >> 1)] + (e & 1) * 2;
+                    dr_split(v[0] * s_up[e & 1], v[1] * s_up[e & 1], hi[h][e], lo[h][e]);
+                }
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                uint32_t b[4];
+                dr_ldsm4(b, st + dr_at<kRow>(8 * i + (lane & 7), 2 * k + (lane >> 3)));
+                dr_mma(x[i], hi[0], b[0], b[1]);
+                dr_mma(x[i], hi[1], b[2], b[3]);
+                dr_mma(x[i], lo[0], b[0], b[1]);
+                dr_mma(x[i], lo[1], b[2], b[3]);
+                dr_ldsm4(b, st + C::kQ + dr_at<kRow>(8 * i + (lane & 7), 2 * k + (lane >> 3)));
+                dr_mma(o[i], hi[0], b[0], b[1]);
+                dr_mma(o[i], hi[1], b[2], b[3]);
+                dr_mma(o[i], lo[0], b[0], b[1]);
+                dr_mma(o[i], lo[1], b[2], b[3]);
+            }
+        }
+        // V - diag(e^G) K S0, transposed, and its two parts
+        {
+            uint32_t v0[4], v1[4];
+            dr_ldsm4t(v0, st + C::kV + dr_at<kVRow>(lane, 2 * warp));
+            dr_ldsm4t(v1, st + C::kV + dr_at<kVRow>(lane, 2 * warp + 1));
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 f = *reinterpret_cast<const float2*>(&cd->fall[8 * i + 2 * q4]);
+                const float2 y0 = DT == 1 ? __half22float2(*reinterpret_cast<const __half2*>(&v0[i]))
+                                          : make_float2(__uint_as_float(v0[i] << 16), __uint_as_float(v0[i] & 0xFFFF0000u));
+                const float2 y1 = DT == 1 ? __half22float2(*reinterpret_cast<const __half2*>(&v1[i]))
+                                          : make_float2(__uint_as_float(v1[i] << 16), __uint_as_float(v1[i] & 0xFFFF0000u));
+                x[i][0] = y0.x - f.x * (x[i][0] * s_inv[0]), x[i][1] = y0.y - f.y * (x[i][1] * s_inv[0]);
+                x[i][2] = y1.x - f.x * (x[i][2] * s_inv[1]), x[i][3] = y1.y - f.y * (x[i][3] * s_inv[1]);
+            }
+        }
+        auto parts = [&](const float(&v)[4][4], const float(&up)[2], uint32_t(&hi)[2][4], uint32_t(&lo)[2][4]) {
+#pragma unroll
+            for (int k = 0; k < 2; ++k)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float* w = v[2 * k + (e >> 1)] + (e & 1) * 2;
+                    dr_split(w[0] * up[e & 1], w[1] * up[e & 1], hi[k][e], lo[k][e]);
+                }
+        };
+        auto row_max = [&](const float(&v)[4][4], float(&m)[2]) {
+            m[0] = m[1] = 0.f;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                m[0] = fmaxf(m[0], fmaxf(fabsf(v[i][0]), fabsf(v[i][1])));
+                m[1] = fmaxf(m[1], fmaxf(fabsf(v[i][2]), fabsf(v[i][3])));
+            }
+            m[0] = quad_max(m[0]), m[1] = quad_max(m[1]);
+        };
+        uint32_t hi[2][4], lo[2][4];
+        row_max(x, most);
+        float up[2] = {dr_scale(most[0]), dr_scale(most[1])};
+        parts(x, up, hi, lo);
+        float u[4][4] = {};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {  // T is lower triangular: the tokens before 16 need its first half only
+            uint32_t th[4], tl[4];
+            dr_ldsm4(th, st + C::kD + dr_at<64>(8 * i + (lane & 7), lane >> 3));
+            dr_ldsm4(tl, st + C::kD + kC * 64 + dr_at<64>(8 * i + (lane & 7), lane >> 3));
+            dr_mma(u[i], hi[0], th[0], th[1]);
+            dr_mma(u[i], lo[0], th[0], th[1]);
+            dr_mma(u[i], hi[0], tl[0], tl[1]);
+            if (i >= 2) {
+                dr_mma(u[i], hi[1], th[2], th[3]);
+                dr_mma(u[i], lo[1], th[2], th[3]);
+                dr_mma(u[i], hi[1], tl[2], tl[3]);
+            }
+        }
+        {
+            const float v_inv[2] = {1.f / up[0], 1.f / up[1]};
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 f = *reinterpret_cast<const float2*>(&cd->t_inv[8 * i + 2 * q4]);
+                u[i][0] *= f.x * v_inv[0], u[i][1] *= f.y * v_inv[0];
+                u[i][2] *= f.x * v_inv[1], u[i][3] *= f.y * v_inv[1];
+            }
+        }
+        // outputs: diag(e^G) Q S0 + P U
+        row_max(u, most);
+        up[0] = dr_scale(most[0]), up[1] = dr_scale(most[1]);
+        parts(u, up, hi, lo);
+        const int tc = t0 + c * kC, n = min(kC, t1 - tc);
+        const float u_inv[2] = {1.f / up[0], 1.f / up[1]};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            uint32_t ph[4], pl[4];
+            float y[4] = {};
+            dr_ldsm4(ph, st + C::kD + 2 * kC * 64 + dr_at<64>(8 * i + (lane & 7), lane >> 3));
+            dr_ldsm4(pl, st + C::kD + 3 * kC * 64 + dr_at<64>(8 * i + (lane & 7), lane >> 3));
+            dr_mma(y, hi[0], ph[0], ph[1]);
+            dr_mma(y, lo[0], ph[0], ph[1]);
+            dr_mma(y, hi[0], pl[0], pl[1]);
+            if (i >= 2) {
+                dr_mma(y, hi[1], ph[2], ph[3]);
+                dr_mma(y, lo[1], ph[2], ph[3]);
+                dr_mma(y, hi[1], pl[2], pl[3]);
+            }
+            const float2 fq = *reinterpret_cast<const float2*>(&cd->q_out[8 * i + 2 * q4]);
+            const float2 fp = *reinterpret_cast<const float2*>(&cd->p_inv[8 * i + 2 * q4]);
+            const float r0 = o[i][0] * s_inv[0] * fq.x + y[0] * u_inv[0] * fp.x, r1 = o[i][1] * s_inv[0] * fq.y + y[1] * u_inv[0] * fp.y;
+            const float r2 = o[i][2] * s_inv[1] * fq.x + y[2] * u_inv[1] * fp.x, r3 = o[i][3] * s_inv[1] * fq.y + y[3] * u_inv[1] * fp.y;
+            // [column][token] -> [token][column]
+            const uint32_t w0 = dr_movm(dr_pack<DT>(r0, r1)), w1 = dr_movm(dr_pack<DT>(r2, r3));
+            if (8 * i + g < n) {
+                uint16_t* to = static_cast<uint16_t*>(a.out) + ((long long)(tc + 8 * i + g) * a.Hv + hv) * a.dv + c0 + warp * 16 + 2 * q4;
+                *reinterpret_cast<uint32_t*>(to) = w0;
+                *reinterpret_cast<uint32_t*>(to + 8) = w1;
+            }
+        }
+        // the state after the chunk
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = *reinterpret_cast<const float2*>(&cd->rest[8 * i + 2 * q4]);
+            u[i][0] *= f.x, u[i][1] *= f.y, u[i][2] *= f.x, u[i][3] *= f.y;
+        }
+        row_max(u, most);
+        const float decay = cd->decay[0];
+        float keep[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            // not so large that the state leaves f32's range in these units
+            up[h] = fminf(dr_scale(most[h]), s_up[h] / unit[h] * 65536.f);
+            keep[h] = decay * unit[h] * up[h];
+            unit[h] = 1.f / up[h];
+        }
+        parts(u, up, hi, lo);
+#pragma unroll
+        for (int k = 0; k < kNt; ++k) {
+            S[k][0] *= keep[0], S[k][1] *= keep[0], S[k][2] *= keep[1], S[k][3] *= keep[1];
+            uint32_t b[4];
+            dr_ldsm4t(b, st + dr_at<kRow>(lane, k));
+            dr_mma(S[k], hi[0], b[0], b[1]);
+            dr_mma(S[k], hi[1], b[2], b[3]);
+            dr_mma(S[k], lo[0], b[0], b[1]);
+            dr_mma(S[k], lo[1], b[2], b[3]);
+        }
+    }
+#pragma unroll
+    for (int k = 0; k < kNt; ++k)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) sp[(long long)(8 * k + 2 * q4 + (e & 1)) * a.dv + (e >> 1) * 8] = S[k][e] * unit[e >> 1];
+}
+
 template <int DT, int DK>
 cudaError_t launch_step(const DeltaArgs& a, cudaStream_t s) {
     // 128 columns a CTA where that still fills the GPU
@@ -140,17 +632,64 @@ cudaError_t launch_step(const DeltaArgs& a, cudaStream_t s) {
     return launch_kernel(f, dim3(a.dv / vs, a.Hv, a.n), dim3(kDrThreads), 0, true, s, args);
 }
 
+// Chunks from this length on; below, token by token.
+constexpr int kChunkFrom = 24;
+
+struct DrPlan {
+    bool chunks;
+    size_t kf, qf, total;  // chunk data first; then, for bf16, the keys and queries in fp16
+};
+DrPlan dr_plan(int n, int T, int Hk, int Hv, int dk, int max_len) {
+    DrPlan p{};
+    p.chunks = max_len >= kChunkFrom;
+    if (!p.chunks) return p;
+    p.kf = static_cast<size_t>(dr_slots(T, n)) * Hv * sizeof(DrChunk);
+    p.qf = p.kf + static_cast<size_t>(T) * Hk * dk * 2;
+    p.total = p.qf + static_cast<size_t>(T) * Hk * dk * 2;
+    return p;
+}
+
+template <int DT, int DK, int W>
+cudaError_t launch_walk(const DeltaArgs& a, const uint16_t* kf, const uint16_t* qf, const DrChunk* data, cudaStream_t s) {
+    const void* f = reinterpret_cast<const void*>(delta_walk_kernel<DT, DK, W>);
+    constexpr int smem = DrWalk<DK, W>::kSmem;
+    cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
+    if (e != cudaSuccess) return e;
+    void* args[] = {const_cast<DeltaArgs*>(&a), &kf, &qf, &data};
+    return launch_kernel(f, dim3(a.dv / (16 * W), a.Hv, a.n), dim3(W * 32), smem, true, s, args);
+}
+
+template <int DT, int DK>
+cudaError_t launch_chunks(const DeltaArgs& a, char* ws, cudaStream_t s) {
+    const DrPlan p = dr_plan(a.n, a.T, a.Hk, a.Hv, a.dk, a.max_len);
+    DrChunk* data = reinterpret_cast<DrChunk*>(ws);
+    uint16_t* kf = reinterpret_cast<uint16_t*>(ws + p.kf);
+    uint16_t* qf = reinterpret_cast<uint16_t*>(ws + p.qf);
+    void* args[] = {const_cast<DeltaArgs*>(&a), &kf, &qf, &data};
+    cudaError_t e = launch_kernel(reinterpret_cast<const void*>(delta_prepare_kernel<DT, DK>), dim3(dr_slots(a.T, a.n), a.Hk), dim3(128), 0,
+                                  true, s, args);
+    if (e != cudaSuccess) return e;
+    const uint16_t* k = DT == 1 ? static_cast<const uint16_t*>(a.k) : kf;
+    const uint16_t* q = DT == 1 ? static_cast<const uint16_t*>(a.q) : qf;
+    if (a.dv % 64 == 0 && (long long)a.n * a.Hv * (a.dv / 64) >= kSms) return launch_walk<DT, DK, 4>(a, k, q, data, s);
+    return launch_walk<DT, DK, 2>(a, k, q, data, s);
+}
+
+template <int DT>
+cudaError_t launch_dt(const DeltaArgs& a, char* ws, cudaStream_t s) {
+    if (a.max_len >= kChunkFrom) return a.dk == 64 ? launch_chunks<DT, 64>(a, ws, s) : launch_chunks<DT, 128>(a, ws, s);
+    return a.dk == 64 ? launch_step<DT, 64>(a, s) : launch_step<DT, 128>(a, s);
+}
+
 }  // namespace
 
 size_t delta_rule_ws_bytes(int n, int T, int Hk, int Hv, int dk, int dv, int max_len) {
-    (void)n, (void)T, (void)Hk, (void)Hv, (void)dk, (void)dv, (void)max_len;
-    return 0;
+    (void)dv;
+    return dr_plan(n, T, Hk, Hv, dk, max_len).total;
 }
 
 cudaError_t launch_delta_rule(const DeltaArgs& a, int dtype, void* ws, cudaStream_t s) {
-    (void)ws;
-    if (dtype == 1) return a.dk == 64 ? launch_step<1, 64>(a, s) : launch_step<1, 128>(a, s);
-    return a.dk == 64 ? launch_step<2, 64>(a, s) : launch_step<2, 128>(a, s);
+    return dtype == 1 ? launch_dt<1>(a, static_cast<char*>(ws), s) : launch_dt<2>(a, static_cast<char*>(ws), s);
 }
 
 }  // namespace escha

@@ -375,29 +375,64 @@ __global__ void __launch_bounds__(128) delta_prepare_kernel(DeltaArgs a, uint16_
     }
 }
 
-// Walks the chunks of one (sequence, value head, 16 W columns of the state):
-// each warp owns 16 columns, held transposed ([16 columns][dk]) in the tensor
+// a pair as two fp16 parts each
+__device__ __forceinline__ void dr_split2(unsigned long long xy, uint32_t& hi, uint32_t& lo) {
+    float x, y;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(xy));
+    const __half2 h = __floats2half2_rn(x, y);
+    const float2 b = __half22float2(h);
+    unsigned long long nb, r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(nb) : "f"(-b.x), "f"(-b.y));
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(xy), "l"(nb));
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(r));
+    hi = *reinterpret_cast<const uint32_t*>(&h);
+    lo = dr_first(x, y);
+}
+__device__ __forceinline__ unsigned long long dr_pair(float x, float y) {
+    unsigned long long r;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
+    return r;
+}
+__device__ __forceinline__ unsigned long long dr_mul2(unsigned long long x, float f) {
+    unsigned long long r;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(dr_pair(f, f)));
+    return r;
+}
+
+// Walks the chunks of one (sequence, value head, 16 W columns of the state).
+// A state warp owns 16 columns, held transposed ([16 columns][dk]) in the tensor
 // cores' accumulator layout for the whole walk. In that form each product's
 // result is the next one's left operand, register for register: S^T K^T, then
-// (V - ...)^T T^T, then U^T K, and S^T Q^T, U^T P^T for the outputs. Nothing of
-// the chain passes through shared memory; the warps meet once a chunk, where
-// the next chunks' K, Q, T, P and V arrive (cp.async).
+// (V - ...)^T T^T, then U^T K. Nothing of that chain passes through shared
+// memory. It hands the operands S^T and U^T to an output warp, which makes
+// S^T Q^T + U^T P^T one chunk later and fetches the next chunks (cp.async); all
+// warps meet once a chunk. The chain bounds a long sequence: one warp doing
+// both took 2.8 us a chunk (128 x 128 states), mostly waiting for its own last
+// instruction.
+template <int kThreads>
+__device__ __forceinline__ void dr_meet() {  // state and output warps, each from its own loop
+    asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
+}
 template <int DK, int W>
 struct DrWalk {
     static constexpr int kRow = DK * 2, kVRow = W * 32;
     static constexpr int kQ = kC * kRow, kV = 2 * kC * kRow, kD = kV + kC * kVRow;
     static constexpr int kStage = kD + static_cast<int>(sizeof(DrChunk));
-    static constexpr int kStages = 3;
-    static constexpr int kSmem = kStages * kStage;
+    static constexpr int kStages = 4;
+    // handed over: S^T and U^T, two parts each, in operand registers, and four factors
+    static constexpr int kUAt = DK / 16 * 2 * 512, kFAt = kUAt + 2 * 2 * 512, kHand = kFAt + 512;
+    static constexpr int kHands = kStages * kStage;
+    static constexpr int kSmem = kHands + 2 * W * kHand;
 };
 template <int DT, int DK, int W>
-__global__ void __launch_bounds__(W * 32) delta_walk_kernel(DeltaArgs a, const uint16_t* kf, const uint16_t* qf, const DrChunk* data) {
+__global__ void __launch_bounds__(W * 64) delta_walk_kernel(DeltaArgs a, const uint16_t* kf, const uint16_t* qf, const DrChunk* data) {
     using C = DrWalk<DK, W>;
-    constexpr int kRow = C::kRow, kVRow = C::kVRow, kNt = DK / 8, kThreads = W * 32, kStages = C::kStages;
+    constexpr int kRow = C::kRow, kVRow = C::kVRow, kNt = DK / 8, kLoaders = W * 32, kStages = C::kStages;
     extern __shared__ __align__(1024) unsigned char smem[];
     pdl_wait();
     pdl_trigger();
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, g = lane >> 2, q4 = lane & 3;
+    const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % W, g = lane >> 2, q4 = lane & 3;
+    const bool output = threadIdx.x >= W * 32;
     const int hv = blockIdx.y, seq = blockIdx.z, hk = hv / (a.Hv / a.Hk), c0 = blockIdx.x * (16 * W);
     int t0, t1;
     dr_tokens(a, seq, t0, t1);
@@ -405,27 +440,117 @@ __global__ void __launch_bounds__(W * 32) delta_walk_kernel(DeltaArgs a, const u
     if (chunks == 0) return;
     data += (t0 / kC + static_cast<long long>(seq)) * a.Hv + hv;
     const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
+    auto hand = [&](int c) { return smem + C::kHands + ((c & 1) * W + warp) * C::kHand; };
 
-    auto load = [&](int c) {
-        const uint32_t to = base + (c % kStages) * C::kStage;
-        const int tc = t0 + c * kC, n = min(kC, t1 - tc);
-        constexpr int kKc = DK / 8, kVc = W * 2;
-        for (int i = tid; i < kC * kKc; i += kThreads) {
-            const int r = i / kKc, ch = i % kKc;
-            const long long off = ((long long)(tc + (r < n ? r : 0)) * a.Hk + hk) * DK + ch * 8;
-            dr_cp16(to + dr_at<kRow>(r, ch), kf + off, r < n);
-            dr_cp16(to + C::kQ + dr_at<kRow>(r, ch), qf + off, r < n);
+    if (output) {
+        const int tid = threadIdx.x - W * 32;
+        auto load = [&](int c) {
+            const uint32_t to = base + (c % kStages) * C::kStage;
+            const int tc = t0 + c * kC, n = min(kC, t1 - tc);
+            constexpr int kKc = DK / 8, kVc = W * 2, kStep = kLoaders / kKc;
+            {
+                const int r0 = tid / kKc, ch = tid % kKc;
+                const long long off = ((long long)tc * a.Hk + hk) * DK + ch * 8, step = (long long)a.Hk * DK;
+#pragma unroll
+                for (int m = 0; m < kC / kStep; ++m) {
+                    const int r = r0 + m * kStep;
+                    const long long at = off + (r < n ? r : 0) * step;
+                    dr_cp16(to + dr_at<kRow>(r, ch), kf + at, r < n);
+                    dr_cp16(to + C::kQ + dr_at<kRow>(r, ch), qf + at, r < n);
+                }
+            }
+            {
+                const int r0 = tid / kVc, ch = tid % kVc;
+                constexpr int kVStep = kLoaders / kVc;
+                const uint16_t* v = static_cast<const uint16_t*>(a.v) + ((long long)tc * a.Hv + hv) * a.dv + c0 + ch * 8;
+#pragma unroll
+                for (int m = 0; m < kC / kVStep; ++m) {
+                    const int r = r0 + m * kVStep;
+                    dr_cp16(to + C::kV + dr_at<kVRow>(r, ch), v + (long long)(r < n ? r : 0) * a.Hv * a.dv, r < n);
+                }
+            }
+            const char* d = reinterpret_cast<const char*>(data + (long long)c * a.Hv) + tid * 16;
+#pragma unroll
+            for (int m = 0; m < 4 * kC * 4 / kLoaders; ++m) {  // four matrices of 32 rows of 64 bytes
+                const int i = tid + m * kLoaders;
+                dr_cp16(to + C::kD + (i >> 7) * (kC * 64) + dr_at<64>((i >> 2) & 31, i & 3), d + m * kLoaders * 16, true);
+            }
+            if (tid < static_cast<int>(sizeof(DrChunk)) / 16 - 4 * kC * 4) dr_cp16(to + C::kD + 4 * kC * 64 + tid * 16, d + 4 * kC * 64, true);
+        };
+        static_assert(static_cast<int>(sizeof(DrChunk)) / 16 - 4 * kC * 4 <= kLoaders, "the factors in one go");
+        load(0);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        if (chunks > 1) load(1);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+        for (int it = 0; it <= chunks; ++it) {
+            asm volatile("cp.async.wait_group 1;" ::: "memory");
+            dr_meet<W * 64>();
+            if (it + 2 < chunks) load(it + 2);
+            asm volatile("cp.async.commit_group;" ::: "memory");
+            if (it == 0) continue;
+            const int c = it - 1;
+            const uint32_t st = base + (c % kStages) * C::kStage;
+            const DrChunk* cd = reinterpret_cast<const DrChunk*>(smem + (c % kStages) * C::kStage + C::kD);
+            const uint4* in = reinterpret_cast<const uint4*>(hand(c)) + lane;
+            const float4 f = *reinterpret_cast<const float4*>(hand(c) + C::kFAt + lane * 16);  // S^T's and U^T's factors
+            float o[4][4] = {}, y[4][4] = {};
+#pragma unroll
+            for (int k = 0; k < DK / 16; k += 2) {
+                uint32_t p[2][2][4];
+#pragma unroll
+                for (int h = 0; h < 4; ++h) {
+                    const uint4 w = in[(2 * k + h) * 32];
+                    p[h >> 1][h & 1][0] = w.x, p[h >> 1][h & 1][1] = w.y, p[h >> 1][h & 1][2] = w.z, p[h >> 1][h & 1][3] = w.w;
+                }
+                uint32_t b[4][4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) dr_ldsm4(b[i], st + C::kQ + dr_at<kRow>(8 * i + (lane & 7), 2 * k + (lane >> 3)));
+#pragma unroll
+                for (int h = 0; h < 4; ++h)
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) dr_mma(o[i], p[h >> 1][h & 1], b[i][(h >> 1) * 2], b[i][(h >> 1) * 2 + 1]);
+            }
+            uint32_t hi[2][4], lo[2][4];
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                const uint4 w = in[C::kUAt / 16 + 2 * k * 32], z = in[C::kUAt / 16 + (2 * k + 1) * 32];
+                hi[k][0] = w.x, hi[k][1] = w.y, hi[k][2] = w.z, hi[k][3] = w.w;
+                lo[k][0] = z.x, lo[k][1] = z.y, lo[k][2] = z.z, lo[k][3] = z.w;
+            }
+            uint32_t ph[4][4], pl[4][4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                dr_ldsm4(ph[i], st + C::kD + 2 * kC * 64 + dr_at<64>(8 * i + (lane & 7), lane >> 3));
+                dr_ldsm4(pl[i], st + C::kD + 3 * kC * 64 + dr_at<64>(8 * i + (lane & 7), lane >> 3));
+            }
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {  // P is lower triangular: the tokens before 16 need its first half only
+#pragma unroll
+                for (int i = 2 * k; i < 4; ++i) dr_mma(y[i], hi[k], ph[i][2 * k], ph[i][2 * k + 1]);
+#pragma unroll
+                for (int i = 2 * k; i < 4; ++i) dr_mma(y[i], lo[k], ph[i][2 * k], ph[i][2 * k + 1]);
+#pragma unroll
+                for (int i = 2 * k; i < 4; ++i) dr_mma(y[i], hi[k], pl[i][2 * k], pl[i][2 * k + 1]);
+            }
+            const int tc = t0 + c * kC, n = min(kC, t1 - tc);
+            uint16_t* to = static_cast<uint16_t*>(a.out) + ((long long)(tc + g) * a.Hv + hv) * a.dv + c0 + warp * 16 + 2 * q4;
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const float2 fq = *reinterpret_cast<const float2*>(&cd->q_out[8 * i + 2 * q4]);
+                const float2 fp = *reinterpret_cast<const float2*>(&cd->p_inv[8 * i + 2 * q4]);
+                const float r0 = o[i][0] * f.x * fq.x + y[i][0] * f.z * fp.x, r1 = o[i][1] * f.x * fq.y + y[i][1] * f.z * fp.y;
+                const float r2 = o[i][2] * f.y * fq.x + y[i][2] * f.w * fp.x, r3 = o[i][3] * f.y * fq.y + y[i][3] * f.w * fp.y;
+                // [column][token] -> [token][column]
+                const uint32_t w0 = dr_movm(dr_pack<DT>(r0, r1)), w1 = dr_movm(dr_pack<DT>(r2, r3));
+                if (8 * i + g < n) {
+                    uint16_t* at = to + (long long)(8 * i) * a.Hv * a.dv;
+                    *reinterpret_cast<uint32_t*>(at) = w0;
+                    *reinterpret_cast<uint32_t*>(at + 8) = w1;
+                }
+            }
         }
-        for (int i = tid; i < kC * kVc; i += kThreads) {
-            const int r = i / kVc, ch = i % kVc;
-            dr_cp16(to + C::kV + dr_at<kVRow>(r, ch),
-                    static_cast<const uint16_t*>(a.v) + ((long long)(tc + (r < n ? r : 0)) * a.Hv + hv) * a.dv + c0 + ch * 8, r < n);
-        }
-        const char* d = reinterpret_cast<const char*>(data + (long long)c * a.Hv);
-        for (int i = tid; i < 4 * kC * 4; i += kThreads)  // four matrices of 32 rows of 64 bytes
-            dr_cp16(to + C::kD + (i >> 7) * (kC * 64) + dr_at<64>((i >> 2) & 31, i & 3), d + i * 16, true);
-        for (int i = tid + 4 * kC * 4; i < static_cast<int>(sizeof(DrChunk) / 16); i += kThreads) dr_cp16(to + C::kD + i * 16, d + i * 16, true);
-    };
+        return;
+    }
 
     // element e of tile k: column c0 + 16 warp + g + 8 (e / 2), key dimension 8 k + 2 q4 + e % 2
     float S[kNt][4];
@@ -434,63 +559,53 @@ __global__ void __launch_bounds__(W * 32) delta_walk_kernel(DeltaArgs a, const u
     for (int k = 0; k < kNt; ++k)
 #pragma unroll
         for (int e = 0; e < 4; ++e) S[k][e] = sp[(long long)(8 * k + 2 * q4 + (e & 1)) * a.dv + (e >> 1) * 8];
-    float unit[2] = {1.f, 1.f};  // the state's columns are S unit
-
-#pragma unroll
-    for (int c = 0; c < kStages - 1; ++c) {
-        if (c < chunks) load(c);
-        asm volatile("cp.async.commit_group;" ::: "memory");
-    }
+    float unit[2] = {1.f, 1.f};  // the state's columns are S unit; powers of two
+    auto quad_max = [](float x) {
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+        return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+    };
     for (int c = 0; c < chunks; ++c) {
-        asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 2) : "memory");
-        __syncthreads();
-        if (c + kStages - 1 < chunks) load(c + kStages - 1);
-        asm volatile("cp.async.commit_group;" ::: "memory");
-        const uint32_t st = base + (c % kStages) * C::kStage;
-        const unsigned char* sd = smem + (c % kStages) * C::kStage + C::kD;
-        const DrChunk* cd = reinterpret_cast<const DrChunk*>(sd);  // its factors; the matrices are swizzled
-
-        // the state's two parts
+        // keep each column's largest within what two fp16 parts hold to 2^-22 of it
         float most[2] = {0.f, 0.f};
 #pragma unroll
         for (int k = 0; k < kNt; ++k) {
             most[0] = fmaxf(most[0], fmaxf(fabsf(S[k][0]), fabsf(S[k][1])));
             most[1] = fmaxf(most[1], fmaxf(fabsf(S[k][2]), fabsf(S[k][3])));
         }
-        auto quad_max = [](float x) {
-            x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-            return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-        };
-        float s_up[2], s_inv[2];
+        most[0] = quad_max(most[0]), most[1] = quad_max(most[1]);
+        float most_s[2] = {most[0], most[1]};
+        const bool out0 = most[0] != 0.f && !(most[0] >= 1.f && most[0] < 32768.f);
+        const bool out1 = most[1] != 0.f && !(most[1] >= 1.f && most[1] < 32768.f);
+        if (__any_sync(0xffffffffu, out0 || out1)) {
+            const float f0 = out0 ? dr_scale(most[0]) : 1.f, f1 = out1 ? dr_scale(most[1]) : 1.f;
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            s_up[h] = dr_scale(quad_max(most[h]));
-            s_inv[h] = unit[h] / s_up[h];
+            for (int k = 0; k < kNt; ++k) S[k][0] *= f0, S[k][1] *= f0, S[k][2] *= f1, S[k][3] *= f1;
+            unit[0] /= f0, unit[1] /= f1;
+            most_s[0] *= f0, most_s[1] *= f1;
         }
-        float x[4][4] = {}, o[4][4] = {};
+        dr_meet<W * 64>();
+        const uint32_t st = base + (c % kStages) * C::kStage;
+        const DrChunk* cd = reinterpret_cast<const DrChunk*>(smem + (c % kStages) * C::kStage + C::kD);  // its factors
+        uint4* give = reinterpret_cast<uint4*>(hand(c)) + lane;
+        float x[4][4] = {};
 #pragma unroll
         for (int k = 0; k < DK / 16; k += 2) {
-            uint32_t hi[2][4], lo[2][4];
+            uint32_t hi[2][4], lo[2][4], b[4][4];
 #pragma unroll
-            for (int h = 0; h < 2; ++h)
+            for (int i = 0; i < 4; ++i) dr_ldsm4(b[i], st + dr_at<kRow>(8 * i + (lane & 7), 2 * k + (lane >> 3)));
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float* v = S[2 * (k + h) + (e >> 1)] + (e & 1) * 2;
-                    dr_split(v[0] * s_up[e & 1], v[1] * s_up[e & 1], hi[h][e], lo[h][e]);
+                    dr_split2(dr_pair(v[0], v[1]), hi[h][e], lo[h][e]);
                 }
+                give[(2 * (k + h)) * 32] = make_uint4(hi[h][0], hi[h][1], hi[h][2], hi[h][3]);
+                give[(2 * (k + h) + 1) * 32] = make_uint4(lo[h][0], lo[h][1], lo[h][2], lo[h][3]);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t b[4];
-                dr_ldsm4(b, st + dr_at<kRow>(8 * i + (lane & 7), 2 * k + (lane >> 3)));
-                dr_mma(x[i], hi[0], b[0], b[1]);
-                dr_mma(x[i], hi[1], b[2], b[3]);
-                dr_mma(x[i], lo[0], b[0], b[1]);
-                dr_mma(x[i], lo[1], b[2], b[3]);
-                dr_ldsm4(b, st + C::kQ + dr_at<kRow>(8 * i + (lane & 7), 2 * k + (lane >> 3)));
-                dr_mma(o[i], hi[0], b[0], b[1]);
-                dr_mma(o[i], hi[1], b[2], b[3]);
-                dr_mma(o[i], lo[0], b[0], b[1]);
-                dr_mma(o[i], lo[1], b[2], b[3]);
+                for (int i = 0; i < 4; ++i) dr_mma(x[i], hi[h], b[i][2 * h], b[i][2 * h + 1]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) dr_mma(x[i], lo[h], b[i][2 * h], b[i][2 * h + 1]);
             }
         }
         // V - diag(e^G) K S0, transposed, and its two parts
@@ -505,8 +620,8 @@ __global__ void __launch_bounds__(W * 32) delta_walk_kernel(DeltaArgs a, const u
                                           : make_float2(__uint_as_float(v0[i] << 16), __uint_as_float(v0[i] & 0xFFFF0000u));
                 const float2 y1 = DT == 1 ? __half22float2(*reinterpret_cast<const __half2*>(&v1[i]))
                                           : make_float2(__uint_as_float(v1[i] << 16), __uint_as_float(v1[i] & 0xFFFF0000u));
-                x[i][0] = y0.x - f.x * (x[i][0] * s_inv[0]), x[i][1] = y0.y - f.y * (x[i][1] * s_inv[0]);
-                x[i][2] = y1.x - f.x * (x[i][2] * s_inv[1]), x[i][3] = y1.y - f.y * (x[i][3] * s_inv[1]);
+                x[i][0] = y0.x - f.x * (x[i][0] * unit[0]), x[i][1] = y0.y - f.y * (x[i][1] * unit[0]);
+                x[i][2] = y1.x - f.x * (x[i][2] * unit[1]), x[i][3] = y1.y - f.y * (x[i][3] * unit[1]);
             }
         }
         auto parts = [&](const float(&v)[4][4], const float(&up)[2], uint32_t(&hi)[2][4], uint32_t(&lo)[2][4]) {
@@ -515,7 +630,7 @@ __global__ void __launch_bounds__(W * 32) delta_walk_kernel(DeltaArgs a, const u
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
                     const float* w = v[2 * k + (e >> 1)] + (e & 1) * 2;
-                    dr_split(w[0] * up[e & 1], w[1] * up[e & 1], hi[k][e], lo[k][e]);
+                    dr_split2(dr_mul2(dr_pair(w[0], w[1]), up[e & 1]), hi[k][e], lo[k][e]);
                 }
         };
         auto row_max = [&](const float(&v)[4][4], float(&m)[2]) {
@@ -527,24 +642,24 @@ __global__ void __launch_bounds__(W * 32) delta_walk_kernel(DeltaArgs a, const u
             }
             m[0] = quad_max(m[0]), m[1] = quad_max(m[1]);
         };
-        uint32_t hi[2][4], lo[2][4];
+        uint32_t hi[2][4], lo[2][4], th[4][4], tl[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            dr_ldsm4(th[i], st + C::kD + dr_at<64>(8 * i + (lane & 7), lane >> 3));
+            dr_ldsm4(tl[i], st + C::kD + kC * 64 + dr_at<64>(8 * i + (lane & 7), lane >> 3));
+        }
         row_max(x, most);
         float up[2] = {dr_scale(most[0]), dr_scale(most[1])};
         parts(x, up, hi, lo);
         float u[4][4] = {};
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {  // T is lower triangular: the tokens before 16 need its first half only
-            uint32_t th[4], tl[4];
-            dr_ldsm4(th, st + C::kD + dr_at<64>(8 * i + (lane & 7), lane >> 3));
-            dr_ldsm4(tl, st + C::kD + kC * 64 + dr_at<64>(8 * i + (lane & 7), lane >> 3));
-            dr_mma(u[i], hi[0], th[0], th[1]);
-            dr_mma(u[i], lo[0], th[0], th[1]);
-            dr_mma(u[i], hi[0], tl[0], tl[1]);
-            if (i >= 2) {
-                dr_mma(u[i], hi[1], th[2], th[3]);
-                dr_mma(u[i], lo[1], th[2], th[3]);
-                dr_mma(u[i], hi[1], tl[2], tl[3]);
-            }
+        for (int k = 0; k < 2; ++k) {  // T is lower triangular
+#pragma unroll
+            for (int i = 2 * k; i < 4; ++i) dr_mma(u[i], hi[k], th[i][2 * k], th[i][2 * k + 1]);
+#pragma unroll
+            for (int i = 2 * k; i < 4; ++i) dr_mma(u[i], lo[k], th[i][2 * k], th[i][2 * k + 1]);
+#pragma unroll
+            for (int i = 2 * k; i < 4; ++i) dr_mma(u[i], hi[k], tl[i][2 * k], tl[i][2 * k + 1]);
         }
         {
             const float v_inv[2] = {1.f / up[0], 1.f / up[1]};
@@ -555,66 +670,59 @@ __global__ void __launch_bounds__(W * 32) delta_walk_kernel(DeltaArgs a, const u
                 u[i][2] *= f.x * v_inv[1], u[i][3] *= f.y * v_inv[1];
             }
         }
-        // outputs: diag(e^G) Q S0 + P U
-        row_max(u, most);
-        up[0] = dr_scale(most[0]), up[1] = dr_scale(most[1]);
-        parts(u, up, hi, lo);
-        const int tc = t0 + c * kC, n = min(kC, t1 - tc);
-        const float u_inv[2] = {1.f / up[0], 1.f / up[1]};
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            uint32_t ph[4], pl[4];
-            float y[4] = {};
-            dr_ldsm4(ph, st + C::kD + 2 * kC * 64 + dr_at<64>(8 * i + (lane & 7), lane >> 3));
-            dr_ldsm4(pl, st + C::kD + 3 * kC * 64 + dr_at<64>(8 * i + (lane & 7), lane >> 3));
-            dr_mma(y, hi[0], ph[0], ph[1]);
-            dr_mma(y, lo[0], ph[0], ph[1]);
-            dr_mma(y, hi[0], pl[0], pl[1]);
-            if (i >= 2) {
-                dr_mma(y, hi[1], ph[2], ph[3]);
-                dr_mma(y, lo[1], ph[2], ph[3]);
-                dr_mma(y, hi[1], pl[2], pl[3]);
-            }
-            const float2 fq = *reinterpret_cast<const float2*>(&cd->q_out[8 * i + 2 * q4]);
-            const float2 fp = *reinterpret_cast<const float2*>(&cd->p_inv[8 * i + 2 * q4]);
-            const float r0 = o[i][0] * s_inv[0] * fq.x + y[0] * u_inv[0] * fp.x, r1 = o[i][1] * s_inv[0] * fq.y + y[1] * u_inv[0] * fp.y;
-            const float r2 = o[i][2] * s_inv[1] * fq.x + y[2] * u_inv[1] * fp.x, r3 = o[i][3] * s_inv[1] * fq.y + y[3] * u_inv[1] * fp.y;
-            // [column][token] -> [token][column]
-            const uint32_t w0 = dr_movm(dr_pack<DT>(r0, r1)), w1 = dr_movm(dr_pack<DT>(r2, r3));
-            if (8 * i + g < n) {
-                uint16_t* to = static_cast<uint16_t*>(a.out) + ((long long)(tc + 8 * i + g) * a.Hv + hv) * a.dv + c0 + warp * 16 + 2 * q4;
-                *reinterpret_cast<uint32_t*>(to) = w0;
-                *reinterpret_cast<uint32_t*>(to + 8) = w1;
-            }
-        }
         // the state after the chunk
+        {
+            float w[4][4];
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
-            const float2 f = *reinterpret_cast<const float2*>(&cd->rest[8 * i + 2 * q4]);
-            u[i][0] *= f.x, u[i][1] *= f.y, u[i][2] *= f.x, u[i][3] *= f.y;
-        }
-        row_max(u, most);
-        const float decay = cd->decay[0];
-        float keep[2];
+            for (int i = 0; i < 4; ++i) {
+                const float2 f = *reinterpret_cast<const float2*>(&cd->rest[8 * i + 2 * q4]);
+                w[i][0] = u[i][0] * f.x, w[i][1] = u[i][1] * f.y, w[i][2] = u[i][2] * f.x, w[i][3] = u[i][3] * f.y;
+            }
+            float more[2];
+            row_max(w, more);
+            const float decay = cd->decay[0];
+            const float s_inv[2] = {unit[0], unit[1]};
+            float keep[2];
 #pragma unroll
-        for (int h = 0; h < 2; ++h) {
-            // not so large that the state leaves f32's range in these units
-            up[h] = fminf(dr_scale(most[h]), s_up[h] / unit[h] * 65536.f);
-            keep[h] = decay * unit[h] * up[h];
-            unit[h] = 1.f / up[h];
-        }
-        parts(u, up, hi, lo);
+            for (int h = 0; h < 2; ++h) {
+                // in the state's own unit, while what is left of it or what is added keeps to that window
+                const float r = fmaxf(decay * most_s[h], more[h] / unit[h]);
+                const float f = r == 0.f || (r >= 1.f && r < 32768.f) ? 1.f : dr_scale(r);
+                keep[h] = decay * f;
+                up[h] = f / unit[h];
+                unit[h] /= f;
+            }
+            parts(w, up, hi, lo);
 #pragma unroll
-        for (int k = 0; k < kNt; ++k) {
-            S[k][0] *= keep[0], S[k][1] *= keep[0], S[k][2] *= keep[1], S[k][3] *= keep[1];
-            uint32_t b[4];
-            dr_ldsm4t(b, st + dr_at<kRow>(lane, k));
-            dr_mma(S[k], hi[0], b[0], b[1]);
-            dr_mma(S[k], hi[1], b[2], b[3]);
-            dr_mma(S[k], lo[0], b[0], b[1]);
-            dr_mma(S[k], lo[1], b[2], b[3]);
+            for (int k = 0; k < kNt; k += 4) {
+                uint32_t b[4][4];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    dr_ldsm4t(b[i], st + dr_at<kRow>(lane, k + i));
+                    S[k + i][0] *= keep[0], S[k + i][1] *= keep[0], S[k + i][2] *= keep[1], S[k + i][3] *= keep[1];
+                }
+#pragma unroll
+                for (int i = 0; i < 4; ++i) dr_mma(S[k + i], hi[0], b[i][0], b[i][1]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) dr_mma(S[k + i], hi[1], b[i][2], b[i][3]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) dr_mma(S[k + i], lo[0], b[i][0], b[i][1]);
+#pragma unroll
+                for (int i = 0; i < 4; ++i) dr_mma(S[k + i], lo[1], b[i][2], b[i][3]);
+            }
+            // U^T for the outputs
+            row_max(u, most);
+            up[0] = dr_scale(most[0]), up[1] = dr_scale(most[1]);
+            parts(u, up, hi, lo);
+#pragma unroll
+            for (int k = 0; k < 2; ++k) {
+                give[C::kUAt / 16 + 2 * k * 32] = make_uint4(hi[k][0], hi[k][1], hi[k][2], hi[k][3]);
+                give[C::kUAt / 16 + (2 * k + 1) * 32] = make_uint4(lo[k][0], lo[k][1], lo[k][2], lo[k][3]);
+            }
+            *reinterpret_cast<float4*>(hand(c) + C::kFAt + lane * 16) = make_float4(s_inv[0], s_inv[1], 1.f / up[0], 1.f / up[1]);
         }
     }
+    dr_meet<W * 64>();  // the last chunk's hand-over
 #pragma unroll
     for (int k = 0; k < kNt; ++k)
 #pragma unroll
@@ -656,7 +764,7 @@ cudaError_t launch_walk(const DeltaArgs& a, const uint16_t* kf, const uint16_t* 
     cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     void* args[] = {const_cast<DeltaArgs*>(&a), &kf, &qf, &data};
-    return launch_kernel(f, dim3(a.dv / (16 * W), a.Hv, a.n), dim3(W * 32), smem, true, s, args);
+    return launch_kernel(f, dim3(a.dv / (16 * W), a.Hv, a.n), dim3(W * 64), smem, true, s, args);
 }
 
 template <int DT, int DK>

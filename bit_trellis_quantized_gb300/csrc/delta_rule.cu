@@ -188,6 +188,8 @@ __device__ __forceinline__ float dr_scale(float most) {
     const int k = min(60, max(-114, 140 - static_cast<int>(__float_as_uint(most) >> 23)));
     return __uint_as_float(static_cast<uint32_t>(k + 127) << 23);
 }
+// 1 / p of a power of two in 2^-126..2^126
+__device__ __forceinline__ float dr_inv(float p) { return __uint_as_float(0x7F000000u - __float_as_uint(p)); }
 // x and y as two fp16 parts each
 __device__ __forceinline__ void dr_split(float x, float y, uint32_t& hi, uint32_t& lo) {
     const __half2 h = __floats2half2_rn(x, y);
@@ -577,10 +579,10 @@ __global__ void __launch_bounds__(W * 64) delta_walk_kernel(DeltaArgs a, const u
         const bool out0 = most[0] != 0.f && !(most[0] >= 1.f && most[0] < 32768.f);
         const bool out1 = most[1] != 0.f && !(most[1] >= 1.f && most[1] < 32768.f);
         if (__any_sync(0xffffffffu, out0 || out1)) {
-            const float f0 = out0 ? dr_scale(most[0]) : 1.f, f1 = out1 ? dr_scale(most[1]) : 1.f;
+            const float f0 = out0 ? fminf(dr_scale(most[0]), unit[0] * 0x1p100f) : 1.f, f1 = out1 ? fminf(dr_scale(most[1]), unit[1] * 0x1p100f) : 1.f;
 #pragma unroll
             for (int k = 0; k < kNt; ++k) S[k][0] *= f0, S[k][1] *= f0, S[k][2] *= f1, S[k][3] *= f1;
-            unit[0] /= f0, unit[1] /= f1;
+            unit[0] *= dr_inv(f0), unit[1] *= dr_inv(f1);
             most_s[0] *= f0, most_s[1] *= f1;
         }
         dr_meet<W * 64>();
@@ -662,7 +664,7 @@ __global__ void __launch_bounds__(W * 64) delta_walk_kernel(DeltaArgs a, const u
             for (int i = 2 * k; i < 4; ++i) dr_mma(u[i], hi[k], tl[i][2 * k], tl[i][2 * k + 1]);
         }
         {
-            const float v_inv[2] = {1.f / up[0], 1.f / up[1]};
+            const float v_inv[2] = {dr_inv(up[0]), dr_inv(up[1])};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
                 const float2 f = *reinterpret_cast<const float2*>(&cd->t_inv[8 * i + 2 * q4]);
@@ -686,11 +688,11 @@ __global__ void __launch_bounds__(W * 64) delta_walk_kernel(DeltaArgs a, const u
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 // in the state's own unit, while what is left of it or what is added keeps to that window
-                const float r = fmaxf(decay * most_s[h], more[h] / unit[h]);
-                const float f = r == 0.f || (r >= 1.f && r < 32768.f) ? 1.f : dr_scale(r);
+                const float r = fmaxf(decay * most_s[h], more[h] * dr_inv(unit[h]));
+                const float f = r == 0.f || (r >= 1.f && r < 32768.f) ? 1.f : fminf(dr_scale(r), unit[h] * 0x1p100f);
                 keep[h] = decay * f;
-                up[h] = f / unit[h];
-                unit[h] /= f;
+                unit[h] *= dr_inv(f);
+                up[h] = dr_inv(unit[h]);
             }
             parts(w, up, hi, lo);
 #pragma unroll
@@ -719,7 +721,7 @@ __global__ void __launch_bounds__(W * 64) delta_walk_kernel(DeltaArgs a, const u
                 give[C::kUAt / 16 + 2 * k * 32] = make_uint4(hi[k][0], hi[k][1], hi[k][2], hi[k][3]);
                 give[C::kUAt / 16 + (2 * k + 1) * 32] = make_uint4(lo[k][0], lo[k][1], lo[k][2], lo[k][3]);
             }
-            *reinterpret_cast<float4*>(hand(c) + C::kFAt + lane * 16) = make_float4(s_inv[0], s_inv[1], 1.f / up[0], 1.f / up[1]);
+            *reinterpret_cast<float4*>(hand(c) + C::kFAt + lane * 16) = make_float4(s_inv[0], s_inv[1], dr_inv(up[0]), dr_inv(up[1]));
         }
     }
     dr_meet<W * 64>();  // the last chunk's hand-over

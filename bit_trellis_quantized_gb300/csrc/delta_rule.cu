@@ -211,13 +211,20 @@ __device__ __forceinline__ uint32_t dr_at(int r, int c) {
 // The chunk data of sequence s begin at slot t0 / kC + s: no two sequences share one.
 __host__ __device__ inline long long dr_slots(int T, int n) { return T / kC + static_cast<long long>(n); }
 
+// One CTA of two warps a (chunk, key head): norms, k . k and q . k on the tensor
+// cores, then a warp a value head. L and P go row by lane, so that a row's
+// largest value and its 16-byte stores are a lane's own; the solve for T goes
+// column by lane, its rows of L broadcast from shared memory. Bound: latency of
+// that chain of some 1600 instructions a head, hidden by six CTAs a
+// multiprocessor.
 template <int DT, int DK>
-__global__ void __launch_bounds__(128) delta_prepare_kernel(DeltaArgs a, uint16_t* kf, uint16_t* qf, DrChunk* out) {
-    constexpr int kRow = DK * 2, kPer = DK / 4;
+__global__ void __launch_bounds__(64) delta_prepare_kernel(DeltaArgs a, uint16_t* kf, uint16_t* qf, DrChunk* out) {
+    constexpr int kRow = DK * 2, kVec = DK / 16;  // 16-byte pieces of half a row
     __shared__ __align__(128) unsigned char ks[kC * kRow], qs[kC * kRow];
     __shared__ float dots[2][kC][kC + 1];  // k_i . k_j and q_i . k_j
     __shared__ float inv[2][kC];           // 1 / |k|, 1 / |q| (with the rows' powers of two)
-    __shared__ __align__(16) float Ls[4][kC][kC];
+    __shared__ float4 col[2][kC];          // by warp, of token j: its sum of decays (two parts), 1 / |k_j|
+    __shared__ __align__(16) float Ls[2][kC][kC + 4];
     pdl_wait();
     pdl_trigger();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, hk = blockIdx.y;
@@ -237,79 +244,87 @@ __global__ void __launch_bounds__(128) delta_prepare_kernel(DeltaArgs a, uint16_
     t0 += static_cast<int>(ahead) * kC;
     const int n = min(kC, t1 - t0);
     {
-        // four threads a row: norms, and for bf16 the power of two that brings the row's largest value to 1..2
-        const int r = tid >> 2, part = tid & 3;
+        // two threads a row: norms, and for bf16 the power of two that brings the row's largest value to 1..2
+        const int r = tid >> 1, part = tid & 1;
+        uint4 w[2][kVec];
 #pragma unroll
         for (int which = 0; which < 2; ++which) {
-            const uint16_t* src = static_cast<const uint16_t*>(which ? a.q : a.k) + ((long long)(t0 + r) * a.Hk + hk) * DK + part * kPer;
-            uint4 w[kPer / 8];
-            float sum = 0.f, most = 0.f;
+            const uint16_t* src = static_cast<const uint16_t*>(which ? a.q : a.k) + ((long long)(t0 + r) * a.Hk + hk) * DK + part * (DK / 2);
 #pragma unroll
-            for (int i = 0; i < kPer / 8; ++i) {
-                w[i] = r < n ? *reinterpret_cast<const uint4*>(src + i * 8) : make_uint4(0, 0, 0, 0);
-                const uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+            for (int i = 0; i < kVec; ++i) w[which][i] = r < n ? *reinterpret_cast<const uint4*>(src + i * 8) : make_uint4(0, 0, 0, 0);
+        }
+#pragma unroll
+        for (int which = 0; which < 2; ++which) {
+            float sum0 = 0.f, sum1 = 0.f, most = 0.f;
+#pragma unroll
+            for (int i = 0; i < kVec; ++i) {
+                const uint32_t v[4] = {w[which][i].x, w[which][i].y, w[which][i].z, w[which][i].w};
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    const float x = DT == 1 ? h2f_bits(v[j] & 0xFFFF) : __uint_as_float(v[j] << 16);
-                    const float y = DT == 1 ? h2f_bits(v[j] >> 16) : __uint_as_float(v[j] & 0xFFFF0000u);
-                    sum += x * x;
-                    sum += y * y;
-                    most = fmaxf(most, fmaxf(fabsf(x), fabsf(y)));
+                    float2 x;
+                    if (DT == 1)
+                        x = __half22float2(*reinterpret_cast<const __half2*>(&v[j]));
+                    else
+                        x = make_float2(__uint_as_float(v[j] << 16), __uint_as_float(v[j] & 0xFFFF0000u));
+                    sum0 += x.x * x.x;
+                    sum1 += x.y * x.y;
+                    if (DT == 2) most = fmaxf(most, fmaxf(fabsf(x.x), fabsf(x.y)));
                 }
             }
+            float sum = sum0 + sum1;
             sum += __shfl_xor_sync(0xffffffffu, sum, 1);
-            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
-            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
-            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
             float up = 1.f;
             if (DT == 2) {
+                most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
                 up = dr_scale(most) * 0x1p-13f;
 #pragma unroll
-                for (int i = 0; i < kPer / 8; ++i) {
-                    uint32_t v[4] = {w[i].x, w[i].y, w[i].z, w[i].w};
+                for (int i = 0; i < kVec; ++i) {
+                    uint32_t v[4] = {w[which][i].x, w[which][i].y, w[which][i].z, w[which][i].w};
 #pragma unroll
                     for (int j = 0; j < 4; ++j)
                         v[j] = dr_first(__uint_as_float(v[j] << 16) * up, __uint_as_float(v[j] & 0xFFFF0000u) * up);
-                    w[i] = make_uint4(v[0], v[1], v[2], v[3]);
+                    w[which][i] = make_uint4(v[0], v[1], v[2], v[3]);
                     if (r < n)
-                        *reinterpret_cast<uint4*>((which ? qf : kf) + ((long long)(t0 + r) * a.Hk + hk) * DK + part * kPer + i * 8) = w[i];
+                        *reinterpret_cast<uint4*>((which ? qf : kf) + ((long long)(t0 + r) * a.Hk + hk) * DK + part * (DK / 2) + i * 8) = w[which][i];
                 }
             }
             if (part == 0) inv[which][r] = r >= n ? 0.f : (a.eps >= 0.f ? 1.f / sqrtf(sum + a.eps) : 1.f) / up;
 #pragma unroll
-            for (int i = 0; i < kPer / 8; ++i)
-                *reinterpret_cast<uint4*>((which ? qs : ks) + dr_at<kRow>(r, part * (kPer / 8) + i)) = w[i];
+            for (int i = 0; i < kVec; ++i)
+                *reinterpret_cast<uint4*>((which ? qs : ks) + dr_at<kRow>(r, part * kVec + i)) = w[which][i];
         }
     }
     __syncthreads();
     {
-        // warps 0 and 1: k . k, 2 and 3: q . k, 16 rows each
-        const int m0 = (warp & 1) * 16;
-        const uint32_t A = static_cast<uint32_t>(__cvta_generic_to_shared(warp < 2 ? ks : qs));
+        // warp 0: k . k, warp 1: q . k
+        const uint32_t A = static_cast<uint32_t>(__cvta_generic_to_shared(warp == 0 ? ks : qs));
         const uint32_t B = static_cast<uint32_t>(__cvta_generic_to_shared(ks));
-        float c[4][4] = {};
+        float c[2][4][4] = {};
 #pragma unroll
         for (int k = 0; k < DK / 16; k += 2) {
-            uint32_t f[2][4];
+            uint32_t b[4][4];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) dr_ldsm4(f[h], A + dr_at<kRow>(m0 + (lane & 15), 2 * (k + h) + (lane >> 4)));
+            for (int i = 0; i < 4; ++i) dr_ldsm4(b[i], B + dr_at<kRow>(8 * i + (lane & 7), 2 * k + (lane >> 3)));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                uint32_t b[4];
-                dr_ldsm4(b, B + dr_at<kRow>(8 * i + (lane & 7), 2 * k + (lane >> 3)));
-                dr_mma(c[i], f[0], b[0], b[1]);
-                dr_mma(c[i], f[1], b[2], b[3]);
-            }
+            for (int h = 0; h < 2; ++h)
+#pragma unroll
+                for (int m = 0; m < 2; ++m) {
+                    uint32_t f[4];
+                    dr_ldsm4(f, A + dr_at<kRow>(16 * m + (lane & 15), 2 * (k + h) + (lane >> 4)));
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) dr_mma(c[m][i], f, b[i][2 * h], b[i][2 * h + 1]);
+                }
         }
 #pragma unroll
-        for (int i = 0; i < 4; ++i)
+        for (int m = 0; m < 2; ++m)
 #pragma unroll
-            for (int e = 0; e < 4; ++e) dots[warp >> 1][m0 + (lane >> 2) + (e >> 1) * 8][8 * i + (lane & 3) * 2 + (e & 1)] = c[i][e];
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) dots[warp][16 * m + (lane >> 2) + (e >> 1) * 8][8 * i + (lane & 3) * 2 + (e & 1)] = c[m][i][e];
     }
     __syncthreads();
-    // a warp a value head; lane j: column j
     const int rep = a.Hv / a.Hk;
-    for (int r = warp; r < rep; r += 4) {
+    for (int r = warp; r < rep; r += 2) {
         const int hv = hk * rep + r;
         DrChunk* o = out + (long long)blockIdx.x * a.Hv + hv;
         const long long at = (long long)(t0 + lane) * a.Hv + hv;
@@ -322,24 +337,45 @@ __global__ void __launch_bounds__(128) delta_prepare_kernel(DeltaArgs a, uint16_
             const double p = __shfl_up_sync(0xffffffffu, G, m);
             if (lane >= m) G += p;
         }
-        const double G_all = __shfl_sync(0xffffffffu, G, 31);
-        const float rk = inv[0][lane];
-        float p_inv = 0.f, t_inv = 0.f;
-        float(&L)[kC][kC] = Ls[warp];
+        const float g_hi = static_cast<float>(G), g_lo = static_cast<float>(G - g_hi);
+        const float all_hi = __shfl_sync(0xffffffffu, g_hi, 31), all_lo = __shfl_sync(0xffffffffu, g_lo, 31);
+        const float rk = inv[0][lane], rq = a.scale * inv[1][lane];
+        float(&L)[kC][kC + 4] = Ls[warp];
         __syncwarp();
-#pragma unroll 4
-        for (int i = 0; i < kC; ++i) {
-            const double Gi = __shfl_sync(0xffffffffu, G, i);
-            const float bi = __shfl_sync(0xffffffffu, beta, i);
-            const float e = lane <= i ? expf(static_cast<float>(Gi - G)) * rk : 0.f;
-            L[i][lane] = lane < i ? bi * inv[0][i] * e * dots[0][i][lane] : 0.f;
-            const float p = lane <= i ? a.scale * inv[1][i] * e * dots[1][i][lane] : 0.f;
-            const float up = dr_scale(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(p)))));
-            uint32_t hi, lo;
-            dr_split(p * up, 0.f, hi, lo);
-            o->p_hi[i][lane] = static_cast<uint16_t>(hi);
-            o->p_lo[i][lane] = static_cast<uint16_t>(lo);
-            if (lane == i) p_inv = 1.f / up;
+        col[warp][lane] = make_float4(g_hi, g_lo, rk, 0.f);
+        __syncwarp();
+        // rows of two matrices -> two fp16 parts of each value times `up`, 16 bytes at a time
+        auto store = [&](uint16_t(&hi)[kC][kC], uint16_t(&lo)[kC][kC], const float(&v)[kC], float up) {
+#pragma unroll
+            for (int j = 0; j < kC; j += 8) {
+                uint32_t h[4], l[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) dr_split(v[j + 2 * e] * up, v[j + 2 * e + 1] * up, h[e], l[e]);
+                *reinterpret_cast<uint4*>(&hi[lane][j]) = make_uint4(h[0], h[1], h[2], h[3]);
+                *reinterpret_cast<uint4*>(&lo[lane][j]) = make_uint4(l[0], l[1], l[2], l[3]);
+            }
+        };
+        {
+            // row `lane` of L and of P
+            float p[kC], most = 0.f;
+            const float bk = beta * rk;
+#pragma unroll
+            for (int j = 0; j < kC; j += 4) {
+                float l[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float4 c = col[warp][j + e];
+                    const float d = (g_hi - c.x) + (g_lo - c.y);
+                    const float f = j + e <= lane ? expf(d) * c.z : 0.f;
+                    l[e] = j + e < lane ? bk * f * dots[0][lane][j + e] : 0.f;
+                    p[j + e] = j + e <= lane ? rq * f * dots[1][lane][j + e] : 0.f;
+                    most = fmaxf(most, fabsf(p[j + e]));
+                }
+                *reinterpret_cast<float4*>(&L[lane][j]) = make_float4(l[0], l[1], l[2], l[3]);
+            }
+            const float up = dr_scale(most);
+            store(o->p_hi, o->p_lo, p, up);
+            o->p_inv[lane] = dr_inv(up);
         }
         __syncwarp();
         // column `lane` of (1 + L)^-1, row by row
@@ -357,23 +393,27 @@ __global__ void __launch_bounds__(128) delta_prepare_kernel(DeltaArgs a, uint16_
             }
             x[i] = (acc[0] + acc[1]) + (acc[2] + acc[3]);
         }
+        __syncwarp();
 #pragma unroll
-        for (int i = 0; i < kC; ++i) {
-            const float t = x[i] * beta;
-            const float up = dr_scale(__uint_as_float(__reduce_max_sync(0xffffffffu, __float_as_uint(fabsf(t)))));
-            uint32_t hi, lo;
-            dr_split(t * up, 0.f, hi, lo);
-            o->t_hi[i][lane] = static_cast<uint16_t>(hi);
-            o->t_lo[i][lane] = static_cast<uint16_t>(lo);
-            if (lane == i) t_inv = 1.f / up;
+        for (int i = 0; i < kC; ++i) L[i][lane] = x[i] * beta;
+        __syncwarp();
+        {
+            float most = 0.f;
+#pragma unroll
+            for (int j = 0; j < kC; j += 4) {
+                const float4 v = *reinterpret_cast<const float4*>(&L[lane][j]);
+                x[j] = v.x, x[j + 1] = v.y, x[j + 2] = v.z, x[j + 3] = v.w;
+                most = fmaxf(fmaxf(most, fmaxf(fabsf(v.x), fabsf(v.y))), fmaxf(fabsf(v.z), fabsf(v.w)));
+            }
+            const float up = dr_scale(most);
+            store(o->t_hi, o->t_lo, x, up);
+            o->t_inv[lane] = dr_inv(up);
         }
-        const float eg = expf(static_cast<float>(G));
+        const float eg = expf(g_hi + g_lo);
         o->fall[lane] = eg * rk;
-        o->rest[lane] = expf(static_cast<float>(G_all - G)) * rk;
-        o->t_inv[lane] = t_inv;
-        o->p_inv[lane] = p_inv;
-        o->q_out[lane] = a.scale * inv[1][lane] * eg;
-        o->decay[lane] = expf(static_cast<float>(G_all));
+        o->rest[lane] = expf((all_hi - g_hi) + (all_lo - g_lo)) * rk;
+        o->q_out[lane] = rq * eg;
+        o->decay[lane] = expf(all_hi + all_lo);
     }
 }
 
@@ -776,7 +816,7 @@ cudaError_t launch_chunks(const DeltaArgs& a, char* ws, cudaStream_t s) {
     uint16_t* kf = reinterpret_cast<uint16_t*>(ws + p.kf);
     uint16_t* qf = reinterpret_cast<uint16_t*>(ws + p.qf);
     void* args[] = {const_cast<DeltaArgs*>(&a), &kf, &qf, &data};
-    cudaError_t e = launch_kernel(reinterpret_cast<const void*>(delta_prepare_kernel<DT, DK>), dim3(dr_slots(a.T, a.n), a.Hk), dim3(128), 0,
+    cudaError_t e = launch_kernel(reinterpret_cast<const void*>(delta_prepare_kernel<DT, DK>), dim3(dr_slots(a.T, a.n), a.Hk), dim3(64), 0,
                                   true, s, args);
     if (e != cudaSuccess) return e;
     const uint16_t* k = DT == 1 ? static_cast<const uint16_t*>(a.k) : kf;

@@ -435,6 +435,9 @@ __device__ __forceinline__ unsigned long long dr_pair(float x, float y) {
     asm("mov.b64 %0, {%1, %2};" : "=l"(r) : "f"(x), "f"(y));
     return r;
 }
+__device__ __forceinline__ void dr_unpair(unsigned long long xy, float& x, float& y) {
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(x), "=f"(y) : "l"(xy));
+}
 __device__ __forceinline__ unsigned long long dr_mul2(unsigned long long x, float f) {
     unsigned long long r;
     asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(r) : "l"(x), "l"(dr_pair(f, f)));
@@ -446,11 +449,11 @@ __device__ __forceinline__ unsigned long long dr_mul2(unsigned long long x, floa
 // cores' accumulator layout for the whole walk. In that form each product's
 // result is the next one's left operand, register for register: S^T K^T, then
 // (V - ...)^T T^T, then U^T K. Nothing of that chain passes through shared
-// memory. It hands the operands S^T and U^T to an output warp, which makes
-// S^T Q^T + U^T P^T one chunk later and fetches the next chunks (cp.async); all
-// warps meet once a chunk. The chain bounds a long sequence: one warp doing
-// both took 2.8 us a chunk (128 x 128 states), mostly waiting for its own last
-// instruction.
+// memory. It hands the operand S^T and U^T to an output warp, which makes
+// S^T Q^T + U^T P^T one chunk later; a loading warp fetches the next chunks
+// (cp.async); all warps meet once a chunk. The chain bounds a long sequence: one
+// warp doing all of it took 2.8 us a chunk (128 x 128 states), mostly waiting
+// for its own last instruction.
 template <int kThreads>
 __device__ __forceinline__ void dr_meet() {  // state and output warps, each from its own loop
     asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
@@ -461,20 +464,22 @@ struct DrWalk {
     static constexpr int kQ = kC * kRow, kV = 2 * kC * kRow, kD = kV + kC * kVRow;
     static constexpr int kStage = kD + static_cast<int>(sizeof(DrChunk));
     static constexpr int kStages = 4;
-    // handed over: S^T and U^T, two parts each, in operand registers, and four factors
-    static constexpr int kUAt = DK / 16 * 2 * 512, kFAt = kUAt + 2 * 2 * 512, kHand = kFAt + 512;
+    // with two warps of each kind, loading ones share a scheduler with output ones: two warps before them leave at once
+    static constexpr int kIdle = W == 2 ? 2 : 0, kThreads = (3 * W + kIdle) * 32, kMeet = 3 * W * 32;
+    // handed over: S^T, two parts in operand registers; U^T in f32; the columns' factors of S
+    static constexpr int kUAt = DK / 16 * 2 * 512, kFAt = kUAt + 4 * 512, kHand = kFAt + 256;
     static constexpr int kHands = kStages * kStage;
     static constexpr int kSmem = kHands + 2 * W * kHand;
 };
 template <int DT, int DK, int W>
-__global__ void __launch_bounds__(W * 64) delta_walk_kernel(DeltaArgs a, const uint16_t* kf, const uint16_t* qf, const DrChunk* data) {
+__global__ void __launch_bounds__(DrWalk<DK, W>::kThreads) delta_walk_kernel(DeltaArgs a, const uint16_t* kf, const uint16_t* qf, const DrChunk* data) {
     using C = DrWalk<DK, W>;
     constexpr int kRow = C::kRow, kVRow = C::kVRow, kNt = DK / 8, kLoaders = W * 32, kStages = C::kStages;
     extern __shared__ __align__(1024) unsigned char smem[];
     pdl_wait();
     pdl_trigger();
     const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % W, g = lane >> 2, q4 = lane & 3;
-    const bool output = threadIdx.x >= W * 32;
+    const int role = threadIdx.x / (W * 32);  // 0: state, 1: output
     const int hv = blockIdx.y, seq = blockIdx.z, hk = hv / (a.Hv / a.Hk), c0 = blockIdx.x * (16 * W);
     int t0, t1;
     dr_tokens(a, seq, t0, t1);
@@ -484,8 +489,32 @@ __global__ void __launch_bounds__(W * 64) delta_walk_kernel(DeltaArgs a, const u
     const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
     auto hand = [&](int c) { return smem + C::kHands + ((c & 1) * W + warp) * C::kHand; };
 
-    if (output) {
-        const int tid = threadIdx.x - W * 32;
+    auto quad_max = [](float x) {
+        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
+        return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
+    };
+    auto parts = [&](const float(&v)[4][4], const float(&up)[2], uint32_t(&hi)[2][4], uint32_t(&lo)[2][4]) {
+#pragma unroll
+        for (int k = 0; k < 2; ++k)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const float* w = v[2 * k + (e >> 1)] + (e & 1) * 2;
+                dr_split2(dr_mul2(dr_pair(w[0], w[1]), up[e & 1]), hi[k][e], lo[k][e]);
+            }
+    };
+    auto row_max = [&](const float(&v)[4][4], float(&m)[2]) {
+        m[0] = m[1] = 0.f;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            m[0] = fmaxf(m[0], fmaxf(fabsf(v[i][0]), fabsf(v[i][1])));
+            m[1] = fmaxf(m[1], fmaxf(fabsf(v[i][2]), fabsf(v[i][3])));
+        }
+        m[0] = quad_max(m[0]), m[1] = quad_max(m[1]);
+    };
+
+    if (threadIdx.x >= 2 * W * 32) {
+        const int tid = static_cast<int>(threadIdx.x) - (2 * W + C::kIdle) * 32;
+        if (tid < 0) return;
         auto load = [&](int c) {
             const uint32_t to = base + (c % kStages) * C::kStage;
             const int tc = t0 + c * kC, n = min(kC, t1 - tc);
@@ -526,15 +555,20 @@ __global__ void __launch_bounds__(W * 64) delta_walk_kernel(DeltaArgs a, const u
         asm volatile("cp.async.commit_group;" ::: "memory");
         for (int it = 0; it <= chunks; ++it) {
             asm volatile("cp.async.wait_group 1;" ::: "memory");
-            dr_meet<W * 64>();
+            dr_meet<C::kMeet>();
             if (it + 2 < chunks) load(it + 2);
             asm volatile("cp.async.commit_group;" ::: "memory");
-            if (it == 0) continue;
-            const int c = it - 1;
+        }
+        return;
+    }
+    if (role == 1) {
+        dr_meet<C::kMeet>();
+        for (int c = 0; c < chunks; ++c) {
+            dr_meet<C::kMeet>();
             const uint32_t st = base + (c % kStages) * C::kStage;
             const DrChunk* cd = reinterpret_cast<const DrChunk*>(smem + (c % kStages) * C::kStage + C::kD);
             const uint4* in = reinterpret_cast<const uint4*>(hand(c)) + lane;
-            const float4 f = *reinterpret_cast<const float4*>(hand(c) + C::kFAt + lane * 16);  // S^T's and U^T's factors
+            const float2 f = *reinterpret_cast<const float2*>(hand(c) + C::kFAt + lane * 8);
             float o[4][4] = {}, y[4][4] = {};
 #pragma unroll
             for (int k = 0; k < DK / 16; k += 2) {
@@ -553,11 +587,18 @@ __global__ void __launch_bounds__(W * 64) delta_walk_kernel(DeltaArgs a, const u
                     for (int i = 0; i < 4; ++i) dr_mma(o[i], p[h >> 1][h & 1], b[i][(h >> 1) * 2], b[i][(h >> 1) * 2 + 1]);
             }
             uint32_t hi[2][4], lo[2][4];
+            float u[4][4], u_inv[2];
+            {
+                float most[2];
 #pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const uint4 w = in[C::kUAt / 16 + 2 * k * 32], z = in[C::kUAt / 16 + (2 * k + 1) * 32];
-                hi[k][0] = w.x, hi[k][1] = w.y, hi[k][2] = w.z, hi[k][3] = w.w;
-                lo[k][0] = z.x, lo[k][1] = z.y, lo[k][2] = z.z, lo[k][3] = z.w;
+                for (int i = 0; i < 4; ++i) {
+                    const uint4 w = in[C::kUAt / 16 + i * 32];
+                    u[i][0] = __uint_as_float(w.x), u[i][1] = __uint_as_float(w.y), u[i][2] = __uint_as_float(w.z), u[i][3] = __uint_as_float(w.w);
+                }
+                row_max(u, most);
+                const float up[2] = {dr_scale(most[0]), dr_scale(most[1])};
+                parts(u, up, hi, lo);
+                u_inv[0] = dr_inv(up[0]), u_inv[1] = dr_inv(up[1]);
             }
             uint32_t ph[4][4], pl[4][4];
 #pragma unroll
@@ -580,8 +621,8 @@ __global__ void __launch_bounds__(W * 64) delta_walk_kernel(DeltaArgs a, const u
             for (int i = 0; i < 4; ++i) {
                 const float2 fq = *reinterpret_cast<const float2*>(&cd->q_out[8 * i + 2 * q4]);
                 const float2 fp = *reinterpret_cast<const float2*>(&cd->p_inv[8 * i + 2 * q4]);
-                const float r0 = o[i][0] * f.x * fq.x + y[i][0] * f.z * fp.x, r1 = o[i][1] * f.x * fq.y + y[i][1] * f.z * fp.y;
-                const float r2 = o[i][2] * f.y * fq.x + y[i][2] * f.w * fp.x, r3 = o[i][3] * f.y * fq.y + y[i][3] * f.w * fp.y;
+                const float r0 = o[i][0] * f.x * fq.x + y[i][0] * u_inv[0] * fp.x, r1 = o[i][1] * f.x * fq.y + y[i][1] * u_inv[0] * fp.y;
+                const float r2 = o[i][2] * f.y * fq.x + y[i][2] * u_inv[1] * fp.x, r3 = o[i][3] * f.y * fq.y + y[i][3] * u_inv[1] * fp.y;
                 // [column][token] -> [token][column]
                 const uint32_t w0 = dr_movm(dr_pack<DT>(r0, r1)), w1 = dr_movm(dr_pack<DT>(r2, r3));
                 if (8 * i + g < n) {
@@ -602,53 +643,57 @@ __global__ void __launch_bounds__(W * 64) delta_walk_kernel(DeltaArgs a, const u
 #pragma unroll
         for (int e = 0; e < 4; ++e) S[k][e] = sp[(long long)(8 * k + 2 * q4 + (e & 1)) * a.dv + (e >> 1) * 8];
     float unit[2] = {1.f, 1.f};  // the state's columns are S unit; powers of two
-    auto quad_max = [](float x) {
-        x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
-        return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
-    };
     for (int c = 0; c < chunks; ++c) {
-        // keep each column's largest within what two fp16 parts hold to 2^-22 of it
-        float most[2] = {0.f, 0.f};
-#pragma unroll
-        for (int k = 0; k < kNt; ++k) {
-            most[0] = fmaxf(most[0], fmaxf(fabsf(S[k][0]), fabsf(S[k][1])));
-            most[1] = fmaxf(most[1], fmaxf(fabsf(S[k][2]), fabsf(S[k][3])));
-        }
-        most[0] = quad_max(most[0]), most[1] = quad_max(most[1]);
-        float most_s[2] = {most[0], most[1]};
-        const bool out0 = most[0] != 0.f && !(most[0] >= 1.f && most[0] < 32768.f);
-        const bool out1 = most[1] != 0.f && !(most[1] >= 1.f && most[1] < 32768.f);
-        if (__any_sync(0xffffffffu, out0 || out1)) {
-            const float f0 = out0 ? fminf(dr_scale(most[0]), unit[0] * 0x1p100f) : 1.f, f1 = out1 ? fminf(dr_scale(most[1]), unit[1] * 0x1p100f) : 1.f;
-#pragma unroll
-            for (int k = 0; k < kNt; ++k) S[k][0] *= f0, S[k][1] *= f0, S[k][2] *= f1, S[k][3] *= f1;
-            unit[0] *= dr_inv(f0), unit[1] *= dr_inv(f1);
-            most_s[0] *= f0, most_s[1] *= f1;
-        }
-        dr_meet<W * 64>();
+        dr_meet<C::kMeet>();
         const uint32_t st = base + (c % kStages) * C::kStage;
         const DrChunk* cd = reinterpret_cast<const DrChunk*>(smem + (c % kStages) * C::kStage + C::kD);  // its factors
         uint4* give = reinterpret_cast<uint4*>(hand(c)) + lane;
-        float x[4][4] = {};
+        float x[4][4], most[2];
+        for (int pass = 0;; ++pass) {
 #pragma unroll
-        for (int k = 0; k < DK / 16; k += 2) {
-            uint32_t hi[2][4], lo[2][4], b[4][4];
+            for (int i = 0; i < 4; ++i) x[i][0] = x[i][1] = x[i][2] = x[i][3] = 0.f;
+            __half2 big[2] = {__half2{}, __half2{}};
 #pragma unroll
-            for (int i = 0; i < 4; ++i) dr_ldsm4(b[i], st + dr_at<kRow>(8 * i + (lane & 7), 2 * k + (lane >> 3)));
+            for (int k = 0; k < DK / 16; k += 2) {
+                uint32_t hi[2][4], lo[2][4], b[4][4];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
+                for (int i = 0; i < 4; ++i) dr_ldsm4(b[i], st + dr_at<kRow>(8 * i + (lane & 7), 2 * k + (lane >> 3)));
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float* v = S[2 * (k + h) + (e >> 1)] + (e & 1) * 2;
-                    dr_split2(dr_pair(v[0], v[1]), hi[h][e], lo[h][e]);
+                for (int h = 0; h < 2; ++h) {
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float* v = S[2 * (k + h) + (e >> 1)] + (e & 1) * 2;
+                        dr_split2(dr_pair(v[0], v[1]), hi[h][e], lo[h][e]);
+                        big[e & 1] = __hmax2(big[e & 1], __habs2(*reinterpret_cast<const __half2*>(&hi[h][e])));
+                    }
+                    give[(2 * (k + h)) * 32] = make_uint4(hi[h][0], hi[h][1], hi[h][2], hi[h][3]);
+                    give[(2 * (k + h) + 1) * 32] = make_uint4(lo[h][0], lo[h][1], lo[h][2], lo[h][3]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) dr_mma(x[i], hi[h], b[i][2 * h], b[i][2 * h + 1]);
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) dr_mma(x[i], lo[h], b[i][2 * h], b[i][2 * h + 1]);
                 }
-                give[(2 * (k + h)) * 32] = make_uint4(hi[h][0], hi[h][1], hi[h][2], hi[h][3]);
-                give[(2 * (k + h) + 1) * 32] = make_uint4(lo[h][0], lo[h][1], lo[h][2], lo[h][3]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) dr_mma(x[i], hi[h], b[i][2 * h], b[i][2 * h + 1]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) dr_mma(x[i], lo[h], b[i][2 * h], b[i][2 * h + 1]);
             }
+            // each column's largest has to lie in 1..2^15, where two fp16 parts hold every value to 2^-22 of it (and
+            // nothing overflows); else the column changes its unit, and again
+            most[0] = quad_max(fmaxf(__low2float(big[0]), __high2float(big[0])));
+            most[1] = quad_max(fmaxf(__low2float(big[1]), __high2float(big[1])));
+            const bool out0 = !(most[0] >= 1.f && most[0] < 32768.f), out1 = !(most[1] >= 1.f && most[1] < 32768.f);
+            if (pass == 1 || !__any_sync(0xffffffffu, out0 || out1)) break;
+            float all[2] = {0.f, 0.f};
+#pragma unroll
+            for (int k = 0; k < kNt; ++k) {
+                all[0] = fmaxf(all[0], fmaxf(fabsf(S[k][0]), fabsf(S[k][1])));
+                all[1] = fmaxf(all[1], fmaxf(fabsf(S[k][2]), fabsf(S[k][3])));
+            }
+            all[0] = quad_max(all[0]), all[1] = quad_max(all[1]);
+            const float f0 = all[0] == 0.f ? 1.f : fminf(dr_scale(all[0]), unit[0] * 0x1p100f);
+            const float f1 = all[1] == 0.f ? 1.f : fminf(dr_scale(all[1]), unit[1] * 0x1p100f);
+            // columns of zeros, and those at the end of the units' range, stay
+            if (!__any_sync(0xffffffffu, (out0 && f0 != 1.f) || (out1 && f1 != 1.f))) break;
+#pragma unroll
+            for (int k = 0; k < kNt; ++k) S[k][0] *= f0, S[k][1] *= f0, S[k][2] *= f1, S[k][3] *= f1;
+            unit[0] *= dr_inv(f0), unit[1] *= dr_inv(f1);
         }
         // V - diag(e^G) K S0, transposed, and its two parts
         {
@@ -666,32 +711,15 @@ __global__ void __launch_bounds__(W * 64) delta_walk_kernel(DeltaArgs a, const u
                 x[i][2] = y1.x - f.x * (x[i][2] * unit[1]), x[i][3] = y1.y - f.y * (x[i][3] * unit[1]);
             }
         }
-        auto parts = [&](const float(&v)[4][4], const float(&up)[2], uint32_t(&hi)[2][4], uint32_t(&lo)[2][4]) {
-#pragma unroll
-            for (int k = 0; k < 2; ++k)
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float* w = v[2 * k + (e >> 1)] + (e & 1) * 2;
-                    dr_split2(dr_mul2(dr_pair(w[0], w[1]), up[e & 1]), hi[k][e], lo[k][e]);
-                }
-        };
-        auto row_max = [&](const float(&v)[4][4], float(&m)[2]) {
-            m[0] = m[1] = 0.f;
-#pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                m[0] = fmaxf(m[0], fmaxf(fabsf(v[i][0]), fabsf(v[i][1])));
-                m[1] = fmaxf(m[1], fmaxf(fabsf(v[i][2]), fabsf(v[i][3])));
-            }
-            m[0] = quad_max(m[0]), m[1] = quad_max(m[1]);
-        };
         uint32_t hi[2][4], lo[2][4], th[4][4], tl[4][4];
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             dr_ldsm4(th[i], st + C::kD + dr_at<64>(8 * i + (lane & 7), lane >> 3));
             dr_ldsm4(tl[i], st + C::kD + kC * 64 + dr_at<64>(8 * i + (lane & 7), lane >> 3));
         }
-        row_max(x, most);
-        float up[2] = {dr_scale(most[0]), dr_scale(most[1])};
+        float more[2];
+        row_max(x, more);
+        float up[2] = {dr_scale(more[0]), dr_scale(more[1])};
         parts(x, up, hi, lo);
         float u[4][4] = {};
 #pragma unroll
@@ -720,16 +748,18 @@ __global__ void __launch_bounds__(W * 64) delta_walk_kernel(DeltaArgs a, const u
                 const float2 f = *reinterpret_cast<const float2*>(&cd->rest[8 * i + 2 * q4]);
                 w[i][0] = u[i][0] * f.x, w[i][1] = u[i][1] * f.y, w[i][2] = u[i][2] * f.x, w[i][3] = u[i][3] * f.y;
             }
-            float more[2];
             row_max(w, more);
             const float decay = cd->decay[0];
-            const float s_inv[2] = {unit[0], unit[1]};
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+                give[C::kUAt / 16 + i * 32] = make_uint4(__float_as_uint(u[i][0]), __float_as_uint(u[i][1]), __float_as_uint(u[i][2]), __float_as_uint(u[i][3]));
+            *reinterpret_cast<float2*>(hand(c) + C::kFAt + lane * 8) = make_float2(unit[0], unit[1]);
             float keep[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-                // in the state's own unit, while what is left of it or what is added keeps to that window
-                const float r = fmaxf(decay * most_s[h], more[h] * dr_inv(unit[h]));
-                const float f = r == 0.f || (r >= 1.f && r < 32768.f) ? 1.f : fminf(dr_scale(r), unit[h] * 0x1p100f);
+                // in the state's own unit, while what is left of it or what is added stays well inside that window
+                const float r = fmaxf(decay * most[h], more[h] * dr_inv(unit[h]));
+                const float f = r == 0.f || (r >= 4.f && r < 2048.f) ? 1.f : fminf(dr_scale(r) * 0x1p-5f, unit[h] * 0x1p100f);
                 keep[h] = decay * f;
                 unit[h] *= dr_inv(f);
                 up[h] = dr_inv(unit[h]);
@@ -741,7 +771,8 @@ __global__ void __launch_bounds__(W * 64) delta_walk_kernel(DeltaArgs a, const u
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
                     dr_ldsm4t(b[i], st + dr_at<kRow>(lane, k + i));
-                    S[k + i][0] *= keep[0], S[k + i][1] *= keep[0], S[k + i][2] *= keep[1], S[k + i][3] *= keep[1];
+                    dr_unpair(dr_mul2(dr_pair(S[k + i][0], S[k + i][1]), keep[0]), S[k + i][0], S[k + i][1]);
+                    dr_unpair(dr_mul2(dr_pair(S[k + i][2], S[k + i][3]), keep[1]), S[k + i][2], S[k + i][3]);
                 }
 #pragma unroll
                 for (int i = 0; i < 4; ++i) dr_mma(S[k + i], hi[0], b[i][0], b[i][1]);
@@ -752,19 +783,9 @@ __global__ void __launch_bounds__(W * 64) delta_walk_kernel(DeltaArgs a, const u
 #pragma unroll
                 for (int i = 0; i < 4; ++i) dr_mma(S[k + i], lo[1], b[i][2], b[i][3]);
             }
-            // U^T for the outputs
-            row_max(u, most);
-            up[0] = dr_scale(most[0]), up[1] = dr_scale(most[1]);
-            parts(u, up, hi, lo);
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                give[C::kUAt / 16 + 2 * k * 32] = make_uint4(hi[k][0], hi[k][1], hi[k][2], hi[k][3]);
-                give[C::kUAt / 16 + (2 * k + 1) * 32] = make_uint4(lo[k][0], lo[k][1], lo[k][2], lo[k][3]);
-            }
-            *reinterpret_cast<float4*>(hand(c) + C::kFAt + lane * 16) = make_float4(s_inv[0], s_inv[1], dr_inv(up[0]), dr_inv(up[1]));
         }
     }
-    dr_meet<W * 64>();  // the last chunk's hand-over
+    dr_meet<C::kMeet>();  // the last chunk's hand-over
 #pragma unroll
     for (int k = 0; k < kNt; ++k)
 #pragma unroll
@@ -806,7 +827,7 @@ cudaError_t launch_walk(const DeltaArgs& a, const uint16_t* kf, const uint16_t* 
     cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, smem);
     if (e != cudaSuccess) return e;
     void* args[] = {const_cast<DeltaArgs*>(&a), &kf, &qf, &data};
-    return launch_kernel(f, dim3(a.dv / (16 * W), a.Hv, a.n), dim3(W * 64), smem, true, s, args);
+    return launch_kernel(f, dim3(a.dv / (16 * W), a.Hv, a.n), dim3(DrWalk<DK, W>::kThreads), smem, true, s, args);
 }
 
 template <int DT, int DK>

@@ -215,13 +215,15 @@ __host__ __device__ inline long long dr_slots(int T, int n) { return T / kC + st
 // cores, then a warp a value head. L and P go row by lane, so that a row's
 // largest value and its 16-byte stores are a lane's own; the solve for T goes
 // column by lane, its rows of L broadcast from shared memory. Bound: latency of
-// that chain of some 1600 instructions a head, hidden by six CTAs a
+// that chain of some 1600 instructions a head, hidden by eight CTAs a
 // multiprocessor.
 template <int DT, int DK>
-__global__ void __launch_bounds__(64) delta_prepare_kernel(DeltaArgs a, uint16_t* kf, uint16_t* qf, DrChunk* out) {
+__global__ void __launch_bounds__(64, 8) delta_prepare_kernel(DeltaArgs a, uint16_t* kf, uint16_t* qf, DrChunk* out) {
     constexpr int kRow = DK * 2, kVec = DK / 16;  // 16-byte pieces of half a row
-    __shared__ __align__(128) unsigned char ks[kC * kRow], qs[kC * kRow];
-    __shared__ float dots[2][kC][kC + 1];  // k_i . k_j and q_i . k_j
+    constexpr int kDots = 2 * kC * (kC + 1) * 4;
+    __shared__ __align__(128) unsigned char kq[2 * kC * kRow > kDots ? 2 * kC * kRow : kDots];  // keys, queries; then their products
+    unsigned char *ks = kq, *qs = kq + kC * kRow;
+    auto dots = reinterpret_cast<float(*)[kC][kC + 1]>(kq);  // k_i . k_j and q_i . k_j
     __shared__ float inv[2][kC];           // 1 / |k|, 1 / |q| (with the rows' powers of two)
     __shared__ float4 col[2][kC];          // by warp, of token j: its sum of decays (two parts), 1 / |k_j|
     __shared__ __align__(16) float Ls[2][kC][kC + 4];
@@ -315,6 +317,7 @@ __global__ void __launch_bounds__(64) delta_prepare_kernel(DeltaArgs a, uint16_t
                     for (int i = 0; i < 4; ++i) dr_mma(c[m][i], f, b[i][2 * h], b[i][2 * h + 1]);
                 }
         }
+        __syncthreads();
 #pragma unroll
         for (int m = 0; m < 2; ++m)
 #pragma unroll
@@ -450,12 +453,14 @@ __device__ __forceinline__ unsigned long long dr_mul2(unsigned long long x, floa
 // result is the next one's left operand, register for register: S^T K^T, then
 // (V - ...)^T T^T, then U^T K. Nothing of that chain passes through shared
 // memory. It hands the operand S^T and U^T to an output warp, which makes
-// S^T Q^T + U^T P^T one chunk later; a loading warp fetches the next chunks
-// (cp.async); all warps meet once a chunk. The chain bounds a long sequence: one
-// warp doing all of it took 2.8 us a chunk (128 x 128 states), mostly waiting
-// for its own last instruction.
+// S^T Q^T + U^T P^T one chunk later; cp.async fetches the next chunks; all warps
+// meet once a chunk. The chain bounds a long sequence: at 128 x 128 states a
+// chunk takes 1.24 us, 146 tensor instructions of 8 cycles and what lies between
+// them. (2.8 us in one warp that did all of it; 1.4 with the key dimensions
+// halved between two warps, which then meet once more; 2.2 with 8 columns a
+// warp as the right operand, which a transpose within the warp has to make.)
 template <int kThreads>
-__device__ __forceinline__ void dr_meet() {  // state and output warps, each from its own loop
+__device__ __forceinline__ void dr_meet() {  // all warps, each from its own loop
     asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");
 }
 template <int DK, int W>
@@ -464,8 +469,10 @@ struct DrWalk {
     static constexpr int kQ = kC * kRow, kV = 2 * kC * kRow, kD = kV + kC * kVRow;
     static constexpr int kStage = kD + static_cast<int>(sizeof(DrChunk));
     static constexpr int kStages = 4;
-    // with two warps of each kind, loading ones share a scheduler with output ones: two warps before them leave at once
-    static constexpr int kIdle = W == 2 ? 2 : 0, kThreads = (3 * W + kIdle) * 32, kMeet = 3 * W * 32;
+    // two warps of each kind: the loading ones share a scheduler with output ones, as two warps before them leave at
+    // once. Four state and four output warps: the output warps load (more warps would take registers from all).
+    static constexpr int kIdle = W == 2 ? 2 : 0, kLoad = W == 2 ? 2 : 0;
+    static constexpr int kThreads = (2 * W + kIdle + kLoad) * 32, kMeet = (2 * W + kLoad) * 32;
     // handed over: S^T, two parts in operand registers; U^T in f32; the columns' factors of S
     static constexpr int kUAt = DK / 16 * 2 * 512, kFAt = kUAt + 4 * 512, kHand = kFAt + 256;
     static constexpr int kHands = kStages * kStage;
@@ -474,12 +481,12 @@ struct DrWalk {
 template <int DT, int DK, int W>
 __global__ void __launch_bounds__(DrWalk<DK, W>::kThreads) delta_walk_kernel(DeltaArgs a, const uint16_t* kf, const uint16_t* qf, const DrChunk* data) {
     using C = DrWalk<DK, W>;
-    constexpr int kRow = C::kRow, kVRow = C::kVRow, kNt = DK / 8, kLoaders = W * 32, kStages = C::kStages;
+    constexpr int kRow = C::kRow, kVRow = C::kVRow, kNt = DK / 8, kStages = C::kStages;
+    constexpr int kLoaders = (C::kLoad ? C::kLoad : W) * 32;
     extern __shared__ __align__(1024) unsigned char smem[];
     pdl_wait();
     pdl_trigger();
-    const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) % W, g = lane >> 2, q4 = lane & 3;
-    const int role = threadIdx.x / (W * 32);  // 0: state, 1: output
+    const int lane = threadIdx.x & 31, wid = threadIdx.x >> 5, warp = wid % W, g = lane >> 2, q4 = lane & 3;
     const int hv = blockIdx.y, seq = blockIdx.z, hk = hv / (a.Hv / a.Hk), c0 = blockIdx.x * (16 * W);
     int t0, t1;
     dr_tokens(a, seq, t0, t1);
@@ -488,7 +495,6 @@ __global__ void __launch_bounds__(DrWalk<DK, W>::kThreads) delta_walk_kernel(Del
     data += (t0 / kC + static_cast<long long>(seq)) * a.Hv + hv;
     const uint32_t base = static_cast<uint32_t>(__cvta_generic_to_shared(smem));
     auto hand = [&](int c) { return smem + C::kHands + ((c & 1) * W + warp) * C::kHand; };
-
     auto quad_max = [](float x) {
         x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 1));
         return fmaxf(x, __shfl_xor_sync(0xffffffffu, x, 2));
@@ -512,59 +518,74 @@ __global__ void __launch_bounds__(DrWalk<DK, W>::kThreads) delta_walk_kernel(Del
         m[0] = quad_max(m[0]), m[1] = quad_max(m[1]);
     };
 
-    if (threadIdx.x >= 2 * W * 32) {
-        const int tid = static_cast<int>(threadIdx.x) - (2 * W + C::kIdle) * 32;
-        if (tid < 0) return;
-        auto load = [&](int c) {
-            const uint32_t to = base + (c % kStages) * C::kStage;
-            const int tc = t0 + c * kC, n = min(kC, t1 - tc);
-            constexpr int kKc = DK / 8, kVc = W * 2, kStep = kLoaders / kKc;
-            {
-                const int r0 = tid / kKc, ch = tid % kKc;
-                const long long off = ((long long)tc * a.Hk + hk) * DK + ch * 8, step = (long long)a.Hk * DK;
+    // ---- loading
+    const int tid = static_cast<int>(threadIdx.x) - (C::kLoad ? 2 * W + C::kIdle : W) * 32;  // of the loading threads
+    auto load = [&](int c) {
+        const uint32_t to = base + (c % kStages) * C::kStage;
+        const int tc = t0 + c * kC, n = min(kC, t1 - tc);
+        constexpr int kKc = DK / 8, kVc = W * 2, kStep = kLoaders / kKc, kVStep = kLoaders / kVc;
+        {
+            const int r0 = tid / kKc, ch = tid % kKc;
+            const long long off = ((long long)tc * a.Hk + hk) * DK + ch * 8, step = (long long)a.Hk * DK;
 #pragma unroll
-                for (int m = 0; m < kC / kStep; ++m) {
-                    const int r = r0 + m * kStep;
-                    const long long at = off + (r < n ? r : 0) * step;
-                    dr_cp16(to + dr_at<kRow>(r, ch), kf + at, r < n);
-                    dr_cp16(to + C::kQ + dr_at<kRow>(r, ch), qf + at, r < n);
-                }
+            for (int m = 0; m < kC / kStep; ++m) {
+                const int r = r0 + m * kStep;
+                const long long at = off + (r < n ? r : 0) * step;
+                dr_cp16(to + dr_at<kRow>(r, ch), kf + at, r < n);
+                dr_cp16(to + C::kQ + dr_at<kRow>(r, ch), qf + at, r < n);
             }
-            {
-                const int r0 = tid / kVc, ch = tid % kVc;
-                constexpr int kVStep = kLoaders / kVc;
-                const uint16_t* v = static_cast<const uint16_t*>(a.v) + ((long long)tc * a.Hv + hv) * a.dv + c0 + ch * 8;
+        }
+        {
+            const int r0 = tid / kVc, ch = tid % kVc;
+            const uint16_t* v = static_cast<const uint16_t*>(a.v) + ((long long)tc * a.Hv + hv) * a.dv + c0 + ch * 8;
 #pragma unroll
-                for (int m = 0; m < kC / kVStep; ++m) {
-                    const int r = r0 + m * kVStep;
-                    dr_cp16(to + C::kV + dr_at<kVRow>(r, ch), v + (long long)(r < n ? r : 0) * a.Hv * a.dv, r < n);
-                }
+            for (int m = 0; m < kC / kVStep; ++m) {
+                const int r = r0 + m * kVStep;
+                dr_cp16(to + C::kV + dr_at<kVRow>(r, ch), v + (long long)(r < n ? r : 0) * a.Hv * a.dv, r < n);
             }
-            const char* d = reinterpret_cast<const char*>(data + (long long)c * a.Hv) + tid * 16;
+        }
+        const char* d = reinterpret_cast<const char*>(data + (long long)c * a.Hv) + tid * 16;
 #pragma unroll
-            for (int m = 0; m < 4 * kC * 4 / kLoaders; ++m) {  // four matrices of 32 rows of 64 bytes
-                const int i = tid + m * kLoaders;
-                dr_cp16(to + C::kD + (i >> 7) * (kC * 64) + dr_at<64>((i >> 2) & 31, i & 3), d + m * kLoaders * 16, true);
-            }
-            if (tid < static_cast<int>(sizeof(DrChunk)) / 16 - 4 * kC * 4) dr_cp16(to + C::kD + 4 * kC * 64 + tid * 16, d + 4 * kC * 64, true);
-        };
-        static_assert(static_cast<int>(sizeof(DrChunk)) / 16 - 4 * kC * 4 <= kLoaders, "the factors in one go");
+        for (int m = 0; m < 4 * kC * 4 / kLoaders; ++m) {  // four matrices of 32 rows of 64 bytes
+            const int i = tid + m * kLoaders;
+            dr_cp16(to + C::kD + (i >> 7) * (kC * 64) + dr_at<64>((i >> 2) & 31, i & 3), d + m * kLoaders * 16, true);
+        }
+        if (tid < static_cast<int>(sizeof(DrChunk)) / 16 - 4 * kC * 4) dr_cp16(to + C::kD + 4 * kC * 64 + tid * 16, d + 4 * kC * 64, true);
+    };
+    static_assert(static_cast<int>(sizeof(DrChunk)) / 16 - 4 * kC * 4 <= kLoaders, "the factors in one go");
+    auto start = [&]() {
         load(0);
         asm volatile("cp.async.commit_group;" ::: "memory");
         if (chunks > 1) load(1);
         asm volatile("cp.async.commit_group;" ::: "memory");
-        for (int it = 0; it <= chunks; ++it) {
-            asm volatile("cp.async.wait_group 1;" ::: "memory");
-            dr_meet<C::kMeet>();
-            if (it + 2 < chunks) load(it + 2);
-            asm volatile("cp.async.commit_group;" ::: "memory");
-        }
+    };
+    // chunk `it` is there; the one after the next is on its way
+    auto turn = [&](int it) {
+        asm volatile("cp.async.wait_group 1;" ::: "memory");
+        dr_meet<C::kMeet>();
+        if (it + 2 < chunks) load(it + 2);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
+    if (C::kLoad && wid >= 2 * W) {
+        if (tid < 0) return;
+        start();
+        for (int it = 0; it <= chunks; ++it) turn(it);
         return;
     }
-    if (role == 1) {
-        dr_meet<C::kMeet>();
-        for (int c = 0; c < chunks; ++c) {
+
+    // ---- outputs, one chunk behind
+    if (wid >= W) {
+        if (!C::kLoad) {
+            start();
+            turn(0);
+        } else {
             dr_meet<C::kMeet>();
+        }
+        for (int c = 0; c < chunks; ++c) {
+            if (!C::kLoad)
+                turn(c + 1);
+            else
+                dr_meet<C::kMeet>();
             const uint32_t st = base + (c % kStages) * C::kStage;
             const DrChunk* cd = reinterpret_cast<const DrChunk*>(smem + (c % kStages) * C::kStage + C::kD);
             const uint4* in = reinterpret_cast<const uint4*>(hand(c)) + lane;
@@ -635,6 +656,7 @@ __global__ void __launch_bounds__(DrWalk<DK, W>::kThreads) delta_walk_kernel(Del
         return;
     }
 
+    // ---- the state
     // element e of tile k: column c0 + 16 warp + g + 8 (e / 2), key dimension 8 k + 2 q4 + e % 2
     float S[kNt][4];
     float* sp = a.state + ((long long)seq * a.Hv + hv) * DK * a.dv + c0 + warp * 16 + g;
@@ -648,10 +670,23 @@ __global__ void __launch_bounds__(DrWalk<DK, W>::kThreads) delta_walk_kernel(Del
         const uint32_t st = base + (c % kStages) * C::kStage;
         const DrChunk* cd = reinterpret_cast<const DrChunk*>(smem + (c % kStages) * C::kStage + C::kD);  // its factors
         uint4* give = reinterpret_cast<uint4*>(hand(c)) + lane;
+        // what the next steps need, on its way while the tensor cores work
+        uint32_t v0[4], v1[4];
+        float2 fall[4], rest[4], t_inv[4];
+        dr_ldsm4t(v0, st + C::kV + dr_at<kVRow>(lane, 2 * warp));
+        dr_ldsm4t(v1, st + C::kV + dr_at<kVRow>(lane, 2 * warp + 1));
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            fall[i] = *reinterpret_cast<const float2*>(&cd->fall[8 * i + 2 * q4]);
+            rest[i] = *reinterpret_cast<const float2*>(&cd->rest[8 * i + 2 * q4]);
+            t_inv[i] = *reinterpret_cast<const float2*>(&cd->t_inv[8 * i + 2 * q4]);
+        }
+        const float decay = cd->decay[0];
         float x[4][4], most[2];
         for (int pass = 0;; ++pass) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) x[i][0] = x[i][1] = x[i][2] = x[i][3] = 0.f;
+            float xl[4][4] = {};
             __half2 big[2] = {__half2{}, __half2{}};
 #pragma unroll
             for (int k = 0; k < DK / 16; k += 2) {
@@ -666,18 +701,22 @@ __global__ void __launch_bounds__(DrWalk<DK, W>::kThreads) delta_walk_kernel(Del
                         dr_split2(dr_pair(v[0], v[1]), hi[h][e], lo[h][e]);
                         big[e & 1] = __hmax2(big[e & 1], __habs2(*reinterpret_cast<const __half2*>(&hi[h][e])));
                     }
-                    give[(2 * (k + h)) * 32] = make_uint4(hi[h][0], hi[h][1], hi[h][2], hi[h][3]);
+                    give[2 * (k + h) * 32] = make_uint4(hi[h][0], hi[h][1], hi[h][2], hi[h][3]);
                     give[(2 * (k + h) + 1) * 32] = make_uint4(lo[h][0], lo[h][1], lo[h][2], lo[h][3]);
 #pragma unroll
                     for (int i = 0; i < 4; ++i) dr_mma(x[i], hi[h], b[i][2 * h], b[i][2 * h + 1]);
 #pragma unroll
-                    for (int i = 0; i < 4; ++i) dr_mma(x[i], lo[h], b[i][2 * h], b[i][2 * h + 1]);
+                    for (int i = 0; i < 4; ++i) dr_mma(xl[i], lo[h], b[i][2 * h], b[i][2 * h + 1]);
                 }
             }
-            // each column's largest has to lie in 1..2^15, where two fp16 parts hold every value to 2^-22 of it (and
-            // nothing overflows); else the column changes its unit, and again
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) x[i][e] += xl[i][e];
             most[0] = quad_max(fmaxf(__low2float(big[0]), __high2float(big[0])));
             most[1] = quad_max(fmaxf(__low2float(big[1]), __high2float(big[1])));
+            // each column's largest has to lie in 1..2^15, where two fp16 parts hold every value to 2^-22 of it (and
+            // nothing overflows); else the column changes its unit, once, and it is done again
             const bool out0 = !(most[0] >= 1.f && most[0] < 32768.f), out1 = !(most[1] >= 1.f && most[1] < 32768.f);
             if (pass == 1 || !__any_sync(0xffffffffu, out0 || out1)) break;
             float all[2] = {0.f, 0.f};
@@ -696,20 +735,15 @@ __global__ void __launch_bounds__(DrWalk<DK, W>::kThreads) delta_walk_kernel(Del
             unit[0] *= dr_inv(f0), unit[1] *= dr_inv(f1);
         }
         // V - diag(e^G) K S0, transposed, and its two parts
-        {
-            uint32_t v0[4], v1[4];
-            dr_ldsm4t(v0, st + C::kV + dr_at<kVRow>(lane, 2 * warp));
-            dr_ldsm4t(v1, st + C::kV + dr_at<kVRow>(lane, 2 * warp + 1));
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 f = *reinterpret_cast<const float2*>(&cd->fall[8 * i + 2 * q4]);
-                const float2 y0 = DT == 1 ? __half22float2(*reinterpret_cast<const __half2*>(&v0[i]))
-                                          : make_float2(__uint_as_float(v0[i] << 16), __uint_as_float(v0[i] & 0xFFFF0000u));
-                const float2 y1 = DT == 1 ? __half22float2(*reinterpret_cast<const __half2*>(&v1[i]))
-                                          : make_float2(__uint_as_float(v1[i] << 16), __uint_as_float(v1[i] & 0xFFFF0000u));
-                x[i][0] = y0.x - f.x * (x[i][0] * unit[0]), x[i][1] = y0.y - f.y * (x[i][1] * unit[0]);
-                x[i][2] = y1.x - f.x * (x[i][2] * unit[1]), x[i][3] = y1.y - f.y * (x[i][3] * unit[1]);
-            }
+        for (int i = 0; i < 4; ++i) {
+            const float2 f = fall[i];
+            const float2 y0 = DT == 1 ? __half22float2(*reinterpret_cast<const __half2*>(&v0[i]))
+                                      : make_float2(__uint_as_float(v0[i] << 16), __uint_as_float(v0[i] & 0xFFFF0000u));
+            const float2 y1 = DT == 1 ? __half22float2(*reinterpret_cast<const __half2*>(&v1[i]))
+                                      : make_float2(__uint_as_float(v1[i] << 16), __uint_as_float(v1[i] & 0xFFFF0000u));
+            x[i][0] = y0.x - f.x * (x[i][0] * unit[0]), x[i][1] = y0.y - f.y * (x[i][1] * unit[0]);
+            x[i][2] = y1.x - f.x * (x[i][2] * unit[1]), x[i][3] = y1.y - f.y * (x[i][3] * unit[1]);
         }
         uint32_t hi[2][4], lo[2][4], th[4][4], tl[4][4];
 #pragma unroll
@@ -731,58 +765,51 @@ __global__ void __launch_bounds__(DrWalk<DK, W>::kThreads) delta_walk_kernel(Del
 #pragma unroll
             for (int i = 2 * k; i < 4; ++i) dr_mma(u[i], hi[k], tl[i][2 * k], tl[i][2 * k + 1]);
         }
+        float w[4][4];
         {
             const float v_inv[2] = {dr_inv(up[0]), dr_inv(up[1])};
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
-                const float2 f = *reinterpret_cast<const float2*>(&cd->t_inv[8 * i + 2 * q4]);
+                const float2 f = t_inv[i], r = rest[i];
                 u[i][0] *= f.x * v_inv[0], u[i][1] *= f.y * v_inv[0];
                 u[i][2] *= f.x * v_inv[1], u[i][3] *= f.y * v_inv[1];
+                w[i][0] = u[i][0] * r.x, w[i][1] = u[i][1] * r.y, w[i][2] = u[i][2] * r.x, w[i][3] = u[i][3] * r.y;
             }
         }
         // the state after the chunk
-        {
-            float w[4][4];
+        row_max(w, more);
 #pragma unroll
-            for (int i = 0; i < 4; ++i) {
-                const float2 f = *reinterpret_cast<const float2*>(&cd->rest[8 * i + 2 * q4]);
-                w[i][0] = u[i][0] * f.x, w[i][1] = u[i][1] * f.y, w[i][2] = u[i][2] * f.x, w[i][3] = u[i][3] * f.y;
+        for (int i = 0; i < 4; ++i)
+            give[C::kUAt / 16 + i * 32] = make_uint4(__float_as_uint(u[i][0]), __float_as_uint(u[i][1]), __float_as_uint(u[i][2]), __float_as_uint(u[i][3]));
+        *reinterpret_cast<float2*>(hand(c) + C::kFAt + lane * 8) = make_float2(unit[0], unit[1]);
+        float keep[2];
+#pragma unroll
+        for (int h = 0; h < 2; ++h) {
+            // in the state's own unit, while what is left of it or what is added stays well inside that window
+            const float r = fmaxf(decay * most[h], more[h] * dr_inv(unit[h]));
+            const float f = r == 0.f || (r >= 4.f && r < 2048.f) ? 1.f : fminf(dr_scale(r) * 0x1p-5f, unit[h] * 0x1p100f);
+            keep[h] = decay * f;
+            unit[h] *= dr_inv(f);
+            up[h] = dr_inv(unit[h]);
+        }
+        parts(w, up, hi, lo);
+#pragma unroll
+        for (int k = 0; k < kNt; k += 8) {
+            uint32_t b[8][4];
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                dr_ldsm4t(b[i], st + dr_at<kRow>(lane, k + i));
+                dr_unpair(dr_mul2(dr_pair(S[k + i][0], S[k + i][1]), keep[0]), S[k + i][0], S[k + i][1]);
+                dr_unpair(dr_mul2(dr_pair(S[k + i][2], S[k + i][3]), keep[1]), S[k + i][2], S[k + i][3]);
             }
-            row_max(w, more);
-            const float decay = cd->decay[0];
 #pragma unroll
-            for (int i = 0; i < 4; ++i)
-                give[C::kUAt / 16 + i * 32] = make_uint4(__float_as_uint(u[i][0]), __float_as_uint(u[i][1]), __float_as_uint(u[i][2]), __float_as_uint(u[i][3]));
-            *reinterpret_cast<float2*>(hand(c) + C::kFAt + lane * 8) = make_float2(unit[0], unit[1]);
-            float keep[2];
+            for (int i = 0; i < 8; ++i) dr_mma(S[k + i], hi[0], b[i][0], b[i][1]);
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                // in the state's own unit, while what is left of it or what is added stays well inside that window
-                const float r = fmaxf(decay * most[h], more[h] * dr_inv(unit[h]));
-                const float f = r == 0.f || (r >= 4.f && r < 2048.f) ? 1.f : fminf(dr_scale(r) * 0x1p-5f, unit[h] * 0x1p100f);
-                keep[h] = decay * f;
-                unit[h] *= dr_inv(f);
-                up[h] = dr_inv(unit[h]);
-            }
-            parts(w, up, hi, lo);
+            for (int i = 0; i < 8; ++i) dr_mma(S[k + i], hi[1], b[i][2], b[i][3]);
 #pragma unroll
-            for (int k = 0; k < kNt; k += 4) {
-                uint32_t b[4][4];
+            for (int i = 0; i < 8; ++i) dr_mma(S[k + i], lo[0], b[i][0], b[i][1]);
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                    dr_ldsm4t(b[i], st + dr_at<kRow>(lane, k + i));
-                    dr_unpair(dr_mul2(dr_pair(S[k + i][0], S[k + i][1]), keep[0]), S[k + i][0], S[k + i][1]);
-                    dr_unpair(dr_mul2(dr_pair(S[k + i][2], S[k + i][3]), keep[1]), S[k + i][2], S[k + i][3]);
-                }
-#pragma unroll
-                for (int i = 0; i < 4; ++i) dr_mma(S[k + i], hi[0], b[i][0], b[i][1]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) dr_mma(S[k + i], hi[1], b[i][2], b[i][3]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) dr_mma(S[k + i], lo[0], b[i][0], b[i][1]);
-#pragma unroll
-                for (int i = 0; i < 4; ++i) dr_mma(S[k + i], lo[1], b[i][2], b[i][3]);
-            }
+            for (int i = 0; i < 8; ++i) dr_mma(S[k + i], lo[1], b[i][2], b[i][3]);
         }
     }
     dr_meet<C::kMeet>();  // the last chunk's hand-over

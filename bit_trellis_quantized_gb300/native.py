@@ -8,6 +8,7 @@ not an sm_103 GPU, calls raise.
 from __future__ import annotations
 
 import ctypes
+import functools
 import os
 
 import numpy as np
@@ -517,9 +518,9 @@ class _On:
 
     __slots__ = ("index", "device", "stream")
 
-    def __init__(self, t: torch.Tensor, stream=None):
-        self.index = t.get_device()
-        self.device = None if self.index == torch.cuda.current_device() else torch.cuda.device(self.index)
+    def __init__(self, index: int, stream=None):
+        self.index = index
+        self.device = None if index == torch._C._cuda_getDevice() else torch.cuda.device(index)
         self.stream = torch.cuda.stream(stream) if stream is not None else None
 
     def __enter__(self):
@@ -547,12 +548,20 @@ def _need(name: str, t, shape, dtype, index: int):
     raise ValueError(f"{name} has shape {tuple(t.shape)}, not {tuple(shape)}")
 
 
-def _scratch(ws, nbytes: int, device):
+def _scratch(ws, nbytes: int, index: int):
+    """(pointer, bytes, tensor to keep) of a workspace: the given one, or a new one of ``nbytes``."""
     if ws is None:
-        return torch.empty(max(nbytes, 16), dtype=torch.uint8, device=device)
-    if ws.device != device or not ws.is_contiguous() or ws.dtype is not torch.uint8:
-        raise ValueError(f"ws must be a contiguous uint8 tensor on {device}")
-    return ws
+        if nbytes == 0:
+            return None, 0, None
+        ws = torch.empty(nbytes, dtype=torch.uint8, device=index)
+    elif ws.get_device() != index or not ws.is_contiguous() or ws.dtype is not torch.uint8:
+        raise ValueError("ws must be a contiguous uint8 CUDA tensor on the inputs' device")
+    return ws.data_ptr(), ws.numel(), ws
+
+
+@functools.lru_cache(maxsize=4096)
+def _ws_bytes(name: str, *sizes) -> int:
+    return getattr(lib(), name)(*sizes)
 
 
 def paged_attention(q, k_pool, v_pool, table, lens, k_new=None, v_new=None, scale=None, max_len=None, out=None,
@@ -567,29 +576,31 @@ def paged_attention(q, k_pool, v_pool, table, lens, k_new=None, v_new=None, scal
         raise ValueError("q is [B][Hq][d], the pools [n_pages][Hkv][page][d], table [B][max_pages]")
     B, Hq, d = q.shape
     n_pages, Hkv, page, _ = k_pool.shape
-    dev, at, dt = q.device, q.get_device(), _dtype_tag(q)
-    _need("q", q, q.shape, q.dtype, at)
-    _need("k_pool", k_pool, (n_pages, Hkv, page, d), q.dtype, at)
-    _need("v_pool", v_pool, k_pool.shape, q.dtype, at)
-    _need("table", table, (B, table.shape[1]), torch.int32, at)
+    max_pages = table.shape[1]
+    at, tag, dt = q.get_device(), _dtype_tag(q), q.dtype
+    _need("q", q, (B, Hq, d), dt, at)
+    _need("k_pool", k_pool, (n_pages, Hkv, page, d), dt, at)
+    _need("v_pool", v_pool, k_pool.shape, dt, at)
+    _need("table", table, (B, max_pages), torch.int32, at)
     _need("lens", lens, (B,), torch.int32, at)
     if (k_new is None) != (v_new is None):
         raise ValueError("k_new and v_new go together")
+    kn = vn = None
     if k_new is not None:
-        _need("k_new", k_new, (B, Hkv, d), q.dtype, at)
-        _need("v_new", v_new, (B, Hkv, d), q.dtype, at)
+        kn = _need("k_new", k_new, (B, Hkv, d), dt, at).data_ptr()
+        vn = _need("v_new", v_new, (B, Hkv, d), dt, at).data_ptr()
     if scale is None:
         scale = d ** -0.5
-    cap = min(table.shape[1] * page, 2 ** 31 - 1)
+    cap = min(max_pages * page, 2 ** 31 - 1)
     max_len = cap if max_len is None else min(int(max_len), cap)
-    with _On(q, stream) as s:
-        out = torch.empty_like(q) if out is None else _need("out", out, q.shape, q.dtype, at)
-        lse = (torch.empty((B, Hq), dtype=torch.float32, device=dev) if lse is None
+    with _On(at, stream) as s:
+        out = torch.empty_like(q) if out is None else _need("out", out, (B, Hq, d), dt, at)
+        lse = (torch.empty((B, Hq), dtype=torch.float32, device=at) if lse is None
                else _need("lse", lse, (B, Hq), torch.float32, at))
-        ws = _scratch(ws, lib().escha_paged_attention_workspace(B, Hq, Hkv, d, max_len), dev)
-        check(lib().escha_paged_attention(ptr(q), ptr(k_pool), ptr(v_pool), dt, ptr(table), ptr(lens), B, Hq, Hkv, d,
-                                          page, n_pages, table.shape[1], max_len, float(scale), ptr(k_new), ptr(v_new),
-                                          ptr(out), ptr(lse), ptr(ws), ws.numel(), s))
+        w, n, ws = _scratch(ws, _ws_bytes("escha_paged_attention_workspace", B, Hq, Hkv, d, max_len), at)
+        check(lib().escha_paged_attention(q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), tag, table.data_ptr(),
+                                          lens.data_ptr(), B, Hq, Hkv, d, page, n_pages, max_pages, max_len, scale, kn,
+                                          vn, out.data_ptr(), lse.data_ptr(), w, n, s))
     return out, lse
 
 
@@ -606,10 +617,10 @@ def delta_rule(q, k, v, g, beta, state, at, scale=None, norm_eps=1e-6, max_len=N
         raise ValueError("q and k are [T][Hk][dk], v is [T][Hv][dv], state [n][Hv][dk][dv]")
     T, Hk, dk = q.shape
     Hv, dv = v.shape[1:]
-    n, dev, on, dt = state.shape[0], q.device, q.get_device(), _dtype_tag(q)
-    _need("q", q, q.shape, q.dtype, on)
-    _need("k", k, q.shape, q.dtype, on)
-    _need("v", v, (T, Hv, dv), q.dtype, on)
+    n, on, tag, dt = state.shape[0], q.get_device(), _dtype_tag(q), q.dtype
+    _need("q", q, (T, Hk, dk), dt, on)
+    _need("k", k, (T, Hk, dk), dt, on)
+    _need("v", v, (T, Hv, dv), dt, on)
     _need("g", g, (T, Hv), torch.float32, on)
     _need("beta", beta, (T, Hv), torch.float32, on)
     _need("state", state, (n, Hv, dk, dv), torch.float32, on)
@@ -621,11 +632,12 @@ def delta_rule(q, k, v, g, beta, state, at, scale=None, norm_eps=1e-6, max_len=N
     elif not norm_eps >= 0:
         raise ValueError("norm_eps must be >= 0, or None")
     max_len = -(-T // max(n, 1)) if max_len is None else int(max_len)
-    with _On(q, stream) as s:
-        out = torch.empty_like(v) if out is None else _need("out", out, v.shape, v.dtype, on)
-        ws = _scratch(ws, lib().escha_delta_rule_workspace(n, T, Hk, Hv, dk, dv, max_len), dev)
-        check(lib().escha_delta_rule(ptr(q), ptr(k), ptr(v), dt, ptr(g), ptr(beta), ptr(state), ptr(at), n, T, Hk, Hv,
-                                     dk, dv, max_len, float(scale), float(norm_eps), ptr(out), ptr(ws), ws.numel(), s))
+    with _On(on, stream) as s:
+        out = torch.empty_like(v) if out is None else _need("out", out, (T, Hv, dv), dt, on)
+        w, size, ws = _scratch(ws, _ws_bytes("escha_delta_rule_workspace", n, T, Hk, Hv, dk, dv, max_len), on)
+        check(lib().escha_delta_rule(q.data_ptr(), k.data_ptr(), v.data_ptr(), tag, g.data_ptr(), beta.data_ptr(),
+                                     state.data_ptr(), at.data_ptr(), n, T, Hk, Hv, dk, dv, max_len, scale, norm_eps,
+                                     out.data_ptr(), w, size, s))
     return out
 
 
@@ -641,20 +653,22 @@ def token_logprobs(logits, ids=None, top: int = 0, ws=None, stream=None) -> dict
     ld = logits.stride(0) if M > 1 else V
     if (V > 1 and logits.stride(1) != 1) or ld < V:
         raise ValueError("the rows of logits must be contiguous and apart")
-    dev, dt = logits.device, _dtype_tag(logits)
+    at, tag, top, dev = logits.get_device(), _dtype_tag(logits), int(top), logits.device
+    n_ids = 0
     if ids is not None:
-        _need("ids", ids, (M,) if ids.dim() == 1 else (M, ids.shape[-1]), torch.int32, logits.get_device())
-    n_ids = 0 if ids is None else (1 if ids.dim() == 1 else ids.shape[1])
-    with _On(logits, stream) as s:
-        f32 = dict(dtype=torch.float32, device=dev)
-        r = {"logprobs": None if ids is None else torch.empty(ids.shape, **f32), "entropy": torch.empty(M, **f32),
-             "lse": torch.empty(M, **f32), "top_ids": torch.empty((M, max(int(top), 0)), dtype=torch.int32, device=dev),
-             "top_logprobs": torch.empty((M, max(int(top), 0)), **f32)}
-        ws = _scratch(ws, lib().escha_token_logprobs_workspace(M, V), dev)
-        check(lib().escha_token_logprobs(ptr(logits), dt, M, V, ld, ptr(ids), n_ids, int(top), ptr(r["logprobs"]),
-                                         ptr(r["entropy"]), ptr(r["lse"]), ptr(r["top_ids"]), ptr(r["top_logprobs"]),
-                                         ptr(ws), ws.numel(), s))
-    return r
+        n_ids = 1 if ids.dim() == 1 else ids.shape[-1]
+        _need("ids", ids, (M,) if ids.dim() == 1 else (M, n_ids), torch.int32, at)
+    with _On(at, stream) as s:
+        lps = None if ids is None else torch.empty(ids.shape, dtype=torch.float32, device=dev)
+        entropy = torch.empty(M, dtype=torch.float32, device=dev)
+        lse = torch.empty(M, dtype=torch.float32, device=dev)
+        top_ids = torch.empty((M, max(top, 0)), dtype=torch.int32, device=dev)
+        top_lps = torch.empty((M, max(top, 0)), dtype=torch.float32, device=dev)
+        w, n, ws = _scratch(ws, _ws_bytes("escha_token_logprobs_workspace", M, V), at)
+        check(lib().escha_token_logprobs(logits.data_ptr(), tag, M, V, ld, ids.data_ptr() if n_ids else None, n_ids, top,
+                                         lps.data_ptr() if n_ids else None, entropy.data_ptr(), lse.data_ptr(),
+                                         top_ids.data_ptr(), top_lps.data_ptr(), w, n, s))
+    return {"logprobs": lps, "entropy": entropy, "lse": lse, "top_ids": top_ids, "top_logprobs": top_lps}
 
 
 def int8_w8a16_dequant(W, scales, stream=None) -> torch.Tensor:

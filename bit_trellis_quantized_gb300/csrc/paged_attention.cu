@@ -494,6 +494,7 @@ __global__ void __launch_bounds__(PaCfg<D, NT>::kThreads, PaCfg<D, NT>::kCtas)
 // ranges: CTA (head of the unit, first CTA of the unit), kSets interleaved sets
 // of parts with D / 4 threads of four values each.
 constexpr int kPaSets = 8;
+static_assert(PaCfg<64, 1>::kCtas <= 4 && PaCfg<128, 1>::kCtas <= 4 && PaCfg<256, 1>::kCtas <= 4, "the join holds a factor a CTA");
 template <int DT, int D>
 __global__ void __launch_bounds__(kPaSets* D / 4) paged_attention_join_kernel(PagedAttnArgs a, int heads, PaParts parts) {
     constexpr int kCols = D / 4, kThreads = kPaSets * kCols, kW = kThreads / 32;
@@ -508,8 +509,11 @@ __global__ void __launch_bounds__(kPaSets* D / 4) paged_attention_join_kernel(Pa
     const long long h = (long long)u.x * a.Hq + u.y * group + u.z * heads + hh;
     // the first CTA's part is its second one
     auto slot = [&](int i) { return 2ll * (blockIdx.y + i) + (i == 0 ? 1 : 0); };
+    // the parts' factors first: what is summed then hangs on no other load
+    constexpr int kHold = kSms * 4;  // CTAs of a launch, at most
+    __shared__ float factor[kHold];
     float top = -INFINITY;
-    for (int i = t; i < n; i += kThreads) top = fmaxf(top, parts.ml[slot(i) * 2 * heads + hh]);
+    for (int i = t; i < n; i += kThreads) top = fmaxf(top, factor[i] = parts.ml[slot(i) * 2 * heads + hh]);
 #pragma unroll
     for (int m = 16; m >= 1; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
     if (lane == 0) red[0][warp] = top;
@@ -518,16 +522,20 @@ __global__ void __launch_bounds__(kPaSets* D / 4) paged_attention_join_kernel(Pa
     for (int w = 0; w < kW; ++w) top = fmaxf(top, red[0][w]);
     const float base = top == -INFINITY ? 0.f : top;
     float sum = 0.f;
-    for (int i = t; i < n; i += kThreads)
-        sum += parts.ml[(slot(i) * 2 + 1) * heads + hh] * ex2(parts.ml[slot(i) * 2 * heads + hh] - base);
+    for (int i = t; i < n; i += kThreads) {
+        const float f = ex2(factor[i] - base);
+        sum += parts.ml[(slot(i) * 2 + 1) * heads + hh] * f;
+        factor[i] = f;
+    }
 #pragma unroll
     for (int m = 16; m >= 1; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
     if (lane == 0) red[1][warp] = sum;
+    __syncthreads();
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 4
+#pragma unroll 8
     for (int i = set; i < n; i += kPaSets) {
-        const float f = ex2(parts.ml[slot(i) * 2 * heads + hh] - base);
         const float4 p = *reinterpret_cast<const float4*>(parts.acc + (slot(i) * heads + hh) * D + col * 4);
+        const float f = factor[i];
         v.x += f * p.x, v.y += f * p.y, v.z += f * p.z, v.w += f * p.w;
     }
     sums[set][col] = v;
@@ -558,7 +566,9 @@ int pa_ctas(int nt) {
 PaPlan pa_plan(int Hq, int Hkv, int d) {
     PaPlan p{};
     const int group = Hq / Hkv;
-    p.nt = group <= 8 ? 1 : 2;
+    // 16 heads of 256 values would not fit the registers: at dimension 256 a unit has 8 heads, and a second one reads the
+    // keys again
+    p.nt = group <= 8 || d == 256 ? 1 : 2;
     p.heads = 8 * p.nt;
     p.tiles = (group + p.heads - 1) / p.heads;
     p.ctas = d == 256 ? pa_ctas<256>(p.nt) : d == 128 ? pa_ctas<128>(p.nt) : pa_ctas<64>(p.nt);
@@ -584,7 +594,7 @@ cudaError_t launch_nt(const PagedAttnArgs& a, const PaPlan& p, const PaParts& pa
     PaDiv div = pa_div(a.page);
     void* args[] = {const_cast<PagedAttnArgs*>(&a), &tiles, &div, const_cast<PaParts*>(&parts)};
     e = launch_kernel(f, dim3(p.ctas), dim3(C::kThreads), C::kSmem, true, s, args);
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || a.max_len <= C::kRound) return e;  // units of one round are never cut
     void* jargs[] = {const_cast<PagedAttnArgs*>(&a), &heads, const_cast<PaParts*>(&parts)};
     return launch_kernel(reinterpret_cast<const void*>(paged_attention_join_kernel<DT, D>), dim3(p.heads, p.ctas), dim3(kPaSets * D / 4), 0, true, s,
                          jargs);
@@ -594,7 +604,7 @@ template <int DT>
 cudaError_t launch_dt(const PagedAttnArgs& a, const PaPlan& p, const PaParts& parts, cudaStream_t s) {
     if (a.d == 64) return p.nt == 1 ? launch_nt<DT, 64, 1>(a, p, parts, s) : launch_nt<DT, 64, 2>(a, p, parts, s);
     if (a.d == 128) return p.nt == 1 ? launch_nt<DT, 128, 1>(a, p, parts, s) : launch_nt<DT, 128, 2>(a, p, parts, s);
-    return p.nt == 1 ? launch_nt<DT, 256, 1>(a, p, parts, s) : launch_nt<DT, 256, 2>(a, p, parts, s);
+    return launch_nt<DT, 256, 1>(a, p, parts, s);
 }
 
 }  // namespace

@@ -122,8 +122,11 @@ __device__ __forceinline__ int pa_len(const PagedAttnArgs& a, int b) {
 struct PaParts {
     float* acc;  // [2 G][heads][D]
     float* ml;   // [2 G][2][heads]
-    int4* open;  // [G] the unit that begins in this CTA's range and ends in another's: sequence, key head,
-                 // tile of heads and number of parts (0: there is none)
+    // Units that begin in one CTA's range and end in another's: sequence, unit of the sequence, first CTA and number of
+    // parts (0: not such a unit). By unit, where there are no more units than CTAs; else one place a CTA, as no more
+    // than one such unit begins in its range. The join's grid is as large: 8 x 456 CTAs that mostly find nothing took 4 us.
+    int4* open;
+    int by_unit;
 };
 
 // A place in the list of rounds: round r of one (sequence, key head, tile of heads).
@@ -184,10 +187,12 @@ __global__ void __launch_bounds__(PaCfg<D, NT>::kThreads, PaCfg<D, NT>::kCtas)
     }
     // every CTA that takes part has a round at least (the join counts on it)
     const long long ctas = min(static_cast<long long>(gridDim.x), total);
-    if (t == 0) parts.open[blockIdx.x] = make_int4(0, 0, 0, 0);
+    if (t == 0 && !parts.by_unit) parts.open[blockIdx.x] = make_int4(0, 0, 0, 0);
     // the sequences without keys
     for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
         if (pa_len(a, b) > 0) continue;
+        if (parts.by_unit)
+            for (int i = t; i < units; i += kThreads) parts.open[b * units + i] = make_int4(0, 0, 0, 0);
         for (int i = t; i < a.Hq * D / 2; i += kThreads) static_cast<uint32_t*>(a.out)[(long long)b * a.Hq * D / 2 + i] = 0u;
         if (a.lse)
             for (int i = t; i < a.Hq; i += kThreads) a.lse[(long long)b * a.Hq + i] = -INFINITY;
@@ -477,11 +482,15 @@ __global__ void __launch_bounds__(PaCfg<D, NT>::kThreads, PaCfg<D, NT>::kCtas)
                     parts.ml[(slot * 2 + 1) * kHeads + t] = sum;
                 }
             }
-            if (t == 0 && piece_r0 == 0 && !last) {
-                // the CTA that holds the unit's last round: the largest c with floor(c total / ctas) <= it
-                const long long end = lo + i + (cur.rounds - 1 - cur.r);
-                const int n = static_cast<int>(((end + 1) * ctas - 1) / total) - static_cast<int>(blockIdx.x) + 1;
-                parts.open[blockIdx.x] = make_int4(cur.b, cur.kvh, cur.tile, n);
+            if (t == 0 && piece_r0 == 0 && (!last || parts.by_unit)) {
+                const int u = cur.kvh * tiles + cur.tile;
+                int n = 0;
+                if (!last) {
+                    // the CTA that holds the unit's last round: the largest c with floor(c total / ctas) <= it
+                    const long long end = lo + i + (cur.rounds - 1 - cur.r);
+                    n = static_cast<int>(((end + 1) * ctas - 1) / total) - static_cast<int>(blockIdx.x) + 1;
+                }
+                parts.open[parts.by_unit ? cur.b * units + u : blockIdx.x] = make_int4(cur.b, u, blockIdx.x, n);
             }
             __syncthreads();
             begin = true;
@@ -491,24 +500,24 @@ __global__ void __launch_bounds__(PaCfg<D, NT>::kThreads, PaCfg<D, NT>::kCtas)
 }
 
 // Joins the parts of one query head of a unit that lies in several CTAs'
-// ranges: CTA (head of the unit, first CTA of the unit), kSets interleaved sets
-// of parts with D / 4 threads of four values each.
+// ranges: CTA (head of the unit, place in `open`), kPaSets interleaved sets of
+// parts with D / 4 threads of four values each.
 constexpr int kPaSets = 8;
 static_assert(PaCfg<64, 1>::kCtas <= 4 && PaCfg<128, 1>::kCtas <= 4 && PaCfg<256, 1>::kCtas <= 4, "the join holds a factor a CTA");
 template <int DT, int D>
-__global__ void __launch_bounds__(kPaSets* D / 4) paged_attention_join_kernel(PagedAttnArgs a, int heads, PaParts parts) {
+__global__ void __launch_bounds__(kPaSets* D / 4) paged_attention_join_kernel(PagedAttnArgs a, int tiles, int heads, PaParts parts) {
     constexpr int kCols = D / 4, kThreads = kPaSets * kCols, kW = kThreads / 32;
     __shared__ float4 sums[kPaSets][kCols];
     __shared__ float red[2][kW];
     pdl_wait();
     pdl_trigger();
     const int4 u = parts.open[blockIdx.y];
-    const int n = u.w, hh = blockIdx.x, group = a.Hq / a.Hkv;
-    if (n == 0 || u.z * heads + hh >= group) return;
+    const int n = u.w, hh = blockIdx.x, group = a.Hq / a.Hkv, kvh = u.y / tiles, tile = u.y % tiles;
+    if (n == 0 || tile * heads + hh >= group) return;
     const int t = threadIdx.x, col = t % kCols, set = t / kCols, lane = t & 31, warp = t >> 5;
-    const long long h = (long long)u.x * a.Hq + u.y * group + u.z * heads + hh;
+    const long long h = (long long)u.x * a.Hq + kvh * group + tile * heads + hh;
     // the first CTA's part is its second one
-    auto slot = [&](int i) { return 2ll * (blockIdx.y + i) + (i == 0 ? 1 : 0); };
+    auto slot = [&](int i) { return 2ll * (u.z + i) + (i == 0 ? 1 : 0); };
     // the parts' factors first: what is summed then hangs on no other load
     constexpr int kHold = kSms * 4;  // CTAs of a launch, at most
     __shared__ float factor[kHold];
@@ -595,9 +604,10 @@ cudaError_t launch_nt(const PagedAttnArgs& a, const PaPlan& p, const PaParts& pa
     void* args[] = {const_cast<PagedAttnArgs*>(&a), &tiles, &div, const_cast<PaParts*>(&parts)};
     e = launch_kernel(f, dim3(p.ctas), dim3(C::kThreads), C::kSmem, true, s, args);
     if (e != cudaSuccess || a.max_len <= C::kRound) return e;  // units of one round are never cut
-    void* jargs[] = {const_cast<PagedAttnArgs*>(&a), &heads, const_cast<PaParts*>(&parts)};
-    return launch_kernel(reinterpret_cast<const void*>(paged_attention_join_kernel<DT, D>), dim3(p.heads, p.ctas), dim3(kPaSets * D / 4), 0, true, s,
-                         jargs);
+    void* jargs[] = {const_cast<PagedAttnArgs*>(&a), &tiles, &heads, const_cast<PaParts*>(&parts)};
+    const int group = a.Hq / a.Hkv, places = parts.by_unit ? a.B * a.Hkv * tiles : p.ctas;
+    return launch_kernel(reinterpret_cast<const void*>(paged_attention_join_kernel<DT, D>), dim3(heads < group ? heads : group, places),
+                         dim3(kPaSets * D / 4), 0, true, s, jargs);
 }
 
 template <int DT>
@@ -618,7 +628,7 @@ cudaError_t launch_paged_attention(const PagedAttnArgs& a, int dtype, void* ws, 
     const PaPlan p = pa_plan(a.Hq, a.Hkv, a.d);
     char* w = static_cast<char*>(ws);
     const PaParts parts{reinterpret_cast<float*>(w + p.acc), reinterpret_cast<float*>(w + p.ml),
-                        reinterpret_cast<int4*>(w + p.open)};
+                        reinterpret_cast<int4*>(w + p.open), (long long)a.B * a.Hkv * p.tiles <= p.ctas};
     return dtype == 1 ? launch_dt<1>(a, p, parts, s) : launch_dt<2>(a, p, parts, s);
 }
 

@@ -71,6 +71,8 @@ SHAPES = [
     ("bf16", [64], 1, 3, 64, 96), ("f16", [63, 65, 0, 129, 1], 2, 4, 128, 128), ("bf16", [200], 1, 2, 128, 256),
     ("f16", [17, 130, 33], 3, 3, 64, 128), ("bf16", [0, 0, 5], 2, 2, 64, 160), ("f16", [300], 2, 4, 128, 32),
     ("bf16", [2, 127, 128, 0, 191, 192, 193], 1, 2, 128, 64),
+    # enough heads for the walk of 64 columns a CTA
+    ("f16", [70, 33, 0, 64, 31] * 8, 2, 4, 64, 64), ("bf16", [100, 1, 40] * 14, 1, 2, 128, 128),
 ]
 
 

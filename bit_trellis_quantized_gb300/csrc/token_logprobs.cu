@@ -678,7 +678,9 @@ LpPlan lp_plan(int M, int V, int dtype) {
     p.per = total / p.ctas;
     p.rest = static_cast<int>(total % p.ctas);
     p.join = p.rest != 0 || p.per % p.units != 0;
-    p.most_parts = p.ctas / M + 2;
+    // ranges of `per` units and more that meet a row's units (a row behind the first `rest` ranges meets more than an
+    // even share of them): 85 at most, as a range has 8 units or a row and more
+    p.most_parts = std::min(p.ctas, std::max(p.units - 2, 0) / static_cast<int>(std::min<long long>(p.per, p.units)) + 2);
     return p;
 }
 

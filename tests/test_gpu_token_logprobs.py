@@ -61,6 +61,18 @@ def test_matches_the_formula(M, V, top, dtype):
         assert torch.equal(a[k], b[k])
 
 
+@pytest.mark.parametrize("dtype,M,V", [("f16", 2, 161024), ("bf16", 4, 165185), ("f16", 5, 135991), ("f32", 2, 156288)])
+def test_last_row_in_more_parts_than_an_even_share(dtype, M, V):
+    """Ranges of 8 and 9 units (16 and 17): the last row lies in the smaller
+    ones, up to 5 parts more than CTAs / M + 2; its largest values are in its
+    last parts."""
+    native = _native()
+    rng = np.random.default_rng(38)
+    x = rng.standard_normal((M, V)) * 3
+    x[:, V - 3000::97] += 20
+    run_and_check(native, torch.from_numpy(x).to(DT[dtype]).cuda(), rng.integers(0, V, (M, 2)), 32)
+
+
 @pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
 def test_rows_that_start_anywhere(dtype):
     """Rows a stride apart that leaves them on every alignment, what lies

@@ -6,7 +6,9 @@
 // Parts over different keys join by their (m, sum, weighted values). Scores,
 // maxima, sums and weighted values are held in f32. A weight e^(x - m) enters
 // the tensor cores as two 16-bit parts (value, remainder), so that the one
-// rounding that shows is that of `out` to its type.
+// rounding that shows is that of `out` to its type. fp16 parts are of the
+// weight times 2^15: its steps end at 2^-24, and keys at 2^-25 of the largest
+// weight, each lost or doubled without it, may be many.
 //
 // Bound: the one read of K and V (a key is used by Hq / Hkv heads: at most 4 x
 // 16 flops a byte). So the layout serves the loads:
@@ -32,6 +34,8 @@ namespace {
 
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
+template <int DT>
+constexpr float kPaUp = DT == 1 ? 0x1p15f : 1.f;  // of a weight's parts
 
 // A warp's ring holds kHalves halves of stages (16 keys, or their 16 values).
 template <int D, int NT>
@@ -371,10 +375,11 @@ __global__ void __launch_bounds__(PaCfg<D, NT>::kThreads, PaCfg<D, NT>::kCtas)
             }
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const uint32_t hi2 = pa_pack<DT>(p[2 * e], p[2 * e + 1]);
+                const float w0 = p[2 * e] * kPaUp<DT>, w1 = p[2 * e + 1] * kPaUp<DT>;
+                const uint32_t hi2 = pa_pack<DT>(w0, w1);
                 const float2 back = pa_unpack<DT>(hi2);
                 ph[n][e] = movm(hi2);
-                pl[n][e] = movm(pa_pack<DT>(p[2 * e] - back.x, p[2 * e + 1] - back.y));
+                pl[n][e] = movm(pa_pack<DT>(w0 - back.x, w1 - back.y));
             }
         }
         // ---- weighted values
@@ -423,7 +428,7 @@ __global__ void __launch_bounds__(PaCfg<D, NT>::kThreads, PaCfg<D, NT>::kCtas)
                     float top = -INFINITY;
 #pragma unroll
                     for (int w = 0; w < kWarps; ++w) top = fmaxf(top, sm_m[w][n * 8 + q4 * 2 + e]);
-                    f[n][e] = ex2(m[n][e] - (top == -INFINITY ? 0.f : top));
+                    f[n][e] = ex2(m[n][e] - (top == -INFINITY ? 0.f : top)) * (1.f / kPaUp<DT>);
                 }
             // element (head 8 n + 2 q4 + e, value 16 k + g + 8 r). At the end of the range every warp has a buffer,
             // its ring; before, the ring is being filled, and the warps of each parity take turns at one.

@@ -149,6 +149,25 @@ def test_far_apart_scores(dtype):
     assert torch.equal(out[0, 0], c["v"][int(c["table"][0, 4]), 0, 7])
 
 
+@pytest.mark.parametrize("dtype,d", [("f16", 64), ("bf16", 128), ("f16", 256)])
+def test_many_keys_of_next_to_no_weight(dtype, d):
+    """One key of value 0 that takes almost all weight; 40000 others, each at
+    2^-25.4 of it, make up the output: their weights are as good as any."""
+    native = _native()
+    c = make(17, [40000], 4, 2, d, 64, dtype, poison=False)
+    c["q"][:] = 0
+    c["q"][:, :, 1] = 1.1  # (of both types: 1.1 rounded)
+    c["k"][:, :, :, 1] = 0
+    pg = int(c["table"][0, 100])
+    c["k"][pg, :, 3] = 0
+    c["k"][pg, :, 3, 1] = 16.0
+    c["v"][:] = c["v"].abs()
+    c["v"][pg, :, 3] = 0
+    out, lse = native.paged_attention(c["q"], c["k"], c["v"], c["table"], c["lens"], scale=1.0)
+    assert float(out.abs().min()) > 5e-4
+    check(c, out, lse, 1.0, dtype)
+
+
 def test_one_long_sequence_among_short_ones():
     native = _native()
     c = make(15, [20000, 3, 0, 777], 16, 2, 256, 64, "bf16")

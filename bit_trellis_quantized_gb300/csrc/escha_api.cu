@@ -1267,6 +1267,7 @@ int check_paged_shape(int B, int Hq, int Hkv, int d, int max_len, const char* na
     if (B < 1 || Hq < 1 || Hkv < 1 || max_len < 1)
         return fail(ESCHA_E_ARG, "%s: B=%d Hq=%d Hkv=%d max_len=%d must be >= 1", name, B, Hq, Hkv, max_len);
     if (B > 65535) return fail(ESCHA_E_SHAPE, "%s: B=%d above 65535", name, B);
+    if (max_len > (1 << 30)) return fail(ESCHA_E_SHAPE, "%s: max_len=%d above 2^30", name, max_len);
     if (Hq % Hkv || Hq / Hkv > 64 || Hkv > 1024)
         return fail(ESCHA_E_SHAPE, "%s: Hq=%d must be 1..64 times Hkv=%d, Hkv <= 1024", name, Hq, Hkv);
     if (d != 64 && d != 128 && d != 256) return fail(ESCHA_E_SHAPE, "%s: d=%d must be 64, 128 or 256", name, d);

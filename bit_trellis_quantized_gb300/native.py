@@ -519,6 +519,8 @@ class _On:
     __slots__ = ("index", "device", "stream")
 
     def __init__(self, index: int, stream=None):
+        if stream is not None and stream.device.index != index:
+            raise ValueError(f"stream is of {stream.device}, the tensors are on cuda:{index}")
         self.index = index
         self.device = None if index == torch._C._cuda_getDevice() else torch.cuda.device(index)
         self.stream = torch.cuda.stream(stream) if stream is not None else None
@@ -591,7 +593,9 @@ def paged_attention(q, k_pool, v_pool, table, lens, k_new=None, v_new=None, scal
         vn = _need("v_new", v_new, (B, Hkv, d), dt, at).data_ptr()
     if scale is None:
         scale = d ** -0.5
-    cap = min(max_pages * page, 2 ** 31 - 1)
+    if max_pages >= 2 ** 31:
+        raise ValueError(f"max_pages={max_pages} is above 2^31 - 1")
+    cap = min(max_pages * page, 2 ** 30)
     max_len = cap if max_len is None else min(int(max_len), cap)
     with _On(at, stream) as s:
         out = torch.empty_like(q) if out is None else _need("out", out, (B, Hq, d), dt, at)
@@ -650,6 +654,8 @@ def token_logprobs(logits, ids=None, top: int = 0, ws=None, stream=None) -> dict
     if logits.dim() != 2 or not logits.is_cuda:
         raise ValueError("logits must be a CUDA tensor [M][V]")
     M, V = logits.shape
+    if max(M, V) >= 2 ** 31:
+        raise ValueError(f"logits [{M}][{V}] is above 2^31 - 1 rows or values")
     ld = logits.stride(0) if M > 1 else V
     if (V > 1 and logits.stride(1) != 1) or ld < V:
         raise ValueError("the rows of logits must be contiguous and apart")

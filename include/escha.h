@@ -520,15 +520,19 @@ int escha_moe_route(const escha_moe_layer* L, const uint16_t* x, int T, uint16_t
  *   k_new, v_new  [B][Hkv][d] or both NULL: the new token's key and value,
  *            stored at position lens[b] - 1 by the call and attended with the
  *            rest. Sequences may share pages, but not the page that holds
- *            another's position lens - 1 (copy it first). When the page entry
+ *            another's position lens - 1 (copy it first), and no table names
+ *            the page of its own new token twice. When the page entry
  *            of that position is outside [0, n_pages), the new token is
  *            neither stored nor attended.
  *   out      [B][Hq][d];  lse f32 [B][Hq] or NULL
  *   d        64, 128 or 256;  Hq = 1..64 times Hkv, Hkv <= 1024, B <= 65535
- *   max_len  host-side bound of lens, >= 1 (max_pages * page always serves)
+ *   max_len  host-side bound of lens, 1..2^30 (max_pages * page serves where
+ *            it is no more than that)
  *   ws       escha_paged_attention_workspace(B, Hq, Hkv, d, max_len) bytes;
  *            nothing in it has to start at zero
- * Positions at or behind lens[b] are never read: they may hold anything.
+ * Positions at or behind lens[b] are never read: they may hold anything. A NaN
+ * or an infinity among the attended keys and values, or q, may make the heads
+ * that read it NaN. out and lse must not overlap the inputs.
  * Results do not depend on what else runs; a call is repeatable bit for bit.
  * Errors: ESCHA_E_ARG, ESCHA_E_SHAPE, ESCHA_E_ALIGN, ESCHA_E_WORKSPACE,
  * ESCHA_E_CUDA, ESCHA_E_DEVICE. */

@@ -37,7 +37,7 @@ def test_paged_attention_validation():
                      (E.ESCHA_E_ARG, dict(scale=float("inf"))), (E.ESCHA_E_ARG, dict(scale=float("nan"))),
                      (E.ESCHA_E_SHAPE, dict(d=96)), (E.ESCHA_E_SHAPE, dict(Hq=15)), (E.ESCHA_E_SHAPE, dict(Hq=130)),
                      (E.ESCHA_E_SHAPE, dict(B=65536)), (E.ESCHA_E_SHAPE, dict(Hq=2048, Hkv=2048)),
-                     (E.ESCHA_E_SHAPE, dict(n=1 << 24, page=64)),
+                     (E.ESCHA_E_SHAPE, dict(n=1 << 24, page=64)), (E.ESCHA_E_SHAPE, dict(ml=(1 << 30) + 1)),
                      (E.ESCHA_E_ALIGN, dict(q=G + 8)), (E.ESCHA_E_ALIGN, dict(lens=G + 4)),
                      (E.ESCHA_E_ALIGN, dict(lse=G + 4)), (E.ESCHA_E_ALIGN, dict(kn=G, vn=G + 2))):
         assert call(**kw) == code, kw
@@ -108,3 +108,29 @@ def test_wrappers_refuse_host_tensors():
                           torch.zeros(2, dtype=torch.int32))
     with pytest.raises(ValueError):
         native.token_logprobs(torch.zeros((2, 9)))
+
+
+def test_wrappers_refuse_a_stream_of_another_device():
+    torch = pytest.importorskip("torch")
+    native, _ = _lib()
+
+    class Stream:
+        device = torch.device("cuda", 1)
+
+    with pytest.raises(ValueError, match="cuda:1"):
+        native._On(0, Stream())
+
+
+def test_wrappers_refuse_sizes_past_the_abis_integers():
+    torch = pytest.importorskip("torch")
+    native, _ = _lib()
+
+    class Tensor:  # as much of one as comes before the check
+        is_cuda = True
+
+        def __init__(self, *shape):
+            self.shape, self.dim = torch.Size(shape), lambda: len(shape)
+
+    for M, V in ((2 ** 32 + 1, 1), (1, 2 ** 31)):
+        with pytest.raises(ValueError, match="2\\^31"):
+            native.token_logprobs(Tensor(M, V))

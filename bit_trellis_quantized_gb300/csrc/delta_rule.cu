@@ -139,10 +139,12 @@ __global__ void __launch_bounds__(kDrThreads) delta_step_kernel(DeltaArgs a) {
 // sequence's chunks; its products run on the tensor cores.
 //
 // Precision: states stay as good as f32 makes them. Keys and queries are fp16
-// values (bf16 ones times a power of two a row), exact. Everything else enters
-// a product as two fp16 parts of its value times a power of two a row (the
-// largest of the row at 2^13): 22 bits and more of the row's largest. Sums are
-// f32.
+// values (bf16 ones times a power of two a row: exact, but for values below
+// 2^-17 of the row's largest, which are 2^-25 of it off at most). Everything
+// else enters a product as two fp16 parts of its value times a power of two a
+// row (the largest of the row at 2^13): 22 bits and more of the row's largest.
+// Sums are f32. What is 2^-38 of a row's largest is lost, and rows of the state
+// and of V - ... whose largest is below 2^-60 have fewer bits.
 constexpr int kC = 32;  // tokens of a chunk
 
 // What the first kernel leaves for one (chunk, value head).
@@ -190,6 +192,10 @@ __device__ __forceinline__ float dr_scale(float most) {
 }
 // 1 / p of a power of two in 2^-126..2^126
 __device__ __forceinline__ float dr_inv(float p) { return __uint_as_float(0x7F000000u - __float_as_uint(p)); }
+// The power of two, within 2^-100..2^114, that r is 2^8 and more times
+__device__ __forceinline__ float dr_unit(float r) {
+    return __uint_as_float(static_cast<uint32_t>(min(241, max(27, static_cast<int>(__float_as_uint(r) >> 23) - 8))) << 23);
+}
 // x and y as two fp16 parts each
 __device__ __forceinline__ void dr_split(float x, float y, uint32_t& hi, uint32_t& lo) {
     const __half2 h = __floats2half2_rn(x, y);
@@ -750,10 +756,10 @@ __global__ void __launch_bounds__(DrWalk<DK, W>::kThreads) delta_walk_kernel(Del
                 all[1] = fmaxf(all[1], fmaxf(fabsf(S[k][2]), fabsf(S[k][3])));
             }
             all[0] = quad_max(all[0]), all[1] = quad_max(all[1]);
-            const float f0 = all[0] == 0.f ? 1.f : fminf(dr_scale(all[0]), unit[0] * 0x1p100f);
-            const float f1 = all[1] == 0.f ? 1.f : fminf(dr_scale(all[1]), unit[1] * 0x1p100f);
+            const float f0 = !out0 || all[0] == 0.f ? 1.f : fminf(dr_scale(all[0]), unit[0] * 0x1p100f);
+            const float f1 = !out1 || all[1] == 0.f ? 1.f : fminf(dr_scale(all[1]), unit[1] * 0x1p100f);
             // columns of zeros, and those at the end of the units' range, stay
-            if (!__any_sync(0xffffffffu, (out0 && f0 != 1.f) || (out1 && f1 != 1.f))) break;
+            if (!__any_sync(0xffffffffu, f0 != 1.f || f1 != 1.f)) break;
 #pragma unroll
             for (int k = 0; k < kNt; ++k) S[k][0] *= f0, S[k][1] *= f0, S[k][2] *= f1, S[k][3] *= f1;
             unit[0] *= dr_inv(f0), unit[1] *= dr_inv(f1);
@@ -809,12 +815,13 @@ __global__ void __launch_bounds__(DrWalk<DK, W>::kThreads) delta_walk_kernel(Del
         float keep[2];
 #pragma unroll
         for (int h = 0; h < 2; ++h) {
-            // in the state's own unit, while what is left of it or what is added stays well inside that window
-            const float r = fmaxf(decay * most[h], more[h] * dr_inv(unit[h]));
-            const float f = r == 0.f || (r >= 4.f && r < 2048.f) ? 1.f : fminf(dr_scale(r) * 0x1p-5f, unit[h] * 0x1p100f);
-            keep[h] = decay * f;
-            unit[h] *= dr_inv(f);
-            up[h] = dr_inv(unit[h]);
+            // in the state's own unit, while what is left of it or what is added stays well inside that window (sizes
+            // as they are, not in units: a quotient of far-apart ones would overflow)
+            const float r = fmaxf(decay * most[h] * unit[h], more[h]);
+            const float to = r == 0.f || (r >= 4.f * unit[h] && r < 2048.f * unit[h]) ? unit[h] : dr_unit(r);
+            keep[h] = decay * unit[h] * dr_inv(to);
+            unit[h] = to;
+            up[h] = dr_inv(to);
         }
         parts(w, up, hi, lo);
 #pragma unroll

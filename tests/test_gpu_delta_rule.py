@@ -120,6 +120,72 @@ def test_keys_alike(max_len, dtype):
     run_and_check(native, c, dtype, max_len=max_len)
 
 
+def check_columns(c, state):
+    """Every column of the state to the bound of run_and_check of its own size:
+    columns do not meet and scale with their values. (All tokens count, as a
+    state that grows keeps what each was off.)"""
+    _, want_state = ref.delta_rule(*(f64(c[x]) for x in ("q", "k", "v", "g", "beta", "state")), c["at"].cpu().numpy(),
+                                      c["k"].shape[2] ** -0.5, 1e-6)
+    T, dk = c["k"].shape[0], c["k"].shape[2]
+    tol = 2.0 ** -20 * np.sqrt(dk * (T + 1))
+    off, size = np.linalg.norm(f64(state) - want_state, axis=2), np.linalg.norm(want_state, axis=2)
+    assert np.all(off <= tol * size)
+
+
+@pytest.mark.parametrize("max_len", [1, 1000])
+@pytest.mark.parametrize("dk", [64, 128])
+def test_columns_of_very_different_sizes(max_len, dk):
+    """Values of 2^-40 to 2^80 by column, over states of their size, and over
+    others 2^-60 to 2^10 times that."""
+    native = _native()
+    c = make(31, [100, 45], 1, 2, dk, 64, "bf16")
+    sizes = torch.exp2(torch.linspace(-40, 80, 64, device="cuda"))
+    c["v"] = (c["v"].float() * sizes).bfloat16()
+    c["state"][0] *= sizes
+    c["state"][1] *= sizes * torch.exp2(torch.linspace(-60, 10, 64, device="cuda")[torch.randperm(64, device="cuda")])
+    state = c["state"].clone()
+    native.delta_rule(*(c[x] for x in ("q", "k", "v", "g", "beta")), state, c["at"], max_len=max_len)
+    check_columns(c, state)
+
+
+@pytest.mark.parametrize("max_len", [1, 1000])
+def test_sizes_that_jump_and_states_that_grow(max_len):
+    """Values that go up from chunk to chunk, 2^-50 to 2^100 at once too; decays
+    of 0 in one head; positive g, which lets the state grow, in another."""
+    native = _native()
+    c = make(32, [32 * 6], 1, 3, 64, 32, "bf16")
+    for i, e in enumerate((-50, -50, 90, 92, 100, 100)):
+        c["v"][32 * i:32 * i + 32] = (c["v"][32 * i:32 * i + 32].float() * 2.0 ** e).bfloat16()
+    c["state"] *= 2.0 ** -50
+    c["g"][32 * 4:, 0] = -float("inf")
+    c["g"][32 * 5, 1] = -float("inf")
+    c["g"][:, 2] = 0.1
+    state = c["state"].clone()
+    native.delta_rule(*(c[x] for x in ("q", "k", "v", "g", "beta")), state, c["at"], max_len=max_len)
+    check_columns(c, state)
+
+
+@pytest.mark.parametrize("max_len", [1, 1000])
+def test_a_nan_stays_in_its_column_and_sequence(max_len):
+    native = _native()
+    c = make(33, [50, 70, 40], 1, 2, 64, 64, "f16")
+    args = [c[x] for x in ("q", "k", "v", "g", "beta")]
+    clean = c["state"].clone()
+    want = native.delta_rule(*args, clean, c["at"], max_len=max_len)
+    c["v"][90, 1, 17] = float("nan")
+    c["state"][0, 0, 5, 3] = float("inf")
+    c["v"][130, 0, 40] = float("inf")
+    state = c["state"].clone()
+    got = native.delta_rule(*args, state, c["at"], max_len=max_len)
+    hit = torch.zeros_like(got, dtype=torch.bool)
+    hit[50:120, 1, 17] = hit[:50, 0, 3] = hit[120:, 0, 40] = True
+    assert torch.equal(got[~hit], want[~hit])
+    assert not bool(got[90:120, 1, 17].isfinite().any()) and not bool(state[1, 1, :, 17].isfinite().all())
+    same = torch.ones_like(state, dtype=torch.bool)
+    same[1, 1, :, 17] = same[0, 0, :, 3] = same[2, 0, :, 40] = False
+    assert torch.equal(state[same], clean[same])
+
+
 @pytest.mark.parametrize("max_len", [1, 1000])
 def test_keys_taken_as_they_are(max_len):
     native = _native()

@@ -20,14 +20,14 @@
 // same bound over what was collected leaves a few more keys than asked for, and
 // each of them counts those above it. Where the buffer is full (a row that
 // ascends, a row of one value) a warp keeps the best 32 of the rest in order,
-// one a lane. Keeping such lists throughout cost more than all else: 250 us
-// where this takes 193 (2048 rows of 152064, top 8; 187 without any).
+// one a lane. (Keeping such lists throughout cost more than all else: 250 us
+// where this took 193, 2048 rows of 152064, top 8.)
 //
 // Bound: one read of the logits. Each lane loads a chunk ahead, and the
 // arithmetic is 5 instructions a value (pairs of f32 where there is an
-// instruction for them), so that it stays behind the loads. All rows, one after
-// another, are cut into equal ranges, one a CTA; a second kernel joins the
-// parts of rows that lie in several.
+// instruction for them), so that it stays behind the loads: 2048 rows of 152064
+// f32 take 211 us, 5.9 TB/s (187 without the top 8). How rows are dealt out to
+// warps, CTAs and clusters is at lp_route.
 #include <algorithm>
 
 #include "common.cuh"
@@ -223,6 +223,13 @@ __device__ __forceinline__ float max_nan(float a, float b) {
     float r;
     asm("max.NaN.f32 %0, %1, %2;" : "=f"(r) : "f"(a), "f"(b));
     return r;
+}
+
+__device__ __forceinline__ void st_cluster_f32(uint32_t addr, float v) {
+    asm volatile("st.shared::cluster.f32 [%0], %1;" ::"r"(addr), "f"(v) : "memory");
+}
+__device__ __forceinline__ void st_cluster_u64(uint32_t addr, unsigned long long v) {
+    asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
 }
 
 // Adds a chunk, kLpValues values of each lane (places past the end hold -inf), to the lane's sums; vmax: its
@@ -455,9 +462,10 @@ constexpr int kLpCtas = 2;  // a multiprocessor, each lane with two chunks of lo
 // into ranges, one a CTA: `per` units, one more for the first `rest` CTAs.
 // Values before a row's first 16-byte boundary and behind its last vector go
 // with the row's first unit.
-template <int DT>
-__global__ void __launch_bounds__(kLpThreads, kLpCtas)
-    token_logprobs_kernel(LogprobArgs a, int units, long long per, int rest, LpParts out) {
+// With kCluster > 1 a cluster of CTAs shares a row evenly instead, and its first
+// CTA joins the parts.
+template <int DT, int kCluster>
+__device__ __forceinline__ void lp_ranges(const LogprobArgs& a, int units, long long per, int rest, LpParts out) {
     using V = LpVec<DT>;
     constexpr int N = V::N, kLpLoads = kLpValues / N;
     constexpr int size = DT == 3 ? 4 : 2;
@@ -466,19 +474,29 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas)
     __shared__ uint4 buf[kLpWarps][kLpLoads * 32];  // by warp; for keys once a part's values are collected
     __shared__ unsigned slots[kLpWarps];
     static_assert(sizeof(buf) >= sizeof(kept.key), "the keys of a part");
+    __shared__ unsigned long long their_keys[kCluster > 1 ? kCluster * 32 : 1];
+    __shared__ LpPart their_sums[kCluster];
+    if (kCluster > 1) cluster_arrive();
     pdl_wait();
     pdl_trigger();
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, cta = blockIdx.x;
-    long long at = cta * per + min(cta, rest);
-    const long long end = at + per + (cta < rest ? 1 : 0);
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, cta = blockIdx.x, rank = kCluster > 1 ? cta % kCluster : 0;
+    long long at, end;
     int row, u0;
-    if (at >> 32) {
-        row = static_cast<int>(at / units), u0 = static_cast<int>(at % units);
+    if (kCluster > 1) {
+        row = cta / kCluster;
+        u0 = static_cast<int>(static_cast<long long>(rank) * units / kCluster);
+        at = 0, end = static_cast<long long>(rank + 1) * units / kCluster - u0;
     } else {
-        row = static_cast<int>(static_cast<unsigned>(at) / units), u0 = static_cast<int>(static_cast<unsigned>(at) % units);
+        at = cta * per + min(cta, rest);
+        end = at + per + (cta < rest ? 1 : 0);
+        if (at >> 32) {
+            row = static_cast<int>(at / units), u0 = static_cast<int>(at % units);
+        } else {
+            row = static_cast<int>(static_cast<unsigned>(at) / units), u0 = static_cast<int>(static_cast<unsigned>(at) % units);
+        }
+        if (threadIdx.x == 0 && out.open != nullptr) out.open[cta] = make_int2(0, 0);
     }
-    if (threadIdx.x == 0) out.open[cta] = make_int2(0, 0);
-    for (; at < end; ++row, u0 = 0) {
+    for (bool one = kCluster > 1; one || at < end; ++row, u0 = 0, one = false) {
         const int u1 = static_cast<int>(min(static_cast<long long>(units), u0 + (end - at)));
         const char* x = static_cast<const char*>(a.logits) + (long long)row * a.ld * size;
         const int head = min(a.V, static_cast<int>(((16 - (reinterpret_cast<uintptr_t>(x) & 15)) & 15) / size));
@@ -541,7 +559,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas)
 #pragma unroll
             for (int i = 0; i < kLpLoads; ++i) r[i] = ahead[i];
         }
-        if (u0 == 0 && warp == 0 && (head > 0 || tail < a.V)) {
+        if ((kCluster > 1 ? rank == 0 : u0 == 0) && warp == 0 && (head > 0 || tail < a.V)) {
             // fewer than N values at each end: as two values of one vector
 #pragma unroll
             for (int i = 0; i < kLpLoads; ++i) r[i] = make_uint4(V::kNone, V::kNone, V::kNone, V::kNone);
@@ -562,6 +580,25 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas)
             }
             lp_select(kept.key, lists ? kLpKept + kLpThreads : n, a.top, reinterpret_cast<unsigned long long*>(buf), best, lane, warp);
         }
+        if (kCluster > 1) {
+            cluster_wait();  // all its CTAs run
+            if (warp == 0) {
+                // to the first CTA's shared memory
+                if (lane == 0) {
+                    const uint32_t to = cluster_map(smem_u32(&their_sums[rank]), 0);
+                    st_cluster_f32(to, w.p.m), st_cluster_f32(to + 4, w.p.s), st_cluster_f32(to + 8, w.p.t);
+                }
+                if (a.top > 0) st_cluster_u64(cluster_map(smem_u32(&their_keys[rank * 32 + lane]), 0), best[lane]);
+            }
+            cluster_arrive();
+            cluster_wait();
+            if (rank != 0) return;
+            w.p = threadIdx.x < kCluster ? their_sums[threadIdx.x] : LpPart{kLowest, 0.f, 0.f};
+            lp_join_sums(w.p, lane, warp);
+            if (a.top > 0) lp_select(their_keys, kCluster * 32, a.top, reinterpret_cast<unsigned long long*>(buf), best, lane, warp);
+            if (warp == 0) lp_finish<DT>(a, row, w.p, a.top > 0 ? best[lane] : 0ull, lane);
+            return;
+        }
         if (warp == 0) {
             const unsigned long long key = a.top > 0 ? best[lane] : 0ull;
             if (u0 == 0 && u1 == units) {
@@ -580,6 +617,17 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas)
         }
         at += u1 - u0;
     }
+}
+
+template <int DT>
+__global__ void __launch_bounds__(kLpThreads, kLpCtas)
+    token_logprobs_kernel(LogprobArgs a, int units, long long per, int rest, LpParts out) {
+    lp_ranges<DT, 1>(a, units, per, rest, out);
+}
+template <int DT, int kCluster>
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kLpThreads, kLpCtas)
+    token_logprobs_cluster_kernel(LogprobArgs a, int units) {
+    lp_ranges<DT, kCluster>(a, units, 0, 0, LpParts{});
 }
 
 // Short rows: a warp each, with no barrier among the warps.
@@ -656,11 +704,25 @@ __global__ void __launch_bounds__(kLpThreads) token_logprobs_join_kernel(Logprob
     if (warp == 0) lp_finish<DT>(a, row, w.p, a.top > 0 ? best[lane] : 0ull, lane);
 }
 
-// Whether rows go to warps (no workspace) or are cut over CTAs; the launch and the workspace's size both go by it.
-// A warp is slower at a row than a CTA from about 1000 values on (one row of 3000, top 8: 12 us against 6), but
-// many rows keep all warps busy without the CTAs' meetings (3000 rows of 29: 19 against 67 us; 4096 rows of 3000:
-// 32 against 83; 600 rows of 3000: 15 against 22, and 32 against 25 at top 32).
-bool lp_by_rows(int M, int V) { return V <= 1024 || (V <= 4096 && M >= 2 * kLpCtas * kSms); }
+// How rows are dealt out: to warps, to clusters of 1 to 8 CTAs (no workspace), or cut over all CTAs with a join
+// behind; the launch and the workspace's size both go by this.
+//  * A warp is slower at a row than a CTA from about 1000 values on (one row of 3000, top 8: 12 us against 6), but many
+//    rows keep all warps busy (4096 rows of 3000: 32 us against 83 cut over CTAs).
+//  * The largest cluster that all fit the GPU at once (28 of 8 CTAs, 68 of 4; the next ones wait for a second round:
+//    30 rows of 152064 f32 in clusters of 8: 12.4 us, 32: 15.0) and gives each CTA a few thousand values (20000
+//    values in 8: 8.0, in 4: 7.5; 5000 in 2: 8.1, in 1: 6.2).
+//  * Cut over all CTAs, rows need a second kernel, 5 us and more (61 rows of 152064 f32: 20.6 us against 15.1 in
+//    clusters of 4; one: 12.1 against 10.4). That pays where clusters leave most CTAs idle for long (one row of 500000:
+//    12.7 against 15.0), by the rates measured: 31 GB/s a CTA, 213 of them fill the memory; and where the last
+//    round of many long rows would (1000 of 152064 f32: 113 against 120; of 16 bits 105 against 102).
+constexpr int kLpRows = -1, kLpCut = 0;
+int lp_route(int M, int V, int size) {
+    if (V <= 1024 || (V <= 4096 && M >= 2 * kLpCtas * kSms)) return kLpRows;
+    const int c = M <= 28 && V >= 30000 ? 8 : M <= 68 && V >= 10000 ? 4 : M <= kSms && V >= 30000 ? 2 : 1;
+    const double bytes = static_cast<double>(V) * size;
+    if (M > kLpCtas * kSms ? bytes > 400e3 : bytes * (1. / c - M / 213.) > 155e3) return kLpCut;
+    return c;
+}
 
 struct LpPlan {
     int units, ctas, rest, most_parts;
@@ -686,13 +748,29 @@ LpPlan lp_plan(int M, int V, int dtype) {
 
 template <int DT>
 cudaError_t launch_dt(const LogprobArgs& a, void* ws, cudaStream_t s) {
-    if (lp_by_rows(a.M, a.V)) {
+    const int route = lp_route(a.M, a.V, DT == 3 ? 4 : 2);
+    if (route == kLpRows) {
         const int ctas = std::min(kLpCtas * kSms, (a.M + kLpWarps - 1) / kLpWarps);
         void* args[] = {const_cast<LogprobArgs*>(&a)};
         return launch_kernel(reinterpret_cast<const void*>(token_logprobs_rows_kernel<DT>), dim3(ctas), dim3(kLpThreads), 0, true,
                              s, args);
     }
     LpPlan p = lp_plan(a.M, a.V, DT);
+    if (route > 1) {
+        void* args[] = {const_cast<LogprobArgs*>(&a), &p.units};
+        const void* f = route == 8   ? reinterpret_cast<const void*>(token_logprobs_cluster_kernel<DT, 8>)
+                        : route == 4 ? reinterpret_cast<const void*>(token_logprobs_cluster_kernel<DT, 4>)
+                                     : reinterpret_cast<const void*>(token_logprobs_cluster_kernel<DT, 2>);
+        return launch_kernel(f, dim3(a.M * route), dim3(kLpThreads), 0, true, s, args);
+    }
+    if (route == 1) {  // ranges of a row each
+        LpParts none{};
+        long long per = p.units;
+        int rest = 0;
+        void* args[] = {const_cast<LogprobArgs*>(&a), &p.units, &per, &rest, &none};
+        return launch_kernel(reinterpret_cast<const void*>(token_logprobs_kernel<DT>), dim3(a.M), dim3(kLpThreads), 0, true, s,
+                             args);
+    }
     LpParts parts{static_cast<LpRecord*>(ws), reinterpret_cast<int2*>(static_cast<LpRecord*>(ws) + 2 * p.ctas)};
     void* args[] = {const_cast<LogprobArgs*>(&a), &p.units, &p.per, &p.rest, &parts};
     cudaError_t e = launch_kernel(reinterpret_cast<const void*>(token_logprobs_kernel<DT>), dim3(p.ctas), dim3(kLpThreads), 0,
@@ -706,7 +784,7 @@ cudaError_t launch_dt(const LogprobArgs& a, void* ws, cudaStream_t s) {
 }  // namespace
 
 size_t token_logprobs_ws_bytes(int M, int V) {
-    if (lp_by_rows(M, V)) return 0;
+    if (lp_route(M, V, 4) != kLpCut) return 0;  // nor do 16-bit rows, half as long, go by it then
     return static_cast<size_t>(lp_plan(M, V, 3).ctas) * (2 * sizeof(LpRecord) + sizeof(int2));
 }
 

@@ -73,6 +73,38 @@ def test_last_row_in_more_parts_than_an_even_share(dtype, M, V):
     run_and_check(native, torch.from_numpy(x).to(DT[dtype]).cuda(), rng.integers(0, V, (M, 2)), 32)
 
 
+@pytest.mark.parametrize("dtype,M,V", [("f32", 1, 500000), ("bf16", 2, 900001), ("f32", 5, 393693), ("bf16", 28, 30001),
+                                       ("f16", 29, 30003), ("f32", 68, 10007), ("bf16", 69, 10005), ("f16", 100, 31000),
+                                       ("f16", 153, 31001), ("f32", 306, 6000)])
+def test_every_way_rows_are_dealt_out(dtype, M, V):
+    """Cut over all CTAs, in clusters of 8, 4 and 2, one a CTA; rows on every
+    alignment, their largest values at both ends and in the middle."""
+    native = _native()
+    rng = np.random.default_rng(39)
+    x = rng.standard_normal((M, V + 1)) * 3
+    for at in (0, 3, V // 2, V - 2, V - 1):
+        x[:, at] += 12 + rng.standard_normal(M)
+    x = torch.from_numpy(x).to(DT[dtype]).cuda()[:, :V]
+    ids = rng.integers(0, V, (M, 2))
+    a, b = run_and_check(native, x, ids, 32), run_and_check(native, x, ids, 32)
+    for k in a:
+        assert torch.equal(a[k], b[k])
+    run_and_check(native, x, None, 0)
+
+
+def test_many_long_rows():
+    native = _native()
+    gen = torch.Generator(device="cuda").manual_seed(40)
+    M, V = 306, 100500
+    x = torch.randn((M, V), generator=gen, device="cuda") * 3
+    r = native.token_logprobs(x, torch.zeros(M, dtype=torch.int32, device="cuda"), 5)
+    lp = torch.log_softmax(x.double(), 1)
+    assert float((r["logprobs"] - lp[:, 0]).abs().max()) <= 2.0 ** -18
+    assert float((r["entropy"] + (lp.exp() * lp).sum(1)).abs().max()) <= 2.0 ** -16
+    want = torch.topk(x, 5, 1).indices
+    assert torch.equal(torch.gather(x, 1, r["top_ids"].long()), torch.gather(x, 1, want))
+
+
 @pytest.mark.parametrize("dtype", ["f16", "bf16", "f32"])
 def test_rows_that_start_anywhere(dtype):
     """Rows a stride apart that leaves them on every alignment, what lies

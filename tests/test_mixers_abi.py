@@ -76,9 +76,9 @@ def test_delta_rule_validation():
 
 def test_token_logprobs_validation():
     native, L = _lib()
-    need = L.escha_token_logprobs_workspace(1, 152064)
+    need = L.escha_token_logprobs_workspace(1, 500000)
     assert need > 0 and L.escha_token_logprobs_workspace(1, 100) == 0
-    base = dict(x=G, dt=native.ESCHA_F32, M=1, V=152064, ld=152064, ids=G, n=1, top=5, lp=G, ent=G, lse=G, ti=G, tl=G,
+    base = dict(x=G, dt=native.ESCHA_F32, M=1, V=500000, ld=500000, ids=G, n=1, top=5, lp=G, ent=G, lse=G, ti=G, tl=G,
                 ws=G, wsb=need, s=None)
 
     def call(**kw):
@@ -87,7 +87,7 @@ def test_token_logprobs_validation():
     E = native
     for code, kw in ((E.ESCHA_E_ARG, dict(x=None)), (E.ESCHA_E_ARG, dict(dt=4)), (E.ESCHA_E_ARG, dict(M=0)),
                      (E.ESCHA_E_ARG, dict(V=0)), (E.ESCHA_E_SHAPE, dict(V=(1 << 30) + 1)),
-                     (E.ESCHA_E_SHAPE, dict(ld=152063)), (E.ESCHA_E_ARG, dict(n=-1)), (E.ESCHA_E_ARG, dict(n=1025)),
+                     (E.ESCHA_E_SHAPE, dict(ld=499999)), (E.ESCHA_E_ARG, dict(n=-1)), (E.ESCHA_E_ARG, dict(n=1025)),
                      (E.ESCHA_E_ARG, dict(top=33)), (E.ESCHA_E_ARG, dict(top=-1)), (E.ESCHA_E_ARG, dict(V=4, top=5)),
                      (E.ESCHA_E_ARG, dict(ids=None)), (E.ESCHA_E_ARG, dict(lp=None)), (E.ESCHA_E_ARG, dict(ti=None)),
                      (E.ESCHA_E_ARG, dict(n=0, top=0, ent=None, lse=None)), (E.ESCHA_E_ALIGN, dict(x=G + 4)),

@@ -13,16 +13,17 @@
 // Bound: the one read of K and V (a key is used by Hq / Hkv heads: at most 4 x
 // 16 flops a byte). So the layout serves the loads:
 //   * A unit is one (sequence, key head, up to 8 NT query heads); its keys are
-//     taken in rounds of 64, 16 a warp. All units' rounds, in order, are cut
-//     into equal ranges, one a CTA: however ragged the lengths, every
-//     multiprocessor reads the same number of bytes. A unit that lies in one
-//     range is finished by its CTA; the parts of the others go to the
-//     workspace, at most two a CTA, and are joined by a second kernel.
+//     taken in rounds of 64, 16 a warp. A cluster of 1 to 8 CTAs takes a unit,
+//     each a run of its rounds, and joins the parts through shared memory. Where
+//     the units are few and long, all units' rounds are cut into equal ranges,
+//     one a CTA, instead, and the parts joined by a second kernel (pa_route).
 //   * Each warp fills its own ring of 16-key stages (cp.async, 16 bytes a lane,
 //     rows of the pages wherever they are) and waits for nobody else. Rows that
 //     are not there are filled with zeros and masked.
 //   * Keys are the M of both products (scores K Q^T, values V^T P^T: m16n8k16),
 //     so that 8 query heads fill the instruction's N exactly.
+// Measured: 192 sequences of 500 to 16384 keys, 2 key heads of 256: 285 us, 6.6
+// TB/s; one of 131071: 53 us, 5.1 TB/s; one of 700: 9.9 us.
 #include "common.cuh"
 #include "context.h"
 #include "kernels.h"
@@ -40,11 +41,11 @@ constexpr float kPaUp = DT == 1 ? 0x1p15f : 1.f;  // of a weight's parts
 // A warp's ring holds kHalves halves of stages (16 keys, or their 16 values).
 template <int D, int NT>
 struct PaCfg {
-    static constexpr int kWarps = D == 256 ? 8 : 4;
+    static constexpr int kWarps = 4;
     static constexpr int kThreads = kWarps * 32;
     static constexpr int kRound = 16 * kWarps;  // keys of a round
     static constexpr int kHalves = D == 256 ? 3 : D == 128 ? 4 : 6;
-    static constexpr int kCtas = D == 256 ? 1 : D == 128 ? (NT == 1 ? 3 : 2) : (NT == 1 ? 4 : 3);  // a multiprocessor
+    static constexpr int kCtas = D == 256 ? 2 : D == 128 ? (NT == 1 ? 3 : 2) : (NT == 1 ? 4 : 3);  // a multiprocessor
     static constexpr int kRow = D * 2;          // bytes of a row
     static constexpr int kTile = 16 * kRow;     // of a half
     static constexpr int kRing = kWarps * kHalves * kTile;
@@ -122,17 +123,27 @@ __device__ __forceinline__ int pa_len(const PagedAttnArgs& a, int b) {
     return max(0, min(a.lens[b], most));
 }
 
-// One part of a unit: 8 NT heads' weighted values, then their maxima and sums.
+// The parts of units cut over CTAs: 8 NT heads' weighted values, then their maxima and sums.
 struct PaParts {
-    float* acc;  // [2 G][heads][D]
-    float* ml;   // [2 G][2][heads]
-    // Units that begin in one CTA's range and end in another's: sequence, unit of the sequence, first CTA and number of
-    // parts (0: not such a unit). By unit, where there are no more units than CTAs; else one place a CTA, as no more
-    // than one such unit begins in its range. The join's grid is as large: 8 x 456 CTAs that mostly find nothing took 4 us.
-    int4* open;
-    int by_unit;
+    float* acc;  // [2 CTAs][heads][D]: a CTA's first part of a unit begun before its range, its part of one that goes on
+    float* ml;   // [2 CTAs][2][heads]
+    int4* open;  // by unit: sequence, unit of the sequence, first CTA and number of parts (0: finished, or no keys)
 };
 
+__device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
+    float v;
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(addr) : "memory");
+    return v;
+}
+__device__ __forceinline__ float2 ld_cluster_f32x2(uint32_t addr) {
+    float2 v;
+    asm volatile("ld.shared::cluster.v2.f32 {%0, %1}, [%2];" : "=f"(v.x), "=f"(v.y) : "r"(addr) : "memory");
+    return v;
+}
+
+// Up to so many sequences are taken longest first, where they are more than the GPU holds at once (31 of 130 to 8000
+// keys, 4 key heads: 41 -> 34 us); finding their order among 192 costs each CTA more than it gives.
+constexpr int kPaSort = 64;
 // A place in the list of rounds: round r of one (sequence, key head, tile of heads).
 struct PaPlace {
     int b, kvh, tile, r, rounds, len;
@@ -155,9 +166,10 @@ struct PaPlace {
     }
 };
 
-template <int DT, int D, int NT>
-__global__ void __launch_bounds__(PaCfg<D, NT>::kThreads, PaCfg<D, NT>::kCtas)
-    paged_attention_kernel(PagedAttnArgs a, int tiles, PaDiv div, PaParts parts) {
+// kCluster > 0: a cluster of so many CTAs takes one unit. 0: all units' rounds
+// in equal ranges.
+template <int DT, int D, int NT, int kCluster>
+__device__ __forceinline__ void pa_units(const PagedAttnArgs& a, int tiles, const PaDiv& div, const PaParts& parts) {
     using C = PaCfg<D, NT>;
     constexpr int kHeads = 8 * NT, kHalves = C::kHalves, kTile = C::kTile, kKs = D / 16, kRound = C::kRound;
     constexpr int kWarps = C::kWarps, kThreads = C::kThreads;
@@ -165,62 +177,91 @@ __global__ void __launch_bounds__(PaCfg<D, NT>::kThreads, PaCfg<D, NT>::kCtas)
     __shared__ long long scan[kWarps];
     __shared__ int first_s[4];
     __shared__ float sm_m[kWarps][kHeads], sm_l[kWarps][kHeads];
+    __shared__ float part_m[kHeads], part_l[kHeads];  // of a cluster's CTA
     pdl_wait();
     pdl_trigger();
     const int t = threadIdx.x, lane = t & 31, warp = t >> 5, g = lane >> 2, q4 = lane & 3;
+    constexpr int kShare = kCluster > 0 ? kCluster : 1;
+    const int rank = blockIdx.x % kShare;
     const int units = a.Hkv * tiles, group = a.Hq / a.Hkv;
 
     // ---- this CTA's range of the rounds
-    const int per = (a.B + kThreads - 1) / kThreads;
-    const int b0 = t * per, b1 = min(a.B, b0 + per);
-    long long mine = 0;
-    for (int b = b0; b < b1; ++b) mine += (long long)((pa_len(a, b) + kRound - 1) / kRound) * units;
-    long long incl = mine;
-#pragma unroll
-    for (int m = 1; m < 32; m <<= 1) {
-        const long long o = __shfl_up_sync(0xffffffffu, incl, m);
-        if (lane >= m) incl += o;
-    }
-    if (lane == 31) scan[warp] = incl;
-    __syncthreads();
-    long long before = 0, total = 0;
-#pragma unroll
-    for (int w = 0; w < kWarps; ++w) {
-        if (w < warp) before += scan[w];
-        total += scan[w];
-    }
-    // every CTA that takes part has a round at least (the join counts on it)
-    const long long ctas = min(static_cast<long long>(gridDim.x), total);
-    if (t == 0 && !parts.by_unit) parts.open[blockIdx.x] = make_int4(0, 0, 0, 0);
-    // the sequences without keys
-    for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
-        if (pa_len(a, b) > 0) continue;
-        if (parts.by_unit)
-            for (int i = t; i < units; i += kThreads) parts.open[b * units + i] = make_int4(0, 0, 0, 0);
-        for (int i = t; i < a.Hq * D / 2; i += kThreads) static_cast<uint32_t*>(a.out)[(long long)b * a.Hq * D / 2 + i] = 0u;
-        if (a.lse)
-            for (int i = t; i < a.Hq; i += kThreads) a.lse[(long long)b * a.Hq + i] = -INFINITY;
-    }
-    if (blockIdx.x >= ctas) return;
-    const long long lo = blockIdx.x * total / ctas;
-    const long long left = (blockIdx.x + 1) * total / ctas - lo;
-    long long x0 = before + incl - mine;
-    if (lo >= x0 && lo < x0 + mine) {
-        for (int b = b0; b < b1; ++b) {
-            const int len = pa_len(a, b), rounds = (len + kRound - 1) / kRound;
-            const long long n = (long long)rounds * units;
-            if (lo < x0 + n) {
-                first_s[0] = b, first_s[1] = static_cast<int>((lo - x0) / rounds);
-                first_s[2] = static_cast<int>((lo - x0) % rounds), first_s[3] = len;
-                break;
-            }
-            x0 += n;
-        }
-    }
-    __syncthreads();
     PaPlace cur;
-    cur.b = first_s[0], cur.kvh = first_s[1] / tiles, cur.tile = first_s[1] % tiles, cur.r = first_s[2], cur.len = first_s[3];
-    cur.rounds = (cur.len + kRound - 1) / kRound;
+    long long lo = 0, left, total = 0, ctas = 0;
+    if (kCluster > 0) {
+        const int unit = blockIdx.x / kShare;
+        cur.b = unit / units, cur.kvh = unit % units / tiles, cur.tile = unit % tiles;
+        if (a.B > 1 && a.B <= kPaSort && gridDim.x > kSms * C::kCtas) {
+            int* lens = reinterpret_cast<int*>(smem);  // (the ring is not in use yet)
+            const int all = (a.B + 3) & ~3;
+            if (t < all) lens[t] = t < a.B ? pa_len(a, t) : -1;
+            __syncthreads();
+            if (t < a.B) {
+                const int n = lens[t];
+                int before = 0;
+                for (int j = 0; j < all; j += 4) {
+                    const int4 o = *reinterpret_cast<const int4*>(&lens[j]);
+                    before += (o.x > n || (o.x == n && j < t)) + (o.y > n || (o.y == n && j + 1 < t)) +
+                              (o.z > n || (o.z == n && j + 2 < t)) + (o.w > n || (o.w == n && j + 3 < t));
+                }
+                if (before == cur.b) first_s[0] = t;
+            }
+            __syncthreads();
+            cur.b = first_s[0];
+        }
+        cur.len = pa_len(a, cur.b);
+        cur.rounds = (cur.len + kRound - 1) / kRound;
+        cur.r = static_cast<int>(static_cast<long long>(cur.rounds) * rank / kShare);
+        left = static_cast<long long>(cur.rounds) * (rank + 1) / kShare - cur.r;
+    } else {
+        const int per = (a.B + kThreads - 1) / kThreads;
+        const int b0 = t * per, b1 = min(a.B, b0 + per);
+        long long mine = 0;
+        for (int b = b0; b < b1; ++b) mine += (long long)((pa_len(a, b) + kRound - 1) / kRound) * units;
+        long long incl = mine;
+#pragma unroll
+        for (int m = 1; m < 32; m <<= 1) {
+            const long long o = __shfl_up_sync(0xffffffffu, incl, m);
+            if (lane >= m) incl += o;
+        }
+        if (lane == 31) scan[warp] = incl;
+        __syncthreads();
+        long long before = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) {
+            if (w < warp) before += scan[w];
+            total += scan[w];
+        }
+        // every CTA that takes part has a round at least (the join counts on it)
+        ctas = min(static_cast<long long>(gridDim.x), total);
+            // the sequences without keys
+        for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
+            if (pa_len(a, b) > 0) continue;
+            for (int i = t; i < units; i += kThreads) parts.open[b * units + i] = make_int4(0, 0, 0, 0);
+            for (int i = t; i < a.Hq * D / 2; i += kThreads) static_cast<uint32_t*>(a.out)[(long long)b * a.Hq * D / 2 + i] = 0u;
+            if (a.lse)
+                for (int i = t; i < a.Hq; i += kThreads) a.lse[(long long)b * a.Hq + i] = -INFINITY;
+        }
+        if (blockIdx.x >= ctas) return;
+        lo = blockIdx.x * total / ctas;
+        left = (blockIdx.x + 1) * total / ctas - lo;
+        long long x0 = before + incl - mine;
+        if (lo >= x0 && lo < x0 + mine) {
+            for (int b = b0; b < b1; ++b) {
+                const int len = pa_len(a, b), rounds = (len + kRound - 1) / kRound;
+                const long long n = (long long)rounds * units;
+                if (lo < x0 + n) {
+                    first_s[0] = b, first_s[1] = static_cast<int>((lo - x0) / rounds);
+                    first_s[2] = static_cast<int>((lo - x0) % rounds), first_s[3] = len;
+                    break;
+                }
+                x0 += n;
+            }
+        }
+        __syncthreads();
+        cur.b = first_s[0], cur.kvh = first_s[1] / tiles, cur.tile = first_s[1] % tiles, cur.r = first_s[2], cur.len = first_s[3];
+        cur.rounds = (cur.len + kRound - 1) / kRound;
+    }
 
     // ---- the warp's ring
     const uint32_t ring = static_cast<uint32_t>(__cvta_generic_to_shared(smem)) + warp * kHalves * kTile;
@@ -294,6 +335,7 @@ __global__ void __launch_bounds__(PaCfg<D, NT>::kThreads, PaCfg<D, NT>::kCtas)
     bool begin = true;
     int piece_r0 = 0, h0 = 0, nh = 0;
     const float sc = a.scale * kLog2e;
+    float* part = reinterpret_cast<float*>(smem + C::kRing);  // of a cluster's CTA
     uint32_t from = ring;
     for (long long i = 0; i < left; ++i) {
         if (begin) {
@@ -452,7 +494,7 @@ __global__ void __launch_bounds__(PaCfg<D, NT>::kThreads, PaCfg<D, NT>::kCtas)
                 }
                 __syncthreads();
             }
-            const bool whole = last && piece_r0 == 0;
+            const bool whole = kCluster == 0 && last && piece_r0 == 0;
             const long long slot = 2ll * blockIdx.x + (piece_r0 == 0 ? 1 : 0);
             for (int at = t * 2; at < nh * D; at += kThreads * 2) {
                 const int h = at / D;
@@ -470,6 +512,8 @@ __global__ void __launch_bounds__(PaCfg<D, NT>::kThreads, PaCfg<D, NT>::kCtas)
                     const float inv = sum == 0.f ? 0.f : 1.f / sum;
                     *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + ((long long)cur.b * a.Hq + h0) * D + at) =
                         pa_pack<DT>(v0 * inv, v1 * inv);
+                } else if (kCluster > 0) {
+                    *reinterpret_cast<float2*>(part + at) = make_float2(v0, v1);
                 } else {
                     *reinterpret_cast<float2*>(parts.acc + slot * kHeads * D + at) = make_float2(v0, v1);
                 }
@@ -482,12 +526,14 @@ __global__ void __launch_bounds__(PaCfg<D, NT>::kThreads, PaCfg<D, NT>::kCtas)
                 for (int w = 0; w < kWarps; ++w) sum += sm_l[w][t] * ex2(sm_m[w][t] - (top == -INFINITY ? 0.f : top));
                 if (whole) {
                     if (a.lse) a.lse[(long long)cur.b * a.Hq + h0 + t] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+                } else if (kCluster > 0) {
+                    part_m[t] = top, part_l[t] = sum;
                 } else {
                     parts.ml[(slot * 2) * kHeads + t] = top;
                     parts.ml[(slot * 2 + 1) * kHeads + t] = sum;
                 }
             }
-            if (t == 0 && piece_r0 == 0 && (!last || parts.by_unit)) {
+            if (kCluster == 0 && t == 0 && piece_r0 == 0) {
                 const int u = cur.kvh * tiles + cur.tile;
                 int n = 0;
                 if (!last) {
@@ -495,13 +541,66 @@ __global__ void __launch_bounds__(PaCfg<D, NT>::kThreads, PaCfg<D, NT>::kCtas)
                     const long long end = lo + i + (cur.rounds - 1 - cur.r);
                     n = static_cast<int>(((end + 1) * ctas - 1) / total) - static_cast<int>(blockIdx.x) + 1;
                 }
-                parts.open[parts.by_unit ? cur.b * units + u : blockIdx.x] = make_int4(cur.b, u, blockIdx.x, n);
+                parts.open[cur.b * units + u] = make_int4(cur.b, u, blockIdx.x, n);
             }
             __syncthreads();
             begin = true;
         }
-        cur.template next<kRound>(a, tiles);
+        if (kCluster == 0) cur.template next<kRound>(a, tiles);
+        else ++cur.r;
     }
+    if (kCluster == 0) return;
+
+    // ---- the unit's parts: each CTA finishes a share of the values
+    h0 = cur.kvh * group + cur.tile * kHeads;
+    nh = min(kHeads, group - cur.tile * kHeads);
+    if (left == 0) {
+        for (int i = t; i < nh * D; i += kThreads) part[i] = 0.f;
+        if (t < nh) part_m[t] = -INFINITY, part_l[t] = 0.f;
+    }
+    __syncthreads();
+    if (kCluster > 1) {
+        cluster_arrive();
+        cluster_wait();
+    }
+    const int each = nh * D / kShare;
+    for (int i = t * 2; i < each; i += kThreads * 2) {
+        const int at = rank * each + i, h = at / D;
+        float pm[kShare], pl[kShare], top = -INFINITY, sum = 0.f, v0 = 0.f, v1 = 0.f;
+        float2 pv[kShare];
+#pragma unroll
+        for (int c = 0; c < kShare; ++c) {
+            pm[c] = ld_cluster_f32(cluster_map(smem_u32(&part_m[h]), c));
+            pl[c] = ld_cluster_f32(cluster_map(smem_u32(&part_l[h]), c));
+            pv[c] = ld_cluster_f32x2(cluster_map(smem_u32(part + at), c));
+        }
+#pragma unroll
+        for (int c = 0; c < kShare; ++c) top = fmaxf(top, pm[c]);
+#pragma unroll
+        for (int c = 0; c < kShare; ++c) {
+            const float f = ex2(pm[c] - (top == -INFINITY ? 0.f : top));
+            sum += pl[c] * f, v0 += pv[c].x * f, v1 += pv[c].y * f;
+        }
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        *reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + ((long long)cur.b * a.Hq + h0) * D + at) =
+            pa_pack<DT>(v0 * inv, v1 * inv);
+        if (a.lse && at % D == 0) a.lse[(long long)cur.b * a.Hq + h0 + h] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+    }
+    if (kCluster > 1) {
+        cluster_arrive();  // no CTA leaves while another reads its part
+        cluster_wait();
+    }
+}
+
+template <int DT, int D, int NT>
+__global__ void __launch_bounds__(PaCfg<D, NT>::kThreads, PaCfg<D, NT>::kCtas)
+    paged_attention_kernel(PagedAttnArgs a, int tiles, PaDiv div, PaParts parts) {
+    pa_units<DT, D, NT, 0>(a, tiles, div, parts);
+}
+template <int DT, int D, int NT, int kCluster>
+__global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(PaCfg<D, NT>::kThreads, PaCfg<D, NT>::kCtas)
+    paged_attention_cluster_kernel(PagedAttnArgs a, int tiles, PaDiv div) {
+    pa_units<DT, D, NT, kCluster>(a, tiles, div, PaParts{});
 }
 
 // Joins the parts of one query head of a unit that lies in several CTAs'
@@ -569,15 +668,30 @@ __global__ void __launch_bounds__(kPaSets* D / 4) paged_attention_join_kernel(Pa
     if (t == 0 && a.lse) a.lse[h] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
 }
 
+// CTAs of a unit's cluster, or 0: units are cut over all CTAs and joined by a second kernel. `ctas`: what the GPU holds at
+// once. A round takes 0.9 us in a CTA alone on its multiprocessor, a CTA 4 us besides, the second kernel 5.
+//  * Few long units cannot fill the GPU by 8 CTAs each: one of 4 key heads of 128 and 12000 keys takes 13 us cut over
+//    all, 25 in clusters; of 3000 keys 10 and 9.1; 8 such sequences of 12000 keys 40 and 37.
+//  * More CTAs a unit even out ragged lengths and shorten the longest unit; each costs its start (64 sequences of 4 key
+//    heads in clusters of 1, 2, 4, 8: up to 700 keys 18, 24, 27, 42 us; up to 3000 55, 40, 41, 57; up to 12000 203,
+//    138, 109, 131). Fewer than half the places are worth filling up (16 sequences of 700: 13, 9.7, 8.5, 14).
+int pa_route(long long units, int rounds, int ctas) {
+    if (16 * units <= ctas && rounds > 64) return 0;
+    const int most = units * 5 <= ctas * 2 ? 8 : units * 2 <= ctas * 3 ? 4 : 2;
+    int c = rounds <= 12 ? 1 : rounds <= 40 ? 2 : rounds <= 80 ? 4 : 8;
+    while (c < 8 && c < rounds && units * c * 2 < ctas) c *= 2;
+    return c < most ? c : most;
+}
 struct PaPlan {
-    int nt, heads, tiles, ctas;
+    int nt, heads, tiles, ctas, cluster;
+    long long units;
     size_t acc, ml, open, total;
 };
 template <int D>
 int pa_ctas(int nt) {
     return kSms * (nt == 1 ? PaCfg<D, 1>::kCtas : PaCfg<D, 2>::kCtas);
 }
-PaPlan pa_plan(int Hq, int Hkv, int d) {
+PaPlan pa_plan(int B, int Hq, int Hkv, int d, int max_len) {
     PaPlan p{};
     const int group = Hq / Hkv;
     // 16 heads of 256 values would not fit the registers: at dimension 256 a unit has 8 heads, and a second one reads the
@@ -586,10 +700,13 @@ PaPlan pa_plan(int Hq, int Hkv, int d) {
     p.heads = 8 * p.nt;
     p.tiles = (group + p.heads - 1) / p.heads;
     p.ctas = d == 256 ? pa_ctas<256>(p.nt) : d == 128 ? pa_ctas<128>(p.nt) : pa_ctas<64>(p.nt);
+    p.units = (long long)B * Hkv * p.tiles;
+    p.cluster = pa_route(p.units, (max_len + 63) / 64, p.ctas);
+    if (p.cluster) return p;
     p.acc = 0;
     p.ml = p.acc + static_cast<size_t>(2) * p.ctas * p.heads * d * 4;
     p.open = p.ml + static_cast<size_t>(2) * p.ctas * 2 * p.heads * 4;
-    p.total = p.open + static_cast<size_t>(p.ctas) * sizeof(int4);
+    p.total = p.open + static_cast<size_t>(p.units) * sizeof(int4);
     return p;
 }
 PaDiv pa_div(int d) {
@@ -601,18 +718,24 @@ PaDiv pa_div(int d) {
 template <int DT, int D, int NT>
 cudaError_t launch_nt(const PagedAttnArgs& a, const PaPlan& p, const PaParts& parts, cudaStream_t s) {
     using C = PaCfg<D, NT>;
-    const void* f = reinterpret_cast<const void*>(paged_attention_kernel<DT, D, NT>);
+    const void* f = p.cluster == 8   ? reinterpret_cast<const void*>(paged_attention_cluster_kernel<DT, D, NT, 8>)
+                    : p.cluster == 4 ? reinterpret_cast<const void*>(paged_attention_cluster_kernel<DT, D, NT, 4>)
+                    : p.cluster == 2 ? reinterpret_cast<const void*>(paged_attention_cluster_kernel<DT, D, NT, 2>)
+                    : p.cluster == 1 ? reinterpret_cast<const void*>(paged_attention_cluster_kernel<DT, D, NT, 1>)
+                                     : reinterpret_cast<const void*>(paged_attention_kernel<DT, D, NT>);
     cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
     if (e != cudaSuccess) return e;
     int tiles = p.tiles, heads = p.heads;
     PaDiv div = pa_div(a.page);
     void* args[] = {const_cast<PagedAttnArgs*>(&a), &tiles, &div, const_cast<PaParts*>(&parts)};
-    e = launch_kernel(f, dim3(p.ctas), dim3(C::kThreads), C::kSmem, true, s, args);
-    if (e != cudaSuccess || a.max_len <= C::kRound) return e;  // units of one round are never cut
+    // 65535 sequences, 1024 key heads, 8 tiles, 2 CTAs (with so many units): below 2^31
+    const unsigned grid = static_cast<unsigned>(p.cluster ? p.units * p.cluster : p.ctas);
+    e = launch_kernel(f, dim3(grid), dim3(C::kThreads), C::kSmem, true, s, args);
+    if (e != cudaSuccess || p.cluster) return e;
     void* jargs[] = {const_cast<PagedAttnArgs*>(&a), &tiles, &heads, const_cast<PaParts*>(&parts)};
-    const int group = a.Hq / a.Hkv, places = parts.by_unit ? a.B * a.Hkv * tiles : p.ctas;
-    return launch_kernel(reinterpret_cast<const void*>(paged_attention_join_kernel<DT, D>), dim3(heads < group ? heads : group, places),
-                         dim3(kPaSets * D / 4), 0, true, s, jargs);
+    const int group = a.Hq / a.Hkv;
+    return launch_kernel(reinterpret_cast<const void*>(paged_attention_join_kernel<DT, D>),
+                         dim3(heads < group ? heads : group, static_cast<unsigned>(p.units)), dim3(kPaSets * D / 4), 0, true, s, jargs);
 }
 
 template <int DT>
@@ -624,16 +747,12 @@ cudaError_t launch_dt(const PagedAttnArgs& a, const PaPlan& p, const PaParts& pa
 
 }  // namespace
 
-size_t paged_attention_ws_bytes(int B, int Hq, int Hkv, int d, int max_len) {
-    (void)B, (void)max_len;
-    return pa_plan(Hq, Hkv, d).total;
-}
+size_t paged_attention_ws_bytes(int B, int Hq, int Hkv, int d, int max_len) { return pa_plan(B, Hq, Hkv, d, max_len).total; }
 
 cudaError_t launch_paged_attention(const PagedAttnArgs& a, int dtype, void* ws, cudaStream_t s) {
-    const PaPlan p = pa_plan(a.Hq, a.Hkv, a.d);
+    const PaPlan p = pa_plan(a.B, a.Hq, a.Hkv, a.d, a.max_len);
     char* w = static_cast<char*>(ws);
-    const PaParts parts{reinterpret_cast<float*>(w + p.acc), reinterpret_cast<float*>(w + p.ml),
-                        reinterpret_cast<int4*>(w + p.open), (long long)a.B * a.Hkv * p.tiles <= p.ctas};
+    const PaParts parts{reinterpret_cast<float*>(w + p.acc), reinterpret_cast<float*>(w + p.ml), reinterpret_cast<int4*>(w + p.open)};
     return dtype == 1 ? launch_dt<1>(a, p, parts, s) : launch_dt<2>(a, p, parts, s);
 }
 

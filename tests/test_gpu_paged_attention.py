@@ -74,6 +74,14 @@ SHAPES = [
     ("bf16", [1000], 16, 2, 256, 64), ("f16", [700, 699], 3, 3, 64, 48), ("bf16", [40, 513], 22, 2, 64, 32),
     ("f16", [257, 31], 64, 1, 64, 128), ("bf16", [33, 2000, 1], 24, 1, 128, 256), ("f16", [4097], 6, 2, 128, 1024),
     ("bf16", [500] * 9 + [0] * 3, 16, 4, 64, 16),
+    # units cut over all CTAs
+    ("bf16", [9000, 0, 5], 24, 1, 128, 32), ("f16", [5000, 130], 64, 2, 64, 48), ("f16", [4500, 4500, 1], 10, 2, 256, 64),
+    # clusters of 4, 2 and 1, longest first and not
+    ("bf16", [3000, 17, 2900] + [64 * (i % 5) + i for i in range(57)], 8, 4, 128, 64),
+    ("bf16", [(i * 37) % 300 for i in range(59)] + [1500], 12, 4, 128, 32),
+    ("f16", [700] + [i * 11 for i in range(59)], 4, 4, 128, 16),
+    ("f16", [900] + [(i * 53) % 200 for i in range(99)], 16, 8, 64, 64), ("bf16", [(i * 29) % 131 for i in range(70)], 16, 16, 64, 16),
+    ("f16", [40, 1300] * 16, 32, 4, 256, 64),
 ]
 
 
@@ -241,4 +249,8 @@ def test_refusals():
     bad(native.EschaError, scale=float("nan"))
     bad(native.EschaError, q=c["q"][:, :3].contiguous())
     bad(native.EschaError, max_len=0)
-    bad(native.EschaError, ws=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    bad(ValueError, ws=torch.empty(16, device="cuda"))
+    wide = torch.zeros((1, 200), dtype=torch.int32, device="cuda")  # long enough to need a workspace
+    one = make(19, [40], 4, 2, 64, 32, "f16")
+    with pytest.raises(native.EschaError, match="workspace"):
+        native.paged_attention(one["q"], one["k"], one["v"], wide, one["lens"], ws=torch.empty(16, dtype=torch.uint8, device="cuda"))

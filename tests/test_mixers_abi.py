@@ -41,10 +41,11 @@ def test_paged_attention_validation():
                      (E.ESCHA_E_ALIGN, dict(q=G + 8)), (E.ESCHA_E_ALIGN, dict(lens=G + 4)),
                      (E.ESCHA_E_ALIGN, dict(lse=G + 4)), (E.ESCHA_E_ALIGN, dict(kn=G, vn=G + 2))):
         assert call(**kw) == code, kw
-    if need:
-        assert call(ws=None) == E.ESCHA_E_ARG
-        assert call(wsb=need - 1) == E.ESCHA_E_WORKSPACE
-        assert call(ws=G + 8) == E.ESCHA_E_ALIGN
+    need = L.escha_paged_attention_workspace(2, 16, 2, 256, 100000)
+    assert need > 0
+    assert call(ml=100000, wsb=need, ws=None) == E.ESCHA_E_ARG
+    assert call(ml=100000, wsb=need - 1) == E.ESCHA_E_WORKSPACE
+    assert call(ml=100000, wsb=need, ws=G + 8) == E.ESCHA_E_ALIGN
     assert b"paged_attention" in L.escha_last_error()
     assert L.escha_paged_attention_workspace(2, 16, 2, 100, 1000) == 0
 

@@ -22,8 +22,8 @@
 //     are not there are filled with zeros and masked.
 //   * Keys are the M of both products (scores K Q^T, values V^T P^T: m16n8k16),
 //     so that 8 query heads fill the instruction's N exactly.
-// Measured: 192 sequences of 500 to 16384 keys, 2 key heads of 256: 285 us, 6.6
-// TB/s; one of 131071: 53 us, 5.1 TB/s; one of 700: 9.9 us.
+// Measured: 192 sequences of 500 to 16384 keys, 2 key heads of 256: 282 us, 6.7
+// TB/s; one of 131071: 53 us, 5.1 TB/s; one of 700: 8.7 us.
 #include "common.cuh"
 #include "context.h"
 #include "kernels.h"
@@ -286,16 +286,16 @@ __device__ __forceinline__ void pa_units(const PagedAttnArgs& a, int tiles, cons
         const int newest = a.k_new ? ld.len - 1 - (ld.r * kRound + warp * 16) : -1;  // the new token's row
         if (static_cast<unsigned>(newest) < 16u) {
             const char* nw = static_cast<const char*>(fresh) + ((long long)ld.b * a.Hkv + ld.kvh) * C::kRow + c8 * 16;
-#pragma unroll 1
+            const int there = __shfl_sync(0xffffffffu, row, newest);
+            const bool keep = ld.tile == 0 && rr == 0 && there >= 0;
+            uint4 w;
+            if (keep) w = *reinterpret_cast<const uint4*>(nw);
+#pragma unroll
             for (int i = 0; i < 16; i += kAtOnce) {
                 const int r = i + rr, n = __shfl_sync(0xffffffffu, row, r);
-                const char* src = n >= 0 ? base + (long long)n * C::kRow : base;
-                if (r == newest && n >= 0) {
-                    if (ld.tile == 0) *reinterpret_cast<uint4*>(const_cast<char*>(src)) = *reinterpret_cast<const uint4*>(nw);
-                    src = nw;
-                }
-                cp16(to + r * C::kRow + ((c8 ^ (r & 7)) << 4), src, n >= 0);
+                cp16(to + r * C::kRow + ((c8 ^ (r & 7)) << 4), r == newest ? nw : base + (long long)max(n, 0) * C::kRow, n >= 0);
             }
+            if (keep) *reinterpret_cast<uint4*>(const_cast<char*>(base) + (long long)there * C::kRow) = w;
         } else {
 #pragma unroll
             for (int i = 0; i < 16; i += kAtOnce) {

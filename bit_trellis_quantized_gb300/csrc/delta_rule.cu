@@ -3,10 +3,13 @@
 //   S <- e^g S,  u = beta (v - S^T k),  S <- S + k u^T,  o = scale S^T q,
 // k and q divided by sqrt(sum x^2 + eps) first where eps >= 0.
 //
-// Token by token: a CTA holds [dk][VS] of one state in registers. Both products
-// with the old state, S^T k and S^T q, come from one pass over it and one
-// reduction, as o = scale (e^g S^T q + (k . q) u). Bound, for one token a
-// sequence: the state's read and write.
+// Token by token (delta_step_kernel): a CTA holds [dk][VS] of one state in
+// registers. Both products with the old state, S^T k and S^T q, come from one
+// pass over it and one reduction, as o = scale (e^g S^T q + (k . q) u). Bound,
+// for one token a sequence: the state's read and write (250 states of 32 x 128
+// x 128: 154 us, 6.8 TB/s).
+// From kChunkFrom tokens on, in chunks of 32 (below): a kernel over all chunks,
+// then one that walks them, bound by the latency of that chain.
 #include "common.cuh"
 #include "context.h"
 #include "kernels.h"
@@ -469,10 +472,19 @@ __device__ __forceinline__ unsigned long long dr_mul2(unsigned long long x, floa
 // memory. It hands the operand S^T and U^T to an output warp, which makes
 // S^T Q^T + U^T P^T one chunk later; cp.async fetches the next chunks; all warps
 // meet once a chunk. The chain bounds a long sequence: at 128 x 128 states a
-// chunk takes 1.24 us, 146 tensor instructions of 8 cycles and what lies between
-// them. (2.8 us in one warp that did all of it; 1.4 with the key dimensions
-// halved between two warps, which then meet once more; 2.2 with 8 columns a
-// warp as the right operand, which a transpose within the warp has to make.)
+// chunk takes 1.15 us, some 2400 cycles, of which 152 tensor instructions of 8
+// cycles are half: K S 900, the new state 640, V - ... 320, T 210, U's factors
+// 300, the meeting 120. The tensor pipes are 39% busy over the multiprocessor.
+// Measured and slower: all of it in one warp (2.8 us a chunk); the key
+// dimensions halved between two warps, which then meet once more (1.4); 8
+// columns a warp as the right operand, which a transpose within the warp has to
+// make (2.2); the next chunk's K S from the state before and U, so that only a
+// product of 32 x 32 stays in the chain, beside warps that walk the state (1.24:
+// those become the chain); S split for the next chunk between the products of
+// this one (1.26: an instruction stream of one warp). tcgen05 takes 128 rows at
+// least, all columns of a state, and its results would pass through tensor
+// memory between the four products of the chain: throughput, which many
+// sequences could use, but not a shorter chain.
 template <int kThreads>
 __device__ __forceinline__ void dr_meet() {  // all warps, each from its own loop
     asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");

@@ -23,7 +23,7 @@
 //   * Keys are the M of both products (scores K Q^T, values V^T P^T: m16n8k16),
 //     so that 8 query heads fill the instruction's N exactly.
 // Measured: 192 sequences of 500 to 16384 keys, 2 key heads of 256: 282 us, 6.7
-// TB/s; one of 131071: 53 us, 5.1 TB/s; one of 700: 8.7 us.
+// TB/s; one of 131071: 52 us, 5.2 TB/s; one of 700: 8.4 us.
 #include "common.cuh"
 #include "context.h"
 #include "kernels.h"
@@ -604,13 +604,14 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(PaCfg<D, NT>:
 }
 
 // Joins the parts of one query head of a unit that lies in several CTAs'
-// ranges: CTA (head of the unit, place in `open`), kPaSets interleaved sets of
-// parts with D / 4 threads of four values each.
-constexpr int kPaSets = 8;
+// ranges: CTA (head of the unit, unit, 64 values), kPaSets interleaved sets of
+// parts with 16 threads of four values each. Bound by its chain of loads: what
+// to join, the parts' maxima and sums, the values.
+constexpr int kPaSets = 32, kPaCols = 16;
 static_assert(PaCfg<64, 1>::kCtas <= 4 && PaCfg<128, 1>::kCtas <= 4 && PaCfg<256, 1>::kCtas <= 4, "the join holds a factor a CTA");
 template <int DT, int D>
-__global__ void __launch_bounds__(kPaSets* D / 4) paged_attention_join_kernel(PagedAttnArgs a, int tiles, int heads, PaParts parts) {
-    constexpr int kCols = D / 4, kThreads = kPaSets * kCols, kW = kThreads / 32;
+__global__ void __launch_bounds__(kPaSets* kPaCols) paged_attention_join_kernel(PagedAttnArgs a, int tiles, int heads, PaParts parts) {
+    constexpr int kCols = kPaCols, kThreads = kPaSets * kCols, kW = kThreads / 32;
     __shared__ float4 sums[kPaSets][kCols];
     __shared__ float red[2][kW];
     pdl_wait();
@@ -618,7 +619,7 @@ __global__ void __launch_bounds__(kPaSets* D / 4) paged_attention_join_kernel(Pa
     const int4 u = parts.open[blockIdx.y];
     const int n = u.w, hh = blockIdx.x, group = a.Hq / a.Hkv, kvh = u.y / tiles, tile = u.y % tiles;
     if (n == 0 || tile * heads + hh >= group) return;
-    const int t = threadIdx.x, col = t % kCols, set = t / kCols, lane = t & 31, warp = t >> 5;
+    const int t = threadIdx.x, col = t % kCols, set = t / kCols, lane = t & 31, warp = t >> 5, d0 = (blockIdx.z * kCols + col) * 4;
     const long long h = (long long)u.x * a.Hq + kvh * group + tile * heads + hh;
     // the first CTA's part is its second one
     auto slot = [&](int i) { return 2ll * (u.z + i) + (i == 0 ? 1 : 0); };
@@ -647,7 +648,7 @@ __global__ void __launch_bounds__(kPaSets* D / 4) paged_attention_join_kernel(Pa
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 8
     for (int i = set; i < n; i += kPaSets) {
-        const float4 p = *reinterpret_cast<const float4*>(parts.acc + (slot(i) * heads + hh) * D + col * 4);
+        const float4 p = *reinterpret_cast<const float4*>(parts.acc + (slot(i) * heads + hh) * D + d0);
         const float f = factor[i];
         v.x += f * p.x, v.y += f * p.y, v.z += f * p.z, v.w += f * p.w;
     }
@@ -663,9 +664,9 @@ __global__ void __launch_bounds__(kPaSets* D / 4) paged_attention_join_kernel(Pa
         v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
     }
     const float inv = sum == 0.f ? 0.f : 1.f / sum;
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + h * D + col * 4) =
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + h * D + d0) =
         make_uint2(pa_pack<DT>(v.x * inv, v.y * inv), pa_pack<DT>(v.z * inv, v.w * inv));
-    if (t == 0 && a.lse) a.lse[h] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
+    if (t == 0 && blockIdx.z == 0 && a.lse) a.lse[h] = sum == 0.f ? -INFINITY : (top + log2f(sum)) * kLn2;
 }
 
 // CTAs of a unit's cluster, or 0: units are cut over all CTAs and joined by a second kernel. `ctas`: what the GPU holds at
@@ -735,7 +736,8 @@ cudaError_t launch_nt(const PagedAttnArgs& a, const PaPlan& p, const PaParts& pa
     void* jargs[] = {const_cast<PagedAttnArgs*>(&a), &tiles, &heads, const_cast<PaParts*>(&parts)};
     const int group = a.Hq / a.Hkv;
     return launch_kernel(reinterpret_cast<const void*>(paged_attention_join_kernel<DT, D>),
-                         dim3(heads < group ? heads : group, static_cast<unsigned>(p.units)), dim3(kPaSets * D / 4), 0, true, s, jargs);
+                         dim3(heads < group ? heads : group, static_cast<unsigned>(p.units), D / (4 * kPaCols)), dim3(kPaSets * kPaCols), 0, true, s,
+                         jargs);
 }
 
 template <int DT>

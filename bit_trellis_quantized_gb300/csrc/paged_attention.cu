@@ -22,8 +22,8 @@
 //     are not there are filled with zeros and masked.
 //   * Keys are the M of both products (scores K Q^T, values V^T P^T: m16n8k16),
 //     so that 8 query heads fill the instruction's N exactly.
-// Measured: 192 sequences of 500 to 16384 keys, 2 key heads of 256: 282 us, 6.7
-// TB/s; one of 131071: 52 us, 5.2 TB/s; one of 700: 8.4 us.
+// Measured: 192 sequences of 500 to 16384 keys, 2 key heads of 256: 280 us, 6.7
+// TB/s; one of 131071: 50 us, 5.3 TB/s; one of 700: 8.2 us.
 #include "common.cuh"
 #include "context.h"
 #include "kernels.h"
@@ -49,7 +49,9 @@ struct PaCfg {
     static constexpr int kRow = D * 2;          // bytes of a row
     static constexpr int kTile = 16 * kRow;     // of a half
     static constexpr int kRing = kWarps * kHalves * kTile;
-    static constexpr int kSmem = kRing + 2 * 8 * NT * D * 4;
+    static_assert(8 * NT * (D + 4) * 4 <= kHalves * kTile, "a warp's weighted values in its ring");
+    static constexpr int kStep = D + 4;         // between heads of a buffer of weighted values: no bank conflicts
+    static constexpr int kSmem = kRing + 2 * 8 * NT * kStep * 4;
 };
 
 // n / d of n < 2^31 by one multiplication: mul = ceil(2^(31 + l) / d), l = ceil(log2 d).
@@ -173,7 +175,7 @@ __device__ __forceinline__ void pa_units(const PagedAttnArgs& a, int tiles, cons
     using C = PaCfg<D, NT>;
     constexpr int kHeads = 8 * NT, kHalves = C::kHalves, kTile = C::kTile, kKs = D / 16, kRound = C::kRound;
     constexpr int kWarps = C::kWarps, kThreads = C::kThreads;
-    extern __shared__ __align__(1024) unsigned char smem[];
+    extern __shared__ __align__(128) unsigned char smem[];  // (1024 would leave one CTA a multiprocessor at D = 256)
     __shared__ long long scan[kWarps];
     __shared__ int first_s[4];
     __shared__ float sm_m[kWarps][kHeads], sm_l[kWarps][kHeads];
@@ -476,7 +478,7 @@ __device__ __forceinline__ void pa_units(const PagedAttnArgs& a, int tiles, cons
             // its ring; before, the ring is being filled, and the warps of each parity take turns at one.
             const bool end = i + 1 == left;
             float* bufs = reinterpret_cast<float*>(end ? smem : smem + C::kRing);
-            const int n_bufs = end ? kWarps : 2, apart = end ? kHalves * kTile / 4 : kHeads * D;
+            const int n_bufs = end ? kWarps : 2, apart = end ? kHalves * kTile / 4 : kHeads * C::kStep;
             float* mybuf = bufs + (end ? warp : warp & 1) * apart;
 #pragma unroll 1
             for (int turn = 0; turn < (end ? 1 : kWarps / 2); ++turn) {
@@ -487,7 +489,7 @@ __device__ __forceinline__ void pa_units(const PagedAttnArgs& a, int tiles, cons
                         for (int k = 0; k < kKs; ++k)
 #pragma unroll
                             for (int e = 0; e < 4; ++e) {
-                                const int at = (n * 8 + q4 * 2 + (e & 1)) * D + k * 16 + g + (e >> 1) * 8;
+                                const int at = (n * 8 + q4 * 2 + (e & 1)) * C::kStep + k * 16 + g + (e >> 1) * 8;
                                 const float v = acc[n][k][e] * f[n][e & 1];
                                 mybuf[at] = turn == 0 ? v : mybuf[at] + v;
                             }
@@ -500,7 +502,7 @@ __device__ __forceinline__ void pa_units(const PagedAttnArgs& a, int tiles, cons
                 const int h = at / D;
                 float v0 = 0.f, v1 = 0.f;
                 for (int w = 0; w < n_bufs; ++w) {
-                    const float2 o = *reinterpret_cast<const float2*>(bufs + w * apart + at);
+                    const float2 o = *reinterpret_cast<const float2*>(bufs + w * apart + h * C::kStep + at % D);
                     v0 += o.x, v1 += o.y;
                 }
                 if (whole) {

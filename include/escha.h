@@ -528,7 +528,8 @@ int escha_moe_route(const escha_moe_layer* L, const uint16_t* x, int T, uint16_t
  *   d        64, 128 or 256;  Hq = 1..64 times Hkv, Hkv <= 1024, B <= 65535
  *   max_len  host-side bound of lens, 1..2^30 (max_pages * page serves where
  *            it is no more than that)
- *   ws       escha_paged_attention_workspace(B, Hq, Hkv, d, max_len) bytes;
+ *   ws       escha_paged_attention_workspace(B, Hq, Hkv, d, max_len) bytes (may
+ *            be 0);
  *            nothing in it has to start at zero
  * Positions at or behind lens[b] are never read: they may hold anything. A NaN
  * or an infinity among the attended keys and values, or q, may make the heads

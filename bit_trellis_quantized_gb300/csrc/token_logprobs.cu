@@ -170,8 +170,15 @@ struct LpWarp {
     float thr;                // values below this are not among the top ones
 };
 
-// The lanes' values in descending order.
-__device__ __forceinline__ unsigned lp_sort(unsigned v, int lane) {
+// The n-th largest of the lanes' values, the same in all lanes: by taking the largest away, or out of a sorted warp.
+__device__ __forceinline__ unsigned lp_nth(unsigned v, int n, int lane) {
+    if (n <= 3) {
+        for (;;) {
+            const unsigned most = __reduce_max_sync(0xffffffffu, v);
+            if (--n == 0) return most;
+            if (lane == __ffs(__ballot_sync(0xffffffffu, v == most)) - 1) v = 0u;
+        }
+    }
 #pragma unroll
     for (int k = 2; k <= 32; k <<= 1)
 #pragma unroll
@@ -180,14 +187,14 @@ __device__ __forceinline__ unsigned lp_sort(unsigned v, int lane) {
             // descending within blocks of k whose bit k is 0
             v = ((lane & j) == 0) == ((lane & k) == 0) ? max(v, o) : min(v, o);
         }
-    return v;
+    return __shfl_sync(0xffffffffu, v, n - 1);
 }
 
 // A value that `top` of the threads' values v (in lp_order) reach: the q-th largest of the warps' p-th largest,
 // p q >= top. All threads of the CTA call it; `slots` may be written again after the next __syncthreads.
 __device__ __forceinline__ unsigned lp_bound(unsigned v, int top, unsigned* slots, int lane, int warp) {
     const int p = (top + 3) / 4, q = (top + p - 1) / p;  // top <= 32: p <= 8, q <= 4
-    v = __shfl_sync(0xffffffffu, lp_sort(v, lane), p - 1);
+    v = lp_nth(v, p, lane);
     if (lane == 0) slots[warp] = v;
     __syncthreads();
     v = lane < kLpWarps ? slots[lane] : 0u;
@@ -232,11 +239,11 @@ __device__ __forceinline__ void st_cluster_u64(uint32_t addr, unsigned long long
     asm volatile("st.shared::cluster.u64 [%0], %1;" ::"r"(addr), "l"(v) : "memory");
 }
 
-// Adds a chunk, kLpValues values of each lane (places past the end hold -inf), to the lane's sums; vmax: its
-// vectors' maxima. `buf`: the warp's 32 kLpValues / N vectors of shared memory.
+// Adds a chunk, kLpValues values of each lane (places past the end hold -inf), to the lane's sums; gives their
+// largest. `buf`: the warp's 32 kLpValues / N vectors of shared memory.
 template <int DT>
 __device__ __forceinline__ float lp_sums(LpPart& p, const uint4 (&r)[kLpValues / LpVec<DT>::N],
-                                         float (&vmax)[kLpValues / LpVec<DT>::N], uint4* buf, int lane) {
+                                         uint4* buf, int lane) {
     using V = LpVec<DT>;
     constexpr int N = V::N, kLpLoads = kLpValues / N;
     float b = -INFINITY;
@@ -244,10 +251,8 @@ __device__ __forceinline__ float lp_sums(LpPart& p, const uint4 (&r)[kLpValues /
     for (int i = 0; i < kLpLoads; ++i) {
         float x[N];
         V::get(r[i], x);
-        vmax[i] = fmaxf(x[0], x[1]);
 #pragma unroll
-        for (int j = 2; j < N; j += 2) vmax[i] = fmaxf(vmax[i], fmaxf(x[j], x[j + 1]));
-        b = fmaxf(b, vmax[i]);
+        for (int j = 0; j < N; j += 2) b = fmaxf(b, fmaxf(x[j], x[j + 1]));
     }
     if (b > p.m) {
         const float d = lp_shift(p.m, b), f = ex2(d);
@@ -306,41 +311,43 @@ struct LpKept {
     int count;  // of all that came, beyond kLpKept too
 };
 
-// Collects a chunk's values that reach w.thr, in `kept` (kPlaces of them) or the warp's list. `index(i, j)` is the
+// Collects a chunk's values (`most`: their largest) that reach w.thr, in `kept` (kPlaces of them) or the warp's list. `index(i, j)` is the
 // index of value j of the lane's vector i, or -1 for a place past the end.
 template <int DT, int kPlaces, typename F>
 __device__ __forceinline__ void lp_collect(LpWarp& w, const uint4 (&r)[kLpValues / LpVec<DT>::N],
-                                           const float (&vmax)[kLpValues / LpVec<DT>::N], uint4* buf, LpKept* kept, int top,
-                                           int lane, F&& index) {
+                                           float most, uint4* buf, LpKept* kept, int top, int lane, F&& index) {
     using V = LpVec<DT>;
     constexpr int N = V::N, kLpLoads = kLpValues / N;
     // a NaN in the sums: a maximum may have passed over one
     const float thr = w.p.s != w.p.s ? -INFINITY : w.thr;
-    unsigned over = 0;  // values that found no place
+    if (!__any_sync(0xffffffffu, !(most < thr))) return;
+    // by lane, which of its values do; those are few, so one short loop takes them, out of shared memory
+    unsigned todo = 0, over = 0;  // over: no place for them
 #pragma unroll
     for (int i = 0; i < kLpLoads; ++i) {
-        if (!__any_sync(0xffffffffu, !(vmax[i] < thr))) continue;
         float x[N];
         V::get(r[i], x);
 #pragma unroll
-        for (int j = 0; j < N; ++j) {
-            if (!(x[j] < thr)) {
-                const int id = index(i, j);
-                if (id >= 0) {
-                    const int at = kPlaces > 0 ? atomicAdd(&kept->count, 1) : 0;
-                    if (at < kPlaces)
-                        kept->key[at] = lp_key(x[j], id);
-                    else
-                        over |= 1u << (i * N + j);
-                }
-            }
+        for (int j = 0; j < N; ++j)
+            if (!(x[j] < thr) && index(i, j) >= 0) todo |= 1u << (i * N + j);
+        buf[i * 32 + lane] = r[i];
+    }
+    if (kPlaces == 0) {
+        over = todo;
+    } else {
+#pragma unroll 1
+        while (todo) {
+            const int k = __ffs(todo) - 1;
+            todo &= todo - 1;
+            const int at = atomicAdd(&kept->count, 1);
+            if (at < kPlaces)
+                kept->key[at] = lp_key(V::one(buf + (k / N) * 32 + lane, k % N), index(k / N, k % N));
+            else
+                over |= 1u << k;
         }
+        __syncwarp();
     }
     if (!__any_sync(0xffffffffu, over != 0)) return;
-    __syncwarp();
-#pragma unroll
-    for (int i = 0; i < kLpLoads; ++i) buf[i * 32 + lane] = r[i];
-    __syncwarp();
     unsigned long long last = __shfl_sync(0xffffffffu, w.mine, top - 1);
 #pragma unroll 1
     for (int k = 0; k < kLpValues; ++k) {
@@ -348,10 +355,10 @@ __device__ __forceinline__ void lp_collect(LpWarp& w, const uint4 (&r)[kLpValues
         if (!__any_sync(0xffffffffu, mine)) continue;
         const float x = V::one(buf + (k / N) * 32 + lane, k % N);
         const unsigned long long key = mine ? lp_key(x, index(k / N, k % N)) : 0ull;
-        unsigned todo = __ballot_sync(0xffffffffu, key > last);
-        while (todo) {
-            const int src = __ffs(todo) - 1;
-            todo &= todo - 1;
+        unsigned more = __ballot_sync(0xffffffffu, key > last);
+        while (more) {
+            const int src = __ffs(more) - 1;
+            more &= more - 1;
             const unsigned long long c = __shfl_sync(0xffffffffu, key, src);
             if (c > last) {
                 lp_insert(w.mine, c, lane);
@@ -521,7 +528,6 @@ __device__ __forceinline__ void lp_ranges(const LogprobArgs& a, int units, long 
         };
         int v = (u0 + warp * mine) * 32;
         uint4 r[kLpLoads];
-        float vmax[kLpLoads];
         load(r, v);
         if (threadIdx.x == 0) kept.count = 0;
         __syncthreads();
@@ -550,9 +556,9 @@ __device__ __forceinline__ void lp_ranges(const LogprobArgs& a, int units, long 
             if (v >= last) continue;
             uint4 ahead[kLpLoads];
             load(ahead, v + 32 * kLpLoads);
-            lp_sums<DT>(w.p, r, vmax, buf[warp], lane);
+            const float most = lp_sums<DT>(w.p, r, buf[warp], lane);
             if (a.top > 0)
-                lp_collect<DT, kLpKept>(w, r, vmax, buf[warp], &kept, a.top, lane, [&](int i, int j) {
+                lp_collect<DT, kLpKept>(w, r, most, buf[warp], &kept, a.top, lane, [&](int i, int j) {
                     const int k = v + i * 32 + lane;
                     return k < last ? head + k * N + j : -1;
                 });
@@ -564,9 +570,9 @@ __device__ __forceinline__ void lp_ranges(const LogprobArgs& a, int units, long 
 #pragma unroll
             for (int i = 0; i < kLpLoads; ++i) r[i] = make_uint4(V::kNone, V::kNone, V::kNone, V::kNone);
             r[0] = V::two(lane < head ? V::one(x, lane) : -INFINITY, tail + lane < a.V ? V::one(x, tail + lane) : -INFINITY);
-            lp_sums<DT>(w.p, r, vmax, buf[0], lane);
+            const float most = lp_sums<DT>(w.p, r, buf[0], lane);
             if (a.top > 0)
-                lp_collect<DT, kLpKept>(w, r, vmax, buf[0], &kept, a.top, lane, [&](int i, int j) {
+                lp_collect<DT, kLpKept>(w, r, most, buf[0], &kept, a.top, lane, [&](int i, int j) {
                     return i > 0 ? -1 : j == 0 && lane < head ? lane : j == 1 && tail + lane < a.V ? tail + lane : -1;
                 });
         }
@@ -647,7 +653,6 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_rows_kerne
         const int nv = (a.V - head) / N, tail = head + nv * N;
         LpWarp w = lp_start();
         uint4 r[kLpLoads];
-        float vmax[kLpLoads];
         // the values at the ends, as two of one vector, after the rest
         for (int v = 0; v < nv; v += 32 * kLpLoads) {
 #pragma unroll
@@ -656,11 +661,11 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_rows_kerne
                 if (v + i * 32 + lane < nv)
                     r[i] = ldg_stream_v4(x + (long long)head * size + (long long)(v + i * 32 + lane) * 16);
             }
-            const float b = lp_sums<DT>(w.p, r, vmax, buf[warp], lane);
+            const float b = lp_sums<DT>(w.p, r, buf[warp], lane);
             if (a.top > 0) {
-                const unsigned kth = __shfl_sync(0xffffffffu, lp_sort(lp_order(b), lane), a.top - 1);
+                const unsigned kth = lp_nth(lp_order(b), a.top, lane);
                 w.thr = fmaxf(w.thr, lp_from_order(kth));
-                lp_collect<DT, 0>(w, r, vmax, buf[warp], nullptr, a.top, lane, [&](int i, int j) {
+                lp_collect<DT, 0>(w, r, b, buf[warp], nullptr, a.top, lane, [&](int i, int j) {
                     const int k = v + i * 32 + lane;
                     return k < nv ? head + k * N + j : -1;
                 });
@@ -670,9 +675,9 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_rows_kerne
 #pragma unroll
             for (int i = 0; i < kLpLoads; ++i) r[i] = make_uint4(V::kNone, V::kNone, V::kNone, V::kNone);
             r[0] = V::two(lane < head ? V::one(x, lane) : -INFINITY, tail + lane < a.V ? V::one(x, tail + lane) : -INFINITY);
-            lp_sums<DT>(w.p, r, vmax, buf[warp], lane);
+            const float most = lp_sums<DT>(w.p, r, buf[warp], lane);
             if (a.top > 0)
-                lp_collect<DT, 0>(w, r, vmax, buf[warp], nullptr, a.top, lane, [&](int i, int j) {
+                lp_collect<DT, 0>(w, r, most, buf[warp], nullptr, a.top, lane, [&](int i, int j) {
                     return i > 0 ? -1 : j == 0 && lane < head ? lane : j == 1 && tail + lane < a.V ? tail + lane : -1;
                 });
         }

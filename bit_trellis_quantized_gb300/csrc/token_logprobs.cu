@@ -26,7 +26,7 @@
 // Bound: one read of the logits. Each lane loads a chunk ahead, and the
 // arithmetic is 5 instructions a value (pairs of f32 where there is an
 // instruction for them), so that it stays behind the loads: 2048 rows of 152064
-// f32 take 211 us, 5.9 TB/s (187 without the top 8). How rows are dealt out to
+// f32 take 203 us, 6.1 TB/s (187 without the top 8). How rows are dealt out to
 // warps, CTAs and clusters is at lp_route.
 #include <algorithm>
 
@@ -377,24 +377,32 @@ __device__ __forceinline__ unsigned lp_keys_bound(const unsigned long long* keys
     return lp_bound(most, top, slots, lane, warp);
 }
 
-// The best `top` of n distinct keys (0: none) in shared memory, in order, to `best`; `work` holds n keys. All
-// threads of the CTA call it; `best` can be read after it.
+// So many keys are ranked as they are (160 of them, a row's top 20 in a cluster of 8: 10.8 us, 10.2 with the bound).
+constexpr int kLpFew = 96;
+// The best `top` of n distinct keys (0: none) in shared memory, in order, to `best`; `work` holds n keys. Each key
+// counts those above it; many are first reduced to those that reach a bound. All threads of the CTA call it; `best`
+// can be read after it.
 __device__ __forceinline__ void lp_select(const unsigned long long* keys, int n, int top, unsigned long long* work,
                                           unsigned long long* best, int lane, int warp) {
     __shared__ unsigned slots[kLpWarps];
     __shared__ int count;
     const int t = threadIdx.x;
-    if (t == 0) count = 0;
     if (t < kLogprobMaxTop) best[t] = 0ull;
-    const unsigned bound = lp_keys_bound(keys, n, top, slots, lane, warp);
-    for (int i = t; i < n; i += kLpThreads)
-        if (keys[i] != 0ull && static_cast<unsigned>(keys[i] >> 32) >= bound) work[atomicAdd(&count, 1)] = keys[i];
+    const bool many = n > kLpFew;
+    if (many) {
+        if (t == 0) count = 0;
+        const unsigned bound = lp_keys_bound(keys, n, top, slots, lane, warp);
+        for (int i = t; i < n; i += kLpThreads)
+            if (keys[i] != 0ull && static_cast<unsigned>(keys[i] >> 32) >= bound) work[atomicAdd(&count, 1)] = keys[i];
+        keys = work;
+    }
     __syncthreads();
-    const int left = count;
-    for (int i = t; i < left; i += kLpThreads) {
-        const unsigned long long mine = work[i];
-        int above = 0;
-        for (int j = 0; j < left; ++j) above += work[j] > mine;
+    if (many) n = count;
+    for (int i = t; i < n; i += kLpThreads) {
+        const unsigned long long mine = keys[i];
+        int above = mine == 0ull ? top : 0;
+#pragma unroll 4
+        for (int j = 0; j < n; ++j) above += keys[j] > mine;
         if (above < top) best[above] = mine;
     }
     __syncthreads();
@@ -427,8 +435,23 @@ __device__ __forceinline__ void lp_join_sums(LpPart& p, int lane, int warp) {
     }
 }
 
+// A given token of a row and its logit, loaded while the row is read.
+struct LpGiven {
+    int id;
+    float x;
+};
 template <int DT>
-__device__ __forceinline__ void lp_finish(const LogprobArgs& a, int row, const LpPart& p, unsigned long long mine, int lane) {
+__device__ __forceinline__ LpGiven lp_given(const LogprobArgs& a, int row, int i) {
+    LpGiven g{-1, 0.f};
+    if (i >= a.n_ids) return g;
+    g.id = a.ids[(long long)row * a.n_ids + i];
+    if (g.id >= 0 && g.id < a.V) g.x = LpVec<DT>::one(static_cast<const char*>(a.logits) + (long long)row * a.ld * (DT == 3 ? 4 : 2), g.id);
+    return g;
+}
+
+template <int DT>
+__device__ __forceinline__ void lp_finish(const LogprobArgs& a, int row, const LpPart& p, unsigned long long mine, const LpGiven& given,
+                                          int lane) {
     const float ls = log2f(p.s);
     const bool none = p.s == 0.f;  // every logit is -inf
     auto logprob = [&](float v) {
@@ -439,13 +462,12 @@ __device__ __forceinline__ void lp_finish(const LogprobArgs& a, int row, const L
         if (a.lse) a.lse[row] = none ? -INFINITY : fabsf(p.m) < kFar ? kLn2 * (lp_scaled(p.m) + ls) : p.m + kLn2 * ls;
         if (a.entropy) a.entropy[row] = none ? 0.f : kLn2 * (ls - p.t / p.s);
     }
-    const char* x = static_cast<const char*>(a.logits) + (long long)row * a.ld * (DT == 3 ? 4 : 2);
     for (int i = lane; i < a.n_ids; i += 32) {
-        const int id = a.ids[(long long)row * a.n_ids + i];
+        const LpGiven g = i < 32 ? given : lp_given<DT>(a, row, i);
         float r = 0.f;
-        if (id >= 0 && id < a.V)
-            r = logprob(LpVec<DT>::one(x, id));
-        else if (id != -1)
+        if (g.id >= 0 && g.id < a.V)
+            r = logprob(g.x);
+        else if (g.id != -1)
             r = __uint_as_float(0x7FC00000u);
         a.logprobs[(long long)row * a.n_ids + i] = r;
     }
@@ -529,6 +551,8 @@ __device__ __forceinline__ void lp_ranges(const LogprobArgs& a, int units, long 
         int v = (u0 + warp * mine) * 32;
         uint4 r[kLpLoads];
         load(r, v);
+        LpGiven given{-1, 0.f};
+        if (warp == 0 && rank == 0 && u0 == 0) given = lp_given<DT>(a, row, lane);
         if (threadIdx.x == 0) kept.count = 0;
         __syncthreads();
         if (a.top > 0) {
@@ -594,21 +618,21 @@ __device__ __forceinline__ void lp_ranges(const LogprobArgs& a, int units, long 
                     const uint32_t to = cluster_map(smem_u32(&their_sums[rank]), 0);
                     st_cluster_f32(to, w.p.m), st_cluster_f32(to + 4, w.p.s), st_cluster_f32(to + 8, w.p.t);
                 }
-                if (a.top > 0) st_cluster_u64(cluster_map(smem_u32(&their_keys[rank * 32 + lane]), 0), best[lane]);
+                if (lane < a.top) st_cluster_u64(cluster_map(smem_u32(&their_keys[rank * a.top + lane]), 0), best[lane]);
             }
             cluster_arrive();
             cluster_wait();
             if (rank != 0) return;
             w.p = threadIdx.x < kCluster ? their_sums[threadIdx.x] : LpPart{kLowest, 0.f, 0.f};
             lp_join_sums(w.p, lane, warp);
-            if (a.top > 0) lp_select(their_keys, kCluster * 32, a.top, reinterpret_cast<unsigned long long*>(buf), best, lane, warp);
-            if (warp == 0) lp_finish<DT>(a, row, w.p, a.top > 0 ? best[lane] : 0ull, lane);
+            if (a.top > 0) lp_select(their_keys, kCluster * a.top, a.top, reinterpret_cast<unsigned long long*>(buf), best, lane, warp);
+            if (warp == 0) lp_finish<DT>(a, row, w.p, a.top > 0 ? best[lane] : 0ull, given, lane);
             return;
         }
         if (warp == 0) {
             const unsigned long long key = a.top > 0 ? best[lane] : 0ull;
             if (u0 == 0 && u1 == units) {
-                lp_finish<DT>(a, row, w.p, key, lane);
+                lp_finish<DT>(a, row, w.p, key, given, lane);
             } else {
                 LpRecord* to = out.rec + 2ll * cta + (u0 == 0 ? 1 : 0);
                 if (lane == 0) to->m = w.p.m, to->s = w.p.s, to->t = w.p.t;
@@ -653,6 +677,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_rows_kerne
         const int nv = (a.V - head) / N, tail = head + nv * N;
         LpWarp w = lp_start();
         uint4 r[kLpLoads];
+        const LpGiven given = lp_given<DT>(a, row, lane);
         // the values at the ends, as two of one vector, after the rest
         for (int v = 0; v < nv; v += 32 * kLpLoads) {
 #pragma unroll
@@ -682,7 +707,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_rows_kerne
                 });
         }
         lp_join_warp(w.p);
-        lp_finish<DT>(a, row, w.p, w.mine, lane);
+        lp_finish<DT>(a, row, w.p, w.mine, given, lane);
     }
 }
 
@@ -699,6 +724,8 @@ __global__ void __launch_bounds__(kLpThreads) token_logprobs_join_kernel(Logprob
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     // the first CTA's part is its second record
     auto rec = [&](int i) { return in.rec + 2ll * (blockIdx.x + i) + (i == 0 ? 1 : 0); };
+    LpGiven given{-1, 0.f};
+    if (warp == 0) given = lp_given<DT>(a, row, lane);
     LpWarp w = lp_start();
     for (int i = threadIdx.x; i < n; i += kLpThreads) w.p = lp_join(w.p, LpPart{rec(i)->m, rec(i)->s, rec(i)->t});
     if (a.top > 0)
@@ -706,7 +733,7 @@ __global__ void __launch_bounds__(kLpThreads) token_logprobs_join_kernel(Logprob
         for (int i = threadIdx.x; i < n * 32; i += kLpThreads) lp_smem[i] = rec(i >> 5)->key[i & 31];
     lp_join_sums(w.p, lane, warp);
     if (a.top > 0) lp_select(lp_smem, n * 32, a.top, lp_smem + n * 32, best, lane, warp);
-    if (warp == 0) lp_finish<DT>(a, row, w.p, a.top > 0 ? best[lane] : 0ull, lane);
+    if (warp == 0) lp_finish<DT>(a, row, w.p, a.top > 0 ? best[lane] : 0ull, given, lane);
 }
 
 // How rows are dealt out: to warps, to clusters of 1 to 8 CTAs (no workspace), or cut over all CTAs with a join

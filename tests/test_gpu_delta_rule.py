@@ -287,3 +287,30 @@ def test_refusals():
     bad(native.EschaError, scale=float("inf"))
     d = make(30, [8], 2, 4, 64, 48, "f16")
     bad(native.EschaError, v=d["v"], state=d["state"])
+
+
+@pytest.mark.parametrize("dtype,T,before,Hk,Hv,dk,dv", [("f16", 6500, 0, 2, 2, 64, 64), ("bf16", 9001, 41, 1, 2, 128, 96),
+                                                        ("bf16", 6400, 31, 2, 4, 64, 32)])
+def test_one_long_sequence(dtype, T, before, Hk, Hv, dk, dv):
+    """Thousands of tokens, the first not on a chunk's boundary; calls one behind
+    another on one workspace, and replayed, give the same bits."""
+    native = _native()
+    c = make(34, [T], Hk, Hv, dk, dv, dtype, before=before, behind=7)
+    got, state = run_and_check(native, c, dtype, max_len=T)
+    args = [c[x] for x in ("q", "k", "v", "g", "beta")]
+    ws = torch.empty(1 << 28, dtype=torch.uint8, device="cuda")
+    st, out = c["state"].clone(), torch.full_like(c["v"], 77.0)
+    # calls one behind another share a workspace
+    for _ in range(3):
+        st.copy_(c["state"])
+        native.delta_rule(*args, st, c["at"], max_len=T, out=out, ws=ws)
+        native.delta_rule(*args, c["state"].clone(), c["at"], max_len=T, ws=ws)
+    assert torch.equal(st, state) and np.array_equal(f64(out), got)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        native.delta_rule(*args, st, c["at"], max_len=T, out=out, ws=ws)
+    for _ in range(2):
+        st.copy_(c["state"])
+        graph.replay()
+    torch.cuda.synchronize()
+    assert torch.equal(st, state) and np.array_equal(f64(out), got)

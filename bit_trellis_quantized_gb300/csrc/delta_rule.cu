@@ -486,10 +486,10 @@ __device__ __forceinline__ unsigned long long dr_mul2(unsigned long long x, floa
 // those become the chain); S split for the next chunk between the products of
 // this one (1.26: an instruction stream of one warp); a long sequence in parts,
 // the chunk data of one made beside the walk of the one before (32000 tokens:
-// 1512 us against 1420). tcgen05 takes 128 rows at
-// least, all columns of a state, and its results would pass through tensor
-// memory between the four products of the chain: throughput, which many
-// sequences could use, but not a shorter chain.
+// 1512 us against 1420). tcgen05 takes 128 rows at least, all columns of a
+// state, and its results would pass through tensor memory between the four
+// products of the chain: throughput, which many sequences could use, but not a
+// shorter chain.
 template <int kThreads>
 __device__ __forceinline__ void dr_meet() {  // all warps, each from its own loop
     asm volatile("bar.sync 1, %0;" ::"n"(kThreads) : "memory");

@@ -236,7 +236,7 @@ __device__ __forceinline__ void pa_units(const PagedAttnArgs& a, int tiles, cons
         }
         // every CTA that takes part has a round at least (the join counts on it)
         ctas = min(static_cast<long long>(gridDim.x), total);
-            // the sequences without keys
+        // the sequences without keys
         for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
             if (pa_len(a, b) > 0) continue;
             for (int i = t; i < units; i += kThreads) parts.open[b * units + i] = make_int4(0, 0, 0, 0);

@@ -71,8 +71,10 @@ SHAPES = [
     ("bf16", [64], 1, 3, 64, 96), ("f16", [63, 65, 0, 129, 1], 2, 4, 128, 128), ("bf16", [200], 1, 2, 128, 256),
     ("f16", [17, 130, 33], 3, 3, 64, 128), ("bf16", [0, 0, 5], 2, 2, 64, 160), ("f16", [300], 2, 4, 128, 32),
     ("bf16", [2, 127, 128, 0, 191, 192, 193], 1, 2, 128, 64),
-    # enough heads for the walk of 64 columns a CTA
+    # many sequences; heads for one round of 64 columns a CTA, or two of 32
     ("f16", [70, 33, 0, 64, 31] * 8, 2, 4, 64, 64), ("bf16", [100, 1, 40] * 14, 1, 2, 128, 128),
+    ("f16", [70, 33, 0, 64, 31] * 6, 2, 4, 64, 64), ("bf16", [100, 1, 40] * 12, 1, 2, 128, 128),
+    ("bf16", [33 + i % 9 for i in range(70)], 1, 2, 64, 64), ("f16", [97] * 5, 3, 15, 128, 128),
 ]
 
 

@@ -23,7 +23,7 @@
 //   * Keys are the M of both products (scores K Q^T, values V^T P^T: m16n8k16),
 //     so that 8 query heads fill the instruction's N exactly.
 // Measured: 192 sequences of 500 to 16384 keys, 2 key heads of 256: 280 us, 6.7
-// TB/s; one of 131071: 50 us, 5.3 TB/s; one of 700: 8.2 us.
+// TB/s; one of 131071: 48 us, 5.6 TB/s; one of 700: 8.2 us.
 #include "common.cuh"
 #include "context.h"
 #include "kernels.h"
@@ -129,7 +129,6 @@ __device__ __forceinline__ int pa_len(const PagedAttnArgs& a, int b) {
 struct PaParts {
     float* acc;  // [2 CTAs][heads][D]: a CTA's first part of a unit begun before its range, its part of one that goes on
     float* ml;   // [2 CTAs][2][heads]
-    int4* open;  // by unit: sequence, unit of the sequence, first CTA and number of parts (0: finished, or no keys)
 };
 
 __device__ __forceinline__ float ld_cluster_f32(uint32_t addr) {
@@ -239,7 +238,6 @@ __device__ __forceinline__ void pa_units(const PagedAttnArgs& a, int tiles, cons
         // the sequences without keys
         for (int b = blockIdx.x; b < a.B; b += gridDim.x) {
             if (pa_len(a, b) > 0) continue;
-            for (int i = t; i < units; i += kThreads) parts.open[b * units + i] = make_int4(0, 0, 0, 0);
             for (int i = t; i < a.Hq * D / 2; i += kThreads) static_cast<uint32_t*>(a.out)[(long long)b * a.Hq * D / 2 + i] = 0u;
             if (a.lse)
                 for (int i = t; i < a.Hq; i += kThreads) a.lse[(long long)b * a.Hq + i] = -INFINITY;
@@ -535,16 +533,6 @@ __device__ __forceinline__ void pa_units(const PagedAttnArgs& a, int tiles, cons
                     parts.ml[(slot * 2 + 1) * kHeads + t] = sum;
                 }
             }
-            if (kCluster == 0 && t == 0 && piece_r0 == 0) {
-                const int u = cur.kvh * tiles + cur.tile;
-                int n = 0;
-                if (!last) {
-                    // the CTA that holds the unit's last round: the largest c with floor(c total / ctas) <= it
-                    const long long end = lo + i + (cur.rounds - 1 - cur.r);
-                    n = static_cast<int>(((end + 1) * ctas - 1) / total) - static_cast<int>(blockIdx.x) + 1;
-                }
-                parts.open[cur.b * units + u] = make_int4(cur.b, u, blockIdx.x, n);
-            }
             __syncthreads();
             begin = true;
         }
@@ -605,34 +593,56 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(PaCfg<D, NT>:
     pa_units<DT, D, NT, kCluster>(a, tiles, div, PaParts{});
 }
 
-// Joins the parts of one query head of a unit that lies in several CTAs'
-// ranges: CTA (head of the unit, unit, 64 values), kPaSets interleaved sets of
-// parts with 16 threads of four values each. Bound by its chain of loads: what
-// to join, the parts' maxima and sums, the values.
+// Joins the parts of one query head of a unit that lies in several of the
+// `grid` CTAs' ranges: CTA (head of the unit, unit, 64 values), kPaSets
+// interleaved sets of parts with 16 threads of four values each. Which CTAs
+// those are it finds from the lengths, as they did, while they still run; behind
+// them all its loads go at once.
 constexpr int kPaSets = 32, kPaCols = 16;
-static_assert(PaCfg<64, 1>::kCtas <= 4 && PaCfg<128, 1>::kCtas <= 4 && PaCfg<256, 1>::kCtas <= 4, "the join holds a factor a CTA");
+constexpr int kPaFew = 38;  // units, and so sequences, that are cut over all CTAs (pa_route), at most
+static_assert(16 * (kPaFew + 1) > kSms * 4 && PaCfg<64, 1>::kCtas <= 4 && PaCfg<128, 1>::kCtas <= 4 && PaCfg<256, 1>::kCtas <= 4, "CTAs of a launch");
 template <int DT, int D>
-__global__ void __launch_bounds__(kPaSets* kPaCols) paged_attention_join_kernel(PagedAttnArgs a, int tiles, int heads, PaParts parts) {
-    constexpr int kCols = kPaCols, kThreads = kPaSets * kCols, kW = kThreads / 32;
+__global__ void __launch_bounds__(kPaSets* kPaCols) paged_attention_join_kernel(PagedAttnArgs a, int tiles, int heads, int grid, PaParts parts) {
+    constexpr int kCols = kPaCols, kThreads = kPaSets * kCols, kW = kThreads / 32, kHold = kSms * 4;
     __shared__ float4 sums[kPaSets][kCols];
-    __shared__ float red[2][kW];
+    __shared__ float red[2][kW], factor[kHold];
+    __shared__ int rounds[kPaFew];
+    const int t = threadIdx.x, col = t % kCols, set = t / kCols, lane = t & 31, warp = t >> 5, d0 = (blockIdx.z * kCols + col) * 4;
+    const int units = a.Hkv * tiles, b = blockIdx.y / units, u = blockIdx.y % units;
+    const int hh = blockIdx.x, group = a.Hq / a.Hkv, kvh = u / tiles, tile = u % tiles;
+    // (lens stands since before the kernel that this one follows)
+    if (t < a.B) rounds[t] = (pa_len(a, t) + 63) / 64;
+    __syncthreads();
+    long long total = 0, first = 0;  // round of the unit
+    for (int i = 0; i < a.B; ++i) {
+        if (i < b) first += rounds[i];
+        total += rounds[i];
+    }
+    total *= units, first = first * units + (long long)u * rounds[b];
+    const long long ctas = min(static_cast<long long>(grid), total);
+    int c0 = 0, n = 0;
+    if (rounds[b] > 0) {
+        // round r is CTA c's, the largest with floor(c total / ctas) <= r
+        c0 = static_cast<int>(((first + 1) * ctas - 1) / total);
+        n = static_cast<int>(((first + rounds[b]) * ctas - 1) / total) - c0 + 1;
+    }
     pdl_wait();
     pdl_trigger();
-    const int4 u = parts.open[blockIdx.y];
-    const int n = u.w, hh = blockIdx.x, group = a.Hq / a.Hkv, kvh = u.y / tiles, tile = u.y % tiles;
-    if (n == 0 || tile * heads + hh >= group) return;
-    const int t = threadIdx.x, col = t % kCols, set = t / kCols, lane = t & 31, warp = t >> 5, d0 = (blockIdx.z * kCols + col) * 4;
-    const long long h = (long long)u.x * a.Hq + kvh * group + tile * heads + hh;
+    if (n <= 1 || tile * heads + hh >= group) return;  // no keys, or finished
+    const long long h = (long long)b * a.Hq + kvh * group + tile * heads + hh;
     // the first CTA's part is its second one
-    auto slot = [&](int i) { return 2ll * (u.z + i) + (i == 0 ? 1 : 0); };
-    // the parts' factors first: what is summed then hangs on no other load
-    constexpr int kHold = kSms * 4;  // CTAs of a launch, at most
-    __shared__ float factor[kHold];
+    auto slot = [&](int i) { return 2ll * (c0 + i) + (i == 0 ? 1 : 0); };
+    auto part = [&](int i) { return *reinterpret_cast<const float4*>(parts.acc + (slot(i) * heads + hh) * D + d0); };
+    constexpr int kAhead = 10;
+    float4 ahead[kAhead];
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k) ahead[k] = set + k * kPaSets < n ? part(set + k * kPaSets) : make_float4(0.f, 0.f, 0.f, 0.f);
     float top = -INFINITY;
     for (int i = t; i < n; i += kThreads) top = fmaxf(top, factor[i] = parts.ml[slot(i) * 2 * heads + hh]);
 #pragma unroll
     for (int m = 16; m >= 1; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
     if (lane == 0) red[0][warp] = top;
+    float l = t < n ? parts.ml[(slot(t) * 2 + 1) * heads + hh] : 0.f;
     __syncthreads();
 #pragma unroll
     for (int w = 0; w < kW; ++w) top = fmaxf(top, red[0][w]);
@@ -640,7 +650,8 @@ __global__ void __launch_bounds__(kPaSets* kPaCols) paged_attention_join_kernel(
     float sum = 0.f;
     for (int i = t; i < n; i += kThreads) {
         const float f = ex2(factor[i] - base);
-        sum += parts.ml[(slot(i) * 2 + 1) * heads + hh] * f;
+        if (i >= kThreads) l = parts.ml[(slot(i) * 2 + 1) * heads + hh];
+        sum += l * f;
         factor[i] = f;
     }
 #pragma unroll
@@ -648,12 +659,14 @@ __global__ void __launch_bounds__(kPaSets* kPaCols) paged_attention_join_kernel(
     if (lane == 0) red[1][warp] = sum;
     __syncthreads();
     float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll 8
-    for (int i = set; i < n; i += kPaSets) {
-        const float4 p = *reinterpret_cast<const float4*>(parts.acc + (slot(i) * heads + hh) * D + d0);
+    auto add = [&](int i, const float4& p) {
         const float f = factor[i];
         v.x += f * p.x, v.y += f * p.y, v.z += f * p.z, v.w += f * p.w;
-    }
+    };
+#pragma unroll
+    for (int k = 0; k < kAhead; ++k)
+        if (set + k * kPaSets < n) add(set + k * kPaSets, ahead[k]);
+    for (int i = set + kAhead * kPaSets; i < n; i += kPaSets) add(i, part(i));
     sums[set][col] = v;
     __syncthreads();
     if (set != 0) return;
@@ -688,11 +701,11 @@ int pa_route(long long units, int rounds, int ctas) {
 struct PaPlan {
     int nt, heads, tiles, ctas, cluster;
     long long units;
-    size_t acc, ml, open, total;
+    size_t acc, ml, total;
 };
 template <int D>
 int pa_ctas(int nt) {
-    return kSms * (nt == 1 ? PaCfg<D, 1>::kCtas : PaCfg<D, 2>::kCtas);
+    return kSms * (nt == 1 ? PaCfg<D, 1>::kCtas : PaCfg<D, D == 256 ? 1 : 2>::kCtas);
 }
 PaPlan pa_plan(int B, int Hq, int Hkv, int d, int max_len) {
     PaPlan p{};
@@ -708,8 +721,7 @@ PaPlan pa_plan(int B, int Hq, int Hkv, int d, int max_len) {
     if (p.cluster) return p;
     p.acc = 0;
     p.ml = p.acc + static_cast<size_t>(2) * p.ctas * p.heads * d * 4;
-    p.open = p.ml + static_cast<size_t>(2) * p.ctas * 2 * p.heads * 4;
-    p.total = p.open + static_cast<size_t>(p.units) * sizeof(int4);
+    p.total = p.ml + static_cast<size_t>(2) * p.ctas * 2 * p.heads * 4;
     return p;
 }
 PaDiv pa_div(int d) {
@@ -735,7 +747,8 @@ cudaError_t launch_nt(const PagedAttnArgs& a, const PaPlan& p, const PaParts& pa
     const unsigned grid = static_cast<unsigned>(p.cluster ? p.units * p.cluster : p.ctas);
     e = launch_kernel(f, dim3(grid), dim3(C::kThreads), C::kSmem, true, s, args);
     if (e != cudaSuccess || p.cluster) return e;
-    void* jargs[] = {const_cast<PagedAttnArgs*>(&a), &tiles, &heads, const_cast<PaParts*>(&parts)};
+    int ctas = p.ctas;
+    void* jargs[] = {const_cast<PagedAttnArgs*>(&a), &tiles, &heads, &ctas, const_cast<PaParts*>(&parts)};
     const int group = a.Hq / a.Hkv;
     return launch_kernel(reinterpret_cast<const void*>(paged_attention_join_kernel<DT, D>),
                          dim3(heads < group ? heads : group, static_cast<unsigned>(p.units), D / (4 * kPaCols)), dim3(kPaSets * kPaCols), 0, true, s,
@@ -756,7 +769,7 @@ size_t paged_attention_ws_bytes(int B, int Hq, int Hkv, int d, int max_len) { re
 cudaError_t launch_paged_attention(const PagedAttnArgs& a, int dtype, void* ws, cudaStream_t s) {
     const PaPlan p = pa_plan(a.B, a.Hq, a.Hkv, a.d, a.max_len);
     char* w = static_cast<char*>(ws);
-    const PaParts parts{reinterpret_cast<float*>(w + p.acc), reinterpret_cast<float*>(w + p.ml), reinterpret_cast<int4*>(w + p.open)};
+    const PaParts parts{reinterpret_cast<float*>(w + p.acc), reinterpret_cast<float*>(w + p.ml)};
     return dtype == 1 ? launch_dt<1>(a, p, parts, s) : launch_dt<2>(a, p, parts, s);
 }
 

@@ -53,11 +53,15 @@ struct LpRecord {  // a part of a row
     float m, s, t, pad;
     unsigned long long key[kLogprobMaxTop];
 };
-// Where parts go: two records a CTA (a row that began before its range; one
-// that goes on behind it) and that last row with the number of its parts.
-struct LpParts {
-    LpRecord* rec;  // [G][2]
-    int2* open;     // [G]
+// All rows' units cut into ranges, one a CTA: `per` units, one more for the first `rest`.
+struct LpCut {
+    long long per;
+    int units, rest;  // units: of a row
+    __device__ __forceinline__ long long begin(int cta) const { return cta * per + min(cta, rest); }
+    __device__ __forceinline__ int cta_of(long long unit) const {
+        const long long longer = rest * (per + 1);
+        return static_cast<int>(unit < longer ? unit / (per + 1) : rest + (unit - longer) / per);
+    }
 };
 
 __device__ __forceinline__ float ex2(float x) {
@@ -494,7 +498,7 @@ constexpr int kLpCtas = 2;  // a multiprocessor, each lane with two chunks of lo
 // With kCluster > 1 a cluster of CTAs shares a row evenly instead, and its first
 // CTA joins the parts.
 template <int DT, int kCluster>
-__device__ __forceinline__ void lp_ranges(const LogprobArgs& a, int units, long long per, int rest, LpParts out) {
+__device__ __forceinline__ void lp_ranges(const LogprobArgs& a, const LpCut& cut, LpRecord* rec) {
     using V = LpVec<DT>;
     constexpr int N = V::N, kLpLoads = kLpValues / N;
     constexpr int size = DT == 3 ? 4 : 2;
@@ -511,19 +515,18 @@ __device__ __forceinline__ void lp_ranges(const LogprobArgs& a, int units, long 
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, cta = blockIdx.x, rank = kCluster > 1 ? cta % kCluster : 0;
     long long at, end;
     int row, u0;
+    const int units = cut.units;
     if (kCluster > 1) {
         row = cta / kCluster;
         u0 = static_cast<int>(static_cast<long long>(rank) * units / kCluster);
         at = 0, end = static_cast<long long>(rank + 1) * units / kCluster - u0;
     } else {
-        at = cta * per + min(cta, rest);
-        end = at + per + (cta < rest ? 1 : 0);
+        at = cut.begin(cta), end = cut.begin(cta + 1);
         if (at >> 32) {
             row = static_cast<int>(at / units), u0 = static_cast<int>(at % units);
         } else {
             row = static_cast<int>(static_cast<unsigned>(at) / units), u0 = static_cast<int>(static_cast<unsigned>(at) % units);
         }
-        if (threadIdx.x == 0 && out.open != nullptr) out.open[cta] = make_int2(0, 0);
     }
     for (bool one = kCluster > 1; one || at < end; ++row, u0 = 0, one = false) {
         const int u1 = static_cast<int>(min(static_cast<long long>(units), u0 + (end - at)));
@@ -634,15 +637,10 @@ __device__ __forceinline__ void lp_ranges(const LogprobArgs& a, int units, long 
             if (u0 == 0 && u1 == units) {
                 lp_finish<DT>(a, row, w.p, key, given, lane);
             } else {
-                LpRecord* to = out.rec + 2ll * cta + (u0 == 0 ? 1 : 0);
+                // two records a CTA: of a row that began before its range, and of one that goes on behind it
+                LpRecord* to = rec + 2ll * cta + (u0 == 0 ? 1 : 0);
                 if (lane == 0) to->m = w.p.m, to->s = w.p.s, to->t = w.p.t;
                 to->key[lane] = key;
-                if (lane == 0 && u0 == 0) {
-                    // the CTA that holds the row's last unit
-                    const long long z = at + units - 1, longer = rest * (per + 1);
-                    const long long c = z < longer ? z / (per + 1) : rest + (z - longer) / per;
-                    out.open[cta] = make_int2(row, static_cast<int>(c) - cta + 1);
-                }
             }
         }
         at += u1 - u0;
@@ -651,13 +649,13 @@ __device__ __forceinline__ void lp_ranges(const LogprobArgs& a, int units, long 
 
 template <int DT>
 __global__ void __launch_bounds__(kLpThreads, kLpCtas)
-    token_logprobs_kernel(LogprobArgs a, int units, long long per, int rest, LpParts out) {
-    lp_ranges<DT, 1>(a, units, per, rest, out);
+    token_logprobs_kernel(LogprobArgs a, LpCut cut, LpRecord* rec) {
+    lp_ranges<DT, 1>(a, cut, rec);
 }
 template <int DT, int kCluster>
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kLpThreads, kLpCtas)
-    token_logprobs_cluster_kernel(LogprobArgs a, int units) {
-    lp_ranges<DT, kCluster>(a, units, 0, 0, LpParts{});
+    token_logprobs_cluster_kernel(LogprobArgs a, LpCut cut) {
+    lp_ranges<DT, kCluster>(a, cut, nullptr);
 }
 
 // Short rows: a warp each, with no barrier among the warps.
@@ -713,17 +711,17 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_rows_kerne
 
 // Joins the parts of the row that begins in CTA c's range and goes on behind it.
 template <int DT>
-__global__ void __launch_bounds__(kLpThreads) token_logprobs_join_kernel(LogprobArgs a, LpParts in) {
+__global__ void __launch_bounds__(kLpThreads) token_logprobs_join_kernel(LogprobArgs a, LpCut cut, const LpRecord* recs) {
     extern __shared__ unsigned long long lp_smem[];  // two lists of 32 keys a part
     __shared__ unsigned long long best[kLogprobMaxTop];
     pdl_wait();
     pdl_trigger();
-    const int2 o = in.open[blockIdx.x];
-    const int row = o.x, n = o.y;
-    if (n == 0) return;
+    const long long end = cut.begin(blockIdx.x + 1), start = (end - 1) / cut.units * cut.units;
+    if (start < cut.begin(blockIdx.x) || start + cut.units == end) return;  // it began before, or it ends here
+    const int row = static_cast<int>(start / cut.units), n = cut.cta_of(start + cut.units - 1) - blockIdx.x + 1;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     // the first CTA's part is its second record
-    auto rec = [&](int i) { return in.rec + 2ll * (blockIdx.x + i) + (i == 0 ? 1 : 0); };
+    auto rec = [&](int i) { return recs + 2ll * (blockIdx.x + i) + (i == 0 ? 1 : 0); };
     LpGiven given{-1, 0.f};
     if (warp == 0) given = lp_given<DT>(a, row, lane);
     LpWarp w = lp_start();
@@ -757,8 +755,8 @@ int lp_route(int M, int V, int size) {
 }
 
 struct LpPlan {
-    int units, ctas, rest, most_parts;
-    long long per;
+    LpCut cut;
+    int ctas, most_parts;
     bool join;
 };
 // kLpCtas CTAs a multiprocessor, while each has a row or 2048 values at least; at
@@ -766,15 +764,15 @@ struct LpPlan {
 LpPlan lp_plan(int M, int V, int dtype) {
     LpPlan p;
     const int per = 32 * 16 / (dtype == 3 ? 4 : 2);
-    p.units = (V + per - 1) / per;
-    const long long want = std::max<long long>(M, (long long)M * V / 2048), total = (long long)M * p.units;
+    p.cut.units = (V + per - 1) / per;
+    const long long want = std::max<long long>(M, (long long)M * V / 2048), total = (long long)M * p.cut.units;
     p.ctas = static_cast<int>(std::min<long long>(std::min<long long>(kLpCtas * kSms, want), 74ll * M));
-    p.per = total / p.ctas;
-    p.rest = static_cast<int>(total % p.ctas);
-    p.join = p.rest != 0 || p.per % p.units != 0;
+    p.cut.per = total / p.ctas;
+    p.cut.rest = static_cast<int>(total % p.ctas);
+    p.join = p.cut.rest != 0 || p.cut.per % p.cut.units != 0;
     // ranges of `per` units and more that meet a row's units (a row behind the first `rest` ranges meets more than an
     // even share of them): 85 at most, as a range has 8 units or a row and more
-    p.most_parts = std::min(p.ctas, std::max(p.units - 2, 0) / static_cast<int>(std::min<long long>(p.per, p.units)) + 2);
+    p.most_parts = std::min(p.ctas, std::max(p.cut.units - 2, 0) / static_cast<int>(std::min<long long>(p.cut.per, p.cut.units)) + 2);
     return p;
 }
 
@@ -789,35 +787,31 @@ cudaError_t launch_dt(const LogprobArgs& a, void* ws, cudaStream_t s) {
     }
     LpPlan p = lp_plan(a.M, a.V, DT);
     if (route > 1) {
-        void* args[] = {const_cast<LogprobArgs*>(&a), &p.units};
+        void* args[] = {const_cast<LogprobArgs*>(&a), &p.cut};
         const void* f = route == 8   ? reinterpret_cast<const void*>(token_logprobs_cluster_kernel<DT, 8>)
                         : route == 4 ? reinterpret_cast<const void*>(token_logprobs_cluster_kernel<DT, 4>)
                                      : reinterpret_cast<const void*>(token_logprobs_cluster_kernel<DT, 2>);
         return launch_kernel(f, dim3(a.M * route), dim3(kLpThreads), 0, true, s, args);
     }
     if (route == 1) {  // ranges of a row each
-        LpParts none{};
-        long long per = p.units;
-        int rest = 0;
-        void* args[] = {const_cast<LogprobArgs*>(&a), &p.units, &per, &rest, &none};
-        return launch_kernel(reinterpret_cast<const void*>(token_logprobs_kernel<DT>), dim3(a.M), dim3(kLpThreads), 0, true, s,
-                             args);
+        p.cut.per = p.cut.units, p.cut.rest = 0;
+        p.ctas = a.M;
+        p.join = false;
     }
-    LpParts parts{static_cast<LpRecord*>(ws), reinterpret_cast<int2*>(static_cast<LpRecord*>(ws) + 2 * p.ctas)};
-    void* args[] = {const_cast<LogprobArgs*>(&a), &p.units, &p.per, &p.rest, &parts};
+    LpRecord* rec = static_cast<LpRecord*>(ws);
+    void* args[] = {const_cast<LogprobArgs*>(&a), &p.cut, &rec};
     cudaError_t e = launch_kernel(reinterpret_cast<const void*>(token_logprobs_kernel<DT>), dim3(p.ctas), dim3(kLpThreads), 0,
                                   true, s, args);
     if (e != cudaSuccess || !p.join) return e;
-    void* jargs[] = {const_cast<LogprobArgs*>(&a), &parts};
     return launch_kernel(reinterpret_cast<const void*>(token_logprobs_join_kernel<DT>), dim3(p.ctas), dim3(kLpThreads),
-                         a.top > 0 ? p.most_parts * 32 * 2 * 8 : 0, true, s, jargs);
+                         a.top > 0 ? p.most_parts * 32 * 2 * 8 : 0, true, s, args);
 }
 
 }  // namespace
 
 size_t token_logprobs_ws_bytes(int M, int V) {
     if (lp_route(M, V, 4) != kLpCut) return 0;  // nor do 16-bit rows, half as long, go by it then
-    return static_cast<size_t>(lp_plan(M, V, 3).ctas) * (2 * sizeof(LpRecord) + sizeof(int2));
+    return static_cast<size_t>(lp_plan(M, V, 3).ctas) * 2 * sizeof(LpRecord);
 }
 
 cudaError_t launch_token_logprobs(const LogprobArgs& a, int dtype, void* ws, cudaStream_t s) {

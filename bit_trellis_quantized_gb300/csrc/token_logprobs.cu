@@ -6,7 +6,9 @@
 //   lse = ln2 (M + log2 s),  logprob(id) = ln2 (z_id - log2 s),
 //   entropy = ln2 (log2 s - t / s).
 // z is one fma with M rounded; as everything goes by that M, its rounding
-// cancels. Where |m| is 1e37 or more (c x may overflow), z = (x - m) c.
+// cancels. That holds while the rounding, half a step of M, is a small part of an
+// exponent: where |m| is 2^20 or more (a row, or what a lane has seen of it, is
+// masked with some -1e9, say), M is c m itself, as z = (x - m) c.
 // Two parts join over the larger maximum, f = 2^(M1 - M):
 //   s = f s1 + ...,  t = f (t1 + (M1 - M) s1) + ...
 // All in f32; m starts at the lowest finite value, so -inf logits (banned
@@ -70,17 +72,16 @@ __device__ __forceinline__ float ex2(float x) {
     return r;
 }
 
-constexpr float kFar = 1e37f;
+// Below this M is rounded, by 2^-4 at most. At 1e9 that would be up to 2^6, and from 1e10 on 2^z could leave the range of f32.
+constexpr float kFar = 0x1p20f;
 
-// M: always this rounded product (never contracted into a sum), see above.
+// M of |m| < kFar: always this rounded product (never contracted into a sum), see above.
 __device__ __forceinline__ float lp_scaled(float m) { return __fmul_rn(m, kLog2e); }
-// c x - M in units of ln 2
-__device__ __forceinline__ float lp_z(float x, float m) {
-    return fabsf(m) < kFar ? fmaf(x, kLog2e, -lp_scaled(m)) : (x - m) * kLog2e;
-}
-// the same between two maxima
+// M of a less M of m, each as its size has it: c a less M of m, less what c a is above M of a
 __device__ __forceinline__ float lp_shift(float a, float m) {
-    return fabsf(a) < kFar && fabsf(m) < kFar ? lp_scaled(a) - lp_scaled(m) : (a - m) * kLog2e;
+    const bool m_near = fabsf(m) < kFar;
+    const float d = fmaf(m_near ? a : a - m, kLog2e, m_near ? -lp_scaled(m) : 0.f);
+    return d - (fabsf(a) < kFar ? fmaf(a, kLog2e, -lp_scaled(a)) : 0.f);
 }
 
 __device__ __forceinline__ LpPart lp_join(const LpPart& a, const LpPart& b) {
@@ -244,10 +245,9 @@ __device__ __forceinline__ void st_cluster_u64(uint32_t addr, unsigned long long
 }
 
 // Adds a chunk, kLpValues values of each lane (places past the end hold -inf), to the lane's sums; gives their
-// largest. `buf`: the warp's 32 kLpValues / N vectors of shared memory.
+// largest.
 template <int DT>
-__device__ __forceinline__ float lp_sums(LpPart& p, const uint4 (&r)[kLpValues / LpVec<DT>::N],
-                                         uint4* buf, int lane) {
+__device__ __forceinline__ float lp_sums(LpPart& p, const uint4 (&r)[kLpValues / LpVec<DT>::N]) {
     using V = LpVec<DT>;
     constexpr int N = V::N, kLpLoads = kLpValues / N;
     float b = -INFINITY;
@@ -265,10 +265,11 @@ __device__ __forceinline__ float lp_sums(LpPart& p, const uint4 (&r)[kLpValues /
         p.m = b;
     }
     const bool empty = b == -INFINITY && p.m == kLowest;  // this lane has seen nothing but -inf (or NaN)
-    if (!__any_sync(0xffffffffu, !empty && !(fabsf(p.m) < kFar))) {
-        const float M = empty ? 0.f : lp_scaled(p.m);
-        const unsigned long long c2 = pack2(kLog2e, kLog2e), m2 = pack2(-M, -M);
-        unsigned long long s2 = 0ull, t2 = 0ull;
+    const bool far = !empty && !(fabsf(p.m) < kFar);
+    const float M = empty || far ? 0.f : lp_scaled(p.m);
+    const unsigned long long c2 = pack2(kLog2e, kLog2e), m2 = pack2(-M, -M);
+    unsigned long long s2 = 0ull, t2 = 0ull;
+    auto add = [&](auto&& z2) {
 #pragma unroll
         for (int i = 0; i < kLpLoads; ++i) {
             float x[N];
@@ -276,35 +277,26 @@ __device__ __forceinline__ float lp_sums(LpPart& p, const uint4 (&r)[kLpValues /
 #pragma unroll
             for (int j = 0; j < N; j += 2) {
                 float z0, z1;
-                unpack2(fma2(pack2(x[j], x[j + 1]), c2, m2), z0, z1);
+                unpack2(z2(pack2(x[j], x[j + 1])), z0, z1);
                 z0 = max_nan(z0, -160.f), z1 = max_nan(z1, -160.f);  // 2^-160 is 0: -inf times it would not be
                 const unsigned long long e = pack2(ex2(z0), ex2(z1));
                 s2 = add2(s2, e);
                 t2 = fma2(pack2(z0, z1), e, t2);
             }
         }
-        float s0, s1, t0, t1;
-        unpack2(s2, s0, s1);
-        unpack2(t2, t0, t1);
-        p.s += s0 + s1;
-        p.t += t0 + t1;
+    };
+    if (!__any_sync(0xffffffffu, far)) {
+        add([&](unsigned long long x) { return fma2(x, c2, m2); });
     } else {
-        __syncwarp();
-#pragma unroll
-        for (int i = 0; i < kLpLoads; ++i) buf[i * 32 + lane] = r[i];
-        __syncwarp();
-#pragma unroll 1
-        for (int i = 0; i < kLpLoads; ++i) {
-            float x[N];
-            V::get(buf[i * 32 + lane], x);
-#pragma unroll
-            for (int j = 0; j < N; ++j) {
-                const float z = max_nan(lp_z(x[j], p.m), -160.f), e = ex2(z);
-                p.s += e;
-                p.t += z * e;
-            }
-        }
+        const float d = far ? -p.m : 0.f;
+        const unsigned long long d2 = pack2(d, d);
+        add([&](unsigned long long x) { return fma2(add2(x, d2), c2, m2); });
     }
+    float s0, s1, t0, t1;
+    unpack2(s2, s0, s1);
+    unpack2(t2, t0, t1);
+    p.s += s0 + s1;
+    p.t += t0 + t1;
     return b;
 }
 
@@ -460,7 +452,8 @@ __device__ __forceinline__ void lp_finish(const LogprobArgs& a, int row, const L
     const bool none = p.s == 0.f;  // every logit is -inf
     auto logprob = [&](float v) {
         if (none) return -INFINITY;
-        return fabsf(v) < kFar && fabsf(p.m) < kFar ? kLn2 * (lp_z(v, p.m) - ls) : (v - p.m) - kLn2 * ls;
+        // (c v of an |v| near the type's end would overflow; there M's rounding is nothing beside v)
+        return fabsf(p.m) < kFar && fabsf(v) < 1e37f ? kLn2 * (fmaf(v, kLog2e, -lp_scaled(p.m)) - ls) : (v - p.m) - kLn2 * ls;
     };
     if (lane == 0) {
         if (a.lse) a.lse[row] = none ? -INFINITY : fabsf(p.m) < kFar ? kLn2 * (lp_scaled(p.m) + ls) : p.m + kLn2 * ls;
@@ -583,7 +576,7 @@ __device__ __forceinline__ void lp_ranges(const LogprobArgs& a, const LpCut& cut
             if (v >= last) continue;
             uint4 ahead[kLpLoads];
             load(ahead, v + 32 * kLpLoads);
-            const float most = lp_sums<DT>(w.p, r, buf[warp], lane);
+            const float most = lp_sums<DT>(w.p, r);
             if (a.top > 0)
                 lp_collect<DT, kLpKept>(w, r, most, buf[warp], &kept, a.top, lane, [&](int i, int j) {
                     const int k = v + i * 32 + lane;
@@ -597,7 +590,7 @@ __device__ __forceinline__ void lp_ranges(const LogprobArgs& a, const LpCut& cut
 #pragma unroll
             for (int i = 0; i < kLpLoads; ++i) r[i] = make_uint4(V::kNone, V::kNone, V::kNone, V::kNone);
             r[0] = V::two(lane < head ? V::one(x, lane) : -INFINITY, tail + lane < a.V ? V::one(x, tail + lane) : -INFINITY);
-            const float most = lp_sums<DT>(w.p, r, buf[0], lane);
+            const float most = lp_sums<DT>(w.p, r);
             if (a.top > 0)
                 lp_collect<DT, kLpKept>(w, r, most, buf[0], &kept, a.top, lane, [&](int i, int j) {
                     return i > 0 ? -1 : j == 0 && lane < head ? lane : j == 1 && tail + lane < a.V ? tail + lane : -1;
@@ -684,7 +677,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_rows_kerne
                 if (v + i * 32 + lane < nv)
                     r[i] = ldg_stream_v4(x + (long long)head * size + (long long)(v + i * 32 + lane) * 16);
             }
-            const float b = lp_sums<DT>(w.p, r, buf[warp], lane);
+            const float b = lp_sums<DT>(w.p, r);
             if (a.top > 0) {
                 const unsigned kth = lp_nth(lp_order(b), a.top, lane);
                 w.thr = fmaxf(w.thr, lp_from_order(kth));
@@ -698,7 +691,7 @@ __global__ void __launch_bounds__(kLpThreads, kLpCtas) token_logprobs_rows_kerne
 #pragma unroll
             for (int i = 0; i < kLpLoads; ++i) r[i] = make_uint4(V::kNone, V::kNone, V::kNone, V::kNone);
             r[0] = V::two(lane < head ? V::one(x, lane) : -INFINITY, tail + lane < a.V ? V::one(x, tail + lane) : -INFINITY);
-            const float most = lp_sums<DT>(w.p, r, buf[warp], lane);
+            const float most = lp_sums<DT>(w.p, r);
             if (a.top > 0)
                 lp_collect<DT, 0>(w, r, most, buf[warp], nullptr, a.top, lane, [&](int i, int j) {
                     return i > 0 ? -1 : j == 0 && lane < head ? lane : j == 1 && tail + lane < a.V ? tail + lane : -1;

@@ -224,3 +224,54 @@ def test_refusals():
                    (ValueError, (x[:1].expand(4, 100), ids))):
         with pytest.raises(exc):
             native.token_logprobs(*a)
+
+
+# by the way that rows are dealt out: a warp a row, a CTA, clusters of 4, 8 and 2, cut over all CTAs
+WAYS = [(14, 50, d) for d in DT] + [(14, 5000, d) for d in DT] + [(14, 12001, d) for d in DT] + [
+    (14, 30001, d) for d in DT] + [(70, 30004, d) for d in DT] + [(14, 1400001, "f16"), (14, 1400001, "bf16"), (14, 700001, "f32")]
+
+
+@pytest.mark.parametrize("M,V,dtype", WAYS)
+def test_finite_masks_and_far_maxima(M, V, dtype):
+    """Tokens masked with finite values of every size, in runs longer than all
+    that a lane, a warp and a CTA read; rows whose largest value is far from 0;
+    values on both sides of 2^20 within reach of each other."""
+    native = _native()
+    rng = np.random.default_rng(41)
+    x = torch.from_numpy(rng.standard_normal((M, V)) * 3).float().cuda()
+    masks, far, edge = (1e9, 1e10, 1e20, 1e30, 1e36), (1e10, 1e30), 2.0 ** 20
+    if dtype == "f16":  # as far as the type goes
+        masks, far, edge = (6e4,) * 5, (6e4, 65504.0), 6e4
+    keep = (slice(7, 12), slice(V - V // 4, V), slice(V - 3, V - 2), slice(V // 3, V // 3 + 9), slice(0, 1))
+    for i in range(M):
+        k, y = i % 14, x[i].clone()
+        if k < 5:
+            x[i] = -masks[k]
+            x[i, keep[k]] = y[keep[k]]
+        elif k == 5:  # three masks, and what is left
+            x[i, :V // 5], x[i, V // 5:V // 2], x[i, V // 2:V - V // 5] = -masks[0], -masks[1], -masks[2]
+        elif k == 6:
+            x[i] = -far[0]
+        elif k == 7:
+            x[i] = far[1]
+        elif k == 8:
+            x[i, V // 2] = far[0]
+        elif k == 9:
+            x[i] = y * far[0] / 100 - far[0]
+        elif k == 10:
+            x[i] = y + edge
+        elif k == 11:
+            x[i] = y - edge
+        elif k == 12:
+            x[i] = y * 5 + 0.95 * edge
+        else:
+            x[i] = y * 5 - 0.95 * edge
+    x = x.to(DT[dtype])
+    if dtype == "f16":
+        x = x.clamp(-65504, 65504)
+    assert bool(x.isfinite().all())
+    ids = rng.integers(0, V, (M, 4))
+    ids[:, 0], ids[:, 1] = V - 3, 8
+    r = run_and_check(native, x, ids, 32)
+    none = native.token_logprobs(x, torch.from_numpy(ids.astype(np.int32)).cuda())
+    assert all(torch.equal(r[k], none[k]) for k in ("lse", "entropy", "logprobs"))  # the sums do not hang on the top list

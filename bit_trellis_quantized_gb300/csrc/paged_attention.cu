@@ -125,6 +125,9 @@ __device__ __forceinline__ int pa_len(const PagedAttnArgs& a, int b) {
     return max(0, min(a.lens[b], most));
 }
 
+// The new token's position, -1: none, as where its sequence's length was cut to `len`.
+__device__ __forceinline__ int pa_new(const PagedAttnArgs& a, int b, int len) { return a.k_new && a.lens[b] == len ? len - 1 : -1; }
+
 // The parts of units cut over CTAs: 8 NT heads' weighted values, then their maxima and sums.
 struct PaParts {
     float* acc;  // [2 CTAs][heads][D]: a CTA's first part of a unit begun before its range, its part of one that goes on
@@ -147,7 +150,7 @@ __device__ __forceinline__ float2 ld_cluster_f32x2(uint32_t addr) {
 constexpr int kPaSort = 64;
 // A place in the list of rounds: round r of one (sequence, key head, tile of heads).
 struct PaPlace {
-    int b, kvh, tile, r, rounds, len;
+    int b, kvh, tile, r, rounds, len, fresh;  // fresh: the new token's position
     template <int kRound>
     __device__ __forceinline__ void next(const PagedAttnArgs& a, int tiles) {
         if (++r < rounds) return;
@@ -162,6 +165,7 @@ struct PaPlace {
                 return;
             }
             len = pa_len(a, b);
+            fresh = pa_new(a, b, len);
             rounds = (len + kRound - 1) / kRound;
         } while (rounds == 0);
     }
@@ -211,6 +215,7 @@ __device__ __forceinline__ void pa_units(const PagedAttnArgs& a, int tiles, cons
             cur.b = first_s[0];
         }
         cur.len = pa_len(a, cur.b);
+        cur.fresh = pa_new(a, cur.b, cur.len);
         cur.rounds = (cur.len + kRound - 1) / kRound;
         cur.r = static_cast<int>(static_cast<long long>(cur.rounds) * rank / kShare);
         left = static_cast<long long>(cur.rounds) * (rank + 1) / kShare - cur.r;
@@ -260,6 +265,7 @@ __device__ __forceinline__ void pa_units(const PagedAttnArgs& a, int tiles, cons
         }
         __syncthreads();
         cur.b = first_s[0], cur.kvh = first_s[1] / tiles, cur.tile = first_s[1] % tiles, cur.r = first_s[2], cur.len = first_s[3];
+        cur.fresh = pa_new(a, cur.b, cur.len);
         cur.rounds = (cur.len + kRound - 1) / kRound;
     }
 
@@ -283,7 +289,7 @@ __device__ __forceinline__ void pa_units(const PagedAttnArgs& a, int tiles, cons
     // one half of the round: its keys (pool kp, new rows kn) or values
     auto load = [&](uint32_t to, const char* pool, const void* fresh) {
         const char* base = pool + c8 * 16;
-        const int newest = a.k_new ? ld.len - 1 - (ld.r * kRound + warp * 16) : -1;  // the new token's row
+        const int newest = ld.fresh - (ld.r * kRound + warp * 16);  // the new token's row
         if (static_cast<unsigned>(newest) < 16u) {
             const char* nw = static_cast<const char*>(fresh) + ((long long)ld.b * a.Hkv + ld.kvh) * C::kRow + c8 * 16;
             const int there = __shfl_sync(0xffffffffu, row, newest);

@@ -573,7 +573,9 @@ def paged_attention(q, k_pool, v_pool, table, lens, k_new=None, v_new=None, scal
     [n_pages][Hkv][page][d]; table int32 [B][max_pages]; lens int32 [B], the
     new token counted. k_new, v_new [B][Hkv][d] are stored at position lens - 1
     and attended. ``scale`` is 1 / sqrt(d) by default; ``max_len`` a host-side
-    bound of lens (by default the table's). Returns (out, lse f32 [B][Hq])."""
+    bound of lens (by default the table's): keys behind it are not read, and a
+    sequence whose length is above it neither stores nor attends its new token.
+    Returns (out, lse f32 [B][Hq])."""
     if q.dim() != 3 or k_pool.dim() != 4 or table.dim() != 2:
         raise ValueError("q is [B][Hq][d], the pools [n_pages][Hkv][page][d], table [B][max_pages]")
     B, Hq, d = q.shape

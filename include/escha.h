@@ -519,7 +519,8 @@ int escha_moe_route(const escha_moe_layer* L, const uint16_t* x, int T, uint16_t
  *            gives out = 0 and lse = -infinity, and nothing is written for it.
  *   k_new, v_new  [B][Hkv][d] or both NULL: the new token's key and value,
  *            stored at position lens[b] - 1 by the call and attended with the
- *            rest. Sequences may share pages, but not the page that holds
+ *            rest; where lens[b] is above that bound, neither stored nor
+ *            attended. Sequences may share pages, but not the page that holds
  *            another's position lens - 1 (copy it first), and no table names
  *            the page of its own new token twice. When the page entry
  *            of that position is outside [0, n_pages), the new token is

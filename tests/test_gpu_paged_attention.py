@@ -254,3 +254,30 @@ def test_refusals():
     one = make(19, [40], 4, 2, 64, 32, "f16")
     with pytest.raises(native.EschaError, match="workspace"):
         native.paged_attention(one["q"], one["k"], one["v"], wide, one["lens"], ws=torch.empty(16, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("dtype,lens,cap,Hq,Hkv,d,page", [
+    ("f16", [48, 33, 1 << 30, 32, 0], 33, 4, 2, 64, 16), ("bf16", [400, 200, 201] * 30, 200, 16, 4, 128, 32),
+    ("f16", [700, 699, 650], 699, 16, 2, 256, 64), ("bf16", [5000, 4501, 4500], 4500, 24, 1, 128, 32),
+    ("f16", [9000], 8999, 16, 1, 64, 48)])
+def test_no_new_token_behind_the_bound(dtype, lens, cap, Hq, Hkv, d, page):
+    """A length past max_len, or past what its row of the table holds, has no
+    place for the new token: it is not stored over a key that is there, and not
+    attended."""
+    native = _native()
+    for by_table in (False, True):
+        c = make(18, [min(n, 10000) for n in lens], Hq, Hkv, d, page, dtype, poison=False)
+        c["lens"] = torch.tensor(lens, dtype=torch.int32, device="cuda")
+        bound = cap // page * page if by_table else cap
+        kw = {} if by_table else dict(max_len=cap)
+        if by_table:
+            c["table"] = c["table"][:, :cap // page].contiguous()
+        want = c["k"].clone(), c["v"].clone()
+        for b, n in enumerate(lens):
+            if 0 < n <= bound:
+                pg = int(c["table"][b, (n - 1) // page])
+                want[0][pg, :, (n - 1) % page], want[1][pg, :, (n - 1) % page] = c["k_new"][b], c["v_new"][b]
+        out, lse = native.paged_attention(c["q"], c["k"], c["v"], c["table"], c["lens"], k_new=c["k_new"], v_new=c["v_new"], **kw)
+        torch.cuda.synchronize()
+        assert torch.equal(c["k"], want[0]) and torch.equal(c["v"], want[1])
+        check(c, out, lse, d ** -0.5, dtype, cap=bound)

@@ -316,3 +316,20 @@ def test_one_long_sequence(dtype, T, before, Hk, Hv, dk, dv):
         graph.replay()
     torch.cuda.synchronize()
     assert torch.equal(st, state) and np.array_equal(f64(out), got)
+
+
+@pytest.mark.parametrize("lens,chunks", [([1] * 255 + [2000], True), ([0] * 255 + [2000], True), ([1] * 63 + [500], True),
+                                         ([700], True), ([12, 1], True), ([1] * 100, False), ([0, 1] * 40, False),
+                                         ([3] * 50, False), ([9], False)])
+def test_without_max_len_a_long_sequence_among_short_ones_goes_in_chunks(lens, chunks):
+    """Only chunks need a workspace. The rows are right either way."""
+    native = _native()
+    c = make(35, lens, 1, 2, 64, 32, "f16")
+    run_and_check(native, c, "f16")
+    call = dict(state=c["state"].clone(), ws=torch.empty(16, dtype=torch.uint8, device="cuda"))
+    args = {x: c[x] for x in ("q", "k", "v", "g", "beta", "at")}
+    if chunks:
+        with pytest.raises(native.EschaError, match="workspace"):
+            native.delta_rule(**args, **call)
+    else:
+        native.delta_rule(**args, **call)

@@ -41,7 +41,7 @@ struct DeltaArgs {
     int n, T, Hk, Hv, dk, dv, max_len;
     float scale, eps;
 };
-size_t delta_rule_ws_bytes(int n, int T, int Hk, int Hv, int dk, int dv, int max_len);
+size_t delta_rule_ws_bytes(int dtype, int n, int T, int Hk, int Hv, int dk, int dv, int max_len);
 cudaError_t launch_delta_rule(const DeltaArgs& a, int dtype, void* ws, cudaStream_t s);
 
 struct LogprobArgs {

@@ -889,15 +889,16 @@ constexpr int kChunkFrom = 10;
 
 struct DrPlan {
     bool chunks;
-    size_t kf, qf, total;  // chunk data first; then, for bf16, the keys and queries in fp16
+    size_t kf, qf, total;  // chunk data first; then, for bf16 alone, the keys and queries in fp16
 };
-DrPlan dr_plan(int n, int T, int Hk, int Hv, int dk, int max_len) {
+DrPlan dr_plan(int dtype, int n, int T, int Hk, int Hv, int dk, int max_len) {
     DrPlan p{};
     p.chunks = max_len >= kChunkFrom;
     if (!p.chunks) return p;
     p.kf = static_cast<size_t>(dr_slots(T, n)) * Hv * sizeof(DrChunk);
-    p.qf = p.kf + static_cast<size_t>(T) * Hk * dk * 2;
-    p.total = p.qf + static_cast<size_t>(T) * Hk * dk * 2;
+    const size_t each = dtype == 1 ? 0 : static_cast<size_t>(T) * Hk * dk * 2;
+    p.qf = p.kf + each;
+    p.total = p.qf + each;
     return p;
 }
 
@@ -913,7 +914,7 @@ cudaError_t launch_walk(const DeltaArgs& a, const uint16_t* kf, const uint16_t* 
 
 template <int DT, int DK>
 cudaError_t launch_chunks(const DeltaArgs& a, char* ws, cudaStream_t s) {
-    const DrPlan p = dr_plan(a.n, a.T, a.Hk, a.Hv, a.dk, a.max_len);
+    const DrPlan p = dr_plan(DT, a.n, a.T, a.Hk, a.Hv, a.dk, a.max_len);
     DrChunk* data = reinterpret_cast<DrChunk*>(ws);
     uint16_t* kf = reinterpret_cast<uint16_t*>(ws + p.kf);
     uint16_t* qf = reinterpret_cast<uint16_t*>(ws + p.qf);
@@ -940,9 +941,9 @@ cudaError_t launch_dt(const DeltaArgs& a, char* ws, cudaStream_t s) {
 
 }  // namespace
 
-size_t delta_rule_ws_bytes(int n, int T, int Hk, int Hv, int dk, int dv, int max_len) {
+size_t delta_rule_ws_bytes(int dtype, int n, int T, int Hk, int Hv, int dk, int dv, int max_len) {
     (void)dv;
-    return dr_plan(n, T, Hk, Hv, dk, max_len).total;
+    return dr_plan(dtype, n, T, Hk, Hv, dk, max_len).total;
 }
 
 cudaError_t launch_delta_rule(const DeltaArgs& a, int dtype, void* ws, cudaStream_t s) {

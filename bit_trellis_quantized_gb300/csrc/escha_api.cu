@@ -1338,7 +1338,17 @@ int escha_paged_attention(const void* q, void* k_pool, void* v_pool, int dtype, 
 
 size_t escha_delta_rule_workspace(int n, int T, int Hk, int Hv, int dk, int dv, int max_len) {
     if (check_delta_shape(n, T, Hk, Hv, dk, dv, max_len, "delta_rule_workspace")) return 0;
-    return escha::delta_rule_ws_bytes(n, T, Hk, Hv, dk, dv, max_len);
+    return escha::delta_rule_ws_bytes(ESCHA_BF16, n, T, Hk, Hv, dk, dv, max_len);
+}
+
+size_t escha_delta_rule_workspace_dtype(int dtype, int n, int T, int Hk, int Hv, int dk, int dv, int max_len) {
+    const char* name = "delta_rule_workspace_dtype";
+    if (check_delta_shape(n, T, Hk, Hv, dk, dv, max_len, name)) return 0;
+    if (dtype != ESCHA_F16 && dtype != ESCHA_BF16) {
+        fail(ESCHA_E_ARG, "%s: dtype=%d", name, dtype);
+        return 0;
+    }
+    return escha::delta_rule_ws_bytes(dtype, n, T, Hk, Hv, dk, dv, max_len);
 }
 
 int escha_delta_rule(const void* q, const void* k, const void* v, int dtype, const float* g, const float* beta,
@@ -1354,7 +1364,7 @@ int escha_delta_rule(const void* q, const void* k, const void* v, int dtype, con
     const void* ps[] = {q, k, v, g, beta, state, at, out};
     for (const void* p : ps)
         if (!aligned16(p)) return fail(ESCHA_E_ALIGN, "%s: pointer not 16-byte aligned", name);
-    if ((r = check_ws(ws, ws_bytes, escha::delta_rule_ws_bytes(n, T, Hk, Hv, dk, dv, max_len), name))) return r;
+    if ((r = check_ws(ws, ws_bytes, escha::delta_rule_ws_bytes(dtype, n, T, Hk, Hv, dk, dv, max_len), name))) return r;
     int sms;
     if ((r = device_check(&sms))) return r;
     const escha::DeltaArgs a{q, k, v, g, beta, state, at, out, n, T, Hk, Hv, dk, dv, max_len, scale, norm_eps};

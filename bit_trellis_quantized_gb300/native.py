@@ -74,6 +74,7 @@ EXPORTS = [
     "escha_paged_attention_workspace",
     "escha_paged_attention",
     "escha_delta_rule_workspace",
+    "escha_delta_rule_workspace_dtype",
     "escha_delta_rule",
     "escha_token_logprobs_workspace",
     "escha_token_logprobs",
@@ -227,6 +228,8 @@ def lib() -> ctypes.CDLL:
         L.escha_paged_attention.restype = _i
         L.escha_delta_rule_workspace.argtypes = [_i] * 7
         L.escha_delta_rule_workspace.restype = _sz
+        L.escha_delta_rule_workspace_dtype.argtypes = [_i] * 8
+        L.escha_delta_rule_workspace_dtype.restype = _sz
         L.escha_delta_rule.argtypes = [_vp, _vp, _vp, _i, _vp, _vp, _vp, _vp, _i, _i, _i, _i, _i, _i, _i, _f, _f, _vp,
                                        _vp, _sz, _vp]
         L.escha_delta_rule.restype = _i
@@ -647,7 +650,7 @@ def delta_rule(q, k, v, g, beta, state, at, scale=None, norm_eps=1e-6, max_len=N
     max_len = int(max_len)
     with _On(on, stream) as s:
         out = torch.empty_like(v) if out is None else _need("out", out, (T, Hv, dv), dt, on)
-        w, size, ws = _scratch(ws, _ws_bytes("escha_delta_rule_workspace", n, T, Hk, Hv, dk, dv, max_len), on)
+        w, size, ws = _scratch(ws, _ws_bytes("escha_delta_rule_workspace_dtype", tag, n, T, Hk, Hv, dk, dv, max_len), on)
         check(lib().escha_delta_rule(q.data_ptr(), k.data_ptr(), v.data_ptr(), tag, g.data_ptr(), beta.data_ptr(),
                                      state.data_ptr(), at.data_ptr(), n, T, Hk, Hv, dk, dv, max_len, scale, norm_eps,
                                      out.data_ptr(), w, size, s))

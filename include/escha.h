@@ -566,14 +566,16 @@ int escha_paged_attention(const void* q, void* k_pool, void* v_pool, int dtype, 
  *   max_len  host-side estimate of the longest sequence, >= 1: it chooses
  *            between the kernels that walk the tokens one by one and those
  *            that take them in chunks; any value gives right results
- *   ws       escha_delta_rule_workspace(n, T, Hk, Hv, dk, dv, max_len) bytes;
- *            nothing in it has to start at zero
+ *   ws       escha_delta_rule_workspace(n, T, Hk, Hv, dk, dv, max_len) bytes
+ *            serve either type; escha_delta_rule_workspace_dtype gives what
+ *            one needs (ESCHA_F16: less). Nothing in it has to start at zero
  * q, k, v, g and beta must not overlap state or out. In chunks (of 32 tokens) a
  * column of v and the state loses what is below 2^-38 of the chunk's largest
  * value, or below 2^-80; a NaN or an infinity may show in its head's outputs up
  * to 31 tokens ahead of it, never in another sequence's. Errors as
  * escha_paged_attention. */
 size_t escha_delta_rule_workspace(int n, int T, int Hk, int Hv, int dk, int dv, int max_len);
+size_t escha_delta_rule_workspace_dtype(int dtype, int n, int T, int Hk, int Hv, int dk, int dv, int max_len);
 int escha_delta_rule(const void* q, const void* k, const void* v, int dtype, const float* g, const float* beta,
                      float* state, const int32_t* at, int n, int T, int Hk, int Hv, int dk, int dv, int max_len,
                      float scale, float norm_eps, void* out, void* ws, size_t ws_bytes, void* stream);

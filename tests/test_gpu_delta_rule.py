@@ -333,3 +333,17 @@ def test_without_max_len_a_long_sequence_among_short_ones_goes_in_chunks(lens, c
             native.delta_rule(**args, **call)
     else:
         native.delta_rule(**args, **call)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+def test_a_workspace_of_the_types_own_size(dtype):
+    native = _native()
+    c = make(36, [100, 333, 1], 2, 4, 128, 64, dtype)
+    need = native.lib().escha_delta_rule_workspace_dtype(native._dtype_tag(c["q"]), 3, 434, 2, 4, 128, 64, 333)
+    whole = torch.full((need + 4096,), 0xA5, dtype=torch.uint8, device="cuda")
+    args = [c[x] for x in ("q", "k", "v", "g", "beta")]
+    want, got = c["state"].clone(), c["state"].clone()
+    out = native.delta_rule(*args, want, c["at"], max_len=333)
+    run_and_check(native, c, dtype, max_len=333)
+    assert torch.equal(native.delta_rule(*args, got, c["at"], max_len=333, ws=whole[:need]), out) and torch.equal(got, want)
+    assert bool((whole[need:] == 0xA5).all())

@@ -135,3 +135,17 @@ def test_wrappers_refuse_sizes_past_the_abis_integers():
     for M, V in ((2 ** 32 + 1, 1), (1, 2 ** 31)):
         with pytest.raises(ValueError, match="2\\^31"):
             native.token_logprobs(Tensor(M, V))
+
+
+def test_delta_rule_workspace_by_type():
+    """fp16 keys and queries are read where they are: no place for copies of them is asked for."""
+    native, L = _lib()
+    sizes = (3, 32000, 16, 32, 128, 128, 32000)
+    either = L.escha_delta_rule_workspace(*sizes)
+    assert L.escha_delta_rule_workspace_dtype(native.ESCHA_BF16, *sizes) == either
+    need = L.escha_delta_rule_workspace_dtype(native.ESCHA_F16, *sizes)
+    assert 0 < need == either - 2 * 32000 * 16 * 128 * 2
+    assert L.escha_delta_rule(G, G, G, native.ESCHA_F16, G, G, G, G, *sizes, 0.1, 1e-6, G, G, need - 1, None) == native.ESCHA_E_WORKSPACE
+    assert L.escha_delta_rule(G, G, G, native.ESCHA_BF16, G, G, G, G, *sizes, 0.1, 1e-6, G, G, need, None) == native.ESCHA_E_WORKSPACE
+    assert L.escha_delta_rule_workspace_dtype(native.ESCHA_F32, *sizes) == 0
+    assert L.escha_delta_rule_workspace_dtype(native.ESCHA_F16, 0, *sizes[1:]) == 0

@@ -347,3 +347,34 @@ def test_a_workspace_of_the_types_own_size(dtype):
     run_and_check(native, c, dtype, max_len=333)
     assert torch.equal(native.delta_rule(*args, got, c["at"], max_len=333, ws=whole[:need]), out) and torch.equal(got, want)
     assert bool((whole[need:] == 0xA5).all())
+
+
+@pytest.mark.parametrize("max_len", [1, 1000])
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("what", ["q", "k", "g", "beta"])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_nan_or_infinity_stays_in_its_heads_and_sequence(max_len, dtype, what, bad):
+    """Of q and k: in the value heads of its key head, of g and beta in its own;
+    nothing else changes by a bit, but outputs of its chunk ahead of it."""
+    native = _native()
+    c = make(37, [50, 70, 40], 2, 4, 64, 64, dtype)
+    names = ("q", "k", "v", "g", "beta")
+    clean = c["state"].clone()
+    want = native.delta_rule(*(c[x] for x in names), clean, c["at"], max_len=max_len)
+    t = 90  # of the second sequence, 40 tokens into it
+    if what in ("q", "k"):
+        c[what][t, 1, 9], heads = bad, slice(2, 4)
+    else:
+        c[what][t, 1], heads = bad, slice(1, 2)
+    state = c["state"].clone()
+    got = native.delta_rule(*(c[x] for x in names), state, c["at"], max_len=max_len)
+    hit = torch.zeros_like(got, dtype=torch.bool)
+    hit[t - (31 if max_len > 1 else 0):120, heads] = True
+    assert torch.equal(got[~hit], want[~hit])
+    assert not bool(got[t, heads].isfinite().any())
+    same = torch.ones_like(state, dtype=torch.bool)
+    same[1, heads] = what == "q"
+    assert torch.equal(state[same], clean[same])
+    if what != "q":
+        assert not bool(state[1, heads].isfinite().any())
+        assert not bool(got[t:120, heads].isfinite().any())

@@ -281,3 +281,29 @@ def test_no_new_token_behind_the_bound(dtype, lens, cap, Hq, Hkv, d, page):
         torch.cuda.synchronize()
         assert torch.equal(c["k"], want[0]) and torch.equal(c["v"], want[1])
         check(c, out, lse, d ** -0.5, dtype, cap=bound)
+
+
+@pytest.mark.parametrize("dtype,lens,Hq,Hkv,d", [("f16", [300, 200, 77], 16, 4, 64), ("bf16", [5000, 4700, 9], 6, 2, 128),
+                                                 ("f16", [700, 650, 31], 24, 2, 256)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_a_nan_or_infinity_stays_with_those_who_read_it(dtype, lens, Hq, Hkv, d, bad):
+    native = _native()
+    group = Hq // Hkv
+    for what in ("q", "k", "v"):
+        c = make(20, lens, Hq, Hkv, d, 16, dtype)
+        args = [c[x] for x in ("q", "k", "v", "table", "lens")]
+        want, want_lse = native.paged_attention(*args)
+        hit = torch.zeros_like(want, dtype=torch.bool)
+        if what == "q":
+            c["q"][1, 3, 5], hit[1, 3] = bad, True
+        else:
+            c[what][int(c["table"][1, 7]), 1, 3, 5] = bad  # position 115 of the second sequence, key head 1
+            hit[1, group:2 * group, slice(None) if what == "k" else 5] = True
+        out, lse = native.paged_attention(*args)
+        assert torch.equal(out[~hit], want[~hit])
+        rows = hit.any(-1) if what != "v" else torch.zeros_like(lse, dtype=torch.bool)
+        assert torch.equal(lse[~rows], want_lse[~rows])
+        if bad != bad:
+            assert bool(out[hit].isnan().all()) and bool(lse[rows].isnan().all())
+        elif what == "v":
+            assert not bool(out[hit].isfinite().any())

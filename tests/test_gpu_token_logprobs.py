@@ -275,3 +275,48 @@ def test_finite_masks_and_far_maxima(M, V, dtype):
     r = run_and_check(native, x, ids, 32)
     none = native.token_logprobs(x, torch.from_numpy(ids.astype(np.int32)).cuda())
     assert all(torch.equal(r[k], none[k]) for k in ("lse", "entropy", "logprobs"))  # the sums do not hang on the top list
+
+
+@pytest.mark.parametrize("M,V,dtype", WAYS[3:])
+def test_masks_infinities_and_ties_every_way(M, V, dtype):
+    """What bans tokens, breaks a row or fills the lists of its largest, over
+    the ways that share a row among warps and CTAs; at both ends of a row and
+    inside, so that each part of it has some."""
+    native = _native()
+    rng = np.random.default_rng(43)
+    x = torch.from_numpy(rng.standard_normal((M, V)) * 3).to(DT[dtype]).cuda()
+    low, inf, nan = torch.finfo(DT[dtype]).min, float("inf"), float("nan")
+    for i in range(M):
+        k, y = i % 14, x[i]
+        if k == 0:
+            y[::2] = -inf
+        elif k == 1:
+            y[:] = -inf  # nothing left
+        elif k == 2:
+            y[:V - 3], y[V - 2:] = -inf, -inf  # one token left
+        elif k == 3:
+            y[:] = low
+        elif k == 4:
+            y[:V // 2], y[V // 2 + 1:] = low, -inf
+        elif k == 5:
+            y[:] = 2.25  # all alike: the lowest ids
+        elif k == 6:
+            x[i] = torch.round(y)  # many ties
+        elif k == 7:
+            y[V - 2] = nan
+        elif k == 8:
+            y[V // 2] = inf
+        elif k == 9:
+            y[:], y[V - 1], y[3] = -inf, inf, nan
+        elif k == 10:
+            x[i] = torch.where(y > 0, 0.0, -0.0)  # both zeros rank alike
+        elif k == 11:
+            x[i] = torch.sort(y.float()).values.to(DT[dtype])  # the largest last
+        elif k == 12:
+            x[i] = torch.sort(y.float(), descending=True).values.to(DT[dtype])
+        else:
+            y[40:] = nan  # more of them than the list holds
+    ids = rng.integers(0, V, (M, 4))
+    ids[:, 1], ids[:, 2], ids[:, 3] = -1, V, V - 3
+    run_and_check(native, x, ids, 32)
+    run_and_check(native, x, ids, 1)

@@ -926,7 +926,8 @@ cudaError_t launch_chunks(const DeltaArgs& a, char* ws, cudaStream_t s) {
     const uint16_t* q = DT == 1 ? static_cast<const uint16_t*>(a.q) : qf;
     // A multiprocessor holds one CTA of either width, and 64 columns take one and a half times as long as 32 (1024 tokens
     // of 32 heads of 128 x 128: 77 and 57 us; of 40 heads, two rounds of 32 columns: 79 and 94; three sequences of 32
-    // heads, two rounds and three: 152 and 145; four: 159 and 190).
+    // heads, two rounds and three: 152 and 145; four: 159 and 190). 64 columns of dk = 128 need more than the 255 registers
+    // of a thread: 80 bytes of it are spilled, which these figures have in them.
     const long long rounds2 = ((long long)a.n * a.Hv * (a.dv / 32) + kSms - 1) / kSms;
     const long long rounds4 = ((long long)a.n * a.Hv * (a.dv / 64) + kSms - 1) / kSms;
     if (a.dv % 64 == 0 && 3 * rounds4 < 2 * rounds2) return launch_walk<DT, DK, 4>(a, k, q, data, s);

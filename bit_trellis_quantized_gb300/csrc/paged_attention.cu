@@ -22,8 +22,8 @@
 //     are not there are filled with zeros and masked.
 //   * Keys are the M of both products (scores K Q^T, values V^T P^T: m16n8k16),
 //     so that 8 query heads fill the instruction's N exactly.
-// Measured: 192 sequences of 500 to 16384 keys, 2 key heads of 256: 280 us, 6.7
-// TB/s; one of 131071: 48 us, 5.6 TB/s; one of 700: 8.2 us.
+// Measured: 192 sequences of 500 to 16384 keys, 2 key heads of 256: 283 us, 6.6
+// TB/s; one of 131071: 49 us, 5.5 TB/s; one of 700: 8.1 us.
 #include "common.cuh"
 #include "context.h"
 #include "kernels.h"
@@ -697,6 +697,9 @@ __global__ void __launch_bounds__(kPaSets* kPaCols) paged_attention_join_kernel(
 //  * More CTAs a unit even out ragged lengths and shorten the longest unit; each costs its start (64 sequences of 4 key
 //    heads in clusters of 1, 2, 4, 8: up to 700 keys 18, 24, 27, 42 us; up to 3000 55, 40, 41, 57; up to 12000 203,
 //    138, 109, 131). Fewer than half the places are worth filling up (16 sequences of 700: 13, 9.7, 8.5, 14).
+// `rounds` are those of max_len, as the host does not know the lengths; the figures above had the longest length for it. A
+// bound far above the lengths takes more CTAs a unit than they need (the 64 sequences of up to 700, with a bound of 700 and
+// of 131072: 16.3 and 21.2 us; up to 3000: 36.5 and 36.7).
 int pa_route(long long units, int rounds, int ctas) {
     if (16 * units <= ctas && rounds > 64) return 0;
     const int most = units * 5 <= ctas * 2 ? 8 : units * 2 <= ctas * 3 ? 4 : 2;

@@ -22,14 +22,17 @@
 // same bound over what was collected leaves a few more keys than asked for, and
 // each of them counts those above it. Where the buffer is full (a row that
 // ascends, a row of one value) a warp keeps the best 32 of the rest in order,
-// one a lane. (Keeping such lists throughout cost more than all else: 250 us
-// where this took 193, 2048 rows of 152064, top 8.)
+// one a lane: right, but slow where most of a row is alike and nothing above it
+// raises the bound (all but 10 tokens masked with one value: 2.0 ms for 2048
+// rows of 152064, top 8).
 //
-// Bound: one read of the logits. Each lane loads a chunk ahead, and the
-// arithmetic is 5 instructions a value (pairs of f32 where there is an
-// instruction for them), so that it stays behind the loads: 2048 rows of 152064
-// f32 take 203 us, 6.1 TB/s (187 without the top 8). How rows are dealt out to
-// warps, CTAs and clusters is at lp_route.
+// Bound: one read of the logits. Each lane loads a chunk ahead; all in all a
+// warp issues 13 instructions for 32 values (pairs of f32 where there is an
+// instruction for them), half of what the multiprocessors can: 2048 rows of
+// 152064 f32 take 202 us, 6.2 TB/s (187 without the top 8). Values of 16 bits
+// cost the same instructions and are unpacked besides, for half the bytes: 1000
+// such rows of bf16 take 91 us, 3.3 TB/s (66 without the top 8), by the
+// arithmetic. How rows are dealt out to warps, CTAs and clusters is at lp_route.
 #include <algorithm>
 
 #include "common.cuh"
@@ -737,7 +740,7 @@ __global__ void __launch_bounds__(kLpThreads) token_logprobs_join_kernel(Logprob
 //  * Cut over all CTAs, rows need a second kernel, 5 us and more (61 rows of 152064 f32: 20.6 us against 15.1 in
 //    clusters of 4; one: 12.1 against 10.4). That pays where clusters leave most CTAs idle for long (one row of 500000:
 //    12.7 against 15.0), by the rates measured: 31 GB/s a CTA, 213 of them fill the memory; and where the last
-//    round of many long rows would (1000 of 152064 f32: 113 against 120; of 16 bits 105 against 102).
+//    round of many long rows would (1000 of 152064 f32, top 8: 107 against 111; of 16 bits 97 against 91).
 constexpr int kLpRows = -1, kLpCut = 0;
 int lp_route(int M, int V, int size) {
     if (V <= 1024 || (V <= 4096 && M >= 2 * kLpCtas * kSms)) return kLpRows;

@@ -560,7 +560,7 @@ int escha_paged_attention(const void* q, void* k_pool, void* v_pool, int dtype, 
  *            clamped. A sequence of no tokens leaves its state as it is. Rows
  *            of out that belong to no sequence are left as they are. (Values
  *            that descend are not allowed: no access leaves the buffers, but
- *            a token of two sequences gets the output of one of them.)
+ *            the outputs and states of the call are undefined.)
  *   dk       64 or 128;  dv a multiple of 32 in 32..256;  Hv a multiple of Hk;
  *            n, Hv <= 65535
  *   max_len  host-side estimate of the longest sequence, >= 1: it chooses

@@ -1274,6 +1274,22 @@ int check_paged_shape(int B, int Hq, int Hkv, int d, int max_len, const char* na
     return ESCHA_OK;
 }
 
+int check_pages(int page, int n_pages, int max_pages, int Hkv, const char* name) {
+    if (page < 1 || n_pages < 1 || max_pages < 1)
+        return fail(ESCHA_E_ARG, "%s: page=%d n_pages=%d max_pages=%d must be >= 1", name, page, n_pages, max_pages);
+    if ((long long)n_pages * page > 0x7fffffffll / Hkv)
+        return fail(ESCHA_E_SHAPE, "%s: n_pages * Hkv * page = %d * %d * %d is above 2^31 - 1 rows", name, n_pages, Hkv, page);
+    return ESCHA_OK;
+}
+
+int check_chunk_shape(int n, int T, int Hq, int Hkv, int d, int max_len, const char* name) {
+    const int r = check_paged_shape(n, Hq, Hkv, d, max_len, name);
+    if (r) return r;
+    if (T < 1) return fail(ESCHA_E_ARG, "%s: T=%d must be >= 1", name, T);
+    if ((long long)T * Hq >= (1ll << 40) / d) return fail(ESCHA_E_SHAPE, "%s: T * Hq * d = %d * %d * %d is above 2^40", name, T, Hq, d);
+    return ESCHA_OK;
+}
+
 int check_delta_shape(int n, int T, int Hk, int Hv, int dk, int dv, int max_len, const char* name) {
     if (n < 1 || T < 1 || Hk < 1 || Hv < 1 || max_len < 1)
         return fail(ESCHA_E_ARG, "%s: n=%d T=%d Hk=%d Hv=%d max_len=%d must be >= 1", name, n, T, Hk, Hv, max_len);
@@ -1318,10 +1334,7 @@ int escha_paged_attention(const void* q, void* k_pool, void* v_pool, int dtype, 
     if (!q || !k_pool || !v_pool || !table || !lens || !out) return fail(ESCHA_E_ARG, "%s: null pointer", name);
     if (!k_new != !v_new) return fail(ESCHA_E_ARG, "%s: k_new and v_new go together", name);
     if (dtype != ESCHA_F16 && dtype != ESCHA_BF16) return fail(ESCHA_E_ARG, "%s: dtype=%d", name, dtype);
-    if (page < 1 || n_pages < 1 || max_pages < 1)
-        return fail(ESCHA_E_ARG, "%s: page=%d n_pages=%d max_pages=%d must be >= 1", name, page, n_pages, max_pages);
-    if ((long long)n_pages * page > 0x7fffffffll / Hkv)
-        return fail(ESCHA_E_SHAPE, "%s: n_pages * Hkv * page = %d * %d * %d is above 2^31 - 1 rows", name, n_pages, Hkv, page);
+    if ((r = check_pages(page, n_pages, max_pages, Hkv, name))) return r;
     if (scale - scale != 0.f) return fail(ESCHA_E_ARG, "%s: scale is not finite", name);
     if (k_pool == v_pool) return fail(ESCHA_E_ARG, "%s: k_pool and v_pool are the same buffer", name);
     const void* ps[] = {q, k_pool, v_pool, table, lens, k_new, v_new, out, lse};
@@ -1401,6 +1414,108 @@ int escha_token_logprobs(const void* logits, int dtype, int M, int V, long long 
     const escha::LogprobArgs a{logits, ids, logprobs, entropy, lse, top_ids, top_logprobs, ld, M, V, n_ids, top};
     return cuda_status(escha::launch_token_logprobs(a, dtype, ws, static_cast<cudaStream_t>(stream)),
                        "token_logprobs launch");
+}
+
+int escha_rotary_append(const void* q, const void* k, const void* v, int src_dtype, long long q_ld, long long k_ld,
+                        long long v_ld, const uint64_t* turns, int rot, int interleaved, float factor,
+                        const int32_t* positions, void* q_out, void* k_pool, void* v_pool, int dtype,
+                        const int32_t* table, const int32_t* at, const int32_t* lens, int n, int T, int Hq, int Hkv,
+                        int d, int page, int n_pages, int max_pages, void* stream) {
+    const char* name = "rotary_append";
+    int r = check_paged_shape(n, Hq, Hkv, d, 1, name);
+    if (r) return r;
+    if (T < 1) return fail(ESCHA_E_ARG, "%s: T=%d must be >= 1", name, T);
+    if (!k || !v || !k_pool || !v_pool || !table || !at || !lens) return fail(ESCHA_E_ARG, "%s: null pointer", name);
+    if (!q != !q_out) return fail(ESCHA_E_ARG, "%s: q and q_out go together", name);
+    if (dtype != ESCHA_F16 && dtype != ESCHA_BF16) return fail(ESCHA_E_ARG, "%s: dtype=%d", name, dtype);
+    if (src_dtype != ESCHA_F32 && src_dtype != dtype)
+        return fail(ESCHA_E_ARG, "%s: src_dtype=%d must be ESCHA_F32 or dtype", name, src_dtype);
+    if (rot < 0 || rot > d || rot % 16)
+        return fail(ESCHA_E_SHAPE, "%s: rot=%d must be a multiple of 16 in 0..d=%d", name, rot, d);
+    if (rot && !turns) return fail(ESCHA_E_ARG, "%s: turns is null", name);
+    if (interleaved != 0 && interleaved != 1) return fail(ESCHA_E_ARG, "%s: interleaved=%d", name, interleaved);
+    if (factor - factor != 0.f) return fail(ESCHA_E_ARG, "%s: factor is not finite", name);
+    if ((r = check_pages(page, n_pages, max_pages, Hkv, name))) return r;
+    if (k_pool == v_pool) return fail(ESCHA_E_ARG, "%s: k_pool and v_pool are the same buffer", name);
+    const long long size = src_dtype == ESCHA_F32 ? 4 : 2, lds[] = {q ? q_ld : (long long)Hq * d, k_ld, v_ld};
+    for (int i = 0; i < 3; ++i) {
+        const long long least = (long long)(i == 0 ? Hq : Hkv) * d;
+        if (lds[i] < least || lds[i] > (1ll << 40))
+            return fail(ESCHA_E_SHAPE, "%s: rows %lld values apart, of %lld", name, lds[i], least);
+        if (lds[i] * size % 16) return fail(ESCHA_E_ALIGN, "%s: rows not 16-byte aligned", name);
+    }
+    if (q && q == q_out && (src_dtype != dtype || q_ld != (long long)Hq * d))
+        return fail(ESCHA_E_ARG, "%s: q_out is q, but of another type or distance of rows", name);
+    const void* ps[] = {q, k, v, turns, positions, q_out, k_pool, v_pool, table, at, lens};
+    for (const void* p : ps)
+        if (!aligned16(p)) return fail(ESCHA_E_ALIGN, "%s: pointer not 16-byte aligned", name);
+    int sms;
+    if ((r = device_check(&sms))) return r;
+    const escha::RotaryArgs a{q,    k,    v,   q_ld, k_ld, v_ld, turns, positions, q_out,       k_pool, v_pool, table,   at,
+                              lens, n,    T,   Hq,   Hkv,  d,    rot,   interleaved, page, n_pages, max_pages, factor};
+    return cuda_status(escha::launch_rotary_append(a, src_dtype, dtype, static_cast<cudaStream_t>(stream)),
+                       "rotary_append launch");
+}
+
+size_t escha_chunk_attention_workspace(int n, int T, int Hq, int Hkv, int d, int max_len) {
+    if (check_chunk_shape(n, T, Hq, Hkv, d, max_len, "chunk_attention_workspace")) return 0;
+    return escha::chunk_attention_ws_bytes(n, T, Hq, Hkv, d, max_len);
+}
+
+int escha_chunk_attention(const void* q, const void* k_pool, const void* v_pool, int dtype, const int32_t* table,
+                          const int32_t* at, const int32_t* lens, int n, int T, int Hq, int Hkv, int d, int page,
+                          int n_pages, int max_pages, int max_len, float scale, void* out, float* lse, void* ws,
+                          size_t ws_bytes, void* stream) {
+    const char* name = "chunk_attention";
+    int r = check_chunk_shape(n, T, Hq, Hkv, d, max_len, name);
+    if (r) return r;
+    if (!q || !k_pool || !v_pool || !table || !at || !lens || !out) return fail(ESCHA_E_ARG, "%s: null pointer", name);
+    if (dtype != ESCHA_F16 && dtype != ESCHA_BF16) return fail(ESCHA_E_ARG, "%s: dtype=%d", name, dtype);
+    if ((r = check_pages(page, n_pages, max_pages, Hkv, name))) return r;
+    if (scale - scale != 0.f) return fail(ESCHA_E_ARG, "%s: scale is not finite", name);
+    const void* ps[] = {q, k_pool, v_pool, table, at, lens, out, lse};
+    for (const void* p : ps)
+        if (!aligned16(p)) return fail(ESCHA_E_ALIGN, "%s: pointer not 16-byte aligned", name);
+    if ((r = check_ws(ws, ws_bytes, escha::chunk_attention_ws_bytes(n, T, Hq, Hkv, d, max_len), name))) return r;
+    int sms;
+    if ((r = device_check(&sms))) return r;
+    const escha::ChunkAttnArgs a{q, k_pool, v_pool, table, at,      lens,      out,     lse,  n, T,
+                                 Hq, Hkv,   d,      page,  n_pages, max_pages, max_len, scale};
+    return cuda_status(escha::launch_chunk_attention(a, dtype, ws, static_cast<cudaStream_t>(stream)),
+                       "chunk_attention launch");
+}
+
+int escha_adjust_logits(const void* logits, void* out, int dtype, int M, int V, long long ld, long long out_ld,
+                        const int32_t* ids, const int32_t* at, int n_ids, const int32_t* prompt,
+                        const float* repetition, const float* frequency, const float* presence,
+                        const int32_t* bias_ids, const float* bias, const int32_t* bias_at, int n_bias,
+                        const int32_t* allowed, int n_masks, const int32_t* allowed_rows, void* stream) {
+    const char* name = "adjust_logits";
+    int r = check_logprob_shape(M, V, name);
+    if (r) return r;
+    if (!logits || !out) return fail(ESCHA_E_ARG, "%s: logits or out is null", name);
+    if (M * (V / 16384 + 1ll) > 0x7fffffffll) return fail(ESCHA_E_SHAPE, "%s: M=%d rows of V=%d are too many", name, M, V);
+    if (dtype != ESCHA_F16 && dtype != ESCHA_BF16 && dtype != ESCHA_F32)
+        return fail(ESCHA_E_ARG, "%s: dtype=%d", name, dtype);
+    if (ld < V || out_ld < V || ld > (1ll << 40) || out_ld > (1ll << 40))
+        return fail(ESCHA_E_SHAPE, "%s: ld=%lld or out_ld=%lld below V=%d", name, ld, out_ld, V);
+    if (logits == out && ld != out_ld) return fail(ESCHA_E_ARG, "%s: out is logits, but out_ld=%lld is not ld=%lld", name, out_ld, ld);
+    if (n_ids < 0 || n_bias < 0 || n_ids >= 1 << 30 || n_bias >= 1 << 30)
+        return fail(ESCHA_E_ARG, "%s: n_ids=%d and n_bias=%d must be in 0..2^30 - 1", name, n_ids, n_bias);
+    if (ids && !at) return fail(ESCHA_E_ARG, "%s: ids without at", name);
+    if (!ids && n_ids) return fail(ESCHA_E_ARG, "%s: n_ids=%d without ids", name, n_ids);
+    if (!bias_ids != !bias || !bias_ids != !bias_at || (!bias_ids && n_bias))
+        return fail(ESCHA_E_ARG, "%s: bias_ids, bias and bias_at go together", name);
+    if (allowed ? n_masks < 1 || (!allowed_rows && n_masks < M) : allowed_rows || n_masks)
+        return fail(ESCHA_E_ARG, "%s: n_masks=%d masks of %d rows", name, n_masks, M);
+    const void* ps[] = {logits, out, ids, at, prompt, repetition, frequency, presence, bias_ids, bias, bias_at, allowed, allowed_rows};
+    for (const void* p : ps)
+        if (!aligned16(p)) return fail(ESCHA_E_ALIGN, "%s: pointer not 16-byte aligned", name);
+    int sms;
+    if ((r = device_check(&sms))) return r;
+    const escha::AdjustArgs a{logits,   out,  ids,     at,      prompt,       repetition, frequency, presence, bias_ids, bias,
+                              bias_at, allowed, allowed_rows, ld,         out_ld,    M,        V,        n_ids, n_bias, n_masks};
+    return cuda_status(escha::launch_adjust_logits(a, dtype, static_cast<cudaStream_t>(stream)), "adjust_logits launch");
 }
 
 }  // extern "C"

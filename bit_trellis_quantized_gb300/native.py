@@ -9,6 +9,7 @@ from __future__ import annotations
 
 import ctypes
 import functools
+import math
 import os
 
 import numpy as np
@@ -78,6 +79,10 @@ EXPORTS = [
     "escha_delta_rule",
     "escha_token_logprobs_workspace",
     "escha_token_logprobs",
+    "escha_rotary_append",
+    "escha_chunk_attention_workspace",
+    "escha_chunk_attention",
+    "escha_adjust_logits",
     "int8_w8a16_workspace",
     "int8_w8a16_matvec",
     "int8_w8a16_dequant",
@@ -237,6 +242,16 @@ def lib() -> ctypes.CDLL:
         L.escha_token_logprobs_workspace.restype = _sz
         L.escha_token_logprobs.argtypes = [_vp, _i, _i, _i, _ll, _vp, _i, _i, _vp, _vp, _vp, _vp, _vp, _vp, _sz, _vp]
         L.escha_token_logprobs.restype = _i
+        L.escha_rotary_append.argtypes = ([_vp, _vp, _vp, _i, _ll, _ll, _ll, _vp, _i, _i, _f, _vp, _vp, _vp, _vp, _i,
+                                           _vp, _vp, _vp] + [_i] * 8 + [_vp])
+        L.escha_rotary_append.restype = _i
+        L.escha_chunk_attention_workspace.argtypes = [_i] * 6
+        L.escha_chunk_attention_workspace.restype = _sz
+        L.escha_chunk_attention.argtypes = [_vp, _vp, _vp, _i, _vp, _vp, _vp] + [_i] * 9 + [_f, _vp, _vp, _vp, _sz, _vp]
+        L.escha_chunk_attention.restype = _i
+        L.escha_adjust_logits.argtypes = [_vp, _vp, _i, _i, _i, _ll, _ll, _vp, _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp,
+                                          _vp, _i, _vp, _i, _vp, _vp]
+        L.escha_adjust_logits.restype = _i
         L.int8_w8a16_workspace.argtypes = [_i, _i, _i]
         L.int8_w8a16_workspace.restype = _sz
         L.int8_w8a16_matvec.argtypes = [_vp, _vp, _i, _i, _vp, _i, _i, _vp, _vp, _sz, _vp]
@@ -687,6 +702,246 @@ def token_logprobs(logits, ids=None, top: int = 0, ws=None, stream=None) -> dict
                                          lps.data_ptr() if n_ids else None, entropy.data_ptr(), lse.data_ptr(),
                                          top_ids.data_ptr(), top_lps.data_ptr(), w, n, s))
     return {"logprobs": lps, "entropy": entropy, "lse": lse, "top_ids": top_ids, "top_logprobs": top_lps}
+
+
+class Rotary:
+    """Frequencies of a rotation by position, for rotary_append: of the first
+    ``rot`` values of a head (a multiple of 16), pair i < rot / 2 turns by
+    position * base ** (-2 i / rot); pairs are values 2 i and 2 i + 1 where
+    ``interleaved`` is set, else i and i + rot / 2. ``scaling`` for contexts
+    longer than a model was trained on:
+      {"type": "linear", "factor": f}: every frequency divided by f;
+      {"type": "ntk", "factor": f}: base times f ** (rot / (rot - 2)), which
+        divides the lowest frequency by f and leaves the highest;
+      {"type": "yarn", "factor": f, "original": L}: frequencies that turn more
+        than beta_fast (32) times within L positions stay, those that turn less
+        than beta_slow (1) times are divided by f, with a linear ramp over their
+        index between; cosine and sine times ``attention`` (0.1 ln f + 1).
+    ``frequencies`` instead gives them as rot / 2 numbers (radians a position).
+    Attributes: rot, interleaved, factor (of cosine and sine), frequencies
+    (float64 numpy) and turns (int64 on ``device``: 2^64ths of a turn)."""
+
+    def __init__(self, rot: int, base: float = 10000.0, interleaved: bool = False, scaling: dict | None = None,
+                 frequencies=None, device="cuda"):
+        rot = int(rot)
+        if rot < 16 or rot % 16:
+            raise ValueError(f"rot={rot} must be a positive multiple of 16")
+        self.rot, self.interleaved, self.factor = rot, bool(interleaved), 1.0
+        if frequencies is not None:
+            if scaling is not None:
+                raise ValueError("frequencies are taken as they are: no scaling beside them")
+            f = np.asarray(frequencies, np.float64)
+            if f.shape != (rot // 2,):
+                raise ValueError(f"frequencies has shape {f.shape}, not ({rot // 2},)")
+        else:
+            f = self._scaled(float(base), dict(scaling or {}))
+        if not np.all(np.isfinite(f)):
+            raise ValueError("the frequencies are not finite")
+        self.frequencies = f
+        # The product with 2^64 is exact, and so are whole numbers of 64 bits; whole turns a position turn nothing.
+        turns = [round(math.ldexp(x, 64)) % 2 ** 64 for x in (f / (2 * math.pi)).tolist()]
+        self.turns = torch.tensor([x - 2 ** 64 if x >= 2 ** 63 else x for x in turns], dtype=torch.int64, device=device)
+
+    def _scaled(self, base: float, scaling: dict) -> np.ndarray:
+        kind, rot = scaling.pop("type", None), self.rot
+        if not base > 1:
+            raise ValueError(f"base={base} must be above 1")
+        factor = float(scaling.pop("factor", 1.0))
+        if not factor > 0:
+            raise ValueError(f"factor={factor} must be above 0")
+        if kind == "ntk":
+            base *= factor ** (rot / (rot - 2))
+        f = base ** (-2.0 * np.arange(rot // 2) / rot)
+        if kind == "linear":
+            f = f / factor
+        elif kind == "yarn":
+            original = float(scaling.pop("original"))
+            fast, slow = float(scaling.pop("beta_fast", 32.0)), float(scaling.pop("beta_slow", 1.0))
+            # the index whose frequency turns so many times within the original length
+            at = [rot * math.log(original / (n * 2 * math.pi)) / (2 * math.log(base)) for n in (fast, slow)]
+            low, high = max(math.floor(at[0]), 0), min(math.ceil(at[1]), rot - 1)
+            ramp = np.clip((np.arange(rot // 2) - low) / max(high - low, 1e-3), 0, 1)
+            f = f * (1 - ramp) + f / factor * ramp
+            self.factor = float(scaling.pop("attention", 0.1 * math.log(factor) + 1.0 if factor > 1 else 1.0))
+        elif kind not in (None, "ntk"):
+            raise ValueError(f"scaling type {kind!r} is none of linear, ntk and yarn")
+        if scaling:
+            raise ValueError(f"scaling has no {sorted(scaling)}")
+        return f
+
+
+def _heads(name: str, t, T, d, index: int):
+    """Distance of rows of ``t``, [T][heads][d] on CUDA device ``index`` with contiguous heads."""
+    if t.dim() != 3 or t.shape[0] != T or t.shape[2] != d:
+        raise ValueError(f"{name} has shape {tuple(t.shape)}, not ({T}, heads, {d})")
+    if index < 0 or t.get_device() != index:
+        raise ValueError(f"{name} must be a CUDA tensor, all on one device")
+    least = t.shape[1] * d
+    ld, sh, sd = t.stride()
+    if sd != 1 or (t.shape[1] > 1 and sh != d) or (T > 1 and ld < least):
+        raise ValueError(f"the heads of {name} must be contiguous and its rows apart")
+    return ld if T > 1 else least
+
+
+def rotary_append(q, k, v, k_pool, v_pool, table, at, lens, rotary=None, positions=None, out=None, stream=None):
+    """Rotation of a step's queries and keys by their positions, and append of
+    its keys and values to a paged cache (escha_rotary_append). q [T][Hq][d] (or
+    None), k, v [T][Hkv][d], of the pools' type or f32; rows may be parts of
+    longer ones (views of one fused projection). k_pool, v_pool
+    [n_pages][Hkv][page][d] fp16 or bf16; table int32 [n][max_pages]; at int32
+    [n + 1], the first token of each sequence; lens int32 [n], the cached keys
+    and the new tokens. ``rotary``: a Rotary, or None for an append without
+    rotation; ``positions`` int32 [T] to turn by in place of the tokens' places.
+    Returns the turned queries [T][Hq][d] in the pools' type (None without q);
+    rows of no sequence in a given ``out`` are left as they are."""
+    if k.dim() != 3 or k_pool.dim() != 4 or table.dim() != 2:
+        raise ValueError("k is [T][Hkv][d], the pools [n_pages][Hkv][page][d], table [n][max_pages]")
+    T, Hkv, d = k.shape
+    n_pages, _, page, _ = k_pool.shape
+    n, max_pages = table.shape
+    on, tag, dt, src = k.get_device(), _dtype_tag(k_pool), k_pool.dtype, k.dtype
+    k_ld, v_ld = _heads("k", k, T, d, on), _heads("v", v, T, d, on)
+    if v.shape != k.shape or v.dtype is not src or (q is not None and q.dtype is not src):
+        raise ValueError("q, k and v are of one type, v of k's shape")
+    _need("k_pool", k_pool, (n_pages, Hkv, page, d), dt, on)
+    _need("v_pool", v_pool, k_pool.shape, dt, on)
+    _need("table", table, (n, max_pages), torch.int32, on)
+    _need("at", at, (n + 1,), torch.int32, on)
+    _need("lens", lens, (n,), torch.int32, on)
+    if positions is not None:
+        _need("positions", positions, (T,), torch.int32, on)
+    rot, turns, inter, factor = 0, None, 0, 1.0
+    if rotary is not None:
+        rot, inter, factor = rotary.rot, int(rotary.interleaved), rotary.factor
+        turns = _need("rotary.turns", rotary.turns, (rot // 2,), torch.int64, on).data_ptr()
+    Hq, q_ld, qp, op = Hkv, 0, None, None
+    if q is not None:
+        Hq, q_ld, qp = q.shape[1], _heads("q", q, T, d, on), q.data_ptr()
+    elif out is not None:
+        raise ValueError("out without q")
+    with _On(on, stream) as s:
+        if q is not None:
+            out = (torch.empty((T, Hq, d), dtype=dt, device=k.device) if out is None
+                   else _need("out", out, (T, Hq, d), dt, on))
+            op = out.data_ptr()
+        check(lib().escha_rotary_append(qp, k.data_ptr(), v.data_ptr(), _dtype_tag(k), q_ld, k_ld, v_ld, turns, rot,
+                                        inter, factor, None if positions is None else positions.data_ptr(), op,
+                                        k_pool.data_ptr(), v_pool.data_ptr(), tag, table.data_ptr(), at.data_ptr(),
+                                        lens.data_ptr(), n, T, Hq, Hkv, d, page, n_pages, max_pages, s))
+    return out
+
+
+def chunk_attention(q, k_pool, v_pool, table, at, lens, scale=None, max_len=None, out=None, lse=None, ws=None,
+                    stream=None):
+    """Attention of a chunk of new tokens over a paged key-value cache
+    (escha_chunk_attention). q [T][Hq][d] fp16 or bf16; k_pool, v_pool
+    [n_pages][Hkv][page][d], the new tokens' keys and values in them
+    (rotary_append); table int32 [n][max_pages]; at int32 [n + 1], the first
+    token of each sequence; lens int32 [n], the cached keys and the new tokens:
+    a token attends the keys up to its own. ``scale`` is 1 / sqrt(d) by default;
+    ``max_len`` a host-side bound of lens (by default the table's): keys behind
+    it are left out. Returns (out, lse f32 [T][Hq]); rows of no sequence in a
+    given ``out`` or ``lse`` are left as they are."""
+    if q.dim() != 3 or k_pool.dim() != 4 or table.dim() != 2:
+        raise ValueError("q is [T][Hq][d], the pools [n_pages][Hkv][page][d], table [n][max_pages]")
+    T, Hq, d = q.shape
+    n_pages, Hkv, page, _ = k_pool.shape
+    n, max_pages = table.shape
+    on, tag, dt = q.get_device(), _dtype_tag(q), q.dtype
+    _need("q", q, (T, Hq, d), dt, on)
+    _need("k_pool", k_pool, (n_pages, Hkv, page, d), dt, on)
+    _need("v_pool", v_pool, k_pool.shape, dt, on)
+    _need("table", table, (n, max_pages), torch.int32, on)
+    _need("at", at, (n + 1,), torch.int32, on)
+    _need("lens", lens, (n,), torch.int32, on)
+    if scale is None:
+        scale = d ** -0.5
+    if max_pages >= 2 ** 31:
+        raise ValueError(f"max_pages={max_pages} is above 2^31 - 1")
+    cap = min(max_pages * page, 2 ** 30)
+    max_len = cap if max_len is None else min(int(max_len), cap)
+    with _On(on, stream) as s:
+        out = torch.empty_like(q) if out is None else _need("out", out, (T, Hq, d), dt, on)
+        lse = (torch.empty((T, Hq), dtype=torch.float32, device=q.device) if lse is None
+               else _need("lse", lse, (T, Hq), torch.float32, on))
+        w, size, ws = _scratch(ws, _ws_bytes("escha_chunk_attention_workspace", n, T, Hq, Hkv, d, max_len), on)
+        check(lib().escha_chunk_attention(q.data_ptr(), k_pool.data_ptr(), v_pool.data_ptr(), tag, table.data_ptr(),
+                                          at.data_ptr(), lens.data_ptr(), n, T, Hq, Hkv, d, page, n_pages, max_pages,
+                                          max_len, scale, out.data_ptr(), lse.data_ptr(), w, size, s))
+    return out, lse
+
+
+def _rows(name: str, t, M, V) -> int:
+    """Distance of the rows of ``t``, [M][V] with contiguous rows."""
+    ld = t.stride(0) if M > 1 else V
+    if (V > 1 and t.stride(1) != 1) or ld < V:
+        raise ValueError(f"the rows of {name} must be contiguous and apart")
+    return ld
+
+
+def adjust_logits(logits, ids=None, at=None, prompt=None, repetition=None, frequency=None, presence=None,
+                  bias_ids=None, bias=None, bias_at=None, allowed=None, allowed_rows=None, out=None, stream=None):
+    """Penalties for repeated tokens, biases and grammar masks on logits
+    (escha_adjust_logits). logits [M][V] fp16, bf16 or f32, rows contiguous (a
+    row stride above V is fine). ids int32 [N] with at int32 [M + 1]: the tokens
+    of each row so far, the first prompt[m] (int32 [M]) of them its prompt's;
+    repetition (over all of them), frequency and presence (over those behind the
+    prompt) f32 [M]. bias_ids int32 [B], bias f32 [B], bias_at int32 [M + 1]:
+    what is added to single tokens. allowed int32 [masks][ceil(V / 32)], a bit a
+    token; allowed_rows int32 [M]: each row's mask, -1 for none (by default row
+    m has mask m). Returns the adjusted logits: a new tensor, or ``out``, which
+    may be ``logits`` (in place, only what changes is touched)."""
+    if logits.dim() != 2 or not logits.is_cuda:
+        raise ValueError("logits must be a CUDA tensor [M][V]")
+    M, V = logits.shape
+    if max(M, V) >= 2 ** 31:
+        raise ValueError(f"logits [{M}][{V}] is above 2^31 - 1 rows or values")
+    ld, on, tag = _rows("logits", logits, M, V), logits.get_device(), _dtype_tag(logits)
+
+    def need(name, t, shape, dtype):
+        return None if t is None else _need(name, t, shape, dtype, on).data_ptr()
+
+    def count(name, t):
+        if t is None:
+            return 0
+        if t.dim() != 1 or t.shape[0] >= 2 ** 30:
+            raise ValueError(f"{name} must have one dimension, below 2^30 long")
+        return t.shape[0]
+
+    n_ids, n_bias = count("ids", ids), count("bias_ids", bias_ids)
+    if (ids is None) != (at is None) or (ids is None and prompt is not None):
+        raise ValueError("ids and at go together, prompt with them")
+    if (bias_ids is None) != (bias is None) or (bias_ids is None) != (bias_at is None):
+        raise ValueError("bias_ids, bias and bias_at go together")
+    masks = 0
+    if allowed is not None:
+        masks = allowed.shape[0]
+        if allowed_rows is None and masks != M:
+            raise ValueError(f"{masks} masks for {M} rows, without allowed_rows")
+    elif allowed_rows is not None:
+        raise ValueError("allowed_rows without allowed")
+    i32, f32 = torch.int32, torch.float32
+    # (an empty list may have no address)
+    lists = [need("ids", ids, (n_ids,), i32), need("at", at, (M + 1,), i32), n_ids, need("prompt", prompt, (M,), i32)]
+    if n_ids == 0:
+        lists = [None, None, 0, None]
+    biases = [need("bias_ids", bias_ids, (n_bias,), i32), need("bias", bias, (n_bias,), f32),
+              need("bias_at", bias_at, (M + 1,), i32), n_bias]
+    if n_bias == 0:
+        biases = [None, None, None, 0]
+    penalties = [need(name, t, (M,), f32) for name, t in (("repetition", repetition), ("frequency", frequency),
+                                                          ("presence", presence))]
+    mask = [need("allowed", allowed, (masks, (V + 31) // 32), i32), masks, need("allowed_rows", allowed_rows, (M,), i32)]
+    if masks == 0:
+        mask = [None, 0, None]
+    with _On(on, stream) as s:
+        if out is None:
+            out = torch.empty((M, V), dtype=logits.dtype, device=logits.device)
+        elif out.get_device() != on or out.dtype is not logits.dtype or out.shape != logits.shape:
+            raise ValueError("out must be of the logits' shape, type and device")
+        check(lib().escha_adjust_logits(logits.data_ptr(), out.data_ptr(), tag, M, V, ld, _rows("out", out, M, V),
+                                        *lists, *penalties, *biases, *mask, s))
+    return out
 
 
 def int8_w8a16_dequant(W, scales, stream=None) -> torch.Tensor:

@@ -5,8 +5,10 @@
  * 2/3-bit Qwen3.6-35B-A3B-style layer with the packed trellis codes decoded
  * inside the GEMV, never materialised as dense weights, plus the int8 w8a16
  * matvec/GEMM of the dense layers, and what stands before and behind them in
- * a decode step: the token mixers (attention of one new token over a paged
- * cache, gated delta rule) and the log probabilities of the head's logits.
+ * a decode step or a prompt's chunk: the token mixers (attention of one new
+ * token or a chunk of tokens over a paged cache, with the rotation and the
+ * append that precede it; gated delta rule), the penalties, biases and masks
+ * of the head's logits and their log probabilities.
  *
  * Sources (by page):
  *   [PR694]  hipfire PR #694 "Escha-W2 port: 2-bit trellis decoded in the GEMV"
@@ -605,6 +607,103 @@ size_t escha_token_logprobs_workspace(int M, int V);
 int escha_token_logprobs(const void* logits, int dtype, int M, int V, long long ld, const int32_t* ids, int n_ids,
                          int top, float* logprobs, float* entropy, float* lse, int32_t* top_ids, float* top_logprobs,
                          void* ws, size_t ws_bytes, void* stream);
+
+/* ---- rotation by position and append to a paged cache ---------------------
+ * What precedes attention: a step's queries and keys are turned by their
+ * positions, its keys and values go to the cache, in one read of the
+ * projections' outputs and one write. Sequence s < n owns the tokens at[s] <= t
+ * < at[s + 1]; its lens[s] counts the cached keys and these tokens, so that
+ * token t stands at position
+ *   p = lens[s] - (at[s + 1] - at[s]) + (t - at[s]).
+ * Of the first rot values of a head of q and k, pair i < rot / 2 (values 2 i
+ * and 2 i + 1 where interleaved is set, else i and i + rot / 2) turns by the
+ * angle a = p f_i:  (x, y) <- factor (x cos a - y sin a, x sin a + y cos a).
+ * The rest of the head, and v, are taken as they are. Arithmetic is f32, each
+ * output is rounded once; angles are exact to 2^-24 at any position.
+ *   q        [T] rows of [Hq][d], q_ld values apart, or NULL (then q_out is
+ *            NULL too): keys and values alone
+ *   k, v     [T] rows of [Hkv][d], k_ld and v_ld apart (rows of one fused
+ *            projection, say); src_dtype of q, k, v: ESCHA_F32, or dtype. The
+ *            distances are multiples of 16 bytes, and at least a row.
+ *   turns    uint64 [rot / 2]: f_i in turns a position, times 2^64, that is
+ *            round(2^64 f_i / (2 pi)) mod 2^64; scaled frequencies for long
+ *            contexts are just others. May be NULL where rot is 0.
+ *   rot      a multiple of 16 in 0..d;  factor: of cosine and sine (1, or an
+ *            attention factor of the scaling)
+ *   positions  int32 [T] or NULL: positions to turn by in place of p
+ *   q_out    [T][Hq][d] of dtype; may be q itself where that is dtype and
+ *            q_ld = Hq d
+ *   k_pool, v_pool, dtype, table, page, n_pages, max_pages, d, Hq, Hkv as for
+ *            escha_paged_attention
+ *   at       int32 [n + 1], never descending; values outside [0, T] are
+ *            clamped. Rows of no sequence are neither read nor written. (Values
+ *            that descend: no access leaves the buffers, the rest is undefined.)
+ *   lens     int32 [n]
+ * A token whose position is below 0 or at or behind max_pages * page, or whose
+ * page entry is outside [0, n_pages), is not stored; its query is turned all the
+ * same. No two sequences append to one page, and no table names a page twice
+ * among those its tokens go to. n <= 65535. Errors as escha_paged_attention. */
+int escha_rotary_append(const void* q, const void* k, const void* v, int src_dtype, long long q_ld, long long k_ld,
+                        long long v_ld, const uint64_t* turns, int rot, int interleaved, float factor,
+                        const int32_t* positions, void* q_out, void* k_pool, void* v_pool, int dtype,
+                        const int32_t* table, const int32_t* at, const int32_t* lens, int n, int T, int Hq, int Hkv,
+                        int d, int page, int n_pages, int max_pages, void* stream);
+
+/* ---- attention of a chunk of new tokens over a paged cache ----------------
+ * escha_paged_attention for any number of new tokens a sequence: a prompt or a
+ * part of one, several speculated tokens, single tokens beside them. The new
+ * tokens' keys and values are in the cache already (escha_rotary_append). Token
+ * t of sequence s, at position p (as above), attends the keys j <= p of its
+ * sequence:
+ *   x_j = scale * (q[t][h] . K_j),  m = max_j x_j,
+ *   out[t][h] = sum_j e^(x_j - m) V_j / sum_j e^(x_j - m),
+ *   lse[t][h] = m + ln sum_j e^(x_j - m).
+ *   q, out   [T][Hq][d];  lse f32 [T][Hq] or NULL
+ *   at, lens as for escha_rotary_append; table, pools, dtype, d, Hq, Hkv, page
+ *            as for escha_paged_attention
+ *   max_len  host-side bound of lens, 1..2^30: keys at or behind
+ *            min(max_len, max_pages * page) are left out
+ *   ws       escha_chunk_attention_workspace(n, T, Hq, Hkv, d, max_len) bytes
+ *            (may be 0); nothing in it has to start at zero
+ * A token that no key is left to (a position below 0, pages that are none) gives
+ * out = 0 and lse = -infinity. Rows of no sequence are left as they are. Keys
+ * behind a sequence's last token are never read. n <= 65535, T Hq d below 2^40.
+ * Errors as escha_paged_attention. */
+size_t escha_chunk_attention_workspace(int n, int T, int Hq, int Hkv, int d, int max_len);
+int escha_chunk_attention(const void* q, const void* k_pool, const void* v_pool, int dtype, const int32_t* table,
+                          const int32_t* at, const int32_t* lens, int n, int T, int Hq, int Hkv, int d, int page,
+                          int n_pages, int max_pages, int max_len, float scale, void* out, float* lse, void* ws,
+                          size_t ws_bytes, void* stream);
+
+/* ---- penalties, biases and masks on logits ----------------------------------
+ * What stands between the head and the choice of a token (or
+ * escha_token_logprobs). Per row m and token i < V, in this order, in f32:
+ *   among the row's ids:            x = x > 0 ? x / repetition : x * repetition
+ *   c > 0 times behind the prompt:  x = x - (frequency * c + presence)
+ *   each bias of i, in list order:  x = x + bias
+ *   not allowed by the row's mask:  x = -infinity, whatever x was
+ * and the result is rounded once.
+ *   logits   [M] rows of V values, ld >= V apart; dtype ESCHA_F16, ESCHA_BF16
+ *            or ESCHA_F32;  out the same, out_ld apart: logits itself (with ld)
+ *            or a buffer that does not overlap it
+ *   ids      int32 [n_ids] or NULL: row m's are at[m] <= j < at[m + 1], the
+ *            first prompt[m] of them the prompt's (prompt NULL: none); at int32
+ *            [M + 1], never descending, clamped to [0, n_ids]. An id outside
+ *            [0, V) is left out.
+ *   repetition (> 0), frequency, presence  f32 [M] or NULL (1, 0, 0)
+ *   bias_ids int32 [n_bias], bias f32 [n_bias], or NULL: row m's are bias_at[m]
+ *            <= j < bias_at[m + 1] (int32 [M + 1], as at)
+ *   allowed  int32 [n_masks][ceil(V / 32)] or NULL: bit i % 32 of word i / 32
+ *            says that token i is allowed
+ *   allowed_rows  int32 [M]: the row's mask; outside [0, n_masks): none. NULL:
+ *            row m has mask m.
+ * In place, only the logits that change are read or written. n_ids and n_bias
+ * below 2^30. No workspace. Errors as escha_paged_attention. */
+int escha_adjust_logits(const void* logits, void* out, int dtype, int M, int V, long long ld, long long out_ld,
+                        const int32_t* ids, const int32_t* at, int n_ids, const int32_t* prompt,
+                        const float* repetition, const float* frequency, const float* presence,
+                        const int32_t* bias_ids, const float* bias, const int32_t* bias_at, int n_bias,
+                        const int32_t* allowed, int n_masks, const int32_t* allowed_rows, void* stream);
 
 /* ---- int8 w8a16 ----------------------------------------------------------
  * y[m][o] = sum_i (scale[o] * W[o][i]) * x[m][i], f32 output, with the int8

@@ -1,0 +1,285 @@
+"""GPU checks of escha_chunk_attention against its formula in 64 bits."""
+import numpy as np
+import pytest
+
+import chunk_refs as ref
+
+torch = pytest.importorskip("torch")
+pytestmark = pytest.mark.gpu
+
+DT = {"f16": torch.float16, "bf16": torch.bfloat16}
+HALF = {"f16": 2.0 ** -11, "bf16": 2.0 ** -8}
+
+
+def _native():
+    if not torch.cuda.is_available():
+        pytest.skip("no CUDA device")
+    from bit_trellis_quantized_gb300 import native
+
+    return native
+
+
+def make(seed, new, old, Hq, Hkv, d, page, dtype, pad=0, poison=True, spare=3):
+    """A cache with the new tokens in it, whose unused slots hold NaN and infinities."""
+    rng = np.random.default_rng(seed)
+    lens = [a + b for a, b in zip(new, old)]
+    need = [-(-max(n, 0) // page) for n in lens]
+    n_pages, width = sum(need) + spare, max(max(need), 1)
+    table, order, p = np.full((len(lens), width), -1, np.int32), rng.permutation(n_pages), 0
+    for b, c in enumerate(need):
+        table[b, :c], p = order[p:p + c], p + c
+    T = sum(new) + pad
+    q = torch.from_numpy(rng.standard_normal((T, Hq, d)) * 2).to(DT[dtype])
+    q[T - pad:] = float("nan")
+    gen = torch.Generator(device="cuda").manual_seed(seed)
+    c = {x: torch.randn((n_pages, Hkv, page, d), generator=gen, device="cuda").to(DT[dtype]) for x in "kv"}
+    if poison:
+        live = torch.zeros((n_pages, 1, page, 1), dtype=torch.bool)
+        for b, n in enumerate(lens):
+            for j in range(max(n, 0)):
+                live[table[b, j // page], 0, j % page] = True
+        c["k"] = torch.where(live.cuda(), c["k"], float("nan"))
+        c["v"] = torch.where(live.cuda(), c["v"], float("inf"))
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    return dict(c, q=q.cuda(), table=torch.from_numpy(table).cuda(), at=i32(np.cumsum([0] + new).tolist()), lens=i32(lens))
+
+
+def args(c):
+    return c["q"], c["k"], c["v"], c["table"], c["at"], c["lens"]
+
+
+def f64(t):
+    return t.double().cpu().numpy()
+
+
+def check(c, out, lse, scale, dtype, cap=None, odd=False):
+    """Bound of a value: the weights enter the second product rounded to the
+    type (half a step of each: HALF of the absolute weighted values; fp16 ones
+    below 2^-25 of the largest by 2^-36 of it at most), half a step of the
+    output's, and through the scores, each a sum of d products in f32 ((d + 4)
+    2^-24 sum |q||k| off), 2^-15 of each with the exponential and the sums. lse
+    comes from unrounded weights."""
+    h = HALF[dtype]
+    want, want_lse, mass, reach, most = ref.chunk_attention(f64(c["q"]), f64(c["k"]), f64(c["v"]), c["table"].cpu().numpy(),
+                                                            c["at"].cpu().numpy(), c["lens"].cpu().numpy(), scale, cap)
+    on = ~np.isnan(want_lse) if not odd else slice(None)
+    x_err = (c["q"].shape[2] + 4) * 2.0 ** -24 * reach
+    tol = h * np.abs(want) + (h * (1 + h) + 2 * x_err[..., None] + 2.0 ** -15) * mass
+    if dtype == "f16":
+        tol = tol + 2.0 ** -25 + 2.0 ** -36 * most[..., None]
+    assert np.all(np.abs(f64(out) - want)[on] <= tol[on])
+    got, none = f64(lse), np.isneginf(want_lse)
+    assert np.array_equal(np.isneginf(got[on]), none[on])
+    tol = x_err + 2.0 ** -20 + 2.0 ** -22 * np.abs(np.where(none, 0, want_lse))
+    on = ~np.isnan(want_lse) & ~none
+    assert np.all(np.abs(got - want_lse)[on] <= tol[on])
+
+
+SHAPES = [
+    # dtype, new, old, Hq, Hkv, d, page, pad
+    ("f16", [1], [0], 2, 2, 64, 16, 0), ("bf16", [1, 0, 2], [0, 0, 0], 4, 1, 128, 1, 3),
+    ("f16", [4], [696], 16, 2, 256, 64, 0), ("bf16", [15, 16, 17], [0, 1, 300], 8, 1, 256, 16, 0),
+    ("bf16", [63, 64, 65, 0, 129], [1, 0, 63, 0, 100], 16, 2, 256, 64, 2), ("f16", [300, 5, 0, 77], [0, 9, 3, 0], 5, 1, 128, 17, 1),
+    ("f16", [129, 130], [500, 127], 3, 3, 64, 48, 0), ("bf16", [40, 70], [600, 3], 22, 2, 64, 32, 0),
+    ("f16", [31, 2], [257, 31], 64, 1, 64, 128, 0), ("bf16", [33, 1, 1], [900, 2000, 0], 24, 1, 128, 256, 0),
+    ("bf16", [2] * 40, [(i * 37) % 300 for i in range(40)], 16, 4, 64, 16, 7), ("f16", [600], [0], 6, 2, 128, 1024, 0),
+    ("f16", [513], [511], 8, 4, 256, 32, 0), ("bf16", [700], [100], 4, 1, 128, 64, 0), ("f16", [257], [255], 1, 1, 64, 16, 0),
+    ("bf16", [1] * 200, [(i * 53) % 700 for i in range(200)], 8, 2, 128, 16, 0),
+    ("f16", [8], [9000], 16, 2, 256, 64, 0), ("bf16", [3, 1], [6000, 5000], 20, 4, 128, 16, 0), ("f16", [5], [8191], 8, 1, 64, 32, 0),
+    ("bf16", [257, 1, 64], [4000, 4100, 1], 11, 1, 256, 128, 0),
+]
+
+
+@pytest.mark.parametrize("dtype,new,old,Hq,Hkv,d,page,pad", SHAPES)
+def test_matches_the_formula(dtype, new, old, Hq, Hkv, d, page, pad):
+    native = _native()
+    c = make(31, new, old, Hq, Hkv, d, page, dtype, pad)
+    T = sum(new)
+    out, lse = torch.full_like(c["q"], 7.0), torch.full(c["q"].shape[:2], 7.0, device="cuda")
+    native.chunk_attention(*args(c), scale=0.11, out=out, lse=lse)
+    torch.cuda.synchronize()
+    assert bool((out[T:] == 7).all()) and bool((lse[T:] == 7).all())
+    check(c, out, lse, 0.11, dtype)
+    again, lse2 = native.chunk_attention(*args(c), scale=0.11, max_len=max(max(c["lens"].tolist()), 1))
+    assert again.shape == out.shape
+    check(c, again, lse2, 0.11, dtype)
+    third, lse3 = native.chunk_attention(*args(c), scale=0.11)
+    assert torch.equal(out[:T], third[:T]) and torch.equal(lse[:T], lse3[:T])
+
+
+@pytest.mark.parametrize("dtype,d", [("f16", 64), ("bf16", 128), ("f16", 256)])
+def test_dropped_and_bad_pages_hold_no_keys(dtype, d):
+    native = _native()
+    c = make(32, [30, 64, 20, 1, 200], [70, 0, 20, 15, 3], 4, 2, d, 16, dtype)
+    t = c["table"]
+    t[0, 2], t[0, 5] = -1, 1 << 30  # a dropped page, an entry past the pool
+    t[1, :] = -5  # nothing left
+    t[2, 2] = c["k"].shape[0]  # the last tokens' own page is none
+    t[4, 0] = -1  # the first tokens have no key at all
+    out, lse = native.chunk_attention(*args(c))
+    torch.cuda.synchronize()
+    check(c, out, lse, d ** -0.5, dtype)
+    assert torch.all(out[30:94] == 0) and torch.all(torch.isneginf(lse[30:94]))
+    assert torch.all(out[115:128] == 0) and torch.all(torch.isneginf(lse[115:128]))
+
+
+@pytest.mark.parametrize("dtype,d", [("f16", 64), ("bf16", 256)])
+def test_lengths_past_the_table_or_the_bound_and_below_the_tokens(dtype, d):
+    native = _native()
+    c = make(33, [20, 20, 20, 3], [28, 28, 28, 200], 4, 2, d, 16, dtype, poison=False)
+    c["table"] = c["table"][:, :4].contiguous()
+    c["lens"] = torch.tensor([1 << 30, -7, 5, 203], dtype=torch.int32, device="cuda")
+    c["table"][0, 3] = c["table"][1, 3] = 0
+    out, lse = native.chunk_attention(*args(c))
+    check(c, out, lse, d ** -0.5, dtype)
+    assert torch.all(out[20:55] == 0) and torch.all(torch.isneginf(lse[20:55]))
+    out, lse = native.chunk_attention(*args(c), max_len=33)
+    check(c, out, lse, d ** -0.5, dtype, cap=33)
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_far_apart_scores(dtype, d):
+    """One key far above the rest, early or late; rising scores, each tile's far above the last one's; all alike."""
+    native = _native()
+    c = make(34, [150, 150, 150, 150], [250] * 4, 2, 1, d, 32, dtype, poison=False)
+    c["q"][:] = 0
+    c["q"][:, :, 0] = 1.0
+    c["q"][450:] = 0
+    c["k"][:, :, :, 0] = 0.5
+    c["k"][int(c["table"][0, 2]), 0, 7, 0] = 64.0
+    c["k"][int(c["table"][1, 7]), 0, 20, 0] = 64.0
+    for j in range(400):
+        c["k"][int(c["table"][2, j // 32]), 0, j % 32, 0] = j * 0.25
+    out, lse = native.chunk_attention(*args(c), scale=1.0)
+    check(c, out, lse, 1.0, dtype)
+    assert torch.equal(out[0, 0], c["v"][int(c["table"][0, 2]), 0, 7])
+
+
+@pytest.mark.parametrize("dtype,d", [("f16", 64), ("bf16", 128), ("f16", 256)])
+def test_many_keys_of_next_to_no_weight(dtype, d):
+    """One key of value 0 that takes almost all weight; 20000 others, each at
+    2^-25 of it or so, make up the output."""
+    native = _native()
+    c = make(35, [3], [20000], 4, 2, d, 64, dtype, poison=False)
+    c["q"][:] = 0
+    c["q"][:, :, 1] = 1.1
+    c["k"][:, :, :, 1] = 0
+    pg = int(c["table"][0, 100])
+    c["k"][pg, :, 3] = 0
+    c["k"][pg, :, 3, 1] = 15.0
+    c["v"][:] = c["v"].abs()
+    c["v"][pg, :, 3] = 0
+    out, lse = native.chunk_attention(*args(c), scale=1.0)
+    assert float(out.abs().min()) > 2e-4
+    check(c, out, lse, 1.0, dtype)
+
+
+@pytest.mark.parametrize("dtype,new,old,Hq,Hkv,d", [("f16", [200], [100], 16, 4, 64), ("bf16", [150], [3], 6, 2, 128),
+                                                    ("f16", [90, 40], [0, 300], 24, 2, 256), ("bf16", [5], [7000], 16, 2, 256)])
+@pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
+def test_nan_and_infinity_stay_with_the_tokens_that_see_them(dtype, new, old, Hq, Hkv, d, bad):
+    """A key or value behind a token is masked, whatever it holds; the others'
+    outputs keep their bits."""
+    native = _native()
+    group = Hq // Hkv
+    for what in ("q", "k", "v"):
+        c = make(36, new, old, Hq, Hkv, d, 16, dtype)
+        want, want_lse = (x.clone() for x in native.chunk_attention(*args(c)))
+        hit = torch.zeros_like(want, dtype=torch.bool)
+        last = new[0] - 3
+        if what == "q":
+            c["q"][last, 3, 5], hit[last, 3] = bad, True
+        else:
+            p = old[0] + last  # a new token's own key or value
+            c[what][int(c["table"][0, p // 16]), 1, p % 16, 5] = bad
+            hit[last:new[0], group:2 * group, slice(None) if what == "k" else 5] = True
+        out, lse = native.chunk_attention(*args(c))
+        assert torch.equal(out[~hit], want[~hit])
+        rows = hit.any(-1) if what != "v" else torch.zeros_like(lse, dtype=torch.bool)
+        assert torch.equal(lse[~rows], want_lse[~rows])
+        if bad != bad:
+            assert bool(out[hit].isnan().all()) and bool(lse[rows].isnan().all())
+        elif what == "v":
+            assert not bool(out[hit].isfinite().any())
+
+
+def test_pages_behind_32_bit_offsets():
+    native = _native()
+    Hkv, page, d = 8, 64, 256
+    n_pages = (1 << 32) // (Hkv * page * d) + 9
+    k = torch.empty((n_pages, Hkv, page, d), dtype=torch.bfloat16, device="cuda")
+    v = torch.empty_like(k)
+    used = [n_pages - 1, 0, n_pages - 5, n_pages // 2 + 1]
+    gen = torch.Generator(device="cuda").manual_seed(3)
+    for p in used:
+        k[p] = torch.randn(k.shape[1:], generator=gen, device="cuda").bfloat16()
+        v[p] = torch.randn(k.shape[1:], generator=gen, device="cuda").bfloat16()
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    c = dict(q=torch.randn((30, 16, d), generator=gen, device="cuda").bfloat16(), k=k, v=v, table=i32([used]),
+             at=i32([0, 30]), lens=i32([250]))
+    out, lse = native.chunk_attention(*args(c))
+    c.update(k=k[used].clone(), v=v[used].clone(), table=i32([[0, 1, 2, 3]]))
+    check(c, out, lse, 1 / 16, "bf16")
+
+
+@pytest.mark.parametrize("dtype,d,Hq,Hkv", [("f16", 256, 16, 2), ("bf16", 128, 20, 4), ("f16", 64, 3, 3)])
+def test_chunks_of_a_prompt_and_single_tokens_agree(dtype, d, Hq, Hkv):
+    """A prompt at once, in parts, and its last token as a decode step's: all within the bound of the formula."""
+    native = _native()
+    c = make(37, [400], [0], Hq, Hkv, d, 16, dtype)
+    out, lse = native.chunk_attention(*args(c))
+    check(c, out, lse, d ** -0.5, dtype)
+    i32 = lambda a: torch.tensor(a, dtype=torch.int32, device="cuda")  # noqa: E731
+    for a, b in ((0, 7), (7, 200), (200, 399), (399, 400)):
+        part = dict(c, q=c["q"][a:b].contiguous(), at=i32([0, b - a]), lens=i32([b]))
+        o, l = native.chunk_attention(*args(part))
+        check(part, o, l, d ** -0.5, dtype)
+    o, l = native.paged_attention(c["q"][399:].contiguous(), c["k"], c["v"], c["table"], c["lens"])
+    assert float((o.float() - out[399:].float()).abs().max()) <= 4 * HALF[dtype] * float(c["v"].float().nan_to_num(0, 0, 0).abs().max())
+    assert float((l - lse[399:]).abs().max()) <= 2.0 ** -17
+
+
+def test_streams_and_a_captured_step():
+    native = _native()
+    c = make(38, [3, 40, 0, 1], [90, 400, 0, 33], 8, 2, 128, 16, "f16", poison=False)
+    want, want_lse = native.chunk_attention(*args(c))
+    torch.cuda.synchronize()
+    side = [torch.cuda.Stream() for _ in range(3)]
+    got = [native.chunk_attention(*args(c), stream=s) for s in side for _ in range(4)]
+    torch.cuda.synchronize()
+    for o, l in got:
+        assert torch.equal(o, want) and torch.equal(l, want_lse)
+    out, lse = torch.empty_like(want), torch.empty_like(want_lse)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        native.chunk_attention(*args(c), out=out, lse=lse)
+    c["lens"].copy_(torch.tensor([80, 430, 7, 3], dtype=torch.int32))  # lengths and bounds are read by the replay
+    c["at"].copy_(torch.tensor([0, 10, 37, 41, 44], dtype=torch.int32))
+    c["table"][2, :1] = c["table"][1, 0]
+    graph.replay()
+    torch.cuda.synchronize()
+    check(c, out, lse, 128 ** -0.5, "f16")
+
+
+def test_refusals():
+    native = _native()
+    c = make(39, [10], [30], 4, 2, 64, 16, "f16")
+    good = dict(q=c["q"], k_pool=c["k"], v_pool=c["v"], table=c["table"], at=c["at"], lens=c["lens"])
+
+    def bad(exc, **kw):
+        with pytest.raises(exc):
+            native.chunk_attention(**{**good, **kw})
+
+    bad(TypeError, k_pool=c["k"].bfloat16())
+    bad(TypeError, lens=c["lens"].long())
+    bad(TypeError, at=c["at"].float())
+    bad(ValueError, lens=c["lens"].repeat(2))
+    bad(ValueError, at=c["at"].repeat(2))
+    bad(ValueError, q=c["q"].transpose(1, 2))
+    bad(ValueError, table=c["table"].cpu())
+    bad(ValueError, out=c["q"][:5].clone())
+    bad(native.EschaError, scale=float("nan"))
+    bad(native.EschaError, q=c["q"][:, :3].contiguous())
+    bad(native.EschaError, max_len=0)
+    bad(ValueError, ws=torch.empty(16, device="cuda"))

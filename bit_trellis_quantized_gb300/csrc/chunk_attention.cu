@@ -5,93 +5,1011 @@
 //   x_j = scale q . k_j,  m = max_j x_j,  out = sum_j e^(x_j - m) v_j / sum_j e^(x_j - m),
 //   lse = m + ln sum_j e^(x_j - m).
 //
-// A warp takes one (token, query head), a lane d / 32 values, key by key; 64
-// keys are summed by themselves, then added to the rest, so that many small
-// weights count beside a large one.
+// A unit is one (sequence, key head, run of rows); its rows are the pairs of a
+// token and a query head of the key head, tokens outermost, so that tiles of
+// 128 rows are full whatever the group of heads is. A CTA takes a unit, or a
+// run of its keys, in tiles of 128 keys:
+//   S = Q K^T (tcgen05, Q and K in shared memory, S in tensor memory), the
+//   weights P = 2^(S c - m) by one thread a row, back to tensor memory over S
+//   as 16-bit values, O += P V (A from tensor memory, O stays there).
+// Warps: 4 a tile of rows for the softmax, 4 that load keys and values
+// (cp.async, rows of the pages wherever they are; rows that are not there are
+// zeros and masked), one thread that issues the products.
+//
+// The running maximum that P is scaled by is moved, and O multiplied, only
+// where a row's maximum rises by more than kTau powers of two over it: with
+// the sum scaled alike the result is the same, and O is left alone nearly
+// always. Weights enter the second product rounded once to the type (half a
+// step of each weight; the sums and lse are of the unrounded ones): two parts
+// as in the decode kernel would cost the products half as much again. fp16 ones are
+// of the weight times 2^kUp, so that keys at 2^-25 of the largest weight keep
+// all but their last bit (steps below 2^-14 are 2^-24).
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
 #include "common.cuh"
 #include "context.h"
 #include "kernels.h"
+#include "tcgen05.cuh"
 #include "trellis_core.cuh"
 
 namespace escha {
 
 namespace {
 
-constexpr int kCaWarps = 4;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kLn2 = 0.6931471805599453f;
+template <int DT>
+constexpr float kTau = DT == 1 ? 4.f : 8.f;  // P is at most 2^(kTau + kUp): 2^15 in fp16
+template <int DT>
+constexpr float kUp = DT == 1 ? 11.f : 0.f;
 
-template <int DT, int D>
-__global__ void __launch_bounds__(kCaWarps * 32) chunk_attention_kernel(ChunkAttnArgs a) {
-    constexpr int kV = D / 32;
-    pdl_wait();
-    pdl_trigger();
-    const int lane = threadIdx.x & 31;
-    const long long item = (long long)blockIdx.x * kCaWarps + (threadIdx.x >> 5);
-    const int t = static_cast<int>(item / a.Hq), h = static_cast<int>(item % a.Hq);
-    if (t >= a.T) return;
-    int lo = 0, span = a.n;
-    while (span > 1) {
-        const int step = (span + 31) / 32, i = lo + lane * step;
-        const unsigned m = __ballot_sync(0xffffffffu, lane * step < span && a.at[i] <= t);
-        const int k = m ? 31 - __clz(m) : 0;
-        span = min(step, span - k * step);
-        lo += k * step;
+constexpr int kKeys = 128;  // of a tile
+template <int D>
+struct CaCfg {
+    static constexpr int kNQ = D == 256 ? 1 : 2;  // tiles of 128 rows: O of both and two S fill tensor memory
+    static constexpr int kRows = 128 * kNQ;
+    // warps: 4 a tile of rows, then 2 that load, one that issues the products, one that hands out the units
+    static constexpr int kSoftWarps = 4 * kNQ, kLoadWarps = 2, kMmaWarp = kSoftWarps + kLoadWarps, kUnitWarp = kMmaWarp + 1;
+    static constexpr int kThreads = 32 * (kUnitWarp + 1);
+    static constexpr int kSlotD = D < 128 ? D : 128;  // a slot of the ring: 128 keys of up to 128 values
+    static constexpr int kParts = D / kSlotD;
+    static constexpr int kSlotBytes = kKeys * kSlotD * 2;
+    static constexpr int kSlots = D == 64 ? 10 : 5;
+    static constexpr int kAhead = D == 64 ? 6 : 3;  // slots whose loads are in flight
+    static constexpr int kQBytes = kRows * D * 2;
+    static constexpr int kSmem = kQBytes + kSlots * kSlotBytes + 1024;
+    static constexpr uint32_t kScol = 256;  // S of tile q, or of every other tile of keys, at kScol + 128 q
+};
+constexpr int kMasks = 8;  // (the loads are never more than 5 tiles ahead of the weights)
+
+// n / d of n < 2^31 by one multiplication: mul = ceil(2^(31 + l) / d), l = ceil(log2 d).
+struct CaDiv {
+    uint32_t mul;
+    int shift;
+    __device__ __forceinline__ int operator()(int n) const {
+        return static_cast<int>((static_cast<unsigned long long>(n) * mul) >> shift);
     }
-    const int first = max(a.at[lo], 0), end = min(a.at[lo + 1], a.T);
-    if (t < first || t >= end) return;  // of no sequence
-    const long long pos = (long long)a.lens[lo] - (end - first) + (t - first);
-    const long long cap = min((long long)a.max_pages * a.page, (long long)a.max_len);
-    const int keys = static_cast<int>(max(0ll, min(pos + 1, cap)));
-    const int kvh = h / (a.Hq / a.Hkv);
-    const uint16_t* q = static_cast<const uint16_t*>(a.q) + ((long long)t * a.Hq + h) * D;
-    float qv[kV], acc[kV], sum[kV], m = -INFINITY, l = 0.f, part = 0.f;
+};
+
+template <int DT>
+__device__ __forceinline__ uint32_t ca_pack(float x, float y) {
+    if (DT == 1) {
+        const __half2 h = __floats2half2_rn(x, y);
+        return *reinterpret_cast<const uint32_t*>(&h);
+    }
+    const __nv_bfloat162 h = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+__device__ __forceinline__ float ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+__device__ __forceinline__ void cp16(uint32_t dst, const void* src, bool ok) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst), "l"(src), "r"(ok ? 16 : 0) : "memory");
+}
+__device__ __forceinline__ void cp_commit() { asm volatile("cp.async.commit_group;" ::: "memory"); }
+template <int N>
+__device__ __forceinline__ void cp_wait() {
+    asm volatile("cp.async.wait_group %0;" ::"n"(N) : "memory");
+}
+
+// Sequences' runs of rows, where they are cut over all CTAs, for the join. With the key heads outermost, a unit is (key
+// head, run); the tiles of keys of all units are numbered in this order.
+constexpr int kCaRuns = kSms;
+struct CaList {
+    int n, tiles;         // runs, tiles of all of them
+    uint32_t unit[kCaRuns];  // sequence, run << 16
+    int first[kCaRuns + 1];  // tiles of the runs before it
+};
+struct CaParts {
+    float* acc;  // [2 CTAs][rows][D]: a CTA's part of a unit begun before its range, its part of one that goes on
+    float* ml;   // [2 CTAs][rows][2]: maximum (powers of two), sum
+    CaList* list;
+};
+struct CaArgs {
+    CUtensorMap keys, values;  // the pools as rows of d values, in boxes of `box` rows and 64 values
+    ChunkAttnArgs a;
+    int box;  // rows of a page that are loaded at once: 8 to 128, or 0 (pages not of a multiple of 8): rows one by one
+    int cap;  // keys that may be read
+    CaDiv by_page, by_group;
+    CaParts parts;
+};
+
+// A sequence's tokens and positions.
+struct CaSeq {
+    int first, tokens;  // of q
+    int pos;            // of the first one
+    __device__ __forceinline__ CaSeq(const ChunkAttnArgs& a, int s) {
+        const bool there = s < a.n;
+        first = there ? min(max(a.at[s], 0), a.T) : 0;
+        tokens = there ? max(min(a.at[s + 1], a.T) - first, 0) : 0;
+        pos = there ? max(a.lens[s], 0) - tokens : 0;
+    }
+    __device__ __forceinline__ CaSeq() {}
+    __device__ __forceinline__ CaSeq of(int lane) const {
+        CaSeq o;
+        o.first = __shfl_sync(0xffffffffu, first, lane), o.tokens = __shfl_sync(0xffffffffu, tokens, lane), o.pos = __shfl_sync(0xffffffffu, pos, lane);
+        return o;
+    }
+    template <int kRows>
+    __device__ __forceinline__ int runs(int group) const {
+        return (tokens * group + kRows - 1) / kRows;
+    }
+    // keys that the rows [run kRows, (run + 1) kRows) see
+    template <int kRows>
+    __device__ __forceinline__ int keys(int run, int group, const CaArgs& c) const {
+        const int last = c.by_group(min((run + 1) * kRows, tokens * group) - 1);
+        return max(0, min(pos + last + 1, c.cap));
+    }
+};
+__device__ __forceinline__ int ca_tiles(int keys) { return max(1, (keys + kKeys - 1) / kKeys); }
+
+// What a CTA works on next, handed to all its warps.
+struct CaUnit {
+    int s, kvh, row0, rows;  // rows of the sequence's pairs of token and head
+    int first, pos;          // the sequence's first token in q, its position
+    int tile0, tiles, keys;  // tiles 0: no more units
+    int whole;
+};
+struct CaBars {
+    unsigned long long full[10], empty[10], raw[10], s_full[2], p_full[2], pv_done[2], o_full[2], o_empty[2], q_full, q_empty, unit_full[2], unit_empty[2], want, stolen, end;
+    uint32_t tmem;
+    int bad;
+    CaUnit unit[2];
+    __align__(16) uint32_t masks[kMasks][4];  // of a tile's keys, which are there
+    uint32_t odd[2][4][4], any_odd[2];  // of a unit's last tiles, keys whose values are not all finite
+};
+
+// A wait that gives up after 2^19 polls (a second or two), or once another has: the CTA then runs on to its end and the
+// rows in work become NaN.
+__device__ __forceinline__ bool ca_bad(CaBars& b) { return *reinterpret_cast<volatile int*>(&b.bad) != 0; }
+__device__ __forceinline__ void ca_wait_long(CaBars& b, uint32_t at, uint32_t parity) {
+#pragma unroll 1
+    for (int it = 0; it < 1 << 19; ++it)
+        if (tc::mbar_test_parity(at, parity) || ca_bad(b)) return;
+    *reinterpret_cast<volatile int*>(&b.bad) = 1;
+}
+__device__ __forceinline__ void ca_wait(CaBars& b, unsigned long long* bar, uint32_t parity) {
+    const uint32_t at = tc::smem_addr(bar);
+    if (!tc::mbar_test_parity(at, parity)) ca_wait_long(b, at, parity);
+}
+__device__ __forceinline__ void ca_arrive(unsigned long long* bar) { tc::mbar_arrive_cta(tc::smem_addr(bar)); }
+
+// The next unit (the k-th), false: none. Every warp that works on units calls it once a unit.
+__device__ __forceinline__ bool ca_next(CaBars& b, uint32_t k, int lane, CaUnit& u) {
+    ca_wait(b, &b.unit_full[k & 1], (k >> 1) & 1);
+    u = b.unit[k & 1];
+    __syncwarp();
+    if (lane == 0) ca_arrive(&b.unit_empty[k & 1]);
+    return u.tiles > 0 && !ca_bad(b);
+}
+
+// ---- the warp that hands out units
+// kRanges: this CTA's range of all units' tiles. Else units, the longest of a sequence first: that of blockIdx, then those
+// of CTAs that have not begun yet, taken over (cancelled) one at a time when the one in work comes to its end.
+template <int kRows, bool kRanges>
+__device__ __forceinline__ void ca_units(const CaArgs& c, CaBars& b, CaList& list, uint4* response) {
+    const ChunkAttnArgs& a = c.a;
+    const int lane = threadIdx.x & 31, group = a.Hq / a.Hkv;
+    uint32_t k = 0;
+    auto give = [&](const CaSeq& q, int s, int run, int kvh, int tile0, int tiles, int keys) {
+        ca_wait(b, &b.unit_empty[k & 1], ((k >> 1) - 1) & 1);
+        if (lane == 0) {
+            const int row0 = run * kRows;
+            b.unit[k & 1] = CaUnit{s, kvh, row0, min(kRows, q.tokens * group - row0), q.first, q.pos, tile0, tiles, keys, tiles == ca_tiles(keys)};
+            ca_arrive(&b.unit_full[k & 1]);
+        }
+        ++k;
+    };
+    auto stop = [&]() {
+        ca_wait(b, &b.unit_empty[k & 1], ((k >> 1) - 1) & 1);
+        if (lane == 0) {
+            b.unit[k & 1].tiles = 0;
+            ca_arrive(&b.unit_full[k & 1]);
+        }
+    };
+    if (kRanges) {
+        int n = 0, tiles = 0;
+        for (int s0 = 0; s0 < a.n; s0 += 32) {
+            const CaSeq mine(a, s0 + lane);
+            const int runs = mine.runs<kRows>(group);
+            unsigned some = __ballot_sync(0xffffffffu, runs > 0);
+            const bool single = __all_sync(0xffffffffu, runs <= 1);
+            // sequences of one run all at once, others one after the other, a run a lane
+            do {
+                const int src = single ? 0 : __ffs(some) - 1;
+                const CaSeq q = single ? mine : mine.of(max(src, 0));
+                const int m = single ? 1 : q.runs<kRows>(group);
+                for (int r0 = 0; r0 < m && some; r0 += 32) {
+                    const int run = single ? 0 : r0 + lane;
+                    const bool on = single ? runs > 0 : run < m;
+                    const int w = on ? ca_tiles(q.keys<kRows>(run, group, c)) : 0;
+                    int incl = w;
 #pragma unroll
-    for (int i = 0; i < kV; ++i) qv[i] = load_act(q, lane + 32 * i, DT), acc[i] = sum[i] = 0.f;
-    for (int j = 0; j < keys; ++j) {
-        const int p = j / a.page, pg = a.table[(long long)lo * a.max_pages + p];
-        if (static_cast<unsigned>(pg) >= static_cast<unsigned>(a.n_pages)) continue;
-        const long long row = (((long long)pg * a.Hkv + kvh) * a.page + (j - p * a.page)) * D;
-        float x = 0.f;
+                    for (int d = 1; d < 32; d <<= 1) {
+                        const int o = __shfl_up_sync(0xffffffffu, incl, d);
+                        if (lane >= d) incl += o;
+                    }
+                    const unsigned ons = __ballot_sync(0xffffffffu, on);
+                    const int e = n + __popc(ons & ((1u << lane) - 1));
+                    if (on && e < kCaRuns) list.unit[e] = (s0 + (single ? lane : src)) | run << 16, list.first[e] = tiles + incl - w;
+                    n += __popc(ons);
+                    tiles += __shfl_sync(0xffffffffu, incl, 31);
+                }
+                some &= some - 1;
+            } while (!single && some);
+        }
+        n = min(n, kCaRuns);
+        if (lane == 0) list.n = n, list.tiles = tiles, list.first[n] = tiles;
+        __syncwarp();
+        if (blockIdx.x == 0)  // for the join
+            for (int i = lane; i < static_cast<int>(sizeof(CaList) / 4); i += 32) reinterpret_cast<int*>(c.parts.list)[i] = reinterpret_cast<const int*>(&list)[i];
+        // CTA i begins at tile floor(i total / ctas)
+        const int total = tiles * a.Hkv, ctas = min(static_cast<int>(gridDim.x), total), i = blockIdx.x;
+        if (i < ctas) {
+            const int each = total / ctas, rest = total % ctas;
+            int at = i * each + i * rest / ctas;
+            const int end = (i + 1) * each + (i + 1) * rest / ctas;
+            int kvh = at / tiles, off = at % tiles, e = 0, e1 = n;
+            while (e1 - e > 1) {
+                const int mid = (e + e1) / 2;
+                (list.first[mid] <= off ? e : e1) = mid;
+            }
+            int tile0 = off - list.first[e];
+            while (at < end) {
+                const int s = list.unit[e] & 0xFFFFu, run = list.unit[e] >> 16, now = min(list.first[e + 1] - list.first[e] - tile0, end - at);
+                const CaSeq q(a, s);
+                give(q, s, run, kvh, tile0, now, q.keys<kRows>(run, group, c));
+                at += now, tile0 = 0;
+                if (++e == n) e = 0, ++kvh;
+            }
+        }
+        stop();
+        return;
+    }
+    int unit = blockIdx.x, s0 = 0, before = 0;
+    CaSeq mine(a, lane);
+    uint32_t steals = 0;
+    while (true) {
+        // the sequence: 32 at a time, on from the one before
+        int w, incl;
+        while (true) {
+            w = mine.runs<kRows>(group) * a.Hkv, incl = w;
 #pragma unroll
-        for (int i = 0; i < kV; ++i) x += qv[i] * load_act(a.k_pool, row + lane + 32 * i, DT);
+            for (int d = 1; d < 32; d <<= 1) {
+                const int o = __shfl_up_sync(0xffffffffu, incl, d);
+                if (lane >= d) incl += o;
+            }
+            const int all = __shfl_sync(0xffffffffu, incl, 31);
+            if (unit < before + all || s0 + 32 >= a.n) break;
+            before += all, s0 += 32;
+            mine = CaSeq(a, s0 + lane);
+        }
+        const unsigned has = __ballot_sync(0xffffffffu, unit < before + incl);
+        if (!has) break;  // past the last unit
+        const int src = __ffs(has) - 1, off = unit - before - __shfl_sync(0xffffffffu, incl - w, src);
+        const CaSeq q = mine.of(src);
+        const int run = q.runs<kRows>(group) - 1 - off / a.Hkv, keys = q.keys<kRows>(run, group, c);
+        give(q, s0 + src, run, off % a.Hkv, 0, ca_tiles(keys), keys);
+        ca_wait(b, &b.want, steals & 1);
+        if (ca_bad(b)) break;
+        if (lane == 0) {
+            tc::fence_proxy_async_smem();
+            tc::mbar_arrive_expect_tx(tc::smem_addr(&b.stolen), 16);
+            asm volatile("clusterlaunchcontrol.try_cancel.async.shared::cta.mbarrier::complete_tx::bytes.b128 [%0], [%1];" ::"r"(tc::smem_addr(response)),
+                         "r"(tc::smem_addr(&b.stolen))
+                         : "memory");
+        }
+        __syncwarp();
+        ca_wait(b, &b.stolen, steals & 1);
+        if (ca_bad(b)) break;
+        ++steals;
+        uint32_t got, id;
+        asm volatile(
+            "{\n\t.reg .b128 h;\n\t.reg .pred p;\n\tld.shared.b128 h, [%2];\n\t"
+            "clusterlaunchcontrol.query_cancel.is_canceled.pred.b128 p, h;\n\tselp.u32 %0, 1, 0, p;\n\tmov.u32 %1, 0;\n\t"
+            "@p clusterlaunchcontrol.query_cancel.get_first_ctaid::x.b32.b128 %1, h;\n\t}"
+            : "=r"(got), "=r"(id)
+            : "r"(tc::smem_addr(response))
+            : "memory");
+        if (!got) break;
+        unit = id;
+    }
+    stop();
+}
+
+// ---- the warps that load
+// A unit's queries, by both.
+template <int D>
+__device__ __forceinline__ void ca_queries(const CaArgs& c, const CaUnit& u, uint32_t q_smem) {
+    constexpr int kPieces = D / 8, kStep = 32 * CaCfg<D>::kLoadWarps / kPieces;
+    const int t = threadIdx.x - 32 * CaCfg<D>::kSoftWarps, group = c.a.Hq / c.a.Hkv, p = t % kPieces;
+    const char* q0 = static_cast<const char*>(c.a.q) + ((static_cast<long long>(u.first) * c.a.Hq + u.kvh * group) * D + p * 8) * 2;
+    const int end = u.rows > 128 ? CaCfg<D>::kRows : 128;
+#pragma unroll 4
+    for (int r = t / kPieces; r < end; r += kStep) {
+        const int R = u.row0 + r, tok = r < u.rows ? c.by_group(R) : 0;
+        const long long from = r < u.rows ? (static_cast<long long>(tok) * c.a.Hq + (R - tok * group)) * (D * 2) : 0;
+        cp16(q_smem + (r >> 7) * (128 * D * 2) + (p >> 3) * 16384 + tc::kmajor_off(r & 127, (p & 7) * 8), q0 + from, r < u.rows);
+    }
+    cp_commit();
+}
+__device__ __forceinline__ void ca_queries_landed(CaBars& b) {
+    cp_wait<0>();
+    tc::fence_proxy_async_smem();
+    __syncwarp();
+    if ((threadIdx.x & 31) == 0) ca_arrive(&b.q_full);
+}
+
+// The first tile that not every row of the unit sees in full, from the unit's first one.
+__device__ __forceinline__ int ca_partly(const CaArgs& c, const CaUnit& u) {
+    return max(max(0, u.pos + c.by_group(u.row0) + 1) / kKeys - u.tile0, 0);
+}
+
+// The values of such a tile: a weight of 0 would still carry what is not finite into rows that do not see it (keys of
+// later tokens, what lies behind the last one). So it is taken out here, and added at the end where it is seen. A warp's
+// rows r0, r0 + step, ... of a slot, a 16-byte piece a lane; `odd`: a bit a key of the tile.
+template <int DT, int D>
+__device__ __forceinline__ void ca_take_odd(uint32_t slot, int r0, int r1, uint32_t* odd, uint32_t* any) {
+    constexpr int kPieces = CaCfg<D>::kSlotD / 8;
+    const int lane = threadIdx.x & 31, p = lane % kPieces;
+#pragma unroll 1
+    for (int r = r0 + lane / kPieces; r < r1; r += 32 / kPieces) {
+        const uint32_t at = slot + (p >> 3) * 16384 + tc::kmajor_off(r, (p & 7) * 8);
+        uint32_t x[4];
+        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(at) : "memory");
+        constexpr uint32_t kExp = DT == 1 ? 0x7C00u : 0x7F80u;
+        bool some = false;
 #pragma unroll
-        for (int o = 16; o >= 1; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-        x *= a.scale;
-        const float top = fmaxf(m, x), base = top == -INFINITY ? 0.f : top;
-        const float corr = expf(m - base), w = expf(x - base);
-        m = top, l *= corr, part = part * corr + w;
-#pragma unroll
-        for (int i = 0; i < kV; ++i) sum[i] *= corr, acc[i] = acc[i] * corr + w * load_act(a.v_pool, row + lane + 32 * i, DT);
-        if (j % 64 == 63) {
-            l += part, part = 0.f;
-#pragma unroll
-            for (int i = 0; i < kV; ++i) sum[i] += acc[i], acc[i] = 0.f;
+        for (int e = 0; e < 4; ++e) {
+            const bool lo = (x[e] & kExp) == kExp, hi = (x[e] >> 16 & kExp) == kExp;
+            some |= lo | hi;
+            if (lo) x[e] &= 0xFFFF0000u;
+            if (hi) x[e] &= 0x0000FFFFu;
+        }
+        if (some) {
+            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]) : "memory");
+            atomicOr(odd + (r >> 5), 1u << (r & 31));
+            *any = 1;
         }
     }
-    l += part;
-    uint16_t* out = static_cast<uint16_t*>(a.out) + ((long long)t * a.Hq + h) * D;
+}
+
+// Pages of a multiple of 8 keys: the first warp loads boxes of a page's rows, a lane a box (TMA), the second looks through
+// the values of the tiles that are seen in part.
+template <int DT, int D, bool kRanges>
+__device__ __forceinline__ void ca_load_boxes(const CaArgs& c, CaBars& b, uint32_t q_smem, uint32_t ring) {
+    using C = CaCfg<D>;
+    const ChunkAttnArgs& a = c.a;
+    const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - C::kSoftWarps;
+    constexpr int kSlots = C::kSlots, kChunks = C::kSlotD / 64;
+    const int boxes = kKeys / c.box, nowhere = a.n_pages * a.Hkv * a.page;  // (rows behind the pool's last are zeros)
+    const int my_box = lane % boxes, my_chunk = lane / boxes;
+    uint32_t slot = 0, tile = 0, k = 0, phases = 0;
+    CaUnit u;
+    for (; ca_next(b, k, lane, u); ++k) {
+        ca_wait(b, &b.q_empty, (k - 1) & 1);
+        const int partly = ca_partly(c, u);
+        uint32_t* odd = &b.odd[k & 1][0][0];
+        if (w == 1) {
+            ca_queries<D>(c, u, q_smem);
+            ca_queries_landed(b);
+#pragma unroll 1
+            for (int j = partly; j < u.tiles; ++j)
+#pragma unroll 1
+                for (int p = 0; p < C::kParts; ++p) {
+                    // (order of the slots: below)
+                    const uint32_t i = slot + p + C::kParts * (C::kNQ == 1 ? min(2 * j + 2, 2 * u.tiles - 1) : 2 * j + 1), at = i % kSlots;
+                    ca_wait(b, &b.raw[at], phases >> at & 1);
+                    phases ^= 1u << at;
+                    ca_take_odd<DT, D>(ring + at * C::kSlotBytes, 0, kKeys, odd + 4 * (j - partly), &b.any_odd[k & 1]);
+                    tc::fence_proxy_async_smem();
+                    __syncwarp();
+                    if (lane == 0) ca_arrive(&b.full[at]);
+                }
+            slot += 2 * C::kParts * u.tiles;
+            continue;
+        }
+        if (lane < 16) odd[lane] = 0;
+        if (lane == 16) b.any_odd[k & 1] = 0;
+        __syncwarp();
+        ca_queries<D>(c, u, q_smem);
+        const int32_t* table = a.table + static_cast<long long>(u.s) * a.max_pages;
+        auto find = [&](int j) -> int {  // this lane's box of tile j: its row in the pools
+            const int key = (u.tile0 + j) * kKeys + my_box * c.box;
+            if (j >= u.tiles || key >= u.keys) return nowhere;
+            const int p = c.by_page(key), pg = table[p];
+            return static_cast<unsigned>(pg) < static_cast<unsigned>(a.n_pages) ? (pg * a.Hkv + u.kvh) * a.page + (key - p * a.page) : nowhere;
+        };
+        // of tile j: its keys, then the values of the tile before it or (two tiles of rows) of its own
+        int row = find(0), last = nowhere, next = find(1);
+#pragma unroll 1
+        for (int j = 0; j < u.tiles + (C::kNQ == 1 ? 1 : 0); ++j) {
+            const int later = find(j + 2);
+            if (j < u.tiles) {
+                const uint32_t on = __ballot_sync(0xffffffffu, row != nowhere);
+                if (lane < 4) {
+                    uint32_t m = 0;
 #pragma unroll
-    for (int i = 0; i < kV; ++i) {
-        const float y = l == 0.f ? 0.f : (sum[i] + acc[i]) / l;
-        out[lane + 32 * i] = DT == 1 ? __half_as_ushort(__float2half_rn(y)) : __bfloat16_as_ushort(__float2bfloat16_rn(y));
+                    for (int g = 0; g < 4; ++g) m |= (on >> (32 * lane + 8 * g) / c.box & 1) * (0xFFu << 8 * g);
+                    const int n = u.keys - (u.tile0 + j) * kKeys - 32 * lane;
+                    b.masks[(tile + j) % kMasks][lane] = m & (n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1);
+                }
+                __syncwarp();
+            }
+#pragma unroll 1
+            for (int i = 0; i < 2 * C::kParts; ++i) {
+                const bool keys_now = i < C::kParts;
+                if (C::kNQ == 1 && (keys_now ? j == u.tiles : j == 0)) continue;
+                const int of = C::kNQ == 1 && !keys_now ? j - 1 : j;
+                const uint32_t at = slot % kSlots, use = slot / kSlots;
+                if (use > 0) ca_wait(b, &b.empty[at], (use - 1) & 1);
+                const uint32_t bar = tc::smem_addr(!keys_now && of >= partly ? &b.raw[at] : &b.full[at]);
+                if (lane == 0) tc::mbar_arrive_expect_tx(bar, C::kSlotBytes);
+                __syncwarp();
+                if (my_chunk < kChunks)
+                    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
+                                     ring + at * C::kSlotBytes + my_chunk * 16384 + my_box * c.box * 128),
+                                 "l"(keys_now ? &c.keys : &c.values), "r"((keys_now ? i : i - C::kParts) * C::kSlotD + my_chunk * 64), "r"(of < j ? last : row),
+                                 "r"(bar)
+                                 : "memory");
+                ++slot;
+            }
+            if (j == 0) ca_queries_landed(b);
+            if (!kRanges && lane == 0 && j == max(u.tiles - 3, 0)) ca_arrive(&b.want);
+            last = row, row = next, next = later;
+        }
+        tile += u.tiles;
     }
-    if (a.lse && lane == 0) a.lse[(long long)t * a.Hq + h] = l == 0.f ? -INFINITY : m + logf(l);
+}
+
+// Pages of any size: warp w loads the rows 64 w .. 64 w + 63 of a tile, 16 bytes a lane.
+template <int DT, int D, bool kRanges>
+__device__ __forceinline__ void ca_load_rows(const CaArgs& c, CaBars& b, uint32_t q_smem, uint32_t ring) {
+    using C = CaCfg<D>;
+    const ChunkAttnArgs& a = c.a;
+    const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - C::kSoftWarps;
+    constexpr int kPieces = C::kSlotD / 8, kAtOnce = 32 / kPieces, kSlots = C::kSlots;
+    const int c8 = lane % kPieces, rr = lane / kPieces;
+    uint32_t slot = 0, tile = 0, k = 0;
+    int pending = 0;
+    uint32_t marks = 0;  // of the slots in flight, oldest lowest, 4 bits each: 1 + which of the unit's last tiles the values are of
+    const uint32_t mine = (c8 >> 3) * 16384 + (64 * w + rr) * 128;
+    // the slots in flight beyond `keep` have landed
+    auto landed = [&](int keep) {
+        if (keep) cp_wait<C::kAhead>();
+        else cp_wait<0>();
+#pragma unroll 1
+        for (; pending > keep; --pending, marks >>= 4) {
+            const uint32_t at = (slot - pending) % kSlots, mark = marks & 15;
+            if (mark) ca_take_odd<DT, D>(ring + at * C::kSlotBytes, 64 * w, 64 * w + 64, b.odd[k & 1][mark - 1], &b.any_odd[k & 1]);
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) ca_arrive(&b.full[at]);
+        }
+    };
+    auto room = [&](unsigned long long* bar, uint32_t parity) {
+        if (__all_sync(0xffffffffu, tc::mbar_test_parity(tc::smem_addr(bar), parity))) return;
+        landed(0);  // the products may wait for these
+        ca_wait(b, bar, parity);
+    };
+    CaUnit u;
+    for (; ca_next(b, k, lane, u); ++k) {
+        ca_wait(b, &b.q_empty, (k - 1) & 1);  // (nothing is in flight)
+        if (w == 0 && lane < 16) b.odd[k & 1][lane >> 2][lane & 3] = 0;
+        if (w == 0 && lane == 16) b.any_odd[k & 1] = 0;
+        asm volatile("bar.sync 1, %0;" ::"n"(32 * C::kLoadWarps) : "memory");
+        ca_queries<D>(c, u, q_smem);
+        ca_queries_landed(b);
+        const int32_t* table = a.table + static_cast<long long>(u.s) * a.max_pages;
+        // lane r's rows 64 w + r and 64 w + 32 + r of tile j: their numbers in the pools (-1: not there)
+        auto find = [&](int j, int (&row)[2]) {
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const int key = (u.tile0 + j) * kKeys + 64 * w + 32 * h + lane;
+                row[h] = -1;
+                if (j < u.tiles && key < u.keys) {
+                    const int p = c.by_page(key), pg = table[p];
+                    if (static_cast<unsigned>(pg) < static_cast<unsigned>(a.n_pages)) row[h] = (pg * a.Hkv + u.kvh) * a.page + (key - p * a.page);
+                }
+            }
+        };
+        const int partly = ca_partly(c, u);
+        // (in the order of the boxes)
+        int row[2], last[2] = {-1, -1};
+        find(0, row);
+#pragma unroll 1
+        for (int j = 0; j < u.tiles + (C::kNQ == 1 ? 1 : 0); ++j) {
+            int next[2];
+            find(j + 1, next);
+            if (j < u.tiles) {
+                const uint32_t m0 = __ballot_sync(0xffffffffu, row[0] >= 0), m1 = __ballot_sync(0xffffffffu, row[1] >= 0);
+                if (lane == 0) b.masks[(tile + j) % kMasks][2 * w] = m0, b.masks[(tile + j) % kMasks][2 * w + 1] = m1;
+            }
+#pragma unroll 1
+            for (int i = 0; i < 2 * C::kParts; ++i) {
+                const bool keys_now = i < C::kParts;
+                if (C::kNQ == 1 && (keys_now ? j == u.tiles : j == 0)) continue;
+                const int of = C::kNQ == 1 && !keys_now ? j - 1 : j;
+                const int r0 = of < j ? last[0] : row[0], r1 = of < j ? last[1] : row[1];
+                const uint32_t use = slot / kSlots;
+                if (use > 0) room(&b.empty[slot % kSlots], (use - 1) & 1);
+                const char* base = static_cast<const char*>(keys_now ? a.k_pool : a.v_pool) + (keys_now ? i : i - C::kParts) * (C::kSlotD * 2) + c8 * 16;
+                const uint32_t to = ring + slot % kSlots * C::kSlotBytes + mine;
+#pragma unroll 1
+                for (int h = 0; h < 2; ++h) {
+                    const int from = h ? r1 : r0;
+#pragma unroll
+                    for (int r = 0; r < 32; r += kAtOnce) {
+                        const int n = __shfl_sync(0xffffffffu, from, r + rr);
+                        cp16(to + (32 * h + r) * 128 + (((c8 & 7) ^ ((r + rr) & 7)) << 4), base + static_cast<long long>(max(n, 0)) * (D * 2), n >= 0);
+                    }
+                }
+                cp_commit();
+                if (!keys_now && of >= partly) marks |= (of - partly + 1) << (4 * pending);
+                ++slot, ++pending;
+                if (pending > C::kAhead) landed(C::kAhead);
+            }
+            if (!kRanges && w == 0 && lane == 0 && j == max(u.tiles - 3, 0)) ca_arrive(&b.want);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) last[h] = row[h], row[h] = next[h];
+        }
+        tile += u.tiles;
+        landed(0);
+    }
+}
+
+// ---- the thread that issues the products
+template <int DT, int D>
+__device__ __forceinline__ void ca_products(CaBars& b, uint32_t q_smem, uint32_t ring, uint32_t tmem) {
+    using C = CaCfg<D>;
+    constexpr int kNQ = C::kNQ, kParts = C::kParts, kSlots = C::kSlots;
+    constexpr uint32_t is = tc::idesc_f16(128, 128, false, false, DT == 2), io = tc::idesc_f16(128, C::kSlotD, false, true, DT == 2);
+    const uint64_t k_desc = tc::smem_desc(ring, 16, 1024, tc::kSwizzle128B), q_desc = tc::smem_desc(q_smem, 16, 1024, tc::kSwizzle128B);
+    const uint64_t v_desc = tc::smem_desc(ring, 16384, 1024, tc::kSwizzle128B);  // (addresses in 16 bytes, added to)
+    uint32_t slot = 0, k_first = 0, v_first = 0, k = 0;
+    uint32_t soft0 = 0, soft1 = 0, units1 = 0;  // tiles of keys of either tile of rows, units that have the second one
+    auto full = [&](uint32_t i) {
+        ca_wait(b, &b.full[i % kSlots], (i / kSlots) & 1);
+        tc::fence_after_sync();
+    };
+    auto scores = [&](int q, uint32_t g, bool release) {
+        const uint32_t buf = kNQ == 1 ? g & 1 : q;
+#pragma unroll 1
+        for (int p = 0; p < kParts; ++p) {
+            full(k_first + p);
+            const uint64_t kb = k_desc + ((k_first + p) % kSlots) * (C::kSlotBytes / 16);
+            const uint64_t qb = q_desc + (q * (128 * D * 2) + p * (C::kSlotD / 64) * 16384) / 16;
+#pragma unroll 1
+            for (int c = 0; c < C::kSlotD / 64; ++c)
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    tc::mma_f16(tmem + C::kScol + 128 * buf, qb + (c * 16384 + x * 32) / 16, kb + (c * 16384 + x * 32) / 16, is, p + c + x > 0);
+            if (release) tc::commit(tc::smem_addr(&b.empty[(k_first + p) % kSlots]));
+        }
+        tc::commit(tc::smem_addr(&b.s_full[buf]));
+    };
+    auto values = [&](int q, uint32_t g, int j, uint32_t units, bool last, bool release) {
+        const uint32_t buf = kNQ == 1 ? g & 1 : q;
+        if (j == 0) ca_wait(b, &b.o_empty[q], (units - 1) & 1);
+        ca_wait(b, &b.p_full[buf], kNQ == 1 ? (g >> 1) & 1 : g & 1);
+        tc::fence_after_sync();
+#pragma unroll 1
+        for (int p = 0; p < kParts; ++p) {
+            full(v_first + p);
+            const uint64_t vb = v_desc + ((v_first + p) % kSlots) * (C::kSlotBytes / 16);
+#pragma unroll 1
+            for (int k0 = 0; k0 < kKeys / 16; k0 += 4)
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+                    tc::mma_f16_ts(tmem + q * D + p * 128, tmem + C::kScol + 128 * buf + (k0 + x) * 8, vb + (k0 + x) * (2048 / 16), io, j + k0 + x > 0);
+            if (release) tc::commit(tc::smem_addr(&b.empty[(v_first + p) % kSlots]));
+        }
+        // A parity tells two phases apart: pv_done of tile j - 1 is asked for while that of j cannot be there yet (its
+        // weights are not), and the last one has a barrier of its own.
+        tc::commit(tc::smem_addr(last ? &b.o_full[q] : &b.pv_done[q]));
+    };
+    auto take = [&](uint32_t& first) { first = slot, slot += kParts; };
+    while (true) {
+        ca_wait(b, &b.unit_full[k & 1], (k >> 1) & 1);
+        const int tiles = b.unit[k & 1].tiles, nq = kNQ == 2 && b.unit[k & 1].rows > 128 ? 2 : 1;
+        ca_arrive(&b.unit_empty[k & 1]);
+        if (tiles <= 0 || ca_bad(b)) break;
+        ca_wait(b, &b.q_full, k & 1);
+        tc::fence_after_sync();
+        // one tile of rows: scores of tile j, then values of the one before; two: the values of either, then its scores
+        // of the next tile
+#pragma unroll 1
+        for (int j = kNQ == 1 ? 0 : -1; j < tiles + (kNQ == 1 ? 1 : 0); ++j) {
+            if (kNQ == 1) {
+                if (j < tiles) {
+                    take(k_first);
+                    scores(0, soft0 + j, true);
+                    if (j + 1 == tiles) tc::commit(tc::smem_addr(&b.q_empty));
+                }
+                if (j > 0) {
+                    take(v_first);
+                    values(0, soft0 + j - 1, j - 1, k, j == tiles, true);
+                }
+            } else {
+                if (j >= 0) take(v_first);
+                if (j + 1 < tiles) take(k_first);
+#pragma unroll 1
+                for (int q = 0; q < nq; ++q) {
+                    const uint32_t g = (q ? soft1 : soft0) + j;
+                    if (j >= 0) values(q, g, j, q ? units1 : k, j + 1 == tiles, q + 1 == nq);
+                    if (j + 1 < tiles) scores(q, g + 1, q + 1 == nq);
+                }
+                if (j + 2 == tiles) tc::commit(tc::smem_addr(&b.q_empty));
+            }
+        }
+        soft0 += tiles;
+        if (nq == 2) soft1 += tiles, ++units1;
+        ++k;
+    }
+    if (ca_bad(b)) {
+        // a wait gave up: the products in flight still end before tensor memory is given back
+        tc::commit(tc::smem_addr(&b.end));
+        tc::mbar_wait_parity_bounded(tc::smem_addr(&b.end), 0, 1 << 19);
+    }
+}
+
+// What was taken out of the values of a unit's last tiles, added to 32 values of a row that sees it.
+template <int DT, int D>
+__device__ __noinline__ void ca_add_odd(const CaArgs& c, const CaBars& b, const CaUnit& u, uint32_t k, int pos, int col, float* v) {
+    const int first = u.tile0 + ca_partly(c, u);
+    for (int i = 0; i < 16; ++i)
+        for (uint32_t m = b.odd[k & 1][i >> 2][i & 3]; m; m &= m - 1) {
+            const int key = (first + (i >> 2)) * kKeys + 32 * (i & 3) + __ffs(m) - 1;
+            if (key > pos || key >= u.keys) return;
+            const int p = c.by_page(key), pg = c.a.table[static_cast<long long>(u.s) * c.a.max_pages + p];  // (a page that is there)
+            const long long row = (static_cast<long long>(pg) * c.a.Hkv + u.kvh) * c.a.page + (key - p * c.a.page);
+            for (int e = 0; e < 32; ++e) {
+                const float x = load_act(c.a.v_pool, row * D + col + e, DT);
+                if (!(fabsf(x) < INFINITY)) v[e] += x;
+            }
+        }
+}
+
+// ---- the weights, one row a thread
+template <int DT, int D>
+__device__ __forceinline__ void ca_soft(const CaArgs& c, CaBars& b, uint32_t tmem) {
+    using C = CaCfg<D>;
+    constexpr int kNQ = C::kNQ;
+    const ChunkAttnArgs& a = c.a;
+    const int r = threadIdx.x, lane = r & 31, q = r >> 7, group = a.Hq / a.Hkv;  // row of the unit, tile of rows
+    const uint32_t lanes = static_cast<uint32_t>(r & 96) << 16, o_col = tmem + lanes + q * D;
+    const bool flip = a.scale < 0.f;
+    // (a scale of 0 is next to 0: masked scores stay -infinity so)
+    const float sc = a.scale == 0.f ? 1e-30f : fabsf(a.scale) * kLog2e;
+    uint32_t tile = 0, soft = 0, units = 0;  // tiles of keys; those, and units, that have this tile of rows
+    CaUnit u;
+    for (uint32_t k = 0; ca_next(b, k, lane, u); ++k, tile += u.tiles) {
+        if (128 * q >= u.rows) continue;
+        const int R = u.row0 + r, tok = c.by_group(R), pos = r < u.rows ? u.pos + tok : -1;
+        float m = -INFINITY, l = 0.f;
+#pragma unroll 1
+        for (int j = 0; j < u.tiles; ++j) {
+            const uint32_t g = soft + j;
+            const int buf = kNQ == 1 ? g & 1 : q;
+            const uint32_t s_col = tmem + lanes + C::kScol + 128 * buf;
+            ca_wait(b, &b.s_full[buf], kNQ == 1 ? (g >> 1) & 1 : g & 1);
+            tc::fence_after_sync();
+            // keys of the tile that the row sees
+            const int lim = pos + 1 - (u.tile0 + j) * kKeys;
+            const uint4 there = *reinterpret_cast<const uint4*>(b.masks[(tile + j) % kMasks]);
+            if (!__all_sync(0xffffffffu, lim >= kKeys && (there.x & there.y & there.z & there.w) == 0xFFFFFFFFu)) {
+#pragma unroll 1
+                for (int x = 0; x < 4; ++x) {
+                    const int n = lim - 32 * x;
+                    const uint32_t see = (x == 0 ? there.x : x == 1 ? there.y : x == 2 ? there.z : there.w) & (n >= 32 ? 0xFFFFFFFFu : n <= 0 ? 0u : (1u << n) - 1);
+                    float v[32];
+                    tc::tmem_ld32(s_col + 32 * x, v);
+                    tc::tmem_ld_wait();
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) v[e] = see >> e & 1 ? v[e] : flip ? INFINITY : -INFINITY;
+                    tc::tmem_st32(s_col + 32 * x, v);
+                }
+                tc::tmem_st_wait();
+            }
+            // all of the row at once: a wait for tensor memory takes hundreds of cycles beside the products
+            float v[4][32];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) tc::tmem_ld32(s_col + 32 * x, v[x]);
+            tc::tmem_ld_wait();
+            if (flip) {
+#pragma unroll
+                for (int x = 0; x < 4; ++x)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e) v[x][e] = -v[x][e];
+            }
+            float tops[4];
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                tops[x] = fmaxf(v[x][0], v[x][1]);
+#pragma unroll
+                for (int e = 2; e < 32; e += 2) tops[x] = fmaxf(tops[x], fmaxf(v[x][e], v[x][e + 1]));
+            }
+            float top = fmaxf(fmaxf(tops[0], tops[1]), fmaxf(tops[2], tops[3])) * sc;
+            const bool rise = top > m + kTau<DT>;
+            if (__any_sync(0xffffffffu, rise)) {
+                const float corr = rise ? ex2(m - top) : 1.f;
+                if (rise) m = top, l *= corr;
+                if (j > 0) {
+                    ca_wait(b, &b.pv_done[q], (g - 1 - units) & 1);
+                    tc::fence_after_sync();
+#pragma unroll 1
+                    for (int x = 0; x < D; x += 16) {
+                        float o[16];
+                        tc::tmem_ld16(o_col + x, o);
+                        tc::tmem_ld_wait();
+                        uint32_t p[16];
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) p[e] = __float_as_uint(o[e] * corr);
+                        tc::tmem_st16(o_col + x, p);
+                    }
+                }
+            }
+            const float back = kUp<DT> - (m == -INFINITY ? 0.f : m);
+            const float2 sc2 = make_float2(sc, sc), back2 = make_float2(back, back);
+            float2 sum[2] = {make_float2(0.f, 0.f), make_float2(0.f, 0.f)};
+#pragma unroll
+            for (int x = 0; x < 4; ++x) {
+                uint32_t p[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e) {
+                    const float2 y = __ffma2_rn(make_float2(v[x][2 * e], v[x][2 * e + 1]), sc2, back2);
+                    const float2 w = make_float2(ex2(y.x), ex2(y.y));
+                    sum[e & 1] = __fadd2_rn(sum[e & 1], w);
+                    p[e] = ca_pack<DT>(w.x, w.y);
+                }
+                tc::tmem_st16(s_col + 16 * x, p);
+            }
+            l += (sum[0].x + sum[0].y) + (sum[1].x + sum[1].y);
+            tc::tmem_st_wait();
+            tc::fence_before_sync();
+            __syncwarp();
+            if (lane == 0) ca_arrive(&b.p_full[buf]);
+        }
+        ca_wait(b, &b.o_full[q], units & 1);
+        tc::fence_after_sync();
+        if (ca_bad(b)) l = NAN;
+        const bool odd = *reinterpret_cast<volatile uint32_t*>(&b.any_odd[k & 1]) != 0;
+        const long long head = static_cast<long long>(u.first + tok) * a.Hq + u.kvh * group + (R - tok * group);
+        const long long slot = 2ll * blockIdx.x + (u.tile0 == 0 ? 1 : 0);
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+#pragma unroll 1
+        for (int x = 0; x < D; x += 32) {
+            float v[32];
+            tc::tmem_ld32(o_col + x, v);
+            tc::tmem_ld_wait();
+            if (odd) {
+                float w[32];
+#pragma unroll
+                for (int e = 0; e < 32; ++e) w[e] = v[e];
+                ca_add_odd<DT, D>(c, b, u, k, pos, x, w);
+#pragma unroll
+                for (int e = 0; e < 32; ++e) v[e] = w[e];
+            }
+            if (r < u.rows) {
+                if (u.whole) {
+                    uint16_t* out = static_cast<uint16_t*>(a.out) + head * D + x;
+#pragma unroll
+                    for (int e = 0; e < 32; e += 8)
+                        *reinterpret_cast<uint4*>(out + e) = make_uint4(ca_pack<DT>(v[e] * inv, v[e + 1] * inv), ca_pack<DT>(v[e + 2] * inv, v[e + 3] * inv),
+                                                                       ca_pack<DT>(v[e + 4] * inv, v[e + 5] * inv), ca_pack<DT>(v[e + 6] * inv, v[e + 7] * inv));
+                } else {
+                    float* acc = c.parts.acc + (slot * C::kRows + r) * D + x;
+#pragma unroll
+                    for (int e = 0; e < 32; e += 4) *reinterpret_cast<float4*>(acc + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                }
+            }
+        }
+        tc::fence_before_sync();
+        __syncwarp();
+        if (lane == 0) ca_arrive(&b.o_empty[q]);
+        if (r < u.rows) {
+            if (!u.whole) *reinterpret_cast<float2*>(c.parts.ml + (slot * C::kRows + r) * 2) = make_float2(m, l);
+            else if (a.lse) a.lse[head] = l == 0.f ? -INFINITY : (m - kUp<DT> + log2f(l)) * kLn2;
+        }
+        soft += u.tiles, ++units;
+    }
+}
+
+template <int DT, int D, bool kRanges>
+__global__ void __launch_bounds__(CaCfg<D>::kThreads, 1) chunk_attention_kernel(const __grid_constant__ CaArgs c) {
+    using C = CaCfg<D>;
+    extern __shared__ unsigned char raw[];
+    __shared__ __align__(16) CaBars b;
+    __shared__ CaList list;
+    __shared__ uint4 response;
+    const int t = threadIdx.x, warp = t >> 5;
+    if (t == 0) {
+        auto init = [](unsigned long long* bar, uint32_t count) { tc::mbar_init_cta(tc::smem_addr(bar), count); };
+#pragma unroll 1
+        for (int i = 0; i < C::kSlots; ++i) init(&b.full[i], c.box ? 1 : C::kLoadWarps), init(&b.empty[i], 1), init(&b.raw[i], 1);
+#pragma unroll 1
+        for (int i = 0; i < 2; ++i) {
+            init(&b.s_full[i], 1), init(&b.p_full[i], 4), init(&b.pv_done[i], 1), init(&b.o_full[i], 1), init(&b.o_empty[i], 4);
+            init(&b.unit_full[i], 1), init(&b.unit_empty[i], C::kSoftWarps + C::kLoadWarps + 1);
+        }
+        init(&b.q_full, C::kLoadWarps), init(&b.q_empty, 1), init(&b.want, 1), init(&b.stolen, 1), init(&b.end, 1);
+        b.bad = 0;
+        tc::fence_proxy_async_smem();
+    }
+    if (warp == C::kMmaWarp) {
+        tc::tmem_alloc(&b.tmem, 512);
+        tc::tmem_relinquish();
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    pdl_wait();
+    pdl_trigger();
+    const uint32_t tmem = b.tmem, q_smem = (tc::smem_addr(raw) + 1023) & ~1023u, ring = q_smem + C::kQBytes;
+    // Two tiles of rows: 384 threads begin with 168 registers each, 256 x 200 + 128 x 104 in all.
+    if (warp < C::kSoftWarps) {
+        if (C::kNQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
+        ca_soft<DT, D>(c, b, tmem);
+    } else {
+        if (C::kNQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
+        if (warp < C::kMmaWarp && c.box) ca_load_boxes<DT, D, kRanges>(c, b, q_smem, ring);
+        else if (warp < C::kMmaWarp) ca_load_rows<DT, D, kRanges>(c, b, q_smem, ring);
+        else if (warp == C::kUnitWarp) ca_units<C::kRows, kRanges>(c, b, list, &response);
+        else if ((t & 31) == 0) ca_products<DT, D>(b, q_smem, ring, tmem);
+        __syncwarp();
+    }
+    tc::fence_before_sync();
+    __syncthreads();
+    tc::fence_after_sync();
+    if (warp == C::kMmaWarp) tc::tmem_dealloc(tmem, 512);
+}
+
+// Joins the parts of a unit that lies in several of the `grid` CTAs' ranges: CTA (rows_each rows, run, key head). kSets
+// sets of threads take interleaved parts.
+constexpr int kCaJoinThreads = 256;
+template <int DT, int D>
+__global__ void __launch_bounds__(kCaJoinThreads) chunk_attention_join_kernel(const __grid_constant__ CaArgs c, int grid, int rows_each) {
+    const ChunkAttnArgs& a = c.a;
+    const CaParts& parts = c.parts;
+    constexpr int kRows = CaCfg<D>::kRows, kCols = D / 4, kSets = kCaJoinThreads / kCols, kAtOnce = 4;
+    __shared__ float4 sums[kSets][kCols];
+    __shared__ __align__(8) float mls[kSms][2];
+    const int group = a.Hq / a.Hkv, t = threadIdx.x, col = t % kCols, set = t / kCols, d = col * 4;
+    pdl_wait();
+    pdl_trigger();
+    const CaList& list = *parts.list;
+    if (static_cast<int>(blockIdx.y) >= list.n) return;
+    const int kvh = blockIdx.z, s = list.unit[blockIdx.y] & 0xFFFFu, run = list.unit[blockIdx.y] >> 16;
+    const int total = list.tiles * a.Hkv, first = list.tiles * kvh + list.first[blockIdx.y], last = list.tiles * kvh + list.first[blockIdx.y + 1] - 1;
+    const int ctas = min(grid, total), each = total / ctas, rest = total % ctas;
+    // CTA i begins at tile i each + floor(i rest / ctas): tile x is CTA x / each's, or one of the few before it
+    auto owner = [&](int x) {
+        int i = min(x / each, ctas - 1);
+        while (i * each + i * rest / ctas > x) --i;
+        return i;
+    };
+    const int c0 = owner(first), n = owner(last) - c0 + 1;
+    const CaSeq seq(a, s);
+    if (n == 1) return;  // finished
+    const int r0 = blockIdx.x * rows_each, r1 = min(r0 + rows_each, min(kRows, seq.tokens * group - run * kRows));
+    for (int r = r0; r < r1; ++r) {
+        // (a CTA's part of a unit that it begins is its second one)
+        auto at = [&](int i) { return (2ll * (c0 + i) + (i == 0 ? 1 : 0)) * kRows + r; };
+        __syncthreads();
+        for (int i = t; i < n; i += kCaJoinThreads) *reinterpret_cast<float2*>(mls[i]) = *reinterpret_cast<const float2*>(parts.ml + at(i) * 2);
+        __syncthreads();
+        float top = -INFINITY, sum = 0.f;
+        for (int i = 0; i < n; ++i) top = fmaxf(top, mls[i][0]);
+        const float base = top == -INFINITY ? 0.f : top;
+        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int i = set; i < n; i += kSets * kAtOnce) {
+            float4 o[kAtOnce];
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k)
+                o[k] = i + k * kSets < n ? *reinterpret_cast<const float4*>(parts.acc + at(i + k * kSets) * D + d) : make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k) {
+                const float f = i + k * kSets < n ? ex2(mls[i + k * kSets][0] - base) : 0.f;
+                v.x += o[k].x * f, v.y += o[k].y * f, v.z += o[k].z * f, v.w += o[k].w * f;
+            }
+        }
+        sums[set][col] = v;
+        for (int i = 0; i < n; ++i) sum += mls[i][1] * ex2(mls[i][0] - base);
+        __syncthreads();
+        if (set == 0) {
+#pragma unroll
+            for (int k = 1; k < kSets; ++k) {
+                const float4 o = sums[k][col];
+                v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
+            }
+            const float inv = sum == 0.f ? 0.f : 1.f / sum;
+            const int R = run * kRows + r, tok = c.by_group(R);
+            const long long head = (long long)(seq.first + tok) * a.Hq + kvh * group + (R - tok * group);
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + head * D + d) =
+                make_uint2(ca_pack<DT>(v.x * inv, v.y * inv), ca_pack<DT>(v.z * inv, v.w * inv));
+            if (d == 0 && a.lse) a.lse[head] = sum == 0.f ? -INFINITY : (top - kUp<DT> + log2f(sum)) * kLn2;
+        }
+    }
+}
+
+struct CaPlan {
+    long long runs;  // at most
+    bool ranges;
+    int ctas;
+    size_t ml, list, total;
+};
+CaPlan ca_plan(int n, int T, int Hq, int Hkv, int d, int max_len) {
+    CaPlan p{};
+    const int rows = d == 256 ? 128 : 256, group = Hq / Hkv;
+    p.runs = (long long)T * group / rows + (n < T ? n : T);
+    const long long units = p.runs * Hkv;
+    p.ranges = p.runs <= kCaRuns && units < 100 && max_len > 2 * kKeys && units * (max_len / kKeys + 1) < 1ll << 30;
+    p.ctas = kSms;
+    if (p.ranges) {
+        p.ml = static_cast<size_t>(2) * p.ctas * rows * d * 4;
+        p.list = p.ml + static_cast<size_t>(2) * p.ctas * rows * 8;
+        p.total = p.list + sizeof(CaList);
+    }
+    return p;
+}
+CaDiv ca_div(int d) {
+    int l = 0;
+    while ((1ll << l) < d) ++l;
+    return CaDiv{static_cast<uint32_t>(((1ull << (31 + l)) + d - 1) / d), 31 + l};
+}
+
+// A pool as a matrix of rows of d values, for loads of `box` rows and 64 values.
+bool ca_map(CUtensorMap* map, const void* pool, int dtype, int d, int box, const ChunkAttnArgs& a) {
+    static const PFN_cuTensorMapEncodeTiled_v12000 encode = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
+        void* f = nullptr;
+        cudaDriverEntryPointQueryResult found;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) != cudaSuccess) return nullptr;
+        return found == cudaDriverEntryPointSuccess ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f) : nullptr;
+    }();
+    const cuuint64_t size[2] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(a.n_pages) * a.Hkv * a.page}, stride[1] = {static_cast<cuuint64_t>(d) * 2};
+    const cuuint32_t part[2] = {64, static_cast<cuuint32_t>(box)}, step[2] = {1, 1};
+    return encode && encode(map, dtype == 1 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(pool), size, stride, part,
+                            step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                            CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
+template <int DT, int D>
+cudaError_t ca_launch(const ChunkAttnArgs& a, void* ws, cudaStream_t s) {
+    using C = CaCfg<D>;
+    const CaPlan p = ca_plan(a.n, a.T, a.Hq, a.Hkv, D, a.max_len);
+    const long long cap = (long long)a.max_pages * a.page;
+    char* w = static_cast<char*>(ws);
+    CaArgs c{{}, {}, a, 0, static_cast<int>(cap < a.max_len ? cap : a.max_len), ca_div(a.page), ca_div(a.Hq / a.Hkv),
+             CaParts{reinterpret_cast<float*>(w), reinterpret_cast<float*>(w + p.ml), reinterpret_cast<CaList*>(w + p.list)}};
+    if (a.page % 8 == 0) {
+        c.box = 8;
+        while (c.box < kKeys && a.page % (2 * c.box) == 0) c.box *= 2;
+        if (!ca_map(&c.keys, a.k_pool, DT, D, c.box, a) || !ca_map(&c.values, a.v_pool, DT, D, c.box, a)) c.box = 0;
+    }
+    const void* f = p.ranges ? reinterpret_cast<const void*>(chunk_attention_kernel<DT, D, true>)
+                             : reinterpret_cast<const void*>(chunk_attention_kernel<DT, D, false>);
+    cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);
+    if (e != cudaSuccess) return e;
+    void* args[] = {&c};
+    e = launch_kernel(f, dim3(static_cast<unsigned>(p.ranges ? p.ctas : p.runs * a.Hkv)), dim3(C::kThreads), C::kSmem, true, s, args);
+    if (e != cudaSuccess || !p.ranges) return e;
+    int grid = p.ctas, rows_each = 1;
+    while (rows_each < 8 && p.runs * a.Hkv * (C::kRows / rows_each) > 16 * kSms) rows_each *= 2;
+    void* jargs[] = {&c, &grid, &rows_each};
+    return launch_kernel(reinterpret_cast<const void*>(chunk_attention_join_kernel<DT, D>),
+                         dim3(C::kRows / rows_each, static_cast<unsigned>(p.runs), a.Hkv), dim3(kCaJoinThreads), 0, true, s, jargs);
 }
 
 }  // namespace
 
-size_t chunk_attention_ws_bytes(int, int, int, int, int, int) { return 0; }
+size_t chunk_attention_ws_bytes(int n, int T, int Hq, int Hkv, int d, int max_len) { return ca_plan(n, T, Hq, Hkv, d, max_len).total; }
 
-cudaError_t launch_chunk_attention(const ChunkAttnArgs& a, int dtype, void*, cudaStream_t s) {
-    const void* fs[2][3] = {{reinterpret_cast<const void*>(chunk_attention_kernel<1, 64>),
-                             reinterpret_cast<const void*>(chunk_attention_kernel<1, 128>),
-                             reinterpret_cast<const void*>(chunk_attention_kernel<1, 256>)},
-                            {reinterpret_cast<const void*>(chunk_attention_kernel<2, 64>),
-                             reinterpret_cast<const void*>(chunk_attention_kernel<2, 128>),
-                             reinterpret_cast<const void*>(chunk_attention_kernel<2, 256>)}};
-    const long long items = (long long)a.T * a.Hq;
-    void* args[] = {const_cast<ChunkAttnArgs*>(&a)};
-    return launch_kernel(fs[dtype - 1][a.d / 128], dim3(static_cast<unsigned>((items + kCaWarps - 1) / kCaWarps)),
-                         dim3(kCaWarps * 32), 0, true, s, args);
+cudaError_t launch_chunk_attention(const ChunkAttnArgs& a, int dtype, void* ws, cudaStream_t s) {
+    if (dtype == 1) return a.d == 64 ? ca_launch<1, 64>(a, ws, s) : a.d == 128 ? ca_launch<1, 128>(a, ws, s) : ca_launch<1, 256>(a, ws, s);
+    return a.d == 64 ? ca_launch<2, 64>(a, ws, s) : a.d == 128 ? ca_launch<2, 128>(a, ws, s) : ca_launch<2, 256>(a, ws, s);
 }
 
 }  // namespace escha

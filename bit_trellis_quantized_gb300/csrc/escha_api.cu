@@ -1286,7 +1286,7 @@ int check_chunk_shape(int n, int T, int Hq, int Hkv, int d, int max_len, const c
     const int r = check_paged_shape(n, Hq, Hkv, d, max_len, name);
     if (r) return r;
     if (T < 1) return fail(ESCHA_E_ARG, "%s: T=%d must be >= 1", name, T);
-    if ((long long)T * Hq >= (1ll << 40) / d) return fail(ESCHA_E_SHAPE, "%s: T * Hq * d = %d * %d * %d is above 2^40", name, T, Hq, d);
+    if ((long long)T * Hq >= (1ll << 40) / d || (long long)T * (Hq / Hkv) > 0x7fff0000ll) return fail(ESCHA_E_SHAPE, "%s: T=%d tokens of Hq=%d heads of d=%d are too many", name, T, Hq, d);
     return ESCHA_OK;
 }
 

@@ -667,7 +667,8 @@ int escha_rotary_append(const void* q, const void* k, const void* v, int src_dty
  *            (may be 0); nothing in it has to start at zero
  * A token that no key is left to (a position below 0, pages that are none) gives
  * out = 0 and lse = -infinity. Rows of no sequence are left as they are. Keys
- * behind a sequence's last token are never read. n <= 65535, T Hq d below 2^40.
+ * behind a sequence's last token are never read. n <= 65535, T Hq d below 2^40,
+ * T Hq / Hkv below 2^31 - 65535.
  * Errors as escha_paged_attention. */
 size_t escha_chunk_attention_workspace(int n, int T, int Hq, int Hkv, int d, int max_len);
 int escha_chunk_attention(const void* q, const void* k_pool, const void* v_pool, int dtype, const int32_t* table,

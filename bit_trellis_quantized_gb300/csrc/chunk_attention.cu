@@ -328,11 +328,14 @@ __device__ __forceinline__ void ca_queries(const CaArgs& c, const CaUnit& u, uin
     const int t = threadIdx.x - 32 * CaCfg<D>::kSoftWarps, group = c.a.Hq / c.a.Hkv, p = t % kPieces;
     const char* q0 = static_cast<const char*>(c.a.q) + ((static_cast<long long>(u.first) * c.a.Hq + u.kvh * group) * D + p * 8) * 2;
     const int end = u.rows > 128 ? CaCfg<D>::kRows : 128;
+    int r = t / kPieces, tok = c.by_group(u.row0 + r), g = u.row0 + r - tok * group;
 #pragma unroll 4
-    for (int r = t / kPieces; r < end; r += kStep) {
-        const int R = u.row0 + r, tok = r < u.rows ? c.by_group(R) : 0;
-        const long long from = r < u.rows ? (static_cast<long long>(tok) * c.a.Hq + (R - tok * group)) * (D * 2) : 0;
-        cp16(q_smem + (r >> 7) * (128 * D * 2) + (p >> 3) * 16384 + tc::kmajor_off(r & 127, (p & 7) * 8), q0 + from, r < u.rows);
+    for (; r < end; r += kStep) {
+        const bool on = r < u.rows;
+        const long long from = on ? (static_cast<long long>(tok) * c.a.Hq + g) * (D * 2) : 0;
+        cp16(q_smem + (r >> 7) * (128 * D * 2) + (p >> 3) * 16384 + tc::kmajor_off(r & 127, (p & 7) * 8), q0 + from, on);
+        g += kStep;
+        while (g >= group) g -= group, ++tok;
     }
     cp_commit();
 }
@@ -355,23 +358,38 @@ template <int DT, int D>
 __device__ __forceinline__ void ca_take_odd(uint32_t slot, int r0, int r1, uint32_t* odd, uint32_t* any) {
     constexpr int kPieces = CaCfg<D>::kSlotD / 8;
     const int lane = threadIdx.x & 31, p = lane % kPieces;
+    constexpr int kBatch = 8, kStep = 32 / kPieces;
+    constexpr uint32_t kExp = DT == 1 ? 0x7C00u : 0x7F80u;
 #pragma unroll 1
-    for (int r = r0 + lane / kPieces; r < r1; r += 32 / kPieces) {
-        const uint32_t at = slot + (p >> 3) * 16384 + tc::kmajor_off(r, (p & 7) * 8);
-        uint32_t x[4];
-        asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(x[0]), "=r"(x[1]), "=r"(x[2]), "=r"(x[3]) : "r"(at) : "memory");
-        constexpr uint32_t kExp = DT == 1 ? 0x7C00u : 0x7F80u;
-        bool some = false;
+    for (int r = r0 + lane / kPieces; r < r1; r += kBatch * kStep) {
+        uint32_t x[kBatch][4], some = 0;
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const bool lo = (x[e] & kExp) == kExp, hi = (x[e] >> 16 & kExp) == kExp;
-            some |= lo | hi;
-            if (lo) x[e] &= 0xFFFF0000u;
-            if (hi) x[e] &= 0x0000FFFFu;
-        }
-        if (some) {
-            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(x[0]), "r"(x[1]), "r"(x[2]), "r"(x[3]) : "memory");
-            atomicOr(odd + (r >> 5), 1u << (r & 31));
+        for (int i = 0; i < kBatch; ++i)
+            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(x[i][0]), "=r"(x[i][1]), "=r"(x[i][2]), "=r"(x[i][3])
+                         : "r"(slot + (p >> 3) * 16384 + tc::kmajor_off(r + i * kStep, (p & 7) * 8))
+                         : "memory");
+#pragma unroll
+        for (int i = 0; i < kBatch; ++i)
+#pragma unroll
+            for (int e = 0; e < 4; ++e)  // an exponent of all ones carries out
+                some |= ((x[i][e] & 0x7FFF7FFFu) + ((0x8000u - kExp) * 0x10001u)) & 0x80008000u;
+        if (some == 0) continue;
+#pragma unroll 1
+        for (int i = 0; i < kBatch; ++i) {
+            const uint32_t at = slot + (p >> 3) * 16384 + tc::kmajor_off(r + i * kStep, (p & 7) * 8);
+            uint32_t y[4];
+            asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(y[0]), "=r"(y[1]), "=r"(y[2]), "=r"(y[3]) : "r"(at) : "memory");
+            bool hit = false;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const bool lo = (y[e] & kExp) == kExp, hi = (y[e] >> 16 & kExp) == kExp;
+                hit |= lo | hi;
+                if (lo) y[e] &= 0xFFFF0000u;
+                if (hi) y[e] &= 0x0000FFFFu;
+            }
+            if (!hit) continue;
+            asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(at), "r"(y[0]), "r"(y[1]), "r"(y[2]), "r"(y[3]) : "memory");
+            atomicOr(odd + ((r + i * kStep) >> 5), 1u << ((r + i * kStep) & 31));
             *any = 1;
         }
     }
@@ -561,97 +579,129 @@ __device__ __forceinline__ void ca_load_rows(const CaArgs& c, CaBars& b, uint32_
     }
 }
 
-// ---- the thread that issues the products
+// ---- the warp that issues the products. All of it keeps step, so that addresses stay in uniform registers (one thread by
+// itself takes longer over an instruction's operands than the tensor cores over its product); one lane's count.
+__device__ __forceinline__ void ca_mma(uint32_t d, uint32_t a_lo, uint32_t a_hi, uint32_t b_lo, uint32_t b_hi, uint32_t idesc, bool add, bool lead) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 x, y;\n\tsetp.ne.b32 p, %6, 0;\n\tsetp.ne.b32 q, %7, 0;\n\tmov.b64 x, {%1, %2};\n\tmov.b64 y, {%3, %4};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], x, y, %5, p;\n\t}" ::"r"(d),
+        "r"(a_lo), "r"(a_hi), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(add ? 1u : 0u), "r"(lead ? 1u : 0u)
+        : "memory");
+}
+__device__ __forceinline__ void ca_mma_ts(uint32_t d, uint32_t a_tmem, uint32_t b_lo, uint32_t b_hi, uint32_t idesc, bool add, bool lead) {
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .b64 y;\n\tsetp.ne.b32 p, %5, 0;\n\tsetp.ne.b32 q, %6, 0;\n\tmov.b64 y, {%2, %3};\n\t"
+        "@q tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], y, %4, p;\n\t}" ::"r"(d),
+        "r"(a_tmem), "r"(b_lo), "r"(b_hi), "r"(idesc), "r"(add ? 1u : 0u), "r"(lead ? 1u : 0u)
+        : "memory");
+}
 template <int DT, int D>
-__device__ __forceinline__ void ca_products(CaBars& b, uint32_t q_smem, uint32_t ring, uint32_t tmem) {
+__device__ __forceinline__ void ca_products(CaBars& b, uint32_t q_smem, uint32_t ring) {
     using C = CaCfg<D>;
     constexpr int kNQ = C::kNQ, kParts = C::kParts, kSlots = C::kSlots;
     constexpr uint32_t is = tc::idesc_f16(128, 128, false, false, DT == 2), io = tc::idesc_f16(128, C::kSlotD, false, true, DT == 2);
-    const uint64_t k_desc = tc::smem_desc(ring, 16, 1024, tc::kSwizzle128B), q_desc = tc::smem_desc(q_smem, 16, 1024, tc::kSwizzle128B);
-    const uint64_t v_desc = tc::smem_desc(ring, 16384, 1024, tc::kSwizzle128B);  // (addresses in 16 bytes, added to)
-    uint32_t slot = 0, k_first = 0, v_first = 0, k = 0;
-    uint32_t soft0 = 0, soft1 = 0, units1 = 0;  // tiles of keys of either tile of rows, units that have the second one
-    auto full = [&](uint32_t i) {
-        ca_wait(b, &b.full[i % kSlots], (i / kSlots) & 1);
+    // descriptors: addresses in 16 bytes, added to, under constant upper halves
+    const uint32_t kq_hi = static_cast<uint32_t>(tc::smem_desc(0, 16, 1024, tc::kSwizzle128B) >> 32), v_hi = kq_hi;
+    const uint32_t kq_lo = static_cast<uint32_t>(tc::smem_desc(0, 16, 1024, tc::kSwizzle128B)), v_lo = static_cast<uint32_t>(tc::smem_desc(0, 16384, 1024, tc::kSwizzle128B));
+    const uint32_t q16 = q_smem >> 4, ring16 = ring >> 4;
+    const bool lead = (threadIdx.x & 31) == 0;
+    uint32_t k_at = 0, v_at = 0, k = 0;           // slots of the current tile's keys and values (of the ring)
+    uint32_t next = 0, round = 0;                 // the next slot, and how often the ring has been gone round
+    uint32_t k_round = 0, v_round = 0;
+    uint32_t soft0 = 0, soft1 = 0, units1 = 0;    // tiles of keys of either tile of rows, units that have the second one
+    auto commit = [&](unsigned long long* bar) {
+        if (lead) tc::commit(tc::smem_addr(bar));
+        __syncwarp();
+    };
+    auto wait = [&](unsigned long long* bar, uint32_t parity) {
+        ca_wait(b, bar, parity);
+        __syncwarp();
         tc::fence_after_sync();
     };
+    auto after = [&](uint32_t at, uint32_t& r) {  // the slot behind `at`
+        if (++at == kSlots) at = 0, ++r;
+        return at;
+    };
     auto scores = [&](int q, uint32_t g, bool release) {
-        const uint32_t buf = kNQ == 1 ? g & 1 : q;
-#pragma unroll 1
-        for (int p = 0; p < kParts; ++p) {
-            full(k_first + p);
-            const uint64_t kb = k_desc + ((k_first + p) % kSlots) * (C::kSlotBytes / 16);
-            const uint64_t qb = q_desc + (q * (128 * D * 2) + p * (C::kSlotD / 64) * 16384) / 16;
-#pragma unroll 1
-            for (int c = 0; c < C::kSlotD / 64; ++c)
+        const uint32_t buf = kNQ == 1 ? g & 1 : q, d = C::kScol + 128 * buf;
+        uint32_t at = k_at, r = k_round;
 #pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    tc::mma_f16(tmem + C::kScol + 128 * buf, qb + (c * 16384 + x * 32) / 16, kb + (c * 16384 + x * 32) / 16, is, p + c + x > 0);
-            if (release) tc::commit(tc::smem_addr(&b.empty[(k_first + p) % kSlots]));
+        for (int p = 0; p < kParts; ++p) {
+            wait(&b.full[at], r & 1);
+            const uint32_t kb = kq_lo + ring16 + at * (C::kSlotBytes / 16), qb = kq_lo + q16 + (q * (128 * D * 2) + p * (C::kSlotD / 64) * 16384) / 16;
+#pragma unroll
+            for (int x = 0; x < C::kSlotD / 16; ++x) {
+                const uint32_t o = ((x >> 2) * 16384 + (x & 3) * 32) / 16;
+                ca_mma(d, qb + o, kq_hi, kb + o, kq_hi, is, p + x > 0, lead);
+            }
+            if (release) commit(&b.empty[at]);
+            at = after(at, r);
         }
-        tc::commit(tc::smem_addr(&b.s_full[buf]));
+        commit(&b.s_full[buf]);
     };
     auto values = [&](int q, uint32_t g, int j, uint32_t units, bool last, bool release) {
         const uint32_t buf = kNQ == 1 ? g & 1 : q;
-        if (j == 0) ca_wait(b, &b.o_empty[q], (units - 1) & 1);
-        ca_wait(b, &b.p_full[buf], kNQ == 1 ? (g >> 1) & 1 : g & 1);
-        tc::fence_after_sync();
-#pragma unroll 1
-        for (int p = 0; p < kParts; ++p) {
-            full(v_first + p);
-            const uint64_t vb = v_desc + ((v_first + p) % kSlots) * (C::kSlotBytes / 16);
-#pragma unroll 1
-            for (int k0 = 0; k0 < kKeys / 16; k0 += 4)
+        if (j == 0) wait(&b.o_empty[q], (units - 1) & 1);
+        wait(&b.p_full[buf], kNQ == 1 ? (g >> 1) & 1 : g & 1);
+        uint32_t at = v_at, r = v_round;
 #pragma unroll
-                for (int x = 0; x < 4; ++x)
-                    tc::mma_f16_ts(tmem + q * D + p * 128, tmem + C::kScol + 128 * buf + (k0 + x) * 8, vb + (k0 + x) * (2048 / 16), io, j + k0 + x > 0);
-            if (release) tc::commit(tc::smem_addr(&b.empty[(v_first + p) % kSlots]));
+        for (int p = 0; p < kParts; ++p) {
+            wait(&b.full[at], r & 1);
+            const uint32_t vb = v_lo + ring16 + at * (C::kSlotBytes / 16);
+#pragma unroll
+            for (int x = 0; x < kKeys / 16; ++x)
+                ca_mma_ts(q * D + p * 128, C::kScol + 128 * buf + x * 8, vb + x * (2048 / 16), v_hi, io, j > 0 || x > 0, lead);
+            if (release) commit(&b.empty[at]);
+            at = after(at, r);
         }
         // A parity tells two phases apart: pv_done of tile j - 1 is asked for while that of j cannot be there yet (its
         // weights are not), and the last one has a barrier of its own.
-        tc::commit(tc::smem_addr(last ? &b.o_full[q] : &b.pv_done[q]));
+        commit(last ? &b.o_full[q] : &b.pv_done[q]);
     };
-    auto take = [&](uint32_t& first) { first = slot, slot += kParts; };
+    auto take = [&](uint32_t& at, uint32_t& r) {
+        at = next, r = round;
+#pragma unroll
+        for (int p = 0; p < kParts; ++p) next = after(next, round);
+    };
     while (true) {
-        ca_wait(b, &b.unit_full[k & 1], (k >> 1) & 1);
-        const int tiles = b.unit[k & 1].tiles, nq = kNQ == 2 && b.unit[k & 1].rows > 128 ? 2 : 1;
-        ca_arrive(&b.unit_empty[k & 1]);
-        if (tiles <= 0 || ca_bad(b)) break;
-        ca_wait(b, &b.q_full, k & 1);
-        tc::fence_after_sync();
+        wait(&b.unit_full[k & 1], (k >> 1) & 1);
+        const int tiles = __shfl_sync(0xffffffffu, b.unit[k & 1].tiles, 0), nq = kNQ == 2 && __shfl_sync(0xffffffffu, b.unit[k & 1].rows, 0) > 128 ? 2 : 1;
+        if (lead) ca_arrive(&b.unit_empty[k & 1]);
+        if (tiles <= 0 || __any_sync(0xffffffffu, ca_bad(b))) break;
+        wait(&b.q_full, k & 1);
         // one tile of rows: scores of tile j, then values of the one before; two: the values of either, then its scores
         // of the next tile
 #pragma unroll 1
         for (int j = kNQ == 1 ? 0 : -1; j < tiles + (kNQ == 1 ? 1 : 0); ++j) {
             if (kNQ == 1) {
                 if (j < tiles) {
-                    take(k_first);
+                    take(k_at, k_round);
                     scores(0, soft0 + j, true);
-                    if (j + 1 == tiles) tc::commit(tc::smem_addr(&b.q_empty));
+                    if (j + 1 == tiles) commit(&b.q_empty);
                 }
                 if (j > 0) {
-                    take(v_first);
+                    take(v_at, v_round);
                     values(0, soft0 + j - 1, j - 1, k, j == tiles, true);
                 }
             } else {
-                if (j >= 0) take(v_first);
-                if (j + 1 < tiles) take(k_first);
+                if (j >= 0) take(v_at, v_round);
+                if (j + 1 < tiles) take(k_at, k_round);
 #pragma unroll 1
                 for (int q = 0; q < nq; ++q) {
                     const uint32_t g = (q ? soft1 : soft0) + j;
                     if (j >= 0) values(q, g, j, q ? units1 : k, j + 1 == tiles, q + 1 == nq);
                     if (j + 1 < tiles) scores(q, g + 1, q + 1 == nq);
                 }
-                if (j + 2 == tiles) tc::commit(tc::smem_addr(&b.q_empty));
+                if (j + 2 == tiles) commit(&b.q_empty);
             }
         }
         soft0 += tiles;
         if (nq == 2) soft1 += tiles, ++units1;
         ++k;
     }
-    if (ca_bad(b)) {
+    if (__any_sync(0xffffffffu, ca_bad(b))) {
         // a wait gave up: the products in flight still end before tensor memory is given back
-        tc::commit(tc::smem_addr(&b.end));
+        commit(&b.end);
         tc::mbar_wait_parity_bounded(tc::smem_addr(&b.end), 0, 1 << 19);
     }
 }
@@ -671,6 +721,19 @@ __device__ __noinline__ void ca_add_odd(const CaArgs& c, const CaBars& b, const 
                 if (!(fabsf(x) < INFINITY)) v[e] += x;
             }
         }
+}
+
+// 32 bytes of a row: a whole sector each, as neighbouring lanes write other rows (32-byte aligned: rows are, and so is `p`
+// where the buffer is; others by halves)
+__device__ __forceinline__ void ca_store32(void* p, const uint32_t (&w)[8]) {
+    if (reinterpret_cast<uintptr_t>(p) % 32 == 0) {
+        asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]), "r"(w[3]), "r"(w[4]), "r"(w[5]),
+                     "r"(w[6]), "r"(w[7])
+                     : "memory");
+    } else {
+        static_cast<uint4*>(p)[0] = make_uint4(w[0], w[1], w[2], w[3]);
+        static_cast<uint4*>(p)[1] = make_uint4(w[4], w[5], w[6], w[7]);
+    }
 }
 
 // ---- the weights, one row a thread
@@ -797,13 +860,21 @@ __device__ __forceinline__ void ca_soft(const CaArgs& c, CaBars& b, uint32_t tme
                 if (u.whole) {
                     uint16_t* out = static_cast<uint16_t*>(a.out) + head * D + x;
 #pragma unroll
-                    for (int e = 0; e < 32; e += 8)
-                        *reinterpret_cast<uint4*>(out + e) = make_uint4(ca_pack<DT>(v[e] * inv, v[e + 1] * inv), ca_pack<DT>(v[e + 2] * inv, v[e + 3] * inv),
-                                                                       ca_pack<DT>(v[e + 4] * inv, v[e + 5] * inv), ca_pack<DT>(v[e + 6] * inv, v[e + 7] * inv));
+                    for (int e = 0; e < 32; e += 16) {
+                        uint32_t w[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) w[i] = ca_pack<DT>(v[e + 2 * i] * inv, v[e + 2 * i + 1] * inv);
+                        ca_store32(out + e, w);
+                    }
                 } else {
                     float* acc = c.parts.acc + (slot * C::kRows + r) * D + x;
 #pragma unroll
-                    for (int e = 0; e < 32; e += 4) *reinterpret_cast<float4*>(acc + e) = make_float4(v[e], v[e + 1], v[e + 2], v[e + 3]);
+                    for (int e = 0; e < 32; e += 8) {
+                        uint32_t w[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) w[i] = __float_as_uint(v[e + i]);
+                        ca_store32(acc + e, w);
+                    }
                 }
             }
         }
@@ -848,7 +919,8 @@ __global__ void __launch_bounds__(CaCfg<D>::kThreads, 1) chunk_attention_kernel(
     tc::fence_after_sync();
     pdl_wait();
     pdl_trigger();
-    const uint32_t tmem = b.tmem, q_smem = (tc::smem_addr(raw) + 1023) & ~1023u, ring = q_smem + C::kQBytes;
+    constexpr uint32_t tmem = 0;  // (all of tensor memory is this CTA's)
+    const uint32_t q_smem = (tc::smem_addr(raw) + 1023) & ~1023u, ring = q_smem + C::kQBytes;
     // Two tiles of rows: 384 threads begin with 168 registers each, 256 x 200 + 128 x 104 in all.
     if (warp < C::kSoftWarps) {
         if (C::kNQ == 2) asm volatile("setmaxnreg.inc.sync.aligned.u32 200;");
@@ -858,7 +930,7 @@ __global__ void __launch_bounds__(CaCfg<D>::kThreads, 1) chunk_attention_kernel(
         if (warp < C::kMmaWarp && c.box) ca_load_boxes<DT, D, kRanges>(c, b, q_smem, ring);
         else if (warp < C::kMmaWarp) ca_load_rows<DT, D, kRanges>(c, b, q_smem, ring);
         else if (warp == C::kUnitWarp) ca_units<C::kRows, kRanges>(c, b, list, &response);
-        else if ((t & 31) == 0) ca_products<DT, D>(b, q_smem, ring, tmem);
+        else ca_products<DT, D>(b, q_smem, ring);
         __syncwarp();
     }
     tc::fence_before_sync();

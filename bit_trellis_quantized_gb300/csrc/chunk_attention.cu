@@ -110,8 +110,10 @@ struct CaParts {
 };
 struct CaArgs {
     CUtensorMap keys, values;  // the pools as rows of d values, in boxes of `box` rows and 64 values
+    CUtensorMap queries;       // [T][Hq][d] in boxes of 128 rows of a unit and 64 values
     ChunkAttnArgs a;
     int box;  // rows of a page that are loaded at once: 8 to 128, or 0 (pages not of a multiple of 8): rows one by one
+    bool q_boxes;  // 128 rows are whole tokens
     int cap;  // keys that may be read
     CaDiv by_page, by_group;
     CaParts parts;
@@ -321,16 +323,31 @@ __device__ __forceinline__ void ca_units(const CaArgs& c, CaBars& b, CaList& lis
 }
 
 // ---- the warps that load
-// A unit's queries, by both.
+// A unit's queries: boxes by the first warp, or rows by both, 16 bytes a lane. (Rows of a box behind the sequence's last
+// token see no key.)
 template <int D>
-__device__ __forceinline__ void ca_queries(const CaArgs& c, const CaUnit& u, uint32_t q_smem) {
+__device__ __forceinline__ void ca_queries(const CaArgs& c, CaBars& b, const CaUnit& u, uint32_t q_smem) {
     constexpr int kPieces = D / 8, kStep = 32 * CaCfg<D>::kLoadWarps / kPieces;
     const int t = threadIdx.x - 32 * CaCfg<D>::kSoftWarps, group = c.a.Hq / c.a.Hkv, p = t % kPieces;
+    const int tiles = u.rows > 128 ? 2 : 1;
+    if (c.q_boxes) {
+        if (t == 0) {
+            tc::mbar_arrive_expect_tx(tc::smem_addr(&b.q_full), tiles * 128 * D * 2);
+#pragma unroll 1
+            for (int i = 0; i < tiles * (D / 64); ++i) {
+                const int q = i / (D / 64), x = i % (D / 64);
+                asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(q_smem + i * 16384),
+                             "l"(&c.queries), "r"(x * 64), "r"(u.kvh * group), "r"(u.first + c.by_group(u.row0 + 128 * q)), "r"(tc::smem_addr(&b.q_full))
+                             : "memory");
+            }
+        }
+        __syncwarp();
+        return;
+    }
     const char* q0 = static_cast<const char*>(c.a.q) + ((static_cast<long long>(u.first) * c.a.Hq + u.kvh * group) * D + p * 8) * 2;
-    const int end = u.rows > 128 ? CaCfg<D>::kRows : 128;
     int r = t / kPieces, tok = c.by_group(u.row0 + r), g = u.row0 + r - tok * group;
 #pragma unroll 4
-    for (; r < end; r += kStep) {
+    for (; r < 128 * tiles; r += kStep) {
         const bool on = r < u.rows;
         const long long from = on ? (static_cast<long long>(tok) * c.a.Hq + g) * (D * 2) : 0;
         cp16(q_smem + (r >> 7) * (128 * D * 2) + (p >> 3) * 16384 + tc::kmajor_off(r & 127, (p & 7) * 8), q0 + from, on);
@@ -339,7 +356,8 @@ __device__ __forceinline__ void ca_queries(const CaArgs& c, const CaUnit& u, uin
     }
     cp_commit();
 }
-__device__ __forceinline__ void ca_queries_landed(CaBars& b) {
+__device__ __forceinline__ void ca_queries_landed(const CaArgs& c, CaBars& b) {
+    if (c.q_boxes) return;
     cp_wait<0>();
     tc::fence_proxy_async_smem();
     __syncwarp();
@@ -358,7 +376,7 @@ template <int DT, int D>
 __device__ __forceinline__ void ca_take_odd(uint32_t slot, int r0, int r1, uint32_t* odd, uint32_t* any) {
     constexpr int kPieces = CaCfg<D>::kSlotD / 8;
     const int lane = threadIdx.x & 31, p = lane % kPieces;
-    constexpr int kBatch = 8, kStep = 32 / kPieces;
+    constexpr int kBatch = 16, kStep = 32 / kPieces;
     constexpr uint32_t kExp = DT == 1 ? 0x7C00u : 0x7F80u;
 #pragma unroll 1
     for (int r = r0 + lane / kPieces; r < r1; r += kBatch * kStep) {
@@ -412,8 +430,8 @@ __device__ __forceinline__ void ca_load_boxes(const CaArgs& c, CaBars& b, uint32
         const int partly = ca_partly(c, u);
         uint32_t* odd = &b.odd[k & 1][0][0];
         if (w == 1) {
-            ca_queries<D>(c, u, q_smem);
-            ca_queries_landed(b);
+            ca_queries<D>(c, b, u, q_smem);
+            ca_queries_landed(c, b);
 #pragma unroll 1
             for (int j = partly; j < u.tiles; ++j)
 #pragma unroll 1
@@ -433,7 +451,7 @@ __device__ __forceinline__ void ca_load_boxes(const CaArgs& c, CaBars& b, uint32
         if (lane < 16) odd[lane] = 0;
         if (lane == 16) b.any_odd[k & 1] = 0;
         __syncwarp();
-        ca_queries<D>(c, u, q_smem);
+        ca_queries<D>(c, b, u, q_smem);
         const int32_t* table = a.table + static_cast<long long>(u.s) * a.max_pages;
         auto find = [&](int j) -> int {  // this lane's box of tile j: its row in the pools
             const int key = (u.tile0 + j) * kKeys + my_box * c.box;
@@ -475,7 +493,7 @@ __device__ __forceinline__ void ca_load_boxes(const CaArgs& c, CaBars& b, uint32
                                  : "memory");
                 ++slot;
             }
-            if (j == 0) ca_queries_landed(b);
+            if (j == 0) ca_queries_landed(c, b);
             if (!kRanges && lane == 0 && j == max(u.tiles - 3, 0)) ca_arrive(&b.want);
             last = row, row = next, next = later;
         }
@@ -519,8 +537,8 @@ __device__ __forceinline__ void ca_load_rows(const CaArgs& c, CaBars& b, uint32_
         if (w == 0 && lane < 16) b.odd[k & 1][lane >> 2][lane & 3] = 0;
         if (w == 0 && lane == 16) b.any_odd[k & 1] = 0;
         asm volatile("bar.sync 1, %0;" ::"n"(32 * C::kLoadWarps) : "memory");
-        ca_queries<D>(c, u, q_smem);
-        ca_queries_landed(b);
+        ca_queries<D>(c, b, u, q_smem);
+        ca_queries_landed(c, b);
         const int32_t* table = a.table + static_cast<long long>(u.s) * a.max_pages;
         // lane r's rows 64 w + r and 64 w + 32 + r of tile j: their numbers in the pools (-1: not there)
         auto find = [&](int j, int (&row)[2]) {
@@ -906,7 +924,7 @@ __global__ void __launch_bounds__(CaCfg<D>::kThreads, 1) chunk_attention_kernel(
             init(&b.s_full[i], 1), init(&b.p_full[i], 4), init(&b.pv_done[i], 1), init(&b.o_full[i], 1), init(&b.o_empty[i], 4);
             init(&b.unit_full[i], 1), init(&b.unit_empty[i], C::kSoftWarps + C::kLoadWarps + 1);
         }
-        init(&b.q_full, C::kLoadWarps), init(&b.q_empty, 1), init(&b.want, 1), init(&b.stolen, 1), init(&b.end, 1);
+        init(&b.q_full, c.q_boxes ? 1 : C::kLoadWarps), init(&b.q_empty, 1), init(&b.want, 1), init(&b.stolen, 1), init(&b.end, 1);
         b.bad = 0;
         tc::fence_proxy_async_smem();
     }
@@ -941,7 +959,7 @@ __global__ void __launch_bounds__(CaCfg<D>::kThreads, 1) chunk_attention_kernel(
 
 // Joins the parts of a unit that lies in several of the `grid` CTAs' ranges: CTA (rows_each rows, run, key head). kSets
 // sets of threads take interleaved parts.
-constexpr int kCaJoinThreads = 256;
+constexpr int kCaJoinThreads = 512;
 template <int DT, int D>
 __global__ void __launch_bounds__(kCaJoinThreads) chunk_attention_join_kernel(const __grid_constant__ CaArgs c, int grid, int rows_each) {
     const ChunkAttnArgs& a = c.a;
@@ -970,26 +988,34 @@ __global__ void __launch_bounds__(kCaJoinThreads) chunk_attention_join_kernel(co
     for (int r = r0; r < r1; ++r) {
         // (a CTA's part of a unit that it begins is its second one)
         auto at = [&](int i) { return (2ll * (c0 + i) + (i == 0 ? 1 : 0)) * kRows + r; };
+        auto part = [&](int i) {
+            return i < n ? *reinterpret_cast<const float4*>(parts.acc + at(i) * D + d) : make_float4(0.f, 0.f, 0.f, 0.f);
+        };
+        float4 o[kAtOnce];  // (on their way before their factors are known)
+#pragma unroll
+        for (int k = 0; k < kAtOnce; ++k) o[k] = part(set + k * kSets);
         __syncthreads();
         for (int i = t; i < n; i += kCaJoinThreads) *reinterpret_cast<float2*>(mls[i]) = *reinterpret_cast<const float2*>(parts.ml + at(i) * 2);
         __syncthreads();
         float top = -INFINITY, sum = 0.f;
-        for (int i = 0; i < n; ++i) top = fmaxf(top, mls[i][0]);
+        for (int i = t & 31; i < n; i += 32) top = fmaxf(top, mls[i][0]);
+#pragma unroll
+        for (int m = 16; m >= 1; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
         const float base = top == -INFINITY ? 0.f : top;
+        for (int i = t & 31; i < n; i += 32) sum += mls[i][1] * ex2(mls[i][0] - base);
+#pragma unroll
+        for (int m = 16; m >= 1; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
         for (int i = set; i < n; i += kSets * kAtOnce) {
-            float4 o[kAtOnce];
-#pragma unroll
-            for (int k = 0; k < kAtOnce; ++k)
-                o[k] = i + k * kSets < n ? *reinterpret_cast<const float4*>(parts.acc + at(i + k * kSets) * D + d) : make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll
             for (int k = 0; k < kAtOnce; ++k) {
                 const float f = i + k * kSets < n ? ex2(mls[i + k * kSets][0] - base) : 0.f;
                 v.x += o[k].x * f, v.y += o[k].y * f, v.z += o[k].z * f, v.w += o[k].w * f;
             }
+#pragma unroll
+            for (int k = 0; k < kAtOnce; ++k) o[k] = part(i + (kAtOnce + k) * kSets);
         }
         sums[set][col] = v;
-        for (int i = 0; i < n; ++i) sum += mls[i][1] * ex2(mls[i][0] - base);
         __syncthreads();
         if (set == 0) {
 #pragma unroll
@@ -1017,8 +1043,12 @@ CaPlan ca_plan(int n, int T, int Hq, int Hkv, int d, int max_len) {
     CaPlan p{};
     const int rows = d == 256 ? 128 : 256, group = Hq / Hkv;
     p.runs = (long long)T * group / rows + (n < T ? n : T);
-    const long long units = p.runs * Hkv;
-    p.ranges = p.runs <= kCaRuns && units < 100 && max_len > 2 * kKeys && units * (max_len / kKeys + 1) < 1ll << 30;
+    const long long units = p.runs * Hkv, rounds = (units + kSms - 1) / kSms;
+    // Whole units leave CTAs idle in the last round of them, for the time of (rounds 152 - units) / 152 units of the tiles
+    // that a unit may have (the host does not know the lengths: an even share of the tokens, behind the longest cache);
+    // cut over all CTAs they end together, which costs the parts and a second kernel. In tiles of 1.5 us:
+    const long long tokens = T / n, tiles = (max_len - (tokens < max_len ? tokens : max_len) / 2) / kKeys + 1;
+    p.ranges = p.runs <= kCaRuns && (rounds * kSms - units) * tiles > 12 * kSms && units * (max_len / kKeys + 1) < 1ll << 30;
     p.ctas = kSms;
     if (p.ranges) {
         p.ml = static_cast<size_t>(2) * p.ctas * rows * d * 4;
@@ -1033,19 +1063,32 @@ CaDiv ca_div(int d) {
     return CaDiv{static_cast<uint32_t>(((1ull << (31 + l)) + d - 1) / d), 31 + l};
 }
 
-// A pool as a matrix of rows of d values, for loads of `box` rows and 64 values.
-bool ca_map(CUtensorMap* map, const void* pool, int dtype, int d, int box, const ChunkAttnArgs& a) {
-    static const PFN_cuTensorMapEncodeTiled_v12000 encode = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
-        void* f = nullptr;
+PFN_cuTensorMapEncodeTiled_v12000 ca_encode() {
+    static const PFN_cuTensorMapEncodeTiled_v12000 f = []() -> PFN_cuTensorMapEncodeTiled_v12000 {
+        void* p = nullptr;
         cudaDriverEntryPointQueryResult found;
-        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &f, 12000, cudaEnableDefault, &found) != cudaSuccess) return nullptr;
-        return found == cudaDriverEntryPointSuccess ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(f) : nullptr;
+        if (cudaGetDriverEntryPointByVersion("cuTensorMapEncodeTiled", &p, 12000, cudaEnableDefault, &found) != cudaSuccess) return nullptr;
+        return found == cudaDriverEntryPointSuccess ? reinterpret_cast<PFN_cuTensorMapEncodeTiled_v12000>(p) : nullptr;
     }();
-    const cuuint64_t size[2] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(a.n_pages) * a.Hkv * a.page}, stride[1] = {static_cast<cuuint64_t>(d) * 2};
-    const cuuint32_t part[2] = {64, static_cast<cuuint32_t>(box)}, step[2] = {1, 1};
-    return encode && encode(map, dtype == 1 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 2, const_cast<void*>(pool), size, stride, part,
+    return f;
+}
+bool ca_map(CUtensorMap* map, const void* p, int dtype, int dims, const cuuint64_t* size, const cuuint64_t* stride, const cuuint32_t* box) {
+    const cuuint32_t step[3] = {1, 1, 1};
+    const auto encode = ca_encode();
+    return encode && encode(map, dtype == 1 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dims, const_cast<void*>(p), size, stride, box,
                             step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+bool ca_map_pool(CUtensorMap* map, const void* pool, int dtype, int d, int box, const ChunkAttnArgs& a) {
+    const cuuint64_t size[2] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(a.n_pages) * a.Hkv * a.page}, stride[1] = {static_cast<cuuint64_t>(d) * 2};
+    const cuuint32_t part[2] = {64, static_cast<cuuint32_t>(box)};
+    return ca_map(map, pool, dtype, 2, size, stride, part);
+}
+bool ca_map_queries(CUtensorMap* map, int dtype, int d, const ChunkAttnArgs& a) {
+    const cuuint64_t size[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(a.Hq), static_cast<cuuint64_t>(a.T)};
+    const cuuint64_t stride[2] = {static_cast<cuuint64_t>(d) * 2, static_cast<cuuint64_t>(a.Hq) * d * 2};
+    const cuuint32_t group = a.Hq / a.Hkv, part[3] = {64, group, 128 / group};
+    return ca_map(map, a.q, dtype, 3, size, stride, part);
 }
 
 template <int DT, int D>
@@ -1054,13 +1097,14 @@ cudaError_t ca_launch(const ChunkAttnArgs& a, void* ws, cudaStream_t s) {
     const CaPlan p = ca_plan(a.n, a.T, a.Hq, a.Hkv, D, a.max_len);
     const long long cap = (long long)a.max_pages * a.page;
     char* w = static_cast<char*>(ws);
-    CaArgs c{{}, {}, a, 0, static_cast<int>(cap < a.max_len ? cap : a.max_len), ca_div(a.page), ca_div(a.Hq / a.Hkv),
+    CaArgs c{{}, {}, {}, a, 0, false, static_cast<int>(cap < a.max_len ? cap : a.max_len), ca_div(a.page), ca_div(a.Hq / a.Hkv),
              CaParts{reinterpret_cast<float*>(w), reinterpret_cast<float*>(w + p.ml), reinterpret_cast<CaList*>(w + p.list)}};
     if (a.page % 8 == 0) {
         c.box = 8;
         while (c.box < kKeys && a.page % (2 * c.box) == 0) c.box *= 2;
-        if (!ca_map(&c.keys, a.k_pool, DT, D, c.box, a) || !ca_map(&c.values, a.v_pool, DT, D, c.box, a)) c.box = 0;
+        if (!ca_map_pool(&c.keys, a.k_pool, DT, D, c.box, a) || !ca_map_pool(&c.values, a.v_pool, DT, D, c.box, a)) c.box = 0;
     }
+    c.q_boxes = 128 % (a.Hq / a.Hkv) == 0 && ca_map_queries(&c.queries, DT, D, a);
     const void* f = p.ranges ? reinterpret_cast<const void*>(chunk_attention_kernel<DT, D, true>)
                              : reinterpret_cast<const void*>(chunk_attention_kernel<DT, D, false>);
     cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);

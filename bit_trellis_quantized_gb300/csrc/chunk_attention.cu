@@ -109,7 +109,7 @@ struct CaParts {
     CaList* list;
 };
 struct CaArgs {
-    CUtensorMap keys, values;  // the pools as rows of d values, in boxes of `box` rows and 64 values
+    CUtensorMap keys, values;  // the pools as [rows / 8][d / 64][8][64], in boxes of `box` rows and a slot's values
     CUtensorMap queries;       // [T][Hq][d] in boxes of 128 rows of a unit and 64 values
     ChunkAttnArgs a;
     int box;  // rows of a page that are loaded at once: 8 to 128, or 0 (pages not of a multiple of 8): rows one by one
@@ -323,6 +323,13 @@ __device__ __forceinline__ void ca_units(const CaArgs& c, CaBars& b, CaList& lis
 }
 
 // ---- the warps that load
+// A slot holds 128 keys as groups of 8: [group][64 values][key][128 bytes, swizzled]. 16-byte piece p of key r is at
+template <int D>
+__device__ __forceinline__ uint32_t ca_at(int r, int p) {
+    constexpr uint32_t kChunks = CaCfg<D>::kSlotD / 64;
+    return ((r >> 3) * kChunks + (p >> 3)) * 1024 + (r & 7) * 128 + (((p & 7) ^ (r & 7)) << 4);
+}
+
 // A unit's queries: boxes by the first warp, or rows by both, 16 bytes a lane. (Rows of a box behind the sequence's last
 // token see no key.)
 template <int D>
@@ -364,19 +371,19 @@ __device__ __forceinline__ void ca_queries_landed(const CaArgs& c, CaBars& b) {
     if ((threadIdx.x & 31) == 0) ca_arrive(&b.q_full);
 }
 
-// The first tile that not every row of the unit sees in full, from the unit's first one.
-__device__ __forceinline__ int ca_partly(const CaArgs& c, const CaUnit& u) {
-    return max(max(0, u.pos + c.by_group(u.row0) + 1) / kKeys - u.tile0, 0);
-}
+// Keys that every row of the unit sees.
+__device__ __forceinline__ int ca_common(const CaArgs& c, const CaUnit& u) { return max(0, u.pos + c.by_group(u.row0) + 1); }
+// The first tile that not every row sees in full, from the unit's first one.
+__device__ __forceinline__ int ca_partly(const CaArgs& c, const CaUnit& u) { return max(ca_common(c, u) / kKeys - u.tile0, 0); }
 
 // The values of such a tile: a weight of 0 would still carry what is not finite into rows that do not see it (keys of
 // later tokens, what lies behind the last one). So it is taken out here, and added at the end where it is seen. A warp's
-// rows r0, r0 + step, ... of a slot, a 16-byte piece a lane; `odd`: a bit a key of the tile.
+// rows r0 .. r1 - 1 of a slot (multiples of 8), a 16-byte piece a lane; `odd`: a bit a key of the tile.
 template <int DT, int D>
 __device__ __forceinline__ void ca_take_odd(uint32_t slot, int r0, int r1, uint32_t* odd, uint32_t* any) {
     constexpr int kPieces = CaCfg<D>::kSlotD / 8;
     const int lane = threadIdx.x & 31, p = lane % kPieces;
-    constexpr int kBatch = 16, kStep = 32 / kPieces;
+    constexpr int kStep = 32 / kPieces, kBatch = 8 / kStep;
     constexpr uint32_t kExp = DT == 1 ? 0x7C00u : 0x7F80u;
 #pragma unroll 1
     for (int r = r0 + lane / kPieces; r < r1; r += kBatch * kStep) {
@@ -384,7 +391,7 @@ __device__ __forceinline__ void ca_take_odd(uint32_t slot, int r0, int r1, uint3
 #pragma unroll
         for (int i = 0; i < kBatch; ++i)
             asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(x[i][0]), "=r"(x[i][1]), "=r"(x[i][2]), "=r"(x[i][3])
-                         : "r"(slot + (p >> 3) * 16384 + tc::kmajor_off(r + i * kStep, (p & 7) * 8))
+                         : "r"(slot + ca_at<D>(r + i * kStep, p))
                          : "memory");
 #pragma unroll
         for (int i = 0; i < kBatch; ++i)
@@ -394,7 +401,7 @@ __device__ __forceinline__ void ca_take_odd(uint32_t slot, int r0, int r1, uint3
         if (some == 0) continue;
 #pragma unroll 1
         for (int i = 0; i < kBatch; ++i) {
-            const uint32_t at = slot + (p >> 3) * 16384 + tc::kmajor_off(r + i * kStep, (p & 7) * 8);
+            const uint32_t at = slot + ca_at<D>(r + i * kStep, p);
             uint32_t y[4];
             asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(y[0]), "=r"(y[1]), "=r"(y[2]), "=r"(y[3]) : "r"(at) : "memory");
             bool hit = false;
@@ -420,14 +427,14 @@ __device__ __forceinline__ void ca_load_boxes(const CaArgs& c, CaBars& b, uint32
     using C = CaCfg<D>;
     const ChunkAttnArgs& a = c.a;
     const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - C::kSoftWarps;
-    constexpr int kSlots = C::kSlots, kChunks = C::kSlotD / 64;
+    constexpr int kSlots = C::kSlots;
     const int boxes = kKeys / c.box, nowhere = a.n_pages * a.Hkv * a.page;  // (rows behind the pool's last are zeros)
-    const int my_box = lane % boxes, my_chunk = lane / boxes;
+    const int my_box = lane % boxes;
     uint32_t slot = 0, tile = 0, k = 0, phases = 0;
     CaUnit u;
     for (; ca_next(b, k, lane, u); ++k) {
         ca_wait(b, &b.q_empty, (k - 1) & 1);
-        const int partly = ca_partly(c, u);
+        const int partly = ca_partly(c, u), common = ca_common(c, u);
         uint32_t* odd = &b.odd[k & 1][0][0];
         if (w == 1) {
             ca_queries<D>(c, b, u, q_smem);
@@ -440,7 +447,9 @@ __device__ __forceinline__ void ca_load_boxes(const CaArgs& c, CaBars& b, uint32
                     const uint32_t i = slot + p + C::kParts * (C::kNQ == 1 ? min(2 * j + 2, 2 * u.tiles - 1) : 2 * j + 1), at = i % kSlots;
                     ca_wait(b, &b.raw[at], phases >> at & 1);
                     phases ^= 1u << at;
-                    ca_take_odd<DT, D>(ring + at * C::kSlotBytes, 0, kKeys, odd + 4 * (j - partly), &b.any_odd[k & 1]);
+                    // the rows that not all see and that were loaded: the rest of a box behind the last key, no further
+                    const int key0 = (u.tile0 + j) * kKeys, r0 = max(common - key0, 0) & ~7, r1 = min((u.keys - key0 + c.box - 1) & -c.box, kKeys);
+                    ca_take_odd<DT, D>(ring + at * C::kSlotBytes, r0, r1, odd + 4 * (j - partly), &b.any_odd[k & 1]);
                     tc::fence_proxy_async_smem();
                     __syncwarp();
                     if (lane == 0) ca_arrive(&b.full[at]);
@@ -485,11 +494,11 @@ __device__ __forceinline__ void ca_load_boxes(const CaArgs& c, CaBars& b, uint32
                 const uint32_t bar = tc::smem_addr(!keys_now && of >= partly ? &b.raw[at] : &b.full[at]);
                 if (lane == 0) tc::mbar_arrive_expect_tx(bar, C::kSlotBytes);
                 __syncwarp();
-                if (my_chunk < kChunks)
-                    asm volatile("cp.async.bulk.tensor.2d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3}], [%4];" ::"r"(
-                                     ring + at * C::kSlotBytes + my_chunk * 16384 + my_box * c.box * 128),
-                                 "l"(keys_now ? &c.keys : &c.values), "r"((keys_now ? i : i - C::kParts) * C::kSlotD + my_chunk * 64), "r"(of < j ? last : row),
-                                 "r"(bar)
+                if (lane < boxes)
+                    asm volatile("cp.async.bulk.tensor.4d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %2, %3, %4}], [%5];" ::"r"(
+                                     ring + at * C::kSlotBytes + my_box * c.box * (C::kSlotD * 2)),
+                                 "l"(keys_now ? &c.keys : &c.values), "r"(0), "r"((keys_now ? i : i - C::kParts) * (C::kSlotD / 64)),
+                                 "r"((of < j ? last : row) >> 3), "r"(bar)
                                  : "memory");
                 ++slot;
             }
@@ -512,7 +521,6 @@ __device__ __forceinline__ void ca_load_rows(const CaArgs& c, CaBars& b, uint32_
     uint32_t slot = 0, tile = 0, k = 0;
     int pending = 0;
     uint32_t marks = 0;  // of the slots in flight, oldest lowest, 4 bits each: 1 + which of the unit's last tiles the values are of
-    const uint32_t mine = (c8 >> 3) * 16384 + (64 * w + rr) * 128;
     // the slots in flight beyond `keep` have landed
     auto landed = [&](int keep) {
         if (keep) cp_wait<C::kAhead>();
@@ -573,14 +581,14 @@ __device__ __forceinline__ void ca_load_rows(const CaArgs& c, CaBars& b, uint32_
                 const uint32_t use = slot / kSlots;
                 if (use > 0) room(&b.empty[slot % kSlots], (use - 1) & 1);
                 const char* base = static_cast<const char*>(keys_now ? a.k_pool : a.v_pool) + (keys_now ? i : i - C::kParts) * (C::kSlotD * 2) + c8 * 16;
-                const uint32_t to = ring + slot % kSlots * C::kSlotBytes + mine;
+                const uint32_t to = ring + slot % kSlots * C::kSlotBytes;
 #pragma unroll 1
                 for (int h = 0; h < 2; ++h) {
                     const int from = h ? r1 : r0;
 #pragma unroll
                     for (int r = 0; r < 32; r += kAtOnce) {
                         const int n = __shfl_sync(0xffffffffu, from, r + rr);
-                        cp16(to + (32 * h + r) * 128 + (((c8 & 7) ^ ((r + rr) & 7)) << 4), base + static_cast<long long>(max(n, 0)) * (D * 2), n >= 0);
+                        cp16(to + ca_at<D>(64 * w + 32 * h + r + rr, c8), base + static_cast<long long>(max(n, 0)) * (D * 2), n >= 0);
                     }
                 }
                 cp_commit();
@@ -619,8 +627,11 @@ __device__ __forceinline__ void ca_products(CaBars& b, uint32_t q_smem, uint32_t
     constexpr int kNQ = C::kNQ, kParts = C::kParts, kSlots = C::kSlots;
     constexpr uint32_t is = tc::idesc_f16(128, 128, false, false, DT == 2), io = tc::idesc_f16(128, C::kSlotD, false, true, DT == 2);
     // descriptors: addresses in 16 bytes, added to, under constant upper halves
-    const uint32_t kq_hi = static_cast<uint32_t>(tc::smem_desc(0, 16, 1024, tc::kSwizzle128B) >> 32), v_hi = kq_hi;
-    const uint32_t kq_lo = static_cast<uint32_t>(tc::smem_desc(0, 16, 1024, tc::kSwizzle128B)), v_lo = static_cast<uint32_t>(tc::smem_desc(0, 16384, 1024, tc::kSwizzle128B));
+    constexpr uint32_t kChunks = C::kSlotD / 64;
+    const uint64_t q_desc = tc::smem_desc(0, 16, 1024, tc::kSwizzle128B), k_desc = tc::smem_desc(0, 16, kChunks * 1024, tc::kSwizzle128B);
+    const uint64_t v_desc = tc::smem_desc(0, 1024, kChunks * 1024, tc::kSwizzle128B);
+    const uint32_t q_lo = static_cast<uint32_t>(q_desc), q_hi = static_cast<uint32_t>(q_desc >> 32), k_lo = static_cast<uint32_t>(k_desc);
+    const uint32_t k_hi = static_cast<uint32_t>(k_desc >> 32), v_lo = static_cast<uint32_t>(v_desc), v_hi = static_cast<uint32_t>(v_desc >> 32);
     const uint32_t q16 = q_smem >> 4, ring16 = ring >> 4;
     const bool lead = (threadIdx.x & 31) == 0;
     uint32_t k_at = 0, v_at = 0, k = 0;           // slots of the current tile's keys and values (of the ring)
@@ -646,11 +657,10 @@ __device__ __forceinline__ void ca_products(CaBars& b, uint32_t q_smem, uint32_t
 #pragma unroll
         for (int p = 0; p < kParts; ++p) {
             wait(&b.full[at], r & 1);
-            const uint32_t kb = kq_lo + ring16 + at * (C::kSlotBytes / 16), qb = kq_lo + q16 + (q * (128 * D * 2) + p * (C::kSlotD / 64) * 16384) / 16;
+            const uint32_t kb = k_lo + ring16 + at * (C::kSlotBytes / 16), qb = q_lo + q16 + (q * (128 * D * 2) + p * (C::kSlotD / 64) * 16384) / 16;
 #pragma unroll
             for (int x = 0; x < C::kSlotD / 16; ++x) {
-                const uint32_t o = ((x >> 2) * 16384 + (x & 3) * 32) / 16;
-                ca_mma(d, qb + o, kq_hi, kb + o, kq_hi, is, p + x > 0, lead);
+                ca_mma(d, qb + ((x >> 2) * 16384 + (x & 3) * 32) / 16, q_hi, kb + ((x >> 2) * 1024 + (x & 3) * 32) / 16, k_hi, is, p + x > 0, lead);
             }
             if (release) commit(&b.empty[at]);
             at = after(at, r);
@@ -668,7 +678,7 @@ __device__ __forceinline__ void ca_products(CaBars& b, uint32_t q_smem, uint32_t
             const uint32_t vb = v_lo + ring16 + at * (C::kSlotBytes / 16);
 #pragma unroll
             for (int x = 0; x < kKeys / 16; ++x)
-                ca_mma_ts(q * D + p * 128, C::kScol + 128 * buf + x * 8, vb + x * (2048 / 16), v_hi, io, j > 0 || x > 0, lead);
+                ca_mma_ts(q * D + p * 128, C::kScol + 128 * buf + x * 8, vb + x * (kChunks * 2048 / 16), v_hi, io, j > 0 || x > 0, lead);
             if (release) commit(&b.empty[at]);
             at = after(at, r);
         }
@@ -964,7 +974,7 @@ template <int DT, int D>
 __global__ void __launch_bounds__(kCaJoinThreads) chunk_attention_join_kernel(const __grid_constant__ CaArgs c, int grid, int rows_each) {
     const ChunkAttnArgs& a = c.a;
     const CaParts& parts = c.parts;
-    constexpr int kRows = CaCfg<D>::kRows, kCols = D / 4, kSets = kCaJoinThreads / kCols, kAtOnce = 4;
+    constexpr int kRows = CaCfg<D>::kRows, kCols = D / 4, kSets = kCaJoinThreads / kCols, kAtOnce = 4, kFew = 4;
     __shared__ float4 sums[kSets][kCols];
     __shared__ __align__(8) float mls[kSms][2];
     const int group = a.Hq / a.Hkv, t = threadIdx.x, col = t % kCols, set = t / kCols, d = col * 4;
@@ -985,6 +995,38 @@ __global__ void __launch_bounds__(kCaJoinThreads) chunk_attention_join_kernel(co
     const CaSeq seq(a, s);
     if (n == 1) return;  // finished
     const int r0 = blockIdx.x * rows_each, r1 = min(r0 + rows_each, min(kRows, seq.tokens * group - run * kRows));
+    auto finish = [&](int r, const float4& v, float top, float sum) {
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        const int R = run * kRows + r, tok = c.by_group(R);
+        const long long head = (long long)(seq.first + tok) * a.Hq + kvh * group + (R - tok * group);
+        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + head * D + d) =
+            make_uint2(ca_pack<DT>(v.x * inv, v.y * inv), ca_pack<DT>(v.z * inv, v.w * inv));
+        if (d == 0 && a.lse) a.lse[head] = sum == 0.f ? -INFINITY : (top - kUp<DT> + log2f(sum)) * kLn2;
+    };
+    if (n <= kFew) {  // few parts: a set of threads takes a row, all its parts at once
+        for (int r = r0 + set; r < r1; r += kSets) {
+            float4 o[kFew];
+            float2 ml[kFew];
+#pragma unroll
+            for (int i = 0; i < kFew; ++i) {
+                const long long at = (2ll * (c0 + i) + (i == 0 ? 1 : 0)) * kRows + r;
+                o[i] = i < n ? *reinterpret_cast<const float4*>(parts.acc + at * D + d) : make_float4(0.f, 0.f, 0.f, 0.f);
+                ml[i] = i < n ? *reinterpret_cast<const float2*>(parts.ml + at * 2) : make_float2(-INFINITY, 0.f);
+            }
+            float top = -INFINITY, sum = 0.f;
+#pragma unroll
+            for (int i = 0; i < kFew; ++i) top = fmaxf(top, ml[i].x);
+            const float base = top == -INFINITY ? 0.f : top;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int i = 0; i < kFew; ++i) {
+                const float f = ex2(ml[i].x - base);
+                sum += ml[i].y * f, v.x += o[i].x * f, v.y += o[i].y * f, v.z += o[i].z * f, v.w += o[i].w * f;
+            }
+            finish(r, v, top, sum);
+        }
+        return;
+    }
     for (int r = r0; r < r1; ++r) {
         // (a CTA's part of a unit that it begins is its second one)
         auto at = [&](int i) { return (2ll * (c0 + i) + (i == 0 ? 1 : 0)) * kRows + r; };
@@ -1023,12 +1065,7 @@ __global__ void __launch_bounds__(kCaJoinThreads) chunk_attention_join_kernel(co
                 const float4 o = sums[k][col];
                 v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
             }
-            const float inv = sum == 0.f ? 0.f : 1.f / sum;
-            const int R = run * kRows + r, tok = c.by_group(R);
-            const long long head = (long long)(seq.first + tok) * a.Hq + kvh * group + (R - tok * group);
-            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + head * D + d) =
-                make_uint2(ca_pack<DT>(v.x * inv, v.y * inv), ca_pack<DT>(v.z * inv, v.w * inv));
-            if (d == 0 && a.lse) a.lse[head] = sum == 0.f ? -INFINITY : (top - kUp<DT> + log2f(sum)) * kLn2;
+            finish(r, v, top, sum);
         }
     }
 }
@@ -1073,16 +1110,17 @@ PFN_cuTensorMapEncodeTiled_v12000 ca_encode() {
     return f;
 }
 bool ca_map(CUtensorMap* map, const void* p, int dtype, int dims, const cuuint64_t* size, const cuuint64_t* stride, const cuuint32_t* box) {
-    const cuuint32_t step[3] = {1, 1, 1};
+    const cuuint32_t step[4] = {1, 1, 1, 1};
     const auto encode = ca_encode();
     return encode && encode(map, dtype == 1 ? CU_TENSOR_MAP_DATA_TYPE_FLOAT16 : CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, dims, const_cast<void*>(p), size, stride, box,
                             step, CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
                             CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 bool ca_map_pool(CUtensorMap* map, const void* pool, int dtype, int d, int box, const ChunkAttnArgs& a) {
-    const cuuint64_t size[2] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(a.n_pages) * a.Hkv * a.page}, stride[1] = {static_cast<cuuint64_t>(d) * 2};
-    const cuuint32_t part[2] = {64, static_cast<cuuint32_t>(box)};
-    return ca_map(map, pool, dtype, 2, size, stride, part);
+    const cuuint64_t row = static_cast<cuuint64_t>(d) * 2, size[4] = {64, 8, static_cast<cuuint64_t>(d) / 64, static_cast<cuuint64_t>(a.n_pages) * a.Hkv * a.page / 8};
+    const cuuint64_t stride[3] = {row, 128, 8 * row};
+    const cuuint32_t part[4] = {64, 8, static_cast<cuuint32_t>(d < 128 ? 1 : 2), static_cast<cuuint32_t>(box / 8)};
+    return ca_map(map, pool, dtype, 4, size, stride, part);
 }
 bool ca_map_queries(CUtensorMap* map, int dtype, int d, const ChunkAttnArgs& a) {
     const cuuint64_t size[3] = {static_cast<cuuint64_t>(d), static_cast<cuuint64_t>(a.Hq), static_cast<cuuint64_t>(a.T)};
@@ -1112,8 +1150,9 @@ cudaError_t ca_launch(const ChunkAttnArgs& a, void* ws, cudaStream_t s) {
     void* args[] = {&c};
     e = launch_kernel(f, dim3(static_cast<unsigned>(p.ranges ? p.ctas : p.runs * a.Hkv)), dim3(C::kThreads), C::kSmem, true, s, args);
     if (e != cudaSuccess || !p.ranges) return e;
+    // (many units: of few parts each)
     int grid = p.ctas, rows_each = 1;
-    while (rows_each < 8 && p.runs * a.Hkv * (C::kRows / rows_each) > 16 * kSms) rows_each *= 2;
+    while (rows_each < 32 && p.runs * a.Hkv * (C::kRows / rows_each) > 16 * kSms) rows_each *= 2;
     void* jargs[] = {&c, &grid, &rows_each};
     return launch_kernel(reinterpret_cast<const void*>(chunk_attention_join_kernel<DT, D>),
                          dim3(C::kRows / rows_each, static_cast<unsigned>(p.runs), a.Hkv), dim3(kCaJoinThreads), 0, true, s, jargs);

@@ -7,22 +7,29 @@
 //   each bias of i, in list order:   x = x + bias
 //   not allowed by the row's mask:   x = -infinity
 //
-// A CTA takes a slice of a row and holds a word for each of its tokens in
-// shared memory: how often the row's ids name it, and whether they do at all,
-// as whole-number sums, which come out alike in any order. Then one pass over
-// the slice reads what is to be changed (everything, where the result goes to
-// another buffer) and writes it.
+// A CTA takes 8192 tokens of a row and holds a word for each of them in shared
+// memory: how often the row's ids name it, and whether they do at all, as
+// whole-number sums, which come out alike in any order. Then one pass reads
+// what is to be changed (everything, where the result goes to another buffer),
+// all a thread's next loads at once, and writes it.
+//
+// Bound: the write of the banned and the changed logits, and the read of those
+// next to them. Slices of 32 KB let five CTAs share a multiprocessor, so that
+// one's counting runs beside another's pass.
 #include "common.cuh"
 #include "context.h"
 #include "kernels.h"
 #include "trellis_core.cuh"
 
+#include <limits.h>
+
 namespace escha {
 
 namespace {
 
-constexpr int kAlThreads = 512;
-constexpr int kAlSlice = 32768;  // tokens of a CTA at most: 128 KB of words
+constexpr int kAlThreads = 256;
+constexpr int kAlSlice = 8192;  // tokens of a CTA at most
+constexpr int kAlList = 512;    // biases of a slice in shared memory
 constexpr uint32_t kAlPrompt = 1u << 30, kAlBias = 1u << 31;  // the rest counts
 
 template <int DT>
@@ -50,11 +57,13 @@ struct AlVec<2> {
 };
 
 template <int DT>
-__global__ void __launch_bounds__(kAlThreads) adjust_logits_kernel(AdjustArgs a, int slice, int slices) {
+__global__ void __launch_bounds__(kAlThreads, 5) adjust_logits_kernel(AdjustArgs a, int slices) {
     using A = AlVec<DT>;
     using E = typename A::type;
-    constexpr int kN = A::kN;
-    extern __shared__ __align__(16) uint32_t words[];
+    constexpr int kN = A::kN, kGroups = 16 / kN;  // of a thread at once
+    __shared__ __align__(16) uint32_t words[kAlSlice];
+    __shared__ uint32_t masks[kAlSlice / 32 + 2];
+    __shared__ int list_n, list_at[kAlList], list_token[kAlList];  // biases: their places and tokens of the slice
     pdl_wait();
     pdl_trigger();
     const int t = threadIdx.x, row = blockIdx.x / slices;
@@ -63,96 +72,119 @@ __global__ void __launch_bounds__(kAlThreads) adjust_logits_kernel(AdjustArgs a,
     // Groups of kN values begin where `x` is aligned: group g is [g kN - skew, g kN - skew + kN).
     const int skew = static_cast<int>(reinterpret_cast<uintptr_t>(x) / sizeof(E) % kN);
     const bool vec = reinterpret_cast<uintptr_t>(y) / sizeof(E) % kN == static_cast<uintptr_t>(skew);
-    const long long base = (long long)(blockIdx.x % slices) * slice - skew;  // token of words[0]
-    for (int i = t * 4; i < slice; i += kAlThreads * 4) *reinterpret_cast<uint4*>(words + i) = make_uint4(0, 0, 0, 0);
-    __syncthreads();
-    if (a.ids) {
-        const int i0 = min(max(a.at[row], 0), a.n_ids), i1 = min(max(a.at[row + 1], 0), a.n_ids);
-        const long long late = (long long)i0 + (a.prompt ? max(a.prompt[row], 0) : 0);
+    const int base = static_cast<int>(blockIdx.x % slices) * kAlSlice - skew;  // token of words[0]
+    const int i0 = a.ids ? min(max(a.at[row], 0), a.n_ids) : 0, i1 = a.ids ? min(max(a.at[row + 1], 0), a.n_ids) : 0;
+    const int b0 = a.bias_ids ? min(max(a.bias_at[row], 0), a.n_bias) : 0, b1 = a.bias_ids ? min(max(a.bias_at[row + 1], 0), a.n_bias) : 0;
+    const int mrow = !a.allowed ? -1 : a.allowed_rows ? a.allowed_rows[row] : row, mwords = (a.V + 31) / 32;
+    const bool masked = static_cast<unsigned>(mrow) < static_cast<unsigned>(a.n_masks), copy = a.logits != a.out, counts = i0 < i1 || b0 < b1;
+    if (!masked && !copy && !counts) return;
+    if (masked) {  // masks[0] holds the token max(base, 0)
+        const uint32_t* m = reinterpret_cast<const uint32_t*>(a.allowed) + static_cast<long long>(mrow) * mwords;
+        for (int i = t; i < kAlSlice / 32 + 2; i += kAlThreads) masks[i] = max(base, 0) / 32 + i < mwords ? m[max(base, 0) / 32 + i] : 0u;
+    }
+    if (counts) {
+#pragma unroll
+        for (int i = 0; i < kAlSlice / (kAlThreads * 4); ++i) *reinterpret_cast<uint4*>(words + (i * kAlThreads + t) * 4) = make_uint4(0, 0, 0, 0);
+        if (t == 0) list_n = 0;
+        __syncthreads();
+        const long long late = static_cast<long long>(i0) + (a.prompt ? max(a.prompt[row], 0) : 0);
+#pragma unroll 4
         for (int i = i0 + t; i < i1; i += kAlThreads) {
-            const long long id = a.ids[i], w = id - base;
-            if (id < 0 || id >= a.V || w < 0 || w >= slice) continue;
+            const int id = a.ids[i];
+            const uint32_t w = static_cast<uint32_t>(id) - static_cast<uint32_t>(base);
+            if (static_cast<unsigned>(id) >= static_cast<unsigned>(a.V) || w >= kAlSlice) continue;
             if (i >= late) atomicAdd(&words[w], 1u);
             else atomicOr(&words[w], kAlPrompt);
         }
-    }
-    int b0 = 0, b1 = 0;
-    if (a.bias_ids) {
-        b0 = min(max(a.bias_at[row], 0), a.n_bias), b1 = min(max(a.bias_at[row + 1], 0), a.n_bias);
         for (int i = b0 + t; i < b1; i += kAlThreads) {
-            const long long id = a.bias_ids[i], w = id - base;
-            if (id >= 0 && id < a.V && w >= 0 && w < slice) atomicOr(&words[w], kAlBias);
+            const int id = a.bias_ids[i];
+            const uint32_t w = static_cast<uint32_t>(id) - static_cast<uint32_t>(base);
+            if (static_cast<unsigned>(id) >= static_cast<unsigned>(a.V) || w >= kAlSlice) continue;
+            atomicOr(&words[w], kAlBias);
+            const int at = atomicAdd(&list_n, 1);
+            if (at < kAlList) list_at[at] = i, list_token[at] = static_cast<int>(w);
         }
     }
     __syncthreads();
     const float rep = a.repetition ? a.repetition[row] : 1.f, freq = a.frequency ? a.frequency[row] : 0.f;
     const float pres = a.presence ? a.presence[row] : 0.f;
-    const int mrow = !a.allowed ? -1 : a.allowed_rows ? a.allowed_rows[row] : row;
-    const int mwords = (a.V + 31) / 32;
-    const uint32_t* mask = static_cast<unsigned>(mrow) < static_cast<unsigned>(a.n_masks)
-                               ? reinterpret_cast<const uint32_t*>(a.allowed) + (long long)mrow * mwords : nullptr;
-    const bool copy = a.logits != a.out;
-    for (int w0 = t * kN; w0 < slice; w0 += kAlThreads * kN) {
-        const long long i0 = base + w0;
-        if (i0 >= a.V) break;
-        // the group's allowed tokens and the touched ones, a bit each
-        const int lo = i0 < 0 ? static_cast<int>(-i0) : 0, hi = static_cast<int>(min((long long)kN, a.V - i0));
-        uint32_t open = (1u << kN) - 1;
-        if (mask) {
-            const int at = static_cast<int>(i0) + lo, wd = at / 32;
-            const uint32_t m0 = mask[wd], m1 = wd + 1 < mwords ? mask[wd + 1] : 0;
-            open = __funnelshift_r(m0, m1, at & 31) << lo;
-        }
-        uint32_t n[kN], touched = 0;
+#pragma unroll 1
+    for (int p = 0; p < kAlSlice / (kAlThreads * 16); ++p) {
+        if (base + p * 16 * kAlThreads >= a.V) break;
+        // of each group: the allowed tokens and the touched ones, a bit each, and its values
+        uint32_t open[kGroups], touched[kGroups];
+        __align__(16) E v[kGroups][kN];
 #pragma unroll
-        for (int e = 0; e < kN; e += 4) *reinterpret_cast<uint4*>(n + e) = *reinterpret_cast<const uint4*>(words + w0 + e);
+        for (int k = 0; k < kGroups; ++k) {
+            const int w0 = ((p * kGroups + k) * kAlThreads + t) * kN, g0 = base + w0;
+            const int lo = g0 < 0 ? -g0 : 0, hi = min(max(a.V - g0, 0), kN);
+            const uint32_t all = hi > lo ? ((1u << hi) - 1) & ~((1u << lo) - 1) : 0u;
+            open[k] = all, touched[k] = 0;
+            if (masked) {
+                const int at = g0 + lo - max(base, 0) / 32 * 32;
+                open[k] = all & (__funnelshift_r(masks[at / 32], masks[at / 32 + 1], at & 31) << lo);
+            }
+            if (counts) {
 #pragma unroll
-        for (int e = 0; e < kN; ++e) touched |= (n[e] != 0) << e;
-        const uint32_t all = ((1u << hi) - 1) & ~((1u << lo) - 1);
-        if (!copy && ((touched | ~open) & all) == 0) continue;
-        const bool whole = all == (1u << kN) - 1;
-        __align__(16) E v[kN];
-        if (copy || (open & all)) {
-            if (whole) *reinterpret_cast<uint4*>(v) = *reinterpret_cast<const uint4*>(x + i0);
-            else
-                for (int e = lo; e < hi; ++e) v[e] = x[i0 + e];
-        }
+                for (int e = 0; e < kN; e += 4) {
+                    const uint4 n = *reinterpret_cast<const uint4*>(words + w0 + e);
+                    touched[k] |= ((n.x != 0) | (n.y != 0) << 1 | (n.z != 0) << 2 | (n.w != 0) << 3) << e;
+                }
+                touched[k] &= open[k];
+            }
+            touched[k] |= (all & ~open[k]) << 16;  // and the banned ones
+            if (copy ? all != 0 : touched[k] != 0 && open[k] != 0) {
+                if (all == (1u << kN) - 1) *reinterpret_cast<uint4*>(v[k]) = *reinterpret_cast<const uint4*>(x + g0);
+                else
 #pragma unroll
-        for (int e = 0; e < kN; ++e) {
-            if (!(all >> e & 1)) continue;
-            if (!(open >> e & 1)) {
-                v[e] = A::put(-INFINITY);
-            } else if (n[e]) {
-                float z = A::get(v[e]);
-                const uint32_t c = n[e] & (kAlPrompt - 1);
-                if (n[e] & ~kAlBias) z = z > 0.f ? __fdiv_rn(z, rep) : __fmul_rn(z, rep);
-                if (c) z = __fsub_rn(z, __fadd_rn(__fmul_rn(freq, static_cast<float>(c)), pres));
-                if (n[e] & kAlBias)
-                    for (int b = b0; b < b1; ++b)
-                        if (a.bias_ids[b] == i0 + e) z = __fadd_rn(z, a.bias[b]);
-                v[e] = A::put(z);
+                    for (int e = 0; e < kN; ++e)
+                        if (all >> e & 1) v[k][e] = x[g0 + e];
             }
         }
-        if (whole && vec) *reinterpret_cast<uint4*>(y + i0) = *reinterpret_cast<const uint4*>(v);
-        else
 #pragma unroll
-            for (int e = 0; e < kN; ++e)
-                if (all >> e & 1) y[i0 + e] = v[e];
+        for (int k = 0; k < kGroups; ++k) {
+            const int w0 = ((p * kGroups + k) * kAlThreads + t) * kN, g0 = base + w0;
+            const uint32_t ban = touched[k] >> 16, all = open[k] | ban;
+            if (copy ? all == 0 : touched[k] == 0) continue;
+#pragma unroll
+            for (int e = 0; e < kN; ++e) {
+                if (ban >> e & 1) v[k][e] = A::put(-INFINITY);
+                if (!(touched[k] >> e & 1)) continue;
+                const uint32_t n = words[w0 + e], c = n & (kAlPrompt - 1);
+                float z = A::get(v[k][e]);
+                if (n & ~kAlBias) z = z > 0.f ? __fdiv_rn(z, rep) : __fmul_rn(z, rep);
+                if (c) z = __fsub_rn(z, __fadd_rn(__fmul_rn(freq, static_cast<float>(c)), pres));
+                if (n & kAlBias) {
+                    if (list_n <= kAlList) {  // in the order of their places
+                        for (int last = -1;;) {
+                            int next = INT_MAX;
+                            for (int i = 0; i < list_n; ++i)
+                                if (list_token[i] == w0 + e && list_at[i] > last) next = min(next, list_at[i]);
+                            if (next == INT_MAX) break;
+                            z = __fadd_rn(z, a.bias[next]);
+                            last = next;
+                        }
+                    } else {
+                        for (int b = b0; b < b1; ++b)
+                            if (a.bias_ids[b] == g0 + e) z = __fadd_rn(z, a.bias[b]);
+                    }
+                }
+                v[k][e] = A::put(z);
+            }
+            if (all == (1u << kN) - 1 && vec) *reinterpret_cast<uint4*>(y + g0) = *reinterpret_cast<const uint4*>(v[k]);
+            else
+#pragma unroll
+                for (int e = 0; e < kN; ++e)
+                    if (all >> e & 1) y[g0 + e] = v[k][e];
+        }
     }
 }
 
 template <int DT>
 cudaError_t al_launch(const AdjustArgs& a, cudaStream_t s) {
-    constexpr int kUnit = 4096;
-    const long long whole = (long long)a.V + AlVec<DT>::kN;  // with the skew of a row
-    int slice = kAlSlice;
-    while (slice > kUnit && a.M * ((whole + slice - 1) / slice) < kSms) slice /= 2;
-    int slices = static_cast<int>((whole + slice - 1) / slice);
-    const void* f = reinterpret_cast<const void*>(adjust_logits_kernel<DT>);
-    cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, kAlSlice * 4);
-    if (e != cudaSuccess) return e;
-    void* args[] = {const_cast<AdjustArgs*>(&a), &slice, &slices};
-    return launch_kernel(f, dim3(static_cast<unsigned>(a.M) * slices), dim3(kAlThreads), slice * 4, true, s, args);
+    int slices = static_cast<int>(((long long)a.V + AlVec<DT>::kN - 1 + kAlSlice - 1) / kAlSlice);  // with the skew of a row
+    void* args[] = {const_cast<AdjustArgs*>(&a), &slices};
+    return launch_kernel(reinterpret_cast<const void*>(adjust_logits_kernel<DT>), dim3(static_cast<unsigned>(a.M) * slices), dim3(kAlThreads), 0, true, s, args);
 }
 
 }  // namespace

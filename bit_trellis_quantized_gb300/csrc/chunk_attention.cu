@@ -96,12 +96,13 @@ __device__ __forceinline__ void cp_wait() {
 }
 
 // Sequences' runs of rows, where they are cut over all CTAs, for the join. With the key heads outermost, a unit is (key
-// head, run); the tiles of keys of all units are numbered in this order.
-constexpr int kCaRuns = kSms;
+// head, run); the places of all units are numbered in this order: a unit has one for each tile of keys, behind kCaStart
+// that stand for its beginning and end (queries, first and last products, outputs: about 6 us, with tiles of 1.5).
+constexpr int kCaRuns = kSms, kCaStart = 4;
 struct CaList {
-    int n, tiles;         // runs, tiles of all of them
+    int n, places;           // runs, places of all of them
     uint32_t unit[kCaRuns];  // sequence, run << 16
-    int first[kCaRuns + 1];  // tiles of the runs before it
+    int first[kCaRuns + 1];  // places of the runs before it
 };
 struct CaParts {
     float* acc;  // [2 CTAs][rows][D]: a CTA's part of a unit begun before its range, its part of one that goes on
@@ -188,6 +189,16 @@ __device__ __forceinline__ bool ca_next(CaBars& b, uint32_t k, int lane, CaUnit&
     return u.tiles > 0 && !ca_bad(b);
 }
 
+// The sum over the lanes up to this one.
+__device__ __forceinline__ int ca_sum(int x) {
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const int o = __shfl_up_sync(0xffffffffu, x, d);
+        if (static_cast<int>(threadIdx.x & 31) >= d) x += o;
+    }
+    return x;
+}
+
 // ---- the warp that hands out units
 // kRanges: this CTA's range of all units' tiles. Else units, the longest of a sequence first: that of blockIdx, then those
 // of CTAs that have not begun yet, taken over (cancelled) one at a time when the one in work comes to its end.
@@ -213,58 +224,48 @@ __device__ __forceinline__ void ca_units(const CaArgs& c, CaBars& b, CaList& lis
         }
     };
     if (kRanges) {
-        int n = 0, tiles = 0;
+        int n = 0, places = 0;
         for (int s0 = 0; s0 < a.n; s0 += 32) {
             const CaSeq mine(a, s0 + lane);
             const int runs = mine.runs<kRows>(group);
-            unsigned some = __ballot_sync(0xffffffffu, runs > 0);
-            const bool single = __all_sync(0xffffffffu, runs <= 1);
-            // sequences of one run all at once, others one after the other, a run a lane
-            do {
-                const int src = single ? 0 : __ffs(some) - 1;
-                const CaSeq q = single ? mine : mine.of(max(src, 0));
-                const int m = single ? 1 : q.runs<kRows>(group);
-                for (int r0 = 0; r0 < m && some; r0 += 32) {
-                    const int run = single ? 0 : r0 + lane;
-                    const bool on = single ? runs > 0 : run < m;
-                    const int w = on ? ca_tiles(q.keys<kRows>(run, group, c)) : 0;
-                    int incl = w;
+            const int upto = ca_sum(runs), all = __shfl_sync(0xffffffffu, upto, 31);
+            for (int r0 = 0; r0 < all; r0 += 32) {  // a run a lane
+                const int r = r0 + lane;
+                int src = 0;  // its sequence: the number of those that end before it
 #pragma unroll
-                    for (int d = 1; d < 32; d <<= 1) {
-                        const int o = __shfl_up_sync(0xffffffffu, incl, d);
-                        if (lane >= d) incl += o;
-                    }
-                    const unsigned ons = __ballot_sync(0xffffffffu, on);
-                    const int e = n + __popc(ons & ((1u << lane) - 1));
-                    if (on && e < kCaRuns) list.unit[e] = (s0 + (single ? lane : src)) | run << 16, list.first[e] = tiles + incl - w;
-                    n += __popc(ons);
-                    tiles += __shfl_sync(0xffffffffu, incl, 31);
-                }
-                some &= some - 1;
-            } while (!single && some);
+                for (int d = 16; d >= 1; d >>= 1)
+                    if (__shfl_sync(0xffffffffu, upto, src + d - 1) <= r) src += d;
+                const CaSeq q = mine.of(src & 31);
+                const int run = r - __shfl_sync(0xffffffffu, upto - runs, src & 31);
+                const int w = r < all ? ca_tiles(q.keys<kRows>(run, group, c)) + kCaStart : 0, incl = ca_sum(w);
+                if (r < all && n + lane < kCaRuns) list.unit[n + lane] = (s0 + src) | run << 16, list.first[n + lane] = places + incl - w;
+                n += min(all - r0, 32);
+                places += __shfl_sync(0xffffffffu, incl, 31);
+            }
         }
         n = min(n, kCaRuns);
-        if (lane == 0) list.n = n, list.tiles = tiles, list.first[n] = tiles;
+        if (lane == 0) list.n = n, list.places = places, list.first[n] = places;
         __syncwarp();
         if (blockIdx.x == 0)  // for the join
             for (int i = lane; i < static_cast<int>(sizeof(CaList) / 4); i += 32) reinterpret_cast<int*>(c.parts.list)[i] = reinterpret_cast<const int*>(&list)[i];
-        // CTA i begins at tile floor(i total / ctas)
-        const int total = tiles * a.Hkv, ctas = min(static_cast<int>(gridDim.x), total), i = blockIdx.x;
+        // CTA i begins at place floor(i total / ctas)
+        const int total = places * a.Hkv, ctas = min(static_cast<int>(gridDim.x), total), i = blockIdx.x;
         if (i < ctas) {
             const int each = total / ctas, rest = total % ctas;
             int at = i * each + i * rest / ctas;
             const int end = (i + 1) * each + (i + 1) * rest / ctas;
-            int kvh = at / tiles, off = at % tiles, e = 0, e1 = n;
+            int kvh = at / places, off = at % places, e = 0, e1 = n;
             while (e1 - e > 1) {
                 const int mid = (e + e1) / 2;
                 (list.first[mid] <= off ? e : e1) = mid;
             }
-            int tile0 = off - list.first[e];
+            off -= list.first[e];
             while (at < end) {
-                const int s = list.unit[e] & 0xFFFFu, run = list.unit[e] >> 16, now = min(list.first[e + 1] - list.first[e] - tile0, end - at);
+                const int s = list.unit[e] & 0xFFFFu, run = list.unit[e] >> 16, now = min(list.first[e + 1] - list.first[e] - off, end - at);
+                const int tile0 = max(off - kCaStart, 0), tiles = max(off + now - kCaStart, 0) - tile0;
                 const CaSeq q(a, s);
-                give(q, s, run, kvh, tile0, now, q.keys<kRows>(run, group, c));
-                at += now, tile0 = 0;
+                if (tiles > 0) give(q, s, run, kvh, tile0, tiles, q.keys<kRows>(run, group, c));
+                at += now, off = 0;
                 if (++e == n) e = 0, ++kvh;
             }
         }
@@ -278,12 +279,7 @@ __device__ __forceinline__ void ca_units(const CaArgs& c, CaBars& b, CaList& lis
         // the sequence: 32 at a time, on from the one before
         int w, incl;
         while (true) {
-            w = mine.runs<kRows>(group) * a.Hkv, incl = w;
-#pragma unroll
-            for (int d = 1; d < 32; d <<= 1) {
-                const int o = __shfl_up_sync(0xffffffffu, incl, d);
-                if (lane >= d) incl += o;
-            }
+            w = mine.runs<kRows>(group) * a.Hkv, incl = ca_sum(w);
             const int all = __shfl_sync(0xffffffffu, incl, 31);
             if (unit < before + all || s0 + 32 >= a.n) break;
             before += all, s0 += 32;
@@ -983,9 +979,9 @@ __global__ void __launch_bounds__(kCaJoinThreads) chunk_attention_join_kernel(co
     const CaList& list = *parts.list;
     if (static_cast<int>(blockIdx.y) >= list.n) return;
     const int kvh = blockIdx.z, s = list.unit[blockIdx.y] & 0xFFFFu, run = list.unit[blockIdx.y] >> 16;
-    const int total = list.tiles * a.Hkv, first = list.tiles * kvh + list.first[blockIdx.y], last = list.tiles * kvh + list.first[blockIdx.y + 1] - 1;
+    const int total = list.places * a.Hkv, first = list.places * kvh + list.first[blockIdx.y] + kCaStart, last = list.places * kvh + list.first[blockIdx.y + 1] - 1;
     const int ctas = min(grid, total), each = total / ctas, rest = total % ctas;
-    // CTA i begins at tile i each + floor(i rest / ctas): tile x is CTA x / each's, or one of the few before it
+    // CTA i begins at place i each + floor(i rest / ctas): place x is CTA x / each's, or one of the few before it
     auto owner = [&](int x) {
         int i = min(x / each, ctas - 1);
         while (i * each + i * rest / ctas > x) --i;
@@ -1085,7 +1081,7 @@ CaPlan ca_plan(int n, int T, int Hq, int Hkv, int d, int max_len) {
     // that a unit may have (the host does not know the lengths: an even share of the tokens, behind the longest cache);
     // cut over all CTAs they end together, which costs the parts and a second kernel. In tiles of 1.5 us:
     const long long tokens = T / n, tiles = (max_len - (tokens < max_len ? tokens : max_len) / 2) / kKeys + 1;
-    p.ranges = p.runs <= kCaRuns && (rounds * kSms - units) * tiles > 12 * kSms && units * (max_len / kKeys + 1) < 1ll << 30;
+    p.ranges = p.runs <= kCaRuns && (rounds * kSms - units) * tiles > 12 * kSms && units * (max_len / kKeys + 1 + kCaStart) < 1ll << 30;
     p.ctas = kSms;
     if (p.ranges) {
         p.ml = static_cast<size_t>(2) * p.ctas * rows * d * 4;

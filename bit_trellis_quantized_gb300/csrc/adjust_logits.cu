@@ -7,14 +7,14 @@
 //   each bias of i, in list order:   x = x + bias
 //   not allowed by the row's mask:   x = -infinity
 //
-// A CTA takes 8192 tokens of a row and holds a word for each of them in shared
+// A CTA takes 4096 tokens of a row and holds a word for each of them in shared
 // memory: how often the row's ids name it, and whether they do at all, as
-// whole-number sums, which come out alike in any order. Then one pass reads
-// what is to be changed (everything, where the result goes to another buffer),
-// all a thread's next loads at once, and writes it.
+// whole-number sums, which come out alike in any order. beside a list of those
+// that have one. One pass over the slice bans and copies, then each listed token
+// gets what is its own, a thread a token.
 //
 // Bound: the write of the banned and the changed logits, and the read of those
-// next to them. Slices of 32 KB let five CTAs share a multiprocessor, so that
+// next to them. Slices of 16 KB let six CTAs share a multiprocessor, so that
 // one's counting runs beside another's pass.
 #include "common.cuh"
 #include "context.h"
@@ -28,7 +28,7 @@ namespace escha {
 namespace {
 
 constexpr int kAlThreads = 256;
-constexpr int kAlSlice = 8192;  // tokens of a CTA at most
+constexpr int kAlSlice = 4096;  // tokens of a CTA at most
 constexpr int kAlList = 512;    // biases of a slice in shared memory
 constexpr uint32_t kAlPrompt = 1u << 30, kAlBias = 1u << 31;  // the rest counts
 
@@ -57,13 +57,14 @@ struct AlVec<2> {
 };
 
 template <int DT>
-__global__ void __launch_bounds__(kAlThreads, 5) adjust_logits_kernel(AdjustArgs a, int slices) {
+__global__ void __launch_bounds__(kAlThreads, 6) adjust_logits_kernel(AdjustArgs a, int slices) {
     using A = AlVec<DT>;
     using E = typename A::type;
-    constexpr int kN = A::kN, kGroups = 16 / kN;  // of a thread at once
+    constexpr int kN = A::kN, kEach = kAlSlice / (kAlThreads * kN), kGroups = kEach < 4 ? kEach : 4;  // groups of a thread, and at once
     __shared__ __align__(16) uint32_t words[kAlSlice];
     __shared__ uint32_t masks[kAlSlice / 32 + 2];
-    __shared__ int list_n, list_at[kAlList], list_token[kAlList];  // biases: their places and tokens of the slice
+    __shared__ uint16_t touched[kAlSlice];                                    // tokens with a word, in any order
+    __shared__ int touched_n, list_n, list_at[kAlList], list_token[kAlList];  // biases: their places and tokens of the slice
     pdl_wait();
     pdl_trigger();
     const int t = threadIdx.x, row = blockIdx.x / slices;
@@ -85,98 +86,127 @@ __global__ void __launch_bounds__(kAlThreads, 5) adjust_logits_kernel(AdjustArgs
     if (counts) {
 #pragma unroll
         for (int i = 0; i < kAlSlice / (kAlThreads * 4); ++i) *reinterpret_cast<uint4*>(words + (i * kAlThreads + t) * 4) = make_uint4(0, 0, 0, 0);
-        if (t == 0) list_n = 0;
-        __syncthreads();
+        if (t == 0) list_n = touched_n = 0;
+    }
+    __syncthreads();
+    if (counts) {
         const long long late = static_cast<long long>(i0) + (a.prompt ? max(a.prompt[row], 0) : 0);
 #pragma unroll 4
         for (int i = i0 + t; i < i1; i += kAlThreads) {
             const int id = a.ids[i];
             const uint32_t w = static_cast<uint32_t>(id) - static_cast<uint32_t>(base);
             if (static_cast<unsigned>(id) >= static_cast<unsigned>(a.V) || w >= kAlSlice) continue;
-            if (i >= late) atomicAdd(&words[w], 1u);
-            else atomicOr(&words[w], kAlPrompt);
+            if ((i >= late ? atomicAdd(&words[w], 1u) : atomicOr(&words[w], kAlPrompt)) == 0) touched[atomicAdd(&touched_n, 1)] = static_cast<uint16_t>(w);
         }
         for (int i = b0 + t; i < b1; i += kAlThreads) {
             const int id = a.bias_ids[i];
             const uint32_t w = static_cast<uint32_t>(id) - static_cast<uint32_t>(base);
             if (static_cast<unsigned>(id) >= static_cast<unsigned>(a.V) || w >= kAlSlice) continue;
-            atomicOr(&words[w], kAlBias);
+            if (atomicOr(&words[w], kAlBias) == 0) touched[atomicAdd(&touched_n, 1)] = static_cast<uint16_t>(w);
             const int at = atomicAdd(&list_n, 1);
             if (at < kAlList) list_at[at] = i, list_token[at] = static_cast<int>(w);
         }
     }
+    // the allowed ones of a group's tokens, a bit each, and those that there are
+    auto bits = [&](int g0) {
+        const int lo = g0 < 0 ? -g0 : 0, hi = min(max(a.V - g0, 0), kN);
+        return hi > lo ? ((1u << hi) - 1) & ~((1u << lo) - 1) : 0u;
+    };
+    auto allowed = [&](int g0) {
+        if (!masked) return ~0u;
+        const int lo = g0 < 0 ? -g0 : 0, at = g0 + lo - max(base, 0) / 32 * 32;
+        return __funnelshift_r(masks[at / 32], masks[at / 32 + 1], at & 31) << lo;
+    };
+    // ---- what is banned, and the copy; where all groups are whole and begin at a multiple of 32 tokens, a word of the mask
+    // serves 32 / kN threads as it is
+    if ((masked || copy) && skew == 0 && vec && base + kAlSlice <= a.V) {
+        const E* xt = x + base + t * kN;
+        E* yt = y + base + t * kN;
+        const uint32_t* mt = masks + t * kN / 32;
+        constexpr uint32_t kAll = (1u << kN) - 1;
+#pragma unroll 1
+        for (int p = 0; p < kEach; p += kGroups) {
+            __align__(16) E v[kGroups][kN];
+            uint32_t open[kGroups];
+#pragma unroll
+            for (int k = 0; k < kGroups; ++k) {
+                open[k] = masked ? mt[(p + k) * (kAlThreads * kN / 32)] >> (t * kN & 31) & kAll : kAll;
+                if (open[k] != 0 && (copy || open[k] != kAll)) *reinterpret_cast<uint4*>(v[k]) = *reinterpret_cast<const uint4*>(xt + (p + k) * (kAlThreads * kN));
+            }
+#pragma unroll
+            for (int k = 0; k < kGroups; ++k) {
+#pragma unroll
+                for (int e = 0; e < kN; ++e)
+                    if (!(open[k] >> e & 1)) v[k][e] = A::put(-INFINITY);
+                if (copy || open[k] != kAll) *reinterpret_cast<uint4*>(yt + (p + k) * (kAlThreads * kN)) = *reinterpret_cast<const uint4*>(v[k]);
+            }
+        }
+    } else if (masked || copy) {
+#pragma unroll 1
+        for (int p = 0; p < kEach; p += kGroups) {
+            __align__(16) E v[kGroups][kN];
+            uint32_t all[kGroups], open[kGroups];
+#pragma unroll
+            for (int k = 0; k < kGroups; ++k) {
+                const int g0 = base + ((p + k) * kAlThreads + t) * kN;
+                all[k] = bits(g0), open[k] = all[k] ? allowed(g0) & all[k] : 0u;
+                if (!copy && open[k] == all[k]) all[k] = 0;  // nothing to write
+                if (all[k] == (1u << kN) - 1 && open[k]) *reinterpret_cast<uint4*>(v[k]) = *reinterpret_cast<const uint4*>(x + g0);
+            }
+#pragma unroll
+            for (int k = 0; k < kGroups; ++k) {
+                const int g0 = base + ((p + k) * kAlThreads + t) * kN;
+                const bool whole = all[k] == (1u << kN) - 1;
+                if (whole) {
+#pragma unroll
+                    for (int e = 0; e < kN; ++e)
+                        if (!(open[k] >> e & 1)) v[k][e] = A::put(-INFINITY);
+                }
+                if (whole && vec) {
+                    *reinterpret_cast<uint4*>(y + g0) = *reinterpret_cast<const uint4*>(v[k]);
+                } else if (whole) {
+#pragma unroll
+                    for (int e = 0; e < kN; ++e) y[g0 + e] = v[k][e];
+                } else if (all[k]) {
+#pragma unroll 1
+                    for (int e = 0; e < kN; ++e)
+                        if (all[k] >> e & 1) y[g0 + e] = open[k] >> e & 1 ? x[g0 + e] : A::put(-INFINITY);
+                }
+            }
+        }
+    }
+    if (!counts) return;
     __syncthreads();
+    // ---- the touched ones
     const float rep = a.repetition ? a.repetition[row] : 1.f, freq = a.frequency ? a.frequency[row] : 0.f;
     const float pres = a.presence ? a.presence[row] : 0.f;
 #pragma unroll 1
-    for (int p = 0; p < kAlSlice / (kAlThreads * 16); ++p) {
-        if (base + p * 16 * kAlThreads >= a.V) break;
-        // of each group: the allowed tokens and the touched ones, a bit each, and its values
-        uint32_t open[kGroups], touched[kGroups];
-        __align__(16) E v[kGroups][kN];
-#pragma unroll
-        for (int k = 0; k < kGroups; ++k) {
-            const int w0 = ((p * kGroups + k) * kAlThreads + t) * kN, g0 = base + w0;
-            const int lo = g0 < 0 ? -g0 : 0, hi = min(max(a.V - g0, 0), kN);
-            const uint32_t all = hi > lo ? ((1u << hi) - 1) & ~((1u << lo) - 1) : 0u;
-            open[k] = all, touched[k] = 0;
-            if (masked) {
-                const int at = g0 + lo - max(base, 0) / 32 * 32;
-                open[k] = all & (__funnelshift_r(masks[at / 32], masks[at / 32 + 1], at & 31) << lo);
-            }
-            if (counts) {
-#pragma unroll
-                for (int e = 0; e < kN; e += 4) {
-                    const uint4 n = *reinterpret_cast<const uint4*>(words + w0 + e);
-                    touched[k] |= ((n.x != 0) | (n.y != 0) << 1 | (n.z != 0) << 2 | (n.w != 0) << 3) << e;
+    for (int i = t; i < touched_n; i += kAlThreads) {
+        const int w = touched[i];
+        if (masked) {
+            const int at = base + w - max(base, 0) / 32 * 32;
+            if (!(masks[at / 32] >> (at & 31) & 1)) continue;
+        }
+        const uint32_t n = words[w], c = n & (kAlPrompt - 1);
+        float z = A::get(x[base + w]);
+        if (n & ~kAlBias) z = z > 0.f ? __fdiv_rn(z, rep) : __fmul_rn(z, rep);
+        if (c) z = __fsub_rn(z, __fadd_rn(__fmul_rn(freq, static_cast<float>(c)), pres));
+        if (n & kAlBias) {
+            if (list_n <= kAlList) {  // in the order of their places
+                for (int last = -1;;) {
+                    int next = INT_MAX;
+                    for (int k = 0; k < list_n; ++k)
+                        if (list_token[k] == w && list_at[k] > last) next = min(next, list_at[k]);
+                    if (next == INT_MAX) break;
+                    z = __fadd_rn(z, a.bias[next]);
+                    last = next;
                 }
-                touched[k] &= open[k];
-            }
-            touched[k] |= (all & ~open[k]) << 16;  // and the banned ones
-            if (copy ? all != 0 : touched[k] != 0 && open[k] != 0) {
-                if (all == (1u << kN) - 1) *reinterpret_cast<uint4*>(v[k]) = *reinterpret_cast<const uint4*>(x + g0);
-                else
-#pragma unroll
-                    for (int e = 0; e < kN; ++e)
-                        if (all >> e & 1) v[k][e] = x[g0 + e];
+            } else {
+                for (int k = b0; k < b1; ++k)
+                    if (a.bias_ids[k] == base + w) z = __fadd_rn(z, a.bias[k]);
             }
         }
-#pragma unroll
-        for (int k = 0; k < kGroups; ++k) {
-            const int w0 = ((p * kGroups + k) * kAlThreads + t) * kN, g0 = base + w0;
-            const uint32_t ban = touched[k] >> 16, all = open[k] | ban;
-            if (copy ? all == 0 : touched[k] == 0) continue;
-#pragma unroll
-            for (int e = 0; e < kN; ++e) {
-                if (ban >> e & 1) v[k][e] = A::put(-INFINITY);
-                if (!(touched[k] >> e & 1)) continue;
-                const uint32_t n = words[w0 + e], c = n & (kAlPrompt - 1);
-                float z = A::get(v[k][e]);
-                if (n & ~kAlBias) z = z > 0.f ? __fdiv_rn(z, rep) : __fmul_rn(z, rep);
-                if (c) z = __fsub_rn(z, __fadd_rn(__fmul_rn(freq, static_cast<float>(c)), pres));
-                if (n & kAlBias) {
-                    if (list_n <= kAlList) {  // in the order of their places
-                        for (int last = -1;;) {
-                            int next = INT_MAX;
-                            for (int i = 0; i < list_n; ++i)
-                                if (list_token[i] == w0 + e && list_at[i] > last) next = min(next, list_at[i]);
-                            if (next == INT_MAX) break;
-                            z = __fadd_rn(z, a.bias[next]);
-                            last = next;
-                        }
-                    } else {
-                        for (int b = b0; b < b1; ++b)
-                            if (a.bias_ids[b] == g0 + e) z = __fadd_rn(z, a.bias[b]);
-                    }
-                }
-                v[k][e] = A::put(z);
-            }
-            if (all == (1u << kN) - 1 && vec) *reinterpret_cast<uint4*>(y + g0) = *reinterpret_cast<const uint4*>(v[k]);
-            else
-#pragma unroll
-                for (int e = 0; e < kN; ++e)
-                    if (all >> e & 1) y[g0 + e] = v[k][e];
-        }
+        y[base + w] = A::put(z);
     }
 }
 

@@ -33,6 +33,8 @@
 #include "tcgen05.cuh"
 #include "trellis_core.cuh"
 
+#include <type_traits>
+
 namespace escha {
 
 namespace {
@@ -963,23 +965,21 @@ __global__ void __launch_bounds__(CaCfg<D>::kThreads, 1) chunk_attention_kernel(
     if (warp == C::kMmaWarp) tc::tmem_dealloc(tmem, 512);
 }
 
-// Joins the parts of a unit that lies in several of the `grid` CTAs' ranges: CTA (rows_each rows, run, key head). kSets
-// sets of threads take interleaved parts.
-constexpr int kCaJoinThreads = 512;
+// Joins the parts of a unit that lies in several of the `grid` CTAs' ranges: CTA (rows, run, key head), a warp 128 values
+// (64) of a row, a part's factor a lane, 8 parts' values on their way at once and nothing shared between warps.
+constexpr int kCaJoinWarps = 8;
 template <int DT, int D>
-__global__ void __launch_bounds__(kCaJoinThreads) chunk_attention_join_kernel(const __grid_constant__ CaArgs c, int grid, int rows_each) {
+__global__ void __launch_bounds__(kCaJoinWarps * 32) chunk_attention_join_kernel(const __grid_constant__ CaArgs c, int grid) {
+    constexpr int kRows = CaCfg<D>::kRows, kVec = D == 64 ? 2 : 4, kSplit = D / (32 * kVec), kAtOnce = 8;
+    using Vec = std::conditional_t<kVec == 2, float2, float4>;
     const ChunkAttnArgs& a = c.a;
-    const CaParts& parts = c.parts;
-    constexpr int kRows = CaCfg<D>::kRows, kCols = D / 4, kSets = kCaJoinThreads / kCols, kAtOnce = 4, kFew = 4;
-    __shared__ float4 sums[kSets][kCols];
-    __shared__ __align__(8) float mls[kSms][2];
-    const int group = a.Hq / a.Hkv, t = threadIdx.x, col = t % kCols, set = t / kCols, d = col * 4;
+    const int group = a.Hq / a.Hkv, lane = threadIdx.x & 31;
     pdl_wait();
     pdl_trigger();
-    const CaList& list = *parts.list;
-    if (static_cast<int>(blockIdx.y) >= list.n) return;
-    const int kvh = blockIdx.z, s = list.unit[blockIdx.y] & 0xFFFFu, run = list.unit[blockIdx.y] >> 16;
-    const int total = list.places * a.Hkv, first = list.places * kvh + list.first[blockIdx.y] + kCaStart, last = list.places * kvh + list.first[blockIdx.y + 1] - 1;
+    const CaList& list = *c.parts.list;
+    const int e = blockIdx.y, kvh = blockIdx.z, s = list.unit[e] & 0xFFFFu, run = list.unit[e] >> 16;
+    const int total = list.places * a.Hkv, first = list.places * kvh + list.first[e] + kCaStart, last = list.places * kvh + list.first[e + 1] - 1;
+    if (e >= list.n) return;
     const int ctas = min(grid, total), each = total / ctas, rest = total % ctas;
     // CTA i begins at place i each + floor(i rest / ctas): place x is CTA x / each's, or one of the few before it
     auto owner = [&](int x) {
@@ -988,81 +988,52 @@ __global__ void __launch_bounds__(kCaJoinThreads) chunk_attention_join_kernel(co
         return i;
     };
     const int c0 = owner(first), n = owner(last) - c0 + 1;
-    const CaSeq seq(a, s);
     if (n == 1) return;  // finished
-    const int r0 = blockIdx.x * rows_each, r1 = min(r0 + rows_each, min(kRows, seq.tokens * group - run * kRows));
-    auto finish = [&](int r, const float4& v, float top, float sum) {
-        const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        const int R = run * kRows + r, tok = c.by_group(R);
-        const long long head = (long long)(seq.first + tok) * a.Hq + kvh * group + (R - tok * group);
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + head * D + d) =
-            make_uint2(ca_pack<DT>(v.x * inv, v.y * inv), ca_pack<DT>(v.z * inv, v.w * inv));
-        if (d == 0 && a.lse) a.lse[head] = sum == 0.f ? -INFINITY : (top - kUp<DT> + log2f(sum)) * kLn2;
-    };
-    if (n <= kFew) {  // few parts: a set of threads takes a row, all its parts at once
-        for (int r = r0 + set; r < r1; r += kSets) {
-            float4 o[kFew];
-            float2 ml[kFew];
-#pragma unroll
-            for (int i = 0; i < kFew; ++i) {
-                const long long at = (2ll * (c0 + i) + (i == 0 ? 1 : 0)) * kRows + r;
-                o[i] = i < n ? *reinterpret_cast<const float4*>(parts.acc + at * D + d) : make_float4(0.f, 0.f, 0.f, 0.f);
-                ml[i] = i < n ? *reinterpret_cast<const float2*>(parts.ml + at * 2) : make_float2(-INFINITY, 0.f);
-            }
-            float top = -INFINITY, sum = 0.f;
-#pragma unroll
-            for (int i = 0; i < kFew; ++i) top = fmaxf(top, ml[i].x);
-            const float base = top == -INFINITY ? 0.f : top;
-            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-            for (int i = 0; i < kFew; ++i) {
-                const float f = ex2(ml[i].x - base);
-                sum += ml[i].y * f, v.x += o[i].x * f, v.y += o[i].y * f, v.z += o[i].z * f, v.w += o[i].w * f;
-            }
-            finish(r, v, top, sum);
-        }
-        return;
-    }
-    for (int r = r0; r < r1; ++r) {
+    const CaSeq seq(a, s);
+    const int rows = min(kRows, seq.tokens * group - run * kRows);
+    for (int task = blockIdx.x * kCaJoinWarps + (threadIdx.x >> 5); task < rows * kSplit; task += gridDim.x * kCaJoinWarps) {
+        const int r = task / kSplit, d = (task % kSplit) * 128 + lane * kVec;
         // (a CTA's part of a unit that it begins is its second one)
         auto at = [&](int i) { return (2ll * (c0 + i) + (i == 0 ? 1 : 0)) * kRows + r; };
-        auto part = [&](int i) {
-            return i < n ? *reinterpret_cast<const float4*>(parts.acc + at(i) * D + d) : make_float4(0.f, 0.f, 0.f, 0.f);
+        auto part = [&](int i, float (&o)[kVec]) {
+            if (i < n) *reinterpret_cast<Vec*>(o) = *reinterpret_cast<const Vec*>(c.parts.acc + at(i) * D + d);
         };
-        float4 o[kAtOnce];  // (on their way before their factors are known)
+        __align__(16) float o[kAtOnce][kVec];
 #pragma unroll
-        for (int k = 0; k < kAtOnce; ++k) o[k] = part(set + k * kSets);
-        __syncthreads();
-        for (int i = t; i < n; i += kCaJoinThreads) *reinterpret_cast<float2*>(mls[i]) = *reinterpret_cast<const float2*>(parts.ml + at(i) * 2);
-        __syncthreads();
-        float top = -INFINITY, sum = 0.f;
-        for (int i = t & 31; i < n; i += 32) top = fmaxf(top, mls[i][0]);
+        for (int k = 0; k < kAtOnce; ++k) part(k, o[k]);  // (on their way before their factors are known)
+        float v[kVec] = {}, top = -INFINITY, sum = 0.f;
+        for (int i0 = 0; i0 < n; i0 += 32) {
+            const float2 ml = i0 + lane < n ? *reinterpret_cast<const float2*>(c.parts.ml + at(i0 + lane) * 2) : make_float2(-INFINITY, 0.f);
+            float m = ml.x;
 #pragma unroll
-        for (int m = 16; m >= 1; m >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, m));
-        const float base = top == -INFINITY ? 0.f : top;
-        for (int i = t & 31; i < n; i += 32) sum += mls[i][1] * ex2(mls[i][0] - base);
+            for (int x = 16; x >= 1; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
+            m = fmaxf(m, top);
+            const float base = m == -INFINITY ? 0.f : m, corr = ex2(top - base), f = ex2(ml.x - base);
+            float l = ml.y * f;
 #pragma unroll
-        for (int m = 16; m >= 1; m >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, m);
-        float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int i = set; i < n; i += kSets * kAtOnce) {
+            for (int x = 16; x >= 1; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
+            top = m, sum = sum * corr + l;
 #pragma unroll
-            for (int k = 0; k < kAtOnce; ++k) {
-                const float f = i + k * kSets < n ? ex2(mls[i + k * kSets][0] - base) : 0.f;
-                v.x += o[k].x * f, v.y += o[k].y * f, v.z += o[k].z * f, v.w += o[k].w * f;
+            for (int x = 0; x < kVec; ++x) v[x] *= corr;
+            for (int k0 = 0; k0 < 32 && i0 + k0 < n; k0 += kAtOnce) {
+#pragma unroll
+                for (int k = 0; k < kAtOnce; ++k) {
+                    const float w = __shfl_sync(0xffffffffu, f, k0 + k);
+                    if (i0 + k0 + k < n) {
+#pragma unroll
+                        for (int x = 0; x < kVec; ++x) v[x] += o[k][x] * w;
+                    }
+                    part(i0 + k0 + kAtOnce + k, o[k]);
+                }
             }
-#pragma unroll
-            for (int k = 0; k < kAtOnce; ++k) o[k] = part(i + (kAtOnce + k) * kSets);
         }
-        sums[set][col] = v;
-        __syncthreads();
-        if (set == 0) {
-#pragma unroll
-            for (int k = 1; k < kSets; ++k) {
-                const float4 o = sums[k][col];
-                v.x += o.x, v.y += o.y, v.z += o.z, v.w += o.w;
-            }
-            finish(r, v, top, sum);
-        }
+        const float inv = sum == 0.f ? 0.f : 1.f / sum;
+        const int R = run * kRows + r, tok = c.by_group(R);
+        const long long head = static_cast<long long>(seq.first + tok) * a.Hq + kvh * group + (R - tok * group);
+        uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + head * D + d);
+        if (kVec == 2) *out = ca_pack<DT>(v[0] * inv, v[1] * inv);
+        else *reinterpret_cast<uint2*>(out) = make_uint2(ca_pack<DT>(v[0] * inv, v[1] * inv), ca_pack<DT>(v[kVec - 2] * inv, v[kVec - 1] * inv));
+        if (d == 0 && a.lse) a.lse[head] = sum == 0.f ? -INFINITY : (top - kUp<DT> + log2f(sum)) * kLn2;
     }
 }
 
@@ -1146,12 +1117,13 @@ cudaError_t ca_launch(const ChunkAttnArgs& a, void* ws, cudaStream_t s) {
     void* args[] = {&c};
     e = launch_kernel(f, dim3(static_cast<unsigned>(p.ranges ? p.ctas : p.runs * a.Hkv)), dim3(C::kThreads), C::kSmem, true, s, args);
     if (e != cudaSuccess || !p.ranges) return e;
-    // (many units: of few parts each)
-    int grid = p.ctas, rows_each = 1;
-    while (rows_each < 32 && p.runs * a.Hkv * (C::kRows / rows_each) > 16 * kSms) rows_each *= 2;
-    void* jargs[] = {&c, &grid, &rows_each};
+    // (few of many units are cut, and the CTAs of others end at once)
+    int grid = p.ctas;
+    const long long units = p.runs * a.Hkv, most = C::kRows * (D == 256 ? 2 : 1) / kCaJoinWarps, fit = 16 * kSms / units;
+    void* jargs[] = {&c, &grid};
     return launch_kernel(reinterpret_cast<const void*>(chunk_attention_join_kernel<DT, D>),
-                         dim3(C::kRows / rows_each, static_cast<unsigned>(p.runs), a.Hkv), dim3(kCaJoinThreads), 0, true, s, jargs);
+                         dim3(static_cast<unsigned>(fit < 1 ? 1 : fit < most ? fit : most), static_cast<unsigned>(p.runs), a.Hkv),
+                         dim3(kCaJoinWarps * 32), 0, true, s, jargs);
 }
 
 }  // namespace

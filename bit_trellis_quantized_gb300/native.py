@@ -770,15 +770,16 @@ class Rotary:
         return f
 
 
-def _heads(name: str, t, T, d, index: int):
-    """Distance of rows of ``t``, [T][heads][d] on CUDA device ``index`` with contiguous heads."""
-    if t.dim() != 3 or t.shape[0] != T or t.shape[2] != d:
-        raise ValueError(f"{name} has shape {tuple(t.shape)}, not ({T}, heads, {d})")
+def _heads(name: str, t, T: int, d: int, index: int) -> int:
+    """Distance of the rows of ``t``, [T][heads][d] on CUDA device ``index`` with contiguous heads."""
+    shape = t.shape
+    if len(shape) != 3 or shape[0] != T or shape[2] != d:
+        raise ValueError(f"{name} has shape {tuple(shape)}, not ({T}, heads, {d})")
     if index < 0 or t.get_device() != index:
         raise ValueError(f"{name} must be a CUDA tensor, all on one device")
-    least = t.shape[1] * d
     ld, sh, sd = t.stride()
-    if sd != 1 or (t.shape[1] > 1 and sh != d) or (T > 1 and ld < least):
+    least = shape[1] * d
+    if sd != 1 or (sh != d and shape[1] > 1) or (ld < least and T > 1):
         raise ValueError(f"the heads of {name} must be contiguous and its rows apart")
     return ld if T > 1 else least
 

@@ -60,7 +60,7 @@ template <int DT>
 __global__ void __launch_bounds__(kAlThreads, 6) adjust_logits_kernel(AdjustArgs a, int slices) {
     using A = AlVec<DT>;
     using E = typename A::type;
-    constexpr int kN = A::kN, kEach = kAlSlice / (kAlThreads * kN), kGroups = kEach < 4 ? kEach : 4;  // groups of a thread, and at once
+    constexpr int kN = A::kN, kEach = kAlSlice / (kAlThreads * kN);  // groups of a thread
     __shared__ __align__(16) uint32_t words[kAlSlice];
     __shared__ uint32_t masks[kAlSlice / 32 + 2];
     __shared__ uint16_t touched[kAlSlice];                                    // tokens with a word, in any order
@@ -83,21 +83,40 @@ __global__ void __launch_bounds__(kAlThreads, 6) adjust_logits_kernel(AdjustArgs
         const uint32_t* m = reinterpret_cast<const uint32_t*>(a.allowed) + static_cast<long long>(mrow) * mwords;
         for (int i = t; i < kAlSlice / 32 + 2; i += kAlThreads) masks[i] = max(base, 0) / 32 + i < mwords ? m[max(base, 0) / 32 + i] : 0u;
     }
+    constexpr int kFirst = 4;  // of the row's ids: loads that go ahead, with the mask's
+    int first[kFirst];
     if (counts) {
+#pragma unroll
+        for (int k = 0; k < kFirst; ++k) first[k] = i0 + k * kAlThreads + t < i1 ? a.ids[i0 + k * kAlThreads + t] : -1;
 #pragma unroll
         for (int i = 0; i < kAlSlice / (kAlThreads * 4); ++i) *reinterpret_cast<uint4*>(words + (i * kAlThreads + t) * 4) = make_uint4(0, 0, 0, 0);
         if (t == 0) list_n = touched_n = 0;
     }
     __syncthreads();
+    // ---- what is banned, and the copy. Where all groups are whole and begin at a multiple of 32 tokens, a word of the mask
+    // serves 32 / kN threads as it is, and the values are on their way while the ids are counted.
+    constexpr uint32_t kAll = (1u << kN) - 1;
+    const bool plain = (masked || copy) && skew == 0 && vec && base + kAlSlice <= a.V;
+    __align__(16) E v[kEach][kN];
+    uint32_t open[kEach];
+    if (plain) {
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            open[k] = masked ? masks[(k * kAlThreads + t) * kN / 32] >> (t * kN & 31) & kAll : kAll;
+            if (open[k] != 0 && (copy || open[k] != kAll)) *reinterpret_cast<uint4*>(v[k]) = *reinterpret_cast<const uint4*>(x + base + (k * kAlThreads + t) * kN);
+        }
+    }
     if (counts) {
         const long long late = static_cast<long long>(i0) + (a.prompt ? max(a.prompt[row], 0) : 0);
-#pragma unroll 4
-        for (int i = i0 + t; i < i1; i += kAlThreads) {
-            const int id = a.ids[i];
+        auto count = [&](int i, int id) {
             const uint32_t w = static_cast<uint32_t>(id) - static_cast<uint32_t>(base);
-            if (static_cast<unsigned>(id) >= static_cast<unsigned>(a.V) || w >= kAlSlice) continue;
+            if (static_cast<unsigned>(id) >= static_cast<unsigned>(a.V) || w >= kAlSlice) return;
             if ((i >= late ? atomicAdd(&words[w], 1u) : atomicOr(&words[w], kAlPrompt)) == 0) touched[atomicAdd(&touched_n, 1)] = static_cast<uint16_t>(w);
-        }
+        };
+#pragma unroll
+        for (int k = 0; k < kFirst; ++k) count(i0 + k * kAlThreads + t, first[k]);
+#pragma unroll 4
+        for (int i = i0 + kFirst * kAlThreads + t; i < i1; i += kAlThreads) count(i, a.ids[i]);
         for (int i = b0 + t; i < b1; i += kAlThreads) {
             const int id = a.bias_ids[i];
             const uint32_t w = static_cast<uint32_t>(id) - static_cast<uint32_t>(base);
@@ -117,61 +136,41 @@ __global__ void __launch_bounds__(kAlThreads, 6) adjust_logits_kernel(AdjustArgs
         const int lo = g0 < 0 ? -g0 : 0, at = g0 + lo - max(base, 0) / 32 * 32;
         return __funnelshift_r(masks[at / 32], masks[at / 32 + 1], at & 31) << lo;
     };
-    // ---- what is banned, and the copy; where all groups are whole and begin at a multiple of 32 tokens, a word of the mask
-    // serves 32 / kN threads as it is
-    if ((masked || copy) && skew == 0 && vec && base + kAlSlice <= a.V) {
-        const E* xt = x + base + t * kN;
-        E* yt = y + base + t * kN;
-        const uint32_t* mt = masks + t * kN / 32;
-        constexpr uint32_t kAll = (1u << kN) - 1;
-#pragma unroll 1
-        for (int p = 0; p < kEach; p += kGroups) {
-            __align__(16) E v[kGroups][kN];
-            uint32_t open[kGroups];
+    if (plain) {
 #pragma unroll
-            for (int k = 0; k < kGroups; ++k) {
-                open[k] = masked ? mt[(p + k) * (kAlThreads * kN / 32)] >> (t * kN & 31) & kAll : kAll;
-                if (open[k] != 0 && (copy || open[k] != kAll)) *reinterpret_cast<uint4*>(v[k]) = *reinterpret_cast<const uint4*>(xt + (p + k) * (kAlThreads * kN));
-            }
+        for (int k = 0; k < kEach; ++k) {
 #pragma unroll
-            for (int k = 0; k < kGroups; ++k) {
+            for (int e = 0; e < kN; ++e)
+                if (!(open[k] >> e & 1)) v[k][e] = A::put(-INFINITY);
+            if (copy || open[k] != kAll) *reinterpret_cast<uint4*>(y + base + (k * kAlThreads + t) * kN) = *reinterpret_cast<const uint4*>(v[k]);
+        }
+    } else if (masked || copy) {
+        uint32_t all[kEach];
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            const int g0 = base + (k * kAlThreads + t) * kN;
+            all[k] = bits(g0), open[k] = all[k] ? allowed(g0) & all[k] : 0u;
+            if (!copy && open[k] == all[k]) all[k] = 0;  // nothing to write
+            if (all[k] == (1u << kN) - 1 && open[k]) *reinterpret_cast<uint4*>(v[k]) = *reinterpret_cast<const uint4*>(x + g0);
+        }
+#pragma unroll
+        for (int k = 0; k < kEach; ++k) {
+            const int g0 = base + (k * kAlThreads + t) * kN;
+            const bool whole = all[k] == (1u << kN) - 1;
+            if (whole) {
 #pragma unroll
                 for (int e = 0; e < kN; ++e)
                     if (!(open[k] >> e & 1)) v[k][e] = A::put(-INFINITY);
-                if (copy || open[k] != kAll) *reinterpret_cast<uint4*>(yt + (p + k) * (kAlThreads * kN)) = *reinterpret_cast<const uint4*>(v[k]);
             }
-        }
-    } else if (masked || copy) {
+            if (whole && vec) {
+                *reinterpret_cast<uint4*>(y + g0) = *reinterpret_cast<const uint4*>(v[k]);
+            } else if (whole) {
+#pragma unroll
+                for (int e = 0; e < kN; ++e) y[g0 + e] = v[k][e];
+            } else if (all[k]) {
 #pragma unroll 1
-        for (int p = 0; p < kEach; p += kGroups) {
-            __align__(16) E v[kGroups][kN];
-            uint32_t all[kGroups], open[kGroups];
-#pragma unroll
-            for (int k = 0; k < kGroups; ++k) {
-                const int g0 = base + ((p + k) * kAlThreads + t) * kN;
-                all[k] = bits(g0), open[k] = all[k] ? allowed(g0) & all[k] : 0u;
-                if (!copy && open[k] == all[k]) all[k] = 0;  // nothing to write
-                if (all[k] == (1u << kN) - 1 && open[k]) *reinterpret_cast<uint4*>(v[k]) = *reinterpret_cast<const uint4*>(x + g0);
-            }
-#pragma unroll
-            for (int k = 0; k < kGroups; ++k) {
-                const int g0 = base + ((p + k) * kAlThreads + t) * kN;
-                const bool whole = all[k] == (1u << kN) - 1;
-                if (whole) {
-#pragma unroll
-                    for (int e = 0; e < kN; ++e)
-                        if (!(open[k] >> e & 1)) v[k][e] = A::put(-INFINITY);
-                }
-                if (whole && vec) {
-                    *reinterpret_cast<uint4*>(y + g0) = *reinterpret_cast<const uint4*>(v[k]);
-                } else if (whole) {
-#pragma unroll
-                    for (int e = 0; e < kN; ++e) y[g0 + e] = v[k][e];
-                } else if (all[k]) {
-#pragma unroll 1
-                    for (int e = 0; e < kN; ++e)
-                        if (all[k] >> e & 1) y[g0 + e] = open[k] >> e & 1 ? x[g0 + e] : A::put(-INFINITY);
-                }
+                for (int e = 0; e < kN; ++e)
+                    if (all[k] >> e & 1) y[g0 + e] = open[k] >> e & 1 ? x[g0 + e] : A::put(-INFINITY);
             }
         }
     }

@@ -7,14 +7,14 @@
 //   each bias of i, in list order:   x = x + bias
 //   not allowed by the row's mask:   x = -infinity
 //
-// A CTA takes 4096 tokens of a row and holds a word for each of them in shared
+// A CTA takes 8192 tokens of a row and holds a word for each of them in shared
 // memory: how often the row's ids name it, and whether they do at all, as
 // whole-number sums, which come out alike in any order. beside a list of those
 // that have one. One pass over the slice bans and copies, then each listed token
 // gets what is its own, a thread a token.
 //
 // Bound: the write of the banned and the changed logits, and the read of those
-// next to them. Slices of 16 KB let six CTAs share a multiprocessor, so that
+// next to them. Slices of 32 KB let three CTAs share a multiprocessor, so that
 // one's counting runs beside another's pass.
 #include "common.cuh"
 #include "context.h"
@@ -27,8 +27,8 @@ namespace escha {
 
 namespace {
 
-constexpr int kAlThreads = 256;
-constexpr int kAlSlice = 4096;  // tokens of a CTA at most
+constexpr int kAlThreads = 512;
+constexpr int kAlSlice = 8192;  // tokens of a CTA at most
 constexpr int kAlList = 512;    // biases of a slice in shared memory
 constexpr uint32_t kAlPrompt = 1u << 30, kAlBias = 1u << 31;  // the rest counts
 
@@ -57,7 +57,7 @@ struct AlVec<2> {
 };
 
 template <int DT>
-__global__ void __launch_bounds__(kAlThreads, 6) adjust_logits_kernel(AdjustArgs a, int slices) {
+__global__ void __launch_bounds__(kAlThreads, 3) adjust_logits_kernel(AdjustArgs a, int slices) {
     using A = AlVec<DT>;
     using E = typename A::type;
     constexpr int kN = A::kN, kEach = kAlSlice / (kAlThreads * kN);  // groups of a thread

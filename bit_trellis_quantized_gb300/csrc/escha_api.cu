@@ -1494,7 +1494,7 @@ int escha_adjust_logits(const void* logits, void* out, int dtype, int M, int V, 
     int r = check_logprob_shape(M, V, name);
     if (r) return r;
     if (!logits || !out) return fail(ESCHA_E_ARG, "%s: logits or out is null", name);
-    if (M * (V / 4096 + 2ll) > 0x7fffffffll) return fail(ESCHA_E_SHAPE, "%s: M=%d rows of V=%d are too many", name, M, V);
+    if (M * (V / 8192 + 2ll) > 0x7fffffffll) return fail(ESCHA_E_SHAPE, "%s: M=%d rows of V=%d are too many", name, M, V);
     if (dtype != ESCHA_F16 && dtype != ESCHA_BF16 && dtype != ESCHA_F32)
         return fail(ESCHA_E_ARG, "%s: dtype=%d", name, dtype);
     if (ld < V || out_ld < V || ld > (1ll << 40) || out_ld > (1ll << 40))

@@ -5,10 +5,10 @@
 //   x_j = scale q . k_j,  m = max_j x_j,  out = sum_j e^(x_j - m) v_j / sum_j e^(x_j - m),
 //   lse = m + ln sum_j e^(x_j - m).
 //
-// A unit is one (sequence, key head, run of rows); its rows are the pairs of a
-// token and a query head of the key head, tokens outermost, so that tiles of
-// 128 rows are full whatever the group of heads is. A CTA takes a unit, or a
-// run of its keys, in tiles of 128 keys:
+// A unit is one (sequence, key head, run of tokens); its rows are the pairs of a
+// token and a query head of the key head, tokens outermost, in tiles of as many
+// whole tokens as 128 rows hold (all 128 where the group of heads divides it). A
+// CTA takes a unit, or a run of its keys, in tiles of 128 keys:
 //   S = Q K^T (tcgen05, Q and K in shared memory, S in tensor memory), the
 //   weights P = 2^(S c - m) by one thread a row, back to tensor memory over S
 //   as 16-bit values, O += P V (A from tensor memory, O stays there).
@@ -116,7 +116,7 @@ struct CaArgs {
     CUtensorMap queries;       // [T][Hq][d] in boxes of 128 rows of a unit and 64 values
     ChunkAttnArgs a;
     int box;  // rows of a page that are loaded at once: 8 to 128, or 0 (pages not of a multiple of 8): rows one by one
-    bool q_boxes;  // 128 rows are whole tokens
+    int span;  // tokens of a tile of rows
     int cap;  // keys that may be read
     CaDiv by_page, by_group;
     CaParts parts;
@@ -138,22 +138,16 @@ struct CaSeq {
         o.first = __shfl_sync(0xffffffffu, first, lane), o.tokens = __shfl_sync(0xffffffffu, tokens, lane), o.pos = __shfl_sync(0xffffffffu, pos, lane);
         return o;
     }
-    template <int kRows>
-    __device__ __forceinline__ int runs(int group) const {
-        return (tokens * group + kRows - 1) / kRows;
-    }
-    // keys that the rows [run kRows, (run + 1) kRows) see
-    template <int kRows>
-    __device__ __forceinline__ int keys(int run, int group, const CaArgs& c) const {
-        const int last = c.by_group(min((run + 1) * kRows, tokens * group) - 1);
-        return max(0, min(pos + last + 1, c.cap));
-    }
+    // runs of `most` tokens
+    __device__ __forceinline__ int runs(int most) const { return (tokens + most - 1) / most; }
+    // keys that the run's tokens see
+    __device__ __forceinline__ int keys(int run, int most, int cap) const { return max(0, min(pos + min((run + 1) * most, tokens), cap)); }
 };
 __device__ __forceinline__ int ca_tiles(int keys) { return max(1, (keys + kKeys - 1) / kKeys); }
 
 // What a CTA works on next, handed to all its warps.
 struct CaUnit {
-    int s, kvh, row0, rows;  // rows of the sequence's pairs of token and head
+    int s, kvh, tok0, toks;  // its tokens, of the sequence's
     int first, pos;          // the sequence's first token in q, its position
     int tile0, tiles, keys;  // tiles 0: no more units
     int whole;
@@ -204,16 +198,15 @@ __device__ __forceinline__ int ca_sum(int x) {
 // ---- the warp that hands out units
 // kRanges: this CTA's range of all units' tiles. Else units, the longest of a sequence first: that of blockIdx, then those
 // of CTAs that have not begun yet, taken over (cancelled) one at a time when the one in work comes to its end.
-template <int kRows, bool kRanges>
+template <int kNQ, bool kRanges>
 __device__ __forceinline__ void ca_units(const CaArgs& c, CaBars& b, CaList& list, uint4* response) {
     const ChunkAttnArgs& a = c.a;
-    const int lane = threadIdx.x & 31, group = a.Hq / a.Hkv;
+    const int lane = threadIdx.x & 31, most = kNQ * c.span;
     uint32_t k = 0;
     auto give = [&](const CaSeq& q, int s, int run, int kvh, int tile0, int tiles, int keys) {
         ca_wait(b, &b.unit_empty[k & 1], ((k >> 1) - 1) & 1);
         if (lane == 0) {
-            const int row0 = run * kRows;
-            b.unit[k & 1] = CaUnit{s, kvh, row0, min(kRows, q.tokens * group - row0), q.first, q.pos, tile0, tiles, keys, tiles == ca_tiles(keys)};
+            b.unit[k & 1] = CaUnit{s, kvh, run * most, min(most, q.tokens - run * most), q.first, q.pos, tile0, tiles, keys, tiles == ca_tiles(keys)};
             ca_arrive(&b.unit_full[k & 1]);
         }
         ++k;
@@ -229,7 +222,7 @@ __device__ __forceinline__ void ca_units(const CaArgs& c, CaBars& b, CaList& lis
         int n = 0, places = 0;
         for (int s0 = 0; s0 < a.n; s0 += 32) {
             const CaSeq mine(a, s0 + lane);
-            const int runs = mine.runs<kRows>(group);
+            const int runs = mine.runs(most);
             const int upto = ca_sum(runs), all = __shfl_sync(0xffffffffu, upto, 31);
             for (int r0 = 0; r0 < all; r0 += 32) {  // a run a lane
                 const int r = r0 + lane;
@@ -239,7 +232,7 @@ __device__ __forceinline__ void ca_units(const CaArgs& c, CaBars& b, CaList& lis
                     if (__shfl_sync(0xffffffffu, upto, src + d - 1) <= r) src += d;
                 const CaSeq q = mine.of(src & 31);
                 const int run = r - __shfl_sync(0xffffffffu, upto - runs, src & 31);
-                const int w = r < all ? ca_tiles(q.keys<kRows>(run, group, c)) + kCaStart : 0, incl = ca_sum(w);
+                const int w = r < all ? ca_tiles(q.keys(run, most, c.cap)) + kCaStart : 0, incl = ca_sum(w);
                 if (r < all && n + lane < kCaRuns) list.unit[n + lane] = (s0 + src) | run << 16, list.first[n + lane] = places + incl - w;
                 n += min(all - r0, 32);
                 places += __shfl_sync(0xffffffffu, incl, 31);
@@ -266,7 +259,7 @@ __device__ __forceinline__ void ca_units(const CaArgs& c, CaBars& b, CaList& lis
                 const int s = list.unit[e] & 0xFFFFu, run = list.unit[e] >> 16, now = min(list.first[e + 1] - list.first[e] - off, end - at);
                 const int tile0 = max(off - kCaStart, 0), tiles = max(off + now - kCaStart, 0) - tile0;
                 const CaSeq q(a, s);
-                if (tiles > 0) give(q, s, run, kvh, tile0, tiles, q.keys<kRows>(run, group, c));
+                if (tiles > 0) give(q, s, run, kvh, tile0, tiles, q.keys(run, most, c.cap));
                 at += now, off = 0;
                 if (++e == n) e = 0, ++kvh;
             }
@@ -281,7 +274,7 @@ __device__ __forceinline__ void ca_units(const CaArgs& c, CaBars& b, CaList& lis
         // the sequence: 32 at a time, on from the one before
         int w, incl;
         while (true) {
-            w = mine.runs<kRows>(group) * a.Hkv, incl = ca_sum(w);
+            w = mine.runs(most) * a.Hkv, incl = ca_sum(w);
             const int all = __shfl_sync(0xffffffffu, incl, 31);
             if (unit < before + all || s0 + 32 >= a.n) break;
             before += all, s0 += 32;
@@ -291,7 +284,7 @@ __device__ __forceinline__ void ca_units(const CaArgs& c, CaBars& b, CaList& lis
         if (!has) break;  // past the last unit
         const int src = __ffs(has) - 1, off = unit - before - __shfl_sync(0xffffffffu, incl - w, src);
         const CaSeq q = mine.of(src);
-        const int run = q.runs<kRows>(group) - 1 - off / a.Hkv, keys = q.keys<kRows>(run, group, c);
+        const int run = q.runs(most) - 1 - off / a.Hkv, keys = q.keys(run, most, c.cap);
         give(q, s0 + src, run, off % a.Hkv, 0, ca_tiles(keys), keys);
         ca_wait(b, &b.want, steals & 1);
         if (ca_bad(b)) break;
@@ -328,51 +321,25 @@ __device__ __forceinline__ uint32_t ca_at(int r, int p) {
     return ((r >> 3) * kChunks + (p >> 3)) * 1024 + (r & 7) * 128 + (((p & 7) ^ (r & 7)) << 4);
 }
 
-// A unit's queries: boxes by the first warp, or rows by both, 16 bytes a lane. (Rows of a box behind the sequence's last
-// token see no key.)
+// A unit's queries. (Rows of a box behind the sequence's last token, and those behind a tile's last token, see no key.)
 template <int D>
 __device__ __forceinline__ void ca_queries(const CaArgs& c, CaBars& b, const CaUnit& u, uint32_t q_smem) {
-    constexpr int kPieces = D / 8, kStep = 32 * CaCfg<D>::kLoadWarps / kPieces;
-    const int t = threadIdx.x - 32 * CaCfg<D>::kSoftWarps, group = c.a.Hq / c.a.Hkv, p = t % kPieces;
-    const int tiles = u.rows > 128 ? 2 : 1;
-    if (c.q_boxes) {
-        if (t == 0) {
-            tc::mbar_arrive_expect_tx(tc::smem_addr(&b.q_full), tiles * 128 * D * 2);
+    if (threadIdx.x % 32 == 0) {
+        const int group = c.a.Hq / c.a.Hkv, boxes = (u.toks > c.span ? 2 : 1) * (D / 64);
+        tc::mbar_arrive_expect_tx(tc::smem_addr(&b.q_full), boxes * c.span * group * 128);
 #pragma unroll 1
-            for (int i = 0; i < tiles * (D / 64); ++i) {
-                const int q = i / (D / 64), x = i % (D / 64);
-                asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(q_smem + i * 16384),
-                             "l"(&c.queries), "r"(x * 64), "r"(u.kvh * group), "r"(u.first + c.by_group(u.row0 + 128 * q)), "r"(tc::smem_addr(&b.q_full))
-                             : "memory");
-            }
-        }
-        __syncwarp();
-        return;
+        for (int i = 0; i < boxes; ++i)
+            asm volatile("cp.async.bulk.tensor.3d.shared::cluster.global.tile.mbarrier::complete_tx::bytes [%0], [%1, {%2, %3, %4}], [%5];" ::"r"(q_smem + i * 16384),
+                         "l"(&c.queries), "r"(i % (D / 64) * 64), "r"(u.kvh * group), "r"(u.first + u.tok0 + i / (D / 64) * c.span), "r"(tc::smem_addr(&b.q_full))
+                         : "memory");
     }
-    const char* q0 = static_cast<const char*>(c.a.q) + ((static_cast<long long>(u.first) * c.a.Hq + u.kvh * group) * D + p * 8) * 2;
-    int r = t / kPieces, tok = c.by_group(u.row0 + r), g = u.row0 + r - tok * group;
-#pragma unroll 4
-    for (; r < 128 * tiles; r += kStep) {
-        const bool on = r < u.rows;
-        const long long from = on ? (static_cast<long long>(tok) * c.a.Hq + g) * (D * 2) : 0;
-        cp16(q_smem + (r >> 7) * (128 * D * 2) + (p >> 3) * 16384 + tc::kmajor_off(r & 127, (p & 7) * 8), q0 + from, on);
-        g += kStep;
-        while (g >= group) g -= group, ++tok;
-    }
-    cp_commit();
-}
-__device__ __forceinline__ void ca_queries_landed(const CaArgs& c, CaBars& b) {
-    if (c.q_boxes) return;
-    cp_wait<0>();
-    tc::fence_proxy_async_smem();
     __syncwarp();
-    if ((threadIdx.x & 31) == 0) ca_arrive(&b.q_full);
 }
 
 // Keys that every row of the unit sees.
-__device__ __forceinline__ int ca_common(const CaArgs& c, const CaUnit& u) { return max(0, u.pos + c.by_group(u.row0) + 1); }
+__device__ __forceinline__ int ca_common(const CaUnit& u) { return max(0, u.pos + u.tok0 + 1); }
 // The first tile that not every row sees in full, from the unit's first one.
-__device__ __forceinline__ int ca_partly(const CaArgs& c, const CaUnit& u) { return max(ca_common(c, u) / kKeys - u.tile0, 0); }
+__device__ __forceinline__ int ca_partly(const CaUnit& u) { return max(ca_common(u) / kKeys - u.tile0, 0); }
 
 // The values of such a tile: a weight of 0 would still carry what is not finite into rows that do not see it (keys of
 // later tokens, what lies behind the last one). So it is taken out here, and added at the end where it is seen. A warp's
@@ -432,11 +399,9 @@ __device__ __forceinline__ void ca_load_boxes(const CaArgs& c, CaBars& b, uint32
     CaUnit u;
     for (; ca_next(b, k, lane, u); ++k) {
         ca_wait(b, &b.q_empty, (k - 1) & 1);
-        const int partly = ca_partly(c, u), common = ca_common(c, u);
+        const int partly = ca_partly(u), common = ca_common(u);
         uint32_t* odd = &b.odd[k & 1][0][0];
         if (w == 1) {
-            ca_queries<D>(c, b, u, q_smem);
-            ca_queries_landed(c, b);
 #pragma unroll 1
             for (int j = partly; j < u.tiles; ++j)
 #pragma unroll 1
@@ -500,7 +465,6 @@ __device__ __forceinline__ void ca_load_boxes(const CaArgs& c, CaBars& b, uint32
                                  : "memory");
                 ++slot;
             }
-            if (j == 0) ca_queries_landed(c, b);
             if (!kRanges && lane == 0 && j == max(u.tiles - 3, 0)) ca_arrive(&b.want);
             last = row, row = next, next = later;
         }
@@ -543,8 +507,7 @@ __device__ __forceinline__ void ca_load_rows(const CaArgs& c, CaBars& b, uint32_
         if (w == 0 && lane < 16) b.odd[k & 1][lane >> 2][lane & 3] = 0;
         if (w == 0 && lane == 16) b.any_odd[k & 1] = 0;
         asm volatile("bar.sync 1, %0;" ::"n"(32 * C::kLoadWarps) : "memory");
-        ca_queries<D>(c, b, u, q_smem);
-        ca_queries_landed(c, b);
+        if (w == 0) ca_queries<D>(c, b, u, q_smem);
         const int32_t* table = a.table + static_cast<long long>(u.s) * a.max_pages;
         // lane r's rows 64 w + r and 64 w + 32 + r of tile j: their numbers in the pools (-1: not there)
         auto find = [&](int j, int (&row)[2]) {
@@ -558,7 +521,7 @@ __device__ __forceinline__ void ca_load_rows(const CaArgs& c, CaBars& b, uint32_
                 }
             }
         };
-        const int partly = ca_partly(c, u);
+        const int partly = ca_partly(u);
         // (in the order of the boxes)
         int row[2], last[2] = {-1, -1};
         find(0, row);
@@ -620,7 +583,7 @@ __device__ __forceinline__ void ca_mma_ts(uint32_t d, uint32_t a_tmem, uint32_t 
         : "memory");
 }
 template <int DT, int D>
-__device__ __forceinline__ void ca_products(CaBars& b, uint32_t q_smem, uint32_t ring) {
+__device__ __forceinline__ void ca_products(CaBars& b, int span, uint32_t q_smem, uint32_t ring) {
     using C = CaCfg<D>;
     constexpr int kNQ = C::kNQ, kParts = C::kParts, kSlots = C::kSlots;
     constexpr uint32_t is = tc::idesc_f16(128, 128, false, false, DT == 2), io = tc::idesc_f16(128, C::kSlotD, false, true, DT == 2);
@@ -691,7 +654,7 @@ __device__ __forceinline__ void ca_products(CaBars& b, uint32_t q_smem, uint32_t
     };
     while (true) {
         wait(&b.unit_full[k & 1], (k >> 1) & 1);
-        const int tiles = __shfl_sync(0xffffffffu, b.unit[k & 1].tiles, 0), nq = kNQ == 2 && __shfl_sync(0xffffffffu, b.unit[k & 1].rows, 0) > 128 ? 2 : 1;
+        const int tiles = __shfl_sync(0xffffffffu, b.unit[k & 1].tiles, 0), nq = kNQ == 2 && __shfl_sync(0xffffffffu, b.unit[k & 1].toks, 0) > span ? 2 : 1;
         if (lead) ca_arrive(&b.unit_empty[k & 1]);
         if (tiles <= 0 || __any_sync(0xffffffffu, ca_bad(b))) break;
         wait(&b.q_full, k & 1);
@@ -735,7 +698,7 @@ __device__ __forceinline__ void ca_products(CaBars& b, uint32_t q_smem, uint32_t
 // What was taken out of the values of a unit's last tiles, added to 32 values of a row that sees it.
 template <int DT, int D>
 __device__ __noinline__ void ca_add_odd(const CaArgs& c, const CaBars& b, const CaUnit& u, uint32_t k, int pos, int col, float* v) {
-    const int first = u.tile0 + ca_partly(c, u);
+    const int first = u.tile0 + ca_partly(u);
     for (int i = 0; i < 16; ++i)
         for (uint32_t m = b.odd[k & 1][i >> 2][i & 3]; m; m &= m - 1) {
             const int key = (first + (i >> 2)) * kKeys + 32 * (i & 3) + __ffs(m) - 1;
@@ -774,10 +737,12 @@ __device__ __forceinline__ void ca_soft(const CaArgs& c, CaBars& b, uint32_t tme
     // (a scale of 0 is next to 0: masked scores stay -infinity so)
     const float sc = a.scale == 0.f ? 1e-30f : fabsf(a.scale) * kLog2e;
     uint32_t tile = 0, soft = 0, units = 0;  // tiles of keys; those, and units, that have this tile of rows
+    const int mine = c.by_group(r & 127), g_head = (r & 127) - mine * group, tok = q * c.span + mine;  // token of the unit, head of the group
     CaUnit u;
     for (uint32_t k = 0; ca_next(b, k, lane, u); ++k, tile += u.tiles) {
-        if (128 * q >= u.rows) continue;
-        const int R = u.row0 + r, tok = c.by_group(R), pos = r < u.rows ? u.pos + tok : -1;
+        if (q * c.span >= u.toks) continue;
+        const bool on = mine < c.span && tok < u.toks;
+        const int pos = on ? u.pos + u.tok0 + tok : -1;
         float m = -INFINITY, l = 0.f;
 #pragma unroll 1
         for (int j = 0; j < u.tiles; ++j) {
@@ -866,7 +831,7 @@ __device__ __forceinline__ void ca_soft(const CaArgs& c, CaBars& b, uint32_t tme
         tc::fence_after_sync();
         if (ca_bad(b)) l = NAN;
         const bool odd = *reinterpret_cast<volatile uint32_t*>(&b.any_odd[k & 1]) != 0;
-        const long long head = static_cast<long long>(u.first + tok) * a.Hq + u.kvh * group + (R - tok * group);
+        const long long head = static_cast<long long>(u.first + u.tok0 + tok) * a.Hq + u.kvh * group + g_head;
         const long long slot = 2ll * blockIdx.x + (u.tile0 == 0 ? 1 : 0);
         const float inv = l == 0.f ? 0.f : 1.f / l;
 #pragma unroll 1
@@ -882,7 +847,7 @@ __device__ __forceinline__ void ca_soft(const CaArgs& c, CaBars& b, uint32_t tme
 #pragma unroll
                 for (int e = 0; e < 32; ++e) v[e] = w[e];
             }
-            if (r < u.rows) {
+            if (on) {
                 if (u.whole) {
                     uint16_t* out = static_cast<uint16_t*>(a.out) + head * D + x;
 #pragma unroll
@@ -907,7 +872,7 @@ __device__ __forceinline__ void ca_soft(const CaArgs& c, CaBars& b, uint32_t tme
         tc::fence_before_sync();
         __syncwarp();
         if (lane == 0) ca_arrive(&b.o_empty[q]);
-        if (r < u.rows) {
+        if (on) {
             if (!u.whole) *reinterpret_cast<float2*>(c.parts.ml + (slot * C::kRows + r) * 2) = make_float2(m, l);
             else if (a.lse) a.lse[head] = l == 0.f ? -INFINITY : (m - kUp<DT> + log2f(l)) * kLn2;
         }
@@ -932,7 +897,7 @@ __global__ void __launch_bounds__(CaCfg<D>::kThreads, 1) chunk_attention_kernel(
             init(&b.s_full[i], 1), init(&b.p_full[i], 4), init(&b.pv_done[i], 1), init(&b.o_full[i], 1), init(&b.o_empty[i], 4);
             init(&b.unit_full[i], 1), init(&b.unit_empty[i], C::kSoftWarps + C::kLoadWarps + 1);
         }
-        init(&b.q_full, c.q_boxes ? 1 : C::kLoadWarps), init(&b.q_empty, 1), init(&b.want, 1), init(&b.stolen, 1), init(&b.end, 1);
+        init(&b.q_full, 1), init(&b.q_empty, 1), init(&b.want, 1), init(&b.stolen, 1), init(&b.end, 1);
         b.bad = 0;
         tc::fence_proxy_async_smem();
     }
@@ -955,8 +920,8 @@ __global__ void __launch_bounds__(CaCfg<D>::kThreads, 1) chunk_attention_kernel(
         if (C::kNQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
         if (warp < C::kMmaWarp && c.box) ca_load_boxes<DT, D, kRanges>(c, b, q_smem, ring);
         else if (warp < C::kMmaWarp) ca_load_rows<DT, D, kRanges>(c, b, q_smem, ring);
-        else if (warp == C::kUnitWarp) ca_units<C::kRows, kRanges>(c, b, list, &response);
-        else ca_products<DT, D>(b, q_smem, ring);
+        else if (warp == C::kUnitWarp) ca_units<C::kNQ, kRanges>(c, b, list, &response);
+        else ca_products<DT, D>(b, c.span, q_smem, ring);
         __syncwarp();
     }
     tc::fence_before_sync();
@@ -990,9 +955,10 @@ __global__ void __launch_bounds__(kCaJoinWarps * 32) chunk_attention_join_kernel
     const int c0 = owner(first), n = owner(last) - c0 + 1;
     if (n == 1) return;  // finished
     const CaSeq seq(a, s);
-    const int rows = min(kRows, seq.tokens * group - run * kRows);
+    const int tok0 = run * CaCfg<D>::kNQ * c.span, rows = min(CaCfg<D>::kNQ * c.span, seq.tokens - tok0) * group;
     for (int task = blockIdx.x * kCaJoinWarps + (threadIdx.x >> 5); task < rows * kSplit; task += gridDim.x * kCaJoinWarps) {
-        const int r = task / kSplit, d = (task % kSplit) * 128 + lane * kVec;
+        const int pair = task / kSplit, tok = c.by_group(pair), d = (task % kSplit) * 128 + lane * kVec;
+        const int r = tok < c.span ? pair : 128 + pair - c.span * group;  // of the unit
         // (a CTA's part of a unit that it begins is its second one)
         auto at = [&](int i) { return (2ll * (c0 + i) + (i == 0 ? 1 : 0)) * kRows + r; };
         auto part = [&](int i, float (&o)[kVec]) {
@@ -1028,8 +994,7 @@ __global__ void __launch_bounds__(kCaJoinWarps * 32) chunk_attention_join_kernel
             }
         }
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
-        const int R = run * kRows + r, tok = c.by_group(R);
-        const long long head = static_cast<long long>(seq.first + tok) * a.Hq + kvh * group + (R - tok * group);
+        const long long head = static_cast<long long>(seq.first + tok0 + tok) * a.Hq + kvh * group + (pair - tok * group);
         uint32_t* out = reinterpret_cast<uint32_t*>(static_cast<uint16_t*>(a.out) + head * D + d);
         if (kVec == 2) *out = ca_pack<DT>(v[0] * inv, v[1] * inv);
         else *reinterpret_cast<uint2*>(out) = make_uint2(ca_pack<DT>(v[0] * inv, v[1] * inv), ca_pack<DT>(v[kVec - 2] * inv, v[kVec - 1] * inv));
@@ -1045,8 +1010,8 @@ struct CaPlan {
 };
 CaPlan ca_plan(int n, int T, int Hq, int Hkv, int d, int max_len) {
     CaPlan p{};
-    const int rows = d == 256 ? 128 : 256, group = Hq / Hkv;
-    p.runs = (long long)T * group / rows + (n < T ? n : T);
+    const int rows = d == 256 ? 128 : 256, group = Hq / Hkv, most = rows / 128 * (128 / group);
+    p.runs = T / most + (n < T ? n : T);
     const long long units = p.runs * Hkv, rounds = (units + kSms - 1) / kSms;
     // Whole units leave CTAs idle in the last round of them, for the time of (rounds 152 - units) / 152 units of the tiles
     // that a unit may have (the host does not know the lengths: an even share of the tokens, behind the longest cache);
@@ -1102,14 +1067,14 @@ cudaError_t ca_launch(const ChunkAttnArgs& a, void* ws, cudaStream_t s) {
     const CaPlan p = ca_plan(a.n, a.T, a.Hq, a.Hkv, D, a.max_len);
     const long long cap = (long long)a.max_pages * a.page;
     char* w = static_cast<char*>(ws);
-    CaArgs c{{}, {}, {}, a, 0, false, static_cast<int>(cap < a.max_len ? cap : a.max_len), ca_div(a.page), ca_div(a.Hq / a.Hkv),
+    CaArgs c{{}, {}, {}, a, 0, 128 / (a.Hq / a.Hkv), static_cast<int>(cap < a.max_len ? cap : a.max_len), ca_div(a.page), ca_div(a.Hq / a.Hkv),
              CaParts{reinterpret_cast<float*>(w), reinterpret_cast<float*>(w + p.ml), reinterpret_cast<CaList*>(w + p.list)}};
     if (a.page % 8 == 0) {
         c.box = 8;
         while (c.box < kKeys && a.page % (2 * c.box) == 0) c.box *= 2;
         if (!ca_map_pool(&c.keys, a.k_pool, DT, D, c.box, a) || !ca_map_pool(&c.values, a.v_pool, DT, D, c.box, a)) c.box = 0;
     }
-    c.q_boxes = 128 % (a.Hq / a.Hkv) == 0 && ca_map_queries(&c.queries, DT, D, a);
+    if (!ca_map_queries(&c.queries, DT, D, a)) return cudaErrorNotSupported;
     const void* f = p.ranges ? reinterpret_cast<const void*>(chunk_attention_kernel<DT, D, true>)
                              : reinterpret_cast<const void*>(chunk_attention_kernel<DT, D, false>);
     cudaError_t e = cudaFuncSetAttribute(f, cudaFuncAttributeMaxDynamicSharedMemorySize, C::kSmem);

@@ -117,6 +117,7 @@ struct CaArgs {
     ChunkAttnArgs a;
     int box;  // rows of a page that are loaded at once: 8 to 128, or 0 (pages not of a multiple of 8): rows one by one
     int span;  // tokens of a tile of rows
+    int runs;  // of all sequences, at most (bounds that descend may give more: those are left out)
     int cap;  // keys that may be read
     CaDiv by_page, by_group;
     CaParts parts;
@@ -161,24 +162,26 @@ struct CaBars {
     uint32_t odd[2][4][4], any_odd[2];  // of a unit's last tiles, keys whose values are not all finite
 };
 
-// A wait that gives up after 2^19 polls (a second or two), or once another has: the CTA then runs on to its end and the
-// rows in work become NaN.
+// A wait that gives up after so many polls of 4 us at most, or once another has: the CTA then runs on to its end and the
+// rows in work become NaN. Waits are for a tile's work (2^19 polls, two seconds), or for a unit's (2^26): one of 2^30 keys
+// takes ten seconds.
 __device__ __forceinline__ bool ca_bad(CaBars& b) { return *reinterpret_cast<volatile int*>(&b.bad) != 0; }
-__device__ __forceinline__ void ca_wait_long(CaBars& b, uint32_t at, uint32_t parity) {
+__device__ __forceinline__ void ca_wait_long(CaBars& b, uint32_t at, uint32_t parity, int polls) {
 #pragma unroll 1
-    for (int it = 0; it < 1 << 19; ++it)
+    for (int it = 0; it < polls; ++it)
         if (tc::mbar_test_parity(at, parity) || ca_bad(b)) return;
     *reinterpret_cast<volatile int*>(&b.bad) = 1;
 }
-__device__ __forceinline__ void ca_wait(CaBars& b, unsigned long long* bar, uint32_t parity) {
+__device__ __forceinline__ void ca_wait(CaBars& b, unsigned long long* bar, uint32_t parity, int polls = 1 << 19) {
     const uint32_t at = tc::smem_addr(bar);
-    if (!tc::mbar_test_parity(at, parity)) ca_wait_long(b, at, parity);
+    if (!tc::mbar_test_parity(at, parity)) ca_wait_long(b, at, parity, polls);
 }
+constexpr int kUnitPolls = 1 << 26;
 __device__ __forceinline__ void ca_arrive(unsigned long long* bar) { tc::mbar_arrive_cta(tc::smem_addr(bar)); }
 
 // The next unit (the k-th), false: none. Every warp that works on units calls it once a unit.
 __device__ __forceinline__ bool ca_next(CaBars& b, uint32_t k, int lane, CaUnit& u) {
-    ca_wait(b, &b.unit_full[k & 1], (k >> 1) & 1);
+    ca_wait(b, &b.unit_full[k & 1], (k >> 1) & 1, kUnitPolls);
     u = b.unit[k & 1];
     __syncwarp();
     if (lane == 0) ca_arrive(&b.unit_empty[k & 1]);
@@ -204,7 +207,7 @@ __device__ __forceinline__ void ca_units(const CaArgs& c, CaBars& b, CaList& lis
     const int lane = threadIdx.x & 31, most = kNQ * c.span;
     uint32_t k = 0;
     auto give = [&](const CaSeq& q, int s, int run, int kvh, int tile0, int tiles, int keys) {
-        ca_wait(b, &b.unit_empty[k & 1], ((k >> 1) - 1) & 1);
+        ca_wait(b, &b.unit_empty[k & 1], ((k >> 1) - 1) & 1, kUnitPolls);
         if (lane == 0) {
             b.unit[k & 1] = CaUnit{s, kvh, run * most, min(most, q.tokens - run * most), q.first, q.pos, tile0, tiles, keys, tiles == ca_tiles(keys)};
             ca_arrive(&b.unit_full[k & 1]);
@@ -212,7 +215,7 @@ __device__ __forceinline__ void ca_units(const CaArgs& c, CaBars& b, CaList& lis
         ++k;
     };
     auto stop = [&]() {
-        ca_wait(b, &b.unit_empty[k & 1], ((k >> 1) - 1) & 1);
+        ca_wait(b, &b.unit_empty[k & 1], ((k >> 1) - 1) & 1, kUnitPolls);
         if (lane == 0) {
             b.unit[k & 1].tiles = 0;
             ca_arrive(&b.unit_full[k & 1]);
@@ -224,7 +227,7 @@ __device__ __forceinline__ void ca_units(const CaArgs& c, CaBars& b, CaList& lis
             const CaSeq mine(a, s0 + lane);
             const int runs = mine.runs(most);
             const int upto = ca_sum(runs), all = __shfl_sync(0xffffffffu, upto, 31);
-            for (int r0 = 0; r0 < all; r0 += 32) {  // a run a lane
+            for (int r0 = 0; r0 < all && n < kCaRuns; r0 += 32) {  // a run a lane
                 const int r = r0 + lane;
                 int src = 0;  // its sequence: the number of those that end before it
 #pragma unroll
@@ -232,13 +235,13 @@ __device__ __forceinline__ void ca_units(const CaArgs& c, CaBars& b, CaList& lis
                     if (__shfl_sync(0xffffffffu, upto, src + d - 1) <= r) src += d;
                 const CaSeq q = mine.of(src & 31);
                 const int run = r - __shfl_sync(0xffffffffu, upto - runs, src & 31);
-                const int w = r < all ? ca_tiles(q.keys(run, most, c.cap)) + kCaStart : 0, incl = ca_sum(w);
-                if (r < all && n + lane < kCaRuns) list.unit[n + lane] = (s0 + src) | run << 16, list.first[n + lane] = places + incl - w;
-                n += min(all - r0, 32);
+                const int w = r < all && n + lane < min(c.runs, kCaRuns) ? ca_tiles(q.keys(run, most, c.cap)) + kCaStart : 0, incl = ca_sum(w);
+                if (w) list.unit[n + lane] = (s0 + src) | run << 16, list.first[n + lane] = places + incl - w;
+                n = min(n + min(all - r0, 32), kCaRuns);
                 places += __shfl_sync(0xffffffffu, incl, 31);
             }
         }
-        n = min(n, kCaRuns);
+        n = min(n, min(c.runs, kCaRuns));
         if (lane == 0) list.n = n, list.places = places, list.first[n] = places;
         __syncwarp();
         if (blockIdx.x == 0)  // for the join
@@ -282,11 +285,11 @@ __device__ __forceinline__ void ca_units(const CaArgs& c, CaBars& b, CaList& lis
         }
         const unsigned has = __ballot_sync(0xffffffffu, unit < before + incl);
         if (!has) break;  // past the last unit
-        const int src = __ffs(has) - 1, off = unit - before - __shfl_sync(0xffffffffu, incl - w, src);
+        const int src = __ffs(has) - 1, off = max(unit - before - __shfl_sync(0xffffffffu, incl - w, src), 0);
         const CaSeq q = mine.of(src);
-        const int run = q.runs(most) - 1 - off / a.Hkv, keys = q.keys(run, most, c.cap);
+        const int run = max(q.runs(most) - 1 - off / a.Hkv, 0), keys = q.keys(run, most, c.cap);
         give(q, s0 + src, run, off % a.Hkv, 0, ca_tiles(keys), keys);
-        ca_wait(b, &b.want, steals & 1);
+        ca_wait(b, &b.want, steals & 1, kUnitPolls);
         if (ca_bad(b)) break;
         if (lane == 0) {
             tc::fence_proxy_async_smem();
@@ -337,7 +340,7 @@ __device__ __forceinline__ void ca_queries(const CaArgs& c, CaBars& b, const CaU
 }
 
 // Keys that every row of the unit sees.
-__device__ __forceinline__ int ca_common(const CaUnit& u) { return max(0, u.pos + u.tok0 + 1); }
+__device__ __forceinline__ int ca_common(const CaUnit& u) { return max(0, min(u.pos + u.tok0 + 1, u.keys)); }
 // The first tile that not every row sees in full, from the unit's first one.
 __device__ __forceinline__ int ca_partly(const CaUnit& u) { return max(ca_common(u) / kKeys - u.tile0, 0); }
 
@@ -398,7 +401,7 @@ __device__ __forceinline__ void ca_load_boxes(const CaArgs& c, CaBars& b, uint32
     uint32_t slot = 0, tile = 0, k = 0, phases = 0;
     CaUnit u;
     for (; ca_next(b, k, lane, u); ++k) {
-        ca_wait(b, &b.q_empty, (k - 1) & 1);
+        ca_wait(b, &b.q_empty, (k - 1) & 1, kUnitPolls);
         const int partly = ca_partly(u), common = ca_common(u);
         uint32_t* odd = &b.odd[k & 1][0][0];
         if (w == 1) {
@@ -408,7 +411,7 @@ __device__ __forceinline__ void ca_load_boxes(const CaArgs& c, CaBars& b, uint32
                 for (int p = 0; p < C::kParts; ++p) {
                     // (order of the slots: below)
                     const uint32_t i = slot + p + C::kParts * (C::kNQ == 1 ? min(2 * j + 2, 2 * u.tiles - 1) : 2 * j + 1), at = i % kSlots;
-                    ca_wait(b, &b.raw[at], phases >> at & 1);
+                    ca_wait(b, &b.raw[at], phases >> at & 1, kUnitPolls);
                     phases ^= 1u << at;
                     // the rows that not all see and that were loaded: the rest of a box behind the last key, no further
                     const int key0 = (u.tile0 + j) * kKeys, r0 = max(common - key0, 0) & ~7, r1 = min((u.keys - key0 + c.box - 1) & -c.box, kKeys);
@@ -503,7 +506,7 @@ __device__ __forceinline__ void ca_load_rows(const CaArgs& c, CaBars& b, uint32_
     };
     CaUnit u;
     for (; ca_next(b, k, lane, u); ++k) {
-        ca_wait(b, &b.q_empty, (k - 1) & 1);  // (nothing is in flight)
+        ca_wait(b, &b.q_empty, (k - 1) & 1, kUnitPolls);  // (nothing is in flight)
         if (w == 0 && lane < 16) b.odd[k & 1][lane >> 2][lane & 3] = 0;
         if (w == 0 && lane == 16) b.any_odd[k & 1] = 0;
         asm volatile("bar.sync 1, %0;" ::"n"(32 * C::kLoadWarps) : "memory");
@@ -603,8 +606,8 @@ __device__ __forceinline__ void ca_products(CaBars& b, int span, uint32_t q_smem
         if (lead) tc::commit(tc::smem_addr(bar));
         __syncwarp();
     };
-    auto wait = [&](unsigned long long* bar, uint32_t parity) {
-        ca_wait(b, bar, parity);
+    auto wait = [&](unsigned long long* bar, uint32_t parity, int polls = 1 << 19) {
+        ca_wait(b, bar, parity, polls);
         __syncwarp();
         tc::fence_after_sync();
     };
@@ -653,7 +656,7 @@ __device__ __forceinline__ void ca_products(CaBars& b, int span, uint32_t q_smem
         for (int p = 0; p < kParts; ++p) next = after(next, round);
     };
     while (true) {
-        wait(&b.unit_full[k & 1], (k >> 1) & 1);
+        wait(&b.unit_full[k & 1], (k >> 1) & 1, kUnitPolls);
         const int tiles = __shfl_sync(0xffffffffu, b.unit[k & 1].tiles, 0), nq = kNQ == 2 && __shfl_sync(0xffffffffu, b.unit[k & 1].toks, 0) > span ? 2 : 1;
         if (lead) ca_arrive(&b.unit_empty[k & 1]);
         if (tiles <= 0 || __any_sync(0xffffffffu, ca_bad(b))) break;
@@ -1067,7 +1070,7 @@ cudaError_t ca_launch(const ChunkAttnArgs& a, void* ws, cudaStream_t s) {
     const CaPlan p = ca_plan(a.n, a.T, a.Hq, a.Hkv, D, a.max_len);
     const long long cap = (long long)a.max_pages * a.page;
     char* w = static_cast<char*>(ws);
-    CaArgs c{{}, {}, {}, a, 0, 128 / (a.Hq / a.Hkv), static_cast<int>(cap < a.max_len ? cap : a.max_len), ca_div(a.page), ca_div(a.Hq / a.Hkv),
+    CaArgs c{{}, {}, {}, a, 0, 128 / (a.Hq / a.Hkv), static_cast<int>(p.runs), static_cast<int>(cap < a.max_len ? cap : a.max_len), ca_div(a.page), ca_div(a.Hq / a.Hkv),
              CaParts{reinterpret_cast<float*>(w), reinterpret_cast<float*>(w + p.ml), reinterpret_cast<CaList*>(w + p.list)}};
     if (a.page % 8 == 0) {
         c.box = 8;

@@ -262,6 +262,124 @@ def test_streams_and_a_captured_step():
     check(c, out, lse, 128 ** -0.5, "f16")
 
 
+def test_nothing_behind_the_bound_counts():
+    """max_len inside a page: what lies behind it, in pages that are there, holds NaN and infinities."""
+    native = _native()
+    for dtype, d, page in (("f16", 64, 16), ("bf16", 128, 64), ("f16", 256, 128), ("bf16", 256, 17)):
+        for cap in (33, 100, 129, 200):
+            c = make(40, [20, 90, 1], [190, 130, 209], 4, 2, d, page, dtype)
+            for b in range(3):
+                for j in range(cap, 260):
+                    if j // page < c["table"].shape[1] and int(c["table"][b, j // page]) >= 0:
+                        c["k"][int(c["table"][b, j // page]), :, j % page] = float("nan")
+                        c["v"][int(c["table"][b, j // page]), :, j % page] = float("inf")
+            out, lse = native.chunk_attention(*args(c), max_len=cap)
+            check(c, out, lse, d ** -0.5, dtype, cap=cap)
+
+
+@pytest.mark.parametrize("scale", [-0.2, 0.0, 1e-3, 3.0])
+@pytest.mark.parametrize("dtype,d,Hq", [("f16", 64, 7), ("bf16", 128, 9), ("f16", 256, 13)])
+def test_scales_of_any_sign_and_odd_groups(dtype, d, Hq, scale):
+    native = _native()
+    c = make(41, [70, 3], [200, 0], Hq, 1, d, 16, dtype)
+    out, lse = native.chunk_attention(*args(c), scale=scale)
+    check(c, out, lse, scale, dtype)
+
+
+def test_sequences_that_share_pages():
+    """A prefix of one sequence in the tables of others, and one page in every place of a table."""
+    native = _native()
+    c = make(42, [5, 40, 12], [150, 160, 180], 8, 2, 128, 16, "bf16", poison=False)
+    c["table"][1, :9] = c["table"][0, :9]
+    c["table"][2, :] = c["table"][0, 0]
+    out, lse = native.chunk_attention(*args(c))
+    check(c, out, lse, 128 ** -0.5, "bf16")
+
+
+@pytest.mark.parametrize("dtype,new,old,Hq,Hkv,d,page", [
+    ("f16", [2500], [500], 16, 4, 256, 64), ("bf16", [1800, 3, 700], [100, 5000, 0], 12, 4, 128, 16),
+    ("f16", [3100, 40], [0, 2000], 8, 8, 64, 32), ("bf16", [300], [20000], 16, 2, 256, 64)])
+def test_many_units(dtype, new, old, Hq, Hkv, d, page):
+    """More units than CTAs, handed on and cut, against products in 64 bits on the GPU (bound as in check)."""
+    native = _native()
+    c = make(43, new, old, Hq, Hkv, d, page, dtype, poison=False)
+    out, lse = native.chunk_attention(*args(c))
+    again, lse2 = native.chunk_attention(*args(c))
+    first, h, group = 0, HALF[dtype], Hq // Hkv
+    for b, (n, o) in enumerate(zip(new, old)):
+        pages = c["table"][b, :-(-(n + o) // page)].long()
+        for i in range(Hkv):
+            k, v = (c[x][pages, i].reshape(-1, d)[:n + o].double() for x in "kv")
+            for a in range(0, n, 512):
+                e = min(n, a + 512)
+                q = c["q"][first + a:first + e, i * group:(i + 1) * group].double()
+                x = torch.einsum("thd,kd->thk", q, k) * d ** -0.5
+                seen = torch.ones(e - a, n + o, dtype=torch.bool, device="cuda").tril(o + a)[:, None]
+                x = torch.where(seen, x, -torch.inf)
+                p = torch.softmax(x, 2)
+                want, mass = torch.einsum("thk,kd->thd", p, v), torch.einsum("thk,kd->thd", p, v.abs())
+                reach = torch.where(seen, torch.einsum("thd,kd->thk", q.abs(), k.abs()), 0).amax(2) * d ** -0.5
+                x_err = (d + 4) * 2.0 ** -24 * reach
+                tol = h * want.abs() + (h * (1 + h) + 2 * x_err[..., None] + 2.0 ** -15) * mass
+                if dtype == "f16":
+                    tol = tol + 2.0 ** -25 + 2.0 ** -36 * (n + o) * float(v.abs().max())
+                rows = slice(first + a, first + e), slice(i * group, (i + 1) * group)
+                assert bool(((out[rows].double() - want).abs() <= tol).all())
+                want = torch.logsumexp(x, 2)
+                assert bool(((lse[rows].double() - want).abs() <= x_err + 2.0 ** -20 + 2.0 ** -22 * want.abs()).all())
+        first += n
+    assert torch.equal(lse, lse2) and torch.equal(out, again)
+
+
+def test_outputs_at_any_16_bytes():
+    native = _native()
+    c = make(44, [33], [50], 6, 2, 64, 16, "f16")
+    want, want_lse = native.chunk_attention(*args(c))
+    for off in (8, 16, 24):
+        buf = torch.full((33 * 6 * 64 + 64,), 7.0, dtype=torch.float16, device="cuda")
+        out = buf[off:off + 33 * 6 * 64].view(33, 6, 64)
+        native.chunk_attention(*args(c), out=out)
+        assert torch.equal(out, want) and bool((buf[:off] == 7).all()) and bool((buf[off + 33 * 6 * 64:] == 7).all())
+
+
+@pytest.mark.parametrize("d", [64, 128, 256])
+def test_bounds_that_descend_stay_in_the_buffers(d):
+    """Not allowed, and without meaning: but the call ends, what lies around the buffers stays, and the next call is right."""
+    native = _native()
+    c = make(45, [30, 30, 30, 30], [300, 0, 5000, 9], 4, 2, d, 16, "bf16", poison=False)
+    want, want_lse = native.chunk_attention(*args(c))
+    for at in ([0, 120, 0, 120, 5], [120, 90, 60, 30, 0], [-5, 1 << 30, -1 << 30, 7, 1 << 30], [0, 0, 0, 0, 0]):
+        buf = torch.full((120 * 4 * d + 2048,), 7.0, dtype=torch.bfloat16, device="cuda")
+        out = buf[1024:1024 + 120 * 4 * d].view(120, 4, d)
+        bad = dict(c, at=torch.tensor(at, dtype=torch.int32, device="cuda"))
+        native.chunk_attention(*args(bad), out=out)
+        torch.cuda.synchronize()
+        assert bool((buf[:1024] == 7).all()) and bool((buf[-1024:] == 7).all())
+    out, lse = native.chunk_attention(*args(c))
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+def test_two_captured_graphs_with_their_own_workspaces():
+    native = _native()
+    cs = [make(46 + i, [4, 1], [5000, 300], 16, 2, 256, 64, "f16", poison=False) for i in range(2)]
+    want = [native.chunk_attention(*args(c)) for c in cs]
+    torch.cuda.synchronize()
+    graphs, outs = [], []
+    for c in cs:
+        g = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(g):
+            outs.append(native.chunk_attention(*args(c)))
+        graphs.append(g)
+    side = [torch.cuda.Stream() for _ in graphs]
+    for _ in range(5):
+        for g, s in zip(graphs, side):
+            with torch.cuda.stream(s):
+                g.replay()
+    torch.cuda.synchronize()
+    for o, w in zip(outs, want):
+        assert torch.equal(o[0], w[0]) and torch.equal(o[1], w[1])
+
+
 def test_refusals():
     native = _native()
     c = make(39, [10], [30], 4, 2, 64, 16, "f16")
@@ -283,3 +401,6 @@ def test_refusals():
     bad(native.EschaError, q=c["q"][:, :3].contiguous())
     bad(native.EschaError, max_len=0)
     bad(ValueError, ws=torch.empty(16, device="cuda"))
+    one = make(39, [4], [20000], 16, 2, 64, 16, "f16", poison=False)  # few tokens over many keys: parts in a workspace
+    with pytest.raises(native.EschaError, match="workspace"):
+        native.chunk_attention(*args(one), ws=torch.empty(256, dtype=torch.uint8, device="cuda"))

@@ -933,68 +933,99 @@ __global__ void __launch_bounds__(CaCfg<D>::kThreads, 1) chunk_attention_kernel(
     if (warp == C::kMmaWarp) tc::tmem_dealloc(tmem, 512);
 }
 
-// Joins the parts of a unit that lies in several of the `grid` CTAs' ranges: CTA (rows, run, key head), a warp 128 values
-// (64) of a row, a part's factor a lane, 8 parts' values on their way at once and nothing shared between warps.
-constexpr int kCaJoinWarps = 8;
+// Joins the parts of the units that lie in several of the `grid` CTAs' ranges. CTA (rows, unit, key head); where the units
+// are more than the borders between ranges (by_border), CTA (rows, border), for the unit whose first border that is. Of few
+// parts, a warp takes 128 values (64) of a row, eight parts' at once; of many, a CTA does, an eighth of the parts a warp.
+constexpr int kCaJoinWarps = 8, kCaAtOnce = 8, kCaFew = 16;
 template <int DT, int D>
-__global__ void __launch_bounds__(kCaJoinWarps * 32) chunk_attention_join_kernel(const __grid_constant__ CaArgs c, int grid) {
-    constexpr int kRows = CaCfg<D>::kRows, kVec = D == 64 ? 2 : 4, kSplit = D / (32 * kVec), kAtOnce = 8;
+__global__ void __launch_bounds__(kCaJoinWarps * 32, 4) chunk_attention_join_kernel(const __grid_constant__ CaArgs c, int grid, int by_border) {
+    constexpr int kRows = CaCfg<D>::kRows, kVec = D == 64 ? 2 : 4, kSplit = D / (32 * kVec), kWide = 32 * kVec;
     using Vec = std::conditional_t<kVec == 2, float2, float4>;
+    __shared__ __align__(16) float sums[kCaJoinWarps][kWide];
+    __shared__ float2 mls[kCaJoinWarps][kSms];  // of a row's parts: maximum, then factor; sum
     const ChunkAttnArgs& a = c.a;
-    const int group = a.Hq / a.Hkv, lane = threadIdx.x & 31;
+    const int group = a.Hq / a.Hkv, lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     pdl_wait();
     pdl_trigger();
     const CaList& list = *c.parts.list;
-    const int e = blockIdx.y, kvh = blockIdx.z, s = list.unit[e] & 0xFFFFu, run = list.unit[e] >> 16;
-    const int total = list.places * a.Hkv, first = list.places * kvh + list.first[e] + kCaStart, last = list.places * kvh + list.first[e + 1] - 1;
-    if (e >= list.n) return;
-    const int ctas = min(grid, total), each = total / ctas, rest = total % ctas;
+    const int places = list.places, total = places * a.Hkv, ctas = min(grid, total);
+    if (total == 0) return;
+    const int each = total / ctas, rest = total % ctas;
     // CTA i begins at place i each + floor(i rest / ctas): place x is CTA x / each's, or one of the few before it
+    auto begin = [&](int i) { return i * each + i * rest / ctas; };
     auto owner = [&](int x) {
         int i = min(x / each, ctas - 1);
-        while (i * each + i * rest / ctas > x) --i;
+        while (begin(i) > x) --i;
         return i;
     };
+    int e = blockIdx.y, kvh = blockIdx.z;
+    if (by_border) {
+        if (e + 1 >= ctas) return;
+        const int at = begin(e + 1), off = at % places;
+        kvh = at / places, e = 0;
+        for (int e1 = list.n; e1 - e > 1;) {
+            const int mid = (e + e1) / 2;
+            (list.first[mid] <= off ? e : e1) = mid;
+        }
+    } else if (e >= list.n) {
+        return;
+    }
+    const int first = places * kvh + list.first[e] + kCaStart, last = places * kvh + list.first[e + 1] - 1;
     const int c0 = owner(first), n = owner(last) - c0 + 1;
-    if (n == 1) return;  // finished
-    const CaSeq seq(a, s);
-    const int tok0 = run * CaCfg<D>::kNQ * c.span, rows = min(CaCfg<D>::kNQ * c.span, seq.tokens - tok0) * group;
-    for (int task = blockIdx.x * kCaJoinWarps + (threadIdx.x >> 5); task < rows * kSplit; task += gridDim.x * kCaJoinWarps) {
-        const int pair = task / kSplit, tok = c.by_group(pair), d = (task % kSplit) * 128 + lane * kVec;
+    if (n == 1 || (by_border && c0 != static_cast<int>(blockIdx.y))) return;  // finished, or another border's
+    const CaSeq seq(a, list.unit[e] & 0xFFFFu);
+    const int tok0 = (list.unit[e] >> 16) * CaCfg<D>::kNQ * c.span, rows = min(CaCfg<D>::kNQ * c.span, seq.tokens - tok0) * group;
+    // (many parts: by CTAs only where there are CTAs for all rows: 24 sequences of 8 tokens, up to 21 parts, 15 CTAs a unit: 39 us
+    // by warps, 52 by CTAs; one of 16 over 65520 keys, 76 parts, 256 CTAs a unit: 51 and 47)
+    const bool few = n <= kCaFew || static_cast<int>(gridDim.x) * 2 < rows * kSplit;
+    const int tasks = few ? kCaJoinWarps : 1;  // of a CTA at once
+    for (int task = blockIdx.x * tasks + (few ? warp : 0); task < rows * kSplit; task += gridDim.x * tasks) {
+        const int pair = task / kSplit, tok = c.by_group(pair), d = (task % kSplit) * kWide + lane * kVec;
         const int r = tok < c.span ? pair : 128 + pair - c.span * group;  // of the unit
         // (a CTA's part of a unit that it begins is its second one)
         auto at = [&](int i) { return (2ll * (c0 + i) + (i == 0 ? 1 : 0)) * kRows + r; };
-        auto part = [&](int i, float (&o)[kVec]) {
-            if (i < n) *reinterpret_cast<Vec*>(o) = *reinterpret_cast<const Vec*>(c.parts.acc + at(i) * D + d);
-        };
-        __align__(16) float o[kAtOnce][kVec];
-#pragma unroll
-        for (int k = 0; k < kAtOnce; ++k) part(k, o[k]);  // (on their way before their factors are known)
         float v[kVec] = {}, top = -INFINITY, sum = 0.f;
-        for (int i0 = 0; i0 < n; i0 += 32) {
-            const float2 ml = i0 + lane < n ? *reinterpret_cast<const float2*>(c.parts.ml + at(i0 + lane) * 2) : make_float2(-INFINITY, 0.f);
-            float m = ml.x;
+        // parts i0, i0 + step, ..., kCaAtOnce of them at once; their factors are of the largest maximum
+        const int i0 = few ? 0 : warp, step = few ? 1 : kCaJoinWarps;
+        __align__(16) float o[kCaAtOnce][kVec];
+        auto ahead = [&](int i) {
 #pragma unroll
-            for (int x = 16; x >= 1; x >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, x));
-            m = fmaxf(m, top);
-            const float base = m == -INFINITY ? 0.f : m, corr = ex2(top - base), f = ex2(ml.x - base);
-            float l = ml.y * f;
+            for (int k = 0; k < kCaAtOnce; ++k)
+                if (i + k * step < n) *reinterpret_cast<Vec*>(o[k]) = *reinterpret_cast<const Vec*>(c.parts.acc + at(i + k * step) * D + d);
+        };
+        ahead(i0);
+        for (int i = lane; i < n; i += 32) mls[warp][i] = *reinterpret_cast<const float2*>(c.parts.ml + at(i) * 2);
+        for (int i = lane; i < n; i += 32) top = fmaxf(top, mls[warp][i].x);
 #pragma unroll
-            for (int x = 16; x >= 1; x >>= 1) l += __shfl_xor_sync(0xffffffffu, l, x);
-            top = m, sum = sum * corr + l;
+        for (int x = 16; x >= 1; x >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, x));
+        const float base = top == -INFINITY ? 0.f : top;
+        for (int i = lane; i < n; i += 32) {
+            const float f = ex2(mls[warp][i].x - base);
+            mls[warp][i].x = f, sum += mls[warp][i].y * f;
+        }
 #pragma unroll
-            for (int x = 0; x < kVec; ++x) v[x] *= corr;
-            for (int k0 = 0; k0 < 32 && i0 + k0 < n; k0 += kAtOnce) {
+        for (int x = 16; x >= 1; x >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, x);
+        __syncwarp();
+        for (int i = i0; i < n; i += kCaAtOnce * step) {
 #pragma unroll
-                for (int k = 0; k < kAtOnce; ++k) {
-                    const float w = __shfl_sync(0xffffffffu, f, k0 + k);
-                    if (i0 + k0 + k < n) {
+            for (int k = 0; k < kCaAtOnce; ++k) {
+                if (i + k * step >= n) continue;
+                const float w = mls[warp][i + k * step].x;
 #pragma unroll
-                        for (int x = 0; x < kVec; ++x) v[x] += o[k][x] * w;
-                    }
-                    part(i0 + k0 + kAtOnce + k, o[k]);
-                }
+                for (int x = 0; x < kVec; ++x) v[x] += o[k][x] * w;
             }
+            ahead(i + kCaAtOnce * step);
+        }
+        __syncwarp();
+        if (!few) {
+            __syncthreads();
+            *reinterpret_cast<Vec*>(&sums[warp][lane * kVec]) = *reinterpret_cast<const Vec*>(v);
+            __syncthreads();
+            if (warp != 0) continue;
+#pragma unroll
+            for (int w = 1; w < kCaJoinWarps; ++w)
+#pragma unroll
+                for (int x = 0; x < kVec; ++x) v[x] += sums[w][lane * kVec + x];
         }
         const float inv = sum == 0.f ? 0.f : 1.f / sum;
         const long long head = static_cast<long long>(seq.first + tok0 + tok) * a.Hq + kvh * group + (pair - tok * group);
@@ -1085,13 +1116,14 @@ cudaError_t ca_launch(const ChunkAttnArgs& a, void* ws, cudaStream_t s) {
     void* args[] = {&c};
     e = launch_kernel(f, dim3(static_cast<unsigned>(p.ranges ? p.ctas : p.runs * a.Hkv)), dim3(C::kThreads), C::kSmem, true, s, args);
     if (e != cudaSuccess || !p.ranges) return e;
-    // (few of many units are cut, and the CTAs of others end at once)
-    int grid = p.ctas;
-    const long long units = p.runs * a.Hkv, most = C::kRows * (D == 256 ? 2 : 1) / kCaJoinWarps, fit = 16 * kSms / units;
-    void* jargs[] = {&c, &grid};
+    const long long units = p.runs * a.Hkv;
+    int grid = p.ctas, by_border = units >= p.ctas;
+    // as many CTAs as are on the GPU at once, but no more a unit than it has rows' parts
+    const long long most = C::kRows * (D == 256 ? 2 : 1) / (by_border ? kCaJoinWarps : 1), fit = 6 * kSms / (by_border ? p.ctas - 1 : units);
+    void* jargs[] = {&c, &grid, &by_border};
+    const unsigned x = static_cast<unsigned>(fit < 1 ? 1 : fit < most ? fit : most);
     return launch_kernel(reinterpret_cast<const void*>(chunk_attention_join_kernel<DT, D>),
-                         dim3(static_cast<unsigned>(fit < 1 ? 1 : fit < most ? fit : most), static_cast<unsigned>(p.runs), a.Hkv),
-                         dim3(kCaJoinWarps * 32), 0, true, s, jargs);
+                         by_border ? dim3(x, p.ctas - 1) : dim3(x, static_cast<unsigned>(p.runs), a.Hkv), dim3(kCaJoinWarps * 32), 0, true, s, jargs);
 }
 
 }  // namespace

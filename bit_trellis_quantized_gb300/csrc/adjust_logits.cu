@@ -15,7 +15,10 @@
 //
 // Bound: the write of the banned and the changed logits, and the read of those
 // next to them. Slices of 32 KB let three CTAs share a multiprocessor, so that
-// one's counting runs beside another's pass.
+// one's counting runs beside another's pass. Measured in f32: 256 rows of 152064,
+// all under masks of one token in eight, up to 8000 ids, 65 us (the sectors that
+// it cannot do without, 259 MB with those read for their allowed tokens: 38); 61 of
+// 248320 copied, 24 us (18); one row in place 4.3 us. Slices of 4096 to 256 threads: 70 and 25 us.
 #include "common.cuh"
 #include "context.h"
 #include "kernels.h"

@@ -666,8 +666,12 @@ int escha_rotary_append(const void* q, const void* k, const void* v, int src_dty
  *   ws       escha_chunk_attention_workspace(n, T, Hq, Hkv, d, max_len) bytes
  *            (may be 0); nothing in it has to start at zero
  * A token that no key is left to (a position below 0, pages that are none) gives
- * out = 0 and lse = -infinity. Rows of no sequence are left as they are. Keys
- * behind a sequence's last token are never read. n <= 65535, T Hq d below 2^40,
+ * out = 0 and lse = -infinity. Rows of no sequence are left as they are. What
+ * a sequence's pages hold behind its last token or the bound does not count, whatever
+ * it is, and what a token's successors hold does not either: a NaN or an infinity
+ * shows in the tokens that attend it (heads of its key, values of its place). Weights
+ * are rounded once to dtype for the second product; sums are f32. Results are
+ * repeatable bit for bit. out, lse and ws must not overlap the inputs. n <= 65535, T Hq d below 2^40,
  * T Hq / Hkv below 2^31 - 65535.
  * Errors as escha_paged_attention. */
 size_t escha_chunk_attention_workspace(int n, int T, int Hq, int Hkv, int d, int max_len);

@@ -1070,9 +1070,13 @@ CaPlan ca_plan(int n, int T, int Hq, int Hkv, int d, int max_len) {
     const long long units = p.runs * Hkv, rounds = (units + kSms - 1) / kSms;
     // Whole units leave CTAs idle in the last round of them, for the time of (rounds 152 - units) / 152 units of the tiles
     // that a unit may have (the host does not know the lengths: an even share of the tokens, behind the longest cache);
-    // cut over all CTAs they end together, which costs the parts and a second kernel. In tiles of 1.5 us:
+    // cut over all CTAs they end together, which costs the parts and a second kernel: 15 us of few units, 30 of many. In
+    // tiles of 1.5 us. Whole and cut (16 heads on 2 key heads of 256): 4 tokens over 700 keys 16 and 12 us, 64 over 4064
+    // 60 and 29, 256 over 4352 63 and 37, 512 14 and 38, 2048 36 and 65, 2048 behind 8192 242 and 250, behind 14336 392 and
+    // 373, behind 30720 788 and 730; 32 heads on 8 of 128, 4096 behind 16384: 1024 and 945.
     const long long tokens = T / n, tiles = (max_len - (tokens < max_len ? tokens : max_len) / 2) / kKeys + 1;
-    p.ranges = p.runs <= kCaRuns && (rounds * kSms - units) * tiles > 12 * kSms && units * (max_len / kKeys + 1 + kCaStart) < 1ll << 30;
+    p.ranges = p.runs <= kCaRuns && (rounds * kSms - units) * tiles > (units < kSms ? 10 : 22) * kSms &&
+               units * (max_len / kKeys + 1 + kCaStart) < 1ll << 30;
     p.ctas = kSms;
     if (p.ranges) {
         p.ml = static_cast<size_t>(2) * p.ctas * rows * d * 4;

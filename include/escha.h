@@ -664,7 +664,8 @@ int escha_rotary_append(const void* q, const void* k, const void* v, int src_dty
  *   max_len  host-side bound of lens, 1..2^30: keys at or behind
  *            min(max_len, max_pages * page) are left out
  *   ws       escha_chunk_attention_workspace(n, T, Hq, Hkv, d, max_len) bytes
- *            (may be 0); nothing in it has to start at zero
+ *            (may be 0); nothing in it has to start at zero. Calls that may
+ *            overlap, captured graphs among them, need one each.
  * A token that no key is left to (a position below 0, pages that are none) gives
  * out = 0 and lse = -infinity. Rows of no sequence are left as they are. What
  * a sequence's pages hold behind its last token or the bound does not count, whatever
@@ -672,7 +673,8 @@ int escha_rotary_append(const void* q, const void* k, const void* v, int src_dty
  * shows in the tokens that attend it (heads of its key, values of its place). Weights
  * are rounded once to dtype for the second product; sums are f32. Results are
  * repeatable bit for bit. out, lse and ws must not overlap the inputs. n <= 65535, T Hq d below 2^40,
- * T Hq / Hkv below 2^31 - 65535.
+ * T Hq / Hkv below 2^31 - 65535. A wait between the kernel's warps that gives up (after seconds; none is known to)
+ * leaves NaN in the rows in work.
  * Errors as escha_paged_attention. */
 size_t escha_chunk_attention_workspace(int n, int T, int Hq, int Hkv, int d, int max_len);
 int escha_chunk_attention(const void* q, const void* k_pool, const void* v_pool, int dtype, const int32_t* table,

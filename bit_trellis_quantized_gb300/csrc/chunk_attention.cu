@@ -134,12 +134,12 @@ struct CaParts {
 };
 struct CaArgs {
     CUtensorMap keys, values;  // the pools as [rows / 8][d / 64][8][64], in boxes of `box` rows and a slot's values
-    CUtensorMap queries;       // [T][Hq][d] in boxes of 128 rows of a unit and 64 values
+    CUtensorMap queries;       // [T][Hq][d] in boxes of a tile's tokens, a key head's heads and 64 values
     ChunkAttnArgs a;
-    int box;  // rows of a page that are loaded at once: 8 to 128, or 0 (pages not of a multiple of 8): rows one by one
+    int box;   // rows of a page that are loaded at once: 8 to 128, or 0 (pages not of a multiple of 8): rows one by one
     int span;  // tokens of a tile of rows
     int runs;  // of all sequences, at most (bounds that descend may give more: those are left out)
-    int cap;  // keys that may be read
+    int cap;   // keys that may be read
     CaDiv by_page, by_group;
     CaParts parts;
 };
@@ -187,6 +187,7 @@ struct CaBars {
 // rows in work become NaN. Waits are for a tile's work (2^19 polls, two seconds), or for a unit's (2^26): one of 2^30 keys
 // takes ten seconds.
 __device__ __forceinline__ bool ca_bad(CaBars& b) { return *reinterpret_cast<volatile int*>(&b.bad) != 0; }
+__device__ __forceinline__ bool ca_any_bad(CaBars& b) { return __any_sync(0xffffffffu, ca_bad(b)); }  // (of a warp together)
 __device__ __forceinline__ void ca_wait_long(CaBars& b, uint32_t at, uint32_t parity, int polls) {
 #pragma unroll 1
     for (int it = 0; it < polls; ++it)
@@ -206,7 +207,7 @@ __device__ __forceinline__ bool ca_next(CaBars& b, uint32_t k, int lane, CaUnit&
     u = b.unit[k & 1];
     __syncwarp();
     if (lane == 0) ca_arrive(&b.unit_empty[k & 1]);
-    return u.tiles > 0 && !ca_bad(b);
+    return u.tiles > 0 && !ca_any_bad(b);
 }
 
 // The sum over the lanes up to this one.
@@ -311,7 +312,7 @@ __device__ __forceinline__ void ca_units(const CaArgs& c, CaBars& b, CaList& lis
         const int run = max(q.runs(most) - 1 - off / a.Hkv, 0), keys = q.keys(run, most, c.cap);
         give(q, s0 + src, run, off % a.Hkv, 0, ca_tiles(keys), keys);
         ca_wait(b, &b.want, steals & 1, kUnitPolls);
-        if (ca_bad(b)) break;
+        if (ca_any_bad(b)) break;
         if (lane == 0) {
             tc::fence_proxy_async_smem();
             tc::mbar_arrive_expect_tx(tc::smem_addr(&b.stolen), 16);
@@ -321,7 +322,7 @@ __device__ __forceinline__ void ca_units(const CaArgs& c, CaBars& b, CaList& lis
         }
         __syncwarp();
         ca_wait(b, &b.stolen, steals & 1);
-        if (ca_bad(b)) break;
+        if (ca_any_bad(b)) break;
         ++steals;
         uint32_t got, id;
         asm volatile(
@@ -478,6 +479,7 @@ __device__ __forceinline__ void ca_load_boxes(const CaArgs& c, CaBars& b, uint32
                 const int of = C::kNQ == 1 && !keys_now ? j - 1 : j;
                 const uint32_t at = slot % kSlots, use = slot / kSlots;
                 if (use > 0) ca_wait(b, &b.empty[at], (use - 1) & 1);
+                if (ca_any_bad(b)) return;
                 const uint32_t bar = tc::smem_addr(!keys_now && of >= partly ? &b.raw[at] : &b.full[at]);
                 if (lane == 0) tc::mbar_arrive_expect_tx(bar, C::kSlotBytes);
                 __syncwarp();
@@ -680,7 +682,7 @@ __device__ __forceinline__ void ca_products(CaBars& b, int span, uint32_t q_smem
         wait(&b.unit_full[k & 1], (k >> 1) & 1, kUnitPolls);
         const int tiles = __shfl_sync(0xffffffffu, b.unit[k & 1].tiles, 0), nq = kNQ == 2 && __shfl_sync(0xffffffffu, b.unit[k & 1].toks, 0) > span ? 2 : 1;
         if (lead) ca_arrive(&b.unit_empty[k & 1]);
-        if (tiles <= 0 || __any_sync(0xffffffffu, ca_bad(b))) break;
+        if (tiles <= 0 || ca_any_bad(b)) break;
         wait(&b.q_full, k & 1);
         // one tile of rows: scores of tile j, then values of the one before; two: the values of either, then its scores
         // of the next tile
@@ -712,7 +714,7 @@ __device__ __forceinline__ void ca_products(CaBars& b, int span, uint32_t q_smem
         if (nq == 2) soft1 += tiles, ++units1;
         ++k;
     }
-    if (__any_sync(0xffffffffu, ca_bad(b))) {
+    if (ca_any_bad(b)) {
         // a wait gave up: the products in flight still end before tensor memory is given back
         commit(&b.end);
         tc::mbar_wait_parity_bounded(tc::smem_addr(&b.end), 0, 1 << 19);
@@ -948,6 +950,10 @@ __global__ void __launch_bounds__(CaCfg<D>::kThreads, 1) chunk_attention_kernel(
         else ca_products<DT, D>(b, c.span, q_smem, ring);
         __syncwarp();
     }
+    // (where a wait gave up: loads in flight land long before this is over)
+    if (ca_bad(b))
+        for (int i = 0; i < 2000; ++i) __nanosleep(1000);
+    __syncwarp();
     tc::fence_before_sync();
     __syncthreads();
     tc::fence_after_sync();

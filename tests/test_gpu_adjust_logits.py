@@ -164,6 +164,20 @@ def test_bounds_of_the_lists_are_clamped_and_masks_out_of_range_are_none():
     check(x, c, native.adjust_logits(x, **dev(c)), "f32")
 
 
+@pytest.mark.parametrize("dtype", ["f16", "f32"])
+def test_more_biases_than_a_slice_lists_and_every_token_touched(dtype):
+    native = _native()
+    x, c = make(49, 2, 9001, dtype, 0, 3000, 1)
+    c["bias_ids"][:600] = 7  # one token's, far apart
+    check(x, c, native.adjust_logits(x, **dev(c)), dtype)
+    n = 2 * 9001
+    c.update(ids=np.tile(np.arange(9001, dtype=np.int32), 4), at=np.array([0, n, 2 * n], np.int32), prompt=np.array([9001, 100], np.int32),
+             repetition=np.array([1.5, 2.0], np.float32), frequency=np.array([0.5, 0.1], np.float32), presence=np.array([0.0, 1.0], np.float32))
+    got = native.adjust_logits(x, **dev(c))
+    check(x, c, got, dtype)
+    assert torch.equal(native.adjust_logits(x, **dev(c), out=x), got)
+
+
 def test_no_masks_and_empty_lists():
     native = _native()
     x, _ = make(45, 3, 77, "bf16")

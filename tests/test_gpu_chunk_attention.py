@@ -178,13 +178,14 @@ def test_many_keys_of_next_to_no_weight(dtype, d):
 @pytest.mark.parametrize("dtype,new,old,Hq,Hkv,d", [("f16", [200], [100], 16, 4, 64), ("bf16", [150], [3], 6, 2, 128),
                                                     ("f16", [90, 40], [0, 300], 24, 2, 256), ("bf16", [5], [7000], 16, 2, 256)])
 @pytest.mark.parametrize("bad", [float("nan"), float("inf"), float("-inf")])
-def test_nan_and_infinity_stay_with_the_tokens_that_see_them(dtype, new, old, Hq, Hkv, d, bad):
+@pytest.mark.parametrize("page", [16, 17])
+def test_nan_and_infinity_stay_with_the_tokens_that_see_them(dtype, new, old, Hq, Hkv, d, page, bad):
     """A key or value behind a token is masked, whatever it holds; the others'
     outputs keep their bits."""
     native = _native()
     group = Hq // Hkv
     for what in ("q", "k", "v"):
-        c = make(36, new, old, Hq, Hkv, d, 16, dtype)
+        c = make(36, new, old, Hq, Hkv, d, page, dtype)
         want, want_lse = (x.clone() for x in native.chunk_attention(*args(c)))
         hit = torch.zeros_like(want, dtype=torch.bool)
         last = new[0] - 3
@@ -192,7 +193,7 @@ def test_nan_and_infinity_stay_with_the_tokens_that_see_them(dtype, new, old, Hq
             c["q"][last, 3, 5], hit[last, 3] = bad, True
         else:
             p = old[0] + last  # a new token's own key or value
-            c[what][int(c["table"][0, p // 16]), 1, p % 16, 5] = bad
+            c[what][int(c["table"][0, p // page]), 1, p % page, 5] = bad
             hit[last:new[0], group:2 * group, slice(None) if what == "k" else 5] = True
         out, lse = native.chunk_attention(*args(c))
         assert torch.equal(out[~hit], want[~hit])

@@ -167,6 +167,10 @@ struct CaSeq {
 };
 __device__ __forceinline__ int ca_tiles(int keys) { return max(1, (keys + kKeys - 1) / kKeys); }
 
+// Lists of a unit's values that are not finite, by k % kOdd: the loads of unit k + 1 and k + 2 may begin while the outputs of unit
+// k leave (a short unit's scores end before them). Unit k + 3 is handed out when all warps have taken unit k + 1, so are done with k.
+constexpr int kOdd = 3;
+
 // What a CTA works on next, handed to all its warps.
 struct CaUnit {
     int s, kvh, tok0, toks;  // its tokens, of the sequence's
@@ -174,13 +178,18 @@ struct CaUnit {
     int tile0, tiles, keys;  // tiles 0: no more units
     int whole;
 };
+// A slot has landed, is free again, has landed but is to be looked through.
+template <int kSlots>
+struct CaRing {
+    unsigned long long full[kSlots], empty[kSlots], raw[kSlots];
+};
 struct CaBars {
-    unsigned long long full[10], empty[10], raw[10], s_full[2], p_full[2], pv_done[2], o_full[2], o_empty[2], q_full, q_empty, unit_full[2], unit_empty[2], want, stolen, end;
+    unsigned long long s_full[2], p_full[2], pv_done[2], o_full[2], o_empty[2], q_full, q_empty, unit_full[2], unit_empty[2], want, stolen, end;
     uint32_t tmem;
     int bad;
     CaUnit unit[2];
     __align__(16) uint32_t masks[kMasks][4];  // of a tile's keys, which are there
-    uint32_t odd[2][4][4], any_odd[2];  // of a unit's last tiles, keys whose values are not all finite
+    uint32_t odd[kOdd][4][4], any_odd[kOdd];  // of a unit's last tiles, keys whose values are not all finite
 };
 
 // A wait that gives up after so many polls of 4 us at most, or once another has: the CTA then runs on to its end and the
@@ -413,7 +422,7 @@ __device__ __forceinline__ void ca_take_odd(uint32_t slot, int r0, int r1, uint3
 // Pages of a multiple of 8 keys: the first warp loads boxes of a page's rows, a lane a box (TMA), the second looks through
 // the values of the tiles that are seen in part.
 template <int DT, int D, bool kRanges>
-__device__ __forceinline__ void ca_load_boxes(const CaArgs& c, CaBars& b, uint32_t q_smem, uint32_t ring) {
+__device__ __forceinline__ void ca_load_boxes(const CaArgs& c, CaBars& b, CaRing<CaCfg<D>::kSlots>& bars, uint32_t q_smem, uint32_t ring) {
     using C = CaCfg<D>;
     const ChunkAttnArgs& a = c.a;
     const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - C::kSoftWarps;
@@ -425,7 +434,7 @@ __device__ __forceinline__ void ca_load_boxes(const CaArgs& c, CaBars& b, uint32
     for (; ca_next(b, k, lane, u); ++k) {
         ca_wait(b, &b.q_empty, (k - 1) & 1, kUnitPolls);
         const int partly = ca_partly(u), common = ca_common(u);
-        uint32_t* odd = &b.odd[k & 1][0][0];
+        uint32_t* odd = &b.odd[k % kOdd][0][0];
         if (w == 1) {
 #pragma unroll 1
             for (int j = partly; j < u.tiles; ++j)
@@ -433,20 +442,20 @@ __device__ __forceinline__ void ca_load_boxes(const CaArgs& c, CaBars& b, uint32
                 for (int p = 0; p < C::kParts; ++p) {
                     // (order of the slots: below)
                     const uint32_t i = slot + p + C::kParts * (C::kNQ == 1 ? min(2 * j + 2, 2 * u.tiles - 1) : 2 * j + 1), at = i % kSlots;
-                    ca_wait(b, &b.raw[at], phases >> at & 1, kUnitPolls);
+                    ca_wait(b, &bars.raw[at], phases >> at & 1, kUnitPolls);
                     phases ^= 1u << at;
                     // the rows that not all see and that were loaded: the rest of a box behind the last key, no further
                     const int key0 = (u.tile0 + j) * kKeys, r0 = max(common - key0, 0) & ~7, r1 = min((u.keys - key0 + c.box - 1) & -c.box, kKeys);
-                    ca_take_odd<DT, D>(ring + at * C::kSlotBytes, r0, r1, odd + 4 * (j - partly), &b.any_odd[k & 1]);
+                    ca_take_odd<DT, D>(ring + at * C::kSlotBytes, r0, r1, odd + 4 * (j - partly), &b.any_odd[k % kOdd]);
                     tc::fence_proxy_async_smem();
                     __syncwarp();
-                    if (lane == 0) ca_arrive(&b.full[at]);
+                    if (lane == 0) ca_arrive(&bars.full[at]);
                 }
             slot += 2 * C::kParts * u.tiles;
             continue;
         }
         if (lane < 16) odd[lane] = 0;
-        if (lane == 16) b.any_odd[k & 1] = 0;
+        if (lane == 16) b.any_odd[k % kOdd] = 0;
         __syncwarp();
         ca_queries<D>(c, b, u, q_smem);
         const int32_t* table = a.table + static_cast<long long>(u.s) * a.max_pages;
@@ -478,9 +487,9 @@ __device__ __forceinline__ void ca_load_boxes(const CaArgs& c, CaBars& b, uint32
                 if (C::kNQ == 1 && (keys_now ? j == u.tiles : j == 0)) continue;
                 const int of = C::kNQ == 1 && !keys_now ? j - 1 : j;
                 const uint32_t at = slot % kSlots, use = slot / kSlots;
-                if (use > 0) ca_wait(b, &b.empty[at], (use - 1) & 1);
+                if (use > 0) ca_wait(b, &bars.empty[at], (use - 1) & 1);
                 if (ca_any_bad(b)) return;
-                const uint32_t bar = tc::smem_addr(!keys_now && of >= partly ? &b.raw[at] : &b.full[at]);
+                const uint32_t bar = tc::smem_addr(!keys_now && of >= partly ? &bars.raw[at] : &bars.full[at]);
                 if (lane == 0) tc::mbar_arrive_expect_tx(bar, C::kSlotBytes);
                 __syncwarp();
                 if (lane < boxes)
@@ -500,7 +509,7 @@ __device__ __forceinline__ void ca_load_boxes(const CaArgs& c, CaBars& b, uint32
 
 // Pages of any size: warp w loads the rows 64 w .. 64 w + 63 of a tile, 16 bytes a lane.
 template <int DT, int D, bool kRanges>
-__device__ __forceinline__ void ca_load_rows(const CaArgs& c, CaBars& b, uint32_t q_smem, uint32_t ring) {
+__device__ __forceinline__ void ca_load_rows(const CaArgs& c, CaBars& b, CaRing<CaCfg<D>::kSlots>& bars, uint32_t q_smem, uint32_t ring) {
     using C = CaCfg<D>;
     const ChunkAttnArgs& a = c.a;
     const int lane = threadIdx.x & 31, w = (threadIdx.x >> 5) - C::kSoftWarps;
@@ -516,10 +525,10 @@ __device__ __forceinline__ void ca_load_rows(const CaArgs& c, CaBars& b, uint32_
 #pragma unroll 1
         for (; pending > keep; --pending, marks >>= 4) {
             const uint32_t at = (slot - pending) % kSlots, mark = marks & 15;
-            if (mark) ca_take_odd<DT, D>(ring + at * C::kSlotBytes, 64 * w, 64 * w + 64, b.odd[k & 1][mark - 1], &b.any_odd[k & 1]);
+            if (mark) ca_take_odd<DT, D>(ring + at * C::kSlotBytes, 64 * w, 64 * w + 64, b.odd[k % kOdd][mark - 1], &b.any_odd[k % kOdd]);
             tc::fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) ca_arrive(&b.full[at]);
+            if (lane == 0) ca_arrive(&bars.full[at]);
         }
     };
     auto room = [&](unsigned long long* bar, uint32_t parity) {
@@ -530,8 +539,8 @@ __device__ __forceinline__ void ca_load_rows(const CaArgs& c, CaBars& b, uint32_
     CaUnit u;
     for (; ca_next(b, k, lane, u); ++k) {
         ca_wait(b, &b.q_empty, (k - 1) & 1, kUnitPolls);  // (nothing is in flight)
-        if (w == 0 && lane < 16) b.odd[k & 1][lane >> 2][lane & 3] = 0;
-        if (w == 0 && lane == 16) b.any_odd[k & 1] = 0;
+        if (w == 0 && lane < 16) b.odd[k % kOdd][lane >> 2][lane & 3] = 0;
+        if (w == 0 && lane == 16) b.any_odd[k % kOdd] = 0;
         asm volatile("bar.sync 1, %0;" ::"n"(32 * C::kLoadWarps) : "memory");
         if (w == 0) ca_queries<D>(c, b, u, q_smem);
         const int32_t* table = a.table + static_cast<long long>(u.s) * a.max_pages;
@@ -566,7 +575,7 @@ __device__ __forceinline__ void ca_load_rows(const CaArgs& c, CaBars& b, uint32_
                 const int of = C::kNQ == 1 && !keys_now ? j - 1 : j;
                 const int r0 = of < j ? last[0] : row[0], r1 = of < j ? last[1] : row[1];
                 const uint32_t use = slot / kSlots;
-                if (use > 0) room(&b.empty[slot % kSlots], (use - 1) & 1);
+                if (use > 0) room(&bars.empty[slot % kSlots], (use - 1) & 1);
                 const char* base = static_cast<const char*>(keys_now ? a.k_pool : a.v_pool) + (keys_now ? i : i - C::kParts) * (C::kSlotD * 2) + c8 * 16;
                 const uint32_t to = ring + slot % kSlots * C::kSlotBytes;
 #pragma unroll 1
@@ -609,7 +618,7 @@ __device__ __forceinline__ void ca_mma_ts(uint32_t d, uint32_t a_tmem, uint32_t 
         : "memory");
 }
 template <int DT, int D>
-__device__ __forceinline__ void ca_products(CaBars& b, int span, uint32_t q_smem, uint32_t ring) {
+__device__ __forceinline__ void ca_products(CaBars& b, CaRing<CaCfg<D>::kSlots>& bars, int span, uint32_t q_smem, uint32_t ring) {
     using C = CaCfg<D>;
     constexpr int kNQ = C::kNQ, kParts = C::kParts, kSlots = C::kSlots;
     constexpr uint32_t is = tc::idesc_f16(128, 128, false, false, DT == 2), io = tc::idesc_f16(128, C::kSlotD, false, true, DT == 2);
@@ -643,13 +652,13 @@ __device__ __forceinline__ void ca_products(CaBars& b, int span, uint32_t q_smem
         uint32_t at = k_at, r = k_round;
 #pragma unroll
         for (int p = 0; p < kParts; ++p) {
-            wait(&b.full[at], r & 1);
+            wait(&bars.full[at], r & 1);
             const uint32_t kb = k_lo + ring16 + at * (C::kSlotBytes / 16), qb = q_lo + q16 + (q * (128 * D * 2) + p * (C::kSlotD / 64) * 16384) / 16;
 #pragma unroll
             for (int x = 0; x < C::kSlotD / 16; ++x) {
                 ca_mma(d, qb + ((x >> 2) * 16384 + (x & 3) * 32) / 16, q_hi, kb + ((x >> 2) * 1024 + (x & 3) * 32) / 16, k_hi, is, p + x > 0, lead);
             }
-            if (release) commit(&b.empty[at]);
+            if (release) commit(&bars.empty[at]);
             at = after(at, r);
         }
         commit(&b.s_full[buf]);
@@ -661,12 +670,12 @@ __device__ __forceinline__ void ca_products(CaBars& b, int span, uint32_t q_smem
         uint32_t at = v_at, r = v_round;
 #pragma unroll
         for (int p = 0; p < kParts; ++p) {
-            wait(&b.full[at], r & 1);
+            wait(&bars.full[at], r & 1);
             const uint32_t vb = v_lo + ring16 + at * (C::kSlotBytes / 16);
 #pragma unroll
             for (int x = 0; x < kKeys / 16; ++x)
                 ca_mma_ts(q * D + p * 128, C::kScol + 128 * buf + x * 8, vb + x * (kChunks * 2048 / 16), v_hi, io, j > 0 || x > 0, lead);
-            if (release) commit(&b.empty[at]);
+            if (release) commit(&bars.empty[at]);
             at = after(at, r);
         }
         // A parity tells two phases apart: pv_done of tile j - 1 is asked for while that of j cannot be there yet (its
@@ -726,10 +735,11 @@ template <int DT, int D>
 __device__ __noinline__ void ca_add_odd(const CaArgs& c, const CaBars& b, const CaUnit& u, uint32_t k, int pos, int col, float* v) {
     const int first = u.tile0 + ca_partly(u);
     for (int i = 0; i < 16; ++i)
-        for (uint32_t m = b.odd[k & 1][i >> 2][i & 3]; m; m &= m - 1) {
+        for (uint32_t m = b.odd[k % kOdd][i >> 2][i & 3]; m; m &= m - 1) {
             const int key = (first + (i >> 2)) * kKeys + 32 * (i & 3) + __ffs(m) - 1;
             if (key > pos || key >= u.keys) return;
-            const int p = c.by_page(key), pg = c.a.table[static_cast<long long>(u.s) * c.a.max_pages + p];  // (a page that is there)
+            const int p = c.by_page(key), pg = c.a.table[static_cast<long long>(u.s) * c.a.max_pages + p];
+            if (static_cast<unsigned>(pg) >= static_cast<unsigned>(c.a.n_pages)) continue;  // (listed only after a wait that gave up)
             const long long row = (static_cast<long long>(pg) * c.a.Hkv + u.kvh) * c.a.page + (key - p * c.a.page);
             for (int e = 0; e < 32; ++e) {
                 const float x = load_act(c.a.v_pool, row * D + col + e, DT);
@@ -856,7 +866,7 @@ __device__ __forceinline__ void ca_soft(const CaArgs& c, CaBars& b, uint32_t tme
         ca_wait(b, &b.o_full[q], units & 1);
         tc::fence_after_sync();
         if (ca_bad(b)) l = NAN;
-        const bool odd = *reinterpret_cast<volatile uint32_t*>(&b.any_odd[k & 1]) != 0;
+        const bool odd = *reinterpret_cast<volatile uint32_t*>(&b.any_odd[k % kOdd]) != 0;
         const long long head = static_cast<long long>(u.first + u.tok0 + tok) * a.Hq + u.kvh * group + g_head;
         const long long slot = 2ll * blockIdx.x + (u.tile0 == 0 ? 1 : 0);
         const float inv = l == 0.f ? 0.f : 1.f / l;
@@ -911,13 +921,14 @@ __global__ void __launch_bounds__(CaCfg<D>::kThreads, 1) chunk_attention_kernel(
     using C = CaCfg<D>;
     extern __shared__ unsigned char raw[];
     __shared__ __align__(16) CaBars b;
+    __shared__ CaRing<C::kSlots> bars;
     __shared__ CaList list;
     __shared__ uint4 response;
     const int t = threadIdx.x, warp = t >> 5;
     if (t == 0) {
         auto init = [](unsigned long long* bar, uint32_t count) { tc::mbar_init_cta(tc::smem_addr(bar), count); };
 #pragma unroll 1
-        for (int i = 0; i < C::kSlots; ++i) init(&b.full[i], c.box ? 1 : C::kLoadWarps), init(&b.empty[i], 1), init(&b.raw[i], 1);
+        for (int i = 0; i < C::kSlots; ++i) init(&bars.full[i], c.box ? 1 : C::kLoadWarps), init(&bars.empty[i], 1), init(&bars.raw[i], 1);
 #pragma unroll 1
         for (int i = 0; i < 2; ++i) {
             init(&b.s_full[i], 1), init(&b.p_full[i], 4), init(&b.pv_done[i], 1), init(&b.o_full[i], 1), init(&b.o_empty[i], 4);
@@ -944,10 +955,10 @@ __global__ void __launch_bounds__(CaCfg<D>::kThreads, 1) chunk_attention_kernel(
         ca_soft<DT, D>(c, b, tmem);
     } else {
         if (C::kNQ == 2) asm volatile("setmaxnreg.dec.sync.aligned.u32 104;");
-        if (warp < C::kMmaWarp && c.box) ca_load_boxes<DT, D, kRanges>(c, b, q_smem, ring);
-        else if (warp < C::kMmaWarp) ca_load_rows<DT, D, kRanges>(c, b, q_smem, ring);
+        if (warp < C::kMmaWarp && c.box) ca_load_boxes<DT, D, kRanges>(c, b, bars, q_smem, ring);
+        else if (warp < C::kMmaWarp) ca_load_rows<DT, D, kRanges>(c, b, bars, q_smem, ring);
         else if (warp == C::kUnitWarp) ca_units<C::kNQ, kRanges>(c, b, list, &response);
-        else ca_products<DT, D>(b, c.span, q_smem, ring);
+        else ca_products<DT, D>(b, bars, c.span, q_smem, ring);
         __syncwarp();
     }
     // (where a wait gave up: loads in flight land long before this is over)

@@ -405,3 +405,45 @@ def test_refusals():
     one = make(39, [4], [20000], 16, 2, 64, 16, "f16", poison=False)  # few tokens over many keys: parts in a workspace
     with pytest.raises(native.EschaError, match="workspace"):
         native.chunk_attention(*args(one), ws=torch.empty(256, dtype=torch.uint8, device="cuda"))
+
+
+@pytest.mark.parametrize("dtype,Hq,Hkv,d", [("f16", 8, 2, 64), ("bf16", 6, 3, 128), ("f16", 16, 2, 256)])
+@pytest.mark.parametrize("page", [16, 17])
+@pytest.mark.parametrize("cut", [False, True])
+def test_short_sequences_keep_their_values_that_are_not_finite(dtype, Hq, Hkv, d, page, cut):
+    """CTAs that take one short unit after another: a NaN or an infinity among a sequence's last values shows in every column that has
+    one, of every token that attends it, and nowhere else. ``cut``: few enough sequences under a bound that cuts all units into ranges."""
+    native = _native()
+    rng = np.random.default_rng(50)
+    if cut:
+        Hkv, Hq = 8, 8 * (Hq // Hkv)
+    n, max_len = (110, 1 << 18) if cut else (300, 128)
+    new = rng.integers(1, 6, n).tolist()
+    c = make(51, new, rng.integers(0, 123, n).tolist(), Hq, Hkv, d, page, dtype)
+    c["table"] = torch.nn.functional.pad(c["table"], (0, max_len // page), value=0)
+    need = native.lib().escha_chunk_attention_workspace(n, sum(new), Hq, Hkv, d, max_len)
+    assert (need > 0) == cut
+    table, lens = c["table"].cpu().numpy(), c["lens"].tolist()
+    for s in range(n):
+        for _ in range(rng.integers(0, 4)):  # values of new tokens: seen by them and those behind them
+            j, (a, b) = lens[s] - 1 - rng.integers(0, new[s]), sorted(rng.integers(0, d + 1, 2))
+            c["v"][int(table[s, j // page]), rng.integers(0, Hkv), j % page, a:b] = (float("nan"), float("inf"), float("-inf"))[rng.integers(0, 3)]
+    nan, plus, minus = (np.zeros((sum(new), Hq, d), bool) for _ in range(3))
+    seq, pos = ref.places(np.cumsum([0] + new), lens, sum(new))
+    v = f64(c["v"])
+    for t in range(sum(new)):  # what each token attends, from the cache as it is
+        pages = table[seq[t], :pos[t] // page + 1]
+        rows = np.concatenate(v[pages], 1)[:, :pos[t] + 1]
+        for what, has in ((nan, np.isnan(rows)), (plus, np.isposinf(rows)), (minus, np.isneginf(rows))):
+            what[t] = np.repeat(has.any(1), Hq // Hkv, 0)
+    nan |= plus & minus
+    for _ in range(3):
+        out, lse = native.chunk_attention(*args(c), max_len=max_len)
+        got = f64(out)
+        assert np.array_equal(np.isnan(got), nan)
+        assert np.array_equal(got == np.inf, plus & ~nan) and np.array_equal(got == -np.inf, minus & ~nan)
+    clean = dict(c, v=torch.where(c["v"].isfinite(), c["v"], 0))
+    want, want_lse = native.chunk_attention(*args(clean), max_len=max_len)
+    odd = torch.from_numpy(nan | plus | minus).cuda()
+    assert torch.equal(out[~odd], want[~odd]) and torch.equal(lse, want_lse)
+    check(clean, want, want_lse, d ** -0.5, dtype)

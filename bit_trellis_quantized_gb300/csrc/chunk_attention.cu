@@ -231,7 +231,7 @@ __device__ __forceinline__ int ca_sum(int x) {
 
 // ---- the warp that hands out units
 // kRanges: this CTA's range of all units' tiles. Else units, the longest of a sequence first: that of blockIdx, then those
-// of CTAs that have not begun yet, taken over (cancelled) one at a time when the one in work comes to its end.
+// of CTAs that have not begun yet, taken over (cancelled) one at a time when the one in work comes to its end, in any order.
 template <int kNQ, bool kRanges>
 __device__ __forceinline__ void ca_units(const CaArgs& c, CaBars& b, CaList& list, uint4* response) {
     const ChunkAttnArgs& a = c.a;
@@ -301,12 +301,17 @@ __device__ __forceinline__ void ca_units(const CaArgs& c, CaBars& b, CaList& lis
         stop();
         return;
     }
-    int unit = blockIdx.x, s0 = 0, before = 0;
+    auto of_cta = [&](int id) { return a.backwards ? static_cast<int>(gridDim.x) - 1 - id : id; };
+    int unit = of_cta(blockIdx.x), s0 = 0, before = 0;
     CaSeq mine(a, lane);
     uint32_t steals = 0;
     while (true) {
-        // the sequence: 32 at a time, on from the one before
+        // the sequence: 32 at a time, on from those of the unit before, or from the first one where that lies behind
         int w, incl;
+        if (unit < before) {
+            before = 0, s0 = 0;
+            mine = CaSeq(a, lane);
+        }
         while (true) {
             w = mine.runs(most) * a.Hkv, incl = ca_sum(w);
             const int all = __shfl_sync(0xffffffffu, incl, 31);
@@ -316,9 +321,9 @@ __device__ __forceinline__ void ca_units(const CaArgs& c, CaBars& b, CaList& lis
         }
         const unsigned has = __ballot_sync(0xffffffffu, unit < before + incl);
         if (!has) break;  // past the last unit
-        const int src = __ffs(has) - 1, off = max(unit - before - __shfl_sync(0xffffffffu, incl - w, src), 0);
+        const int src = __ffs(has) - 1, off = unit - before - __shfl_sync(0xffffffffu, incl - w, src);
         const CaSeq q = mine.of(src);
-        const int run = max(q.runs(most) - 1 - off / a.Hkv, 0), keys = q.keys(run, most, c.cap);
+        const int run = q.runs(most) - 1 - off / a.Hkv, keys = q.keys(run, most, c.cap);
         give(q, s0 + src, run, off % a.Hkv, 0, ca_tiles(keys), keys);
         ca_wait(b, &b.want, steals & 1, kUnitPolls);
         if (ca_any_bad(b)) break;
@@ -342,7 +347,7 @@ __device__ __forceinline__ void ca_units(const CaArgs& c, CaBars& b, CaList& lis
             : "r"(tc::smem_addr(response))
             : "memory");
         if (!got) break;
-        unit = id;
+        unit = of_cta(static_cast<int>(id));
     }
     stop();
 }

@@ -90,6 +90,7 @@ std::atomic<long long> g_fz_wait_ns{2000000000ll};
 std::atomic<int> g_fz_skip_publish{0};
 std::atomic<int> g_mbar_limit_log2{24};
 std::atomic<int> g_skip_cluster_arrive{0};
+std::atomic<int> g_chunk_backwards{0};
 
 int check_trellis(const uint16_t* codes, int in, int out, int K, int mult, const char* name) {
     if (!codes) return fail(ESCHA_E_ARG, "%s: codes is null", name);
@@ -1457,6 +1458,13 @@ int escha_rotary_append(const void* q, const void* k, const void* v, int src_dty
                        "rotary_append launch");
 }
 
+int escha_debug_set_chunk_order(int backwards) {
+    if (backwards != 0 && backwards != 1)
+        return fail(ESCHA_E_ARG, "debug_set_chunk_order: backwards=%d must be 0 or 1", backwards);
+    g_chunk_backwards.store(backwards);
+    return ESCHA_OK;
+}
+
 size_t escha_chunk_attention_workspace(int n, int T, int Hq, int Hkv, int d, int max_len) {
     if (check_chunk_shape(n, T, Hq, Hkv, d, max_len, "chunk_attention_workspace")) return 0;
     return escha::chunk_attention_ws_bytes(n, T, Hq, Hkv, d, max_len);
@@ -1480,7 +1488,7 @@ int escha_chunk_attention(const void* q, const void* k_pool, const void* v_pool,
     int sms;
     if ((r = device_check(&sms))) return r;
     const escha::ChunkAttnArgs a{q, k_pool, v_pool, table, at,      lens,      out,     lse,  n, T,
-                                 Hq, Hkv,   d,      page,  n_pages, max_pages, max_len, scale};
+                                 Hq, Hkv,   d,      page,  n_pages, max_pages, max_len, scale, g_chunk_backwards.load()};
     return cuda_status(escha::launch_chunk_attention(a, dtype, ws, static_cast<cudaStream_t>(stream)),
                        "chunk_attention launch");
 }

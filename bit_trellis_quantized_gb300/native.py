@@ -82,6 +82,7 @@ EXPORTS = [
     "escha_rotary_append",
     "escha_chunk_attention_workspace",
     "escha_chunk_attention",
+    "escha_debug_set_chunk_order",
     "escha_adjust_logits",
     "int8_w8a16_workspace",
     "int8_w8a16_matvec",
@@ -249,6 +250,8 @@ def lib() -> ctypes.CDLL:
         L.escha_chunk_attention_workspace.restype = _sz
         L.escha_chunk_attention.argtypes = [_vp, _vp, _vp, _i, _vp, _vp, _vp] + [_i] * 9 + [_f, _vp, _vp, _vp, _sz, _vp]
         L.escha_chunk_attention.restype = _i
+        L.escha_debug_set_chunk_order.argtypes = [_i]
+        L.escha_debug_set_chunk_order.restype = _i
         L.escha_adjust_logits.argtypes = [_vp, _vp, _i, _i, _i, _ll, _ll, _vp, _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp,
                                           _vp, _i, _vp, _i, _vp, _vp]
         L.escha_adjust_logits.restype = _i
@@ -285,6 +288,12 @@ def set_cluster_wait(poll_limit_log2: int = 24, skip_arrive: bool = False) -> No
     polls), and the test hook that keeps ranks != 0 from storing or arriving
     so that rank 0's wait runs out."""
     check(lib().escha_debug_set_cluster_wait(int(poll_limit_log2), int(bool(skip_arrive))))
+
+
+def set_chunk_order(backwards: bool = False) -> None:
+    """Diagnostic: chunk_attention's whole units from the last one on, so that
+    a CTA takes over units that lie before those it had."""
+    check(lib().escha_debug_set_chunk_order(int(bool(backwards))))
 
 
 class EschaError(RuntimeError):

@@ -681,6 +681,10 @@ int escha_chunk_attention(const void* q, const void* k_pool, const void* v_pool,
                           const int32_t* at, const int32_t* lens, int n, int T, int Hq, int Hkv, int d, int page,
                           int n_pages, int max_pages, int max_len, float scale, void* out, float* lse, void* ws,
                           size_t ws_bytes, void* stream);
+/* For tests: backwards = 1 gives whole units to the CTAs from the last one on, so that a CTA takes over units that lie
+ * before those it had (0, the default: from the first one on). The outputs are the same bits. Process-wide, read when a
+ * call is enqueued; ESCHA_E_ARG for other values. */
+int escha_debug_set_chunk_order(int backwards);
 
 /* ---- penalties, biases and masks on logits ----------------------------------
  * What stands between the head and the choice of a token (or

@@ -146,3 +146,9 @@ def test_scalings():
                dict(rot=32, frequencies=[1.0] * 16, scaling={"type": "linear", "factor": 2})):
         with pytest.raises(ValueError):
             native.Rotary(**kw, device="cpu")
+
+
+def test_chunk_order_is_0_or_1():
+    native, L = _lib()
+    assert L.escha_debug_set_chunk_order(2) == native.ESCHA_E_ARG and L.escha_debug_set_chunk_order(-1) == native.ESCHA_E_ARG
+    assert L.escha_debug_set_chunk_order(1) == 0 and L.escha_debug_set_chunk_order(0) == 0

@@ -447,3 +447,28 @@ def test_short_sequences_keep_their_values_that_are_not_finite(dtype, Hq, Hkv, d
     odd = torch.from_numpy(nan | plus | minus).cuda()
     assert torch.equal(out[~odd], want[~odd]) and torch.equal(lse, want_lse)
     check(clean, want, want_lse, d ** -0.5, dtype)
+
+
+@pytest.mark.parametrize("dtype,n,longest,Hq,Hkv,d,page", [("f16", 300, 6, 8, 2, 64, 16), ("bf16", 400, 3, 4, 4, 128, 17), ("f16", 200, 60, 16, 2, 256, 64)])
+def test_units_are_taken_over_in_any_order(dtype, n, longest, Hq, Hkv, d, page):
+    """Whole units of many sequences, handed out from the first or from the last one on: every row is written, with the same bits."""
+    native = _native()
+    rng = np.random.default_rng(52)
+    new = rng.integers(0, longest + 1, n)
+    new[rng.integers(0, n, n // 10)] = 0
+    new[40:90] = 0  # more than 32 in a row that have none
+    c = make(53, new.tolist(), rng.integers(0, 200, n).tolist(), Hq, Hkv, d, page, dtype, pad=2)
+    assert native.lib().escha_chunk_attention_workspace(n, int(new.sum()) + 2, Hq, Hkv, d, 512) == 0  # (whole units)
+    got = []
+    for backwards in (False, True):
+        native.set_chunk_order(backwards)
+        try:
+            out, lse = torch.full_like(c["q"], 7.0), torch.full(c["q"].shape[:2], 7.0, device="cuda")
+            native.chunk_attention(*args(c), max_len=512, out=out, lse=lse)
+            torch.cuda.synchronize()
+        finally:
+            native.set_chunk_order()
+        assert bool((out[-2:] == 7).all()) and bool((lse[-2:] == 7).all())
+        got.append((out, lse))
+    check(c, *got[0], d ** -0.5, dtype)
+    assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])

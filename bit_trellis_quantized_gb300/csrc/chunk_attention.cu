@@ -38,7 +38,8 @@
 // step of each weight; the sums and lse are of the unrounded ones): two parts
 // as in the decode kernel would cost the products half as much again. fp16 ones are
 // of the weight times 2^kUp, so that keys at 2^-25 of the largest weight keep
-// all but their last bit (steps below 2^-14 are 2^-24).
+// all but their last bit (steps below 2^-14 are 2^-24); bf16 ones times 2^-kTau, so that none is above 1 and sums of large
+// values end as f32 does.
 //
 // Bound: the products; a tile of 128 rows and keys of 256 values takes 1.37 us,
 // 1.86 PFLOP/s (97% of cuBLAS's measured burst), while tiles follow each other. Around them: 6 us a unit, and
@@ -63,9 +64,9 @@ namespace {
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kLn2 = 0.6931471805599453f;
 template <int DT>
-constexpr float kTau = DT == 1 ? 4.f : 8.f;  // P is at most 2^(kTau + kUp): 2^15 in fp16
+constexpr float kTau = DT == 1 ? 4.f : 8.f;  // P is at most 2^(kTau + kUp): 2^15 in fp16, 1 in bf16
 template <int DT>
-constexpr float kUp = DT == 1 ? 11.f : 0.f;
+constexpr float kUp = DT == 1 ? 11.f : -kTau<DT>;
 
 constexpr int kKeys = 128;  // of a tile
 template <int D>

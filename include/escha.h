@@ -671,7 +671,8 @@ int escha_rotary_append(const void* q, const void* k, const void* v, int src_dty
  * a sequence's pages hold behind its last token or the bound does not count, whatever
  * it is, and what a token's successors hold does not either: a NaN or an infinity
  * shows in the tokens that attend it (heads of its key, values of its place). Weights
- * are rounded once to dtype for the second product; sums are f32. Results are
+ * are rounded once to dtype for the second product; sums are f32, and infinite where
+ * sum_j e^(x_j - m) |V_j| passes f32's range. Results are
  * repeatable bit for bit. out, lse and ws must not overlap the inputs. n <= 65535, T Hq d below 2^40,
  * T Hq / Hkv below 2^31 - 65535. A wait between the kernel's warps that gives up (after seconds; none is known to)
  * leaves NaN in the rows in work.

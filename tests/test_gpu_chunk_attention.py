@@ -472,3 +472,21 @@ def test_units_are_taken_over_in_any_order(dtype, n, longest, Hq, Hkv, d, page):
         got.append((out, lse))
     check(c, *got[0], d ** -0.5, dtype)
     assert torch.equal(got[0][0], got[1][0]) and torch.equal(got[0][1], got[1][1])
+
+
+@pytest.mark.parametrize("d,old", [(64, 200), (128, 200), (256, 200), (256, 9000)])
+def test_large_values_behind_a_slowly_rising_maximum(d, old):
+    """bf16 values near the type's largest, where the scores' maximum rises by 5.8 powers of two from a tile to a later one: the weights
+    of what is summed stay at 1 or below, so the sums of two such values with weights 1 and e^-4 stay finite (1.02 * 2e38)."""
+    native = _native()
+    c = make(55, [6, 40], [old, 150], 4, 2, d, 16, "bf16", poison=False)
+    c["q"][:] = 0
+    c["q"][:, :, 0] = 1
+    c["k"][..., 0] = -100
+    for s in range(2):
+        for j, x in ((3, 0.0), (140, 4.0)):
+            pg = int(c["table"][s, j // 16])
+            c["k"][pg, :, j % 16, 0], c["v"][pg, :, j % 16] = x, 2e38
+    out, lse = native.chunk_attention(*args(c), scale=1.0)
+    assert bool(out.isfinite().all())
+    check(c, out, lse, 1.0, "bf16")

@@ -9,9 +9,13 @@
 //
 // A CTA takes 8192 tokens of a row and holds a word for each of them in shared
 // memory: how often the row's ids name it, and whether they do at all, as
-// whole-number sums, which come out alike in any order. beside a list of those
+// whole-number sums, which come out alike in any order, beside a list of those
 // that have one. One pass over the slice bans and copies, then each listed token
-// gets what is its own, a thread a token.
+// gets what is its own, a thread a token. The biases of a slice are listed, and
+// looked through by the tokens that have one; where they are more than 32, after
+// the list is put in the order of their places; more than 512 are taken from the
+// row's list 512 places at a time, in order. So a list of any length takes a time
+// in proportion to it (152064 biases of as many tokens: 0.77 ms).
 //
 // Bound: the write of the banned and the changed logits, and the read of those
 // next to them. Slices of 32 KB let three CTAs share a multiprocessor, so that
@@ -32,7 +36,8 @@ namespace {
 
 constexpr int kAlThreads = 512;
 constexpr int kAlSlice = 8192;  // tokens of a CTA at most
-constexpr int kAlList = 512;    // biases of a slice in shared memory
+constexpr int kAlList = kAlThreads;  // biases that are taken at once, one a thread
+constexpr int kAlFew = 32;            // up to so many of a slice, the list is searched as it is
 constexpr uint32_t kAlPrompt = 1u << 30, kAlBias = 1u << 31;  // the rest counts
 
 template <int DT>
@@ -66,8 +71,9 @@ __global__ void __launch_bounds__(kAlThreads, 3) adjust_logits_kernel(AdjustArgs
     constexpr int kN = A::kN, kEach = kAlSlice / (kAlThreads * kN);  // groups of a thread
     __shared__ __align__(16) uint32_t words[kAlSlice];
     __shared__ uint32_t masks[kAlSlice / 32 + 2];
-    __shared__ uint16_t touched[kAlSlice];                                    // tokens with a word, in any order
-    __shared__ int touched_n, list_n, list_at[kAlList], list_token[kAlList];  // biases: their places and tokens of the slice
+    __shared__ uint16_t touched[kAlSlice];  // tokens with a word, in any order
+    __shared__ int touched_n, list_n[2];
+    __shared__ int list_at[kAlList], list_token[kAlList];  // biases of the slice: their places (values, once they are in order) and tokens
     pdl_wait();
     pdl_trigger();
     const int t = threadIdx.x, row = blockIdx.x / slices;
@@ -93,7 +99,7 @@ __global__ void __launch_bounds__(kAlThreads, 3) adjust_logits_kernel(AdjustArgs
         for (int k = 0; k < kFirst; ++k) first[k] = i0 + k * kAlThreads + t < i1 ? a.ids[i0 + k * kAlThreads + t] : -1;
 #pragma unroll
         for (int i = 0; i < kAlSlice / (kAlThreads * 4); ++i) *reinterpret_cast<uint4*>(words + (i * kAlThreads + t) * 4) = make_uint4(0, 0, 0, 0);
-        if (t == 0) list_n = touched_n = 0;
+        if (t == 0) list_n[0] = list_n[1] = touched_n = 0;
     }
     __syncthreads();
     // ---- what is banned, and the copy. Where all groups are whole and begin at a multiple of 32 tokens, a word of the mask
@@ -125,10 +131,23 @@ __global__ void __launch_bounds__(kAlThreads, 3) adjust_logits_kernel(AdjustArgs
             const uint32_t w = static_cast<uint32_t>(id) - static_cast<uint32_t>(base);
             if (static_cast<unsigned>(id) >= static_cast<unsigned>(a.V) || w >= kAlSlice) continue;
             if (atomicOr(&words[w], kAlBias) == 0) touched[atomicAdd(&touched_n, 1)] = static_cast<uint16_t>(w);
-            const int at = atomicAdd(&list_n, 1);
+            const int at = atomicAdd(&list_n[0], 1);
             if (at < kAlList) list_at[at] = i, list_token[at] = static_cast<int>(w);
         }
     }
+    // the n listed biases in the order of their places, a thread each
+    auto order = [&](int n) {
+        int rank = 0, token = 0;
+        float value = 0.f;
+        if (t < n) {
+            const int at = list_at[t];
+            token = list_token[t], value = a.bias[at];
+            for (int k = 0; k < n; ++k) rank += list_at[k] < at;
+        }
+        __syncthreads();
+        if (t < n) list_at[rank] = __float_as_int(value), list_token[rank] = token;
+        __syncthreads();
+    };
     // the allowed ones of a group's tokens, a bit each, and those that there are
     auto bits = [&](int g0) {
         const int lo = g0 < 0 ? -g0 : 0, hi = min(max(a.V - g0, 0), kN);
@@ -179,9 +198,15 @@ __global__ void __launch_bounds__(kAlThreads, 3) adjust_logits_kernel(AdjustArgs
     }
     if (!counts) return;
     __syncthreads();
-    // ---- the touched ones
+    // ---- the touched ones. More biases than a list holds are added to the tokens' values, which wait in their words.
     const float rep = a.repetition ? a.repetition[row] : 1.f, freq = a.frequency ? a.frequency[row] : 0.f;
     const float pres = a.presence ? a.presence[row] : 0.f;
+    const int biases = list_n[0];
+    const bool many = biases > kAlList;
+    constexpr uint16_t kWaits = 0x8000;
+    static_assert(kAlSlice <= kWaits, "a bit beside the token");
+    // (in order takes a barrier more: 256 x 152064, 0 to 50 biases a row, 66.3 us as it is, 68.6 in order)
+    if (biases > kAlFew && !many) order(biases);
 #pragma unroll 1
     for (int i = t; i < touched_n; i += kAlThreads) {
         const int w = touched[i];
@@ -194,22 +219,48 @@ __global__ void __launch_bounds__(kAlThreads, 3) adjust_logits_kernel(AdjustArgs
         if (n & ~kAlBias) z = z > 0.f ? __fdiv_rn(z, rep) : __fmul_rn(z, rep);
         if (c) z = __fsub_rn(z, __fadd_rn(__fmul_rn(freq, static_cast<float>(c)), pres));
         if (n & kAlBias) {
-            if (list_n <= kAlList) {  // in the order of their places
+            if (many) {
+                words[w] = __float_as_uint(z), touched[i] = static_cast<uint16_t>(w | kWaits);
+                continue;
+            }
+            if (biases > kAlFew) {
+                for (int k = 0; k < biases; ++k)
+                    if (list_token[k] == w) z = __fadd_rn(z, __int_as_float(list_at[k]));
+            } else {  // the next place, again and again
                 for (int last = -1;;) {
                     int next = INT_MAX;
-                    for (int k = 0; k < list_n; ++k)
+                    for (int k = 0; k < biases; ++k)
                         if (list_token[k] == w && list_at[k] > last) next = min(next, list_at[k]);
                     if (next == INT_MAX) break;
                     z = __fadd_rn(z, a.bias[next]);
                     last = next;
                 }
-            } else {
-                for (int k = b0; k < b1; ++k)
-                    if (a.bias_ids[k] == base + w) z = __fadd_rn(z, a.bias[k]);
             }
         }
         y[base + w] = A::put(z);
     }
+    if (!many) return;
+    // a thread a place, then a thread every kAlThreads-th token
+    for (int b = b0, p = 1; b < b1; b += kAlThreads, p ^= 1) {
+        const int i = b + t, id = i < b1 ? a.bias_ids[i] : -1;
+        const uint32_t w = static_cast<uint32_t>(id) - static_cast<uint32_t>(base);
+        if (static_cast<unsigned>(id) < static_cast<unsigned>(a.V) && w < kAlSlice) {
+            const int at = atomicAdd(&list_n[p], 1);
+            list_at[at] = i, list_token[at] = static_cast<int>(w);
+        }
+        __syncthreads();
+        const int n = list_n[p];
+        if (t == 0) list_n[p ^ 1] = 0;  // (of the next places, which are counted behind the next barriers)
+        order(n);
+        for (int k = 0; k < n; ++k) {
+            const int of = list_token[k];
+            if (of % kAlThreads == t) words[of] = __float_as_uint(__fadd_rn(__uint_as_float(words[of]), __int_as_float(list_at[k])));
+        }
+        __syncthreads();
+    }
+#pragma unroll 1
+    for (int i = t; i < touched_n; i += kAlThreads)
+        if (touched[i] & kWaits) y[base + (touched[i] & ~kWaits)] = A::put(__uint_as_float(words[touched[i] & ~kWaits]));
 }
 
 template <int DT>

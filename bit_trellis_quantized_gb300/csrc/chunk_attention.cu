@@ -187,15 +187,16 @@ struct CaRing {
 struct CaBars {
     unsigned long long s_full[2], p_full[2], pv_done[2], o_full[2], o_empty[2], q_full, q_empty, unit_full[2], unit_empty[2], want, stolen, end;
     uint32_t tmem;
-    int bad;
+    int bad, polls;
     CaUnit unit[2];
     __align__(16) uint32_t masks[kMasks][4];  // of a tile's keys, which are there
     uint32_t odd[kOdd][4][4], any_odd[kOdd];  // of a unit's last tiles, keys whose values are not all finite
 };
 
 // A wait that gives up after so many polls of 4 us at most, or once another has: the CTA then runs on to its end and the
-// rows in work become NaN. Waits are for a tile's work (2^19 polls, two seconds), or for a unit's (2^26): one of 2^30 keys
-// takes ten seconds.
+// rows in work become NaN. Waits are for a tile's work (ChunkAttnArgs::polls, 2^19: two seconds), or for a unit's (2^7 times
+// as many): one of 2^30 keys takes ten seconds. After such a wait no warp arrives at a barrier of loads that count their bytes:
+// where one is on its way, an arrival that is not due takes the count below 0, which is a fault.
 __device__ __forceinline__ bool ca_bad(CaBars& b) { return *reinterpret_cast<volatile int*>(&b.bad) != 0; }
 __device__ __forceinline__ bool ca_any_bad(CaBars& b) { return __any_sync(0xffffffffu, ca_bad(b)); }  // (of a warp together)
 __device__ __forceinline__ void ca_wait_long(CaBars& b, uint32_t at, uint32_t parity, int polls) {
@@ -204,16 +205,15 @@ __device__ __forceinline__ void ca_wait_long(CaBars& b, uint32_t at, uint32_t pa
         if (tc::mbar_test_parity(at, parity) || ca_bad(b)) return;
     *reinterpret_cast<volatile int*>(&b.bad) = 1;
 }
-__device__ __forceinline__ void ca_wait(CaBars& b, unsigned long long* bar, uint32_t parity, int polls = 1 << 19) {
+__device__ __forceinline__ void ca_wait(CaBars& b, unsigned long long* bar, uint32_t parity, bool unit = false) {
     const uint32_t at = tc::smem_addr(bar);
-    if (!tc::mbar_test_parity(at, parity)) ca_wait_long(b, at, parity, polls);
+    if (!tc::mbar_test_parity(at, parity)) ca_wait_long(b, at, parity, b.polls << (unit ? 7 : 0));
 }
-constexpr int kUnitPolls = 1 << 26;
 __device__ __forceinline__ void ca_arrive(unsigned long long* bar) { tc::mbar_arrive_cta(tc::smem_addr(bar)); }
 
 // The next unit (the k-th), false: none. Every warp that works on units calls it once a unit.
 __device__ __forceinline__ bool ca_next(CaBars& b, uint32_t k, int lane, CaUnit& u) {
-    ca_wait(b, &b.unit_full[k & 1], (k >> 1) & 1, kUnitPolls);
+    ca_wait(b, &b.unit_full[k & 1], (k >> 1) & 1, true);
     u = b.unit[k & 1];
     __syncwarp();
     if (lane == 0) ca_arrive(&b.unit_empty[k & 1]);
@@ -239,7 +239,7 @@ __device__ __forceinline__ void ca_units(const CaArgs& c, CaBars& b, CaList& lis
     const int lane = threadIdx.x & 31, most = kNQ * c.span;
     uint32_t k = 0;
     auto give = [&](const CaSeq& q, int s, int run, int kvh, int tile0, int tiles, int keys) {
-        ca_wait(b, &b.unit_empty[k & 1], ((k >> 1) - 1) & 1, kUnitPolls);
+        ca_wait(b, &b.unit_empty[k & 1], ((k >> 1) - 1) & 1, true);
         if (lane == 0) {
             b.unit[k & 1] = CaUnit{s, kvh, run * most, min(most, q.tokens - run * most), q.first, q.pos, tile0, tiles, keys, tiles == ca_tiles(keys)};
             ca_arrive(&b.unit_full[k & 1]);
@@ -247,7 +247,7 @@ __device__ __forceinline__ void ca_units(const CaArgs& c, CaBars& b, CaList& lis
         ++k;
     };
     auto stop = [&]() {
-        ca_wait(b, &b.unit_empty[k & 1], ((k >> 1) - 1) & 1, kUnitPolls);
+        ca_wait(b, &b.unit_empty[k & 1], ((k >> 1) - 1) & 1, true);
         if (lane == 0) {
             b.unit[k & 1].tiles = 0;
             ca_arrive(&b.unit_full[k & 1]);
@@ -326,7 +326,7 @@ __device__ __forceinline__ void ca_units(const CaArgs& c, CaBars& b, CaList& lis
         const CaSeq q = mine.of(src);
         const int run = q.runs(most) - 1 - off / a.Hkv, keys = q.keys(run, most, c.cap);
         give(q, s0 + src, run, off % a.Hkv, 0, ca_tiles(keys), keys);
-        ca_wait(b, &b.want, steals & 1, kUnitPolls);
+        ca_wait(b, &b.want, steals & 1, true);
         if (ca_any_bad(b)) break;
         if (lane == 0) {
             tc::fence_proxy_async_smem();
@@ -438,7 +438,8 @@ __device__ __forceinline__ void ca_load_boxes(const CaArgs& c, CaBars& b, CaRing
     uint32_t slot = 0, tile = 0, k = 0, phases = 0;
     CaUnit u;
     for (; ca_next(b, k, lane, u); ++k) {
-        ca_wait(b, &b.q_empty, (k - 1) & 1, kUnitPolls);
+        ca_wait(b, &b.q_empty, (k - 1) & 1, true);
+        if (ca_any_bad(b)) return;
         const int partly = ca_partly(u), common = ca_common(u);
         uint32_t* odd = &b.odd[k % kOdd][0][0];
         if (w == 1) {
@@ -448,7 +449,8 @@ __device__ __forceinline__ void ca_load_boxes(const CaArgs& c, CaBars& b, CaRing
                 for (int p = 0; p < C::kParts; ++p) {
                     // (order of the slots: below)
                     const uint32_t i = slot + p + C::kParts * (C::kNQ == 1 ? min(2 * j + 2, 2 * u.tiles - 1) : 2 * j + 1), at = i % kSlots;
-                    ca_wait(b, &bars.raw[at], phases >> at & 1, kUnitPolls);
+                    ca_wait(b, &bars.raw[at], phases >> at & 1, true);
+                    if (ca_any_bad(b)) return;  // (the slot may be another load's)
                     phases ^= 1u << at;
                     // the rows that not all see and that were loaded: the rest of a box behind the last key, no further
                     const int key0 = (u.tile0 + j) * kKeys, r0 = max(common - key0, 0) & ~7, r1 = min((u.keys - key0 + c.box - 1) & -c.box, kKeys);
@@ -544,7 +546,8 @@ __device__ __forceinline__ void ca_load_rows(const CaArgs& c, CaBars& b, CaRing<
     };
     CaUnit u;
     for (; ca_next(b, k, lane, u); ++k) {
-        ca_wait(b, &b.q_empty, (k - 1) & 1, kUnitPolls);  // (nothing is in flight)
+        ca_wait(b, &b.q_empty, (k - 1) & 1, true);  // (nothing is in flight)
+        if (ca_any_bad(b)) return;
         if (w == 0 && lane < 16) b.odd[k % kOdd][lane >> 2][lane & 3] = 0;
         if (w == 0 && lane == 16) b.any_odd[k % kOdd] = 0;
         asm volatile("bar.sync 1, %0;" ::"n"(32 * C::kLoadWarps) : "memory");
@@ -644,8 +647,8 @@ __device__ __forceinline__ void ca_products(CaBars& b, CaRing<CaCfg<D>::kSlots>&
         if (lead) tc::commit(tc::smem_addr(bar));
         __syncwarp();
     };
-    auto wait = [&](unsigned long long* bar, uint32_t parity, int polls = 1 << 19) {
-        ca_wait(b, bar, parity, polls);
+    auto wait = [&](unsigned long long* bar, uint32_t parity, bool unit = false) {
+        ca_wait(b, bar, parity, unit);
         __syncwarp();
         tc::fence_after_sync();
     };
@@ -694,7 +697,7 @@ __device__ __forceinline__ void ca_products(CaBars& b, CaRing<CaCfg<D>::kSlots>&
         for (int p = 0; p < kParts; ++p) next = after(next, round);
     };
     while (true) {
-        wait(&b.unit_full[k & 1], (k >> 1) & 1, kUnitPolls);
+        wait(&b.unit_full[k & 1], (k >> 1) & 1, true);
         const int tiles = __shfl_sync(0xffffffffu, b.unit[k & 1].tiles, 0), nq = kNQ == 2 && __shfl_sync(0xffffffffu, b.unit[k & 1].toks, 0) > span ? 2 : 1;
         if (lead) ca_arrive(&b.unit_empty[k & 1]);
         if (tiles <= 0 || ca_any_bad(b)) break;
@@ -941,7 +944,7 @@ __global__ void __launch_bounds__(CaCfg<D>::kThreads, 1) chunk_attention_kernel(
             init(&b.unit_full[i], 1), init(&b.unit_empty[i], C::kSoftWarps + C::kLoadWarps + 1);
         }
         init(&b.q_full, 1), init(&b.q_empty, 1), init(&b.want, 1), init(&b.stolen, 1), init(&b.end, 1);
-        b.bad = 0;
+        b.bad = 0, b.polls = c.a.polls;
         tc::fence_proxy_async_smem();
     }
     if (warp == C::kMmaWarp) {

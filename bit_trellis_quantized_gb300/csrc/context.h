@@ -90,6 +90,7 @@ struct ChunkAttnArgs {
     int n, T, Hq, Hkv, d, page, n_pages, max_pages, max_len;
     float scale;
     int backwards;  // CTA i has the i-th unit from the last one on (tests)
+    int polls;      // after which a wait for a tile's work gives up
 };
 size_t chunk_attention_ws_bytes(int n, int T, int Hq, int Hkv, int d, int max_len);
 cudaError_t launch_chunk_attention(const ChunkAttnArgs& a, int dtype, void* ws, cudaStream_t s);

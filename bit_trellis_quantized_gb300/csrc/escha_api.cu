@@ -91,6 +91,8 @@ std::atomic<int> g_fz_skip_publish{0};
 std::atomic<int> g_mbar_limit_log2{24};
 std::atomic<int> g_skip_cluster_arrive{0};
 std::atomic<int> g_chunk_backwards{0};
+constexpr int kChunkPolls = 1 << 19;
+std::atomic<int> g_chunk_polls{kChunkPolls};
 
 int check_trellis(const uint16_t* codes, int in, int out, int K, int mult, const char* name) {
     if (!codes) return fail(ESCHA_E_ARG, "%s: codes is null", name);
@@ -1465,6 +1467,13 @@ int escha_debug_set_chunk_order(int backwards) {
     return ESCHA_OK;
 }
 
+int escha_debug_set_chunk_wait(int polls) {
+    if (polls < 0 || polls > kChunkPolls)
+        return fail(ESCHA_E_ARG, "debug_set_chunk_wait: polls=%d not in 0..%d", polls, kChunkPolls);
+    g_chunk_polls.store(polls);
+    return ESCHA_OK;
+}
+
 size_t escha_chunk_attention_workspace(int n, int T, int Hq, int Hkv, int d, int max_len) {
     if (check_chunk_shape(n, T, Hq, Hkv, d, max_len, "chunk_attention_workspace")) return 0;
     return escha::chunk_attention_ws_bytes(n, T, Hq, Hkv, d, max_len);
@@ -1488,7 +1497,7 @@ int escha_chunk_attention(const void* q, const void* k_pool, const void* v_pool,
     int sms;
     if ((r = device_check(&sms))) return r;
     const escha::ChunkAttnArgs a{q, k_pool, v_pool, table, at,      lens,      out,     lse,  n, T,
-                                 Hq, Hkv,   d,      page,  n_pages, max_pages, max_len, scale, g_chunk_backwards.load()};
+                                 Hq, Hkv,   d,      page,  n_pages, max_pages, max_len, scale, g_chunk_backwards.load(), g_chunk_polls.load()};
     return cuda_status(escha::launch_chunk_attention(a, dtype, ws, static_cast<cudaStream_t>(stream)),
                        "chunk_attention launch");
 }

@@ -83,6 +83,7 @@ EXPORTS = [
     "escha_chunk_attention_workspace",
     "escha_chunk_attention",
     "escha_debug_set_chunk_order",
+    "escha_debug_set_chunk_wait",
     "escha_adjust_logits",
     "int8_w8a16_workspace",
     "int8_w8a16_matvec",
@@ -252,6 +253,8 @@ def lib() -> ctypes.CDLL:
         L.escha_chunk_attention.restype = _i
         L.escha_debug_set_chunk_order.argtypes = [_i]
         L.escha_debug_set_chunk_order.restype = _i
+        L.escha_debug_set_chunk_wait.argtypes = [_i]
+        L.escha_debug_set_chunk_wait.restype = _i
         L.escha_adjust_logits.argtypes = [_vp, _vp, _i, _i, _i, _ll, _ll, _vp, _vp, _i, _vp, _vp, _vp, _vp, _vp, _vp,
                                           _vp, _i, _vp, _i, _vp, _vp]
         L.escha_adjust_logits.restype = _i
@@ -294,6 +297,12 @@ def set_chunk_order(backwards: bool = False) -> None:
     """Diagnostic: chunk_attention's whole units from the last one on, so that
     a CTA takes over units that lie before those it had."""
     check(lib().escha_debug_set_chunk_order(int(bool(backwards))))
+
+
+def set_chunk_wait(polls: int = 1 << 19) -> None:
+    """Diagnostic: the polls after which chunk_attention's waits between the
+    warps of a CTA give up."""
+    check(lib().escha_debug_set_chunk_wait(int(polls)))
 
 
 class EschaError(RuntimeError):

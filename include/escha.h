@@ -686,6 +686,10 @@ int escha_chunk_attention(const void* q, const void* k_pool, const void* v_pool,
  * before those it had (0, the default: from the first one on). The outputs are the same bits. Process-wide, read when a
  * call is enqueued; ESCHA_E_ARG for other values. */
 int escha_debug_set_chunk_order(int backwards);
+/* For tests: the polls (of 4 us at most) after which a wait for a tile's work gives up, 0..2^19 (the default), and 2^7
+ * times as many for a unit's; so few that waits run out in an ordinary call, which then ends early. Process-wide, read
+ * when a call is enqueued; ESCHA_E_ARG for other values. */
+int escha_debug_set_chunk_wait(int polls);
 
 /* ---- penalties, biases and masks on logits ----------------------------------
  * What stands between the head and the choice of a token (or

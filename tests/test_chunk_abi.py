@@ -152,3 +152,9 @@ def test_chunk_order_is_0_or_1():
     native, L = _lib()
     assert L.escha_debug_set_chunk_order(2) == native.ESCHA_E_ARG and L.escha_debug_set_chunk_order(-1) == native.ESCHA_E_ARG
     assert L.escha_debug_set_chunk_order(1) == 0 and L.escha_debug_set_chunk_order(0) == 0
+
+
+def test_chunk_wait_is_bounded():
+    native, L = _lib()
+    assert L.escha_debug_set_chunk_wait(-1) == native.ESCHA_E_ARG and L.escha_debug_set_chunk_wait((1 << 19) + 1) == native.ESCHA_E_ARG
+    assert L.escha_debug_set_chunk_wait(0) == 0 and L.escha_debug_set_chunk_wait(1 << 19) == 0

@@ -1,4 +1,6 @@
 """GPU checks of escha_chunk_attention against its formula in 64 bits."""
+import time
+
 import numpy as np
 import pytest
 
@@ -490,3 +492,28 @@ def test_large_values_behind_a_slowly_rising_maximum(d, old):
     out, lse = native.chunk_attention(*args(c), scale=1.0)
     assert bool(out.isfinite().all())
     check(c, out, lse, 1.0, "bf16")
+
+
+GIVE_UP = [("f16", [3] * 200, [(i * 37) % 400 for i in range(200)], 8, 2, 64, 1024), ("bf16", [4, 30], [9000, 700], 16, 2, 256, None),
+           ("bf16", [700, 2, 40], [100, 3000, 0], 12, 4, 128, None), ("f16", [900], [300], 16, 2, 256, 1200)]
+
+
+@pytest.mark.parametrize("dtype,new,old,Hq,Hkv,d,max_len", GIVE_UP)
+@pytest.mark.parametrize("page", [16])
+def test_a_call_whose_waits_give_up_ends(dtype, new, old, Hq, Hkv, d, max_len, page):
+    """Waits between the warps that run out after a few polls: the call ends, and the next one is right."""
+    native = _native()
+    c = make(54, new, old, Hq, Hkv, d, page, dtype, poison=False)
+    want, want_lse = native.chunk_attention(*args(c), max_len=max_len)
+    torch.cuda.synchronize()
+    for polls in (0, 1, 3, 10, 40):
+        native.set_chunk_wait(polls)
+        try:
+            began = time.time()
+            native.chunk_attention(*args(c), max_len=max_len)
+            torch.cuda.synchronize()
+            assert time.time() - began < 5
+        finally:
+            native.set_chunk_wait()
+        out, lse = native.chunk_attention(*args(c), max_len=max_len)
+        assert torch.equal(out, want) and torch.equal(lse, want_lse)

@@ -185,7 +185,7 @@ struct CaRing {
     unsigned long long full[kSlots], empty[kSlots], raw[kSlots];
 };
 struct CaBars {
-    unsigned long long s_full[2], p_full[2], pv_done[2], o_full[2], o_empty[2], q_full, q_empty, unit_full[2], unit_empty[2], want, stolen, end;
+    unsigned long long s_full[2], p_full[2], pv_done[2], o_full[2], o_empty[2], q_full, q_empty, unit_full[2], unit_empty[2], want, stolen, cleared, end;
     uint32_t tmem;
     int bad, polls;
     CaUnit unit[2];
@@ -195,8 +195,9 @@ struct CaBars {
 
 // A wait that gives up after so many polls of 4 us at most, or once another has: the CTA then runs on to its end and the
 // rows in work become NaN. Waits are for a tile's work (ChunkAttnArgs::polls, 2^19: two seconds), or for a unit's (2^7 times
-// as many): one of 2^30 keys takes ten seconds. After such a wait no warp arrives at a barrier of loads that count their bytes:
-// where one is on its way, an arrival that is not due takes the count below 0, which is a fault.
+// as many): one of 2^30 keys takes ten seconds. No warp waits for another in any other way until the CTA's last barrier.
+// After such a wait no warp arrives at a barrier of loads that count their bytes: where one is on its way, an arrival that
+// is not due takes the count below 0, which is a fault.
 __device__ __forceinline__ bool ca_bad(CaBars& b) { return *reinterpret_cast<volatile int*>(&b.bad) != 0; }
 __device__ __forceinline__ bool ca_any_bad(CaBars& b) { return __any_sync(0xffffffffu, ca_bad(b)); }  // (of a warp together)
 __device__ __forceinline__ void ca_wait_long(CaBars& b, uint32_t at, uint32_t parity, int polls) {
@@ -550,8 +551,13 @@ __device__ __forceinline__ void ca_load_rows(const CaArgs& c, CaBars& b, CaRing<
         if (ca_any_bad(b)) return;
         if (w == 0 && lane < 16) b.odd[k % kOdd][lane >> 2][lane & 3] = 0;
         if (w == 0 && lane == 16) b.any_odd[k % kOdd] = 0;
-        asm volatile("bar.sync 1, %0;" ::"n"(32 * C::kLoadWarps) : "memory");
-        if (w == 0) ca_queries<D>(c, b, u, q_smem);
+        __syncwarp();
+        if (w == 0) {
+            if (lane == 0) ca_arrive(&b.cleared);
+            ca_queries<D>(c, b, u, q_smem);
+        } else {  // (the first warp clears for unit k + 1 once the scores of unit k, with this warp's keys, are done)
+            ca_wait(b, &b.cleared, k & 1, true);
+        }
         const int32_t* table = a.table + static_cast<long long>(u.s) * a.max_pages;
         // lane r's rows 64 w + r and 64 w + 32 + r of tile j: their numbers in the pools (-1: not there)
         auto find = [&](int j, int (&row)[2]) {
@@ -943,7 +949,7 @@ __global__ void __launch_bounds__(CaCfg<D>::kThreads, 1) chunk_attention_kernel(
             init(&b.s_full[i], 1), init(&b.p_full[i], 4), init(&b.pv_done[i], 1), init(&b.o_full[i], 1), init(&b.o_empty[i], 4);
             init(&b.unit_full[i], 1), init(&b.unit_empty[i], C::kSoftWarps + C::kLoadWarps + 1);
         }
-        init(&b.q_full, 1), init(&b.q_empty, 1), init(&b.want, 1), init(&b.stolen, 1), init(&b.end, 1);
+        init(&b.q_full, 1), init(&b.q_empty, 1), init(&b.want, 1), init(&b.stolen, 1), init(&b.cleared, 1), init(&b.end, 1);
         b.bad = 0, b.polls = c.a.polls;
         tc::fence_proxy_async_smem();
     }

@@ -499,7 +499,7 @@ GIVE_UP = [("f16", [3] * 200, [(i * 37) % 400 for i in range(200)], 8, 2, 64, 10
 
 
 @pytest.mark.parametrize("dtype,new,old,Hq,Hkv,d,max_len", GIVE_UP)
-@pytest.mark.parametrize("page", [16])
+@pytest.mark.parametrize("page", [16, 17])
 def test_a_call_whose_waits_give_up_ends(dtype, new, old, Hq, Hkv, d, max_len, page):
     """Waits between the warps that run out after a few polls: the call ends, and the next one is right."""
     native = _native()

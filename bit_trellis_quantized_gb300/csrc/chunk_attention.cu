@@ -172,12 +172,17 @@ __device__ __forceinline__ int ca_tiles(int keys) { return max(1, (keys + kKeys 
 // k leave (a short unit's scores end before them). Unit k + 3 is handed out when all warps have taken unit k + 1, so are done with k.
 constexpr int kOdd = 3;
 
+constexpr int kUnits = 4;
+
 // What a CTA works on next, handed to all its warps.
 struct CaUnit {
     int s, kvh, tok0, toks;  // its tokens, of the sequence's
     int first, pos;          // the sequence's first token in q, its position
     int tile0, tiles, keys;  // tiles 0: no more units
     int whole;
+    __device__ __forceinline__ CaUnit() {}
+    __device__ __forceinline__ CaUnit(const CaSeq& q, int s, int run, int most, int kvh, int tile0, int tiles, int keys)
+        : s(s), kvh(kvh), tok0(run * most), toks(min(most, q.tokens - run * most)), first(q.first), pos(q.pos), tile0(tile0), tiles(tiles), keys(keys), whole(tiles == ca_tiles(keys)) {}
 };
 // A slot has landed, is free again, has landed but is to be looked through.
 template <int kSlots>
@@ -188,13 +193,13 @@ struct CaBars {
     unsigned long long s_full[2], p_full[2], pv_done[2], o_full[2], o_empty[2], q_full, q_empty, unit_full[2], unit_empty[2], want, stolen, cleared, end;
     uint32_t tmem;
     int bad, polls;
-    CaUnit unit[2];
+    CaUnit unit[kUnits];                      // handed out two ahead at most; those before them stay for ca_spoil
     __align__(16) uint32_t masks[kMasks][4];  // of a tile's keys, which are there
     uint32_t odd[kOdd][4][4], any_odd[kOdd];  // of a unit's last tiles, keys whose values are not all finite
 };
 
-// A wait that gives up after so many polls of 4 us at most, or once another has: the CTA then runs on to its end and the
-// rows in work become NaN. Waits are for a tile's work (ChunkAttnArgs::polls, 2^19: two seconds), or for a unit's (2^7 times
+// A wait that gives up after so many polls of 4 us at most, or once another has: the CTA then runs on to its end and makes
+// NaN of what it had to do (ca_spoil). Waits are for a tile's work (ChunkAttnArgs::polls, 2^19: two seconds), or for a unit's (2^7 times
 // as many): one of 2^30 keys takes ten seconds. No warp waits for another in any other way until the CTA's last barrier.
 // After such a wait no warp arrives at a barrier of loads that count their bytes: where one is on its way, an arrival that
 // is not due takes the count below 0, which is a fault.
@@ -215,7 +220,7 @@ __device__ __forceinline__ void ca_arrive(unsigned long long* bar) { tc::mbar_ar
 // The next unit (the k-th), false: none. Every warp that works on units calls it once a unit.
 __device__ __forceinline__ bool ca_next(CaBars& b, uint32_t k, int lane, CaUnit& u) {
     ca_wait(b, &b.unit_full[k & 1], (k >> 1) & 1, true);
-    u = b.unit[k & 1];
+    u = b.unit[k % kUnits];
     __syncwarp();
     if (lane == 0) ca_arrive(&b.unit_empty[k & 1]);
     return u.tiles > 0 && !ca_any_bad(b);
@@ -231,6 +236,32 @@ __device__ __forceinline__ int ca_sum(int x) {
     return x;
 }
 
+// This CTA's range: f(unit) for each that it has tiles of. CTA i begins at place floor(i total / ctas).
+template <int kNQ, class F>
+__device__ __forceinline__ void ca_range(const CaArgs& c, const CaList& list, const F& f) {
+    const ChunkAttnArgs& a = c.a;
+    const int most = kNQ * c.span;
+    const int total = list.places * a.Hkv, ctas = min(static_cast<int>(gridDim.x), total), i = blockIdx.x;
+    if (i >= ctas) return;
+    const int each = total / ctas, rest = total % ctas;
+    int at = i * each + i * rest / ctas;
+    const int end = (i + 1) * each + (i + 1) * rest / ctas;
+    int kvh = at / list.places, off = at % list.places, e = 0, e1 = list.n;
+    while (e1 - e > 1) {
+        const int mid = (e + e1) / 2;
+        (list.first[mid] <= off ? e : e1) = mid;
+    }
+    off -= list.first[e];
+    while (at < end) {
+        const int now = min(list.first[e + 1] - list.first[e] - off, end - at), tile0 = max(off - kCaStart, 0), tiles = max(off + now - kCaStart, 0) - tile0;
+        const int s = list.unit[e] & 0xFFFFu, run = list.unit[e] >> 16;
+        const CaSeq q(a, s);
+        if (tiles > 0) f(CaUnit(q, s, run, most, kvh, tile0, tiles, q.keys(run, most, c.cap)));
+        at += now, off = 0;
+        if (++e == list.n) e = 0, ++kvh;
+    }
+}
+
 // ---- the warp that hands out units
 // kRanges: this CTA's range of all units' tiles. Else units, the longest of a sequence first: that of blockIdx, then those
 // of CTAs that have not begun yet, taken over (cancelled) one at a time when the one in work comes to its end, in any order.
@@ -239,10 +270,10 @@ __device__ __forceinline__ void ca_units(const CaArgs& c, CaBars& b, CaList& lis
     const ChunkAttnArgs& a = c.a;
     const int lane = threadIdx.x & 31, most = kNQ * c.span;
     uint32_t k = 0;
-    auto give = [&](const CaSeq& q, int s, int run, int kvh, int tile0, int tiles, int keys) {
+    auto give = [&](const CaUnit& u) {
         ca_wait(b, &b.unit_empty[k & 1], ((k >> 1) - 1) & 1, true);
         if (lane == 0) {
-            b.unit[k & 1] = CaUnit{s, kvh, run * most, min(most, q.tokens - run * most), q.first, q.pos, tile0, tiles, keys, tiles == ca_tiles(keys)};
+            b.unit[k % kUnits] = u;
             ca_arrive(&b.unit_full[k & 1]);
         }
         ++k;
@@ -250,7 +281,7 @@ __device__ __forceinline__ void ca_units(const CaArgs& c, CaBars& b, CaList& lis
     auto stop = [&]() {
         ca_wait(b, &b.unit_empty[k & 1], ((k >> 1) - 1) & 1, true);
         if (lane == 0) {
-            b.unit[k & 1].tiles = 0;
+            b.unit[k % kUnits].tiles = 0;
             ca_arrive(&b.unit_full[k & 1]);
         }
     };
@@ -279,27 +310,9 @@ __device__ __forceinline__ void ca_units(const CaArgs& c, CaBars& b, CaList& lis
         __syncwarp();
         if (blockIdx.x == 0)  // for the join
             for (int i = lane; i < static_cast<int>(sizeof(CaList) / 4); i += 32) reinterpret_cast<int*>(c.parts.list)[i] = reinterpret_cast<const int*>(&list)[i];
-        // CTA i begins at place floor(i total / ctas)
-        const int total = places * a.Hkv, ctas = min(static_cast<int>(gridDim.x), total), i = blockIdx.x;
-        if (i < ctas) {
-            const int each = total / ctas, rest = total % ctas;
-            int at = i * each + i * rest / ctas;
-            const int end = (i + 1) * each + (i + 1) * rest / ctas;
-            int kvh = at / places, off = at % places, e = 0, e1 = n;
-            while (e1 - e > 1) {
-                const int mid = (e + e1) / 2;
-                (list.first[mid] <= off ? e : e1) = mid;
-            }
-            off -= list.first[e];
-            while (at < end) {
-                const int s = list.unit[e] & 0xFFFFu, run = list.unit[e] >> 16, now = min(list.first[e + 1] - list.first[e] - off, end - at);
-                const int tile0 = max(off - kCaStart, 0), tiles = max(off + now - kCaStart, 0) - tile0;
-                const CaSeq q(a, s);
-                if (tiles > 0) give(q, s, run, kvh, tile0, tiles, q.keys(run, most, c.cap));
-                at += now, off = 0;
-                if (++e == n) e = 0, ++kvh;
-            }
-        }
+        ca_range<kNQ>(c, list, [&](const CaUnit& u) {
+            if (!ca_any_bad(b)) give(u);
+        });
         stop();
         return;
     }
@@ -326,7 +339,7 @@ __device__ __forceinline__ void ca_units(const CaArgs& c, CaBars& b, CaList& lis
         const int src = __ffs(has) - 1, off = unit - before - __shfl_sync(0xffffffffu, incl - w, src);
         const CaSeq q = mine.of(src);
         const int run = q.runs(most) - 1 - off / a.Hkv, keys = q.keys(run, most, c.cap);
-        give(q, s0 + src, run, off % a.Hkv, 0, ca_tiles(keys), keys);
+        give(CaUnit(q, s0 + src, run, most, off % a.Hkv, 0, ca_tiles(keys), keys));
         ca_wait(b, &b.want, steals & 1, true);
         if (ca_any_bad(b)) break;
         if (lane == 0) {
@@ -337,8 +350,11 @@ __device__ __forceinline__ void ca_units(const CaArgs& c, CaBars& b, CaList& lis
                          : "memory");
         }
         __syncwarp();
-        ca_wait(b, &b.stolen, steals & 1);
-        if (ca_any_bad(b)) break;
+        // (whether another wait has given up or not: a unit taken over is this CTA's)
+        if (!__all_sync(0xffffffffu, tc::mbar_wait_parity_bounded(tc::smem_addr(&b.stolen), steals & 1, 1 << 19))) {
+            *reinterpret_cast<volatile int*>(&b.bad) = 1;
+            break;
+        }
         ++steals;
         uint32_t got, id;
         asm volatile(
@@ -704,7 +720,8 @@ __device__ __forceinline__ void ca_products(CaBars& b, CaRing<CaCfg<D>::kSlots>&
     };
     while (true) {
         wait(&b.unit_full[k & 1], (k >> 1) & 1, true);
-        const int tiles = __shfl_sync(0xffffffffu, b.unit[k & 1].tiles, 0), nq = kNQ == 2 && __shfl_sync(0xffffffffu, b.unit[k & 1].toks, 0) > span ? 2 : 1;
+        const CaUnit& u = b.unit[k % kUnits];
+        const int tiles = __shfl_sync(0xffffffffu, u.tiles, 0), nq = kNQ == 2 && __shfl_sync(0xffffffffu, u.toks, 0) > span ? 2 : 1;
         if (lead) ca_arrive(&b.unit_empty[k & 1]);
         if (tiles <= 0 || ca_any_bad(b)) break;
         wait(&b.q_full, k & 1);
@@ -880,7 +897,6 @@ __device__ __forceinline__ void ca_soft(const CaArgs& c, CaBars& b, uint32_t tme
         }
         ca_wait(b, &b.o_full[q], units & 1);
         tc::fence_after_sync();
-        if (ca_bad(b)) l = NAN;
         const bool odd = *reinterpret_cast<volatile uint32_t*>(&b.any_odd[k % kOdd]) != 0;
         const long long head = static_cast<long long>(u.first + u.tok0 + tok) * a.Hq + u.kvh * group + g_head;
         const long long slot = 2ll * blockIdx.x + (u.tile0 == 0 ? 1 : 0);
@@ -931,6 +947,33 @@ __device__ __forceinline__ void ca_soft(const CaArgs& c, CaBars& b, uint32_t tme
     }
 }
 
+// After a wait that gave up (one warp): NaN in all that may not be finished or not begun: whole units, of those handed out
+// the last ones (a finished one may be among them); ranges, all of this CTA's.
+template <int D, bool kRanges>
+__device__ __noinline__ void ca_spoil(const CaArgs& c, const CaBars& b, const CaList& list) {
+    const ChunkAttnArgs& a = c.a;
+    const int lane = threadIdx.x & 31, group = a.Hq / a.Hkv;
+    auto spoil = [&](const CaUnit& u) {
+        if (!u.whole) {
+            for (int r = lane; r < CaCfg<D>::kRows; r += 32)
+                *reinterpret_cast<float2*>(c.parts.ml + ((2ll * blockIdx.x + (u.tile0 == 0 ? 1 : 0)) * CaCfg<D>::kRows + r) * 2) = make_float2(0.f, NAN);
+            return;
+        }
+        for (int i = 0; i < u.toks * group; ++i) {
+            const int tok = c.by_group(i);
+            const long long head = static_cast<long long>(u.first + u.tok0 + tok) * a.Hq + u.kvh * group + (i - tok * group);
+            for (int x = lane; x < D / 8; x += 32) reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + head * D)[x] = make_uint4(0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu, 0x7FFF7FFFu);
+            if (lane == 0 && a.lse) a.lse[head] = NAN;
+        }
+    };
+    if (kRanges) {
+        ca_range<CaCfg<D>::kNQ>(c, list, spoil);
+    } else {
+        for (int i = 0; i < kUnits; ++i)
+            if (b.unit[i].tiles > 0) spoil(b.unit[i]);
+    }
+}
+
 template <int DT, int D, bool kRanges>
 __global__ void __launch_bounds__(CaCfg<D>::kThreads, 1) chunk_attention_kernel(const __grid_constant__ CaArgs c) {
     using C = CaCfg<D>;
@@ -951,6 +994,8 @@ __global__ void __launch_bounds__(CaCfg<D>::kThreads, 1) chunk_attention_kernel(
         }
         init(&b.q_full, 1), init(&b.q_empty, 1), init(&b.want, 1), init(&b.stolen, 1), init(&b.cleared, 1), init(&b.end, 1);
         b.bad = 0, b.polls = c.a.polls;
+#pragma unroll 1
+        for (int i = 0; i < kUnits; ++i) b.unit[i].tiles = 0;
         tc::fence_proxy_async_smem();
     }
     if (warp == C::kMmaWarp) {
@@ -984,6 +1029,7 @@ __global__ void __launch_bounds__(CaCfg<D>::kThreads, 1) chunk_attention_kernel(
     __syncthreads();
     tc::fence_after_sync();
     if (warp == C::kMmaWarp) tc::tmem_dealloc(tmem, 512);
+    if (warp == C::kUnitWarp && ca_bad(b)) ca_spoil<D, kRanges>(c, b, list);
 }
 
 // Joins the parts of the units that lie in several of the `grid` CTAs' ranges. CTA (rows, unit, key head); where the units

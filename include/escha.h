@@ -674,8 +674,8 @@ int escha_rotary_append(const void* q, const void* k, const void* v, int src_dty
  * are rounded once to dtype for the second product; sums are f32, and infinite where
  * sum_j e^(x_j - m) |V_j| passes f32's range. Results are
  * repeatable bit for bit. out, lse and ws must not overlap the inputs. n <= 65535, T Hq d below 2^40,
- * T Hq / Hkv below 2^31 - 65535. A wait between the kernel's warps that gives up (after seconds; none is known to)
- * leaves NaN in the rows in work.
+ * T Hq / Hkv below 2^31 - 65535. Where a wait between the kernel's warps gives up (after seconds; none is known to), the
+ * call ends, with NaN in all rows that are not right (and in some that were).
  * Errors as escha_paged_attention. */
 size_t escha_chunk_attention_workspace(int n, int T, int Hq, int Hkv, int d, int max_len);
 int escha_chunk_attention(const void* q, const void* k_pool, const void* v_pool, int dtype, const int32_t* table,

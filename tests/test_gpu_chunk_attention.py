@@ -517,3 +517,34 @@ def test_a_call_whose_waits_give_up_ends(dtype, new, old, Hq, Hkv, d, max_len, p
             native.set_chunk_wait()
         out, lse = native.chunk_attention(*args(c), max_len=max_len)
         assert torch.equal(out, want) and torch.equal(lse, want_lse)
+
+
+@pytest.mark.parametrize("dtype,new,old,Hq,Hkv,d,max_len", GIVE_UP)
+@pytest.mark.parametrize("page", [16, 17])
+@pytest.mark.parametrize("backwards", [False, True])
+def test_rows_are_right_or_nan_after_waits_that_gave_up(dtype, new, old, Hq, Hkv, d, max_len, page, backwards):
+    """Whatever was left undone is NaN, in whole heads and in lse, not what the buffers or the workspace held."""
+    native = _native()
+    c = make(56, new, old, Hq, Hkv, d, page, dtype, poison=False)
+    want, want_lse = native.chunk_attention(*args(c), max_len=max_len)
+    n, T, cap = len(new), sum(new), max_len or c["table"].shape[1] * page
+    ws = torch.empty(max(native.lib().escha_chunk_attention_workspace(n, T, Hq, Hkv, d, cap), 16), dtype=torch.uint8, device="cuda")
+    other = dict(c, q=torch.randn_like(c["q"]))
+    for polls in (0, 1, 2, 5, 20, 100):
+        native.chunk_attention(*args(other), max_len=max_len, ws=ws)  # parts of another call in the workspace
+        out, lse = torch.full_like(want, 7.0), torch.full_like(want_lse, 7.0)
+        native.set_chunk_wait(polls)
+        native.set_chunk_order(backwards)
+        try:
+            native.chunk_attention(*args(c), max_len=max_len, ws=ws, out=out, lse=lse)
+            torch.cuda.synchronize()
+        finally:
+            native.set_chunk_wait()
+            native.set_chunk_order()
+        nan = lse.isnan()
+        assert bool(((out == want).all(-1) | nan).all()) and bool(((lse == want_lse) | nan).all())
+        assert bool(out[nan].isnan().all())
+        if polls == 0:
+            assert bool(nan.any())
+    out, lse = native.chunk_attention(*args(c), max_len=max_len)
+    assert torch.equal(out, want) and torch.equal(lse, want_lse)

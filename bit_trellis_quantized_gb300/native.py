@@ -773,8 +773,10 @@ class Rotary:
         if kind == "linear":
             f = f / factor
         elif kind == "yarn":
-            original = float(scaling.pop("original"))
+            original = float(scaling.pop("original", 0))
             fast, slow = float(scaling.pop("beta_fast", 32.0)), float(scaling.pop("beta_slow", 1.0))
+            if not (original > 0 and fast > 0 and slow > 0):
+                raise ValueError(f"original={original}, beta_fast={fast} and beta_slow={slow} must be above 0")
             # the index whose frequency turns so many times within the original length
             at = [rot * math.log(original / (n * 2 * math.pi)) / (2 * math.log(base)) for n in (fast, slow)]
             low, high = max(math.floor(at[0]), 0), min(math.ceil(at[1]), rot - 1)

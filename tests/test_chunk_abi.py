@@ -158,3 +158,13 @@ def test_chunk_wait_is_bounded():
     native, L = _lib()
     assert L.escha_debug_set_chunk_wait(-1) == native.ESCHA_E_ARG and L.escha_debug_set_chunk_wait((1 << 19) + 1) == native.ESCHA_E_ARG
     assert L.escha_debug_set_chunk_wait(0) == 0 and L.escha_debug_set_chunk_wait(1 << 19) == 0
+
+
+def test_yarn_without_its_lengths_is_refused():
+    native, _ = _lib()
+    good = {"type": "yarn", "factor": 4, "original": 4096}
+    native.Rotary(64, scaling=good, device="cpu")
+    for bad in ({"type": "yarn", "factor": 4}, {**good, "original": 0}, {**good, "original": -1}, {**good, "beta_fast": 0},
+                {**good, "beta_slow": -1.0}, {**good, "original": math.nan}):
+        with pytest.raises(ValueError):
+            native.Rotary(64, scaling=bad, device="cpu")

@@ -22,7 +22,7 @@
 // one's counting runs beside another's pass. Measured in f32: 256 rows of 152064,
 // all under masks of one token in eight, up to 8000 ids, 65 us (the sectors that
 // it cannot do without, 259 MB with those read for their allowed tokens: 38); 61 of
-// 248320 copied, 24 us (18); one row in place 4.3 us. Slices of 4096 to 256 threads: 70 and 25 us.
+// 248320 copied, 24 us (18); one row in place 4 us. Slices of 4096 to 256 threads: 70 and 25 us.
 #include "common.cuh"
 #include "context.h"
 #include "kernels.h"
@@ -205,7 +205,8 @@ __global__ void __launch_bounds__(kAlThreads, 3) adjust_logits_kernel(AdjustArgs
     const bool many = biases > kAlList;
     constexpr uint16_t kWaits = 0x8000;
     static_assert(kAlSlice <= kWaits, "a bit beside the token");
-    // (in order takes a barrier more: 256 x 152064, 0 to 50 biases a row, 66.3 us as it is, 68.6 in order)
+    // As it is, the list is gone through once for each bias of a token: 512 of one token would be 512 x 512 steps of a thread, and are
+    // 17 us in order. In order takes barriers more: 256 x 152064, 0 to 50 biases a row, 66.3 us as it is, 68.6 in order.
     if (biases > kAlFew && !many) order(biases);
 #pragma unroll 1
     for (int i = t; i < touched_n; i += kAlThreads) {

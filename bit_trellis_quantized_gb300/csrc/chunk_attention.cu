@@ -45,7 +45,11 @@
 // 1.86 PFLOP/s (97% of cuBLAS's measured burst), while tiles follow each other. Around them: 6 us a unit, and
 // the power limit in long calls. Measured, 16 heads on 2 key heads of 256: 2048
 // tokens 36 us (0.96 PFLOP/s), 8192 tokens 390 (1.41), 2048 behind 63488
-// 1.47 ms captured (1.47), 1.74 ms in a long run (1.25); 32 heads on 8 of 128, 4096 tokens 121 (1.14).
+// 1.52 ms captured (1.42), 1.74 ms in a long run (1.25); 32 heads on 8 of 128, 4096 tokens 121 (1.14).
+//
+// Running maximum and sum: Milakov and Gimelshein, "Online normalizer calculation
+// for softmax", 2018. Tiles of rows in turn, and a maximum that moves only past a
+// threshold, are published methods of such kernels as well.
 #include <cuda.h>
 #include <cudaTypedefs.h>
 
@@ -1152,6 +1156,8 @@ CaPlan ca_plan(int n, int T, int Hq, int Hkv, int d, int max_len) {
     // tiles of 1.5 us. Whole and cut (16 heads on 2 key heads of 256): 4 tokens over 700 keys 16 and 12 us, 64 over 4064
     // 60 and 29, 256 over 4352 63 and 37, 512 14 and 38, 2048 36 and 65, 2048 behind 8192 242 and 250, behind 14336 392 and
     // 373, behind 30720 788 and 730; 32 heads on 8 of 128, 4096 behind 16384: 1024 and 945.
+    // More runs than the list in shared memory has room for stay whole, whatever that costs: sequences of 1 to 4 tokens over
+    // up to 16000 keys, 120 of them cut 96 us, 140 whole 232, 200 whole 251 (their bytes: 67, 76, 103).
     const long long tokens = T / n, tiles = (max_len - (tokens < max_len ? tokens : max_len) / 2) / kKeys + 1;
     p.ranges = p.runs <= kCaRuns && (rounds * kSms - units) * tiles > (units < kSms ? 10 : 22) * kSms &&
                units * (max_len / kKeys + 1 + kCaStart) < 1ll << 30;

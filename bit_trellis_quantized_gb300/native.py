@@ -911,7 +911,8 @@ def adjust_logits(logits, ids=None, at=None, prompt=None, repetition=None, frequ
     what is added to single tokens. allowed int32 [masks][ceil(V / 32)], a bit a
     token; allowed_rows int32 [M]: each row's mask, -1 for none (by default row
     m has mask m). Returns the adjusted logits: a new tensor, or ``out``, which
-    may be ``logits`` (in place, only what changes is touched)."""
+    may be ``logits`` (in place: allowed logits within 16 bytes of a banned one
+    are written back as they were)."""
     if logits.dim() != 2 or not logits.is_cuda:
         raise ValueError("logits must be a CUDA tensor [M][V]")
     M, V = logits.shape

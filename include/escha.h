@@ -713,8 +713,9 @@ int escha_debug_set_chunk_wait(int polls);
  *            says that token i is allowed
  *   allowed_rows  int32 [M]: the row's mask; outside [0, n_masks): none. NULL:
  *            row m has mask m.
- * In place, only the logits that change are read or written. n_ids and n_bias
- * below 2^30. No workspace. Errors as escha_paged_attention. */
+ * In place, rows without a list or a mask are not touched; next to a banned token, up
+ * to the 16 bytes around it, allowed ones are written back as they were. The time goes
+ * by the length of the lists. n_ids and n_bias below 2^30. No workspace. Errors as escha_paged_attention. */
 int escha_adjust_logits(const void* logits, void* out, int dtype, int M, int V, long long ld, long long out_ld,
                         const int32_t* ids, const int32_t* at, int n_ids, const int32_t* prompt,
                         const float* repetition, const float* frequency, const float* presence,
